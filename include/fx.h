@@ -89,6 +89,7 @@ typedef enum {
 #define FX_DEVERR_OFFSETS 4u  /* branch suffix offsets decreasing or past the suffix rows; branch suffix skipped */
 #define FX_DEVERR_CAPACITY 8u /* a compacted cache would exceed its capacity; extra rows not written */
 #define FX_DEVERR_TIMEOUT 16u /* a bounded wait for an asynchronous copy gave up; that call's output is invalid */
+#define FX_DEVERR_PAGE 32u    /* a page number outside [0, n_pages) for a row in use; that row was skipped */
 
 /*
  * One layer's KV cache, read-only.  Element (b, h, t, c) of K is at k[b*stride_b + h*stride_h +
@@ -407,6 +408,138 @@ FX_API int fx_branch_pool_prefix_refs(fx_branch_pool* pool);
 FX_API int fx_branch_pool_prefix_len(fx_branch_pool* pool);
 FX_API int fx_branch_pool_batch(fx_branch_pool* pool, int32_t* ids, int32_t* suf_start, int32_t* suf_len,
                          int32_t* prefix_len);
+
+/* ------------------------------------------------------------------------------------------- */
+/* Paged KV cache, in bf16 or in 4 bits.  [FastKV] 2.B and [FastOCR] decode over caches that grow token
+ * by token and differ in length between sequences; a paged cache lets them share one pool, and a 4-bit
+ * one holds 3.6 times the tokens.  The pages describe neither layout: both are this library's.
+ *
+ * The rows of sequence b, KV head h live in pages of page_rows rows: row t is row t % page_rows of page
+ * table[b*table_stride + t / page_rows] of the pool, at
+ *   k + page*stride_page + h*stride_h + (t % page_rows)*stride_t        (v with the same strides)
+ * Strides count the elements of a row's storage: bf16 values (FX_PAGED_BF16) or bytes (FX_PAGED_E2M1).
+ *   FX_PAGED_BF16  a row is 128 bf16 values; k_scale and v_scale are NULL.
+ *   FX_PAGED_E2M1  a row is 64 bytes of codes -- dimension 2i in the low half of byte i, 2i+1 in the high
+ *                  half -- and 8 bytes of scales at k_scale + page*scale_stride_page + h*scale_stride_h +
+ *                  (t % page_rows)*scale_stride_t, one for each block of 16 dimensions.  A code is sign,
+ *                  two exponent bits, one mantissa bit: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}.  A scale is an
+ *                  e4m3 byte (sign, 4 exponent bits with bias 7, 3 mantissa bits; 0x7f and 0xff are NaN).
+ *                  The value held is code * scale * 2^k_exp (K) or * 2^v_exp (V).  It has at most 6
+ *                  significant bits, so bf16 holds it exactly.
+ *   table    device [B, table_stride] int32; entries of pages that hold no row in use are never read as
+ *            pages.  A bad entry for a row in use sets FX_DEVERR_PAGE and its rows are skipped.
+ *   len      device [B] int32: rows t < len[b] are valid (outside [0, max_pages*page_rows]: clamped,
+ *            FX_DEVERR_LEN).  Rows at or past it are never used, whatever they hold.
+ *   page_rows  16, 32, 64, 128, 256, 512 or 1024;  n_pages: pages in the pool;  max_pages: table entries
+ *            of one sequence.  n_pages*page_rows is below 2^31, max_pages*page_rows below 2^30.
+ *   Codes and bf16 rows start on 16-byte boundaries, scale rows on 8-byte boundaries.  -64 <= k_exp,
+ *   v_exp <= 64 (both 0 with FX_PAGED_BF16).
+ */
+#define FX_PAGED_BF16 0
+#define FX_PAGED_E2M1 1
+typedef struct {
+    void* k;
+    void* v;
+    void* k_scale;
+    void* v_scale;
+    const int32_t* table;
+    const int32_t* len;
+    int64_t stride_page, stride_h, stride_t;
+    int64_t scale_stride_page, scale_stride_h, scale_stride_t;
+    int64_t table_stride;
+    int32_t format, B, Hkv, d, page_rows, n_pages, max_pages, k_exp, v_exp;
+} fx_paged_desc;
+
+/* fx_paged_append -- new rows join the cache, rotated by their position on the way.
+ *
+ * Token i < n of the call (a decode step's token of one sequence, a draft, a prompt's token) writes row
+ * pos[i] of sequence seq[i] of every KV head:
+ *   K row = stored(rotated(k[i, h, :])),  V row = stored(v[i, h, :])
+ * and, when q is given, q_out[i, g, :] = rotated(q[i, g, :]) for every query head.
+ * rotated: with rot > 0 and the position t = rope_pos[i] (pos[i] when rope_pos is NULL), pair j < rot/2 of
+ *   dimensions (a, b) = (j, j + rot/2), or (2j, 2j+1) when interleaved, becomes
+ *     x_a' = bf16(x_a c - x_b s),  x_b' = bf16(x_b c + x_a s)
+ *   with c = cos_sin[t*rot + j], s = cos_sin[t*rot + rot/2 + j]; each product and each sum is rounded to
+ *   fp32.  The other dimensions stay as they are, and so does everything with rot = 0.
+ * stored: FX_PAGED_BF16 the bits.  FX_PAGED_E2M1, per block of 16 dimensions with y = x * 2^-exp:
+ *   scale = e4m3(max|y| / 6) rounded to nearest even, at least 2^-9 and at most 448; code = y / scale
+ *   rounded to nearest (ties to the even code), at most 6 in magnitude.  A block that holds an infinity
+ *   or a NaN gets a NaN scale (0x7f) and zero codes: all of it reads back as NaN.
+ *   k, v     bf16 rows (i, h) at k + i*stride_n + h*stride_h (v with the same strides)
+ *   q, q_out bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h, q_out + i*qo_stride_n + g*qo_stride_h;
+ *            both NULL or both given; q_out may be q (same strides)
+ *   seq      int32 [n]; seq[i] = -1 marks a padding token, of which nothing is read or written.  Another
+ *            value outside [0, B) sets FX_DEVERR_INDEX, pos[i] outside [0, max_pages*page_rows)
+ *            FX_DEVERR_LEN, a rotation position outside [0, n_pos) FX_DEVERR_INDEX: that token is skipped,
+ *            its q_out rows included.  A bad page (FX_DEVERR_PAGE) skips the K and V rows only.
+ *   cos_sin  fp32 [n_pos, rot], 16-byte aligned; rot is 0 or a multiple of 16 up to 128
+ * Tokens of one call write distinct rows of the pool (two that name the same row leave a mixture of both).
+ * cache->len is not read (lengths stay the caller's) and may be NULL.  No workspace.
+ */
+typedef struct {
+    const fx_bf16* k;
+    const fx_bf16* v;
+    int64_t stride_n, stride_h;
+    const fx_bf16* q;
+    fx_bf16* q_out;
+    int64_t q_stride_n, q_stride_h, qo_stride_n, qo_stride_h;
+    const int32_t* seq;
+    const int32_t* pos;
+    const int32_t* rope_pos;
+    const float* cos_sin;
+    int32_t n, Hq, rot, n_pos, interleaved;
+} fx_paged_rows;
+
+FX_API fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows, unsigned flags, void* stream);
+
+/* fx_paged_gather -- rows of a paged cache as contiguous bf16 rows (exact for both formats), for the calls
+ * that take a contiguous cache.
+ *
+ * Row i < n of sequence b, KV head h of k_out and v_out [B, Hkv, n, 128] receives cache row
+ *   t = idx[b, h, i]   (idx given: a t outside [0, len[b]) sets FX_DEVERR_INDEX, its row is not written)
+ *   t = lo[b] + i      (idx NULL; lo NULL means 0: rows with t >= len[b] are not written; lo[b] < 0 sets
+ *                       FX_DEVERR_LEN and counts as 0)
+ * idx: int32 [B, Hkv, n] or NULL; lo: int32 [B] or NULL (only without idx).  No workspace.
+ */
+FX_API fx_status fx_paged_gather(const fx_paged_desc* cache, const int32_t* idx, const int32_t* lo, int n,
+                                 fx_bf16* k_out, fx_bf16* v_out, unsigned flags, void* stream);
+
+/* fx_paged_decode -- attention over a paged cache: dense, or over listed rows and a dense tail.
+ * [FastOCR] Focal-Guided Pruning, [FastKV] 2.B and [HPD] P-MTP as in fx_sparse_gqa_decode and
+ * fx_shared_prefix_decode, for caches that live in pages.
+ *
+ * Query i < Mq of sequence b sits at row len[b] - Mq + i of the cache (the queries' own rows have been
+ * appended): it sees rows t <= len[b] - Mq + i.  For KV head h and query head g = h*G + gi:
+ *   S = { idx[b, h, 0..k) } followed by { tail_lo[b] .. len[b]-1 },  each only where query i sees it
+ *   out[b, g, i, :] = sum_{t in S} softmax_S(scale * q . k_t) v_t
+ *   lse[b, g, i]    = log sum_{t in S} exp(scale * q . k_t)                       (written when lse != NULL)
+ * k = 0 with tail_lo = NULL is dense attention.  An empty S gives out = 0 and lse = -infinity.  An idx
+ * entry outside [0, len[b]) sets FX_DEVERR_INDEX and is skipped; a row listed twice, or listed and in the
+ * tail, counts twice.  A row that query i does not see does not reach it, whatever it holds.
+ *   q         bf16 rows (b, g, i) at q + b*q_stride_b + g*q_stride_h + i*q_stride_i
+ *   tail_lo   int32 [B] (device) or NULL, which means 0; a negative value sets FX_DEVERR_LEN and counts as 0
+ *   out [B, Hq, Mq, 128] fp32, lse [B, Hq, Mq] fp32 or NULL;  G*Mq <= 64, scale finite
+ * Workspace: fx_paged_decode_workspace_bytes(B, Hkv, Hq, Mq) bytes.
+ */
+FX_API size_t fx_paged_decode_workspace_bytes(int B, int Hkv, int Hq, int Mq);
+FX_API fx_status fx_paged_decode(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
+                                 int64_t q_stride_i, int Hq, int Mq, const int32_t* idx, int k,
+                                 const int32_t* tail_lo, float scale, float* out, float* lse, void* ws,
+                                 size_t ws_bytes, unsigned flags, void* stream);
+
+/* fx_paged_importance -- the importance of every row of a paged cache, from the lse of fx_paged_decode: what
+ * fx_focal_attn_scores reports for a contiguous cache and fx_topk_select ranks.
+ *
+ *   scores[b, h, t - cand_lo] = sum over the group's query heads g and positions i that see row t of
+ *                               exp(scale * q_{g,i} . k_t - lse[b, g, i]),   cand_lo <= t < cand_hi
+ * Rows t >= len[b] report 0, and query rows whose lse is -infinity add nothing.  Queries, strides, visibility
+ * and limits as in fx_paged_decode.  scores [B, Hkv, cand_hi - cand_lo] fp32; 0 <= cand_lo <= cand_hi <=
+ * max_pages*page_rows.  No workspace.
+ */
+FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b,
+                                     int64_t q_stride_h, int64_t q_stride_i, int Hq, int Mq, const float* lse,
+                                     float scale, int cand_lo, int cand_hi, float* scores, unsigned flags,
+                                     void* stream);
 
 /* ------------------------------------------------------------------------------------------- */
 /* fx_test_stall_wait -- testing hook for the device-side failure path; the pages have no counterpart.

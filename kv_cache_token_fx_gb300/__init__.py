@@ -8,6 +8,7 @@ Build the library with ``python -m kv_cache_token_fx_gb300.build`` (or ``__graft
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -25,11 +26,15 @@ __all__ = [
     "fx_device_errors", "fx_focal_workspace_bytes", "fx_sparse_workspace_bytes", "fx_shared_prefix_workspace_bytes",
     "FX_DEVERR_LEN", "FX_DEVERR_INDEX", "FX_DEVERR_OFFSETS", "FX_DEVERR_CAPACITY", "FX_DEVERR_TIMEOUT",
     "FX_LAUNCH_PDL", "FX_LAUNCH_INPUTS_READY", "BranchPool",
+    "PagedKV", "fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance",
+    "fx_paged_decode_workspace_bytes", "FX_DEVERR_PAGE", "FX_PAGED_BF16", "FX_PAGED_E2M1",
 ]
 
 FX_OK, FX_ERR_INVALID_ARG, FX_ERR_UNSUPPORTED, FX_ERR_WORKSPACE, FX_ERR_CUDA, FX_ERR_DEVICE = range(6)
 FX_DEVERR_LEN, FX_DEVERR_INDEX, FX_DEVERR_OFFSETS, FX_DEVERR_CAPACITY, FX_DEVERR_TIMEOUT = 1, 2, 4, 8, 16
+FX_DEVERR_PAGE = 32
 FX_LAUNCH_PDL, FX_LAUNCH_INPUTS_READY = 1, 2
+FX_PAGED_BF16, FX_PAGED_E2M1 = 0, 1
 FX_CSFR_FOCAL, FX_CSFR_CURRENT, FX_CSFR_PREVIOUS, FX_CSFR_DENSE = range(4)
 _STATUS = {0: "FX_OK", 1: "FX_ERR_INVALID_ARG", 2: "FX_ERR_UNSUPPORTED", 3: "FX_ERR_WORKSPACE",
            4: "FX_ERR_CUDA", 5: "FX_ERR_DEVICE"}
@@ -63,6 +68,21 @@ class BranchDesc(ctypes.Structure):
                 ("suf_off", c_vp), ("suf_rows", c_i32), ("max_suffix", c_i32), ("draft_k", c_vp),
                 ("draft_v", c_vp), ("draft_stride_b", c_i64), ("draft_stride_i", c_i64),
                 ("draft_stride_h", c_i64), ("Br", c_i32), ("Mq", c_i32), ("suf_len", c_vp)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("table", c_vp), ("len", c_vp),
+                ("stride_page", c_i64), ("stride_h", c_i64), ("stride_t", c_i64), ("scale_stride_page", c_i64),
+                ("scale_stride_h", c_i64), ("scale_stride_t", c_i64), ("table_stride", c_i64), ("format", c_i32),
+                ("B", c_i32), ("Hkv", c_i32), ("d", c_i32), ("page_rows", c_i32), ("n_pages", c_i32),
+                ("max_pages", c_i32), ("k_exp", c_i32), ("v_exp", c_i32)]
+
+
+class PagedRows(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("stride_n", c_i64), ("stride_h", c_i64), ("q", c_vp), ("q_out", c_vp),
+                ("q_stride_n", c_i64), ("q_stride_h", c_i64), ("qo_stride_n", c_i64), ("qo_stride_h", c_i64),
+                ("seq", c_vp), ("pos", c_vp), ("rope_pos", c_vp), ("cos_sin", c_vp), ("n", c_i32), ("Hq", c_i32),
+                ("rot", c_i32), ("n_pos", c_i32), ("interleaved", c_i32)]
 
 
 _lib = None
@@ -126,6 +146,17 @@ def load_library():
         lib.fx_shared_prefix_workspace_bytes.restype = c_size
         lib.fx_shared_prefix_decode.argtypes = [ctypes.POINTER(PrefixDesc), ctypes.POINTER(BranchDesc), c_vp, c_int,
                                                 c_vp, c_int, c_float, c_vp, c_vp, c_size, c_uint, c_vp]
+        paged = ctypes.POINTER(PagedDesc)
+        lib.fx_paged_append.argtypes = [paged, ctypes.POINTER(PagedRows), c_uint, c_vp]
+        lib.fx_paged_gather.argtypes = [paged, c_vp, c_vp, c_int, c_vp, c_vp, c_uint, c_vp]
+        lib.fx_paged_decode_workspace_bytes.argtypes = [c_int] * 4
+        lib.fx_paged_decode_workspace_bytes.restype = c_size
+        lib.fx_paged_decode.argtypes = [paged, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_int, c_vp, c_float,
+                                        c_vp, c_vp, c_vp, c_size, c_uint, c_vp]
+        lib.fx_paged_importance.argtypes = [paged, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_float, c_int,
+                                            c_int, c_vp, c_uint, c_vp]
+        for name in ("fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance"):
+            getattr(lib, name).restype = c_int
         for name in ("fx_device_errors", "fx_workspace_init", "fx_focal_attn_scores", "fx_topk_select",
                      "fx_focal_mass", "fx_choose_focal_layers", "fx_csfr_schedule",
                      "fx_sparse_gqa_decode", "fx_kv_compact", "fx_kv_append", "fx_kv_retain_per_layer",
@@ -474,6 +505,254 @@ def fx_shared_prefix_decode(pk, pv, sk, sv, off, dk, dv, q, *, max_suffix: int, 
     _check(lib.fx_shared_prefix_decode(ctypes.byref(pre), ctypes.byref(brd), _ptr(q), Hq, _ptr(prefix_idx), kp, sc,
                                        _ptr(out), _ptr(buf), buf.numel(), int(flags), _stream(stream)))
     return out
+
+
+def _strides(t):
+    """The strides of a view, 0 for a dimension of one entry (whose stride addresses nothing)."""
+    return tuple([s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)])
+
+
+class PagedKV:
+    """One layer's paged KV cache (include/fx.h: paged KV cache), as the fx_paged_* calls take it.
+
+    k, v       bf16 [n_pages, Hkv, page_rows, 128], or uint8 [n_pages, Hkv, page_rows, 64] (4-bit codes)
+    k_scale, v_scale   uint8 or float8_e4m3fn [n_pages, Hkv, page_rows, 8] (4-bit only)
+    table      int32 [B, max_pages]: the pages of each sequence in order
+    length     int32 [B]: rows of each sequence, read on the device by every call
+    k_exp, v_exp       4-bit: the values held are code * scale * 2^exp
+
+    Views with any strides work (unit last stride, rows on 16-byte, scale rows on 8-byte boundaries; k and v,
+    k_scale and v_scale with equal strides).  The object keeps its tensors; their contents may change between calls.
+    """
+
+    def __init__(self, k, v, table, length, *, k_scale=None, v_scale=None, k_exp: int = 0, v_exp: int = 0):
+        packed = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
+        for t, name in ((k, "k"), (v, "v")):
+            _need_cuda(t, name, torch.uint8 if packed else torch.bfloat16)
+        width = 64 if packed else 128
+        if k.dim() != 4 or k.shape != v.shape or _strides(k) != _strides(v) or k.shape[3] != width or k.stride(3) != 1:
+            raise FxError(FX_ERR_INVALID_ARG, f"k and v must be [n_pages, Hkv, page_rows, {width}] views with equal "
+                                              "strides, unit last stride")
+        if (k_scale is None) == packed or (v_scale is None) == packed:
+            raise FxError(FX_ERR_INVALID_ARG, "a 4-bit cache needs k_scale and v_scale, a bf16 cache has none")
+        if packed:
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _need_cuda(t, name, torch.float8_e4m3fn if getattr(t, "dtype", None) == torch.float8_e4m3fn
+                           else torch.uint8)
+            if k_scale.shape != k.shape[:3] + (8,) or k_scale.shape != v_scale.shape or k_scale.stride(3) != 1 or \
+                    _strides(k_scale) != _strides(v_scale):
+                raise FxError(FX_ERR_INVALID_ARG, "k_scale and v_scale must be [n_pages, Hkv, page_rows, 8] views with "
+                                                  "equal strides, unit last stride")
+        _need_cuda(table, "table", torch.int32)
+        _need_cuda(length, "length", torch.int32)
+        if table.dim() != 2 or table.stride(1) != 1 or length.dim() != 1 or length.shape[0] != table.shape[0] or \
+                not length.is_contiguous():
+            raise FxError(FX_ERR_INVALID_ARG, "table must be [B, max_pages] with unit last stride, length [B]")
+        if any(t is not None and t.device != k.device for t in (v, table, length, k_scale, v_scale)):
+            raise FxError(FX_ERR_INVALID_ARG, "the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale, self.table, self.length = k, v, k_scale, v_scale, table, length
+        self.device = k.device
+        self.n_pages, self.Hkv, self.page_rows, _ = k.shape
+        self.B, self.max_pages = table.shape
+        ks, ss = _strides(k), _strides(k_scale) if packed else (0, 0, 0, 0)
+        self._desc = PagedDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if packed else None,
+                               v_scale.data_ptr() if packed else None, table.data_ptr(), length.data_ptr(),
+                               ks[0], ks[1], ks[2], ss[0], ss[1], ss[2],
+                               table.stride(0) if self.B > 1 else self.max_pages,
+                               FX_PAGED_E2M1 if packed else FX_PAGED_BF16, self.B, self.Hkv, 128, self.page_rows,
+                               self.n_pages, self.max_pages, int(k_exp), int(v_exp))
+        self._ref = ctypes.byref(self._desc)
+
+
+def _paged_tensor(cache, t, name, dtype, shape, contiguous=True):
+    if not isinstance(t, torch.Tensor) or t.device != cache.device:
+        raise FxError(FX_ERR_INVALID_ARG, f"{name} must be a tensor on {cache.device}")
+    if t.dtype != dtype or t.shape != shape:
+        raise FxError(FX_ERR_INVALID_ARG, f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise FxError(FX_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+def _paged_launch(cache, stream):
+    """(library, stream handle) of a call on the cache, which must live on the current device."""
+    if not isinstance(cache, PagedKV):
+        raise FxError(FX_ERR_INVALID_ARG, "cache must be a PagedKV")
+    if torch.cuda.current_device() != cache.device.index:
+        raise FxError(FX_ERR_INVALID_ARG, f"the cache is on {cache.device}, the current device is another one")
+    return load_library(), _stream(stream)
+
+
+def _on(cache, stream):
+    """Context in which memory is allocated for the stream that uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream), cache.device))
+
+
+def _paged_alloc(cache, stream, shape, dtype):
+    with _on(cache, stream):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+
+
+def fx_paged_append(cache, k_new, v_new, seq, pos, *, cos_sin=None, rope_pos=None, interleaved: bool = False, q=None,
+                    q_out=None, stream=None, flags: int = 0):
+    """Append the rows of n tokens to a paged cache, rotated by position on the way; returns the rotated queries.
+
+    k_new, v_new [n, Hkv, 128] bf16 views with equal strides; seq, pos int32 [n]: the sequence (-1: padding, left
+    out) and the row each token writes.  cos_sin fp32 [n_pos, rot] (rot/2 cosines, rot/2 sines a row) rotates the
+    first rot dimensions of K and of q [n, Hq, 128] by rope_pos (int32 [n]; pos when None), in halves or, with
+    interleaved, in neighbouring pairs.  q_out [n, Hq, 128] (allocated when None; may be q).
+    """
+    lib, st = _paged_launch(cache, stream)
+    n = seq.shape[0] if isinstance(seq, torch.Tensor) and seq.dim() == 1 else -1
+    _paged_tensor(cache, seq, "seq", torch.int32, (n,))
+    _paged_tensor(cache, pos, "pos", torch.int32, (n,))
+    _paged_tensor(cache, k_new, "k_new", torch.bfloat16, (n, cache.Hkv, 128), False)
+    _paged_tensor(cache, v_new, "v_new", torch.bfloat16, (n, cache.Hkv, 128), False)
+    sn, sh, sd = _strides(k_new)
+    if _strides(v_new) != (sn, sh, sd) or sd != 1:
+        raise FxError(FX_ERR_INVALID_ARG, "k_new and v_new must have equal strides, unit last stride")
+    rows = PagedRows(k_new.data_ptr(), v_new.data_ptr(), sn, sh)
+    if q is not None:
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
+        _paged_tensor(cache, q, "q", torch.bfloat16, (n, Hq, 128), False)
+        if q_out is None:
+            q_out = _paged_alloc(cache, stream, (n, Hq, 128), torch.bfloat16)
+        _paged_tensor(cache, q_out, "q_out", torch.bfloat16, (n, Hq, 128), False)
+        a, b = _strides(q), _strides(q_out)
+        if a[2] != 1 or b[2] != 1:
+            raise FxError(FX_ERR_INVALID_ARG, "q and q_out must have unit last stride")
+        rows.q, rows.q_out, rows.Hq = q.data_ptr(), q_out.data_ptr(), Hq
+        rows.q_stride_n, rows.q_stride_h, rows.qo_stride_n, rows.qo_stride_h = a[0], a[1], b[0], b[1]
+    elif q_out is not None:
+        raise FxError(FX_ERR_INVALID_ARG, "q_out needs q")
+    if n == 0:
+        return q_out
+    rows.seq, rows.pos, rows.n = seq.data_ptr(), pos.data_ptr(), n
+    if rope_pos is not None:
+        _paged_tensor(cache, rope_pos, "rope_pos", torch.int32, (n,))
+        rows.rope_pos = rope_pos.data_ptr()
+    if cos_sin is not None:
+        n_pos, rot = cos_sin.shape if isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2 else (-1, -1)
+        _paged_tensor(cache, cos_sin, "cos_sin", torch.float32, (n_pos, rot))
+        rows.cos_sin, rows.rot, rows.n_pos = cos_sin.data_ptr(), rot, n_pos
+    rows.interleaved = 1 if interleaved else 0
+    _check(lib.fx_paged_append(cache._ref, ctypes.byref(rows), int(flags), st))
+    return q_out
+
+
+def fx_paged_gather(cache, n: int, *, idx=None, lo=None, k_out=None, v_out=None, stream=None, flags: int = 0):
+    """Rows of a paged cache as bf16 [B, Hkv, n, 128] K and V: rows idx [B, Hkv, n] (int32) of each (sequence, KV
+    head), or rows lo[b] .. lo[b] + n - 1 (lo int32 [B], 0 when None).  Rows past the length are not written: give
+    k_out and v_out where that can happen and their old contents count.
+    """
+    lib, st = _paged_launch(cache, stream)
+    n = int(n)
+    shape = (cache.B, cache.Hkv, n, 128)
+    if idx is not None:
+        _paged_tensor(cache, idx, "idx", torch.int32, shape[:3])
+    if lo is not None:
+        _paged_tensor(cache, lo, "lo", torch.int32, (cache.B,))
+    if k_out is None:
+        k_out = _paged_alloc(cache, stream, shape, torch.bfloat16)
+    if v_out is None:
+        v_out = _paged_alloc(cache, stream, shape, torch.bfloat16)
+    _paged_tensor(cache, k_out, "k_out", torch.bfloat16, shape)
+    _paged_tensor(cache, v_out, "v_out", torch.bfloat16, shape)
+    if n == 0:
+        return k_out, v_out
+    _check(lib.fx_paged_gather(cache._ref, None if idx is None else idx.data_ptr(), None if lo is None else lo.data_ptr(),
+                               n, k_out.data_ptr(), v_out.data_ptr(), int(flags), st))
+    return k_out, v_out
+
+
+def fx_paged_decode_workspace_bytes(B, Hkv, Hq, Mq) -> int:
+    return int(load_library().fx_paged_decode_workspace_bytes(B, Hkv, Hq, Mq))
+
+
+_stream_ws = {}
+
+
+def _paged_workspace(cache, ws, nbytes, stream, handle):
+    """The call's workspace: the caller's, or one of this device and stream (two streams never share one).  A call
+    that is being captured gets one of its own, from the graph's memory."""
+    if ws is not None:
+        return ws.ensure(nbytes, stream)
+    if torch.cuda.is_current_stream_capturing():
+        ws = Workspace(cache.device)
+    else:
+        key = (cache.device.index, handle.value or 0)
+        ws = _stream_ws.get(key)
+        if ws is None:
+            ws = _stream_ws[key] = Workspace(cache.device)
+    with _on(cache, stream):
+        return ws.ensure(nbytes, stream)
+
+
+def _paged_queries(cache, q):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.device != cache.device or q.dtype != torch.bfloat16:
+        raise FxError(FX_ERR_INVALID_ARG, f"q must be a bf16 [B, Hq, Mq, 128] tensor on {cache.device}")
+    B, Hq, Mq, d = q.shape
+    if B != cache.B or d != 128 or q.stride(3) != 1:
+        raise FxError(FX_ERR_INVALID_ARG, f"q must be [{cache.B}, Hq, Mq, 128] with unit last stride")
+    return Hq, Mq
+
+
+def fx_paged_decode(cache, q, idx=None, tail_lo=None, *, scale=None, out=None, lse=None, want_lse=False, ws=None,
+                    stream=None, flags: int = 0):
+    """Attention of q [B, Hq, Mq, 128] (bf16, any strides) over a paged cache; query i sits at row len - Mq + i.
+
+    Dense, or over the rows idx [B, Hkv, k] (int32) and the tail from row tail_lo[b] (int32 [B]) on.  Returns out
+    [B, Hq, Mq, 128] fp32, or (out, lse [B, Hq, Mq]) when lse is given or wanted.
+    """
+    lib, st = _paged_launch(cache, stream)
+    Hq, Mq = _paged_queries(cache, q)
+    kk = 0
+    if idx is not None:
+        kk = idx.shape[-1] if isinstance(idx, torch.Tensor) and idx.dim() == 3 else -1
+        _paged_tensor(cache, idx, "idx", torch.int32, (cache.B, cache.Hkv, kk))
+    if tail_lo is not None:
+        _paged_tensor(cache, tail_lo, "tail_lo", torch.int32, (cache.B,))
+    shape = (cache.B, Hq, Mq)
+    if out is None:
+        out = _paged_alloc(cache, stream, shape + (128,), torch.float32)
+    _paged_tensor(cache, out, "out", torch.float32, shape + (128,))
+    if lse is None and want_lse:
+        lse = _paged_alloc(cache, stream, shape, torch.float32)
+    if lse is not None:
+        _paged_tensor(cache, lse, "lse", torch.float32, shape)
+    buf = _paged_workspace(cache, ws, lib.fx_paged_decode_workspace_bytes(cache.B, cache.Hkv, Hq, Mq), stream, st)
+    sb, sh, si, _ = _strides(q)
+    sc = _default_scale(128) if scale is None else float(scale)
+    _check(lib.fx_paged_decode(cache._ref, q.data_ptr(), sb, sh, si, Hq, Mq, idx.data_ptr() if kk else None, kk,
+                               None if tail_lo is None else tail_lo.data_ptr(), sc, out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), int(flags), st))
+    return out if lse is None else (out, lse)
+
+
+def fx_paged_importance(cache, q, lse, *, scale=None, cand=None, scores=None, stream=None, flags: int = 0):
+    """Importance of the rows cand = (lo, hi) of a paged cache (default: the whole capacity, or the width of scores
+    when given): fp32 [B, Hkv, hi - lo], from the queries and the lse [B, Hq, Mq] of fx_paged_decode."""
+    lib, st = _paged_launch(cache, stream)
+    Hq, Mq = _paged_queries(cache, q)
+    _paged_tensor(cache, lse, "lse", torch.float32, (cache.B, Hq, Mq))
+    if cand is not None:
+        lo, hi = int(cand[0]), int(cand[1])
+    else:
+        lo, hi = 0, cache.max_pages * cache.page_rows
+        if isinstance(scores, torch.Tensor) and scores.dim() == 3:
+            hi = scores.shape[2]
+    if scores is None:
+        scores = _paged_alloc(cache, stream, (cache.B, cache.Hkv, max(hi - lo, 0)), torch.float32)
+    _paged_tensor(cache, scores, "scores", torch.float32, (cache.B, cache.Hkv, hi - lo))
+    if hi == lo:
+        return scores
+    sb, sh, si, _ = _strides(q)
+    sc = _default_scale(128) if scale is None else float(scale)
+    _check(lib.fx_paged_importance(cache._ref, q.data_ptr(), sb, sh, si, Hq, Mq, lse.data_ptr(), sc, lo, hi,
+                                   scores.data_ptr(), int(flags), st))
+    return scores
 
 
 class BranchPool:

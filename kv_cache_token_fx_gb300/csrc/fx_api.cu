@@ -1001,6 +1001,255 @@ fx_status fx_shared_prefix_decode(const fx_prefix_desc* prefix, const fx_branch_
     return FX_OK;
 }
 
+// ---------------------------------------------------------------------------------------------
+// Paged cache
+}  // extern "C"
+
+namespace {
+
+bool multiple_of(int64_t s, int64_t m) { return s >= 0 && s % m == 0; }
+
+// Checks a paged cache and turns it into the kernels' view.  `need_len`: the call reads len.
+fx_status paged_view(const fx_paged_desc* d, bool need_len, PagedCache* c)
+{
+    if (!d) return fail(FX_ERR_INVALID_ARG, "cache is NULL");
+    if (d->format != FX_PAGED_BF16 && d->format != FX_PAGED_E2M1)
+        return fail(FX_ERR_INVALID_ARG, "cache: unknown format %d", d->format);
+    const bool e2m1 = d->format == FX_PAGED_E2M1;
+    if (!d->k || !d->v || !d->table || (need_len && !d->len))
+        return fail(FX_ERR_INVALID_ARG, "cache: k, v, table and len must be non-NULL");
+    if (d->d != kHeadDim) return fail(FX_ERR_UNSUPPORTED, "cache: head dim %d (only 128 is implemented)", d->d);
+    if (d->B < 1 || d->Hkv < 1 || d->n_pages < 1 || d->max_pages < 1 || d->table_stride < d->max_pages)
+        return fail(FX_ERR_INVALID_ARG, "cache: need B, Hkv, n_pages, max_pages >= 1 and table_stride >= max_pages");
+    if (d->page_rows < 16 || d->page_rows > 1024 || (d->page_rows & (d->page_rows - 1)) != 0)
+        return fail(FX_ERR_UNSUPPORTED, "cache: page_rows %d (a power of two from 16 to 1024)", d->page_rows);
+    if ((int64_t)d->n_pages * d->page_rows >= (1ll << 31) || (int64_t)d->max_pages * d->page_rows >= (1ll << 30))
+        return fail(FX_ERR_UNSUPPORTED, "cache: 2^31 rows or more in the pool, or 2^30 in a sequence");
+    if (d->B > 65535 || d->Hkv > 65535) return fail(FX_ERR_UNSUPPORTED, "cache: B and Hkv are at most 65535");
+    if (!aligned16(d->k) || !aligned16(d->v)) return fail(FX_ERR_INVALID_ARG, "cache: k and v must be 16-byte aligned");
+    const int64_t unit = e2m1 ? 16 : 8;   // 16 bytes
+    if (!multiple_of(d->stride_page, unit) || !multiple_of(d->stride_h, unit) || !multiple_of(d->stride_t, unit))
+        return fail(FX_ERR_INVALID_ARG, "cache: strides must be non-negative multiples of 16 bytes");
+    if (e2m1) {
+        if (!d->k_scale || !d->v_scale) return fail(FX_ERR_INVALID_ARG, "cache: k_scale and v_scale must be non-NULL");
+        if (((reinterpret_cast<uintptr_t>(d->k_scale) | reinterpret_cast<uintptr_t>(d->v_scale)) & 7u) != 0 ||
+            !multiple_of(d->scale_stride_page, 8) || !multiple_of(d->scale_stride_h, 8) ||
+            !multiple_of(d->scale_stride_t, 8))
+            return fail(FX_ERR_INVALID_ARG, "cache: scale rows must start on 8-byte boundaries");
+        if (d->k_exp < -64 || d->k_exp > 64 || d->v_exp < -64 || d->v_exp > 64)
+            return fail(FX_ERR_INVALID_ARG, "cache: k_exp and v_exp must be in [-64, 64]");
+    } else if (d->k_scale || d->v_scale || d->k_exp != 0 || d->v_exp != 0) {
+        return fail(FX_ERR_INVALID_ARG, "cache: a bf16 cache has no scales (NULL) and no exponents (0)");
+    }
+    const int64_t bytes = e2m1 ? 1 : 2;
+    c->k = static_cast<char*>(d->k);
+    c->v = static_cast<char*>(d->v);
+    c->ks = static_cast<char*>(d->k_scale);
+    c->vs = static_cast<char*>(d->v_scale);
+    c->table = d->table;
+    c->len = d->len;
+    c->sp = d->stride_page * bytes;
+    c->sh = d->stride_h * bytes;
+    c->st = d->stride_t * bytes;
+    c->ssp = d->scale_stride_page;
+    c->ssh = d->scale_stride_h;
+    c->sst = d->scale_stride_t;
+    c->table_stride = d->table_stride;
+    c->B = d->B;
+    c->Hkv = d->Hkv;
+    c->n_pages = d->n_pages;
+    c->cap = d->max_pages * d->page_rows;
+    c->page_shift = 0;
+    while ((1 << c->page_shift) < d->page_rows) ++c->page_shift;
+    c->page_mask = d->page_rows - 1;
+    c->k_mul = ldexpf(1.f, d->k_exp);
+    c->v_mul = ldexpf(1.f, d->v_exp);
+    c->k_inv = ldexpf(1.f, -d->k_exp);
+    c->v_inv = ldexpf(1.f, -d->v_exp);
+    return FX_OK;
+}
+
+// The checks that fx_paged_decode and fx_paged_importance share; fills the queries' part of p.
+fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
+                        int64_t q_stride_i, int Hq, int Mq, float scale, unsigned flags, PagedAttnParams* p)
+{
+    memset(p, 0, sizeof *p);
+    fx_status st = paged_view(cache, true, &p->c);
+    if (st != FX_OK) return st;
+    if ((st = check_flags(flags)) != FX_OK) return st;
+    if ((st = check_heads(Hq, cache->Hkv, Mq)) != FX_OK) return st;
+    if (!q || !aligned16(q)) return fail(FX_ERR_INVALID_ARG, "q must be non-NULL and 16-byte aligned");
+    if (!row_stride_ok(q_stride_b) || !row_stride_ok(q_stride_h) || !row_stride_ok(q_stride_i))
+        return fail(FX_ERR_INVALID_ARG, "q strides must be non-negative multiples of 8 elements");
+    if (!isfinite(scale)) return fail(FX_ERR_INVALID_ARG, "scale must be finite");
+    p->q = q;
+    p->q_b = q_stride_b;
+    p->q_h = q_stride_h;
+    p->q_i = q_stride_i;
+    p->Hq = Hq;
+    p->G = Hq / cache->Hkv;
+    p->Mq = Mq;
+    p->R = p->G * Mq;
+    p->qscale = log2e_scale(scale) * p->c.k_mul;
+    return FX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows, unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_append");
+    PagedAppendParams p;
+    memset(&p, 0, sizeof p);
+    fx_status st = paged_view(cache, false, &p.c);
+    if (st != FX_OK) return st;
+    if ((st = check_flags(flags)) != FX_OK) return st;
+    if (!rows) return fail(FX_ERR_INVALID_ARG, "rows is NULL");
+    if (rows->n < 0) return fail(FX_ERR_INVALID_ARG, "rows: n must be >= 0");
+    if (!rows->k || !rows->v || !rows->seq || !rows->pos)
+        return fail(FX_ERR_INVALID_ARG, "rows: k, v, seq and pos must be non-NULL");
+    if (!aligned16(rows->k) || !aligned16(rows->v)) return fail(FX_ERR_INVALID_ARG, "rows: k and v must be 16-byte aligned");
+    if (!row_stride_ok(rows->stride_n) || !row_stride_ok(rows->stride_h))
+        return fail(FX_ERR_INVALID_ARG, "rows: strides must be non-negative multiples of 8 elements");
+    if ((rows->q == nullptr) != (rows->q_out == nullptr))
+        return fail(FX_ERR_INVALID_ARG, "rows: q and q_out come together");
+    if (rows->q) {
+        if (!aligned16(rows->q) || !aligned16(rows->q_out))
+            return fail(FX_ERR_INVALID_ARG, "rows: q and q_out must be 16-byte aligned");
+        if (rows->Hq < 1) return fail(FX_ERR_INVALID_ARG, "rows: Hq must be >= 1");
+        if (!row_stride_ok(rows->q_stride_n) || !row_stride_ok(rows->q_stride_h) || !row_stride_ok(rows->qo_stride_n) ||
+            !row_stride_ok(rows->qo_stride_h))
+            return fail(FX_ERR_INVALID_ARG, "rows: q strides must be non-negative multiples of 8 elements");
+        if (rows->q == rows->q_out && (rows->q_stride_n != rows->qo_stride_n || rows->q_stride_h != rows->qo_stride_h))
+            return fail(FX_ERR_INVALID_ARG, "rows: q_out in the place of q needs the strides of q");
+    }
+    if (rows->rot < 0 || rows->rot > kHeadDim || rows->rot % 16 != 0)
+        return fail(FX_ERR_UNSUPPORTED, "rows: rot %d (0 or a multiple of 16 up to 128)", rows->rot);
+    if (rows->rot > 0 && (!rows->cos_sin || !aligned16(rows->cos_sin) || rows->n_pos < 1))
+        return fail(FX_ERR_INVALID_ARG, "rows: rot > 0 needs cos_sin (16-byte aligned) of n_pos >= 1 positions");
+    const int Hq = rows->q ? rows->Hq : 0;
+    if (Hq > 65535 || (int64_t)rows->n * (2 * (int64_t)cache->Hkv + Hq) > (int64_t)0x7fffffff * 16)
+        return fail(FX_ERR_UNSUPPORTED, "too many rows");
+    if (rows->n == 0) return FX_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.k = rows->k;
+    p.v = rows->v;
+    p.n_stride = rows->stride_n;
+    p.h_stride = rows->stride_h;
+    p.q = rows->q;
+    p.q_out = rows->q_out;
+    p.q_n = rows->q_stride_n;
+    p.q_h = rows->q_stride_h;
+    p.qo_n = rows->qo_stride_n;
+    p.qo_h = rows->qo_stride_h;
+    p.seq = rows->seq;
+    p.pos = rows->pos;
+    p.rope_pos = rows->rope_pos;
+    p.cos_sin = rows->cos_sin;
+    p.n = rows->n;
+    p.Hq = Hq;
+    p.rot = rows->rot;
+    p.n_pos = rows->n_pos;
+    p.interleaved = rows->interleaved != 0;
+    p.err = ds->err;
+    cudaError_t e = launch_paged_append(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+                                        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+    return FX_OK;
+}
+
+fx_status fx_paged_gather(const fx_paged_desc* cache, const int32_t* idx, const int32_t* lo, int n, fx_bf16* k_out,
+                          fx_bf16* v_out, unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_gather");
+    PagedGatherParams p;
+    memset(&p, 0, sizeof p);
+    fx_status st = paged_view(cache, true, &p.c);
+    if (st != FX_OK) return st;
+    if ((st = check_flags(flags)) != FX_OK) return st;
+    if (n < 0) return fail(FX_ERR_INVALID_ARG, "n must be >= 0");
+    if (idx && lo) return fail(FX_ERR_INVALID_ARG, "idx and lo exclude each other");
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+        return fail(FX_ERR_INVALID_ARG, "k_out and v_out must be non-NULL and 16-byte aligned");
+    if (n > (1 << 30)) return fail(FX_ERR_UNSUPPORTED, "n is at most 2^30");
+    if (n == 0) return FX_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.idx = idx;
+    p.lo = lo;
+    p.n = n;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.err = ds->err;
+    cudaError_t e = launch_paged_gather(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+                                        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged gather launch");
+    return FX_OK;
+}
+
+size_t fx_paged_decode_workspace_bytes(int B, int Hkv, int Hq, int Mq)
+{
+    if (B < 1 || Hkv < 1 || Hq < Hkv || Mq < 1 || (int64_t)(Hq / Hkv) * Mq > kMaxRows) return 0;
+    return paged_decode_workspace_bytes(B, Hkv, (Hq / Hkv) * Mq, sm_count_or_default());
+}
+
+fx_status fx_paged_decode(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
+                          int64_t q_stride_i, int Hq, int Mq, const int32_t* idx, int k, const int32_t* tail_lo,
+                          float scale, float* out, float* lse, void* ws, size_t ws_bytes, unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_decode");
+    PagedAttnParams p;
+    fx_status st = paged_queries(cache, q, q_stride_b, q_stride_h, q_stride_i, Hq, Mq, scale, flags, &p);
+    if (st != FX_OK) return st;
+    if (!out || !aligned16(out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+    if (k < 0 || (k > 0 && !idx)) return fail(FX_ERR_INVALID_ARG, "need k >= 0 and idx when k > 0");
+    if (k > (1 << 30)) return fail(FX_ERR_UNSUPPORTED, "k is at most 2^30");
+    const size_t need = paged_decode_workspace_bytes(p.c.B, p.c.Hkv, p.R, sm_count_or_default());
+    if ((st = check_ws(ws, ws_bytes, need)) != FX_OK) return st;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.idx = k > 0 ? idx : nullptr;
+    p.kk = k;
+    p.tail_lo = tail_lo;
+    p.out = out;
+    p.lse = lse;
+    p.counters = static_cast<unsigned*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
+    p.err = ds->err;
+    cudaError_t e = launch_paged_decode(p, cache->format == FX_PAGED_E2M1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
+                                        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+    return FX_OK;
+}
+
+fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
+                              int64_t q_stride_i, int Hq, int Mq, const float* lse, float scale, int cand_lo,
+                              int cand_hi, float* scores, unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_importance");
+    PagedAttnParams p;
+    fx_status st = paged_queries(cache, q, q_stride_b, q_stride_h, q_stride_i, Hq, Mq, scale, flags, &p);
+    if (st != FX_OK) return st;
+    if (!lse || !scores) return fail(FX_ERR_INVALID_ARG, "lse and scores must be non-NULL");
+    if (cand_lo < 0 || cand_hi < cand_lo || cand_hi > p.c.cap)
+        return fail(FX_ERR_INVALID_ARG, "need 0 <= cand_lo (%d) <= cand_hi (%d) <= %d", cand_lo, cand_hi, p.c.cap);
+    if (cand_lo == cand_hi) return FX_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.lse = const_cast<float*>(lse);
+    p.cand_lo = cand_lo;
+    p.cand_hi = cand_hi;
+    p.scores = scores;
+    p.err = ds->err;
+    cudaError_t e = launch_paged_importance(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+                                            static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged importance launch");
+    return FX_OK;
+}
+
 }  // extern "C"
 
 // Tensor maps of one layer's K and V for the streaming decode kernel: [B][Hkv][Tcap][128] bf16 with the

@@ -216,6 +216,67 @@ struct AppendParams {
     unsigned* err;
 };
 
+// One layer's paged cache as the kernels see it: strides in bytes.
+struct PagedCache {
+    char* k;
+    char* v;
+    char* ks;               // e4m3 scale rows (4-bit format), else nullptr
+    char* vs;
+    const int32_t* table;
+    const int32_t* len;
+    int64_t sp, sh, st;     // page, head, row
+    int64_t ssp, ssh, sst;  // the same of the scale rows
+    int64_t table_stride;
+    int B, Hkv, n_pages, cap;   // cap = max_pages * page_rows
+    int page_shift, page_mask;
+    float k_mul, v_mul;     // 2^k_exp, 2^v_exp
+    float k_inv, v_inv;     // 2^-k_exp, 2^-v_exp
+};
+
+struct PagedAppendParams {
+    PagedCache c;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t n_stride, h_stride;
+    const uint16_t* q;
+    uint16_t* q_out;
+    int64_t q_n, q_h, qo_n, qo_h;
+    const int32_t* seq;
+    const int32_t* pos;
+    const int32_t* rope_pos;
+    const float* cos_sin;
+    int n, Hq, rot, n_pos, interleaved;   // Hq = 0: no queries
+    unsigned* err;
+};
+
+struct PagedGatherParams {
+    PagedCache c;
+    const int32_t* idx;
+    const int32_t* lo;
+    int n;
+    uint16_t* k_out;
+    uint16_t* v_out;
+    unsigned* err;
+};
+
+struct PagedAttnParams {
+    PagedCache c;
+    const uint16_t* q;
+    int64_t q_b, q_h, q_i;
+    int Hq, G, Mq, R;
+    const int32_t* idx;
+    int kk;
+    const int32_t* tail_lo;
+    float qscale;             // scale * log2(e) * 2^k_exp: logits are kept in base-2 units
+    float* out;               // [B, Hq, Mq, 128]
+    float* lse;               // [B, Hq, Mq], natural logarithm (decode: written or nullptr; importance: read)
+    int cand_lo, cand_hi;     // importance
+    float* scores;
+    unsigned* counters;       // decode: arrival counters (zero between calls), then the split partials
+    float* part;
+    unsigned* err;
+};
+
 // An NVTX range over one library call, so that profiler timelines show each fx_* call by name (header-only
 // NVTX v3: without a tool attached a push/pop costs a few nanoseconds).
 struct NvtxRange {
@@ -256,6 +317,12 @@ cudaError_t launch_focal_mass(const float* scores, int rows, int n, float inv_r,
                               bool pdl, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams& p, bool pdl, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, bool pdl, cudaStream_t s);
+// Paged cache (paged_rows.cu, paged_attn.cu); `e2m1`: the 4-bit format.
+cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, bool pdl, cudaStream_t s);
+size_t paged_decode_workspace_bytes(int B, int Hkv, int R, int sm_count);
 
 // Launch `kern` with optional programmatic stream serialization and a (1, cluster_y, 1) cluster.
 template <typename... KArgs, typename... Args>
