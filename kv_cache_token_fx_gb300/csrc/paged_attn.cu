@@ -455,50 +455,62 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[n][e] = fast_exp2(x2[n][e]);
-                l[n][e & 1] += s[n][e];
+                float w = fast_exp2(x2[n][e]);
+                if (!E2M1) {
+                    // to 17 bits, which the two bf16 parts hold exactly: the sum then counts the weights as
+                    // they are multiplied (one weight far above the others comes out as 1)
+                    const float c = __fmul_rn(w, 129.f);
+                    w = __fsub_rn(c, __fsub_rn(c, w));
+                }
+                s[n][e] = w;
+                l[n][e & 1] += w;
             }
 
-        // O^T += V^T P^T with P as a sum of two 16-bit parts
-        auto product = [&](const float (&pr)[NT][4], uint32_t vm) {
-            uint32_t bh[NT][2], bl[NT][2];
+        // O^T += V^T P^T with P as a sum of two 16-bit parts.  Each tile's product starts from zero and is added
+        // to O by an fp32 addition: the tensor core aligns all products to the accumulator and cuts them off
+        // (2^-23 of it), which over a long row costs small weights beside a large one, and drifts.
+        uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t hi, lo2;
-                    split_p<E2M1>(pr[n][2 * u], pr[n][2 * u + 1], hi, lo2);
-                    if (DUP) {
-                        bh[n][u] = movmatrix_t(t < 2 ? hi : lo2);
-                    } else {
-                        bh[n][u] = movmatrix_t(hi);
-                        bl[n][u] = movmatrix_t(lo2);
-                    }
+            for (int u = 0; u < 2; ++u) {
+                uint32_t hi, lo2;
+                split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo2);
+                if (DUP) {
+                    bh[n][u] = movmatrix_t(t < 2 ? hi : lo2);
+                } else {
+                    bh[n][u] = movmatrix_t(hi);
+                    bl[n][u] = movmatrix_t(lo2);
                 }
+            }
+        auto product = [&](uint32_t vm, uint32_t add) {   // bit 2n + e of add: row 2t + e of N tile n takes it
             v_tiles<E2M1>(x, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma16<E2M1>(o[n][i], a0, a1, a2, a3, bh[n][0], bh[n][1]);
-                    if (!DUP) mma16<E2M1>(o[n][i], a0, a1, a2, a3, bl[n][0], bl[n][1]);
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
+                    if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((add >> (2 * n + (e & 1))) & 1u) o[n][i][e] += c[e];
                 }
             });
         };
         if (!late) {
-            product(s, rows.vm);
+            product(rows.vm, 0xffffu);
         } else {
-            // rows that only later queries see: one product per query position, with the rows it does not
-            // see as zeros (their values may be anything, and 0 * NaN is NaN)
+            // rows that only later queries see: one product per query position, over the rows it sees (the
+            // others may hold anything, and 0 * NaN is NaN) and for its query rows alone
             for (int i = 0; i < p.Mq; ++i) {
-                float si[NT][4];
+                uint32_t add = 0;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
-                        si[n][e] = r % p.Mq == i ? s[n][e] : 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
+                        if (r % p.Mq == i) add |= 1u << (2 * n + e);
                     }
-                const uint32_t vi = __ballot_sync(kFull, rows.pos <= seen + i) & rows.vm;
-                product(si, vi);
+                product(__ballot_sync(kFull, rows.pos <= seen + i) & rows.vm, add);
             }
         }
     }

@@ -155,12 +155,13 @@ class Cache:
 
 
 def attend(c, q, scale, idx=None, tail_lo=None):
-    """fx_paged_decode in 64 bits: (out [B, Hq, Mq, 128], lse [B, Hq, Mq], mag [B, Hq, Mq, 128], dl [B, Hq, Mq]).
-    mag = sum p |v|; dl = the largest scale * sum_d |q_d k_d| of a row (what a logit's error is relative to)."""
+    """fx_paged_decode in 64 bits: (out [B, Hq, Mq, 128], lse [B, Hq, Mq], mag [B, Hq, Mq, 128], dl [B, Hq, Mq],
+    far [B, Hq, Mq, 128]).  mag = sum p |v|; far = sum |v|; dl = the largest scale * sum_d |q_d k_d| of a row (what
+    a logit's error is relative to)."""
     q = np.asarray(q, np.float64)
     B, Hq, Mq, _ = q.shape
     G = Hq // c.Hkv
-    out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    out, mag, far = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     lse, dl = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
     for b in range(B):
         for g in range(Hq):
@@ -175,10 +176,10 @@ def attend(c, q, scale, idx=None, tail_lo=None):
                 e = np.exp(x - m)
                 z = e.sum()
                 p = e / z
-                out[b, g, i], mag[b, g, i] = p @ v, p @ np.abs(v)
+                out[b, g, i], mag[b, g, i], far[b, g, i] = p @ v, p @ np.abs(v), np.abs(v).sum(0)
                 lse[b, g, i] = m + np.log(z)
                 dl[b, g, i] = abs(scale) * (np.abs(k) @ np.abs(q[b, g, i])).max()
-    return out, lse, mag, dl
+    return out, lse, mag, dl, far
 
 
 def importance(c, q, lse, scale, lo, hi):

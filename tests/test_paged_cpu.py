@@ -164,13 +164,13 @@ def test_quantize_borders_and_blocks_that_are_not_finite():
 def test_attend_closed_forms():
     c = pr.Cache("bf16", [5, 0, 20], 2, 16, seed=3)
     q = np.zeros((3, 4, 2, 128))
-    out, lse, mag, _ = pr.attend(c, q, 1.0)
+    out, lse, _, _, _ = pr.attend(c, q, 1.0)
     assert np.allclose(out[0, 0, 1], c.rows(1, 0, 0, range(5)).mean(0)) and np.allclose(lse[0, :, 1], np.log(5))
     assert np.allclose(out[0, 3, 0], c.rows(1, 0, 1, range(4)).mean(0))        # query 0 does not see the last row
     assert not out[1].any() and np.all(lse[1] == -np.inf)
     s, _ = pr.importance(c, q, lse, 1.0, 0, 20)
     assert np.allclose(s.sum(-1), [[4, 4], [0, 0], [4, 4]])                    # 2 heads x 2 positions
     idx = np.array([[[3, 3, -1]] * 2, [[0, 1, 2]] * 2, [[19, 2, 7]] * 2])
-    out, lse, _, _ = pr.attend(c, q, 1.0, idx, [4, 0, 20])
+    out, lse, _, _, _ = pr.attend(c, q, 1.0, idx, [4, 0, 20])
     v = lambda at: c.rows(1, 0, 0, at)  # noqa: E731
     assert np.allclose(out[0, 0, 1], (2 * v(3) + v(4)) / 3) and np.allclose(out[0, 0, 0], v(3))
