@@ -1193,7 +1193,7 @@ fx_status fx_paged_gather(const fx_paged_desc* cache, const int32_t* idx, const 
 size_t fx_paged_decode_workspace_bytes(int B, int Hkv, int Hq, int Mq)
 {
     if (B < 1 || Hkv < 1 || Hq < Hkv || Mq < 1 || (int64_t)(Hq / Hkv) * Mq > kMaxRows) return 0;
-    return paged_decode_workspace_bytes(B, Hkv, (Hq / Hkv) * Mq, sm_count_or_default());
+    return paged_decode_workspace_bytes((Hq / Hkv) * Mq, sm_count_or_default());
 }
 
 fx_status fx_paged_decode(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
@@ -1207,7 +1207,7 @@ fx_status fx_paged_decode(const fx_paged_desc* cache, const fx_bf16* q, int64_t 
     if (!out || !aligned16(out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
     if (k < 0 || (k > 0 && !idx)) return fail(FX_ERR_INVALID_ARG, "need k >= 0 and idx when k > 0");
     if (k > (1 << 30)) return fail(FX_ERR_UNSUPPORTED, "k is at most 2^30");
-    const size_t need = paged_decode_workspace_bytes(p.c.B, p.c.Hkv, p.R, sm_count_or_default());
+    const size_t need = paged_decode_workspace_bytes(p.R, sm_count_or_default());
     if ((st = check_ws(ws, ws_bytes, need)) != FX_OK) return st;
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != FX_OK) return st;

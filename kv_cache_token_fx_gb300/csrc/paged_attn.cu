@@ -29,6 +29,7 @@ namespace {
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTileRows = 16;
+constexpr int kMinTiles = 2;   // tiles a warp gets at least, before more CTAs share a call
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -294,276 +295,525 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
     }
 }
 
-// The rows of tile `it` of a sequence: the first nl tiles hold the list, the others the tail, whose tiles start
-// at multiples of 16 (so that a tile lies inside one page).
-__device__ __forceinline__ Rows tile_rows(const PagedAttnParams& p, int b, int h, int it, int nl, int lo, int len)
+// A tile of a sequence in three steps, each needing what the one before loaded: the lane's row (position), its
+// page, its place in the pool.  The first nl tiles hold the list, the others the tail, whose tiles start at
+// multiples of 16 (so that such a tile lies inside one page).
+struct Seq {
+    const int32_t* idx;     // the list of (b, h)
+    const int32_t* table;   // the pages of b
+    int nl, lo, len;        // list tiles, start of the tail, rows
+};
+__device__ __forceinline__ int tile_pos(const PagedAttnParams& p, const Seq& q, int it)   // -1: no such row
 {
     const int j = threadIdx.x & 15;
-    Rows r;
-    bool ok;
-    if (it < nl) {
+    if (it < q.nl) {
         const int e = it * kTileRows + j;
-        ok = e < p.kk;
-        r.pos = ok ? p.idx[((int64_t)b * p.c.Hkv + h) * p.kk + e] : 0;
-        if (ok && (r.pos < 0 || r.pos >= len)) {
-            ok = false;
-            atomicOr(p.err, FX_DEVERR_INDEX);
-        }
-    } else {
-        r.pos = (lo & ~(kTileRows - 1)) + (it - nl) * kTileRows + j;
-        ok = r.pos >= lo && r.pos < len;
+        return e < p.kk ? q.idx[e] : -1;
     }
-    r.id = 0;
-    if (ok) {
-        const int pg = paged_page(p.c, b, r.pos, p.err);
-        ok = pg >= 0;
-        if (ok) r.id = (pg << p.c.page_shift) | (r.pos & p.c.page_mask);
+    const int pos = (q.lo & ~(kTileRows - 1)) + (it - q.nl) * kTileRows + j;
+    return pos >= q.lo && pos < q.len ? pos : -1;
+}
+__device__ __forceinline__ int tile_page(const PagedAttnParams& p, const Seq& q, int it, int& pos)
+{
+    if (it < q.nl && (unsigned)pos >= (unsigned)q.len) {
+        if (it * kTileRows + (int)(threadIdx.x & 15) < p.kk) atomicOr(p.err, FX_DEVERR_INDEX);
+        pos = -1;
     }
+    return pos >= 0 ? q.table[pos >> p.c.page_shift] : 0;
+}
+__device__ __forceinline__ Rows tile_place(const PagedAttnParams& p, int pos, int page)
+{
+    Rows r;
+    bool ok = pos >= 0;
+    if (ok && (unsigned)page >= (unsigned)p.c.n_pages) {
+        atomicOr(p.err, FX_DEVERR_PAGE);
+        ok = false;
+    }
+    r.pos = pos;
+    r.id = ok ? (page << p.c.page_shift) | (pos & p.c.page_mask) : 0;
     r.vm = __ballot_sync(kFull, ok) & 0xffffu;
     return r;
 }
 
-// One CTA attends NT * 8 query rows (4 with DUP) of one (sequence, KV head) over all its tiles.
-// DUP: at most 4 query rows; columns 4..7 repeat them, so that one product takes P's high part (columns
-// 0..3) and its low part (4..7).
+// Joins the warps' partials of one query row in shared memory: the sum over them of dimension d, with the row's
+// reference m (-inf: no warp saw anything) and its sum z.
+template <int kRows>
+__device__ __forceinline__ float join_row(const float* sm_o, const float* sm_m, const float* sm_l, int row, int d,
+                                          float& m, float& z)
+{
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w * kRows + row]);
+    z = 0.f;
+    float acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        const float mw = sm_m[w * kRows + row];
+        if (mw == -INFINITY) continue;   // that warp saw nothing
+        const float f = fast_exp2(mw - m);
+        z += f * sm_l[w * kRows + row];
+        acc += f * sm_o[(w * kRows + row) * kHeadDim + d];
+    }
+    return acc;
+}
+
+// The query rows of one warp and what it has summed for them.
+template <bool E2M1, int NT, bool DUP>
+struct Acc {
+    uint32_t q[NT][8][2];
+    float rs[NT][2];      // factor of the logits of rows 2t, 2t+1 (of each N tile)
+    float bias[NT][2];    // minus the reference of those rows; +inf: none yet
+    float l[NT][2];
+    float o[NT][8][4];
+};
+
+// Weights of a tile from its logits s (row g + 8 (e >> 1) of the tile, query row 2t + (e & 1) of N tile n), in
+// place; moves the references when one would not fit.  hide: bit 4n + e, that logit does not count.
+template <bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4], uint32_t hide)
+{
+    float x2[NT][4];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x2[n][e] = fmaf(s[n][e], a.rs[n][e & 1], a.bias[n][e & 1]);
+            if ((hide >> (4 * n + e)) & 1u) x2[n][e] = -INFINITY;
+            over |= x2[n][e] > kTop;
+        }
+    if (__any_sync(kFull, over)) {
+        // new references: the largest logit of each row lands on 2^kBase
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float z0 = (hide >> (4 * n + e)) & 1u ? -INFINITY : s[n][e] * a.rs[n][e];
+                const float z1 = (hide >> (4 * n + e + 2)) & 1u ? -INFINITY : s[n][e + 2] * a.rs[n][e];
+                float m = fmaxf(z0, z1);
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+                const float nb = fminf(a.bias[n][e], kBase - m);
+                if (nb < a.bias[n][e]) {   // never for a row without a visible logit
+                    const float f = fast_exp2(nb - a.bias[n][e]);   // 0 for the first reference
+                    a.l[n][e] *= f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a.o[n][i][e] *= f;
+                        a.o[n][i][e + 2] *= f;
+                    }
+                    a.bias[n][e] = nb;
+                }
+                x2[n][e] = (hide >> (4 * n + e)) & 1u ? -INFINITY : fmaf(s[n][e], a.rs[n][e], nb);
+                x2[n][e + 2] = (hide >> (4 * n + e + 2)) & 1u ? -INFINITY : fmaf(s[n][e + 2], a.rs[n][e], nb);
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float w = fast_exp2(x2[n][e]);
+            if (!E2M1) {
+                // to 17 bits, which the two bf16 parts hold exactly: the sum then counts the weights as
+                // they are multiplied (one weight far above the others comes out as 1)
+                const float c = __fmul_rn(w, 129.f);
+                w = __fsub_rn(c, __fsub_rn(c, w));
+            }
+            s[n][e] = w;
+            a.l[n][e & 1] += w;
+        }
+}
+
+// One tile: logits, weights, O^T += V^T P^T.  after_k and after_v run when the tile's K and V rows are no longer
+// needed (the caller loads the next tile into them).
+template <bool E2M1, int NT, bool DUP, typename FK, typename FV>
+__device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, Tile<E2M1>& x,
+                                            const Rows& rows, int r0, int seen, FK&& after_k, FV&& after_v)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float s[NT][4];
+    {
+        float s2[NT][2][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s2[n][e >> 2][e & 3] = 0.f;
+        k_steps<E2M1>(x, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+        });
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
+    }
+    after_k();
+    const bool late = __any_sync(kFull, ((rows.vm >> (lane & 15)) & 1u) && rows.pos > seen);
+    uint32_t hide = 0;
+    if (late || rows.vm != 0xffffu) {
+        const int p0 = __shfl_sync(kFull, rows.pos, g), p1 = __shfl_sync(kFull, rows.pos, g + 8);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
+                const bool see = ((rows.vm >> (g + 8 * (e >> 1))) & 1u) && (e >> 1 ? p1 : p0) <= seen + r % p.Mq;
+                if (!see) hide |= 1u << (4 * n + e);
+            }
+    }
+    weights<E2M1, NT, DUP>(a, s, hide);
+
+    // O^T += V^T P^T with P as a sum of two 16-bit parts.  Each tile's product starts from zero and is added
+    // to O by an fp32 addition: the tensor core aligns all products to the accumulator and cuts them off
+    // (2^-23 of it), which over a long row costs small weights beside a large one, and drifts.
+    uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t hi, lo2;
+            split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo2);
+            if (DUP) {
+                bh[n][u] = movmatrix_t(t < 2 ? hi : lo2);
+            } else {
+                bh[n][u] = movmatrix_t(hi);
+                bl[n][u] = movmatrix_t(lo2);
+            }
+        }
+    auto product = [&](uint32_t vm, auto&& adds) {   // adds(n, e): query row 2t + e of N tile n takes it
+        v_tiles<E2M1>(x, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
+                if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (adds(n, e & 1)) a.o[n][i][e] += c[e];
+            }
+        });
+    };
+    if (!late) {
+        product(rows.vm, [](int, int) { return true; });
+    } else {
+        // rows that only later queries see: one product per query position, over the rows it sees (the
+        // others may hold anything, and 0 * NaN is NaN) and for its query rows alone
+        for (int i = 0; i < p.Mq; ++i) {
+            uint32_t add = 0;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
+                    if (r % p.Mq == i) add |= 1u << (2 * n + e);
+                }
+            product(__ballot_sync(kFull, rows.pos <= seen + i) & rows.vm,
+                    [&](int n, int e) { return ((add >> (2 * n + e)) & 1u) != 0; });
+        }
+    }
+    after_v();
+}
+
+// Query rows of one CTA's pass over a (sequence, KV head).
+template <int NT, bool DUP>
+__host__ __device__ constexpr int pass_rows() { return DUP ? 4 : 8 * NT; }
+
+// Tiles of sequence b (at least one: an empty sequence's tile holds no valid row, and its output is written).
+__device__ __forceinline__ Seq sequence(const PagedAttnParams& p, int b, bool report)
+{
+    Seq q;
+    q.len = p.c.len[b];
+    q.lo = p.tail_lo ? p.tail_lo[b] : 0;
+    if (report && (q.len < 0 || q.len > p.c.cap || q.lo < 0)) atomicOr(p.err, FX_DEVERR_LEN);
+    q.len = min(max(q.len, 0), p.c.cap);
+    q.lo = max(q.lo, 0);
+    q.nl = (p.kk + kTileRows - 1) / kTileRows;
+    q.table = p.c.table + (int64_t)b * p.c.table_stride;
+    q.idx = nullptr;
+    return q;
+}
+__device__ __forceinline__ int tile_count(const Seq& q)
+{
+    const int nt = q.lo < q.len ? (q.len + kTileRows - 1) / kTileRows - q.lo / kTileRows : 0;
+    return max(q.nl + nt, 1);
+}
+
+// Decode.  The tiles of all (sequence, KV head, group of query rows) form one line, which the CTAs share out
+// evenly by the lengths found on the device, so that ragged lengths leave no CTA with more to do than another.
+// A CTA walks its stretch of the line piece by piece (one (sequence, head, group) each); its warps take a
+// piece's tiles in turn and meet in shared memory.  A piece that spans several CTAs is joined by the last of
+// them to arrive, in the order of the CTAs.
+//
+// DUP: at most 4 query rows; columns 4..7 of the products repeat them, so that one product takes P's high part
+// (columns 0..3) and its low part (4..7).
 template <bool E2M1, int NT, bool DUP>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_kernel(const PagedAttnParams p)
 {
-    constexpr int kRows = DUP ? 4 : 8 * NT;   // query rows of the CTA
+    constexpr int kRows = pass_rows<NT, DUP>();
     extern __shared__ float smem[];
     float* sm_o = smem;                                        // [warp][row][128]
     float* sm_m = smem + kAttnWarps * kRows * kHeadDim;        // [warp][row]
     float* sm_l = sm_m + kAttnWarps * kRows;
+    __shared__ long long sm_scan[kAttnWarps];
+    __shared__ int sm_b;
+    __shared__ long long sm_start;
+    __shared__ unsigned sm_last;
 
     griddep_wait();
     griddep_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int nrg = (p.R + kRows - 1) / kRows;
-    const int rg = blockIdx.x % nrg;
-    const int h = (blockIdx.x / nrg) % p.c.Hkv;
-    const int b = blockIdx.x / (nrg * p.c.Hkv);
-    const int r0 = rg * kRows;
-    const int len = paged_len(p.c, b, p.err);
-    int lo = 0;
-    if (p.tail_lo) {
-        lo = p.tail_lo[b];
-        if (lo < 0) {
-            atomicOr(p.err, FX_DEVERR_LEN);
-            lo = 0;
-        }
+    const int per_tile = p.c.Hkv * nrg;   // pieces of one sequence
+
+    // total length of the line, then this CTA's stretch of it and the sequence that it starts in
+    long long total = 0;
+    for (int b = tid; b < p.c.B; b += kAttnThreads) total += tile_count(sequence(p, b, blockIdx.x == 0));
+    {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+        if (lane == 0) sm_scan[warp] = total;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < kAttnWarps; ++w) total += sm_scan[w];
+        total *= per_tile;
     }
-    const int nl = (p.kk + kTileRows - 1) / kTileRows;
-    const int nt = lo < len ? (len + kTileRows - 1) / kTileRows - lo / kTileRows : 0;
-    const int seen = len - p.Mq;   // query i sees rows <= seen + i
-
-    uint32_t q[NT][8][2];
-    float rs[NT][2];               // factor of the logits of rows 2t, 2t+1 (of each N tile)
-    float bias[NT][2];             // minus the reference of those rows; +inf: none yet
-    float l[NT][2];
-    float o[NT][8][4];
+    const int n_cta = (int)min((long long)gridDim.x, max(1ll, total / (kAttnWarps * kMinTiles)));
+    const int cta = blockIdx.x;
+    if (cta >= n_cta) return;
+    long long at = total * cta / n_cta;                  // next tile of the line
+    const long long end = total * (cta + 1) / n_cta;
+    long long before = 0;                                // tiles (of one piece each) of the sequences before b
+    for (int b0 = 0;; b0 += kAttnThreads) {
+        const int b = b0 + tid;
+        const int n = b < p.c.B ? tile_count(sequence(p, b, false)) : 0;
+        long long inc = n;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int r = r0 + 8 * n + (DUP ? g & 3 : g);
-        const float f = load_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, q[n]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            rs[n][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
-            bias[n][e] = INFINITY;
-            l[n][e] = 0.f;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(kFull, inc, d);
+            if (lane >= d) inc += o;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+        __syncthreads();   // sm_scan is free
+        if (tid == 0) sm_b = -1;
+        if (lane == 31) sm_scan[warp] = inc;
+        __syncthreads();
+        long long sum = 0, mine = 0;
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w == warp) mine = sum;
+            sum += sm_scan[w];
+        }
+        const long long first = (before + mine + inc - n) * per_tile;
+        if (n > 0 && at >= first && at < first + (long long)n * per_tile) {
+            sm_b = b;
+            sm_start = first;
+        }
+        __syncthreads();
+        before += sum;
+        if (sm_b >= 0) break;   // always found: at < total
     }
+    int b = sm_b;
+    long long seq_start = sm_start;
+    Seq seq = sequence(p, b, false);
+    int ntile = tile_count(seq);
 
-    for (int it = warp; it < nl + nt; it += kAttnWarps) {
-        const Rows rows = tile_rows(p, b, h, it, nl, lo, len);
-        Tile<E2M1> x;
-        load_k<E2M1>(p.c, h, rows, x);
-        load_v<E2M1>(p.c, h, rows, x);
+    for (bool head = true; at < end; head = false) {
+        while (at >= seq_start + (long long)ntile * per_tile) {
+            seq_start += (long long)ntile * per_tile;
+            seq = sequence(p, ++b, false);
+            ntile = tile_count(seq);
+        }
+        const int piece = (int)((at - seq_start) / ntile);
+        const long long piece_start = seq_start + (long long)piece * ntile;
+        const int h = piece / nrg, r0 = (piece - h * nrg) * kRows;
+        const int s0 = (int)(at - piece_start), s1 = (int)min((long long)ntile, end - piece_start);
+        const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
+        seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
-        float s[NT][4];
-        {
-            float s2[NT][2][4];
+        Acc<E2M1, NT, DUP> a;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const int r = r0 + 8 * n + (DUP ? g & 3 : g);
+            const float f = load_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[n]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s2[n][e >> 2][e & 3] = 0.f;
-            k_steps<E2M1>(x, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, q[n][j][0], q[n][j][1]);
-            });
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
-        }
-        // logits of rows g, g + 8 of the tile (e >> 1) and query rows 2t, 2t + 1 (e & 1)
-        const bool late = __any_sync(kFull, ((rows.vm >> (lane & 15)) & 1u) && rows.pos > seen);
-        const bool edge = late || rows.vm != 0xffffu;
-        uint32_t hide = 0;   // bit 4n + e: that logit does not count
-        if (edge) {
-            const int p0 = __shfl_sync(kFull, rows.pos, g), p1 = __shfl_sync(kFull, rows.pos, g + 8);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
-                    const bool see = ((rows.vm >> (g + 8 * (e >> 1))) & 1u) && (e >> 1 ? p1 : p0) <= seen + r % p.Mq;
-                    if (!see) hide |= 1u << (4 * n + e);
-                }
-        }
-        float x2[NT][4];
-        bool over = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x2[n][e] = fmaf(s[n][e], rs[n][e & 1], bias[n][e & 1]);
-                if ((hide >> (4 * n + e)) & 1u) x2[n][e] = -INFINITY;
-                over |= x2[n][e] > kTop;
+            for (int e = 0; e < 2; ++e) {
+                a.rs[n][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
+                a.bias[n][e] = INFINITY;
+                a.l[n][e] = 0.f;
             }
-        if (__any_sync(kFull, over)) {
-            // new references: the largest logit of each row lands on 2^kBase
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float z0 = (hide >> (4 * n + e)) & 1u ? -INFINITY : s[n][e] * rs[n][e];
-                    const float z1 = (hide >> (4 * n + e + 2)) & 1u ? -INFINITY : s[n][e + 2] * rs[n][e];
-                    float m = fmaxf(z0, z1);
-                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-                    const float nb = fminf(bias[n][e], kBase - m);
-                    if (nb < bias[n][e]) {   // never for a row without a visible logit
-                        const float f = fast_exp2(nb - bias[n][e]);   // 0 for the first reference
-                        l[n][e] *= f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            o[n][i][e] *= f;
-                            o[n][i][e + 2] *= f;
-                        }
-                        bias[n][e] = nb;
+                for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
+        }
+
+        // the warp's tiles s0 + warp, + 8, ...: the rows of the next one are loaded while one is worked on, its
+        // pages one tile earlier, its positions another one earlier
+        int it = s0 + warp;
+        if (it < s1) {
+            int pos = tile_pos(p, seq, it);
+            int page = tile_page(p, seq, it, pos);
+            Rows rows = tile_place(p, pos, page);
+            int pos1 = it + kAttnWarps < s1 ? tile_pos(p, seq, it + kAttnWarps) : -1;
+            int page1 = it + kAttnWarps < s1 ? tile_page(p, seq, it + kAttnWarps, pos1) : 0;
+            int pos2 = it + 2 * kAttnWarps < s1 ? tile_pos(p, seq, it + 2 * kAttnWarps) : -1;
+            Rows next;
+            auto advance = [&]() {   // places the next tile, looks the one after it up
+                next = tile_place(p, pos1, page1);
+                const int i2 = it + 2 * kAttnWarps, i3 = it + 3 * kAttnWarps;
+                page1 = i2 < s1 ? tile_page(p, seq, i2, pos2) : 0;
+                pos1 = pos2;
+                pos2 = i3 < s1 ? tile_pos(p, seq, i3) : -1;
+            };
+            if constexpr (E2M1) {
+                Tile<E2M1> x, y;
+                load_k<E2M1>(p.c, h, rows, x);
+                load_v<E2M1>(p.c, h, rows, x);
+                auto turn = [&](Tile<E2M1>& cur, Tile<E2M1>& nxt) {
+                    advance();
+                    if (it + kAttnWarps < s1) {
+                        load_k<E2M1>(p.c, h, next, nxt);
+                        load_v<E2M1>(p.c, h, next, nxt);
                     }
-                    x2[n][e] = (hide >> (4 * n + e)) & 1u ? -INFINITY : fmaf(s[n][e], rs[n][e], nb);
-                    x2[n][e + 2] = (hide >> (4 * n + e + 2)) & 1u ? -INFINITY : fmaf(s[n][e + 2], rs[n][e], nb);
+                    attend_tile<E2M1, NT, DUP>(p, a, cur, rows, r0, seen, [] {}, [] {});
+                    rows = next;
+                    it += kAttnWarps;
+                };
+                while (true) {
+                    turn(x, y);
+                    if (it >= s1) break;
+                    turn(y, x);
+                    if (it >= s1) break;
                 }
+            } else {
+                // bf16 rows fill 64 registers a lane: the next K takes the place of this tile's once the logits
+                // are there, the next V that of this one's after the product
+                Tile<E2M1> x;
+                load_k<E2M1>(p.c, h, rows, x);
+                load_v<E2M1>(p.c, h, rows, x);
+                for (; it < s1; it += kAttnWarps) {
+                    advance();
+                    const bool more = it + kAttnWarps < s1;
+                    attend_tile<E2M1, NT, DUP>(
+                        p, a, x, rows, r0, seen, [&] { if (more) load_k<E2M1>(p.c, h, next, x); },
+                        [&] { if (more) load_v<E2M1>(p.c, h, next, x); });
+                    rows = next;
+                }
+            }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float w = fast_exp2(x2[n][e]);
-                if (!E2M1) {
-                    // to 17 bits, which the two bf16 parts hold exactly: the sum then counts the weights as
-                    // they are multiplied (one weight far above the others comes out as 1)
-                    const float c = __fmul_rn(w, 129.f);
-                    w = __fsub_rn(c, __fsub_rn(c, w));
-                }
-                s[n][e] = w;
-                l[n][e & 1] += w;
-            }
 
-        // O^T += V^T P^T with P as a sum of two 16-bit parts.  Each tile's product starts from zero and is added
-        // to O by an fp32 addition: the tensor core aligns all products to the accumulator and cuts them off
-        // (2^-23 of it), which over a long row costs small weights beside a large one, and drifts.
-        uint32_t bh[NT][2], bl[NT][2];
+        // the warps' partials meet in shared memory
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t hi, lo2;
-                split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo2);
-                if (DUP) {
-                    bh[n][u] = movmatrix_t(t < 2 ? hi : lo2);
-                } else {
-                    bh[n][u] = movmatrix_t(hi);
-                    bl[n][u] = movmatrix_t(lo2);
+            for (int e = 0; e < 2; ++e) {
+                float z = a.l[n][e];
+                z += __shfl_xor_sync(kFull, z, 4);
+                z += __shfl_xor_sync(kFull, z, 8);
+                z += __shfl_xor_sync(kFull, z, 16);
+                const int row = 8 * n + 2 * t + e;
+                if (g == 0 && row < kRows) {
+                    sm_m[warp * kRows + row] = z != z ? 0.f : -a.bias[n][e];   // a NaN logit leaves no reference but shows
+                    sm_l[warp * kRows + row] = z;
                 }
             }
-        auto product = [&](uint32_t vm, uint32_t add) {   // bit 2n + e of add: row 2t + e of N tile n takes it
-            v_tiles<E2M1>(x, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
-                    if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((add >> (2 * n + (e & 1))) & 1u) o[n][i][e] += c[e];
+            for (int i = 0; i < 8; ++i) {
+                if (DUP) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a.o[n][i][e] += __shfl_xor_sync(kFull, a.o[n][i][e], 2);
                 }
-            });
-        };
-        if (!late) {
-            product(rows.vm, 0xffffu);
-        } else {
-            // rows that only later queries see: one product per query position, over the rows it sees (the
-            // others may hold anything, and 0 * NaN is NaN) and for its query rows alone
-            for (int i = 0; i < p.Mq; ++i) {
-                uint32_t add = 0;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
+                if (!DUP || t < 2) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
-                        if (r % p.Mq == i) add |= 1u << (2 * n + e);
+                        float* to = sm_o + ((warp * kRows + 8 * n + 2 * t + e) * kHeadDim + v_dim<E2M1>(i, g));
+                        *reinterpret_cast<float2*>(to) = make_float2(a.o[n][i][e], a.o[n][i][e + 2]);
                     }
-                product(__ballot_sync(kFull, rows.pos <= seen + i) & rows.vm, add);
-            }
-        }
-    }
-
-    // the warps' partials meet in shared memory
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float z = l[n][e];
-            z += __shfl_xor_sync(kFull, z, 4);
-            z += __shfl_xor_sync(kFull, z, 8);
-            z += __shfl_xor_sync(kFull, z, 16);
-            const int row = 8 * n + 2 * t + e;
-            if (g == 0 && row < kRows) {
-                sm_m[warp * kRows + row] = z != z ? 0.f : -bias[n][e];   // a NaN logit leaves no reference but shows
-                sm_l[warp * kRows + row] = z;
-            }
-        }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (DUP) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][i][e] += __shfl_xor_sync(kFull, o[n][i][e], 2);
-            }
-            if (!DUP || t < 2) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float* at = sm_o + ((warp * kRows + 8 * n + 2 * t + e) * kHeadDim + v_dim<E2M1>(i, g));
-                    *reinterpret_cast<float2*>(at) = make_float2(o[n][i][e], o[n][i][e + 2]);
                 }
             }
+        __syncthreads();
+
+        const bool whole = s0 == 0 && s1 == ntile;
+        if (!whole) {
+            // this CTA's part of the piece goes to its slot; the last CTA to arrive takes all of them over
+            const int slot = cta * 2 + (head ? 0 : 1);
+            float* part = p.part + (size_t)slot * kRows * (kHeadDim + 2);
+            const int d = tid & (kHeadDim - 1);
+            for (int row = tid / kHeadDim; row < kRows; row += kAttnThreads / kHeadDim) {
+                float z, m;
+                const float acc = join_row<kRows>(sm_o, sm_m, sm_l, row, d, m, z);
+                part[row * kHeadDim + d] = acc;
+                if (d == 0) {
+                    part[kRows * kHeadDim + row] = m;
+                    part[kRows * kHeadDim + kRows + row] = z;
+                }
+            }
+            // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
+            const int c0 = (int)(((piece_start + 1) * n_cta - 1) / total);
+            const int c1 = (int)(((piece_start + ntile) * n_cta - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const unsigned n = atomicAdd(p.counters + c0, 1u);
+                sm_last = n == (unsigned)(c1 - c0);
+                if (sm_last) {
+                    p.counters[c0] = 0;   // ready for the next call
+                    __threadfence();
+                }
+            }
+            __syncthreads();
+            if (!sm_last) {
+                at = piece_start + s1;
+                continue;
+            }
+            // each warp takes every eighth part, then the warps' sums meet as before.  A CTA's first piece is in
+            // its slot 0; the piece starts in c0, as that CTA's first piece only if it starts its stretch
+            const int s_first = c0 * 2 + (total * c0 / n_cta == piece_start ? 0 : 1);
+            for (int row = 0; row < kRows; ++row) {
+                float m = -INFINITY;
+                for (int c = c0 + warp + kAttnWarps * lane; c <= c1; c += kAttnWarps * 32) {
+                    const int sl = c == c0 ? s_first : c * 2;
+                    m = fmaxf(m, __ldcg(p.part + (size_t)sl * kRows * (kHeadDim + 2) + kRows * kHeadDim + row));
+                }
+#pragma unroll
+                for (int d2 = 16; d2; d2 >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d2));
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float z = 0.f;
+#pragma unroll 4
+                for (int c = c0 + warp; c <= c1; c += kAttnWarps) {
+                    const int sl = c == c0 ? s_first : c * 2;
+                    const float* from = p.part + (size_t)sl * kRows * (kHeadDim + 2);
+                    const float mc = __ldcg(from + kRows * kHeadDim + row);
+                    const float lc = __ldcg(from + kRows * kHeadDim + kRows + row);
+                    const float4 oc = __ldcg(reinterpret_cast<const float4*>(from + row * kHeadDim) + lane);
+                    const float f = mc == -INFINITY ? 0.f : fast_exp2(mc - m);
+                    z += f * lc;
+                    acc.x += f * oc.x;
+                    acc.y += f * oc.y;
+                    acc.z += f * oc.z;
+                    acc.w += f * oc.w;
+                }
+                *(reinterpret_cast<float4*>(sm_o + (warp * kRows + row) * kHeadDim) + lane) = acc;
+                if (lane == 0) {
+                    sm_m[warp * kRows + row] = m;
+                    sm_l[warp * kRows + row] = z;
+                }
+            }
+            __syncthreads();
         }
-    __syncthreads();
-    const int d = threadIdx.x & (kHeadDim - 1);
-    for (int row = threadIdx.x / kHeadDim; row < kRows && r0 + row < p.R; row += kAttnThreads / kHeadDim) {
-        float m = -INFINITY;
-        for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w * kRows + row]);
-        float z = 0.f, acc = 0.f;
-        for (int w = 0; w < kAttnWarps; ++w) {
-            const float mw = sm_m[w * kRows + row];
-            if (mw == -INFINITY) continue;   // that warp saw nothing
-            const float f = fast_exp2(mw - m);
-            z += f * sm_l[w * kRows + row];
-            acc += f * sm_o[(w * kRows + row) * kHeadDim + d];
+        const int d = tid & (kHeadDim - 1);
+        for (int row = tid / kHeadDim; row < kRows && r0 + row < p.R; row += kAttnThreads / kHeadDim) {
+            float z, m;
+            const float acc = join_row<kRows>(sm_o, sm_m, sm_l, row, d, m, z);
+            const int r = r0 + row;
+            const int64_t to = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
+            const bool none = m == -INFINITY;
+            p.out[to * kHeadDim + d] = none ? 0.f : acc / z * p.c.v_mul;
+            if (p.lse && d == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
         }
-        const int r = r0 + row;
-        const int64_t at = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
-        const bool none = m == -INFINITY;
-        p.out[at * kHeadDim + d] = none ? 0.f : acc / z * p.c.v_mul;
-        if (p.lse && d == 0) p.lse[at] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
+        __syncthreads();   // shared memory is free for the next piece
+        at = piece_start + s1;
     }
 }
 
@@ -580,8 +830,8 @@ __global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const Pa
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int h = blockIdx.y, b = blockIdx.z;
-    const int len = paged_len(p.c, b, p.err);
-    const int seen = len - p.Mq;
+    Seq seq = sequence(p, b, true);
+    const int len = seq.len, seen = len - p.Mq;
     const int ntile = (p.R + 7) / 8;
     for (int n = warp; n < ntile; n += kAttnWarps) {
         const int r = 8 * n + g;
@@ -598,13 +848,16 @@ __global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const Pa
     }
     __syncthreads();
     const int first = (p.cand_lo & ~(kTileRows - 1)) + (blockIdx.x * kAttnWarps + warp) * (kImpTiles * kTileRows);
+    seq.lo = first;
     float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * (p.cand_hi - p.cand_lo);
     for (int u = 0; u < kImpTiles; ++u) {
         const int base = first + u * kTileRows;
         if (base >= p.cand_hi) break;
         float sum[2] = {0.f, 0.f};
         if (base < len) {
-            const Rows rows = tile_rows(p, b, h, u, 0, first, len);
+            int pos = tile_pos(p, seq, u);
+            const int page = tile_page(p, seq, u, pos);
+            const Rows rows = tile_place(p, pos, page);
             Tile<E2M1> x;
             load_k<E2M1>(p.c, h, rows, x);
             uint32_t a[8][4];
@@ -642,37 +895,40 @@ __global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const Pa
     }
 }
 
+// CTAs of a decode call: as many as are resident at once (one with more than 8 query rows, else two per SM).
+int decode_ctas(int R, int sm_count) { return (R > 8 ? 1 : 2) * sm_count; }
+
 template <bool E2M1, int NT, bool DUP>
-cudaError_t launch_decode(const PagedAttnParams& p, bool pdl, cudaStream_t s)
+cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    constexpr int kRows = DUP ? 4 : 8 * NT;
+    constexpr int kRows = pass_rows<NT, DUP>();
     constexpr size_t smem = sizeof(float) * kAttnWarps * kRows * (kHeadDim + 2);
     cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<E2M1, NT, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
-    const int64_t grid = (int64_t)p.c.B * p.c.Hkv * ((p.R + kRows - 1) / kRows);
-    return launch_kernel(paged_decode_kernel<E2M1, NT, DUP>, dim3((unsigned)grid), dim3(kAttnThreads), smem, s, pdl, 0u, p);
+    return launch_kernel(paged_decode_kernel<E2M1, NT, DUP>, dim3(decode_ctas(p.R, sm_count)), dim3(kAttnThreads), smem, s,
+                         pdl, 0u, p);
 }
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int B, int Hkv, int R, int sm_count)
+// The counters' region, then two partials (one of each end of a CTA's stretch) of up to 16 query rows per CTA.
+size_t paged_decode_workspace_bytes(int R, int sm_count)
 {
-    (void)B, (void)Hkv, (void)R, (void)sm_count;
-    return kCounterBytes;
+    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16);
+    return kCounterBytes + (size_t)decode_ctas(R, sm_count) * 2 * rows * (kHeadDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    (void)sm_count;
     if (e2m1) {
-        if (p.R <= 4) return launch_decode<true, 1, true>(p, pdl, s);
-        if (p.R <= 8) return launch_decode<true, 1, false>(p, pdl, s);
-        return launch_decode<true, 2, false>(p, pdl, s);
+        if (p.R <= 4) return launch_decode<true, 1, true>(p, sm_count, pdl, s);
+        if (p.R <= 8) return launch_decode<true, 1, false>(p, sm_count, pdl, s);
+        return launch_decode<true, 2, false>(p, sm_count, pdl, s);
     }
-    if (p.R <= 4) return launch_decode<false, 1, true>(p, pdl, s);
-    if (p.R <= 8) return launch_decode<false, 1, false>(p, pdl, s);
-    return launch_decode<false, 2, false>(p, pdl, s);
+    if (p.R <= 4) return launch_decode<false, 1, true>(p, sm_count, pdl, s);
+    if (p.R <= 8) return launch_decode<false, 1, false>(p, sm_count, pdl, s);
+    return launch_decode<false, 2, false>(p, sm_count, pdl, s);
 }
 
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, bool pdl, cudaStream_t s)
