@@ -1,17 +1,17 @@
 // Attention over a paged cache for sm_103a, bf16 or 4-bit: fx_paged_decode and fx_paged_importance.
 //
-// Work unit of a warp: a tile of 16 cache rows of one (sequence, KV head).  Its K rows go from global memory
-// straight into the registers that mma.sync wants as the A operand of S^T = K Q^T (rows of K on M, the query
-// rows on N), its V rows into those of O^T += V^T P^T (dimensions on M, cache rows on K).  The dimensions of
-// K are permuted inside the product (the queries are laid out the same way), and those of O^T inside M, so that
-// a lane reads contiguous bytes: of K 16 bytes (4-bit) or four times 16 (bf16) of two rows, of V 8 bytes or two
-// times 16 of four rows.
+// Work unit of a warp: a tile of 16 cache rows of one (sequence, KV head).  Every warp owns a ring of tile slots in
+// shared memory and fills it with cp.async a few tiles ahead; no warp waits for another until their results
+// meet.  S^T = K Q^T has the cache rows on M and the query rows on N (mma.sync m16n8k16), O^T += V^T P^T the
+// dimensions on M and the cache rows on K.
 //
-// 4-bit rows: the codes become f16 by cvt.f16x2.e2m1x2, and one multiplication by the block's scale gives
-// the value held, exactly (at most 6 significant bits, between 2^-10 and 2688).  The queries are f16 scaled
-// by a power of two per row (largest magnitude in [2^14, 2^15)), so no bit of a bf16 query within 2^-24 of its
-// row's largest is lost.  P is split into f16 hi + lo (22 bits); bf16 rows take bf16 queries as they are and P
-// as bf16 hi + lo (16 bits): outputs are fp32 and one 16-bit P would leave them 2^-9 (bf16) or 2^-12 (f16) off.
+// 4-bit rows: a lane's K fragments are 16 bytes of codes of two rows (the dimensions are permuted inside the
+// product, the queries are laid out the same way), its V fragments 8 bytes of four rows (the dimensions of O^T
+// are permuted inside M).  The codes become f16 by cvt.f16x2.e2m1x2, and one multiplication by the block's scale
+// gives the value held, exactly (at most 6 significant bits, between 2^-10 and 2688).  The queries are f16
+// scaled by a power of two per row (largest magnitude in [2^14, 2^15)), so no bit of a bf16 query within 2^-24
+// of its row's largest is lost.  P is split into f16 hi + lo (22 bits); bf16 rows take bf16 queries as they are
+// and P as bf16 hi + lo (17 bits): outputs are fp32, and one 16-bit P would leave them 2^-12 (f16) or 2^-9 off.
 //
 // Softmax: base-2 logits, one pass.  p = 2^(x - m) with a reference m per row that all lanes of the row share;
 // it is set so that the largest logit so far gives 2^kBase and moves only when a p would exceed 2^kTop, so most
@@ -26,40 +26,11 @@
 namespace fx {
 namespace {
 
-constexpr int kAttnWarps = 8;
-constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTileRows = 16;
 constexpr int kMinTiles = 2;   // tiles a warp gets at least, before more CTAs share a call
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
-
-__device__ __forceinline__ uint4 ld_stream16(const char* p)
-{
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint2 ld_stream8(const char* p)
-{
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint32_t ld_u16(const char* p)
-{
-    uint16_t r;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint32_t ld_u8(const char* p)
-{
-    uint32_t r;
-    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
-}
 
 template <bool E2M1>
 __device__ __forceinline__ void mma16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -76,82 +47,219 @@ __device__ __forceinline__ void mma16(float d[4], uint32_t a0, uint32_t a1, uint
     }
 }
 
-// The 16 rows of a tile: lane L < 16 of the warp (and L + 16 again) knows row L.
-struct Rows {
-    int id;        // pool row (page * page_rows + row in page); 0 when the row is not valid
-    int pos;       // cache row (position in the sequence)
-    uint32_t vm;   // bit j: row j is valid (uniform over the warp)
-};
-
-// A tile's rows as loaded: raw bytes, two K rows and four V rows per lane.
+// The same from zero.
 template <bool E2M1>
-struct Tile;
-template <>
-struct Tile<true> {
-    uint4 k[2];
-    uint2 v[4];
-    uint32_t ks;   // two scale bytes of row g, two of row g + 8
-    uint32_t vs;   // one scale byte of each of the four V rows
+__device__ __forceinline__ void mma16_zero(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1)
+{
+    if (E2M1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    } else {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    }
+}
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a)
+{
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+
+// ---- rows of a sequence -----------------------------------------------------------------------------
+struct Seq {
+    const int32_t* idx;     // the list of (b, h)
+    const int32_t* table;   // the pages of b
+    int nl, lo, len;        // list tiles, start of the tail, rows
 };
-template <>
-struct Tile<false> {
-    uint4 k[2][4];
-    uint4 v[4][2];
-};
+// Tiles of sequence b (at least one: an empty sequence's tile holds no valid row, and its output is written).
+__device__ __forceinline__ Seq sequence(const PagedAttnParams& p, int b, bool report)
+{
+    Seq q;
+    q.len = p.c.len[b];
+    q.lo = p.tail_lo ? p.tail_lo[b] : 0;
+    if (report && (q.len < 0 || q.len > p.c.cap || q.lo < 0)) atomicOr(p.err, FX_DEVERR_LEN);
+    q.len = min(max(q.len, 0), p.c.cap);
+    q.lo = max(q.lo, 0);
+    q.nl = (p.kk + kTileRows - 1) / kTileRows;
+    q.table = p.c.table + (int64_t)b * p.c.table_stride;
+    q.idx = nullptr;
+    return q;
+}
+__device__ __forceinline__ int tile_count(const Seq& q)
+{
+    const int nt = q.lo < q.len ? (q.len + kTileRows - 1) / kTileRows - q.lo / kTileRows : 0;
+    return max(q.nl + nt, 1);
+}
+
+
+// A tile of a sequence is found in three steps, each needing what the one before loaded: a row (position), its
+// page, its place in the pool.  The first nl tiles hold the list -- lane L < 16 (and L + 16 again) knows row L --
+// the others the tail, whose tiles start at multiples of 16, so that such a tile lies inside one page.
+// List: the lane's row (-1: none).  Tail: the tile's first row.
+__device__ __forceinline__ int tile_pos(const PagedAttnParams& p, const Seq& q, int it)
+{
+    if (it >= q.nl) return (q.lo & ~(kTileRows - 1)) + (it - q.nl) * kTileRows;
+    const int e = it * kTileRows + (int)(threadIdx.x & 15);
+    return e < p.kk ? q.idx[e] : -1;
+}
+__device__ __forceinline__ int tile_page(const PagedAttnParams& p, const Seq& q, int it, int& pos)
+{
+    if (it < q.nl && (unsigned)pos >= (unsigned)q.len) {
+        if (it * kTileRows + (int)(threadIdx.x & 15) < p.kk) atomicOr(p.err, FX_DEVERR_INDEX);
+        pos = -1;
+    }
+    return (unsigned)pos < (unsigned)q.len ? q.table[pos >> p.c.page_shift] : 0;   // an empty sequence has no page
+}
 
 __device__ __forceinline__ int64_t row_offset(const PagedCache& c, int id, int64_t sp, int64_t st)
 {
     return (int64_t)(id >> c.page_shift) * sp + (int64_t)(id & c.page_mask) * st;
 }
 
-template <bool E2M1>
-__device__ __forceinline__ void load_k(const PagedCache& c, int h, const Rows& r, Tile<E2M1>& x)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if constexpr (E2M1) x.ks = 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int id = __shfl_sync(kFull, r.id, g + 8 * u);
-        const char* at = c.k + (int64_t)h * c.sh + row_offset(c, id, c.sp, c.st);
-        if constexpr (E2M1) {
-            x.k[u] = ld_stream16(at + 16 * t);
-            x.ks |= ld_u16(c.ks + (int64_t)h * c.ssh + row_offset(c, id, c.ssp, c.sst) + 2 * t) << (16 * u);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x.k[u][j] = ld_stream16(at + 64 * j + 16 * t);
-        }
-    }
-}
+// ---- tile slots in shared memory --------------------------------------------------------------------
+// 4-bit: K codes (16 rows of 64 bytes), V codes, K scales (16 rows of 8 bytes), V scales; of bf16: K rows (256
+// bytes), V rows; then the 16 rows' positions (-1: not valid).  The importance takes K alone.
+// Codes: two rows share a 128-byte line, whose eight 16-byte chunks are permuted by chunk ^ 2 (line % 4), so
+// that neither the 16-byte reads of K (8 rows side by side) nor the 8-byte reads of V (rows 2t, the halves g of
+// them) meet in a bank.  bf16 rows are permuted as kv_off() has it.
+template <bool E2M1, bool WITH_V = true>
+struct Slot {
+    static constexpr int kV = E2M1 ? 1024 : 4096;
+    static constexpr int kScale = (WITH_V ? 2 : 1) * kV;
+    static constexpr int kPos = kScale + (E2M1 ? (WITH_V ? 256 : 128) : 0);
+    static constexpr int kBytes = kPos + 64;
+};
 
-template <bool E2M1>
-__device__ __forceinline__ void load_v(const PagedCache& c, int h, const Rows& r, Tile<E2M1>& x)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if constexpr (E2M1) x.vs = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int id = __shfl_sync(kFull, r.id, 2 * t + (u & 1) + 8 * (u >> 1));
-        const char* at = c.v + (int64_t)h * c.sh + row_offset(c, id, c.sp, c.st);
-        if constexpr (E2M1) {
-            x.v[u] = ld_stream8(at + 8 * g);
-            x.vs |= ld_u8(c.vs + (int64_t)h * c.ssh + row_offset(c, id, c.ssp, c.sst) + g) << (8 * u);
+// Copies tile `it` into a slot (nothing but the positions where no row is valid).  All lanes call it.
+template <bool E2M1, bool WITH_V>
+struct Feeder {
+    const char* k;    // the lane's places relative to a row: K and V codes or rows, scales
+    const char* v;
+    const char* sc;
+    uint32_t to;      // the lane's place in a slot (codes or rows)
+
+    __device__ __forceinline__ Feeder(const PagedCache& c, int h)
+    {
+        const int lane = threadIdx.x & 31;
+        if (E2M1) {
+            const int row = lane >> 2, chunk = lane & 3;
+            k = c.k + (int64_t)h * c.sh + 16 * chunk;
+            v = c.v + (int64_t)h * c.sh + 16 * chunk;
+            sc = (lane < 16 ? c.ks : c.vs) + (int64_t)h * c.ssh;
+            to = (row >> 1) * 128 + ((((row & 1) * 4 + chunk) ^ (2 * ((row >> 1) & 3))) << 4);
         } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) x.v[u][j] = ld_stream16(at + 128 * j + 16 * g);
+            const int row = lane >> 4, chunk = lane & 15;
+            k = c.k + (int64_t)h * c.sh + 16 * chunk;
+            v = c.v + (int64_t)h * c.sh + 16 * chunk;
+            sc = nullptr;
+            to = row * 256 + ((chunk ^ row) << 4);
         }
     }
-}
+
+    __device__ __forceinline__ void copy(const PagedAttnParams& p, const Seq& q, int it, int pos, int page,
+                                         uint32_t slot) const
+    {
+        const PagedCache& c = p.c;
+        const int lane = threadIdx.x & 31, j = lane & 15;
+        const bool list = it < q.nl;
+        bool ok = (unsigned)pos < (unsigned)q.len;
+        if (ok && (unsigned)page >= (unsigned)c.n_pages) {
+            atomicOr(p.err, FX_DEVERR_PAGE);
+            ok = false;
+        }
+        const int id = ok ? (page << c.page_shift) | (pos & c.page_mask) : 0;   // the lane's row or the tile's first
+        int at = pos;
+        if (!list) {
+            at = pos + j;
+            ok = ok && at >= q.lo && at < q.len;
+        }
+        if (lane < 16) asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane), "r"(ok ? at : -1) : "memory");
+        if (E2M1) {
+            int r0 = lane >> 2, r1 = r0 + 8, rs = j;   // the rows that this lane copies
+            int64_t o0, o1, os;
+            if (list) {
+                r0 = __shfl_sync(kFull, id, r0);
+                r1 = __shfl_sync(kFull, id, r1);
+                o0 = row_offset(c, r0, c.sp, c.st);
+                o1 = row_offset(c, r1, c.sp, c.st);
+                os = row_offset(c, id, c.ssp, c.sst);
+            } else {
+                o0 = row_offset(c, id, c.sp, c.st) + r0 * c.st;
+                o1 = o0 + 8 * c.st;
+                os = row_offset(c, id, c.ssp, c.sst) + rs * c.sst;
+            }
+            cp_async16(slot + to, k + o0);
+            cp_async16(slot + to + 512, k + o1);
+            if (WITH_V) {
+                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to, v + o0);
+                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to + 512, v + o1);
+            }
+            if (WITH_V || lane < 16) cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, sc + os);
+        } else {
+            int64_t o = list ? 0 : row_offset(c, id, c.sp, c.st) + (lane >> 4) * c.st;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (list) o = row_offset(c, __shfl_sync(kFull, id, (lane >> 4) + 2 * u), c.sp, c.st);
+                const uint32_t dst = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
+                cp_async16(dst, k + o);
+                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, v + o);
+                if (!list) o += 2 * c.st;
+            }
+        }
+    }
+};
 
 // Calls f(j, a0, a1, a2, a3) with the A fragments of the eight 16-dimension steps of S^T = K Q^T.
-template <bool E2M1, typename F>
-__device__ __forceinline__ void k_steps(const Tile<E2M1>& x, F&& f)
+template <bool E2M1, bool WITH_V, typename F>
+__device__ __forceinline__ void k_steps(uint32_t slot, F&& f)
 {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if constexpr (E2M1) {
-        const uint32_t s0 = e4m3x2_to_f16x2(x.ks & 0xffffu), s1 = e4m3x2_to_f16x2(x.ks >> 16);
+        const uint32_t at = slot + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (2 * ((g >> 1) & 3))) << 4);
+        const uint4 x0 = lds128(at), x1 = lds128(at + 512);
+        const uint32_t sa = slot + Slot<true, WITH_V>::kScale + 8 * g + 2 * t;
+        const uint32_t s0 = e4m3x2_to_f16x2(lds16(sa)), s1 = e4m3x2_to_f16x2(lds16(sa + 64));
         const uint32_t sc[2][2] = {{__byte_perm(s0, 0, 0x1010), __byte_perm(s0, 0, 0x3232)},
                                    {__byte_perm(s1, 0, 0x1010), __byte_perm(s1, 0, 0x3232)}};
-        const uint32_t w0[4] = {x.k[0].x, x.k[0].y, x.k[0].z, x.k[0].w};
-        const uint32_t w1[4] = {x.k[1].x, x.k[1].y, x.k[1].z, x.k[1].w};
+        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
+        const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t a[4], b[4];
@@ -166,36 +274,41 @@ __device__ __forceinline__ void k_steps(const Tile<E2M1>& x, F&& f)
             f(2 * j + 1, a[2], b[2], a[3], b[3]);
         }
     } else {
+        const int row = lane & 15;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f(2 * j, x.k[0][j].x, x.k[1][j].x, x.k[0][j].y, x.k[1][j].y);
-            f(2 * j + 1, x.k[0][j].z, x.k[1][j].z, x.k[0][j].w, x.k[1][j].w);
+        for (int j = 0; j < 8; ++j) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(slot + kv_off(row, 2 * j + (lane >> 4)), a0, a1, a2, a3);
+            f(j, a0, a1, a2, a3);
         }
     }
 }
 
-// Calls f(i, a0, a1, a2, a3) with the A fragments of the eight M tiles of O^T += V^T P^T; rows outside `vm`
-// count as zero, whatever they hold.
-template <bool E2M1, typename F>
-__device__ __forceinline__ void v_tiles(const Tile<E2M1>& x, uint32_t vm, F&& f)
+// Calls f(i, a0, a1, a2, a3) with the A fragments of the eight M tiles of O^T += V^T P^T.  MASKED: rows outside
+// `vm` count as zero, whatever they hold.
+template <bool E2M1, bool MASKED, typename F>
+__device__ __forceinline__ void v_tiles(uint32_t slot, uint32_t vm, F&& f)
 {
-    const int t = threadIdx.x & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t on = vm >> (2 * t);   // bits 0, 1, 8, 9: rows 2t, 2t + 1, 2t + 8, 2t + 9
     if constexpr (E2M1) {
-        uint32_t vs = x.vs;
-        if (vm != 0xffffu) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (((vm >> (2 * t + (u & 1) + 8 * (u >> 1))) & 1u) == 0) vs &= ~(0xffu << (8 * u));
+        const uint32_t sa = slot + Slot<true>::kScale + 128 + 16 * t + g;
+        uint32_t vs01 = lds8(sa) | (lds8(sa + 8) << 8), vs23 = lds8(sa + 64) | (lds8(sa + 72) << 8);
+        if (MASKED) {
+            vs01 &= (on & 1u ? 0xffu : 0u) | (on & 2u ? 0xff00u : 0u);
+            vs23 &= (on & 0x100u ? 0xffu : 0u) | (on & 0x200u ? 0xff00u : 0u);
         }
-        const uint32_t s01 = e4m3x2_to_f16x2(vs & 0xffffu), s23 = e4m3x2_to_f16x2(vs >> 16);
-        const uint32_t w[4][2] = {{x.v[0].x, x.v[0].y}, {x.v[1].x, x.v[1].y}, {x.v[2].x, x.v[2].y}, {x.v[3].x, x.v[3].y}};
+        const uint32_t s01 = e4m3x2_to_f16x2(vs01), s23 = e4m3x2_to_f16x2(vs23);
+        const uint32_t in = t * 128 + (((g >> 1) ^ (2 * t)) << 4) + (g & 1) * 8;
+        const uint32_t va = slot + Slot<true>::kV + in, vb = slot + Slot<true>::kV + (in ^ 64u);
+        const uint2 x[4] = {lds64(va), lds64(vb), lds64(va + 512), lds64(vb + 512)};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t a[4][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 // neighbouring rows' codes of one dimension side by side, then one conversion a pair
-                const uint32_t x0 = w[2 * u][j], x1 = w[2 * u + 1][j];
+                const uint32_t x0 = j ? x[2 * u].y : x[2 * u].x, x1 = j ? x[2 * u + 1].y : x[2 * u + 1].x;
                 const uint32_t even = (x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u);
                 const uint32_t odd = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
                 e2m1x8_to_f16(even, a[2 * u][0], a[2 * u][1], a[2 * u][2], a[2 * u][3]);
@@ -210,29 +323,28 @@ __device__ __forceinline__ void v_tiles(const Tile<E2M1>& x, uint32_t vm, F&& f)
             for (int i = 0; i < 4; ++i) f(4 * j + i, a[0][i], a[1][i], a[2][i], a[3][i]);
         }
     } else {
+        const uint32_t m01 = (on & 1u ? 0xffffu : 0u) | (on & 2u ? 0xffff0000u : 0u);
+        const uint32_t m23 = (on & 0x100u ? 0xffffu : 0u) | (on & 0x200u ? 0xffff0000u : 0u);
+        const int row = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t w[4][4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool on = (vm >> (2 * t + (u & 1) + 8 * (u >> 1))) & 1u;
-                w[u][0] = on ? x.v[u][j].x : 0u;
-                w[u][1] = on ? x.v[u][j].y : 0u;
-                w[u][2] = on ? x.v[u][j].z : 0u;
-                w[u][3] = on ? x.v[u][j].w : 0u;
+        for (int i = 0; i < 8; ++i) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_t(slot + Slot<false>::kV + kv_off(row, 2 * i + ((lane >> 3) & 1)), a0, a1, a2, a3);
+            if (MASKED) {
+                a0 &= m01;
+                a1 &= m01;
+                a2 &= m23;
+                a3 &= m23;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f(4 * j + i, __byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
-                  __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632));
+            f(i, a0, a1, a2, a3);
         }
     }
 }
-// First of the two dimensions (the other follows it) that M tile i holds for lane group g.
+// The two dimensions that rows g and g + 8 of M tile i hold.
 template <bool E2M1>
-__device__ __forceinline__ int v_dim(int i, int g)
+__device__ __forceinline__ int v_dim(int i, int g, int half)
 {
-    return E2M1 ? 16 * g + 2 * i : 64 * (i >> 2) + 8 * g + 2 * (i & 3);
+    return E2M1 ? 16 * g + 2 * i + half : 16 * i + g + 8 * half;
 }
 
 // The lane's 32 query values of row g (B fragments of the eight steps), and the factor of the row's logits.
@@ -243,13 +355,21 @@ __device__ __forceinline__ float load_query(const uint16_t* src, uint32_t q[8][2
     const int t = threadIdx.x & 3;
     uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (src) x = *reinterpret_cast<const uint4*>(src + (E2M1 ? 32 * t + 8 * j : 32 * j + 8 * t));
-        w[4 * j] = x.x;
-        w[4 * j + 1] = x.y;
-        w[4 * j + 2] = x.z;
-        w[4 * j + 3] = x.w;
+    for (int j = 0; j < 16; ++j) w[j] = 0;
+    if (src) {
+        if (E2M1) {   // step j: dimensions 32t + 4j .. + 3, as a lane's 16 bytes of codes have them
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 x = *reinterpret_cast<const uint4*>(src + 32 * t + 8 * j);
+                w[4 * j] = x.x;
+                w[4 * j + 1] = x.y;
+                w[4 * j + 2] = x.z;
+                w[4 * j + 3] = x.w;
+            }
+        } else {      // step j: dimensions 16j + 2t, + 1 and 16j + 8 + 2t, + 1
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + 8 * j + 2 * t);
+        }
     }
     float factor = 1.f;
     if (E2M1) {
@@ -295,64 +415,24 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
     }
 }
 
-// A tile of a sequence in three steps, each needing what the one before loaded: the lane's row (position), its
-// page, its place in the pool.  The first nl tiles hold the list, the others the tail, whose tiles start at
-// multiples of 16 (so that such a tile lies inside one page).
-struct Seq {
-    const int32_t* idx;     // the list of (b, h)
-    const int32_t* table;   // the pages of b
-    int nl, lo, len;        // list tiles, start of the tail, rows
-};
-__device__ __forceinline__ int tile_pos(const PagedAttnParams& p, const Seq& q, int it)   // -1: no such row
-{
-    const int j = threadIdx.x & 15;
-    if (it < q.nl) {
-        const int e = it * kTileRows + j;
-        return e < p.kk ? q.idx[e] : -1;
-    }
-    const int pos = (q.lo & ~(kTileRows - 1)) + (it - q.nl) * kTileRows + j;
-    return pos >= q.lo && pos < q.len ? pos : -1;
-}
-__device__ __forceinline__ int tile_page(const PagedAttnParams& p, const Seq& q, int it, int& pos)
-{
-    if (it < q.nl && (unsigned)pos >= (unsigned)q.len) {
-        if (it * kTileRows + (int)(threadIdx.x & 15) < p.kk) atomicOr(p.err, FX_DEVERR_INDEX);
-        pos = -1;
-    }
-    return pos >= 0 ? q.table[pos >> p.c.page_shift] : 0;
-}
-__device__ __forceinline__ Rows tile_place(const PagedAttnParams& p, int pos, int page)
-{
-    Rows r;
-    bool ok = pos >= 0;
-    if (ok && (unsigned)page >= (unsigned)p.c.n_pages) {
-        atomicOr(p.err, FX_DEVERR_PAGE);
-        ok = false;
-    }
-    r.pos = pos;
-    r.id = ok ? (page << p.c.page_shift) | (pos & p.c.page_mask) : 0;
-    r.vm = __ballot_sync(kFull, ok) & 0xffffu;
-    return r;
-}
-
-// Joins the warps' partials of one query row in shared memory: the sum over them of dimension d, with the row's
-// reference m (-inf: no warp saw anything) and its sum z.
-template <int kRows>
-__device__ __forceinline__ float join_row(const float* sm_o, const float* sm_m, const float* sm_l, int row, int d,
-                                          float& m, float& z)
+// Joins W partials of one query row in shared memory (partial w: its O at sm_o + w * pitch, m and z in sm_m and
+// sm_l): the sum over them of dimension d, with the row's reference m (-inf: nothing was seen) and its sum z.
+template <int kRows, int W>
+__device__ __forceinline__ float join_row(const float* sm_o, int pitch, const float* sm_m, const float* sm_l, int row,
+                                          int d, float& m, float& z)
 {
     m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w * kRows + row]);
+    for (int w = 0; w < W; ++w) m = fmaxf(m, sm_m[w * kRows + row]);
     z = 0.f;
     float acc = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
         const float mw = sm_m[w * kRows + row];
         if (mw == -INFINITY) continue;   // that warp saw nothing
         const float f = fast_exp2(mw - m);
         z += f * sm_l[w * kRows + row];
-        acc += f * sm_o[(w * kRows + row) * kHeadDim + d];
+        acc += f * sm_o[w * pitch + row * kHeadDim + d];
     }
     return acc;
 }
@@ -425,41 +505,42 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4]
         }
 }
 
-// One tile: logits, weights, O^T += V^T P^T.  after_k and after_v run when the tile's K and V rows are no longer
-// needed (the caller loads the next tile into them).
-template <bool E2M1, int NT, bool DUP, typename FK, typename FV>
-__device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, Tile<E2M1>& x,
-                                            const Rows& rows, int r0, int seen, FK&& after_k, FV&& after_v)
+// One tile: logits, weights, O^T += V^T P^T.
+template <bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int r0,
+                                            int seen)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int pos = (int)lds32(slot + Slot<E2M1>::kPos + 4 * (lane & 15));
+    const uint32_t vm = __ballot_sync(kFull, pos >= 0) & 0xffffu;   // the valid rows
+    const bool late = __any_sync(kFull, pos > seen);                // one lies past what query 0 sees
     float s[NT][4];
     {
         float s2[NT][2][4];
+        k_steps<E2M1, true>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s2[n][e >> 2][e & 3] = 0.f;
-        k_steps<E2M1>(x, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+            for (int n = 0; n < NT; ++n) {
+                if (j < 2)
+                    mma16_zero<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+                else
+                    mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+            }
         });
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
     }
-    after_k();
-    const bool late = __any_sync(kFull, ((rows.vm >> (lane & 15)) & 1u) && rows.pos > seen);
     uint32_t hide = 0;
-    if (late || rows.vm != 0xffffu) {
-        const int p0 = __shfl_sync(kFull, rows.pos, g), p1 = __shfl_sync(kFull, rows.pos, g + 8);
+    if (late || vm != 0xffffu) {
+        const int p0 = (int)lds32(slot + Slot<E2M1>::kPos + 4 * g), p1 = (int)lds32(slot + Slot<E2M1>::kPos + 32 + 4 * g);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
-                const bool see = ((rows.vm >> (g + 8 * (e >> 1))) & 1u) && (e >> 1 ? p1 : p0) <= seen + r % p.Mq;
-                if (!see) hide |= 1u << (4 * n + e);
+                const int at = e >> 1 ? p1 : p0;
+                if (at < 0 || at > seen + r % p.Mq) hide |= 1u << (4 * n + e);
             }
     }
     weights<E2M1, NT, DUP>(a, s, hide);
@@ -472,72 +553,70 @@ __device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            uint32_t hi, lo2;
-            split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo2);
+            uint32_t hi, lo;
+            split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo);
             if (DUP) {
-                bh[n][u] = movmatrix_t(t < 2 ? hi : lo2);
+                bh[n][u] = movmatrix_t(t < 2 ? hi : lo);
             } else {
                 bh[n][u] = movmatrix_t(hi);
-                bl[n][u] = movmatrix_t(lo2);
+                bl[n][u] = movmatrix_t(lo);
             }
         }
-    auto product = [&](uint32_t vm, auto&& adds) {   // adds(n, e): query row 2t + e of N tile n takes it
-        v_tiles<E2M1>(x, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    auto term = [&](float (&c)[4], int n, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        mma16_zero<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
+        if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
+    };
+    if (vm == 0xffffu && !late) {
+        v_tiles<E2M1, false>(slot, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
-                if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
+                float c[4];
+                term(c, n, a0, a1, a2, a3);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (adds(n, e & 1)) a.o[n][i][e] += c[e];
+                for (int e = 0; e < 4; ++e) a.o[n][i][e] += c[e];
             }
         });
-    };
-    if (!late) {
-        product(rows.vm, [](int, int) { return true; });
-    } else {
-        // rows that only later queries see: one product per query position, over the rows it sees (the
-        // others may hold anything, and 0 * NaN is NaN) and for its query rows alone
-        for (int i = 0; i < p.Mq; ++i) {
-            uint32_t add = 0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
-                    if (r % p.Mq == i) add |= 1u << (2 * n + e);
-                }
-            product(__ballot_sync(kFull, rows.pos <= seen + i) & rows.vm,
-                    [&](int n, int e) { return ((add >> (2 * n + e)) & 1u) != 0; });
-        }
+        return;
     }
-    after_v();
+    // rows that are not valid, or that only later queries see, may hold anything, and 0 * NaN is NaN: they count
+    // as zeros, in one product per query position where positions differ, taken by that position's query rows
+    const int passes = late ? p.Mq : 1;
+    for (int i = 0; i < passes; ++i) {
+        uint32_t add = 0;   // bit 2n + e: query row 2t + e of N tile n
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
+                if (!late || r % p.Mq == i) add |= 1u << (2 * n + e);
+            }
+        const uint32_t vi = late ? __ballot_sync(kFull, pos <= seen + i) & vm : vm;
+        v_tiles<E2M1, true>(slot, vi, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float c[4];
+                term(c, n, a0, a1, a2, a3);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((add >> (2 * n + (e & 1))) & 1u) a.o[n][j][e] += c[e];
+            }
+        });
+    }
 }
 
-// Query rows of one CTA's pass over a (sequence, KV head).
-template <int NT, bool DUP>
-__host__ __device__ constexpr int pass_rows() { return DUP ? 4 : 8 * NT; }
-
-// Tiles of sequence b (at least one: an empty sequence's tile holds no valid row, and its output is written).
-__device__ __forceinline__ Seq sequence(const PagedAttnParams& p, int b, bool report)
-{
-    Seq q;
-    q.len = p.c.len[b];
-    q.lo = p.tail_lo ? p.tail_lo[b] : 0;
-    if (report && (q.len < 0 || q.len > p.c.cap || q.lo < 0)) atomicOr(p.err, FX_DEVERR_LEN);
-    q.len = min(max(q.len, 0), p.c.cap);
-    q.lo = max(q.lo, 0);
-    q.nl = (p.kk + kTileRows - 1) / kTileRows;
-    q.table = p.c.table + (int64_t)b * p.c.table_stride;
-    q.idx = nullptr;
-    return q;
-}
-__device__ __forceinline__ int tile_count(const Seq& q)
-{
-    const int nt = q.lo < q.len ? (q.len + kTileRows - 1) / kTileRows - q.lo / kTileRows : 0;
-    return max(q.nl + nt, 1);
-}
+// Shape of the decode kernel for a format and up to 4 (DUP), 8 or 16 query rows a pass.  4-bit tiles are small
+// (2.3 KB) and cost many operations a byte: 16 warps an SM.  bf16 tiles (8 KB) fill the shared memory with 8
+// warps' rings.
+template <bool E2M1, int NT, bool DUP>
+struct Shape {
+    static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
+    static constexpr int kWarps = 8;
+    static constexpr int kCtas = E2M1 && NT == 1 ? 2 : 1;   // per SM
+    static constexpr int kStages = E2M1 ? 4 : 3;
+    static constexpr int kRing = kStages * Slot<E2M1>::kBytes;   // bytes of a warp; its partial O later takes them
+    static constexpr size_t kSmem = (size_t)kWarps * kRing;
+    static_assert(kRows * kHeadDim * 4 <= kRing, "a warp's partial O lies in its ring");
+};
 
 // Decode.  The tiles of all (sequence, KV head, group of query rows) form one line, which the CTAs share out
 // evenly by the lengths found on the device, so that ragged lengths leave no CTA with more to do than another.
@@ -548,14 +627,16 @@ __device__ __forceinline__ int tile_count(const Seq& q)
 // DUP: at most 4 query rows; columns 4..7 of the products repeat them, so that one product takes P's high part
 // (columns 0..3) and its low part (4..7).
 template <bool E2M1, int NT, bool DUP>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_kernel(const PagedAttnParams p)
+__global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1, NT, DUP>::kCtas)
+    paged_decode_kernel(const PagedAttnParams p)
 {
-    constexpr int kRows = pass_rows<NT, DUP>();
-    extern __shared__ float smem[];
-    float* sm_o = smem;                                        // [warp][row][128]
-    float* sm_m = smem + kAttnWarps * kRows * kHeadDim;        // [warp][row]
-    float* sm_l = sm_m + kAttnWarps * kRows;
-    __shared__ long long sm_scan[kAttnWarps];
+    using S = Shape<E2M1, NT, DUP>;
+    constexpr int kRows = S::kRows, W = S::kWarps, kThreadsA = 32 * W, kStages = S::kStages, kSlot = Slot<E2M1>::kBytes;
+    constexpr int kPitch = S::kRing / 4;   // floats between the warps' partial O
+    extern __shared__ __align__(128) float smem[];
+    float* const sm_o = smem;
+    __shared__ float sm_m[W * kRows], sm_l[W * kRows];
+    __shared__ long long sm_scan[W];
     __shared__ int sm_b;
     __shared__ long long sm_start;
     __shared__ unsigned sm_last;
@@ -563,28 +644,27 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
     griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const int nrg = (p.R + kRows - 1) / kRows;
     const int per_tile = p.c.Hkv * nrg;   // pieces of one sequence
 
     // total length of the line, then this CTA's stretch of it and the sequence that it starts in
     long long total = 0;
-    for (int b = tid; b < p.c.B; b += kAttnThreads) total += tile_count(sequence(p, b, blockIdx.x == 0));
-    {
+    for (int b = tid; b < p.c.B; b += kThreadsA) total += tile_count(sequence(p, b, blockIdx.x == 0));
 #pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-        if (lane == 0) sm_scan[warp] = total;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < kAttnWarps; ++w) total += sm_scan[w];
-        total *= per_tile;
-    }
-    const int n_cta = (int)min((long long)gridDim.x, max(1ll, total / (kAttnWarps * kMinTiles)));
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+    if (lane == 0) sm_scan[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < W; ++w) total += sm_scan[w];
+    total *= per_tile;
+    const int n_cta = (int)min((long long)gridDim.x, max(1ll, total / (W * kMinTiles)));
     const int cta = blockIdx.x;
     if (cta >= n_cta) return;
     long long at = total * cta / n_cta;                  // next tile of the line
     const long long end = total * (cta + 1) / n_cta;
     long long before = 0;                                // tiles (of one piece each) of the sequences before b
-    for (int b0 = 0;; b0 += kAttnThreads) {
+    for (int b0 = 0;; b0 += kThreadsA) {
         const int b = b0 + tid;
         const int n = b < p.c.B ? tile_count(sequence(p, b, false)) : 0;
         long long inc = n;
@@ -598,7 +678,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
         if (lane == 31) sm_scan[warp] = inc;
         __syncthreads();
         long long sum = 0, mine = 0;
-        for (int w = 0; w < kAttnWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             if (w == warp) mine = sum;
             sum += sm_scan[w];
         }
@@ -629,6 +709,23 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
         const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
+        // the ring's first tiles on their way; then each step feeds the tile kStages - 1 turns ahead, whose
+        // page was looked up a turn earlier and whose position another turn earlier
+        const Feeder<E2M1, true> feeder(p.c, h);
+        int it = s0 + warp;
+        int pos[kStages], page[kStages];
+#pragma unroll
+        for (int u = 0; u < kStages; ++u) pos[u] = it + u * W < s1 ? tile_pos(p, seq, it + u * W) : -1;
+#pragma unroll
+        for (int u = 0; u < kStages; ++u) page[u] = it + u * W < s1 ? tile_page(p, seq, it + u * W, pos[u]) : 0;
+#pragma unroll
+        for (int u = 0; u < kStages - 1; ++u) {
+            if (it + u * W < s1) feeder.copy(p, seq, it + u * W, pos[u], page[u], ring + u * kSlot);
+            cp_async_commit();
+        }
+        int pos1 = pos[kStages - 1], page1 = page[kStages - 1];
+        int pos2 = it + kStages * W < s1 ? tile_pos(p, seq, it + kStages * W) : -1;
+
         Acc<E2M1, NT, DUP> a;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -646,60 +743,22 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
                 for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
         }
 
-        // the warp's tiles s0 + warp, + 8, ...: the rows of the next one are loaded while one is worked on, its
-        // pages one tile earlier, its positions another one earlier
-        int it = s0 + warp;
-        if (it < s1) {
-            int pos = tile_pos(p, seq, it);
-            int page = tile_page(p, seq, it, pos);
-            Rows rows = tile_place(p, pos, page);
-            int pos1 = it + kAttnWarps < s1 ? tile_pos(p, seq, it + kAttnWarps) : -1;
-            int page1 = it + kAttnWarps < s1 ? tile_page(p, seq, it + kAttnWarps, pos1) : 0;
-            int pos2 = it + 2 * kAttnWarps < s1 ? tile_pos(p, seq, it + 2 * kAttnWarps) : -1;
-            Rows next;
-            auto advance = [&]() {   // places the next tile, looks the one after it up
-                next = tile_place(p, pos1, page1);
-                const int i2 = it + 2 * kAttnWarps, i3 = it + 3 * kAttnWarps;
-                page1 = i2 < s1 ? tile_page(p, seq, i2, pos2) : 0;
-                pos1 = pos2;
-                pos2 = i3 < s1 ? tile_pos(p, seq, i3) : -1;
-            };
-            if constexpr (E2M1) {
-                Tile<E2M1> x, y;
-                load_k<E2M1>(p.c, h, rows, x);
-                load_v<E2M1>(p.c, h, rows, x);
-                auto turn = [&](Tile<E2M1>& cur, Tile<E2M1>& nxt) {
-                    advance();
-                    if (it + kAttnWarps < s1) {
-                        load_k<E2M1>(p.c, h, next, nxt);
-                        load_v<E2M1>(p.c, h, next, nxt);
-                    }
-                    attend_tile<E2M1, NT, DUP>(p, a, cur, rows, r0, seen, [] {}, [] {});
-                    rows = next;
-                    it += kAttnWarps;
-                };
-                while (true) {
-                    turn(x, y);
-                    if (it >= s1) break;
-                    turn(y, x);
-                    if (it >= s1) break;
-                }
-            } else {
-                // bf16 rows fill 64 registers a lane: the next K takes the place of this tile's once the logits
-                // are there, the next V that of this one's after the product
-                Tile<E2M1> x;
-                load_k<E2M1>(p.c, h, rows, x);
-                load_v<E2M1>(p.c, h, rows, x);
-                for (; it < s1; it += kAttnWarps) {
-                    advance();
-                    const bool more = it + kAttnWarps < s1;
-                    attend_tile<E2M1, NT, DUP>(
-                        p, a, x, rows, r0, seen, [&] { if (more) load_k<E2M1>(p.c, h, next, x); },
-                        [&] { if (more) load_v<E2M1>(p.c, h, next, x); });
-                    rows = next;
-                }
-            }
+        uint32_t slot = ring, feed = ring + (kStages - 1) * kSlot;
+        for (; it < s1; it += W) {
+            cp_async_wait_stages<kStages - 1>();   // this lane's copies of the tile; the barrier covers the others'
+            __syncwarp();
+            const int in = it + (kStages - 1) * W;
+            if (in < s1) feeder.copy(p, seq, in, pos1, page1, feed);
+            cp_async_commit();
+            pos1 = pos2;
+            page1 = in + W < s1 ? tile_page(p, seq, in + W, pos1) : 0;
+            pos2 = in + 2 * W < s1 ? tile_pos(p, seq, in + 2 * W) : -1;
+            attend_tile<E2M1, NT, DUP>(p, a, slot, r0, seen);
+            feed = slot;
+            slot = slot + kSlot == ring + kStages * kSlot ? ring : slot + kSlot;
         }
+        cp_async_wait_all_groups();
+        __syncwarp();   // every lane is done with the ring
 
         // the warps' partials meet in shared memory
 #pragma unroll
@@ -726,24 +785,20 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
                 }
                 if (!DUP || t < 2) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float* to = sm_o + ((warp * kRows + 8 * n + 2 * t + e) * kHeadDim + v_dim<E2M1>(i, g));
-                        *reinterpret_cast<float2*>(to) = make_float2(a.o[n][i][e], a.o[n][i][e + 2]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        sm_o[warp * kPitch + (8 * n + 2 * t + (e & 1)) * kHeadDim + v_dim<E2M1>(i, g, e >> 1)] = a.o[n][i][e];
                 }
             }
         __syncthreads();
 
-        const bool whole = s0 == 0 && s1 == ntile;
-        if (!whole) {
+        if (s0 != 0 || s1 != ntile) {
             // this CTA's part of the piece goes to its slot; the last CTA to arrive takes all of them over
-            const int slot = cta * 2 + (head ? 0 : 1);
-            float* part = p.part + (size_t)slot * kRows * (kHeadDim + 2);
+            constexpr int kPart = kRows * (kHeadDim + 2);
+            float* part = p.part + (size_t)(cta * 2 + (head ? 0 : 1)) * kPart;
             const int d = tid & (kHeadDim - 1);
-            for (int row = tid / kHeadDim; row < kRows; row += kAttnThreads / kHeadDim) {
+            for (int row = tid / kHeadDim; row < kRows; row += kThreadsA / kHeadDim) {
                 float z, m;
-                const float acc = join_row<kRows>(sm_o, sm_m, sm_l, row, d, m, z);
-                part[row * kHeadDim + d] = acc;
+                part[row * kHeadDim + d] = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, d, m, z);
                 if (d == 0) {
                     part[kRows * kHeadDim + row] = m;
                     part[kRows * kHeadDim + kRows + row] = z;
@@ -755,8 +810,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const unsigned n = atomicAdd(p.counters + c0, 1u);
-                sm_last = n == (unsigned)(c1 - c0);
+                sm_last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
                 if (sm_last) {
                     p.counters[c0] = 0;   // ready for the next call
                     __threadfence();
@@ -767,23 +821,20 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
                 at = piece_start + s1;
                 continue;
             }
-            // each warp takes every eighth part, then the warps' sums meet as before.  A CTA's first piece is in
-            // its slot 0; the piece starts in c0, as that CTA's first piece only if it starts its stretch
+            // each warp takes every W-th part, then the warps' sums meet as before.  A CTA's first piece is in
+            // its slot 0; this piece is c0's first only if it starts c0's stretch
             const int s_first = c0 * 2 + (total * c0 / n_cta == piece_start ? 0 : 1);
             for (int row = 0; row < kRows; ++row) {
                 float m = -INFINITY;
-                for (int c = c0 + warp + kAttnWarps * lane; c <= c1; c += kAttnWarps * 32) {
-                    const int sl = c == c0 ? s_first : c * 2;
-                    m = fmaxf(m, __ldcg(p.part + (size_t)sl * kRows * (kHeadDim + 2) + kRows * kHeadDim + row));
-                }
+                for (int c = c0 + warp + W * lane; c <= c1; c += W * 32)
+                    m = fmaxf(m, __ldcg(p.part + (size_t)(c == c0 ? s_first : c * 2) * kPart + kRows * kHeadDim + row));
 #pragma unroll
                 for (int d2 = 16; d2; d2 >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d2));
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 float z = 0.f;
 #pragma unroll 4
-                for (int c = c0 + warp; c <= c1; c += kAttnWarps) {
-                    const int sl = c == c0 ? s_first : c * 2;
-                    const float* from = p.part + (size_t)sl * kRows * (kHeadDim + 2);
+                for (int c = c0 + warp; c <= c1; c += W) {
+                    const float* from = p.part + (size_t)(c == c0 ? s_first : c * 2) * kPart;
                     const float mc = __ldcg(from + kRows * kHeadDim + row);
                     const float lc = __ldcg(from + kRows * kHeadDim + kRows + row);
                     const float4 oc = __ldcg(reinterpret_cast<const float4*>(from + row * kHeadDim) + lane);
@@ -794,7 +845,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
                     acc.z += f * oc.z;
                     acc.w += f * oc.w;
                 }
-                *(reinterpret_cast<float4*>(sm_o + (warp * kRows + row) * kHeadDim) + lane) = acc;
+                *(reinterpret_cast<float4*>(sm_o + warp * kPitch + row * kHeadDim) + lane) = acc;
                 if (lane == 0) {
                     sm_m[warp * kRows + row] = m;
                     sm_l[warp * kRows + row] = z;
@@ -803,9 +854,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
             __syncthreads();
         }
         const int d = tid & (kHeadDim - 1);
-        for (int row = tid / kHeadDim; row < kRows && r0 + row < p.R; row += kAttnThreads / kHeadDim) {
+        for (int row = tid / kHeadDim; row < kRows && r0 + row < p.R; row += kThreadsA / kHeadDim) {
             float z, m;
-            const float acc = join_row<kRows>(sm_o, sm_m, sm_l, row, d, m, z);
+            const float acc = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, d, m, z);
             const int r = r0 + row;
             const int64_t to = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
             const bool none = m == -INFINITY;
@@ -817,13 +868,17 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) paged_decode_ke
     }
 }
 
-constexpr int kImpTiles = 4;   // tiles of a warp of the importance kernel
+constexpr int kImpWarps = 8;
+constexpr int kImpStages = 2;
+constexpr int kImpTiles = 8;   // tiles of a warp of the importance kernel
 
 // Importance: each warp takes kImpTiles tiles of 16 rows and every query row; the query fragments lie in
 // shared memory as the products want them.
 template <bool E2M1>
-__global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const PagedAttnParams p)
+__global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const PagedAttnParams p)
 {
+    constexpr int kSlot = Slot<E2M1, false>::kBytes;
+    extern __shared__ __align__(128) float smem[];   // the warps' rings
     __shared__ uint4 sq[kMaxRows / 8][4][32];
     __shared__ float srs[kMaxRows], sls[kMaxRows];
     griddep_wait();
@@ -832,8 +887,25 @@ __global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const Pa
     const int h = blockIdx.y, b = blockIdx.z;
     Seq seq = sequence(p, b, true);
     const int len = seq.len, seen = len - p.Mq;
-    const int ntile = (p.R + 7) / 8;
-    for (int n = warp; n < ntile; n += kAttnWarps) {
+    const int first = (p.cand_lo & ~(kTileRows - 1)) + (blockIdx.x * kImpWarps + warp) * (kImpTiles * kTileRows);
+    seq.lo = first;
+    const int ntile = first < len ? min(kImpTiles, (len - first + kTileRows - 1) / kTileRows) : 0;   // with rows in them
+    const Feeder<E2M1, false> feeder(p.c, h);
+    const uint32_t ring = smem_addr(smem) + warp * kImpStages * kSlot;
+    int pos[kImpStages], page[kImpStages];
+#pragma unroll
+    for (int u = 0; u < kImpStages; ++u) {
+        pos[u] = tile_pos(p, seq, u);
+        page[u] = u < ntile ? tile_page(p, seq, u, pos[u]) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kImpStages - 1; ++u) {
+        if (u < ntile) feeder.copy(p, seq, u, pos[u], page[u], ring + u * kSlot);
+        cp_async_commit();
+    }
+    int page1 = page[kImpStages - 1];
+    const int nq = (p.R + 7) / 8;
+    for (int n = warp; n < nq; n += kImpWarps) {
         const int r = 8 * n + g;
         uint32_t q[8][2];
         const float f = load_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, q);
@@ -847,40 +919,46 @@ __global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const Pa
         }
     }
     __syncthreads();
-    const int first = (p.cand_lo & ~(kTileRows - 1)) + (blockIdx.x * kAttnWarps + warp) * (kImpTiles * kTileRows);
-    seq.lo = first;
     float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * (p.cand_hi - p.cand_lo);
     for (int u = 0; u < kImpTiles; ++u) {
         const int base = first + u * kTileRows;
         if (base >= p.cand_hi) break;
         float sum[2] = {0.f, 0.f};
-        if (base < len) {
-            int pos = tile_pos(p, seq, u);
-            const int page = tile_page(p, seq, u, pos);
-            const Rows rows = tile_place(p, pos, page);
-            Tile<E2M1> x;
-            load_k<E2M1>(p.c, h, rows, x);
+        if (u < ntile) {
+            const uint32_t slot = ring + (u % kImpStages) * kSlot;
+            cp_async_wait_stages<kImpStages - 1>();
+            __syncwarp();
+            const int in = u + kImpStages - 1;
+            if (in < ntile) feeder.copy(p, seq, in, tile_pos(p, seq, in), page1, ring + (in % kImpStages) * kSlot);
+            cp_async_commit();
+            int next = tile_pos(p, seq, in + 1);
+            page1 = in + 1 < ntile ? tile_page(p, seq, in + 1, next) : 0;
             uint32_t a[8][4];
-            k_steps<E2M1>(x, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            k_steps<E2M1, false>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                 a[j][0] = a0;
                 a[j][1] = a1;
                 a[j][2] = a2;
                 a[j][3] = a3;
             });
-            for (int n = 0; n < ntile; ++n) {
-                float s[2][4] = {};
+            const int p0 = (int)lds32(slot + Slot<E2M1, false>::kPos + 4 * g), p1 = (int)lds32(slot + Slot<E2M1, false>::kPos + 32 + 4 * g);
+            for (int n = 0; n < nq; ++n) {
+                float s[2][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint4 q = sq[n][j][lane];
-                    mma16<E2M1>(s[0], a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], q.x, q.y);
-                    mma16<E2M1>(s[1], a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], q.z, q.w);
+                    if (j == 0) {
+                        mma16_zero<E2M1>(s[0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+                        mma16_zero<E2M1>(s[1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                    } else {
+                        mma16<E2M1>(s[0], a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], q.x, q.y);
+                        mma16<E2M1>(s[1], a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], q.z, q.w);
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = 8 * n + 2 * t + (e & 1);
-                    const int pos = base + g + 8 * (e >> 1);
-                    const bool see = ((rows.vm >> (g + 8 * (e >> 1))) & 1u) && r < p.R && pos <= seen + r % p.Mq &&
-                                     sls[r] != INFINITY;
+                    const int row = e >> 1 ? p1 : p0;
+                    const bool see = row >= 0 && r < p.R && row <= seen + r % p.Mq && sls[r] != INFINITY;
                     if (see) sum[e >> 1] += fast_exp2(fmaf(s[0][e] + s[1][e], srs[r], -sls[r]));
                 }
             }
@@ -890,33 +968,42 @@ __global__ void __launch_bounds__(kAttnThreads) paged_importance_kernel(const Pa
             sum[e] += __shfl_xor_sync(kFull, sum[e], 1);
             sum[e] += __shfl_xor_sync(kFull, sum[e], 2);
         }
-        const int pos = base + g + 8 * t;
-        if (t < 2 && pos >= p.cand_lo && pos < p.cand_hi) out[pos - p.cand_lo] = t ? sum[1] : sum[0];
+        const int row = base + g + 8 * t;
+        if (t < 2 && row >= p.cand_lo && row < p.cand_hi) out[row - p.cand_lo] = t ? sum[1] : sum[0];
     }
+    cp_async_wait_all_groups();
 }
-
-// CTAs of a decode call: as many as are resident at once (one with more than 8 query rows, else two per SM).
-int decode_ctas(int R, int sm_count) { return (R > 8 ? 1 : 2) * sm_count; }
 
 template <bool E2M1, int NT, bool DUP>
 cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    constexpr int kRows = pass_rows<NT, DUP>();
-    constexpr size_t smem = sizeof(float) * kAttnWarps * kRows * (kHeadDim + 2);
+    using S = Shape<E2M1, NT, DUP>;
     cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<E2M1, NT, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+                                         (int)S::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_kernel(paged_decode_kernel<E2M1, NT, DUP>, dim3(decode_ctas(p.R, sm_count)), dim3(kAttnThreads), smem, s,
+    return launch_kernel(paged_decode_kernel<E2M1, NT, DUP>, dim3(S::kCtas * sm_count), dim3(32 * S::kWarps), S::kSmem, s,
                          pdl, 0u, p);
+}
+
+template <bool E2M1>
+cudaError_t launch_importance(const PagedAttnParams& p, bool pdl, cudaStream_t s)
+{
+    constexpr size_t smem = (size_t)kImpWarps * kImpStages * Slot<E2M1, false>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(paged_importance_kernel<E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int rows = p.cand_hi - (p.cand_lo & ~(kTileRows - 1));
+    const int per = kImpWarps * kImpTiles * kTileRows;
+    return launch_kernel(paged_importance_kernel<E2M1>, dim3((rows + per - 1) / per, p.c.Hkv, p.c.B), dim3(32 * kImpWarps),
+                         smem, s, pdl, 0u, p);
 }
 
 }  // namespace
 
-// The counters' region, then two partials (one of each end of a CTA's stretch) of up to 16 query rows per CTA.
+// The counters' region, then two partials (one of each end of a CTA's stretch) per CTA.
 size_t paged_decode_workspace_bytes(int R, int sm_count)
 {
-    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16);
-    return kCounterBytes + (size_t)decode_ctas(R, sm_count) * 2 * rows * (kHeadDim + 2) * sizeof(float);
+    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16), ctas = (size_t)(R <= 8 ? 2 : 1) * sm_count;
+    return kCounterBytes + ctas * 2 * rows * (kHeadDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
@@ -933,11 +1020,7 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_coun
 
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, bool pdl, cudaStream_t s)
 {
-    const int rows = p.cand_hi - (p.cand_lo & ~(kTileRows - 1));
-    const int per = kAttnWarps * kImpTiles * kTileRows;
-    const dim3 grid((rows + per - 1) / per, p.c.Hkv, p.c.B);
-    return e2m1 ? launch_kernel(paged_importance_kernel<true>, grid, dim3(kAttnThreads), 0, s, pdl, 0u, p)
-                : launch_kernel(paged_importance_kernel<false>, grid, dim3(kAttnThreads), 0, s, pdl, 0u, p);
+    return e2m1 ? launch_importance<true>(p, pdl, s) : launch_importance<false>(p, pdl, s);
 }
 
 }  // namespace fx
