@@ -129,25 +129,6 @@ __device__ __forceinline__ int tile_count(const Seq& q)
 }
 
 
-// A tile of a sequence is found in three steps, each needing what the one before loaded: a row (position), its
-// page, its place in the pool.  The first nl tiles hold the list -- lane L < 16 (and L + 16 again) knows row L --
-// the others the tail, whose tiles start at multiples of 16, so that such a tile lies inside one page.
-// List: the lane's row (-1: none).  Tail: the tile's first row.
-__device__ __forceinline__ int tile_pos(const PagedAttnParams& p, const Seq& q, int it)
-{
-    if (it >= q.nl) return (q.lo & ~(kTileRows - 1)) + (it - q.nl) * kTileRows;
-    const int e = it * kTileRows + (int)(threadIdx.x & 15);
-    return e < p.kk ? q.idx[e] : -1;
-}
-__device__ __forceinline__ int tile_page(const PagedAttnParams& p, const Seq& q, int it, int& pos)
-{
-    if (it < q.nl && (unsigned)pos >= (unsigned)q.len) {
-        if (it * kTileRows + (int)(threadIdx.x & 15) < p.kk) atomicOr(p.err, FX_DEVERR_INDEX);
-        pos = -1;
-    }
-    return (unsigned)pos < (unsigned)q.len ? q.table[pos >> p.c.page_shift] : 0;   // an empty sequence has no page
-}
-
 __device__ __forceinline__ int64_t row_offset(const PagedCache& c, int id, int64_t sp, int64_t st)
 {
     return (int64_t)(id >> c.page_shift) * sp + (int64_t)(id & c.page_mask) * st;
@@ -167,83 +148,178 @@ struct Slot {
     static constexpr int kBytes = kPos + 64;
 };
 
-// Copies tile `it` into a slot (nothing but the positions where no row is valid).  All lanes call it.
+// Fills slots with the tiles [it, end) of a sequence in order.  The first nl tiles hold the list, the others the
+// tail, whose tiles start at multiples of 16, so that such a tile lies inside one page.  All lanes call it.
+//
+// Tail: the lanes hold the next 32 page numbers, and inside a page the lane's addresses only advance -- a
+// tile costs a few additions beside its copies.  List: the lanes hold the rows of two tiles (lane L: entry L of
+// them), looked up a batch ahead, their positions another batch ahead.
 template <bool E2M1, bool WITH_V>
 struct Feeder {
-    const char* k;    // the lane's places relative to a row: K and V codes or rows, scales
-    const char* v;
-    const char* sc;
+    const PagedAttnParams& p;
+    const Seq& q;
+    const char* k0;   // the lane's places relative to row 0 of page 0: K and V codes or rows, scales
+    const char* v0;
+    const char* s0;
     uint32_t to;      // the lane's place in a slot (codes or rows)
+    int it, end;
+    // tail
+    int pos;          // first row of the next tail tile
+    int pages, page_base;
+    bool fresh, ok;   // no address yet; the page is good
+    const char* ka;
+    const char* va;
+    const char* sa;
+    // list
+    int id, at;       // the lane's pool row (-1: not valid) and position in the current two tiles
+    int at1, page1, at2;
+    bool contig;      // rows of a page follow one another without gaps
 
-    __device__ __forceinline__ Feeder(const PagedCache& c, int h)
+    __device__ __forceinline__ Feeder(const PagedAttnParams& p_, const Seq& q_, int h, int it_, int end_)
+        : p(p_), q(q_), it(it_), end(end_)
     {
+        const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31;
-        if (E2M1) {
-            const int row = lane >> 2, chunk = lane & 3;
-            k = c.k + (int64_t)h * c.sh + 16 * chunk;
-            v = c.v + (int64_t)h * c.sh + 16 * chunk;
-            sc = (lane < 16 ? c.ks : c.vs) + (int64_t)h * c.ssh;
-            to = (row >> 1) * 128 + ((((row & 1) * 4 + chunk) ^ (2 * ((row >> 1) & 3))) << 4);
-        } else {
-            const int row = lane >> 4, chunk = lane & 15;
-            k = c.k + (int64_t)h * c.sh + 16 * chunk;
-            v = c.v + (int64_t)h * c.sh + 16 * chunk;
-            sc = nullptr;
-            to = row * 256 + ((chunk ^ row) << 4);
+        const int chunk = E2M1 ? lane & 3 : lane & 15, row = E2M1 ? lane >> 2 : lane >> 4;
+        k0 = c.k + (int64_t)h * c.sh + 16 * chunk;
+        v0 = c.v + (int64_t)h * c.sh + 16 * chunk;
+        s0 = (lane < 16 ? c.ks : c.vs) + (int64_t)h * c.ssh;
+        to = E2M1 ? (row >> 1) * 128 + ((((row & 1) * 4 + chunk) ^ (2 * ((row >> 1) & 3))) << 4)
+                  : row * 256 + ((chunk ^ row) << 4);
+        contig = c.st == (E2M1 ? 64 : 256) && (!E2M1 || c.sst == 8);
+        if (it < q.nl && it < end) {
+            at = list_pos(it * kTileRows + lane);
+            at1 = list_pos((it + 2) * kTileRows + lane);
+            const int page = list_page(at, it * kTileRows + lane);
+            page1 = list_page(at1, (it + 2) * kTileRows + lane);
+            at2 = list_pos((it + 4) * kTileRows + lane);
+            id = place(at, page);
         }
+        pos = (q.lo & ~(kTileRows - 1)) + (max(it, q.nl) - q.nl) * kTileRows;
+        fresh = true;
+        ok = false;
+        if (end > q.nl) load_pages();
     }
 
-    __device__ __forceinline__ void copy(const PagedAttnParams& p, const Seq& q, int it, int pos, int page,
-                                         uint32_t slot) const
+    __device__ __forceinline__ int list_pos(int e) const { return e < min(p.kk, end * kTileRows) ? q.idx[e] : -1; }
+    __device__ __forceinline__ int list_page(int& t, int e) const
+    {
+        if ((unsigned)t >= (unsigned)q.len) {
+            if (e < min(p.kk, end * kTileRows)) atomicOr(p.err, FX_DEVERR_INDEX);
+            t = -1;
+        }
+        return t >= 0 ? q.table[t >> p.c.page_shift] : 0;
+    }
+    __device__ __forceinline__ int place(int t, int page) const
+    {
+        if (t < 0) return -1;
+        if ((unsigned)page >= (unsigned)p.c.n_pages) {
+            atomicOr(p.err, FX_DEVERR_PAGE);
+            return -1;
+        }
+        return (page << p.c.page_shift) | (t & p.c.page_mask);
+    }
+    __device__ __forceinline__ void load_pages()
+    {
+        page_base = pos >> p.c.page_shift;
+        const int64_t first = (int64_t)(page_base + (int)(threadIdx.x & 31)) << p.c.page_shift;
+        pages = first < q.len ? q.table[page_base + (threadIdx.x & 31)] : -1;
+    }
+
+    __device__ __forceinline__ void feed(uint32_t slot)
+    {
+        if (it < end) {
+            if (it >= q.nl)
+                feed_tail(slot);
+            else
+                feed_list(slot);
+            ++it;
+        }
+        cp_async_commit();
+    }
+
+    __device__ __forceinline__ void feed_tail(uint32_t slot)
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31, j = lane & 15;
-        const bool list = it < q.nl;
-        bool ok = (unsigned)pos < (unsigned)q.len;
-        if (ok && (unsigned)page >= (unsigned)c.n_pages) {
-            atomicOr(p.err, FX_DEVERR_PAGE);
-            ok = false;
+        if (fresh || (pos & c.page_mask) == 0) {
+            fresh = false;
+            if ((pos >> c.page_shift) - page_base >= 32) load_pages();
+            const int page = __shfl_sync(kFull, pages, (pos >> c.page_shift) - page_base);
+            ok = (unsigned)page < (unsigned)c.n_pages;
+            if (!ok && pos < q.len) atomicOr(p.err, FX_DEVERR_PAGE);
+            const int64_t pg = ok ? page : 0, row = pos & c.page_mask;
+            const int64_t o = pg * c.sp + (row + (E2M1 ? lane >> 2 : lane >> 4)) * c.st;
+            ka = k0 + o;
+            va = v0 + o;
+            if (E2M1) sa = s0 + pg * c.ssp + (row + j) * c.sst;
         }
-        const int id = ok ? (page << c.page_shift) | (pos & c.page_mask) : 0;   // the lane's row or the tile's first
-        int at = pos;
-        if (!list) {
-            at = pos + j;
-            ok = ok && at >= q.lo && at < q.len;
-        }
-        if (lane < 16) asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane), "r"(ok ? at : -1) : "memory");
+        const int t = pos + j;
+        if (lane < 16)
+            asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane),
+                         "r"(ok && t >= q.lo && t < q.len ? t : -1)
+                         : "memory");
         if (E2M1) {
-            int r0 = lane >> 2, r1 = r0 + 8, rs = j;   // the rows that this lane copies
-            int64_t o0, o1, os;
-            if (list) {
-                r0 = __shfl_sync(kFull, id, r0);
-                r1 = __shfl_sync(kFull, id, r1);
-                o0 = row_offset(c, r0, c.sp, c.st);
-                o1 = row_offset(c, r1, c.sp, c.st);
-                os = row_offset(c, id, c.ssp, c.sst);
-            } else {
-                o0 = row_offset(c, id, c.sp, c.st) + r0 * c.st;
-                o1 = o0 + 8 * c.st;
-                os = row_offset(c, id, c.ssp, c.sst) + rs * c.sst;
-            }
-            cp_async16(slot + to, k + o0);
-            cp_async16(slot + to + 512, k + o1);
+            const char* k1 = contig ? ka + 512 : ka + 8 * c.st;
+            cp_async16(slot + to, ka);
+            cp_async16(slot + to + 512, k1);
             if (WITH_V) {
-                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to, v + o0);
-                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to + 512, v + o1);
+                const char* v1 = contig ? va + 512 : va + 8 * c.st;
+                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to, va);
+                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to + 512, v1);
             }
-            if (WITH_V || lane < 16) cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, sc + os);
-        } else {
-            int64_t o = list ? 0 : row_offset(c, id, c.sp, c.st) + (lane >> 4) * c.st;
+            if (WITH_V || lane < 16) cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, sa);
+            sa += 16 * c.sst;
+        } else if (contig) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (list) o = row_offset(c, __shfl_sync(kFull, id, (lane >> 4) + 2 * u), c.sp, c.st);
                 const uint32_t dst = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
-                cp_async16(dst, k + o);
-                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, v + o);
-                if (!list) o += 2 * c.st;
+                cp_async16(dst, ka + 512 * u);
+                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, va + 512 * u);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t dst = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
+                cp_async16(dst, ka + 2 * u * c.st);
+                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, va + 2 * u * c.st);
             }
         }
+        ka += 16 * c.st;
+        va += 16 * c.st;
+        pos += kTileRows;
     }
+
+    __device__ __forceinline__ void feed_list(uint32_t slot)
+    {
+        const PagedCache& c = p.c;
+        const int lane = threadIdx.x & 31, j = lane & 15;
+        const int half = parity;
+        const int mine = __shfl_sync(kFull, id, half + j), t = __shfl_sync(kFull, at, half + j);
+        if (lane < 16)
+            asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane), "r"(mine >= 0 ? t : -1)
+                         : "memory");
+        constexpr int kCopies = E2M1 ? 2 : 8;   // rows of K (and V) that a lane copies 16 bytes of
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+            const int row = E2M1 ? (lane >> 2) + 8 * u : (lane >> 4) + 2 * u;
+            const int64_t o = row_offset(c, max(__shfl_sync(kFull, id, half + row), 0), c.sp, c.st);
+            const uint32_t dst = E2M1 ? slot + to + 512 * u : slot + u * 512 + (to ^ ((2 * u & 6) << 4));
+            cp_async16(dst, k0 + o);
+            if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, v0 + o);
+        }
+        if (E2M1 && (WITH_V || lane < 16))
+            cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, s0 + row_offset(c, max(mine, 0), c.ssp, c.sst));
+        parity ^= 16;
+        if (parity == 0) {   // the next two tiles
+            at = at1;
+            id = place(at, page1);
+            at1 = at2;
+            page1 = list_page(at1, (it + 3) * kTileRows + lane);
+            at2 = list_pos((it + 5) * kTileRows + lane);
+        }
+    }
+    int parity = 0;
 };
 
 // Calls f(j, a0, a1, a2, a3) with the A fragments of the eight 16-dimension steps of S^T = K Q^T.
@@ -448,8 +524,8 @@ struct Acc {
 };
 
 // Weights of a tile from its logits s (row g + 8 (e >> 1) of the tile, query row 2t + (e & 1) of N tile n), in
-// place; moves the references when one would not fit.  hide: bit 4n + e, that logit does not count.
-template <bool E2M1, int NT, bool DUP>
+// place; moves the references when one would not fit.  With HIDE, bit 4n + e of hide: that logit does not count.
+template <bool HIDE, bool E2M1, int NT, bool DUP>
 __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4], uint32_t hide)
 {
     float x2[NT][4];
@@ -459,7 +535,7 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4]
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             x2[n][e] = fmaf(s[n][e], a.rs[n][e & 1], a.bias[n][e & 1]);
-            if ((hide >> (4 * n + e)) & 1u) x2[n][e] = -INFINITY;
+            if (HIDE && ((hide >> (4 * n + e)) & 1u)) x2[n][e] = -INFINITY;
             over |= x2[n][e] > kTop;
         }
     if (__any_sync(kFull, over)) {
@@ -468,8 +544,8 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4]
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float z0 = (hide >> (4 * n + e)) & 1u ? -INFINITY : s[n][e] * a.rs[n][e];
-                const float z1 = (hide >> (4 * n + e + 2)) & 1u ? -INFINITY : s[n][e + 2] * a.rs[n][e];
+                const float z0 = HIDE && ((hide >> (4 * n + e)) & 1u) ? -INFINITY : s[n][e] * a.rs[n][e];
+                const float z1 = HIDE && ((hide >> (4 * n + e + 2)) & 1u) ? -INFINITY : s[n][e + 2] * a.rs[n][e];
                 float m = fmaxf(z0, z1);
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
@@ -485,8 +561,8 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4]
                     }
                     a.bias[n][e] = nb;
                 }
-                x2[n][e] = (hide >> (4 * n + e)) & 1u ? -INFINITY : fmaf(s[n][e], a.rs[n][e], nb);
-                x2[n][e + 2] = (hide >> (4 * n + e + 2)) & 1u ? -INFINITY : fmaf(s[n][e + 2], a.rs[n][e], nb);
+                x2[n][e] = HIDE && ((hide >> (4 * n + e)) & 1u) ? -INFINITY : fmaf(s[n][e], a.rs[n][e], nb);
+                x2[n][e + 2] = HIDE && ((hide >> (4 * n + e + 2)) & 1u) ? -INFINITY : fmaf(s[n][e + 2], a.rs[n][e], nb);
             }
     }
 #pragma unroll
@@ -531,8 +607,11 @@ __device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
     }
-    uint32_t hide = 0;
-    if (late || vm != 0xffffu) {
+    const bool edge = late || vm != 0xffffu;
+    if (!edge) {
+        weights<false, E2M1, NT, DUP>(a, s, 0);
+    } else {
+        uint32_t hide = 0;
         const int p0 = (int)lds32(slot + Slot<E2M1>::kPos + 4 * g), p1 = (int)lds32(slot + Slot<E2M1>::kPos + 32 + 4 * g);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -542,8 +621,8 @@ __device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, 
                 const int at = e >> 1 ? p1 : p0;
                 if (at < 0 || at > seen + r % p.Mq) hide |= 1u << (4 * n + e);
             }
+        weights<true, E2M1, NT, DUP>(a, s, hide);
     }
-    weights<E2M1, NT, DUP>(a, s, hide);
 
     // O^T += V^T P^T with P as a sum of two 16-bit parts.  Each tile's product starts from zero and is added
     // to O by an fp32 addition: the tensor core aligns all products to the accumulator and cuts them off
@@ -566,7 +645,7 @@ __device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, 
         mma16_zero<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
         if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
     };
-    if (vm == 0xffffu && !late) {
+    if (!edge) {
         v_tiles<E2M1, false>(slot, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -709,22 +788,14 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
-        // the ring's first tiles on their way; then each step feeds the tile kStages - 1 turns ahead, whose
-        // page was looked up a turn earlier and whose position another turn earlier
-        const Feeder<E2M1, true> feeder(p.c, h);
-        int it = s0 + warp;
-        int pos[kStages], page[kStages];
+        // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on);
+        // the ring's first tiles go on their way, then each turn feeds the tile kStages - 1 turns ahead
+        const int mine = s1 - s0;
+        int it = s0 + mine * warp / W;
+        const int stop = s0 + mine * (warp + 1) / W;
+        Feeder<E2M1, true> feeder(p, seq, h, it, stop);
 #pragma unroll
-        for (int u = 0; u < kStages; ++u) pos[u] = it + u * W < s1 ? tile_pos(p, seq, it + u * W) : -1;
-#pragma unroll
-        for (int u = 0; u < kStages; ++u) page[u] = it + u * W < s1 ? tile_page(p, seq, it + u * W, pos[u]) : 0;
-#pragma unroll
-        for (int u = 0; u < kStages - 1; ++u) {
-            if (it + u * W < s1) feeder.copy(p, seq, it + u * W, pos[u], page[u], ring + u * kSlot);
-            cp_async_commit();
-        }
-        int pos1 = pos[kStages - 1], page1 = page[kStages - 1];
-        int pos2 = it + kStages * W < s1 ? tile_pos(p, seq, it + kStages * W) : -1;
+        for (int u = 0; u < kStages - 1; ++u) feeder.feed(ring + u * kSlot);
 
         Acc<E2M1, NT, DUP> a;
 #pragma unroll
@@ -744,15 +815,10 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         }
 
         uint32_t slot = ring, feed = ring + (kStages - 1) * kSlot;
-        for (; it < s1; it += W) {
+        for (; it < stop; ++it) {
             cp_async_wait_stages<kStages - 1>();   // this lane's copies of the tile; the barrier covers the others'
             __syncwarp();
-            const int in = it + (kStages - 1) * W;
-            if (in < s1) feeder.copy(p, seq, in, pos1, page1, feed);
-            cp_async_commit();
-            pos1 = pos2;
-            page1 = in + W < s1 ? tile_page(p, seq, in + W, pos1) : 0;
-            pos2 = in + 2 * W < s1 ? tile_pos(p, seq, in + 2 * W) : -1;
+            feeder.feed(feed);
             attend_tile<E2M1, NT, DUP>(p, a, slot, r0, seen);
             feed = slot;
             slot = slot + kSlot == ring + kStages * kSlot ? ring : slot + kSlot;
@@ -890,20 +956,10 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
     const int first = (p.cand_lo & ~(kTileRows - 1)) + (blockIdx.x * kImpWarps + warp) * (kImpTiles * kTileRows);
     seq.lo = first;
     const int ntile = first < len ? min(kImpTiles, (len - first + kTileRows - 1) / kTileRows) : 0;   // with rows in them
-    const Feeder<E2M1, false> feeder(p.c, h);
+    Feeder<E2M1, false> feeder(p, seq, h, 0, ntile);
     const uint32_t ring = smem_addr(smem) + warp * kImpStages * kSlot;
-    int pos[kImpStages], page[kImpStages];
 #pragma unroll
-    for (int u = 0; u < kImpStages; ++u) {
-        pos[u] = tile_pos(p, seq, u);
-        page[u] = u < ntile ? tile_page(p, seq, u, pos[u]) : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < kImpStages - 1; ++u) {
-        if (u < ntile) feeder.copy(p, seq, u, pos[u], page[u], ring + u * kSlot);
-        cp_async_commit();
-    }
-    int page1 = page[kImpStages - 1];
+    for (int u = 0; u < kImpStages - 1; ++u) feeder.feed(ring + u * kSlot);
     const int nq = (p.R + 7) / 8;
     for (int n = warp; n < nq; n += kImpWarps) {
         const int r = 8 * n + g;
@@ -928,11 +984,7 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
             const uint32_t slot = ring + (u % kImpStages) * kSlot;
             cp_async_wait_stages<kImpStages - 1>();
             __syncwarp();
-            const int in = u + kImpStages - 1;
-            if (in < ntile) feeder.copy(p, seq, in, tile_pos(p, seq, in), page1, ring + (in % kImpStages) * kSlot);
-            cp_async_commit();
-            int next = tile_pos(p, seq, in + 1);
-            page1 = in + 1 < ntile ? tile_page(p, seq, in + 1, next) : 0;
+            feeder.feed(ring + ((u + kImpStages - 1) % kImpStages) * kSlot);
             uint32_t a[8][4];
             k_steps<E2M1, false>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                 a[j][0] = a0;
