@@ -1,8 +1,8 @@
 // Attention over a paged cache for sm_103a, bf16 or 4-bit: fx_paged_decode and fx_paged_importance.
 //
-// Work unit of a warp: a tile of 16 cache rows of one (sequence, KV head).  Every warp owns a ring of tile slots in
-// shared memory and fills it with cp.async a few tiles ahead; no warp waits for another until their results
-// meet.  S^T = K Q^T has the cache rows on M and the query rows on N (mma.sync m16n8k16), O^T += V^T P^T the
+// Work unit of a warp: a tile of 16 cache rows of one (sequence, KV head); two tiles at a time in 4 bits.  Every
+// warp owns a ring of slots in shared memory and fills it with cp.async ahead of its work; no warp waits for
+// another until their results meet.  S^T = K Q^T has the cache rows on M and the query rows on N (mma.sync m16n8k16), O^T += V^T P^T the
 // dimensions on M and the cache rows on K.
 //
 // 4-bit rows: a lane's K fragments are 16 bytes of codes of two rows (the dimensions are permuted inside the
@@ -173,10 +173,12 @@ struct Feeder {
     // list
     int id, at;       // the lane's pool row (-1: not valid) and position in the current two tiles
     int at1, page1, at2;
+    int parity = 0;   // 16: the second of the two tiles is next
     bool contig;      // rows of a page follow one another without gaps
+    int clear;        // rows below this one are seen by every query
 
     __device__ __forceinline__ Feeder(const PagedAttnParams& p_, const Seq& q_, int h, int it_, int end_)
-        : p(p_), q(q_), it(it_), end(end_)
+        : p(p_), q(q_), it(it_), end(end_), clear(q_.len - p_.Mq + 1)
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31;
@@ -226,19 +228,27 @@ struct Feeder {
         pages = first < q.len ? q.table[page_base + (threadIdx.x & 31)] : -1;
     }
 
-    __device__ __forceinline__ void feed(uint32_t slot)
+    // Feeds the next tile (none past the end: a slot without valid rows).  True when a row of it is not valid or
+    // not seen by every query; only then the rows' positions are in the slot.
+    __device__ __forceinline__ bool feed(uint32_t slot)
     {
+        bool edge = true;
         if (it < end) {
-            if (it >= q.nl)
-                feed_tail(slot);
-            else
-                feed_list(slot);
+            edge = it >= q.nl ? feed_tail(slot) : feed_list(slot);
             ++it;
+        } else {
+            put_pos(slot, -1);
         }
-        cp_async_commit();
+        return edge;
     }
 
-    __device__ __forceinline__ void feed_tail(uint32_t slot)
+    __device__ __forceinline__ void put_pos(uint32_t slot, int t)
+    {
+        const int lane = threadIdx.x & 31;
+        if (lane < 16) asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane), "r"(t) : "memory");
+    }
+
+    __device__ __forceinline__ bool feed_tail(uint32_t slot)
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31, j = lane & 15;
@@ -254,51 +264,53 @@ struct Feeder {
             va = v0 + o;
             if (E2M1) sa = s0 + pg * c.ssp + (row + j) * c.sst;
         }
-        const int t = pos + j;
-        if (lane < 16)
-            asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane),
-                         "r"(ok && t >= q.lo && t < q.len ? t : -1)
-                         : "memory");
+        const bool edge = !ok || pos < q.lo || pos + kTileRows > clear;
+        if (edge) {
+            const int t = pos + j;
+            put_pos(slot, ok && t >= q.lo && t < q.len ? t : -1);
+        }
+        const uint32_t dst = slot + to;
         if (E2M1) {
-            const char* k1 = contig ? ka + 512 : ka + 8 * c.st;
-            cp_async16(slot + to, ka);
-            cp_async16(slot + to + 512, k1);
-            if (WITH_V) {
-                const char* v1 = contig ? va + 512 : va + 8 * c.st;
-                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to, va);
-                cp_async16(slot + Slot<E2M1, WITH_V>::kV + to + 512, v1);
+            cp_async16(dst, ka);
+            if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, va);
+            if (contig) {
+                cp_async16(dst + 512, ka + 512);
+                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV + 512, va + 512);
+            } else {
+                cp_async16(dst + 512, ka + 8 * c.st);
+                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV + 512, va + 8 * c.st);
             }
             if (WITH_V || lane < 16) cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, sa);
             sa += 16 * c.sst;
         } else if (contig) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const uint32_t dst = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
-                cp_async16(dst, ka + 512 * u);
-                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, va + 512 * u);
+                const uint32_t d = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
+                cp_async16(d, ka + 512 * u);
+                if (WITH_V) cp_async16(d + Slot<E2M1, WITH_V>::kV, va + 512 * u);
             }
         } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const uint32_t dst = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
-                cp_async16(dst, ka + 2 * u * c.st);
-                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, va + 2 * u * c.st);
+                const uint32_t d = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
+                cp_async16(d, ka + 2 * u * c.st);
+                if (WITH_V) cp_async16(d + Slot<E2M1, WITH_V>::kV, va + 2 * u * c.st);
             }
         }
         ka += 16 * c.st;
         va += 16 * c.st;
         pos += kTileRows;
+        return edge;
     }
 
-    __device__ __forceinline__ void feed_list(uint32_t slot)
+    __device__ __forceinline__ bool feed_list(uint32_t slot)
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31, j = lane & 15;
         const int half = parity;
         const int mine = __shfl_sync(kFull, id, half + j), t = __shfl_sync(kFull, at, half + j);
-        if (lane < 16)
-            asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane), "r"(mine >= 0 ? t : -1)
-                         : "memory");
+        const bool edge = __any_sync(kFull, mine < 0 || t >= clear);
+        if (edge) put_pos(slot, mine >= 0 ? t : -1);
         constexpr int kCopies = E2M1 ? 2 : 8;   // rows of K (and V) that a lane copies 16 bytes of
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
@@ -318,8 +330,8 @@ struct Feeder {
             page1 = list_page(at1, (it + 3) * kTileRows + lane);
             at2 = list_pos((it + 5) * kTileRows + lane);
         }
+        return edge;
     }
-    int parity = 0;
 };
 
 // Calls f(j, a0, a1, a2, a3) with the A fragments of the eight 16-dimension steps of S^T = K Q^T.
@@ -360,62 +372,81 @@ __device__ __forceinline__ void k_steps(uint32_t slot, F&& f)
     }
 }
 
-// Calls f(i, a0, a1, a2, a3) with the A fragments of the eight M tiles of O^T += V^T P^T.  MASKED: rows outside
-// `vm` count as zero, whatever they hold.
-template <bool E2M1, bool MASKED, typename F>
-__device__ __forceinline__ void v_tiles(uint32_t slot, uint32_t vm, F&& f)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t on = vm >> (2 * t);   // bits 0, 1, 8, 9: rows 2t, 2t + 1, 2t + 8, 2t + 9
-    if constexpr (E2M1) {
+// A tile's V rows: get(i) gives the A fragment of M tile i of O^T += V^T P^T.  MASKED: rows outside `vm` count as
+// zero, whatever they hold.
+template <bool E2M1>
+struct VTile;
+template <>
+struct VTile<true> {
+    uint32_t code[2][4];   // [dimensions 16g .. + 7, + 8 .. + 15][rows 2t, 2t + 1: even, odd dimensions; 2t + 8, + 9]
+    uint32_t s01, s23;     // scales of rows 2t, 2t + 1 and 2t + 8, 2t + 9
+    uint32_t f[4][4];      // the four M tiles in use
+
+    template <bool MASKED>
+    __device__ __forceinline__ void load(uint32_t slot, uint32_t vm)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const uint32_t sa = slot + Slot<true>::kScale + 128 + 16 * t + g;
         uint32_t vs01 = lds8(sa) | (lds8(sa + 8) << 8), vs23 = lds8(sa + 64) | (lds8(sa + 72) << 8);
         if (MASKED) {
+            const uint32_t on = vm >> (2 * t);   // bits 0, 1, 8, 9
             vs01 &= (on & 1u ? 0xffu : 0u) | (on & 2u ? 0xff00u : 0u);
             vs23 &= (on & 0x100u ? 0xffu : 0u) | (on & 0x200u ? 0xff00u : 0u);
         }
-        const uint32_t s01 = e4m3x2_to_f16x2(vs01), s23 = e4m3x2_to_f16x2(vs23);
+        s01 = e4m3x2_to_f16x2(vs01);
+        s23 = e4m3x2_to_f16x2(vs23);
         const uint32_t in = t * 128 + (((g >> 1) ^ (2 * t)) << 4) + (g & 1) * 8;
         const uint32_t va = slot + Slot<true>::kV + in, vb = slot + Slot<true>::kV + (in ^ 64u);
         const uint2 x[4] = {lds64(va), lds64(vb), lds64(va + 512), lds64(vb + 512)};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t a[4][4];
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                // neighbouring rows' codes of one dimension side by side, then one conversion a pair
+            for (int j = 0; j < 2; ++j) {
+                // neighbouring rows' codes of one dimension side by side, so that one conversion takes the pair
                 const uint32_t x0 = j ? x[2 * u].y : x[2 * u].x, x1 = j ? x[2 * u + 1].y : x[2 * u + 1].x;
-                const uint32_t even = (x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u);
-                const uint32_t odd = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
-                e2m1x8_to_f16(even, a[2 * u][0], a[2 * u][1], a[2 * u][2], a[2 * u][3]);
-                e2m1x8_to_f16(odd, a[2 * u + 1][0], a[2 * u + 1][1], a[2 * u + 1][2], a[2 * u + 1][3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[2 * u][i] = hmul2_u32(a[2 * u][i], u ? s23 : s01);
-                    a[2 * u + 1][i] = hmul2_u32(a[2 * u + 1][i], u ? s23 : s01);
-                }
+                code[j][2 * u] = (x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u);
+                code[j][2 * u + 1] = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
             }
+    }
+    template <bool MASKED>
+    __device__ __forceinline__ void get(int i, uint32_t (&x)[4])
+    {
+        if ((i & 3) == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f(4 * j + i, a[0][i], a[1][i], a[2][i], a[3][i]);
+            for (int u = 0; u < 4; ++u) e2m1x8_to_f16(code[i >> 2][u], f[u][0], f[u][1], f[u][2], f[u][3]);
         }
-    } else {
-        const uint32_t m01 = (on & 1u ? 0xffffu : 0u) | (on & 2u ? 0xffff0000u : 0u);
-        const uint32_t m23 = (on & 0x100u ? 0xffffu : 0u) | (on & 0x200u ? 0xffff0000u : 0u);
-        const int row = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4_t(slot + Slot<false>::kV + kv_off(row, 2 * i + ((lane >> 3) & 1)), a0, a1, a2, a3);
-            if (MASKED) {
-                a0 &= m01;
-                a1 &= m01;
-                a2 &= m23;
-                a3 &= m23;
-            }
-            f(i, a0, a1, a2, a3);
+        for (int u = 0; u < 4; ++u) x[u] = hmul2_u32(f[u][i & 3], u < 2 ? s01 : s23);
+    }
+};
+template <>
+struct VTile<false> {
+    uint32_t at;
+    uint32_t m01, m23;
+
+    template <bool MASKED>
+    __device__ __forceinline__ void load(uint32_t slot, uint32_t vm)
+    {
+        at = slot + Slot<false>::kV;
+        if (MASKED) {
+            const uint32_t on = vm >> (2 * (threadIdx.x & 3));   // bits 0, 1, 8, 9: rows 2t, 2t + 1, 2t + 8, 2t + 9
+            m01 = (on & 1u ? 0xffffu : 0u) | (on & 2u ? 0xffff0000u : 0u);
+            m23 = (on & 0x100u ? 0xffffu : 0u) | (on & 0x200u ? 0xffff0000u : 0u);
         }
     }
-}
+    template <bool MASKED>
+    __device__ __forceinline__ void get(int i, uint32_t (&x)[4])
+    {
+        const int lane = threadIdx.x & 31;
+        ldsm_x4_t(at + kv_off((lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)), x[0], x[1], x[2], x[3]);
+        if (MASKED) {
+            x[0] &= m01;
+            x[1] &= m01;
+            x[2] &= m23;
+            x[3] &= m23;
+        }
+    }
+};
 // The two dimensions that rows g and g + 8 of M tile i hold.
 template <bool E2M1>
 __device__ __forceinline__ int v_dim(int i, int g, int half)
@@ -523,20 +554,22 @@ struct Acc {
     float o[NT][8][4];
 };
 
-// Weights of a tile from its logits s (row g + 8 (e >> 1) of the tile, query row 2t + (e & 1) of N tile n), in
-// place; moves the references when one would not fit.  With HIDE, bit 4n + e of hide: that logit does not count.
-template <bool HIDE, bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4], uint32_t hide)
+// Weights of U tiles from their logits s[u * NT + n][e] (row g + 8 (e >> 1) of tile u, query row 2t + (e & 1) of
+// N tile n), in place; moves the references when one would not fit.  With HIDE (one tile), bit 4n + e of hide:
+// that logit does not count.
+template <bool HIDE, int U, bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT][4], uint32_t hide)
 {
-    float x2[NT][4];
+    static_assert(!HIDE || U == 1, "");
+    auto hidden = [&](int n, int e) { return HIDE && ((hide >> (4 * n + e)) & 1u) != 0; };
+    float x2[U * NT][4];
     bool over = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < U * NT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            x2[n][e] = fmaf(s[n][e], a.rs[n][e & 1], a.bias[n][e & 1]);
-            if (HIDE && ((hide >> (4 * n + e)) & 1u)) x2[n][e] = -INFINITY;
-            over |= x2[n][e] > kTop;
+            x2[m][e] = hidden(m, e) ? -INFINITY : fmaf(s[m][e], a.rs[m % NT][e & 1], a.bias[m % NT][e & 1]);
+            over |= x2[m][e] > kTop;
         }
     if (__any_sync(kFull, over)) {
         // new references: the largest logit of each row lands on 2^kBase
@@ -544,9 +577,12 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4]
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float z0 = HIDE && ((hide >> (4 * n + e)) & 1u) ? -INFINITY : s[n][e] * a.rs[n][e];
-                const float z1 = HIDE && ((hide >> (4 * n + e + 2)) & 1u) ? -INFINITY : s[n][e + 2] * a.rs[n][e];
-                float m = fmaxf(z0, z1);
+                float m = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int z = e; z < 4; z += 2)
+                        if (!hidden(n, z)) m = fmaxf(m, s[u * NT + n][z] * a.rs[n][e]);
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
@@ -561,73 +597,58 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[NT][4]
                     }
                     a.bias[n][e] = nb;
                 }
-                x2[n][e] = HIDE && ((hide >> (4 * n + e)) & 1u) ? -INFINITY : fmaf(s[n][e], a.rs[n][e], nb);
-                x2[n][e + 2] = HIDE && ((hide >> (4 * n + e + 2)) & 1u) ? -INFINITY : fmaf(s[n][e + 2], a.rs[n][e], nb);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int z = e; z < 4; z += 2)
+                        x2[u * NT + n][z] = hidden(n, z) ? -INFINITY : fmaf(s[u * NT + n][z], a.rs[n][e], nb);
             }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < U * NT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float w = fast_exp2(x2[n][e]);
+            float w = fast_exp2(x2[m][e]);
             if (!E2M1) {
                 // to 17 bits, which the two bf16 parts hold exactly: the sum then counts the weights as
                 // they are multiplied (one weight far above the others comes out as 1)
                 const float c = __fmul_rn(w, 129.f);
                 w = __fsub_rn(c, __fsub_rn(c, w));
             }
-            s[n][e] = w;
-            a.l[n][e & 1] += w;
+            s[m][e] = w;
+            a.l[m % NT][e & 1] += w;
         }
 }
 
-// One tile: logits, weights, O^T += V^T P^T.
+// Logits of a tile: s[n][e] of row g + 8 (e >> 1) and query row 2t + (e & 1) of N tile n.
 template <bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int r0,
-                                            int seen)
+__device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slot, float (&s)[NT][4])
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int pos = (int)lds32(slot + Slot<E2M1>::kPos + 4 * (lane & 15));
-    const uint32_t vm = __ballot_sync(kFull, pos >= 0) & 0xffffu;   // the valid rows
-    const bool late = __any_sync(kFull, pos > seen);                // one lies past what query 0 sees
-    float s[NT][4];
-    {
-        float s2[NT][2][4];
-        k_steps<E2M1, true>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    float s2[NT][2][4];   // two chains of products, for their latency
+    k_steps<E2M1, true>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (j < 2)
-                    mma16_zero<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
-                else
-                    mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
-            }
-        });
+        for (int n = 0; n < NT; ++n) {
+            if (j < 2)
+                mma16_zero<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+            else
+                mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+        }
+    });
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
-    }
-    const bool edge = late || vm != 0xffffu;
-    if (!edge) {
-        weights<false, E2M1, NT, DUP>(a, s, 0);
-    } else {
-        uint32_t hide = 0;
-        const int p0 = (int)lds32(slot + Slot<E2M1>::kPos + 4 * g), p1 = (int)lds32(slot + Slot<E2M1>::kPos + 32 + 4 * g);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
-                const int at = e >> 1 ? p1 : p0;
-                if (at < 0 || at > seen + r % p.Mq) hide |= 1u << (4 * n + e);
-            }
-        weights<true, E2M1, NT, DUP>(a, s, hide);
-    }
+        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
+}
 
-    // O^T += V^T P^T with P as a sum of two 16-bit parts.  Each tile's product starts from zero and is added
-    // to O by an fp32 addition: the tensor core aligns all products to the accumulator and cuts them off
-    // (2^-23 of it), which over a long row costs small weights beside a large one, and drifts.
-    uint32_t bh[NT][2], bl[NT][2];
+// A tile's weights as B fragments: two 16-bit parts (with DUP the low part sits in columns 4..7 of the first).
+template <int NT>
+struct Weights {
+    uint32_t hi[NT][2], lo[NT][2];
+};
+template <bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void fragments(const float (&s)[NT][4], Weights<NT>& w)
+{
+    const int t = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -635,31 +656,104 @@ __device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, 
             uint32_t hi, lo;
             split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo);
             if (DUP) {
-                bh[n][u] = movmatrix_t(t < 2 ? hi : lo);
+                w.hi[n][u] = movmatrix_t(t < 2 ? hi : lo);
             } else {
-                bh[n][u] = movmatrix_t(hi);
-                bl[n][u] = movmatrix_t(lo);
+                w.hi[n][u] = movmatrix_t(hi);
+                w.lo[n][u] = movmatrix_t(lo);
             }
         }
-    auto term = [&](float (&c)[4], int n, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-        mma16_zero<E2M1>(c, a0, a1, a2, a3, bh[n][0], bh[n][1]);
-        if (!DUP) mma16<E2M1>(c, a0, a1, a2, a3, bl[n][0], bl[n][1]);
-    };
-    if (!edge) {
-        v_tiles<E2M1, false>(slot, vm, [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+}
+template <bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void term(float (&c)[4], const Weights<NT>& w, int n, const uint32_t (&v)[4], bool first)
+{
+    if (first)
+        mma16_zero<E2M1>(c, v[0], v[1], v[2], v[3], w.hi[n][0], w.hi[n][1]);
+    else
+        mma16<E2M1>(c, v[0], v[1], v[2], v[3], w.hi[n][0], w.hi[n][1]);
+    if (!DUP) mma16<E2M1>(c, v[0], v[1], v[2], v[3], w.lo[n][0], w.lo[n][1]);
+}
+
+// U tiles whose rows all count for every query.
+//
+// O^T += V^T P^T: the tiles' product starts from zero and is added to O by an fp32 addition.  The tensor core
+// aligns all products to the accumulator and cuts them off (2^-23 of it): accumulated over a long row that costs
+// small weights beside a large one, and drifts.
+template <bool E2M1, int NT, bool DUP, int U>
+__device__ __forceinline__ void attend(Acc<E2M1, NT, DUP>& a, uint32_t slot)
+{
+    constexpr int kSlot = Slot<E2M1>::kBytes;
+    float s[U * NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float c[4];
-                term(c, n, a0, a1, a2, a3);
+    for (int u = 0; u < U; ++u) logits<E2M1, NT, DUP>(a, slot + u * kSlot, reinterpret_cast<float(&)[NT][4]>(s[u * NT]));
+    weights<false, U, E2M1, NT, DUP>(a, s, 0);
+    Weights<NT> w[U];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a.o[n][i][e] += c[e];
-            }
-        });
-        return;
+    for (int u = 0; u < U; ++u) fragments<E2M1, NT, DUP>(reinterpret_cast<float(&)[NT][4]>(s[u * NT]), w[u]);
+    VTile<E2M1> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u].template load<false>(slot + u * kSlot, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float c[NT][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint32_t x[4];
+            v[u].template get<false>(i, x);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) term<E2M1, NT, DUP>(c[n], w[u], n, x, u == 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a.o[n][i][e] += c[n][e];
     }
-    // rows that are not valid, or that only later queries see, may hold anything, and 0 * NaN is NaN: they count
-    // as zeros, in one product per query position where positions differ, taken by that position's query rows
-    const int passes = late ? p.Mq : 1;
+}
+
+// A tile with rows that do not count for every query (not valid, or past what some query sees), or a whole one
+// beside such a tile.
+template <bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int r0,
+                                            int seen, bool whole)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    int pos = 0;   // of a whole tile: seen by all
+    if (!whole) pos = (int)lds32(slot + Slot<E2M1>::kPos + 4 * (lane & 15));
+    const uint32_t vm = __ballot_sync(kFull, pos >= 0) & 0xffffu;   // the valid rows
+    if (vm == 0) return;
+    float s[NT][4];
+    logits<E2M1, NT, DUP>(a, slot, s);
+    uint32_t hide = 0;
+    const int p0 = __shfl_sync(kFull, pos, g), p1 = __shfl_sync(kFull, pos, g + 8);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
+            const int at = e >> 1 ? p1 : p0;
+            if (at < 0 || at > seen + r % p.Mq) hide |= 1u << (4 * n + e);
+        }
+    weights<true, 1, E2M1, NT, DUP>(a, s, hide);
+    Weights<NT> w;
+    fragments<E2M1, NT, DUP>(s, w);
+    // Rows that are not valid may hold anything, and 0 * NaN is NaN: they count as zeros.  Rows that only later
+    // queries see do so too where they hold an infinity or a NaN: then there is one product per query position,
+    // over the rows that it sees, taken by its query rows alone.
+    int passes = 1;
+    if (__any_sync(kFull, pos > seen)) {
+        bool bad = false;
+        if (E2M1) {   // a NaN scale (the lane looks at half the scales of row lane / 2)
+            const uint32_t z = lds32(slot + Slot<E2M1>::kScale + 128 + 4 * lane) & 0x7f7f7f7fu;
+            const int of = __shfl_sync(kFull, pos, lane >> 1);
+            bad = of > seen && __vcmpeq4(z, 0x7f7f7f7fu) != 0;
+        } else {      // an all-ones exponent
+            for (int j = 0; j < 16; ++j) {
+                const uint2 z = lds64(slot + Slot<E2M1>::kV + 256 * j + 8 * lane);
+                const uint32_t x = __vcmpeq2(z.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(z.y & 0x7f807f80u, 0x7f807f80u);
+                bad |= __shfl_sync(kFull, pos, j) > seen && x != 0;
+            }
+        }
+        if (__any_sync(kFull, bad)) passes = p.Mq;
+    }
     for (int i = 0; i < passes; ++i) {
         uint32_t add = 0;   // bit 2n + e: query row 2t + e of N tile n
 #pragma unroll
@@ -667,19 +761,24 @@ __device__ __forceinline__ void attend_tile(const PagedAttnParams& p, Acc<E2M1, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
-                if (!late || r % p.Mq == i) add |= 1u << (2 * n + e);
+                if (passes == 1 || r % p.Mq == i) add |= 1u << (2 * n + e);
             }
-        const uint32_t vi = late ? __ballot_sync(kFull, pos <= seen + i) & vm : vm;
-        v_tiles<E2M1, true>(slot, vi, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        const uint32_t vi = passes == 1 ? vm : __ballot_sync(kFull, pos <= seen + i) & vm;
+        VTile<E2M1> v;
+        v.template load<true>(slot, vi);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t x[4];
+            v.template get<true>(j, x);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float c[4];
-                term(c, n, a0, a1, a2, a3);
+                term<E2M1, NT, DUP>(c, w, n, x, true);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if ((add >> (2 * n + (e & 1))) & 1u) a.o[n][j][e] += c[e];
             }
-        });
+        }
     }
 }
 
@@ -691,8 +790,9 @@ struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
     static constexpr int kWarps = 8;
     static constexpr int kCtas = E2M1 && NT == 1 ? 2 : 1;   // per SM
-    static constexpr int kStages = E2M1 ? 4 : 3;
-    static constexpr int kRing = kStages * Slot<E2M1>::kBytes;   // bytes of a warp; its partial O later takes them
+    static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
+    static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
+    static constexpr int kRing = kStages * kUnit * Slot<E2M1>::kBytes;   // bytes of a warp; its partial O later takes them
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
     static_assert(kRows * kHeadDim * 4 <= kRing, "a warp's partial O lies in its ring");
 };
@@ -710,7 +810,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     paged_decode_kernel(const PagedAttnParams p)
 {
     using S = Shape<E2M1, NT, DUP>;
-    constexpr int kRows = S::kRows, W = S::kWarps, kThreadsA = 32 * W, kStages = S::kStages, kSlot = Slot<E2M1>::kBytes;
+    constexpr int kRows = S::kRows, W = S::kWarps, kThreadsA = 32 * W, kStages = S::kStages, U = S::kUnit, kSlot = Slot<E2M1>::kBytes;
     constexpr int kPitch = S::kRing / 4;   // floats between the warps' partial O
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
@@ -789,13 +889,19 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
         // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on);
-        // the ring's first tiles go on their way, then each turn feeds the tile kStages - 1 turns ahead
+        // the ring's first units go on their way, then each turn feeds the unit kStages - 1 turns ahead
         const int mine = s1 - s0;
         int it = s0 + mine * warp / W;
         const int stop = s0 + mine * (warp + 1) / W;
         Feeder<E2M1, true> feeder(p, seq, h, it, stop);
+        uint32_t edges = 0;   // bit k U + u: tile U - 1 - u of the unit fed k turns ago has an edge
+        auto feed = [&](uint32_t slot) {
 #pragma unroll
-        for (int u = 0; u < kStages - 1; ++u) feeder.feed(ring + u * kSlot);
+            for (int u = 0; u < U; ++u) edges = 2 * edges + (feeder.feed(slot + u * kSlot) ? 1u : 0u);
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) feed(ring + k * U * kSlot);
 
         Acc<E2M1, NT, DUP> a;
 #pragma unroll
@@ -814,14 +920,21 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
         }
 
-        uint32_t slot = ring, feed = ring + (kStages - 1) * kSlot;
-        for (; it < stop; ++it) {
-            cp_async_wait_stages<kStages - 1>();   // this lane's copies of the tile; the barrier covers the others'
+        uint32_t slot = ring, into = ring + (kStages - 1) * U * kSlot;
+        for (; it < stop; it += U) {
+            cp_async_wait_stages<kStages - 1>();   // this lane's copies of the unit; the barrier covers the others'
             __syncwarp();
-            feeder.feed(feed);
-            attend_tile<E2M1, NT, DUP>(p, a, slot, r0, seen);
-            feed = slot;
-            slot = slot + kSlot == ring + kStages * kSlot ? ring : slot + kSlot;
+            feed(into);
+            const uint32_t edge = (edges >> ((kStages - 1) * U)) & ((1u << U) - 1);
+            if (edge != 0) {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u)
+                    attend_edge<E2M1, NT, DUP>(p, a, slot + u * kSlot, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
+            } else {
+                attend<E2M1, NT, DUP, U>(a, slot);
+            }
+            into = slot;
+            slot = slot + U * kSlot == ring + S::kRing ? ring : slot + U * kSlot;
         }
         cp_async_wait_all_groups();
         __syncwarp();   // every lane is done with the ring
@@ -939,14 +1052,14 @@ constexpr int kImpStages = 2;
 constexpr int kImpTiles = 8;   // tiles of a warp of the importance kernel
 
 // Importance: each warp takes kImpTiles tiles of 16 rows and every query row; the query fragments lie in
-// shared memory as the products want them.
+// shared memory as the products want them.  Rows of the fragments beyond the last query row repeat it and add 2^-inf.
 template <bool E2M1>
 __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const PagedAttnParams p)
 {
     constexpr int kSlot = Slot<E2M1, false>::kBytes;
     extern __shared__ __align__(128) float smem[];   // the warps' rings
     __shared__ uint4 sq[kMaxRows / 8][4][32];
-    __shared__ float srs[kMaxRows], sls[kMaxRows];
+    __shared__ float2 sf[kMaxRows];                  // factor of a row's logits, minus its lse (base 2)
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -958,20 +1071,19 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
     const int ntile = first < len ? min(kImpTiles, (len - first + kTileRows - 1) / kTileRows) : 0;   // with rows in them
     Feeder<E2M1, false> feeder(p, seq, h, 0, ntile);
     const uint32_t ring = smem_addr(smem) + warp * kImpStages * kSlot;
-#pragma unroll
-    for (int u = 0; u < kImpStages - 1; ++u) feeder.feed(ring + u * kSlot);
+    bool edge = feeder.feed(ring);
+    cp_async_commit();
     const int nq = (p.R + 7) / 8;
     for (int n = warp; n < nq; n += kImpWarps) {
-        const int r = 8 * n + g;
+        const int r = 8 * n + g, of = min(r, p.R - 1);
         uint32_t q[8][2];
-        const float f = load_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, q);
+        const float f = load_query<E2M1>(query_row(p, b, h, of), q);
 #pragma unroll
         for (int j = 0; j < 4; ++j) sq[n][j][lane] = make_uint4(q[2 * j][0], q[2 * j][1], q[2 * j + 1][0], q[2 * j + 1][1]);
         if (t == 0) {
-            srs[r] = p.qscale * f;
-            float z = -INFINITY;
-            if (r < p.R) z = p.lse[((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq];
-            sls[r] = z == -INFINITY ? INFINITY : z * 1.4426950408889634f;   // a row that saw nothing adds nothing
+            // a row that saw nothing (lse = -inf) adds nothing
+            const float z = p.lse[((int64_t)b * p.Hq + h * p.G + of / p.Mq) * p.Mq + of % p.Mq];
+            sf[r] = make_float2(p.qscale * f, r >= p.R || z == -INFINITY ? -INFINITY : z * -1.4426950408889634f);
         }
     }
     __syncthreads();
@@ -981,10 +1093,12 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
         if (base >= p.cand_hi) break;
         float sum[2] = {0.f, 0.f};
         if (u < ntile) {
-            const uint32_t slot = ring + (u % kImpStages) * kSlot;
-            cp_async_wait_stages<kImpStages - 1>();
+            const uint32_t slot = ring + (u & 1) * kSlot;
+            cp_async_wait_stages<1>();
             __syncwarp();
-            feeder.feed(ring + ((u + kImpStages - 1) % kImpStages) * kSlot);
+            const bool masked = edge;
+            edge = feeder.feed(ring + (~u & 1) * kSlot);
+            cp_async_commit();
             uint32_t a[8][4];
             k_steps<E2M1, false>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                 a[j][0] = a0;
@@ -992,7 +1106,11 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
                 a[j][2] = a2;
                 a[j][3] = a3;
             });
-            const int p0 = (int)lds32(slot + Slot<E2M1, false>::kPos + 4 * g), p1 = (int)lds32(slot + Slot<E2M1, false>::kPos + 32 + 4 * g);
+            int p0 = 0, p1 = 0;
+            if (masked) {
+                p0 = (int)lds32(slot + Slot<E2M1, false>::kPos + 4 * g);
+                p1 = (int)lds32(slot + Slot<E2M1, false>::kPos + 32 + 4 * g);
+            }
             for (int n = 0; n < nq; ++n) {
                 float s[2][4];
 #pragma unroll
@@ -1006,12 +1124,15 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
                         mma16<E2M1>(s[1], a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], q.z, q.w);
                     }
                 }
+                const float4 f = *reinterpret_cast<const float4*>(&sf[8 * n + 2 * t]);   // rows 2t, 2t + 1
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int r = 8 * n + 2 * t + (e & 1);
-                    const int row = e >> 1 ? p1 : p0;
-                    const bool see = row >= 0 && r < p.R && row <= seen + r % p.Mq && sls[r] != INFINITY;
-                    if (see) sum[e >> 1] += fast_exp2(fmaf(s[0][e] + s[1][e], srs[r], -sls[r]));
+                    float x = fmaf(s[0][e] + s[1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
+                    if (masked) {
+                        const int row = e >> 1 ? p1 : p0;
+                        if (row < 0 || row > seen + (8 * n + 2 * t + (e & 1)) % p.Mq) x = -INFINITY;
+                    }
+                    sum[e >> 1] += fast_exp2(x);
                 }
             }
         }
