@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -146,8 +147,8 @@ def load_library():
         lib.fx_shared_prefix_workspace_bytes.restype = c_size
         lib.fx_shared_prefix_decode.argtypes = [ctypes.POINTER(PrefixDesc), ctypes.POINTER(BranchDesc), c_vp, c_int,
                                                 c_vp, c_int, c_float, c_vp, c_vp, c_size, c_uint, c_vp]
-        paged = ctypes.POINTER(PagedDesc)
-        lib.fx_paged_append.argtypes = [paged, ctypes.POINTER(PagedRows), c_uint, c_vp]
+        paged = c_vp   # the address of a PagedDesc
+        lib.fx_paged_append.argtypes = [paged, ctypes.c_char_p, c_uint, c_vp]   # the bytes of a PagedRows
         lib.fx_paged_gather.argtypes = [paged, c_vp, c_vp, c_int, c_vp, c_vp, c_uint, c_vp]
         lib.fx_paged_decode_workspace_bytes.argtypes = [c_int] * 4
         lib.fx_paged_decode_workspace_bytes.restype = c_size
@@ -551,7 +552,7 @@ class PagedKV:
         if any(t is not None and t.device != k.device for t in (v, table, length, k_scale, v_scale)):
             raise FxError(FX_ERR_INVALID_ARG, "the cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale, self.table, self.length = k, v, k_scale, v_scale, table, length
-        self.device = k.device
+        self.device, self._index = k.device, k.get_device()
         self.n_pages, self.Hkv, self.page_rows, _ = k.shape
         self.B, self.max_pages = table.shape
         ks, ss = _strides(k), _strides(k_scale) if packed else (0, 0, 0, 0)
@@ -561,25 +562,60 @@ class PagedKV:
                                table.stride(0) if self.B > 1 else self.max_pages,
                                FX_PAGED_E2M1 if packed else FX_PAGED_BF16, self.B, self.Hkv, 128, self.page_rows,
                                self.n_pages, self.max_pages, int(k_exp), int(v_exp))
-        self._ref = ctypes.byref(self._desc)
+        self._ref = ctypes.addressof(self._desc)
+        self._rows = self.max_pages * self.page_rows
 
 
-def _paged_tensor(cache, t, name, dtype, shape, contiguous=True):
+# These calls run once or more per layer and token: their checks are written for few interpreter steps.
+_ROWS = struct.Struct("@PPqqPPqqqqPPPPiiiiixxxx")   # PagedRows
+assert _ROWS.size == ctypes.sizeof(PagedRows)
+
+
+def _paged_bad(cache, t, name, dtype, shape, contiguous):
     if not isinstance(t, torch.Tensor) or t.device != cache.device:
         raise FxError(FX_ERR_INVALID_ARG, f"{name} must be a tensor on {cache.device}")
     if t.dtype != dtype or t.shape != shape:
         raise FxError(FX_ERR_INVALID_ARG, f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if contiguous and not t.is_contiguous():
+    if contiguous:
         raise FxError(FX_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+def _paged_tensor(cache, t, name, dtype, shape):
+    """The address of a contiguous tensor of that type and shape on the cache's device; raises otherwise."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == cache._index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _paged_bad(cache, t, name, dtype, shape, True)
+
+
+def _paged_view(cache, t, name, shape):
+    """(address, strides) of a bf16 view with unit last stride."""
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == cache._index:
+            st = t.stride()
+            if st[-1] == 1:
+                for i in st:
+                    if i & 7 and i != 1:
+                        return t.data_ptr(), _strides(t)   # the library refuses what then still is no multiple of 8
+                return t.data_ptr(), st
+            raise FxError(FX_ERR_INVALID_ARG, f"{name} must have unit last stride")
+    except AttributeError:
+        pass
+    _paged_bad(cache, t, name, torch.bfloat16, shape, False)
+    raise FxError(FX_ERR_INVALID_ARG, f"{name} must be a bf16 view")
 
 
 def _paged_launch(cache, stream):
     """(library, stream handle) of a call on the cache, which must live on the current device."""
-    if not isinstance(cache, PagedKV):
+    if type(cache) is not PagedKV and not isinstance(cache, PagedKV):
         raise FxError(FX_ERR_INVALID_ARG, "cache must be a PagedKV")
-    if torch.cuda.current_device() != cache.device.index:
+    if torch.cuda.current_device() != cache._index:
         raise FxError(FX_ERR_INVALID_ARG, f"the cache is on {cache.device}, the current device is another one")
-    return load_library(), _stream(stream)
+    if stream is None:
+        return _lib or load_library(), torch.cuda.current_stream().cuda_stream
+    return _lib or load_library(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _on(cache, stream):
@@ -606,39 +642,36 @@ def fx_paged_append(cache, k_new, v_new, seq, pos, *, cos_sin=None, rope_pos=Non
     """
     lib, st = _paged_launch(cache, stream)
     n = seq.shape[0] if isinstance(seq, torch.Tensor) and seq.dim() == 1 else -1
-    _paged_tensor(cache, seq, "seq", torch.int32, (n,))
-    _paged_tensor(cache, pos, "pos", torch.int32, (n,))
-    _paged_tensor(cache, k_new, "k_new", torch.bfloat16, (n, cache.Hkv, 128), False)
-    _paged_tensor(cache, v_new, "v_new", torch.bfloat16, (n, cache.Hkv, 128), False)
-    sn, sh, sd = _strides(k_new)
-    if _strides(v_new) != (sn, sh, sd) or sd != 1:
-        raise FxError(FX_ERR_INVALID_ARG, "k_new and v_new must have equal strides, unit last stride")
-    rows = PagedRows(k_new.data_ptr(), v_new.data_ptr(), sn, sh)
+    seq_at = _paged_tensor(cache, seq, "seq", torch.int32, (n,))
+    pos_at = _paged_tensor(cache, pos, "pos", torch.int32, (n,))
+    k_at, ks = _paged_view(cache, k_new, "k_new", (n, cache.Hkv, 128))
+    v_at, vs = _paged_view(cache, v_new, "v_new", (n, cache.Hkv, 128))
+    if ks != vs:
+        ks = _strides(k_new)
+        if ks != _strides(v_new):
+            raise FxError(FX_ERR_INVALID_ARG, "k_new and v_new must have equal strides")
+    q_at = o_at = Hq = 0
+    qs = os_ = (0, 0, 1)
     if q is not None:
         Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-        _paged_tensor(cache, q, "q", torch.bfloat16, (n, Hq, 128), False)
+        q_at, qs = _paged_view(cache, q, "q", (n, Hq, 128))
         if q_out is None:
             q_out = _paged_alloc(cache, stream, (n, Hq, 128), torch.bfloat16)
-        _paged_tensor(cache, q_out, "q_out", torch.bfloat16, (n, Hq, 128), False)
-        a, b = _strides(q), _strides(q_out)
-        if a[2] != 1 or b[2] != 1:
-            raise FxError(FX_ERR_INVALID_ARG, "q and q_out must have unit last stride")
-        rows.q, rows.q_out, rows.Hq = q.data_ptr(), q_out.data_ptr(), Hq
-        rows.q_stride_n, rows.q_stride_h, rows.qo_stride_n, rows.qo_stride_h = a[0], a[1], b[0], b[1]
+        o_at, os_ = _paged_view(cache, q_out, "q_out", (n, Hq, 128))
     elif q_out is not None:
         raise FxError(FX_ERR_INVALID_ARG, "q_out needs q")
     if n == 0:
         return q_out
-    rows.seq, rows.pos, rows.n = seq.data_ptr(), pos.data_ptr(), n
-    if rope_pos is not None:
-        _paged_tensor(cache, rope_pos, "rope_pos", torch.int32, (n,))
-        rows.rope_pos = rope_pos.data_ptr()
+    rope_at = 0 if rope_pos is None else _paged_tensor(cache, rope_pos, "rope_pos", torch.int32, (n,))
+    cs_at = rot = n_pos = 0
     if cos_sin is not None:
         n_pos, rot = cos_sin.shape if isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2 else (-1, -1)
-        _paged_tensor(cache, cos_sin, "cos_sin", torch.float32, (n_pos, rot))
-        rows.cos_sin, rows.rot, rows.n_pos = cos_sin.data_ptr(), rot, n_pos
-    rows.interleaved = 1 if interleaved else 0
-    _check(lib.fx_paged_append(cache._ref, ctypes.byref(rows), int(flags), st))
+        cs_at = _paged_tensor(cache, cos_sin, "cos_sin", torch.float32, (n_pos, rot))
+    rows = _ROWS.pack(k_at, v_at, ks[0], ks[1], q_at, o_at, qs[0], qs[1], os_[0], os_[1], seq_at, pos_at, rope_at, cs_at,
+                      n, Hq, rot, n_pos, 1 if interleaved else 0)
+    rc = lib.fx_paged_append(cache._ref, rows, flags, st)
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -650,20 +683,17 @@ def fx_paged_gather(cache, n: int, *, idx=None, lo=None, k_out=None, v_out=None,
     lib, st = _paged_launch(cache, stream)
     n = int(n)
     shape = (cache.B, cache.Hkv, n, 128)
-    if idx is not None:
-        _paged_tensor(cache, idx, "idx", torch.int32, shape[:3])
-    if lo is not None:
-        _paged_tensor(cache, lo, "lo", torch.int32, (cache.B,))
+    idx_at = None if idx is None else _paged_tensor(cache, idx, "idx", torch.int32, shape[:3])
+    lo_at = None if lo is None else _paged_tensor(cache, lo, "lo", torch.int32, (cache.B,))
     if k_out is None:
         k_out = _paged_alloc(cache, stream, shape, torch.bfloat16)
     if v_out is None:
         v_out = _paged_alloc(cache, stream, shape, torch.bfloat16)
-    _paged_tensor(cache, k_out, "k_out", torch.bfloat16, shape)
-    _paged_tensor(cache, v_out, "v_out", torch.bfloat16, shape)
-    if n == 0:
-        return k_out, v_out
-    _check(lib.fx_paged_gather(cache._ref, None if idx is None else idx.data_ptr(), None if lo is None else lo.data_ptr(),
-                               n, k_out.data_ptr(), v_out.data_ptr(), int(flags), st))
+    k_at = _paged_tensor(cache, k_out, "k_out", torch.bfloat16, shape)
+    v_at = _paged_tensor(cache, v_out, "v_out", torch.bfloat16, shape)
+    rc = lib.fx_paged_gather(cache._ref, idx_at, lo_at, n, k_at, v_at, flags, st) if n else 0
+    if rc:
+        _check(rc)
     return k_out, v_out
 
 
@@ -674,29 +704,28 @@ def fx_paged_decode_workspace_bytes(B, Hkv, Hq, Mq) -> int:
 _stream_ws = {}
 
 
-def _paged_workspace(cache, ws, nbytes, stream, handle):
-    """The call's workspace: the caller's, or one of this device and stream (two streams never share one).  A call
-    that is being captured gets one of its own, from the graph's memory."""
-    if ws is not None:
-        return ws.ensure(nbytes, stream)
+def _paged_workspace(cache, nbytes, stream, handle):
+    """The workspace of a call without one of its caller's: one for each device and stream (two streams never share
+    one).  A call that is being captured gets one of its own, from the graph's memory."""
     if torch.cuda.is_current_stream_capturing():
         ws = Workspace(cache.device)
     else:
-        key = (cache.device.index, handle.value or 0)
-        ws = _stream_ws.get(key)
+        ws = _stream_ws.get((cache._index, handle))
         if ws is None:
-            ws = _stream_ws[key] = Workspace(cache.device)
+            ws = _stream_ws[(cache._index, handle)] = Workspace(cache.device)
     with _on(cache, stream):
         return ws.ensure(nbytes, stream)
 
 
 def _paged_queries(cache, q):
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.device != cache.device or q.dtype != torch.bfloat16:
-        raise FxError(FX_ERR_INVALID_ARG, f"q must be a bf16 [B, Hq, Mq, 128] tensor on {cache.device}")
-    B, Hq, Mq, d = q.shape
-    if B != cache.B or d != 128 or q.stride(3) != 1:
-        raise FxError(FX_ERR_INVALID_ARG, f"q must be [{cache.B}, Hq, Mq, 128] with unit last stride")
-    return Hq, Mq
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise FxError(FX_ERR_INVALID_ARG, f"q must be a bf16 [{cache.B}, Hq, Mq, 128] tensor on {cache.device}")
+    _, Hq, Mq, _ = q.shape
+    at, st = _paged_view(cache, q, "q", (cache.B, Hq, Mq, 128))
+    return at, st, Hq, Mq
+
+
+_SCALE = _default_scale(128)
 
 
 def fx_paged_decode(cache, q, idx=None, tail_lo=None, *, scale=None, out=None, lse=None, want_lse=False, ws=None,
@@ -707,27 +736,25 @@ def fx_paged_decode(cache, q, idx=None, tail_lo=None, *, scale=None, out=None, l
     [B, Hq, Mq, 128] fp32, or (out, lse [B, Hq, Mq]) when lse is given or wanted.
     """
     lib, st = _paged_launch(cache, stream)
-    Hq, Mq = _paged_queries(cache, q)
-    kk = 0
+    q_at, qs, Hq, Mq = _paged_queries(cache, q)
+    B = cache.B
+    kk, idx_at = 0, None
     if idx is not None:
         kk = idx.shape[-1] if isinstance(idx, torch.Tensor) and idx.dim() == 3 else -1
-        _paged_tensor(cache, idx, "idx", torch.int32, (cache.B, cache.Hkv, kk))
-    if tail_lo is not None:
-        _paged_tensor(cache, tail_lo, "tail_lo", torch.int32, (cache.B,))
-    shape = (cache.B, Hq, Mq)
+        idx_at = _paged_tensor(cache, idx, "idx", torch.int32, (B, cache.Hkv, kk)) or None
+    lo_at = None if tail_lo is None else _paged_tensor(cache, tail_lo, "tail_lo", torch.int32, (B,))
     if out is None:
-        out = _paged_alloc(cache, stream, shape + (128,), torch.float32)
-    _paged_tensor(cache, out, "out", torch.float32, shape + (128,))
+        out = _paged_alloc(cache, stream, (B, Hq, Mq, 128), torch.float32)
+    out_at = _paged_tensor(cache, out, "out", torch.float32, (B, Hq, Mq, 128))
     if lse is None and want_lse:
-        lse = _paged_alloc(cache, stream, shape, torch.float32)
-    if lse is not None:
-        _paged_tensor(cache, lse, "lse", torch.float32, shape)
-    buf = _paged_workspace(cache, ws, lib.fx_paged_decode_workspace_bytes(cache.B, cache.Hkv, Hq, Mq), stream, st)
-    sb, sh, si, _ = _strides(q)
-    sc = _default_scale(128) if scale is None else float(scale)
-    _check(lib.fx_paged_decode(cache._ref, q.data_ptr(), sb, sh, si, Hq, Mq, idx.data_ptr() if kk else None, kk,
-                               None if tail_lo is None else tail_lo.data_ptr(), sc, out.data_ptr(),
-                               None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), int(flags), st))
+        lse = _paged_alloc(cache, stream, (B, Hq, Mq), torch.float32)
+    lse_at = None if lse is None else _paged_tensor(cache, lse, "lse", torch.float32, (B, Hq, Mq))
+    nbytes = lib.fx_paged_decode_workspace_bytes(B, cache.Hkv, Hq, Mq)
+    buf = _paged_workspace(cache, nbytes, stream, st) if ws is None else ws.ensure(nbytes, stream)
+    rc = lib.fx_paged_decode(cache._ref, q_at, qs[0], qs[1], qs[2], Hq, Mq, idx_at, kk, lo_at,
+                             _SCALE if scale is None else scale, out_at, lse_at, buf.data_ptr(), buf.numel(), flags, st)
+    if rc:
+        _check(rc)
     return out if lse is None else (out, lse)
 
 
@@ -735,23 +762,21 @@ def fx_paged_importance(cache, q, lse, *, scale=None, cand=None, scores=None, st
     """Importance of the rows cand = (lo, hi) of a paged cache (default: the whole capacity, or the width of scores
     when given): fp32 [B, Hkv, hi - lo], from the queries and the lse [B, Hq, Mq] of fx_paged_decode."""
     lib, st = _paged_launch(cache, stream)
-    Hq, Mq = _paged_queries(cache, q)
-    _paged_tensor(cache, lse, "lse", torch.float32, (cache.B, Hq, Mq))
+    q_at, qs, Hq, Mq = _paged_queries(cache, q)
+    lse_at = _paged_tensor(cache, lse, "lse", torch.float32, (cache.B, Hq, Mq))
     if cand is not None:
         lo, hi = int(cand[0]), int(cand[1])
     else:
-        lo, hi = 0, cache.max_pages * cache.page_rows
+        lo, hi = 0, cache._rows
         if isinstance(scores, torch.Tensor) and scores.dim() == 3:
             hi = scores.shape[2]
     if scores is None:
         scores = _paged_alloc(cache, stream, (cache.B, cache.Hkv, max(hi - lo, 0)), torch.float32)
-    _paged_tensor(cache, scores, "scores", torch.float32, (cache.B, cache.Hkv, hi - lo))
-    if hi == lo:
-        return scores
-    sb, sh, si, _ = _strides(q)
-    sc = _default_scale(128) if scale is None else float(scale)
-    _check(lib.fx_paged_importance(cache._ref, q.data_ptr(), sb, sh, si, Hq, Mq, lse.data_ptr(), sc, lo, hi,
-                                   scores.data_ptr(), int(flags), st))
+    s_at = _paged_tensor(cache, scores, "scores", torch.float32, (cache.B, cache.Hkv, hi - lo))
+    rc = 0 if hi == lo else lib.fx_paged_importance(cache._ref, q_at, qs[0], qs[1], qs[2], Hq, Mq, lse_at,
+                                                    _SCALE if scale is None else scale, lo, hi, s_at, flags, st)
+    if rc:
+        _check(rc)
     return scores
 
 

@@ -19,6 +19,18 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& r0, uint32_t
         : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
         : "r"(w));
 }
+// Byte k (a constant) of a word of codes to a pair of f16 values.
+__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t w, int k)
+{
+    uint32_t r;
+    switch (k) {
+    case 0: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w)); break;
+    case 1: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w)); break;
+    case 2: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w)); break;
+    default: asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w)); break;
+    }
+    return r;
+}
 // Two e4m3 bytes to two f16 values, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
 {

@@ -17,8 +17,9 @@
 // it is set so that the largest logit so far gives 2^kBase and moves only when a p would exceed 2^kTop, so most
 // tiles take one vote instead of a reduction; f16 holds such a p to 2^-36 of the row's largest.  Sums are fp32.
 #include <cuda_bf16.h>
-#include <float.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "attn_ptx.cuh"
 #include "paged.cuh"
@@ -27,7 +28,9 @@ namespace fx {
 namespace {
 
 constexpr int kTileRows = 16;
-constexpr int kMinTiles = 2;   // tiles a warp gets at least, before more CTAs share a call
+constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call
+constexpr int kMaxParts = 64;   // CTAs that share one (sequence, KV head, row group) on average, at most: the last
+                                // of them joins all their parts
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -158,17 +161,15 @@ template <bool E2M1, bool WITH_V>
 struct Feeder {
     const PagedAttnParams& p;
     const Seq& q;
-    const char* k0;   // the lane's places relative to row 0 of page 0: K and V codes or rows, scales
-    const char* v0;
-    const char* s0;
+    const char* k0;   // the lane's places relative to row 0 of page 0: K codes or rows, scales (V lies c.v - c.k
+    const char* s0;   // further on: its strides are K's)
     uint32_t to;      // the lane's place in a slot (codes or rows)
     int it, end;
     // tail
     int pos;          // first row of the next tail tile
     int pages, page_base;
-    bool fresh, ok;   // no address yet; the page is good
+    bool ok;          // the page is good
     const char* ka;
-    const char* va;
     const char* sa;
     // list
     int id, at;       // the lane's pool row (-1: not valid) and position in the current two tiles
@@ -184,7 +185,6 @@ struct Feeder {
         const int lane = threadIdx.x & 31;
         const int chunk = E2M1 ? lane & 3 : lane & 15, row = E2M1 ? lane >> 2 : lane >> 4;
         k0 = c.k + (int64_t)h * c.sh + 16 * chunk;
-        v0 = c.v + (int64_t)h * c.sh + 16 * chunk;
         s0 = (lane < 16 ? c.ks : c.vs) + (int64_t)h * c.ssh;
         to = E2M1 ? (row >> 1) * 128 + ((((row & 1) * 4 + chunk) ^ (2 * ((row >> 1) & 3))) << 4)
                   : row * 256 + ((chunk ^ row) << 4);
@@ -198,9 +198,13 @@ struct Feeder {
             id = place(at, page);
         }
         pos = (q.lo & ~(kTileRows - 1)) + (max(it, q.nl) - q.nl) * kTileRows;
-        fresh = true;
         ok = false;
-        if (end > q.nl) load_pages();
+        ka = k0;
+        sa = s0;
+        if (end > q.nl) {
+            load_pages();
+            enter_page();
+        }
     }
 
     __device__ __forceinline__ int list_pos(int e) const { return e < min(p.kk, end * kTileRows) ? q.idx[e] : -1; }
@@ -228,6 +232,19 @@ struct Feeder {
         pages = first < q.len ? q.table[page_base + (threadIdx.x & 31)] : -1;
     }
 
+    __device__ __forceinline__ void enter_page()
+    {
+        const PagedCache& c = p.c;
+        const int lane = threadIdx.x & 31;
+        if ((pos >> c.page_shift) - page_base >= 32) load_pages();
+        const int page = __shfl_sync(kFull, pages, (pos >> c.page_shift) - page_base);
+        ok = (unsigned)page < (unsigned)c.n_pages;
+        if (!ok && pos < q.len) atomicOr(p.err, FX_DEVERR_PAGE);
+        const int64_t pg = ok ? page : 0, row = pos & c.page_mask;
+        ka = k0 + pg * c.sp + (row + (E2M1 ? lane >> 2 : lane >> 4)) * c.st;
+        if (E2M1) sa = s0 + pg * c.ssp + (row + (lane & 15)) * c.sst;
+    }
+
     // Feeds the next tile (none past the end: a slot without valid rows).  True when a row of it is not valid or
     // not seen by every query; only then the rows' positions are in the slot.
     __device__ __forceinline__ bool feed(uint32_t slot)
@@ -252,18 +269,7 @@ struct Feeder {
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31, j = lane & 15;
-        if (fresh || (pos & c.page_mask) == 0) {
-            fresh = false;
-            if ((pos >> c.page_shift) - page_base >= 32) load_pages();
-            const int page = __shfl_sync(kFull, pages, (pos >> c.page_shift) - page_base);
-            ok = (unsigned)page < (unsigned)c.n_pages;
-            if (!ok && pos < q.len) atomicOr(p.err, FX_DEVERR_PAGE);
-            const int64_t pg = ok ? page : 0, row = pos & c.page_mask;
-            const int64_t o = pg * c.sp + (row + (E2M1 ? lane >> 2 : lane >> 4)) * c.st;
-            ka = k0 + o;
-            va = v0 + o;
-            if (E2M1) sa = s0 + pg * c.ssp + (row + j) * c.sst;
-        }
+        const char* va = ka + (c.v - c.k);
         const bool edge = !ok || pos < q.lo || pos + kTileRows > clear;
         if (edge) {
             const int t = pos + j;
@@ -298,8 +304,8 @@ struct Feeder {
             }
         }
         ka += 16 * c.st;
-        va += 16 * c.st;
         pos += kTileRows;
+        if ((pos & c.page_mask) == 0 && it + 1 < end) enter_page();
         return edge;
     }
 
@@ -318,7 +324,7 @@ struct Feeder {
             const int64_t o = row_offset(c, max(__shfl_sync(kFull, id, half + row), 0), c.sp, c.st);
             const uint32_t dst = E2M1 ? slot + to + 512 * u : slot + u * 512 + (to ^ ((2 * u & 6) << 4));
             cp_async16(dst, k0 + o);
-            if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, v0 + o);
+            if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, k0 + (c.v - c.k) + o);
         }
         if (E2M1 && (WITH_V || lane < 16))
             cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, s0 + row_offset(c, max(mine, 0), c.ssp, c.sst));
@@ -380,7 +386,6 @@ template <>
 struct VTile<true> {
     uint32_t code[2][4];   // [dimensions 16g .. + 7, + 8 .. + 15][rows 2t, 2t + 1: even, odd dimensions; 2t + 8, + 9]
     uint32_t s01, s23;     // scales of rows 2t, 2t + 1 and 2t + 8, 2t + 9
-    uint32_t f[4][4];      // the four M tiles in use
 
     template <bool MASKED>
     __device__ __forceinline__ void load(uint32_t slot, uint32_t vm)
@@ -411,12 +416,8 @@ struct VTile<true> {
     template <bool MASKED>
     __device__ __forceinline__ void get(int i, uint32_t (&x)[4])
     {
-        if ((i & 3) == 0) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) e2m1x8_to_f16(code[i >> 2][u], f[u][0], f[u][1], f[u][2], f[u][3]);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = hmul2_u32(f[u][i & 3], u < 2 ? s01 : s23);
+        for (int u = 0; u < 4; ++u) x[u] = hmul2_u32(e2m1x2_to_f16(code[i >> 2][u], i & 3), u < 2 ? s01 : s23);
     }
 };
 template <>
@@ -454,54 +455,47 @@ __device__ __forceinline__ int v_dim(int i, int g, int half)
     return E2M1 ? 16 * g + 2 * i + half : 16 * i + g + 8 * half;
 }
 
-// The lane's 32 query values of row g (B fragments of the eight steps), and the factor of the row's logits.
-// src: the row, or nullptr for a row that does not exist.  All 32 lanes call it.
+// The lane's 32 query values of row g as they lie in memory, in the order of the eight steps' B fragments.
+// src: the row, or nullptr for a row that does not exist.
 template <bool E2M1>
-__device__ __forceinline__ float load_query(const uint16_t* src, uint32_t q[8][2])
+__device__ __forceinline__ void fetch_query(const uint16_t* src, uint32_t (&w)[16])
 {
     const int t = threadIdx.x & 3;
-    uint32_t w[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = 0;
     if (src) {
         if (E2M1) {   // step j: dimensions 32t + 4j .. + 3, as a lane's 16 bytes of codes have them
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 x = *reinterpret_cast<const uint4*>(src + 32 * t + 8 * j);
-                w[4 * j] = x.x;
-                w[4 * j + 1] = x.y;
-                w[4 * j + 2] = x.z;
-                w[4 * j + 3] = x.w;
-            }
+            for (int j = 0; j < 4; ++j)
+                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[4 * j]), "=r"(w[4 * j + 1]), "=r"(w[4 * j + 2]), "=r"(w[4 * j + 3])
+                             : "l"(src + 32 * t + 8 * j));
         } else {      // step j: dimensions 16j + 2t, + 1 and 16j + 8 + 2t, + 1
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + 8 * j + 2 * t);
+            for (int j = 0; j < 16; ++j) asm volatile("ld.global.u32 %0, [%1];" : "=r"(w[j]) : "l"(src + 8 * j + 2 * t));
         }
     }
-    float factor = 1.f;
-    if (E2M1) {
-        uint32_t top = 0;
+}
+// Turns them into the B fragments; returns the factor of the row's logits.  All 32 lanes call it.
+template <bool E2M1>
+__device__ __forceinline__ float make_query(uint32_t (&w)[16])
+{
+    if (!E2M1) return 1.f;
+    uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = max(top, max((w[j] & 0x7fffu) << 16, w[j] & 0x7fff0000u));
-        top = max(top, __shfl_xor_sync(kFull, top, 1));
-        top = max(top, __shfl_xor_sync(kFull, top, 2));
-        // 2^(14 - exponent of the largest); tiny rows (below 2^-100) are scaled as if they were that large
-        const int ex = min(max((int)(top >> 23) - 127, -100), 127);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-        factor = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-        const bool finite = top < 0x7f800000u;
+    for (int j = 0; j < 16; ++j) top = max(top, max((w[j] & 0x7fffu) << 16, w[j] & 0x7fff0000u));
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    // 2^(14 - exponent of the largest); tiny rows (below 2^-100) are scaled as if they were that large
+    const int ex = min(max((int)(top >> 23) - 127, -100), 127);
+    const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+    const bool finite = top < 0x7f800000u;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const __half2 v = __floats2half2_rn(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
-            w[j] = finite ? *reinterpret_cast<const uint32_t*>(&v) : 0x7fff7fffu;   // else the row is NaN
-        }
+    for (int j = 0; j < 16; ++j) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+        w[j] = finite ? *reinterpret_cast<const uint32_t*>(&v) : 0x7fff7fffu;   // else the row is NaN
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        q[j][0] = w[2 * j];
-        q[j][1] = w[2 * j + 1];
-    }
-    return factor;
+    return __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
 }
 
 __device__ __forceinline__ const uint16_t* query_row(const PagedAttnParams& p, int b, int h, int r)
@@ -547,7 +541,7 @@ __device__ __forceinline__ float join_row(const float* sm_o, int pitch, const fl
 // The query rows of one warp and what it has summed for them.
 template <bool E2M1, int NT, bool DUP>
 struct Acc {
-    uint32_t q[NT][8][2];
+    uint32_t q[NT][16];   // B fragments: registers 2j, 2j + 1 of step j
     float rs[NT][2];      // factor of the logits of rows 2t, 2t+1 (of each N tile)
     float bias[NT][2];    // minus the reference of those rows; +inf: none yet
     float l[NT][2];
@@ -629,9 +623,9 @@ __device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slo
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (j < 2)
-                mma16_zero<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+                mma16_zero<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][2 * j], a.q[n][2 * j + 1]);
             else
-                mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][j][0], a.q[n][j][1]);
+                mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][2 * j], a.q[n][2 * j + 1]);
         }
     });
 #pragma unroll
@@ -788,7 +782,7 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
 template <bool E2M1, int NT, bool DUP>
 struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = E2M1 && NT == 2 ? 12 : 8;
     static constexpr int kCtas = E2M1 && NT == 1 ? 2 : 1;   // per SM
     static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
     static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
@@ -816,7 +810,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     float* const sm_o = smem;
     __shared__ float sm_m[W * kRows], sm_l[W * kRows];
     __shared__ long long sm_scan[W];
-    __shared__ int sm_b;
+    __shared__ int sm_b, sm_len, sm_lo;
     __shared__ long long sm_start;
     __shared__ unsigned sm_last;
 
@@ -827,52 +821,69 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     const int nrg = (p.R + kRows - 1) / kRows;
     const int per_tile = p.c.Hkv * nrg;   // pieces of one sequence
 
-    // total length of the line, then this CTA's stretch of it and the sequence that it starts in
-    long long total = 0;
-    for (int b = tid; b < p.c.B; b += kThreadsA) total += tile_count(sequence(p, b, blockIdx.x == 0));
+    // The line: its length, this CTA's stretch of it, the sequence that the stretch starts in.  Up to as many
+    // sequences as threads take one scan, more take one pass for the length and a scan of blocks of them.
+    Seq seq = sequence(p, min(tid, p.c.B - 1), blockIdx.x == 0 && tid < p.c.B);
+    const bool one_scan = p.c.B <= kThreadsA;
+    long long total = tid < p.c.B ? tile_count(seq) : 0;
+    const int n_first = (int)total;
+    if (!one_scan) {
+        for (int b = tid + kThreadsA; b < p.c.B; b += kThreadsA) total += tile_count(sequence(p, b, blockIdx.x == 0));
 #pragma unroll
-    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-    if (lane == 0) sm_scan[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < W; ++w) total += sm_scan[w];
-    total *= per_tile;
-    const int n_cta = (int)min((long long)gridDim.x, max(1ll, total / (W * kMinTiles)));
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+        if (lane == 0) sm_scan[warp] = total;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < W; ++w) total += sm_scan[w];
+        total *= per_tile;
+        __syncthreads();
+    }
     const int cta = blockIdx.x;
-    if (cta >= n_cta) return;
-    long long at = total * cta / n_cta;                  // next tile of the line
-    const long long end = total * (cta + 1) / n_cta;
-    long long before = 0;                                // tiles (of one piece each) of the sequences before b
+    int n_cta = 0;
+    long long at = 0, end = 0;     // next tile of the line, end of the stretch
+    long long before = 0;          // tiles (of one piece each) of the sequences before this block of them
     for (int b0 = 0;; b0 += kThreadsA) {
         const int b = b0 + tid;
-        const int n = b < p.c.B ? tile_count(sequence(p, b, false)) : 0;
+        if (b0 > 0 && b < p.c.B) seq = sequence(p, b, false);
+        const int n = b0 == 0 ? n_first : (b < p.c.B ? tile_count(seq) : 0);
         long long inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long o = __shfl_up_sync(kFull, inc, d);
             if (lane >= d) inc += o;
         }
-        __syncthreads();   // sm_scan is free
-        if (tid == 0) sm_b = -1;
         if (lane == 31) sm_scan[warp] = inc;
+        if (tid == 0) sm_b = -1;
         __syncthreads();
         long long sum = 0, mine = 0;
         for (int w = 0; w < W; ++w) {
             if (w == warp) mine = sum;
             sum += sm_scan[w];
         }
+        if (b0 == 0) {
+            if (one_scan) total = sum * per_tile;
+            n_cta = (int)min(min((long long)gridDim.x, (long long)kMaxParts * p.c.B * per_tile), max(1ll, total / (W * kMinTiles)));
+            if (cta >= n_cta) return;
+            at = total * cta / n_cta;
+            end = total * (cta + 1) / n_cta;
+        }
         const long long first = (before + mine + inc - n) * per_tile;
         if (n > 0 && at >= first && at < first + (long long)n * per_tile) {
             sm_b = b;
             sm_start = first;
+            sm_len = seq.len;
+            sm_lo = seq.lo;
         }
         __syncthreads();
         before += sum;
         if (sm_b >= 0) break;   // always found: at < total
+        __syncthreads();        // all have seen it; the next block may write
     }
     int b = sm_b;
     long long seq_start = sm_start;
-    Seq seq = sequence(p, b, false);
+    seq.len = sm_len;
+    seq.lo = sm_lo;
+    seq.table = p.c.table + (int64_t)b * p.c.table_stride;
     int ntile = tile_count(seq);
 
     for (bool head = true; at < end; head = false) {
@@ -888,6 +899,13 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
+        // the queries, the pages and the first rows are under way together
+        Acc<E2M1, NT, DUP> a;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = r0 + 8 * n + (DUP ? g & 3 : g);
+            fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[n]);
+        }
         // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on);
         // the ring's first units go on their way, then each turn feeds the unit kStages - 1 turns ahead
         const int mine = s1 - s0;
@@ -903,11 +921,9 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) feed(ring + k * U * kSlot);
 
-        Acc<E2M1, NT, DUP> a;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = r0 + 8 * n + (DUP ? g & 3 : g);
-            const float f = load_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[n]);
+            const float f = make_query<E2M1>(a.q[n]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 a.rs[n][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
@@ -926,7 +942,9 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             __syncwarp();
             feed(into);
             const uint32_t edge = (edges >> ((kStages - 1) * U)) & ((1u << U) - 1);
-            if (edge != 0) {
+            if (U > 1 && it + 1 == stop && (edge >> (U - 1)) == 0) {
+                attend<E2M1, NT, DUP, 1>(a, slot);   // the last one alone
+            } else if (edge != 0) {
 #pragma unroll 1
                 for (int u = 0; u < U; ++u)
                     attend_edge<E2M1, NT, DUP>(p, a, slot + u * kSlot, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
@@ -986,9 +1004,9 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
             const int c0 = (int)(((piece_start + 1) * n_cta - 1) / total);
             const int c1 = (int)(((piece_start + ntile) * n_cta - 1) / total);
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
+                __threadfence();   // the CTA's part, which the barrier orders before this fence
                 sm_last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
                 if (sm_last) {
                     p.counters[c0] = 0;   // ready for the next call
@@ -996,41 +1014,74 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 }
             }
             __syncthreads();
-            if (!sm_last) {
-                at = piece_start + s1;
-                continue;
-            }
-            // each warp takes every W-th part, then the warps' sums meet as before.  A CTA's first piece is in
-            // its slot 0; this piece is c0's first only if it starts c0's stretch
-            const int s_first = c0 * 2 + (total * c0 / n_cta == piece_start ? 0 : 1);
-            for (int row = 0; row < kRows; ++row) {
-                float m = -INFINITY;
-                for (int c = c0 + warp + W * lane; c <= c1; c += W * 32)
-                    m = fmaxf(m, __ldcg(p.part + (size_t)(c == c0 ? s_first : c * 2) * kPart + kRows * kHeadDim + row));
+            if (sm_last) {
+                // A CTA's first piece is in its slot 0; this piece is c0's first only if it starts c0's stretch.
+                // All references and sums come to shared memory in one go, then kSplit warps take each row.
+                const int n = c1 - c0 + 1, s_first = c0 * 2 + (total * c0 / n_cta == piece_start ? 0 : 1);
+                float* sm_pm = smem;
+                float* sm_pl = smem + n * kRows;
+                for (int i = tid; i < n * kRows; i += kThreadsA) {
+                    const int c = i / kRows;
+                    const float* from = p.part + (size_t)(c == 0 ? s_first : (c0 + c) * 2) * kPart + kRows * kHeadDim + i % kRows;
+                    sm_pm[i] = __ldcg(from);
+                    sm_pl[i] = __ldcg(from + kRows);
+                }
+                __syncthreads();
+                constexpr int kSplit = W / kRows > 0 ? W / kRows : 1;
+                float4* sm_acc = reinterpret_cast<float4*>(smem + ((2 * n * kRows + 3) & ~3));   // [row][32]
+                for (int row0 = 0; row0 < kRows; row0 += W / kSplit) {
+                    const int row = row0 + warp / kSplit, part0 = warp % kSplit;
+                    const bool live = row < kRows && r0 + row < p.R;
+                    float m = -INFINITY, z = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (live) {
+                        for (int c = lane; c < n; c += 32) m = fmaxf(m, sm_pm[c * kRows + row]);
 #pragma unroll
-                for (int d2 = 16; d2; d2 >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d2));
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float z = 0.f;
-#pragma unroll 4
-                for (int c = c0 + warp; c <= c1; c += W) {
-                    const float* from = p.part + (size_t)(c == c0 ? s_first : c * 2) * kPart;
-                    const float mc = __ldcg(from + kRows * kHeadDim + row);
-                    const float lc = __ldcg(from + kRows * kHeadDim + kRows + row);
-                    const float4 oc = __ldcg(reinterpret_cast<const float4*>(from + row * kHeadDim) + lane);
-                    const float f = mc == -INFINITY ? 0.f : fast_exp2(mc - m);
-                    z += f * lc;
-                    acc.x += f * oc.x;
-                    acc.y += f * oc.y;
-                    acc.z += f * oc.z;
-                    acc.w += f * oc.w;
-                }
-                *(reinterpret_cast<float4*>(sm_o + warp * kPitch + row * kHeadDim) + lane) = acc;
-                if (lane == 0) {
-                    sm_m[warp * kRows + row] = m;
-                    sm_l[warp * kRows + row] = z;
+                        for (int d2 = 16; d2; d2 >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d2));
+                        for (int c = lane; c < n; c += 32) {
+                            const float mc = sm_pm[c * kRows + row];
+                            if (mc != -INFINITY) z += fast_exp2(mc - m) * sm_pl[c * kRows + row];
+                        }
+#pragma unroll
+                        for (int d2 = 16; d2; d2 >>= 1) z += __shfl_xor_sync(kFull, z, d2);
+#pragma unroll 8
+                        for (int c = part0; c < n; c += kSplit) {
+                            const float* from = p.part + (size_t)(c == 0 ? s_first : (c0 + c) * 2) * kPart + row * kHeadDim;
+                            const float4 o = __ldcg(reinterpret_cast<const float4*>(from) + lane);
+                            const float mc = sm_pm[c * kRows + row];
+                            const float f = mc == -INFINITY ? 0.f : fast_exp2(mc - m);
+                            acc.x += f * o.x;
+                            acc.y += f * o.y;
+                            acc.z += f * o.z;
+                            acc.w += f * o.w;
+                        }
+                    }
+                    if (kSplit > 1) {   // (kSplit is 1 or 2)
+                        if (live && part0 == 1) sm_acc[row * 32 + lane] = acc;
+                        __syncthreads();
+                        if (live && part0 == 0) {
+                            const float4 o = sm_acc[row * 32 + lane];
+                            acc.x += o.x;
+                            acc.y += o.y;
+                            acc.z += o.z;
+                            acc.w += o.w;
+                        }
+                    }
+                    if (live && part0 == 0) {
+                        const int r = r0 + row;
+                        const int64_t to = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
+                        const bool none = m == -INFINITY;
+                        const float f = p.c.v_mul;
+                        reinterpret_cast<float4*>(p.out + to * kHeadDim)[lane] =
+                            none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                 : make_float4(acc.x / z * f, acc.y / z * f, acc.z / z * f, acc.w / z * f);
+                        if (p.lse && lane == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
+                    }
                 }
             }
-            __syncthreads();
+            __syncthreads();   // shared memory is free for the next piece
+            at = piece_start + s1;
+            continue;
         }
         const int d = tid & (kHeadDim - 1);
         for (int row = tid / kHeadDim; row < kRows && r0 + row < p.R; row += kThreadsA / kHeadDim) {
@@ -1076,10 +1127,11 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
     const int nq = (p.R + 7) / 8;
     for (int n = warp; n < nq; n += kImpWarps) {
         const int r = 8 * n + g, of = min(r, p.R - 1);
-        uint32_t q[8][2];
-        const float f = load_query<E2M1>(query_row(p, b, h, of), q);
+        uint32_t q[16];
+        fetch_query<E2M1>(query_row(p, b, h, of), q);
+        const float f = make_query<E2M1>(q);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sq[n][j][lane] = make_uint4(q[2 * j][0], q[2 * j][1], q[2 * j + 1][0], q[2 * j + 1][1]);
+        for (int j = 0; j < 4; ++j) sq[n][j][lane] = make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
         if (t == 0) {
             // a row that saw nothing (lse = -inf) adds nothing
             const float z = p.lse[((int64_t)b * p.Hq + h * p.G + of / p.Mq) * p.Mq + of % p.Mq];
@@ -1147,12 +1199,26 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
     cp_async_wait_all_groups();
 }
 
+// Raises a kernel's dynamic shared memory limit, once a device (a runtime call of about a microsecond).
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <bool E2M1, int NT, bool DUP>
 cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     using S = Shape<E2M1, NT, DUP>;
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<E2M1, NT, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)S::kSmem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(paged_decode_kernel<E2M1, NT, DUP>, S::kSmem, done);
     if (e != cudaSuccess) return e;
     return launch_kernel(paged_decode_kernel<E2M1, NT, DUP>, dim3(S::kCtas * sm_count), dim3(32 * S::kWarps), S::kSmem, s,
                          pdl, 0u, p);
@@ -1162,7 +1228,8 @@ template <bool E2M1>
 cudaError_t launch_importance(const PagedAttnParams& p, bool pdl, cudaStream_t s)
 {
     constexpr size_t smem = (size_t)kImpWarps * kImpStages * Slot<E2M1, false>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(paged_importance_kernel<E2M1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(paged_importance_kernel<E2M1>, smem, done);
     if (e != cudaSuccess) return e;
     const int rows = p.cand_hi - (p.cand_lo & ~(kTileRows - 1));
     const int per = kImpWarps * kImpTiles * kTileRows;

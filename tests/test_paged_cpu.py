@@ -47,7 +47,7 @@ def test_every_call_refuses_a_bad_cache(lib, change, status, word):
     d = ctypes.byref(desc(**change))
     rows = PagedRows(256, 256, 512, 128)
     rows.seq, rows.pos, rows.n = 256, 256, 1
-    for call in (lambda: lib.fx_paged_append(d, ctypes.byref(rows), 0, None),
+    for call in (lambda: lib.fx_paged_append(d, bytes(rows), 0, None),
                  lambda: lib.fx_paged_gather(d, None, None, 1, 256, 256, 0, None),
                  lambda: lib.fx_paged_decode(d, 256, 0, 0, 0, 4, 1, None, 0, None, 1.0, 256, None, None, 0, 0, None),
                  lambda: lib.fx_paged_importance(d, 256, 0, 0, 0, 4, 1, 256, 1.0, 0, 1, 256, 0, None)):
@@ -62,7 +62,7 @@ def test_append_refusals(lib):
         r = PagedRows(256, 512, 512, 128, 1024, 2048, 512, 128, 512, 128, 256, 256, None, 256, 3, 4, 128, 9, 0)
         for k, v in kw.items():
             setattr(r, k, v)
-        return lib.fx_paged_append(ctypes.byref(cache or desc()), ctypes.byref(r), flags, None)
+        return lib.fx_paged_append(ctypes.byref(cache or desc()), bytes(r), flags, None)
     assert lib.fx_paged_append(None, None, 0, None) == 1
     assert lib.fx_paged_append(ctypes.byref(desc()), None, 0, None) == 1 and b"rows" in lib.fx_last_error()
     for kw, status, word in ((dict(n=-1), 1, b"n must"), (dict(k=None), 1, b"non-NULL"), (dict(seq=None), 1, b"non-NULL"),
