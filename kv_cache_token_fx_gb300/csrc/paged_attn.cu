@@ -31,6 +31,8 @@ constexpr int kTileRows = 16;
 constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call
 constexpr int kMaxParts = 64;   // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
+constexpr int kSecondPiece = 96;   // a CTA that starts on a second piece loses about the time of this many tiles
+                                   // (start-up and join, 9 us of a CTA that takes 0.09 us a tile)
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -791,11 +793,12 @@ struct Shape {
     static_assert(kRows * kHeadDim * 4 <= kRing, "a warp's partial O lies in its ring");
 };
 
-// Decode.  The tiles of all (sequence, KV head, group of query rows) form one line, which the CTAs share out
-// evenly by the lengths found on the device, so that ragged lengths leave no CTA with more to do than another.
-// A CTA walks its stretch of the line piece by piece (one (sequence, head, group) each); its warps take a
-// piece's tiles in turn and meet in shared memory.  A piece that spans several CTAs is joined by the last of
-// them to arrive, in the order of the CTAs.
+// Decode.  A piece is one (sequence, KV head, group of query rows).  By the lengths found on the device, the CTAs
+// share the tiles of all pieces in one of two ways.  Short work: every piece is cut into equal parts, one to a CTA,
+// so that no CTA starts twice.  Long work, or more pieces than CTAs: the tiles of all pieces form one line, of
+// which every CTA walks an equal stretch piece by piece, so that ragged lengths leave no CTA with more to do than
+// another.  A CTA's warps take a stretch each of its tiles and meet in shared memory; a piece that several CTAs
+// share is joined by the last of them to arrive, in the order of the CTAs.
 //
 // DUP: at most 4 query rows; columns 4..7 of the products repeat them, so that one product takes P's high part
 // (columns 0..3) and its low part (4..7).
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     float* const sm_o = smem;
     __shared__ float sm_m[W * kRows], sm_l[W * kRows];
     __shared__ long long sm_scan[W];
-    __shared__ int sm_b, sm_len, sm_lo;
+    __shared__ int sm_b, sm_len, sm_lo, sm_cnt[kThreadsA], sm_share[W];
     __shared__ long long sm_start;
     __shared__ unsigned sm_last;
 
@@ -821,51 +824,73 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     const int nrg = (p.R + kRows - 1) / kRows;
     const int per_tile = p.c.Hkv * nrg;   // pieces of one sequence
 
-    // The line: its length, this CTA's stretch of it, the sequence that the stretch starts in.  Up to as many
-    // sequences as threads take one scan, more take one pass for the length and a scan of blocks of them.
+    // How the work is shared.  Tiles of up to as many sequences as threads take one scan; more take one pass for
+    // the line's length and a scan of blocks of them.
     Seq seq = sequence(p, min(tid, p.c.B - 1), blockIdx.x == 0 && tid < p.c.B);
     const bool one_scan = p.c.B <= kThreadsA;
-    long long total = tid < p.c.B ? tile_count(seq) : 0;
-    const int n_first = (int)total;
-    if (!one_scan) {
-        for (int b = tid + kThreadsA; b < p.c.B; b += kThreadsA) total += tile_count(sequence(p, b, blockIdx.x == 0));
+    const int n_first = tid < p.c.B ? tile_count(seq) : 0;
+    long long total = n_first;
+    for (int b = tid + kThreadsA; b < p.c.B; b += kThreadsA) total += tile_count(sequence(p, b, blockIdx.x == 0));
 #pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-        if (lane == 0) sm_scan[warp] = total;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < W; ++w) total += sm_scan[w];
-        total *= per_tile;
-        __syncthreads();
-    }
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+    if (lane == 0) sm_scan[warp] = total;
+    if (one_scan) sm_cnt[tid] = n_first;
+    if (tid == 0) sm_b = -1;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < W; ++w) total += sm_scan[w];
+    total *= per_tile;
     const int cta = blockIdx.x;
-    int n_cta = 0;
-    long long at = 0, end = 0;     // next tile of the line, end of the stretch
-    long long before = 0;          // tiles (of one piece each) of the sequences before this block of them
-    for (int b0 = 0;; b0 += kThreadsA) {
+    const long long pieces = (long long)p.c.B * per_tile;
+    const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
+    const int n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
+    int share = 0;   // tiles of a part where every CTA takes one part of one piece; 0: stretches of the line
+    if (one_scan && pieces <= grid) {
+        // the smallest share of a few (a warp tries one) whose parts are no more than the CTAs
+        const long long ideal = max((total + grid - 1) / grid, (long long)(W * kMinTiles));
+        const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (8 + W - 1 - warp) / 8, 0x7ffffffell);
+        long long parts = 0;
+        for (int b = lane; b < p.c.B; b += 32) parts += (sm_cnt[b] - 1) / mine + 1;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) parts += __shfl_xor_sync(kFull, parts, d);
+        int most = 0;
+        if (warp == 0) {
+            for (int b = lane; b < p.c.B; b += 32) most = max(most, sm_cnt[b]);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) most = max(most, __shfl_xor_sync(kFull, most, d));
+        }
+        if (lane == 0) sm_share[warp] = warp == 0 ? most : (parts * per_tile <= grid ? mine : 0x7fffffff);
+        __syncthreads();
+        share = sm_share[0];
+        for (int w = 1; w < W; ++w) share = min(share, sm_share[w]);
+        if (share > ideal + kSecondPiece) share = 0;
+    }
+    const bool whole_line = share == 0;
+    const int per = whole_line ? 1 : share;              // tiles of one unit of the scan
+    long long at = cta, end = cta + 1;                   // place in the line: of tiles, or of parts
+    if (whole_line) {
+        if (cta >= n_cta) return;
+        at = total * cta / n_cta;
+        end = total * (cta + 1) / n_cta;
+    }
+    long long before = 0;          // units (of one piece each) of the sequences before this block of them
+    for (int b0 = 0; b0 < p.c.B; b0 += kThreadsA) {
         const int b = b0 + tid;
         if (b0 > 0 && b < p.c.B) seq = sequence(p, b, false);
-        const int n = b0 == 0 ? n_first : (b < p.c.B ? tile_count(seq) : 0);
+        const int n = b < p.c.B ? ((b0 == 0 ? n_first : tile_count(seq)) - 1) / per + 1 : 0;
         long long inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long o = __shfl_up_sync(kFull, inc, d);
             if (lane >= d) inc += o;
         }
+        __syncthreads();   // sm_scan is free
         if (lane == 31) sm_scan[warp] = inc;
-        if (tid == 0) sm_b = -1;
         __syncthreads();
         long long sum = 0, mine = 0;
         for (int w = 0; w < W; ++w) {
             if (w == warp) mine = sum;
             sum += sm_scan[w];
-        }
-        if (b0 == 0) {
-            if (one_scan) total = sum * per_tile;
-            n_cta = (int)min(min((long long)gridDim.x, (long long)kMaxParts * p.c.B * per_tile), max(1ll, total / (W * kMinTiles)));
-            if (cta >= n_cta) return;
-            at = total * cta / n_cta;
-            end = total * (cta + 1) / n_cta;
         }
         const long long first = (before + mine + inc - n) * per_tile;
         if (n > 0 && at >= first && at < first + (long long)n * per_tile) {
@@ -876,9 +901,9 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         }
         __syncthreads();
         before += sum;
-        if (sm_b >= 0) break;   // always found: at < total
-        __syncthreads();        // all have seen it; the next block may write
+        if (sm_b >= 0) break;
     }
+    if (sm_b < 0) return;   // more CTAs than parts
     int b = sm_b;
     long long seq_start = sm_start;
     seq.len = sm_len;
@@ -887,15 +912,36 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     int ntile = tile_count(seq);
 
     for (bool head = true; at < end; head = false) {
-        while (at >= seq_start + (long long)ntile * per_tile) {
-            seq_start += (long long)ntile * per_tile;
-            seq = sequence(p, ++b, false);
-            ntile = tile_count(seq);
+        long long next;            // place after this piece
+        int piece, s0, s1;         // the piece of sequence b, this CTA's tiles of it
+        int c0, n_part, slot0;     // the CTAs that share it: c0 .. c0 + n_part - 1; the partial slot of the first
+        if (whole_line) {
+            while (at >= seq_start + (long long)ntile * per_tile) {
+                seq_start += (long long)ntile * per_tile;
+                seq = sequence(p, ++b, false);
+                ntile = tile_count(seq);
+            }
+            piece = (int)((at - seq_start) / ntile);
+            const long long start = seq_start + (long long)piece * ntile;
+            s0 = (int)(at - start);
+            s1 = (int)min((long long)ntile, end - start);
+            next = start + s1;
+            // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
+            c0 = (int)(((start + 1) * n_cta - 1) / total);
+            n_part = (int)(((start + ntile) * n_cta - 1) / total) - c0 + 1;
+            // a CTA's first piece uses its slot 0; this one is c0's first only if it starts c0's stretch
+            slot0 = c0 * 2 + (total * c0 / n_cta == start ? 0 : 1);
+        } else {
+            n_part = (ntile - 1) / share + 1;
+            piece = (int)((at - seq_start) / n_part);
+            const int part = (int)(at - seq_start) - piece * n_part;
+            s0 = (int)((long long)ntile * part / n_part);
+            s1 = (int)((long long)ntile * (part + 1) / n_part);
+            next = end;
+            c0 = cta - part;
+            slot0 = c0 * 2;
         }
-        const int piece = (int)((at - seq_start) / ntile);
-        const long long piece_start = seq_start + (long long)piece * ntile;
         const int h = piece / nrg, r0 = (piece - h * nrg) * kRows;
-        const int s0 = (int)(at - piece_start), s1 = (int)min((long long)ntile, end - piece_start);
         const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
@@ -988,7 +1034,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             }
         __syncthreads();
 
-        if (s0 != 0 || s1 != ntile) {
+        if (n_part > 1) {
             // this CTA's part of the piece goes to its slot; the last CTA to arrive takes all of them over
             constexpr int kPart = kRows * (kHeadDim + 2);
             float* part = p.part + (size_t)(cta * 2 + (head ? 0 : 1)) * kPart;
@@ -1001,13 +1047,10 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                     part[kRows * kHeadDim + kRows + row] = z;
                 }
             }
-            // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
-            const int c0 = (int)(((piece_start + 1) * n_cta - 1) / total);
-            const int c1 = (int)(((piece_start + ntile) * n_cta - 1) / total);
             __syncthreads();
             if (tid == 0) {
                 __threadfence();   // the CTA's part, which the barrier orders before this fence
-                sm_last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
+                sm_last = atomicAdd(p.counters + c0, 1u) == (unsigned)(n_part - 1);
                 if (sm_last) {
                     p.counters[c0] = 0;   // ready for the next call
                     __threadfence();
@@ -1015,14 +1058,13 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             }
             __syncthreads();
             if (sm_last) {
-                // A CTA's first piece is in its slot 0; this piece is c0's first only if it starts c0's stretch.
-                // All references and sums come to shared memory in one go, then kSplit warps take each row.
-                const int n = c1 - c0 + 1, s_first = c0 * 2 + (total * c0 / n_cta == piece_start ? 0 : 1);
+                // all references and sums come to shared memory in one go, then kSplit warps take each row
+                const int n = n_part;
                 float* sm_pm = smem;
                 float* sm_pl = smem + n * kRows;
                 for (int i = tid; i < n * kRows; i += kThreadsA) {
                     const int c = i / kRows;
-                    const float* from = p.part + (size_t)(c == 0 ? s_first : (c0 + c) * 2) * kPart + kRows * kHeadDim + i % kRows;
+                    const float* from = p.part + (size_t)(c == 0 ? slot0 : (c0 + c) * 2) * kPart + kRows * kHeadDim + i % kRows;
                     sm_pm[i] = __ldcg(from);
                     sm_pl[i] = __ldcg(from + kRows);
                 }
@@ -1046,7 +1088,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                         for (int d2 = 16; d2; d2 >>= 1) z += __shfl_xor_sync(kFull, z, d2);
 #pragma unroll 8
                         for (int c = part0; c < n; c += kSplit) {
-                            const float* from = p.part + (size_t)(c == 0 ? s_first : (c0 + c) * 2) * kPart + row * kHeadDim;
+                            const float* from = p.part + (size_t)(c == 0 ? slot0 : (c0 + c) * 2) * kPart + row * kHeadDim;
                             const float4 o = __ldcg(reinterpret_cast<const float4*>(from) + lane);
                             const float mc = sm_pm[c * kRows + row];
                             const float f = mc == -INFINITY ? 0.f : fast_exp2(mc - m);
@@ -1080,7 +1122,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 }
             }
             __syncthreads();   // shared memory is free for the next piece
-            at = piece_start + s1;
+            at = next;
             continue;
         }
         const int d = tid & (kHeadDim - 1);
@@ -1094,7 +1136,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             if (p.lse && d == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
         }
         __syncthreads();   // shared memory is free for the next piece
-        at = piece_start + s1;
+        at = next;
     }
 }
 
