@@ -431,7 +431,8 @@ FX_API int fx_branch_pool_batch(fx_branch_pool* pool, int32_t* ids, int32_t* suf
  *   len      device [B] int32: rows t < len[b] are valid (outside [0, max_pages*page_rows]: clamped,
  *            FX_DEVERR_LEN).  Rows at or past it are never used, whatever they hold.
  *   page_rows  16, 32, 64, 128, 256, 512 or 1024;  n_pages: pages in the pool;  max_pages: table entries
- *            of one sequence.  n_pages*page_rows is below 2^31, max_pages*page_rows below 2^30.
+ *            of one sequence.  n_pages*page_rows is below 2^31, max_pages*page_rows below 2^30,
+ *            page and row strides below 2^31 bytes.
  *   Codes and bf16 rows start on 16-byte boundaries, scale rows on 8-byte boundaries.  -64 <= k_exp,
  *   v_exp <= 64 (both 0 with FX_PAGED_BF16).
  */

@@ -1041,19 +1041,21 @@ fx_status paged_view(const fx_paged_desc* d, bool need_len, PagedCache* c)
     } else if (d->k_scale || d->v_scale || d->k_exp != 0 || d->v_exp != 0) {
         return fail(FX_ERR_INVALID_ARG, "cache: a bf16 cache has no scales (NULL) and no exponents (0)");
     }
-    const int64_t bytes = e2m1 ? 1 : 2;
+    const int64_t bytes = e2m1 ? 1 : 2, most = 0x7fffffff;
+    if (d->stride_page * bytes > most || d->stride_t * bytes > most || d->scale_stride_page > most || d->scale_stride_t > most)
+        return fail(FX_ERR_UNSUPPORTED, "cache: page and row strides are below 2^31 bytes");
     c->k = static_cast<char*>(d->k);
     c->v = static_cast<char*>(d->v);
     c->ks = static_cast<char*>(d->k_scale);
     c->vs = static_cast<char*>(d->v_scale);
     c->table = d->table;
     c->len = d->len;
-    c->sp = d->stride_page * bytes;
+    c->sp = (uint32_t)(d->stride_page * bytes);
     c->sh = d->stride_h * bytes;
-    c->st = d->stride_t * bytes;
-    c->ssp = d->scale_stride_page;
-    c->ssh = d->scale_stride_h;
-    c->sst = d->scale_stride_t;
+    c->st = (uint32_t)(d->stride_t * bytes);
+    c->ssp = e2m1 ? (uint32_t)d->scale_stride_page : 0u;
+    c->ssh = e2m1 ? d->scale_stride_h : 0;
+    c->sst = e2m1 ? (uint32_t)d->scale_stride_t : 0u;
     c->table_stride = d->table_stride;
     c->B = d->B;
     c->Hkv = d->Hkv;

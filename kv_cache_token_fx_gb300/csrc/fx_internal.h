@@ -224,8 +224,9 @@ struct PagedCache {
     char* vs;
     const int32_t* table;
     const int32_t* len;
-    int64_t sp, sh, st;     // page, head, row
-    int64_t ssp, ssh, sst;  // the same of the scale rows
+    int64_t sh, ssh;        // head: of the rows, of the scale rows
+    uint32_t sp, st;        // page, row
+    uint32_t ssp, sst;      // the same of the scale rows
     int64_t table_stride;
     int B, Hkv, n_pages, cap;   // cap = max_pages * page_rows
     int page_shift, page_mask;

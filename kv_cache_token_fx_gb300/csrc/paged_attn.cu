@@ -134,51 +134,56 @@ __device__ __forceinline__ int tile_count(const Seq& q)
 }
 
 
-__device__ __forceinline__ int64_t row_offset(const PagedCache& c, int id, int64_t sp, int64_t st)
+__device__ __forceinline__ int64_t row_offset(const PagedCache& c, int id, uint32_t sp, uint32_t st)
 {
-    return (int64_t)(id >> c.page_shift) * sp + (int64_t)(id & c.page_mask) * st;
+    return (uint64_t)(uint32_t)(id >> c.page_shift) * sp + (uint64_t)(uint32_t)(id & c.page_mask) * st;
 }
 
-// ---- tile slots in shared memory --------------------------------------------------------------------
-// 4-bit: K codes (16 rows of 64 bytes), V codes, K scales (16 rows of 8 bytes), V scales; of bf16: K rows (256
-// bytes), V rows; then the 16 rows' positions (-1: not valid).  The importance takes K alone.
+// ---- slots in shared memory ---------------------------------------------------------------------------
+// A slot holds a unit of U tiles.  4-bit: K codes (rows of 64 bytes), V codes, K scales (rows of 8 bytes), V
+// scales; of bf16: K rows (256 bytes), V rows; then the rows' positions (-1: not valid), present only for tiles
+// with an edge.  The importance takes K alone.
 // Codes: two rows share a 128-byte line, whose eight 16-byte chunks are permuted by chunk ^ 2 (line % 4), so
 // that neither the 16-byte reads of K (8 rows side by side) nor the 8-byte reads of V (rows 2t, the halves g of
 // them) meet in a bank.  bf16 rows are permuted as kv_off() has it.
-template <bool E2M1, bool WITH_V = true>
+template <bool E2M1, bool WITH_V, int U>
 struct Slot {
-    static constexpr int kV = E2M1 ? 1024 : 4096;
-    static constexpr int kScale = (WITH_V ? 2 : 1) * kV;
-    static constexpr int kPos = kScale + (E2M1 ? (WITH_V ? 256 : 128) : 0);
-    static constexpr int kBytes = kPos + 64;
+    static constexpr int kTile = E2M1 ? 1024 : 4096;     // K (or V) of one tile
+    static constexpr int kV = U * kTile;
+    static constexpr int kScale = (WITH_V ? 2 : 1) * U * kTile;
+    static constexpr int kScaleV = kScale + U * 128;
+    static constexpr int kPos = kScale + (E2M1 ? (WITH_V ? 2 : 1) * U * 128 : 0);
+    static constexpr int kBytes = kPos + U * 64;
 };
 
 // Fills slots with the tiles [it, end) of a sequence in order.  The first nl tiles hold the list, the others the
-// tail, whose tiles start at multiples of 16, so that such a tile lies inside one page.  All lanes call it.
+// tail, whose tiles start at multiples of 16, so that such a tile lies inside one page; the tail's pairs start
+// at multiples of 32.  All lanes call it.
 //
-// Tail: the lanes hold the next 32 page numbers, and inside a page the lane's addresses only advance -- a
-// tile costs a few additions beside its copies.  List: the lanes hold the rows of two tiles (lane L: entry L of
-// them), looked up a batch ahead, their positions another batch ahead.
-template <bool E2M1, bool WITH_V>
+// Tail: the lanes hold the next 32 page numbers, and inside a page the lane's addresses only advance; a pair of
+// whole tiles of one page is ten copies and a few additions.  List: the lanes hold the rows of two tiles (lane
+// L: entry L of them), looked up a batch ahead, their positions another batch ahead.
+template <bool E2M1, bool WITH_V, int U>
 struct Feeder {
+    using S = Slot<E2M1, WITH_V, U>;
     const PagedAttnParams& p;
     const Seq& q;
-    const char* k0;   // the lane's places relative to row 0 of page 0: K codes or rows, scales (V lies c.v - c.k
-    const char* s0;   // further on: its strides are K's)
-    uint32_t to;      // the lane's place in a slot (codes or rows)
+    const char* k0;   // the lane's places relative to row 0 of page 0: K codes or rows, K scales (V and its scales
+    const char* s0;   // lie c.v - c.k and c.vs - c.ks further on: their strides are K's)
+    uint32_t to;      // the lane's place in a tile (codes or rows)
     int it, end;
+    int plain0, plain1;   // tail tiles whose rows all count for every query, in pages without gaps between rows
+    int clear;        // rows below this one are seen by every query
     // tail
     int pos;          // first row of the next tail tile
     int pages, page_base;
-    bool ok;          // the page is good
-    const char* ka;
+    bool ok;          // its page is good
+    const char* ka;   // the lane's K place of that row (scales: of the lane-th row from it on)
     const char* sa;
     // list
     int id, at;       // the lane's pool row (-1: not valid) and position in the current two tiles
     int at1, page1, at2;
     int parity = 0;   // 16: the second of the two tiles is next
-    bool contig;      // rows of a page follow one another without gaps
-    int clear;        // rows below this one are seen by every query
 
     __device__ __forceinline__ Feeder(const PagedAttnParams& p_, const Seq& q_, int h, int it_, int end_)
         : p(p_), q(q_), it(it_), end(end_), clear(q_.len - p_.Mq + 1)
@@ -186,11 +191,10 @@ struct Feeder {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31;
         const int chunk = E2M1 ? lane & 3 : lane & 15, row = E2M1 ? lane >> 2 : lane >> 4;
-        k0 = c.k + (int64_t)h * c.sh + 16 * chunk;
-        s0 = (lane < 16 ? c.ks : c.vs) + (int64_t)h * c.ssh;
+        k0 = c.k + (int64_t)h * c.sh + row * (int64_t)c.st + 16 * chunk;
+        s0 = c.ks + (int64_t)h * c.ssh + lane * (int64_t)c.sst;
         to = E2M1 ? (row >> 1) * 128 + ((((row & 1) * 4 + chunk) ^ (2 * ((row >> 1) & 3))) << 4)
                   : row * 256 + ((chunk ^ row) << 4);
-        contig = c.st == (E2M1 ? 64 : 256) && (!E2M1 || c.sst == 8);
         if (it < q.nl && it < end) {
             at = list_pos(it * kTileRows + lane);
             at1 = list_pos((it + 2) * kTileRows + lane);
@@ -199,7 +203,10 @@ struct Feeder {
             at2 = list_pos((it + 4) * kTileRows + lane);
             id = place(at, page);
         }
-        pos = (q.lo & ~(kTileRows - 1)) + (max(it, q.nl) - q.nl) * kTileRows;
+        const int tail0 = q.lo & ~(kTileRows - 1);
+        pos = tail0 + (max(it, q.nl) - q.nl) * kTileRows;
+        plain0 = q.nl + (tail0 < q.lo ? 1 : 0);
+        plain1 = c.st == (E2M1 ? 64 : 256) && (!E2M1 || c.sst == 8) ? min(end, q.nl + max(clear - tail0, 0) / kTileRows) : 0;
         ok = false;
         ka = k0;
         sa = s0;
@@ -233,124 +240,150 @@ struct Feeder {
         const int64_t first = (int64_t)(page_base + (int)(threadIdx.x & 31)) << p.c.page_shift;
         pages = first < q.len ? q.table[page_base + (threadIdx.x & 31)] : -1;
     }
-
     __device__ __forceinline__ void enter_page()
     {
         const PagedCache& c = p.c;
-        const int lane = threadIdx.x & 31;
         if ((pos >> c.page_shift) - page_base >= 32) load_pages();
         const int page = __shfl_sync(kFull, pages, (pos >> c.page_shift) - page_base);
         ok = (unsigned)page < (unsigned)c.n_pages;
         if (!ok && pos < q.len) atomicOr(p.err, FX_DEVERR_PAGE);
-        const int64_t pg = ok ? page : 0, row = pos & c.page_mask;
-        ka = k0 + pg * c.sp + (row + (E2M1 ? lane >> 2 : lane >> 4)) * c.st;
-        if (E2M1) sa = s0 + pg * c.ssp + (row + (lane & 15)) * c.sst;
+        const int pg = ok ? page : 0, row = pos & c.page_mask;
+        ka = k0 + (uint64_t)(uint32_t)pg * c.sp + (uint64_t)(uint32_t)row * c.st;
+        if (E2M1) sa = s0 + (uint64_t)(uint32_t)pg * c.ssp + (uint64_t)(uint32_t)row * c.sst;
     }
-
-    // Feeds the next tile (none past the end: a slot without valid rows).  True when a row of it is not valid or
-    // not seen by every query; only then the rows' positions are in the slot.
-    __device__ __forceinline__ bool feed(uint32_t slot)
+    __device__ __forceinline__ void advance(int tiles)
     {
-        bool edge = true;
-        if (it < end) {
-            edge = it >= q.nl ? feed_tail(slot) : feed_list(slot);
-            ++it;
-        } else {
-            put_pos(slot, -1);
-        }
-        return edge;
+        const PagedCache& c = p.c;
+        it += tiles;
+        pos += tiles * kTileRows;
+        ka += (uint64_t)(tiles * kTileRows) * c.st;
+        if (E2M1) sa += (uint64_t)(tiles * kTileRows) * c.sst;
+        if ((pos & c.page_mask) == 0 && it < end) enter_page();
     }
 
-    __device__ __forceinline__ void put_pos(uint32_t slot, int t)
+    // Feeds the next unit.  Bit U - 1 - u of the result: tile u has a row that is not valid or not seen by every
+    // query (or there is no tile u); bit U: there is a tile at all.
+    __device__ __forceinline__ uint32_t feed(uint32_t slot)
+    {
+        const PagedCache& c = p.c;
+        uint32_t flags = 0;
+        if (U == 2 && E2M1 && it >= plain0 && it + 2 <= plain1 && ok && (pos & c.page_mask) + 32 <= c.page_mask + 1) {
+            const int lane = threadIdx.x & 31;
+            const uint32_t dst = slot + to, sdst = slot + S::kScale + 8 * lane;
+            const char* va = ka + (c.v - c.k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                cp_async16(dst + 512 * u, ka + 512 * u);
+                if (WITH_V) cp_async16(dst + S::kV + 512 * u, va + 512 * u);
+            }
+            cp_async8(sdst, sa);
+            if (WITH_V) cp_async8(sdst + U * 128, sa + (c.vs - c.ks));
+            advance(2);
+            flags = 4;
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                bool edge = true;
+                if (it < end && (u == 0 || it < q.nl || (pos & kTileRows) != 0)) {
+                    flags |= 1u << U;
+                    edge = it >= q.nl ? feed_tail(slot, u) : feed_list(slot, u);
+                } else {
+                    put_pos(slot, u, -1);
+                }
+                if (edge) flags |= 1u << (U - 1 - u);
+            }
+        }
+        cp_async_commit();
+        return flags;
+    }
+
+    __device__ __forceinline__ void put_pos(uint32_t slot, int u, int t)
     {
         const int lane = threadIdx.x & 31;
-        if (lane < 16) asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + Slot<E2M1, WITH_V>::kPos + 4 * lane), "r"(t) : "memory");
+        if (lane < 16) asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + S::kPos + 64 * u + 4 * lane), "r"(t) : "memory");
     }
 
-    __device__ __forceinline__ bool feed_tail(uint32_t slot)
+    __device__ __forceinline__ bool feed_tail(uint32_t slot, int u)
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31, j = lane & 15;
-        const char* va = ka + (c.v - c.k);
         const bool edge = !ok || pos < q.lo || pos + kTileRows > clear;
         if (edge) {
             const int t = pos + j;
-            put_pos(slot, ok && t >= q.lo && t < q.len ? t : -1);
+            put_pos(slot, u, ok && t >= q.lo && t < q.len ? t : -1);
         }
-        const uint32_t dst = slot + to;
+        const int64_t dv = c.v - c.k;
         if (E2M1) {
+            const uint32_t dst = slot + to + u * S::kTile;
+            const char* kb = ka + 8 * (int64_t)c.st;
             cp_async16(dst, ka);
-            if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, va);
-            if (contig) {
-                cp_async16(dst + 512, ka + 512);
-                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV + 512, va + 512);
-            } else {
-                cp_async16(dst + 512, ka + 8 * c.st);
-                if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV + 512, va + 8 * c.st);
+            cp_async16(dst + 512, kb);
+            if (WITH_V) {
+                cp_async16(dst + S::kV, ka + dv);
+                cp_async16(dst + S::kV + 512, kb + dv);
             }
-            if (WITH_V || lane < 16) cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, sa);
-            sa += 16 * c.sst;
-        } else if (contig) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint32_t d = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
-                cp_async16(d, ka + 512 * u);
-                if (WITH_V) cp_async16(d + Slot<E2M1, WITH_V>::kV, va + 512 * u);
-            }
+            if (lane < 16)
+                cp_async8(slot + S::kScale + u * 128 + 8 * lane, sa);
+            else if (WITH_V)
+                cp_async8(slot + S::kScaleV + u * 128 + 8 * j, sa + (c.vs - c.ks) - 16 * (int64_t)c.sst);
         } else {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint32_t d = slot + u * 512 + (to ^ ((2 * u & 6) << 4));
-                cp_async16(d, ka + 2 * u * c.st);
-                if (WITH_V) cp_async16(d + Slot<E2M1, WITH_V>::kV, va + 2 * u * c.st);
+            for (int w = 0; w < 8; ++w) {
+                const uint32_t d = slot + u * S::kTile + w * 512 + (to ^ ((2 * w & 6) << 4));
+                const char* from = ka + 2 * w * (int64_t)c.st;
+                cp_async16(d, from);
+                if (WITH_V) cp_async16(d + S::kV, from + dv);
             }
         }
-        ka += 16 * c.st;
-        pos += kTileRows;
-        if ((pos & c.page_mask) == 0 && it + 1 < end) enter_page();
+        advance(1);
         return edge;
     }
 
-    __device__ __forceinline__ bool feed_list(uint32_t slot)
+    __device__ __forceinline__ bool feed_list(uint32_t slot, int u)
     {
         const PagedCache& c = p.c;
         const int lane = threadIdx.x & 31, j = lane & 15;
         const int half = parity;
         const int mine = __shfl_sync(kFull, id, half + j), t = __shfl_sync(kFull, at, half + j);
         const bool edge = __any_sync(kFull, mine < 0 || t >= clear);
-        if (edge) put_pos(slot, mine >= 0 ? t : -1);
+        if (edge) put_pos(slot, u, mine >= 0 ? t : -1);
         constexpr int kCopies = E2M1 ? 2 : 8;   // rows of K (and V) that a lane copies 16 bytes of
+        const int lane_row = E2M1 ? lane >> 2 : lane >> 4;
+        const char* base = k0 - lane_row * (int64_t)c.st;
 #pragma unroll
-        for (int u = 0; u < kCopies; ++u) {
-            const int row = E2M1 ? (lane >> 2) + 8 * u : (lane >> 4) + 2 * u;
-            const int64_t o = row_offset(c, max(__shfl_sync(kFull, id, half + row), 0), c.sp, c.st);
-            const uint32_t dst = E2M1 ? slot + to + 512 * u : slot + u * 512 + (to ^ ((2 * u & 6) << 4));
-            cp_async16(dst, k0 + o);
-            if (WITH_V) cp_async16(dst + Slot<E2M1, WITH_V>::kV, k0 + (c.v - c.k) + o);
+        for (int w = 0; w < kCopies; ++w) {
+            const int row = max(__shfl_sync(kFull, id, half + (E2M1 ? lane_row + 8 * w : lane_row + 2 * w)), 0);
+            const char* from = base + row_offset(c, row, c.sp, c.st);
+            const uint32_t dst = slot + u * S::kTile + 512 * w + (E2M1 ? to : to ^ ((2 * w & 6) << 4));
+            cp_async16(dst, from);
+            if (WITH_V) cp_async16(dst + S::kV, from + (c.v - c.k));
         }
-        if (E2M1 && (WITH_V || lane < 16))
-            cp_async8(slot + Slot<E2M1, WITH_V>::kScale + 8 * lane, s0 + row_offset(c, max(mine, 0), c.ssp, c.sst));
+        if (E2M1 && (WITH_V || lane < 16)) {
+            const char* from = s0 - lane * (int64_t)c.sst + row_offset(c, max(mine, 0), c.ssp, c.sst);
+            cp_async8(slot + (lane < 16 ? S::kScale : S::kScaleV) + u * 128 + 8 * j, lane < 16 ? from : from + (c.vs - c.ks));
+        }
+        ++it;
         parity ^= 16;
         if (parity == 0) {   // the next two tiles
             at = at1;
             id = place(at, page1);
             at1 = at2;
-            page1 = list_page(at1, (it + 3) * kTileRows + lane);
-            at2 = list_pos((it + 5) * kTileRows + lane);
+            page1 = list_page(at1, (it + 2) * kTileRows + lane);
+            at2 = list_pos((it + 4) * kTileRows + lane);
         }
         return edge;
     }
 };
 
 // Calls f(j, a0, a1, a2, a3) with the A fragments of the eight 16-dimension steps of S^T = K Q^T.
-template <bool E2M1, bool WITH_V, typename F>
-__device__ __forceinline__ void k_steps(uint32_t slot, F&& f)
+template <typename S, bool E2M1, typename F>
+__device__ __forceinline__ void k_steps(uint32_t slot, int u, F&& f)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if constexpr (E2M1) {
-        const uint32_t at = slot + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (2 * ((g >> 1) & 3))) << 4);
+        const uint32_t at = slot + u * S::kTile + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (2 * ((g >> 1) & 3))) << 4);
         const uint4 x0 = lds128(at), x1 = lds128(at + 512);
-        const uint32_t sa = slot + Slot<true, WITH_V>::kScale + 8 * g + 2 * t;
+        const uint32_t sa = slot + S::kScale + u * 128 + 8 * g + 2 * t;
         const uint32_t s0 = e4m3x2_to_f16x2(lds16(sa)), s1 = e4m3x2_to_f16x2(lds16(sa + 64));
         const uint32_t sc[2][2] = {{__byte_perm(s0, 0, 0x1010), __byte_perm(s0, 0, 0x3232)},
                                    {__byte_perm(s1, 0, 0x1010), __byte_perm(s1, 0, 0x3232)}};
@@ -362,9 +395,9 @@ __device__ __forceinline__ void k_steps(uint32_t slot, F&& f)
             e2m1x8_to_f16(w0[j], a[0], a[1], a[2], a[3]);
             e2m1x8_to_f16(w1[j], b[0], b[1], b[2], b[3]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                a[u] = hmul2_u32(a[u], sc[0][j >> 1]);
-                b[u] = hmul2_u32(b[u], sc[1][j >> 1]);
+            for (int i = 0; i < 4; ++i) {
+                a[i] = hmul2_u32(a[i], sc[0][j >> 1]);
+                b[i] = hmul2_u32(b[i], sc[1][j >> 1]);
             }
             f(2 * j, a[0], b[0], a[1], b[1]);
             f(2 * j + 1, a[2], b[2], a[3], b[3]);
@@ -374,7 +407,7 @@ __device__ __forceinline__ void k_steps(uint32_t slot, F&& f)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             uint32_t a0, a1, a2, a3;
-            ldsm_x4(slot + kv_off(row, 2 * j + (lane >> 4)), a0, a1, a2, a3);
+            ldsm_x4(slot + u * S::kTile + kv_off(row, 2 * j + (lane >> 4)), a0, a1, a2, a3);
             f(j, a0, a1, a2, a3);
         }
     }
@@ -389,11 +422,11 @@ struct VTile<true> {
     uint32_t code[2][4];   // [dimensions 16g .. + 7, + 8 .. + 15][rows 2t, 2t + 1: even, odd dimensions; 2t + 8, + 9]
     uint32_t s01, s23;     // scales of rows 2t, 2t + 1 and 2t + 8, 2t + 9
 
-    template <bool MASKED>
-    __device__ __forceinline__ void load(uint32_t slot, uint32_t vm)
+    template <bool MASKED, typename S>
+    __device__ __forceinline__ void load(uint32_t slot, int tile, uint32_t vm)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const uint32_t sa = slot + Slot<true>::kScale + 128 + 16 * t + g;
+        const uint32_t sa = slot + S::kScaleV + tile * 128 + 16 * t + g;
         uint32_t vs01 = lds8(sa) | (lds8(sa + 8) << 8), vs23 = lds8(sa + 64) | (lds8(sa + 72) << 8);
         if (MASKED) {
             const uint32_t on = vm >> (2 * t);   // bits 0, 1, 8, 9
@@ -403,7 +436,7 @@ struct VTile<true> {
         s01 = e4m3x2_to_f16x2(vs01);
         s23 = e4m3x2_to_f16x2(vs23);
         const uint32_t in = t * 128 + (((g >> 1) ^ (2 * t)) << 4) + (g & 1) * 8;
-        const uint32_t va = slot + Slot<true>::kV + in, vb = slot + Slot<true>::kV + (in ^ 64u);
+        const uint32_t va = slot + S::kV + tile * S::kTile + in, vb = slot + S::kV + tile * S::kTile + (in ^ 64u);
         const uint2 x[4] = {lds64(va), lds64(vb), lds64(va + 512), lds64(vb + 512)};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -427,10 +460,10 @@ struct VTile<false> {
     uint32_t at;
     uint32_t m01, m23;
 
-    template <bool MASKED>
-    __device__ __forceinline__ void load(uint32_t slot, uint32_t vm)
+    template <bool MASKED, typename S>
+    __device__ __forceinline__ void load(uint32_t slot, int tile, uint32_t vm)
     {
-        at = slot + Slot<false>::kV;
+        at = slot + S::kV + tile * S::kTile;
         if (MASKED) {
             const uint32_t on = vm >> (2 * (threadIdx.x & 3));   // bits 0, 1, 8, 9: rows 2t, 2t + 1, 2t + 8, 2t + 9
             m01 = (on & 1u ? 0xffffu : 0u) | (on & 2u ? 0xffff0000u : 0u);
@@ -617,11 +650,11 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
 }
 
 // Logits of a tile: s[n][e] of row g + 8 (e >> 1) and query row 2t + (e & 1) of N tile n.
-template <bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slot, float (&s)[NT][4])
+template <typename S, bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slot, int u, float (&s)[NT][4])
 {
     float s2[NT][2][4];   // two chains of products, for their latency
-    k_steps<E2M1, true>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    k_steps<S, E2M1>(slot, u, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (j < 2)
@@ -674,20 +707,19 @@ __device__ __forceinline__ void term(float (&c)[4], const Weights<NT>& w, int n,
 // O^T += V^T P^T: the tiles' product starts from zero and is added to O by an fp32 addition.  The tensor core
 // aligns all products to the accumulator and cuts them off (2^-23 of it): accumulated over a long row that costs
 // small weights beside a large one, and drifts.
-template <bool E2M1, int NT, bool DUP, int U>
+template <int U, typename S, bool E2M1, int NT, bool DUP>
 __device__ __forceinline__ void attend(Acc<E2M1, NT, DUP>& a, uint32_t slot)
 {
-    constexpr int kSlot = Slot<E2M1>::kBytes;
     float s[U * NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) logits<E2M1, NT, DUP>(a, slot + u * kSlot, reinterpret_cast<float(&)[NT][4]>(s[u * NT]));
+    for (int u = 0; u < U; ++u) logits<S, E2M1, NT, DUP>(a, slot, u, reinterpret_cast<float(&)[NT][4]>(s[u * NT]));
     weights<false, U, E2M1, NT, DUP>(a, s, 0);
     Weights<NT> w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) fragments<E2M1, NT, DUP>(reinterpret_cast<float(&)[NT][4]>(s[u * NT]), w[u]);
     VTile<E2M1> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u].template load<false>(slot + u * kSlot, 0);
+    for (int u = 0; u < U; ++u) v[u].template load<false, S>(slot, u, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float c[NT][4];
@@ -707,17 +739,17 @@ __device__ __forceinline__ void attend(Acc<E2M1, NT, DUP>& a, uint32_t slot)
 
 // A tile with rows that do not count for every query (not valid, or past what some query sees), or a whole one
 // beside such a tile.
-template <bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int r0,
+template <typename S, bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int u, int r0,
                                             int seen, bool whole)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int pos = 0;   // of a whole tile: seen by all
-    if (!whole) pos = (int)lds32(slot + Slot<E2M1>::kPos + 4 * (lane & 15));
+    if (!whole) pos = (int)lds32(slot + S::kPos + 64 * u + 4 * (lane & 15));
     const uint32_t vm = __ballot_sync(kFull, pos >= 0) & 0xffffu;   // the valid rows
     if (vm == 0) return;
     float s[NT][4];
-    logits<E2M1, NT, DUP>(a, slot, s);
+    logits<S, E2M1, NT, DUP>(a, slot, u, s);
     uint32_t hide = 0;
     const int p0 = __shfl_sync(kFull, pos, g), p1 = __shfl_sync(kFull, pos, g + 8);
 #pragma unroll
@@ -738,12 +770,12 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
     if (__any_sync(kFull, pos > seen)) {
         bool bad = false;
         if (E2M1) {   // a NaN scale (the lane looks at half the scales of row lane / 2)
-            const uint32_t z = lds32(slot + Slot<E2M1>::kScale + 128 + 4 * lane) & 0x7f7f7f7fu;
+            const uint32_t z = lds32(slot + S::kScaleV + 128 * u + 4 * lane) & 0x7f7f7f7fu;
             const int of = __shfl_sync(kFull, pos, lane >> 1);
             bad = of > seen && __vcmpeq4(z, 0x7f7f7f7fu) != 0;
         } else {      // an all-ones exponent
             for (int j = 0; j < 16; ++j) {
-                const uint2 z = lds64(slot + Slot<E2M1>::kV + 256 * j + 8 * lane);
+                const uint2 z = lds64(slot + S::kV + u * S::kTile + 256 * j + 8 * lane);
                 const uint32_t x = __vcmpeq2(z.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(z.y & 0x7f807f80u, 0x7f807f80u);
                 bad |= __shfl_sync(kFull, pos, j) > seen && x != 0;
             }
@@ -761,7 +793,7 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
             }
         const uint32_t vi = passes == 1 ? vm : __ballot_sync(kFull, pos <= seen + i) & vm;
         VTile<E2M1> v;
-        v.template load<true>(slot, vi);
+        v.template load<true, S>(slot, u, vi);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             uint32_t x[4];
@@ -788,7 +820,8 @@ struct Shape {
     static constexpr int kCtas = E2M1 && NT == 1 ? 2 : 1;   // per SM
     static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
     static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
-    static constexpr int kRing = kStages * kUnit * Slot<E2M1>::kBytes;   // bytes of a warp; its partial O later takes them
+    using Unit = Slot<E2M1, true, kUnit>;
+    static constexpr int kRing = kStages * Unit::kBytes;   // bytes of a warp; its partial O later takes them
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
     static_assert(kRows * kHeadDim * 4 <= kRing, "a warp's partial O lies in its ring");
 };
@@ -807,7 +840,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     paged_decode_kernel(const PagedAttnParams p)
 {
     using S = Shape<E2M1, NT, DUP>;
-    constexpr int kRows = S::kRows, W = S::kWarps, kThreadsA = 32 * W, kStages = S::kStages, U = S::kUnit, kSlot = Slot<E2M1>::kBytes;
+    constexpr int kRows = S::kRows, W = S::kWarps, kThreadsA = 32 * W, kStages = S::kStages, U = S::kUnit, kSlot = S::Unit::kBytes;
     constexpr int kPitch = S::kRing / 4;   // floats between the warps' partial O
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
@@ -843,11 +876,12 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     const int cta = blockIdx.x;
     const long long pieces = (long long)p.c.B * per_tile;
     const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
-    const int n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
+    static_assert(kMinTiles == 2 && (W == 8 || W == 12), "");
+    const int n_cta = (int)min((long long)grid, max(1ll, total >> 4));   // at least kMinTiles tiles a warp (of 8)
     int share = 0;   // tiles of a part where every CTA takes one part of one piece; 0: stretches of the line
     if (one_scan && pieces <= grid) {
         // the smallest share of a few (a warp tries one) whose parts are no more than the CTAs
-        const long long ideal = max((total + grid - 1) / grid, (long long)(W * kMinTiles));
+        const long long ideal = max((long long)((float)total / (float)grid) + 1, (long long)(W * kMinTiles));
         const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (8 + W - 1 - warp) / 8, 0x7ffffffell);
         long long parts = 0;
         for (int b = lane; b < p.c.B; b += 32) parts += (sm_cnt[b] - 1) / mine + 1;
@@ -952,20 +986,17 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             const int r = r0 + 8 * n + (DUP ? g & 3 : g);
             fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[n]);
         }
-        // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on);
-        // the ring's first units go on their way, then each turn feeds the unit kStages - 1 turns ahead
-        const int mine = s1 - s0;
-        int it = s0 + mine * warp / W;
-        const int stop = s0 + mine * (warp + 1) / W;
-        Feeder<E2M1, true> feeder(p, seq, h, it, stop);
-        uint32_t edges = 0;   // bit k U + u: tile U - 1 - u of the unit fed k turns ago has an edge
-        auto feed = [&](uint32_t slot) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) edges = 2 * edges + (feeder.feed(slot + u * kSlot) ? 1u : 0u);
-            cp_async_commit();
+        // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on; pairs
+        // start at multiples of 32); the ring's first units go on their way, then each turn feeds the unit
+        // kStages - 1 turns ahead
+        auto share_start = [&](int w) {
+            const int x = s0 + (int)((long long)(s1 - s0) * w / W);
+            return w == W ? s1 : (w == 0 || U == 1 || x < seq.nl ? x : min(x + (((seq.lo >> 4) + x - seq.nl) & 1), s1));
         };
+        Feeder<E2M1, true, U> feeder(p, seq, h, share_start(warp), share_start(warp + 1));
+        uint32_t flags[kStages];   // of the units in the ring, oldest first
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) feed(ring + k * U * kSlot);
+        for (int k = 0; k < kStages - 1; ++k) flags[k] = feeder.feed(ring + k * kSlot);
 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -982,23 +1013,23 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
         }
 
-        uint32_t slot = ring, into = ring + (kStages - 1) * U * kSlot;
-        for (; it < stop; it += U) {
+        uint32_t slot = ring, into = ring + (kStages - 1) * kSlot;
+        while (flags[0] >> U) {
             cp_async_wait_stages<kStages - 1>();   // this lane's copies of the unit; the barrier covers the others'
             __syncwarp();
-            feed(into);
-            const uint32_t edge = (edges >> ((kStages - 1) * U)) & ((1u << U) - 1);
-            if (U > 1 && it + 1 == stop && (edge >> (U - 1)) == 0) {
-                attend<E2M1, NT, DUP, 1>(a, slot);   // the last one alone
-            } else if (edge != 0) {
+            flags[kStages - 1] = feeder.feed(into);
+            const uint32_t edge = flags[0] & ((1u << U) - 1);
+            if (edge == 0) {
+                attend<U, typename S::Unit>(a, slot);
+            } else {
 #pragma unroll 1
                 for (int u = 0; u < U; ++u)
-                    attend_edge<E2M1, NT, DUP>(p, a, slot + u * kSlot, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
-            } else {
-                attend<E2M1, NT, DUP, U>(a, slot);
+                    attend_edge<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
             }
             into = slot;
-            slot = slot + U * kSlot == ring + S::kRing ? ring : slot + U * kSlot;
+            slot = slot + kSlot == ring + S::kRing ? ring : slot + kSlot;
+#pragma unroll
+            for (int k = 0; k < kStages - 1; ++k) flags[k] = flags[k + 1];
         }
         cp_async_wait_all_groups();
         __syncwarp();   // every lane is done with the ring
@@ -1141,7 +1172,6 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 }
 
 constexpr int kImpWarps = 8;
-constexpr int kImpStages = 2;
 constexpr int kImpTiles = 8;   // tiles of a warp of the importance kernel
 
 // Importance: each warp takes kImpTiles tiles of 16 rows and every query row; the query fragments lie in
@@ -1149,7 +1179,8 @@ constexpr int kImpTiles = 8;   // tiles of a warp of the importance kernel
 template <bool E2M1>
 __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const PagedAttnParams p)
 {
-    constexpr int kSlot = Slot<E2M1, false>::kBytes;
+    constexpr int U = E2M1 ? 2 : 1;
+    using S = Slot<E2M1, false, U>;
     extern __shared__ __align__(128) float smem[];   // the warps' rings
     __shared__ uint4 sq[kMaxRows / 8][4][32];
     __shared__ float2 sf[kMaxRows];                  // factor of a row's logits, minus its lse (base 2)
@@ -1159,13 +1190,12 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
     const int h = blockIdx.y, b = blockIdx.z;
     Seq seq = sequence(p, b, true);
     const int len = seq.len, seen = len - p.Mq;
-    const int first = (p.cand_lo & ~(kTileRows - 1)) + (blockIdx.x * kImpWarps + warp) * (kImpTiles * kTileRows);
+    const int first = (p.cand_lo & ~(2 * kTileRows - 1)) + (blockIdx.x * kImpWarps + warp) * (kImpTiles * kTileRows);
     seq.lo = first;
     const int ntile = first < len ? min(kImpTiles, (len - first + kTileRows - 1) / kTileRows) : 0;   // with rows in them
-    Feeder<E2M1, false> feeder(p, seq, h, 0, ntile);
-    const uint32_t ring = smem_addr(smem) + warp * kImpStages * kSlot;
-    bool edge = feeder.feed(ring);
-    cp_async_commit();
+    Feeder<E2M1, false, U> feeder(p, seq, h, 0, ntile);
+    const uint32_t ring = smem_addr(smem) + warp * 2 * S::kBytes;   // two slots
+    uint32_t flags = feeder.feed(ring);
     const int nq = (p.R + 7) / 8;
     for (int n = warp; n < nq; n += kImpWarps) {
         const int r = 8 * n + g, of = min(r, p.R - 1);
@@ -1182,19 +1212,23 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
     }
     __syncthreads();
     float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * (p.cand_hi - p.cand_lo);
+    uint32_t edges = 0;
     for (int u = 0; u < kImpTiles; ++u) {
         const int base = first + u * kTileRows;
         if (base >= p.cand_hi) break;
         float sum[2] = {0.f, 0.f};
         if (u < ntile) {
-            const uint32_t slot = ring + (u & 1) * kSlot;
-            cp_async_wait_stages<1>();
-            __syncwarp();
-            const bool masked = edge;
-            edge = feeder.feed(ring + (~u & 1) * kSlot);
-            cp_async_commit();
+            const int in = u % U;
+            const uint32_t slot = ring + (u / U & 1) * S::kBytes;
+            if (in == 0) {
+                cp_async_wait_stages<1>();
+                __syncwarp();
+                edges = flags;
+                flags = feeder.feed(ring + (~(u / U) & 1) * S::kBytes);
+            }
+            const bool masked = (edges >> (U - 1 - in)) & 1u;
             uint32_t a[8][4];
-            k_steps<E2M1, false>(slot, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            k_steps<S, E2M1>(slot, in, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                 a[j][0] = a0;
                 a[j][1] = a1;
                 a[j][2] = a2;
@@ -1202,8 +1236,8 @@ __global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const 
             });
             int p0 = 0, p1 = 0;
             if (masked) {
-                p0 = (int)lds32(slot + Slot<E2M1, false>::kPos + 4 * g);
-                p1 = (int)lds32(slot + Slot<E2M1, false>::kPos + 32 + 4 * g);
+                p0 = (int)lds32(slot + S::kPos + 64 * in + 4 * g);
+                p1 = (int)lds32(slot + S::kPos + 64 * in + 32 + 4 * g);
             }
             for (int n = 0; n < nq; ++n) {
                 float s[2][4];
@@ -1269,11 +1303,11 @@ cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cuda
 template <bool E2M1>
 cudaError_t launch_importance(const PagedAttnParams& p, bool pdl, cudaStream_t s)
 {
-    constexpr size_t smem = (size_t)kImpWarps * kImpStages * Slot<E2M1, false>::kBytes;
+    constexpr size_t smem = (size_t)kImpWarps * 2 * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(paged_importance_kernel<E2M1>, smem, done);
     if (e != cudaSuccess) return e;
-    const int rows = p.cand_hi - (p.cand_lo & ~(kTileRows - 1));
+    const int rows = p.cand_hi - (p.cand_lo & ~(2 * kTileRows - 1));
     const int per = kImpWarps * kImpTiles * kTileRows;
     return launch_kernel(paged_importance_kernel<E2M1>, dim3((rows + per - 1) / per, p.c.Hkv, p.c.B), dim3(32 * kImpWarps),
                          smem, s, pdl, 0u, p);

@@ -157,13 +157,13 @@ __global__ void __launch_bounds__(kThreadsRows) paged_append_kernel(const PagedA
     if (p.rot > 0) x = rotate_chunk(x, c, cs, p.rot, p.interleaved != 0);
     if (is_q && live) *reinterpret_cast<uint4*>(p.q_out + i * p.qo_n + h * p.qo_h + 8 * c) = x;
     const int64_t row = pos & p.c.page_mask;
-    char* dst = (is_v ? p.c.v : p.c.k) + page * p.c.sp + h * p.c.sh + row * p.c.st;
+    char* dst = (is_v ? p.c.v : p.c.k) + (int64_t)page * p.c.sp + h * p.c.sh + row * p.c.st;
     if (E2M1) {
         uint32_t sb;
         const uint32_t codes = quantize_chunk(x, is_v ? p.c.v_inv : p.c.k_inv, sb);
         if (live && !is_q) {
             *reinterpret_cast<uint32_t*>(dst + 4 * c) = codes;
-            char* sd = (is_v ? p.c.vs : p.c.ks) + page * p.c.ssp + h * p.c.ssh + row * p.c.sst;
+            char* sd = (is_v ? p.c.vs : p.c.ks) + (int64_t)page * p.c.ssp + h * p.c.ssh + row * p.c.sst;
             if ((c & 1) == 0) sd[c >> 1] = (char)sb;
         }
     } else if (live && !is_q) {
@@ -201,14 +201,14 @@ __global__ void __launch_bounds__(kThreadsRows) paged_gather_kernel(const PagedG
     const int page = paged_page(p.c, b, (int)t, p.err);
     if (page < 0) return;
     const int64_t row = t & p.c.page_mask;
-    const int64_t at = page * p.c.sp + h * p.c.sh + row * p.c.st;
+    const int64_t at = (int64_t)page * p.c.sp + h * p.c.sh + row * p.c.st;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         const char* src = (w ? p.c.v : p.c.k) + at;
         uint4 x;
         if (E2M1) {
             const uint32_t codes = *reinterpret_cast<const uint32_t*>(src + 4 * c);
-            const char* ss = (w ? p.c.vs : p.c.ks) + page * p.c.ssp + h * p.c.ssh + row * p.c.sst;
+            const char* ss = (w ? p.c.vs : p.c.ks) + (int64_t)page * p.c.ssp + h * p.c.ssh + row * p.c.sst;
             const uint32_t sb = (uint8_t)ss[c >> 1];
             const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sb) & 0xffffu))) *
                             (w ? p.c.v_mul : p.c.k_mul);

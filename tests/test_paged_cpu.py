@@ -34,7 +34,8 @@ BAD_CACHES = [
     (dict(max_pages=0), 1, b"max_pages"), (dict(table_stride=4), 1, b"table_stride"), (dict(page_rows=8), 2, b"page_rows"),
     (dict(page_rows=48), 2, b"page_rows"), (dict(page_rows=2048), 2, b"page_rows"),
     (dict(n_pages=1 << 26), 2, b"rows"), (dict(max_pages=1 << 25, table_stride=1 << 25), 2, b"rows"),
-    (dict(B=65536), 2, b"65535"), (dict(k=264), 1, b"aligned"), (dict(stride_t=72), 1, b"16 bytes"),
+    (dict(B=65536), 2, b"65535"), (dict(stride_page=1 << 31), 2, b"2^31 bytes"), (dict(scale_stride_t=1 << 32), 2, b"2^31 bytes"),
+    (dict(BF16, stride_t=1 << 30), 2, b"2^31 bytes"), (dict(k=264), 1, b"aligned"), (dict(stride_t=72), 1, b"16 bytes"),
     (dict(stride_h=-64), 1, b"16 bytes"), (dict(k_scale=None), 1, b"k_scale"), (dict(v_scale=1028), 1, b"8-byte"),
     (dict(scale_stride_t=4), 1, b"8-byte"), (dict(k_exp=65), 1, b"k_exp"), (dict(v_exp=-65), 1, b"v_exp"),
     (dict(format=0), 1, b"no scales"), (dict(BF16, k_exp=1), 1, b"exponents"), (dict(BF16, stride_t=68), 1, b"16 bytes"),
