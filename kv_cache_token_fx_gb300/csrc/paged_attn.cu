@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kTileRows = 16;
 constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call
-constexpr int kMaxParts = 64;   // CTAs that share one (sequence, KV head, row group) on average, at most: the last
+constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
 constexpr int kSecondPiece = 96;   // a CTA that starts on a second piece loses about the time of this many tiles
                                    // (start-up and join, 9 us of a CTA that takes 0.09 us a tile)
@@ -816,8 +816,8 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
 template <bool E2M1, int NT, bool DUP>
 struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
-    static constexpr int kWarps = E2M1 && NT == 2 ? 12 : 8;
-    static constexpr int kCtas = E2M1 && NT == 1 ? 2 : 1;   // per SM
+    static constexpr int kWarps = 4;                     // few, so that other CTAs of the SM work while one starts or joins
+    static constexpr int kCtas = E2M1 ? (NT == 1 ? 4 : 3) : 2;   // per SM
     static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
     static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
     using Unit = Slot<E2M1, true, kUnit>;
@@ -876,13 +876,12 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     const int cta = blockIdx.x;
     const long long pieces = (long long)p.c.B * per_tile;
     const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
-    static_assert(kMinTiles == 2 && (W == 8 || W == 12), "");
-    const int n_cta = (int)min((long long)grid, max(1ll, total >> 4));   // at least kMinTiles tiles a warp (of 8)
+    const int n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
     int share = 0;   // tiles of a part where every CTA takes one part of one piece; 0: stretches of the line
     if (one_scan && pieces <= grid) {
         // the smallest share of a few (a warp tries one) whose parts are no more than the CTAs
         const long long ideal = max((long long)((float)total / (float)grid) + 1, (long long)(W * kMinTiles));
-        const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (8 + W - 1 - warp) / 8, 0x7ffffffell);
+        const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (4 + W - 1 - warp) / 4, 0x7ffffffell);
         long long parts = 0;
         for (int b = lane; b < p.c.B; b += 32) parts += (sm_cnt[b] - 1) / mine + 1;
 #pragma unroll
@@ -1318,7 +1317,7 @@ cudaError_t launch_importance(const PagedAttnParams& p, bool pdl, cudaStream_t s
 // The counters' region, then two partials (one of each end of a CTA's stretch) per CTA.
 size_t paged_decode_workspace_bytes(int R, int sm_count)
 {
-    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16), ctas = (size_t)(R <= 8 ? 2 : 1) * sm_count;
+    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16), ctas = (size_t)(R <= 8 ? 4 : 3) * sm_count;
     return kCounterBytes + ctas * 2 * rows * (kHeadDim + 2) * sizeof(float);
 }
 
