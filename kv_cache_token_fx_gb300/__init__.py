@@ -567,6 +567,9 @@ class PagedKV:
 
 
 # These calls run once or more per layer and token: their checks are written for few interpreter steps.
+# The current stream's handle without a Stream object around it (3 us against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _ROWS = struct.Struct("@PPqqPPqqqqPPPPiiiiixxxx")   # PagedRows
 assert _ROWS.size == ctypes.sizeof(PagedRows)
 
@@ -614,7 +617,7 @@ def _paged_launch(cache, stream):
     if torch.cuda.current_device() != cache._index:
         raise FxError(FX_ERR_INVALID_ARG, f"the cache is on {cache.device}, the current device is another one")
     if stream is None:
-        return _lib or load_library(), torch.cuda.current_stream().cuda_stream
+        return _lib or load_library(), _raw_stream(cache._index)
     return _lib or load_library(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -1132,7 +1132,7 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
     if (rows->rot > 0 && (!rows->cos_sin || !aligned16(rows->cos_sin) || rows->n_pos < 1))
         return fail(FX_ERR_INVALID_ARG, "rows: rot > 0 needs cos_sin (16-byte aligned) of n_pos >= 1 positions");
     const int Hq = rows->q ? rows->Hq : 0;
-    if (Hq > 65535 || (int64_t)rows->n * (2 * (int64_t)cache->Hkv + Hq) > (int64_t)0x7fffffff * 16)
+    if (Hq > 65535 || (int64_t)rows->n * (2 * (int64_t)cache->Hkv + Hq) > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "too many rows");
     if (rows->n == 0) return FX_OK;
     DeviceState* ds = nullptr;
