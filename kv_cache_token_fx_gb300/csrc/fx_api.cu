@@ -1246,7 +1246,7 @@ fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int6
     p.cand_hi = cand_hi;
     p.scores = scores;
     p.err = ds->err;
-    cudaError_t e = launch_paged_importance(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+    cudaError_t e = launch_paged_importance(p, cache->format == FX_PAGED_E2M1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
                                             static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged importance launch");
     return FX_OK;

@@ -322,7 +322,7 @@ cudaError_t launch_append(const AppendParams& p, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
-cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);
 
 // Launch `kern` with optional programmatic stream serialization and a (1, cluster_y, 1) cluster.

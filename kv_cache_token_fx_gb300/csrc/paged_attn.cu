@@ -177,7 +177,7 @@ struct Feeder {
     // tail
     int pos;          // first row of the next tail tile
     int pages, page_base;
-    bool ok;          // its page is good
+    bool enter, ok;   // it starts a page (or the feeder); its page is good
     const char* ka;   // the lane's K place of that row (scales: of the lane-th row from it on)
     const char* sa;
     // list
@@ -210,10 +210,8 @@ struct Feeder {
         ok = false;
         ka = k0;
         sa = s0;
-        if (end > q.nl) {
-            load_pages();
-            enter_page();
-        }
+        enter = true;
+        if (end > q.nl) load_pages();
     }
 
     __device__ __forceinline__ int list_pos(int e) const { return e < min(p.kk, end * kTileRows) ? q.idx[e] : -1; }
@@ -240,7 +238,7 @@ struct Feeder {
         const int64_t first = (int64_t)(page_base + (int)(threadIdx.x & 31)) << p.c.page_shift;
         pages = first < q.len ? q.table[page_base + (threadIdx.x & 31)] : -1;
     }
-    __device__ __forceinline__ void enter_page()
+    __device__ __forceinline__ bool enter_page()
     {
         const PagedCache& c = p.c;
         if ((pos >> c.page_shift) - page_base >= 32) load_pages();
@@ -250,51 +248,64 @@ struct Feeder {
         const int pg = ok ? page : 0, row = pos & c.page_mask;
         ka = k0 + (uint64_t)(uint32_t)pg * c.sp + (uint64_t)(uint32_t)row * c.st;
         if (E2M1) sa = s0 + (uint64_t)(uint32_t)pg * c.ssp + (uint64_t)(uint32_t)row * c.sst;
+        enter = false;
+        return true;
     }
-    __device__ __forceinline__ void advance(int tiles)
-    {
-        const PagedCache& c = p.c;
-        it += tiles;
-        pos += tiles * kTileRows;
-        ka += (uint64_t)(tiles * kTileRows) * c.st;
-        if (E2M1) sa += (uint64_t)(tiles * kTileRows) * c.sst;
-        if ((pos & c.page_mask) == 0 && it < end) enter_page();
-    }
-
     // Feeds the next unit.  Bit U - 1 - u of the result: tile u has a row that is not valid or not seen by every
     // query (or there is no tile u); bit U: there is a tile at all.
     __device__ __forceinline__ uint32_t feed(uint32_t slot)
     {
         const PagedCache& c = p.c;
         uint32_t flags = 0;
-        if (U == 2 && E2M1 && it >= plain0 && it + 2 <= plain1 && ok && (pos & c.page_mask) + 32 <= c.page_mask + 1) {
-            const int lane = threadIdx.x & 31;
-            const uint32_t dst = slot + to, sdst = slot + S::kScale + 8 * lane;
-            const char* va = ka + (c.v - c.k);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                cp_async16(dst + 512 * u, ka + 512 * u);
-                if (WITH_V) cp_async16(dst + S::kV + 512 * u, va + 512 * u);
-            }
-            cp_async8(sdst, sa);
-            if (WITH_V) cp_async8(sdst + U * 128, sa + (c.vs - c.ks));
+        if (E2M1 && U == 2 && it >= plain0 && it + 2 <= plain1 && (pos & c.page_mask) + 32 <= c.page_mask + 1 &&
+            (!enter || enter_page()) && ok) {
+            feed_pair(slot);
             advance(2);
-            flags = 4;
+            flags = 1u << U;
         } else {
 #pragma unroll 1
             for (int u = 0; u < U; ++u) {
                 bool edge = true;
-                if (it < end && (u == 0 || it < q.nl || (pos & kTileRows) != 0)) {
-                    flags |= 1u << U;
-                    edge = it >= q.nl ? feed_tail(slot, u) : feed_list(slot, u);
-                } else {
+                if (it >= end || (u > 0 && it >= q.nl && (pos & kTileRows) == 0)) {
                     put_pos(slot, u, -1);
+                } else {
+                    flags |= 1u << U;
+                    if (it < q.nl) {
+                        edge = feed_list(slot, u);
+                        ++it;
+                    } else {
+                        if (enter) enter_page();
+                        edge = feed_tail(slot, u);
+                        advance(1);
+                    }
                 }
                 if (edge) flags |= 1u << (U - 1 - u);
             }
         }
         cp_async_commit();
         return flags;
+    }
+    __device__ __forceinline__ void advance(int n)
+    {
+        it += n;
+        pos += n * kTileRows;
+        ka += (uint64_t)(uint32_t)(n * kTileRows) * p.c.st;
+        if (E2M1) sa += (uint64_t)(uint32_t)(n * kTileRows) * p.c.sst;
+        enter = (pos & p.c.page_mask) == 0;
+    }
+
+    __device__ __forceinline__ void feed_pair(uint32_t slot)
+    {
+        const PagedCache& c = p.c;
+        const uint32_t dst = slot + to, sdst = slot + S::kScale + 8 * (threadIdx.x & 31);
+        const char* va = ka + (c.v - c.k);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            cp_async16(dst + 512 * u, ka + 512 * u);
+            if (WITH_V) cp_async16(dst + S::kV + 512 * u, va + 512 * u);
+        }
+        cp_async8(sdst, sa);
+        if (WITH_V) cp_async8(sdst + U * 128, sa + (c.vs - c.ks));
     }
 
     __device__ __forceinline__ void put_pos(uint32_t slot, int u, int t)
@@ -335,7 +346,6 @@ struct Feeder {
                 if (WITH_V) cp_async16(d + S::kV, from + dv);
             }
         }
-        advance(1);
         return edge;
     }
 
@@ -362,14 +372,13 @@ struct Feeder {
             const char* from = s0 - lane * (int64_t)c.sst + row_offset(c, max(mine, 0), c.ssp, c.sst);
             cp_async8(slot + (lane < 16 ? S::kScale : S::kScaleV) + u * 128 + 8 * j, lane < 16 ? from : from + (c.vs - c.ks));
         }
-        ++it;
         parity ^= 16;
         if (parity == 0) {   // the next two tiles
             at = at1;
             id = place(at, page1);
             at1 = at2;
-            page1 = list_page(at1, (it + 2) * kTileRows + lane);
-            at2 = list_pos((it + 4) * kTileRows + lane);
+            page1 = list_page(at1, (it + 3) * kTileRows + lane);
+            at2 = list_pos((it + 5) * kTileRows + lane);
         }
         return edge;
     }
@@ -810,6 +819,181 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
     }
 }
 
+// How the CTAs of a kernel share its work.  A piece is one (sequence, KV head, group of query rows).  By the
+// lengths found on the device, the tiles of all pieces are shared in one of two ways.  Short work: every piece is
+// cut into equal parts, one to a CTA, so that no CTA starts twice.  Long work, or more pieces than CTAs: the tiles
+// of all pieces form one line, of which every CTA walks an equal stretch piece by piece, so that ragged lengths
+// leave no CTA with more to do than another.
+template <int W>
+struct LineSmem {
+    long long scan[W], start;
+    int b, len, lo, share[W], cnt[32 * W];
+};
+template <int W, typename Count>
+struct Line {
+    const PagedAttnParams& p;
+    const Count count;         // tiles of a sequence's piece, at least 1
+    const int per_seq;         // pieces of one sequence
+    Seq seq;
+    int b, ntile;              // the sequence, tiles of its pieces
+    int piece, s0, s1;         // the piece of the sequence, this CTA's tiles of it
+    int c0, n_part, slot0;     // the CTAs that share it: c0 .. c0 + n_part - 1; the partial slot of the first
+    int slot;                  // this CTA's partial slot
+
+    __device__ __forceinline__ Line(const PagedAttnParams& p_, Count count_, int per_seq_)
+        : p(p_), count(count_), per_seq(per_seq_)
+    {
+    }
+
+    // False: nothing for this CTA.  All threads call it.
+    __device__ __forceinline__ bool start(LineSmem<W>& sm)
+    {
+        constexpr int kThreadsL = 32 * W;
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        const int B = p.c.B;
+        // Up to as many sequences as threads take one scan; more take one pass for the line's length and a scan
+        // of blocks of them.
+        seq = sequence(p, min(tid, B - 1), blockIdx.x == 0 && tid < B);
+        const bool one_scan = B <= kThreadsL;
+        const int n_first = tid < B ? count(seq) : 0;
+        total = n_first;
+        for (int i = tid + kThreadsL; i < B; i += kThreadsL) total += count(sequence(p, i, blockIdx.x == 0));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+        if (lane == 0) sm.scan[warp] = total;
+        if (one_scan) sm.cnt[tid] = n_first;
+        if (tid == 0) sm.b = -1;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) total += sm.scan[w];
+        total *= per_seq;
+        cta = blockIdx.x;
+        const long long pieces = (long long)B * per_seq;
+        const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
+        n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
+        share = 0;
+        if (one_scan && pieces <= grid) {
+            // the smallest share of a few (a warp tries one) whose parts are no more than the CTAs
+            const long long ideal = max((long long)((float)total / (float)grid) + 1, (long long)(W * kMinTiles));
+            const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (3 + W - warp) / 4, 0x7ffffffell);
+            long long parts = 0;
+            int most = 0;
+            for (int i = lane; i < B; i += 32) {
+                parts += (sm.cnt[i] - 1) / mine + 1;
+                most = max(most, sm.cnt[i]);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+                parts += __shfl_xor_sync(kFull, parts, d);
+                most = max(most, __shfl_xor_sync(kFull, most, d));
+            }
+            if (lane == 0) sm.share[warp] = warp == 0 ? most : (parts * per_seq <= grid ? mine : 0x7fffffff);
+            __syncthreads();
+            share = sm.share[0];
+#pragma unroll
+            for (int w = 1; w < W; ++w) share = min(share, sm.share[w]);
+            if (share > ideal + kSecondPiece) share = 0;
+        }
+        at = cta;
+        end = cta + 1;
+        if (share == 0) {
+            if (cta >= n_cta) return false;
+            at = total * cta / n_cta;
+            end = total * (cta + 1) / n_cta;
+        }
+        const int per = share == 0 ? 1 : share;   // tiles of one unit of the scan
+        long long before = 0;                     // units (of one piece each) of the sequences before this block
+        for (int b0 = 0; b0 < B; b0 += kThreadsL) {
+            const int i = b0 + tid;
+            if (b0 > 0 && i < B) seq = sequence(p, i, false);
+            const int n = i < B ? ((b0 == 0 ? n_first : count(seq)) - 1) / per + 1 : 0;
+            long long inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long o = __shfl_up_sync(kFull, inc, d);
+                if (lane >= d) inc += o;
+            }
+            __syncthreads();   // sm.scan is free
+            if (lane == 31) sm.scan[warp] = inc;
+            __syncthreads();
+            long long sum = 0, mine = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w == warp) mine = sum;
+                sum += sm.scan[w];
+            }
+            const long long first = (before + mine + inc - n) * per_seq;
+            if (n > 0 && at >= first && at < first + (long long)n * per_seq) {
+                sm.b = i;
+                sm.start = first;
+                sm.len = seq.len;
+                sm.lo = seq.lo;
+            }
+            __syncthreads();
+            before += sum;
+            if (sm.b >= 0) break;
+        }
+        b = sm.b;
+        if (b < 0) return false;   // more CTAs than parts
+        seq_start = sm.start;
+        seq.len = sm.len;
+        seq.lo = sm.lo;
+        seq.table = p.c.table + (int64_t)b * p.c.table_stride;
+        ntile = count(seq);
+        slot = cta * 2;
+        return true;
+    }
+
+    // The next piece of this CTA; false: there is none.
+    __device__ __forceinline__ bool next()
+    {
+        if (at >= end) return false;
+        if (share == 0) {
+            while (at >= seq_start + (long long)ntile * per_seq) {
+                seq_start += (long long)ntile * per_seq;
+                seq = sequence(p, ++b, false);
+                ntile = count(seq);
+            }
+            piece = (int)((at - seq_start) / ntile);
+            const long long from = seq_start + (long long)piece * ntile;
+            s0 = (int)(at - from);
+            s1 = (int)min((long long)ntile, end - from);
+            // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
+            c0 = (int)(((from + 1) * n_cta - 1) / total);
+            n_part = (int)(((from + ntile) * n_cta - 1) / total) - c0 + 1;
+            // a CTA's first piece uses its slot 0; this one is c0's first only if it starts c0's stretch
+            slot0 = c0 * 2 + (total * c0 / n_cta == from ? 0 : 1);
+            slot = cta * 2 + (at == total * cta / n_cta ? 0 : 1);
+            at = from + s1;
+        } else {
+            n_part = (ntile - 1) / share + 1;
+            piece = (int)((at - seq_start) / n_part);
+            const int part = (int)(at - seq_start) - piece * n_part;
+            s0 = (int)((long long)ntile * part / n_part);
+            s1 = (int)((long long)ntile * (part + 1) / n_part);
+            c0 = cta - part;
+            slot0 = c0 * 2;
+            at = end;
+        }
+        return true;
+    }
+
+private:
+    int cta, n_cta, share;     // share: tiles of a part where every CTA takes one part of one piece; 0: stretches
+    long long total, at, end;  // length of the line (tiles), next place and end of this CTA's (tiles, or parts)
+    long long seq_start;       // place where the sequence starts
+};
+
+// Start of warp w's stretch of the tiles [s0, s1) of a sequence: nearly equal ones; where tiles are taken in pairs,
+// the tail's start at multiples of 32 rows.
+template <int U, int W>
+__device__ __forceinline__ int warp_start(const Seq& q, int s0, int s1, int w)
+{
+    const int x = s0 + (int)((long long)(s1 - s0) * w / W);
+    return w == W ? s1 : (w == 0 || U == 1 || x < q.nl ? x : min(x + (((q.lo >> 4) + x - q.nl) & 1), s1));
+}
+
 // Shape of the decode kernel for a format and up to 4 (DUP), 8 or 16 query rows a pass.  4-bit tiles are small
 // (2.3 KB) and cost many operations a byte: 16 warps an SM.  bf16 tiles (8 KB) fill the shared memory with 8
 // warps' rings.
@@ -826,12 +1010,8 @@ struct Shape {
     static_assert(kRows * kHeadDim * 4 <= kRing, "a warp's partial O lies in its ring");
 };
 
-// Decode.  A piece is one (sequence, KV head, group of query rows).  By the lengths found on the device, the CTAs
-// share the tiles of all pieces in one of two ways.  Short work: every piece is cut into equal parts, one to a CTA,
-// so that no CTA starts twice.  Long work, or more pieces than CTAs: the tiles of all pieces form one line, of
-// which every CTA walks an equal stretch piece by piece, so that ragged lengths leave no CTA with more to do than
-// another.  A CTA's warps take a stretch each of its tiles and meet in shared memory; a piece that several CTAs
-// share is joined by the last of them to arrive, in the order of the CTAs.
+// Decode.  A CTA's warps take a stretch each of its tiles of a piece and meet in shared memory; a piece that several
+// CTAs share is joined by the last of them to arrive, in the order of the CTAs.
 //
 // DUP: at most 4 query rows; columns 4..7 of the products repeat them, so that one product takes P's high part
 // (columns 0..3) and its low part (4..7).
@@ -845,9 +1025,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
     __shared__ float sm_m[W * kRows], sm_l[W * kRows];
-    __shared__ long long sm_scan[W];
-    __shared__ int sm_b, sm_len, sm_lo, sm_cnt[kThreadsA], sm_share[W];
-    __shared__ long long sm_start;
+    __shared__ LineSmem<W> sm_line;
     __shared__ unsigned sm_last;
 
     griddep_wait();
@@ -855,126 +1033,14 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const int nrg = (p.R + kRows - 1) / kRows;
-    const int per_tile = p.c.Hkv * nrg;   // pieces of one sequence
+    auto tiles = [](const Seq& q) { return tile_count(q); };
+    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv * nrg);
+    if (!line.start(sm_line)) return;
 
-    // How the work is shared.  Tiles of up to as many sequences as threads take one scan; more take one pass for
-    // the line's length and a scan of blocks of them.
-    Seq seq = sequence(p, min(tid, p.c.B - 1), blockIdx.x == 0 && tid < p.c.B);
-    const bool one_scan = p.c.B <= kThreadsA;
-    const int n_first = tid < p.c.B ? tile_count(seq) : 0;
-    long long total = n_first;
-    for (int b = tid + kThreadsA; b < p.c.B; b += kThreadsA) total += tile_count(sequence(p, b, blockIdx.x == 0));
-#pragma unroll
-    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-    if (lane == 0) sm_scan[warp] = total;
-    if (one_scan) sm_cnt[tid] = n_first;
-    if (tid == 0) sm_b = -1;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < W; ++w) total += sm_scan[w];
-    total *= per_tile;
-    const int cta = blockIdx.x;
-    const long long pieces = (long long)p.c.B * per_tile;
-    const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
-    const int n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
-    int share = 0;   // tiles of a part where every CTA takes one part of one piece; 0: stretches of the line
-    if (one_scan && pieces <= grid) {
-        // the smallest share of a few (a warp tries one) whose parts are no more than the CTAs
-        const long long ideal = max((long long)((float)total / (float)grid) + 1, (long long)(W * kMinTiles));
-        const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (4 + W - 1 - warp) / 4, 0x7ffffffell);
-        long long parts = 0;
-        for (int b = lane; b < p.c.B; b += 32) parts += (sm_cnt[b] - 1) / mine + 1;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) parts += __shfl_xor_sync(kFull, parts, d);
-        int most = 0;
-        if (warp == 0) {
-            for (int b = lane; b < p.c.B; b += 32) most = max(most, sm_cnt[b]);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) most = max(most, __shfl_xor_sync(kFull, most, d));
-        }
-        if (lane == 0) sm_share[warp] = warp == 0 ? most : (parts * per_tile <= grid ? mine : 0x7fffffff);
-        __syncthreads();
-        share = sm_share[0];
-        for (int w = 1; w < W; ++w) share = min(share, sm_share[w]);
-        if (share > ideal + kSecondPiece) share = 0;
-    }
-    const bool whole_line = share == 0;
-    const int per = whole_line ? 1 : share;              // tiles of one unit of the scan
-    long long at = cta, end = cta + 1;                   // place in the line: of tiles, or of parts
-    if (whole_line) {
-        if (cta >= n_cta) return;
-        at = total * cta / n_cta;
-        end = total * (cta + 1) / n_cta;
-    }
-    long long before = 0;          // units (of one piece each) of the sequences before this block of them
-    for (int b0 = 0; b0 < p.c.B; b0 += kThreadsA) {
-        const int b = b0 + tid;
-        if (b0 > 0 && b < p.c.B) seq = sequence(p, b, false);
-        const int n = b < p.c.B ? ((b0 == 0 ? n_first : tile_count(seq)) - 1) / per + 1 : 0;
-        long long inc = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(kFull, inc, d);
-            if (lane >= d) inc += o;
-        }
-        __syncthreads();   // sm_scan is free
-        if (lane == 31) sm_scan[warp] = inc;
-        __syncthreads();
-        long long sum = 0, mine = 0;
-        for (int w = 0; w < W; ++w) {
-            if (w == warp) mine = sum;
-            sum += sm_scan[w];
-        }
-        const long long first = (before + mine + inc - n) * per_tile;
-        if (n > 0 && at >= first && at < first + (long long)n * per_tile) {
-            sm_b = b;
-            sm_start = first;
-            sm_len = seq.len;
-            sm_lo = seq.lo;
-        }
-        __syncthreads();
-        before += sum;
-        if (sm_b >= 0) break;
-    }
-    if (sm_b < 0) return;   // more CTAs than parts
-    int b = sm_b;
-    long long seq_start = sm_start;
-    seq.len = sm_len;
-    seq.lo = sm_lo;
-    seq.table = p.c.table + (int64_t)b * p.c.table_stride;
-    int ntile = tile_count(seq);
-
-    for (bool head = true; at < end; head = false) {
-        long long next;            // place after this piece
-        int piece, s0, s1;         // the piece of sequence b, this CTA's tiles of it
-        int c0, n_part, slot0;     // the CTAs that share it: c0 .. c0 + n_part - 1; the partial slot of the first
-        if (whole_line) {
-            while (at >= seq_start + (long long)ntile * per_tile) {
-                seq_start += (long long)ntile * per_tile;
-                seq = sequence(p, ++b, false);
-                ntile = tile_count(seq);
-            }
-            piece = (int)((at - seq_start) / ntile);
-            const long long start = seq_start + (long long)piece * ntile;
-            s0 = (int)(at - start);
-            s1 = (int)min((long long)ntile, end - start);
-            next = start + s1;
-            // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
-            c0 = (int)(((start + 1) * n_cta - 1) / total);
-            n_part = (int)(((start + ntile) * n_cta - 1) / total) - c0 + 1;
-            // a CTA's first piece uses its slot 0; this one is c0's first only if it starts c0's stretch
-            slot0 = c0 * 2 + (total * c0 / n_cta == start ? 0 : 1);
-        } else {
-            n_part = (ntile - 1) / share + 1;
-            piece = (int)((at - seq_start) / n_part);
-            const int part = (int)(at - seq_start) - piece * n_part;
-            s0 = (int)((long long)ntile * part / n_part);
-            s1 = (int)((long long)ntile * (part + 1) / n_part);
-            next = end;
-            c0 = cta - part;
-            slot0 = c0 * 2;
-        }
-        const int h = piece / nrg, r0 = (piece - h * nrg) * kRows;
+    while (line.next()) {
+        const int b = line.b, s0 = line.s0, s1 = line.s1, n_part = line.n_part;
+        const int h = line.piece / nrg, r0 = (line.piece - h * nrg) * kRows;
+        Seq seq = line.seq;
         const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
 
@@ -988,15 +1054,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on; pairs
         // start at multiples of 32); the ring's first units go on their way, then each turn feeds the unit
         // kStages - 1 turns ahead
-        auto share_start = [&](int w) {
-            const int x = s0 + (int)((long long)(s1 - s0) * w / W);
-            return w == W ? s1 : (w == 0 || U == 1 || x < seq.nl ? x : min(x + (((seq.lo >> 4) + x - seq.nl) & 1), s1));
-        };
-        Feeder<E2M1, true, U> feeder(p, seq, h, share_start(warp), share_start(warp + 1));
-        uint32_t flags[kStages];   // of the units in the ring, oldest first
-#pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) flags[k] = feeder.feed(ring + k * kSlot);
-
+        Feeder<E2M1, true, U> feeder(p, seq, h, warp_start<U, W>(seq, s0, s1, warp), warp_start<U, W>(seq, s0, s1, warp + 1));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float f = make_query<E2M1>(a.q[n]);
@@ -1012,21 +1070,27 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
         }
 
-        uint32_t slot = ring, into = ring + (kStages - 1) * kSlot;
-        while (flags[0] >> U) {
-            cp_async_wait_stages<kStages - 1>();   // this lane's copies of the unit; the barrier covers the others'
+        uint32_t flags[kStages];   // of the units in the ring, oldest first
+#pragma unroll
+        for (int k = 0; k < kStages; ++k) flags[k] = 1u << U;
+        uint32_t slot = ring + kSlot, into = ring;   // (the first turns only feed)
+        for (int turn = 1 - kStages; flags[0] >> U; ++turn) {
+            if (turn >= 0) cp_async_wait_stages<kStages - 1>();   // this lane's copies; the barrier covers the others'
             __syncwarp();
             flags[kStages - 1] = feeder.feed(into);
-            const uint32_t edge = flags[0] & ((1u << U) - 1);
-            if (edge == 0) {
-                attend<U, typename S::Unit>(a, slot);
-            } else {
+            if (turn == -1) slot = ring;
+            if (turn >= 0) {
+                const uint32_t edge = flags[0] & ((1u << U) - 1);
+                if (edge == 0) {
+                    attend<U, typename S::Unit>(a, slot);
+                } else {
 #pragma unroll 1
-                for (int u = 0; u < U; ++u)
-                    attend_edge<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
+                    for (int u = 0; u < U; ++u)
+                        attend_edge<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
+                }
+                slot = slot + kSlot == ring + S::kRing ? ring : slot + kSlot;
             }
-            into = slot;
-            slot = slot + kSlot == ring + S::kRing ? ring : slot + kSlot;
+            into = into + kSlot == ring + S::kRing ? ring : into + kSlot;
 #pragma unroll
             for (int k = 0; k < kStages - 1; ++k) flags[k] = flags[k + 1];
         }
@@ -1067,7 +1131,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         if (n_part > 1) {
             // this CTA's part of the piece goes to its slot; the last CTA to arrive takes all of them over
             constexpr int kPart = kRows * (kHeadDim + 2);
-            float* part = p.part + (size_t)(cta * 2 + (head ? 0 : 1)) * kPart;
+            float* part = p.part + (size_t)line.slot * kPart;
             const int d = tid & (kHeadDim - 1);
             for (int row = tid / kHeadDim; row < kRows; row += kThreadsA / kHeadDim) {
                 float z, m;
@@ -1080,9 +1144,9 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             __syncthreads();
             if (tid == 0) {
                 __threadfence();   // the CTA's part, which the barrier orders before this fence
-                sm_last = atomicAdd(p.counters + c0, 1u) == (unsigned)(n_part - 1);
+                sm_last = atomicAdd(p.counters + line.c0, 1u) == (unsigned)(n_part - 1);
                 if (sm_last) {
-                    p.counters[c0] = 0;   // ready for the next call
+                    p.counters[line.c0] = 0;   // ready for the next call
                     __threadfence();
                 }
             }
@@ -1094,7 +1158,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 float* sm_pl = smem + n * kRows;
                 for (int i = tid; i < n * kRows; i += kThreadsA) {
                     const int c = i / kRows;
-                    const float* from = p.part + (size_t)(c == 0 ? slot0 : (c0 + c) * 2) * kPart + kRows * kHeadDim + i % kRows;
+                    const float* from = p.part + (size_t)(c == 0 ? line.slot0 : (line.c0 + c) * 2) * kPart + kRows * kHeadDim + i % kRows;
                     sm_pm[i] = __ldcg(from);
                     sm_pl[i] = __ldcg(from + kRows);
                 }
@@ -1118,7 +1182,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                         for (int d2 = 16; d2; d2 >>= 1) z += __shfl_xor_sync(kFull, z, d2);
 #pragma unroll 8
                         for (int c = part0; c < n; c += kSplit) {
-                            const float* from = p.part + (size_t)(c == 0 ? slot0 : (c0 + c) * 2) * kPart + row * kHeadDim;
+                            const float* from = p.part + (size_t)(c == 0 ? line.slot0 : (line.c0 + c) * 2) * kPart + row * kHeadDim;
                             const float4 o = __ldcg(reinterpret_cast<const float4*>(from) + lane);
                             const float mc = sm_pm[c * kRows + row];
                             const float f = mc == -INFINITY ? 0.f : fast_exp2(mc - m);
@@ -1152,7 +1216,6 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 }
             }
             __syncthreads();   // shared memory is free for the next piece
-            at = next;
             continue;
         }
         const int d = tid & (kHeadDim - 1);
@@ -1166,112 +1229,134 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             if (p.lse && d == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
         }
         __syncthreads();   // shared memory is free for the next piece
-        at = next;
     }
 }
 
-constexpr int kImpWarps = 8;
-constexpr int kImpTiles = 8;   // tiles of a warp of the importance kernel
+constexpr int kImpWarps = 4;
+__host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
-// Importance: each warp takes kImpTiles tiles of 16 rows and every query row; the query fragments lie in
-// shared memory as the products want them.  Rows of the fragments beyond the last query row repeat it and add 2^-inf.
+// Importance.  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
+// want them, and each of them serves a unit of tiles at a time.  Rows of the fragments beyond the last query row
+// repeat it and add 2^-inf.
 template <bool E2M1>
-__global__ void __launch_bounds__(32 * kImpWarps) paged_importance_kernel(const PagedAttnParams p)
+__global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importance_kernel(const PagedAttnParams p)
 {
-    constexpr int U = E2M1 ? 2 : 1;
+    constexpr int U = E2M1 ? 2 : 1, W = kImpWarps;
     using S = Slot<E2M1, false, U>;
-    extern __shared__ __align__(128) float smem[];   // the warps' rings
-    __shared__ uint4 sq[kMaxRows / 8][4][32];
+    extern __shared__ __align__(128) uint4 sq[];     // [8-row tile][4][32], then the warps' rings
     __shared__ float2 sf[kMaxRows];                  // factor of a row's logits, minus its lse (base 2)
+    __shared__ LineSmem<W> sm_line;
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int h = blockIdx.y, b = blockIdx.z;
-    Seq seq = sequence(p, b, true);
-    const int len = seq.len, seen = len - p.Mq;
-    const int first = (p.cand_lo & ~(2 * kTileRows - 1)) + (blockIdx.x * kImpWarps + warp) * (kImpTiles * kTileRows);
-    seq.lo = first;
-    const int ntile = first < len ? min(kImpTiles, (len - first + kTileRows - 1) / kTileRows) : 0;   // with rows in them
-    Feeder<E2M1, false, U> feeder(p, seq, h, 0, ntile);
-    const uint32_t ring = smem_addr(smem) + warp * 2 * S::kBytes;   // two slots
-    uint32_t flags = feeder.feed(ring);
-    const int nq = (p.R + 7) / 8;
-    for (int n = warp; n < nq; n += kImpWarps) {
-        const int r = 8 * n + g, of = min(r, p.R - 1);
-        uint32_t q[16];
-        fetch_query<E2M1>(query_row(p, b, h, of), q);
-        const float f = make_query<E2M1>(q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sq[n][j][lane] = make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
-        if (t == 0) {
+    const int nq = (p.R + 7) / 8, n_cand = p.cand_hi - p.cand_lo;
+    const uint32_t ring = smem_addr(sq + nq * 128) + warp * 2 * S::kBytes;   // two slots
+    const int base = p.cand_lo & ~(2 * kTileRows - 1);                       // first row of the first tile
+    // candidates past a sequence's end
+    for (int64_t i = blockIdx.x; i < (int64_t)p.c.B * p.c.Hkv; i += gridDim.x) {
+        const int len = sequence(p, (int)(i / p.c.Hkv), false).len;
+        for (int r = max(len, p.cand_lo) + threadIdx.x; r < p.cand_hi; r += 32 * W) p.scores[i * n_cand + r - p.cand_lo] = 0.f;
+    }
+    auto tiles = [&](const Seq& q) { return max((min(q.len, p.cand_hi) - base + kTileRows - 1) / kTileRows, 1); };
+    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv);
+    if (!line.start(sm_line)) return;
+
+    while (line.next()) {
+        const int b = line.b, h = line.piece;
+        Seq seq = line.seq;
+        seq.lo = base;
+        const int seen = seq.len - p.Mq, stop = min(seq.len, p.cand_hi);
+        Feeder<E2M1, false, U> feeder(p, seq, h, warp_start<U, W>(seq, line.s0, line.s1, warp),
+                                      warp_start<U, W>(seq, line.s0, line.s1, warp + 1));
+        int row0 = base + feeder.it * kTileRows;     // first row of the unit in work
+        for (int n = warp; n < nq; n += W) {
+            const int r = 8 * n + g, of = min(r, p.R - 1);
+            uint32_t q[16];
+            fetch_query<E2M1>(query_row(p, b, h, of), q);
             // a row that saw nothing (lse = -inf) adds nothing
             const float z = p.lse[((int64_t)b * p.Hq + h * p.G + of / p.Mq) * p.Mq + of % p.Mq];
-            sf[r] = make_float2(p.qscale * f, r >= p.R || z == -INFINITY ? -INFINITY : z * -1.4426950408889634f);
+            const float f = make_query<E2M1>(q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sq[(n * 4 + j) * 32 + lane] = make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+            if (t == 0) sf[r] = make_float2(p.qscale * f, r >= p.R || z == -INFINITY ? -INFINITY : z * -1.4426950408889634f);
         }
-    }
-    __syncthreads();
-    float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * (p.cand_hi - p.cand_lo);
-    uint32_t edges = 0;
-    for (int u = 0; u < kImpTiles; ++u) {
-        const int base = first + u * kTileRows;
-        if (base >= p.cand_hi) break;
-        float sum[2] = {0.f, 0.f};
-        if (u < ntile) {
-            const int in = u % U;
-            const uint32_t slot = ring + (u / U & 1) * S::kBytes;
-            if (in == 0) {
-                cp_async_wait_stages<1>();
-                __syncwarp();
-                edges = flags;
-                flags = feeder.feed(ring + (~(u / U) & 1) * S::kBytes);
+        __syncthreads();
+        float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * n_cand - p.cand_lo;
+        uint32_t flags = feeder.feed(ring), slot = ring;
+        while (flags >> U) {
+            cp_async_wait_all_groups();   // this lane's copies of the unit; the barrier covers the others'
+            __syncwarp();
+            const uint32_t edges = flags & ((1u << U) - 1);
+            const int here = row0;
+            row0 = base + feeder.it * kTileRows;
+            const uint32_t next = slot == ring ? ring + S::kBytes : ring;
+            flags = feeder.feed(next);
+            uint32_t a[U][8][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                k_steps<S, E2M1>(slot, u, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    a[u][j][0] = a0;
+                    a[u][j][1] = a1;
+                    a[u][j][2] = a2;
+                    a[u][j][3] = a3;
+                });
+            int pos[U][2];   // of the tile's rows g, g + 8
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                pos[u][0] = pos[u][1] = 0;
+                if ((edges >> (U - 1 - u)) & 1u) {
+                    pos[u][0] = (int)lds32(slot + S::kPos + 64 * u + 4 * g);
+                    pos[u][1] = (int)lds32(slot + S::kPos + 64 * u + 32 + 4 * g);
+                }
             }
-            const bool masked = (edges >> (U - 1 - in)) & 1u;
-            uint32_t a[8][4];
-            k_steps<S, E2M1>(slot, in, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                a[j][0] = a0;
-                a[j][1] = a1;
-                a[j][2] = a2;
-                a[j][3] = a3;
-            });
-            int p0 = 0, p1 = 0;
-            if (masked) {
-                p0 = (int)lds32(slot + S::kPos + 64 * in + 4 * g);
-                p1 = (int)lds32(slot + S::kPos + 64 * in + 32 + 4 * g);
-            }
+            float sum[U][2] = {};
+#pragma unroll 1
             for (int n = 0; n < nq; ++n) {
-                float s[2][4];
+                float s[U][2][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint4 q = sq[n][j][lane];
-                    if (j == 0) {
-                        mma16_zero<E2M1>(s[0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
-                        mma16_zero<E2M1>(s[1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
-                    } else {
-                        mma16<E2M1>(s[0], a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], q.x, q.y);
-                        mma16<E2M1>(s[1], a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], q.z, q.w);
+                    const uint4 q = sq[(n * 4 + j) * 32 + lane];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t(&x)[4] = a[u][2 * j], (&y)[4] = a[u][2 * j + 1];
+                        if (j == 0) {
+                            mma16_zero<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
+                            mma16_zero<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
+                        } else {
+                            mma16<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
+                            mma16<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
+                        }
                     }
                 }
                 const float4 f = *reinterpret_cast<const float4*>(&sf[8 * n + 2 * t]);   // rows 2t, 2t + 1
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = fmaf(s[0][e] + s[1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
-                    if (masked) {
-                        const int row = e >> 1 ? p1 : p0;
-                        if (row < 0 || row > seen + (8 * n + 2 * t + (e & 1)) % p.Mq) x = -INFINITY;
-                    }
-                    sum[e >> 1] += fast_exp2(x);
-                }
-            }
-        }
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            sum[e] += __shfl_xor_sync(kFull, sum[e], 1);
-            sum[e] += __shfl_xor_sync(kFull, sum[e], 2);
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(s[u][0][e] + s[u][1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
+                        if (edges != 0) {
+                            const int row = pos[u][e >> 1];
+                            if (row < 0 || row > seen + (8 * n + 2 * t + (e & 1)) % p.Mq) x = -INFINITY;
+                        }
+                        sum[u][e >> 1] += fast_exp2(x);
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sum[u][e] += __shfl_xor_sync(kFull, sum[u][e], 1);
+                    sum[u][e] += __shfl_xor_sync(kFull, sum[u][e], 2);
+                }
+                // (a tile of the unit that does not exist starts at or past `stop`, or the next unit writes it)
+                const int row = here + u * kTileRows + g + 8 * t;
+                const bool mine = u == 0 || !((edges >> (U - 1 - u)) & 1u) || here + u * kTileRows < row0;
+                if (t < 2 && mine && row >= p.cand_lo && row < stop) out[row] = t ? sum[u][1] : sum[u][0];
+            }
+            slot = next;
         }
-        const int row = base + g + 8 * t;
-        if (t < 2 && row >= p.cand_lo && row < p.cand_hi) out[row - p.cand_lo] = t ? sum[1] : sum[0];
+        __syncthreads();   // the query fragments are free for the next piece
     }
-    cp_async_wait_all_groups();
 }
 
 // Raises a kernel's dynamic shared memory limit, once a device (a runtime call of about a microsecond).
@@ -1300,16 +1385,14 @@ cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cuda
 }
 
 template <bool E2M1>
-cudaError_t launch_importance(const PagedAttnParams& p, bool pdl, cudaStream_t s)
+cudaError_t launch_importance(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    constexpr size_t smem = (size_t)kImpWarps * 2 * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
+    constexpr size_t ring = (size_t)kImpWarps * 2 * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(paged_importance_kernel<E2M1>, smem, done);
+    const cudaError_t e = allow_smem(paged_importance_kernel<E2M1>, ring + kMaxRows / 8 * 2048, done);
     if (e != cudaSuccess) return e;
-    const int rows = p.cand_hi - (p.cand_lo & ~(2 * kTileRows - 1));
-    const int per = kImpWarps * kImpTiles * kTileRows;
-    return launch_kernel(paged_importance_kernel<E2M1>, dim3((rows + per - 1) / per, p.c.Hkv, p.c.B), dim3(32 * kImpWarps),
-                         smem, s, pdl, 0u, p);
+    return launch_kernel(paged_importance_kernel<E2M1>, dim3(imp_ctas(E2M1) * sm_count), dim3(32 * kImpWarps), ring + (p.R + 7) / 8 * 2048, s,
+                         pdl, 0u, p);
 }
 
 }  // namespace
@@ -1333,9 +1416,9 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_coun
     return launch_decode<false, 2, false>(p, sm_count, pdl, s);
 }
 
-cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, bool pdl, cudaStream_t s)
+cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    return e2m1 ? launch_importance<true>(p, pdl, s) : launch_importance<false>(p, pdl, s);
+    return e2m1 ? launch_importance<true>(p, sm_count, pdl, s) : launch_importance<false>(p, sm_count, pdl, s);
 }
 
 }  // namespace fx
