@@ -31,8 +31,8 @@ constexpr int kTileRows = 16;
 constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call
 constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
-constexpr int kSecondPiece = 96;   // a CTA that starts on a second piece loses about the time of this many tiles
-                                   // (start-up and join, 9 us of a CTA that takes 0.09 us a tile)
+constexpr int kSecondPiece = 32;   // a CTA that starts on a second piece loses about the time of this many tiles
+                                   // (start-up and join, 7 us of a CTA that takes 0.22 us a tile)
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -560,26 +560,45 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
     }
 }
 
-// Joins W partials of one query row in shared memory (partial w: its O at sm_o + w * pitch, m and z in sm_m and
-// sm_l): the sum over them of dimension d, with the row's reference m (-inf: nothing was seen) and its sum z.
+// Joins the W warps' partials of one query row in shared memory (partial w: its O at sm_o + w * pitch, rows kOPitch
+// apart, m and z in sm_m and sm_l): the sum over them of the lane's dimensions 4 lane .. + 3, with the row's
+// reference m (-inf: nothing was seen) and its sum z.
+constexpr int kOPitch = kHeadDim + 4;   // floats; the pad spreads the rows 2t over the banks
 template <int kRows, int W>
-__device__ __forceinline__ float join_row(const float* sm_o, int pitch, const float* sm_m, const float* sm_l, int row,
-                                          int d, float& m, float& z)
+__device__ __forceinline__ float4 join_row(const float* sm_o, int pitch, const float* sm_m, const float* sm_l, int row,
+                                           float& m, float& z)
 {
+    const int lane = threadIdx.x & 31;
     m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < W; ++w) m = fmaxf(m, sm_m[w * kRows + row]);
     z = 0.f;
-    float acc = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const float mw = sm_m[w * kRows + row];
         if (mw == -INFINITY) continue;   // that warp saw nothing
         const float f = fast_exp2(mw - m);
+        const float4 o = *(reinterpret_cast<const float4*>(sm_o + w * pitch + row * kOPitch) + lane);
         z += f * sm_l[w * kRows + row];
-        acc += f * sm_o[w * pitch + row * kHeadDim + d];
+        acc.x += f * o.x;
+        acc.y += f * o.y;
+        acc.z += f * o.z;
+        acc.w += f * o.w;
     }
     return acc;
+}
+
+// Writes one query row's output (the lane's dimensions 4 lane .. + 3) and its lse.
+__device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h, int r, float4 acc, float m, float z)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t to = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
+    const bool none = m == -INFINITY;
+    const float f = p.c.v_mul;
+    reinterpret_cast<float4*>(p.out + to * kHeadDim)[lane] =
+        none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / z * f, acc.y / z * f, acc.z / z * f, acc.w / z * f);
+    if (p.lse && lane == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
 }
 
 // The query rows of one warp and what it has summed for them.
@@ -827,7 +846,7 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
 template <int W>
 struct LineSmem {
     long long scan[W], start;
-    int b, len, lo, share[W], cnt[32 * W];
+    int b, len, lo, cnt[32 * W];
 };
 template <int W, typename Count>
 struct Line {
@@ -845,100 +864,137 @@ struct Line {
     {
     }
 
+    // Parts that a piece of n tiles is cut into (at most n of them).
+    __device__ __forceinline__ int parts(int n) const { return min((int)((float)n * inv) + 1, n); }
+
+    // Chooses how the work is shared from its length (total) and the tiles of every sequence's piece (get(i), i < B):
+    // the lanes try shares of 1 to 2 times the ideal one and agree on the one with the shortest longest part.
+    template <typename Get>
+    __device__ __forceinline__ void choose(int B, const Get& get)
+    {
+        cta = blockIdx.x;
+        const long long pieces = (long long)B * per_seq;
+        const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
+        n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
+        inv = 0.f;
+        if (pieces <= grid) {
+            const float ideal = fmaxf((float)total / (float)grid, (float)(W * kMinTiles));
+            inv = 1.f / (ideal * (1.f + (float)(threadIdx.x & 31) / 32.f));
+            int sum = 0;
+            float longest = 0.f;
+            for (int i = 0; i < B; ++i) {
+                const int n = get(i), k = parts(n);
+                sum += k;
+                longest = fmaxf(longest, __fdividef((float)n, (float)k));
+            }
+            if ((long long)sum * per_seq > grid) longest = INFINITY;
+            float best = longest;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, d));
+            const unsigned who = __ballot_sync(kFull, longest == best);
+            inv = __shfl_sync(kFull, inv, __ffs(who) - 1);
+            if (!(best <= ideal + kSecondPiece)) inv = 0.f;
+        }
+        at = cta;
+        end = cta + 1;
+        if (inv == 0.f) {
+            at = total * cta / n_cta;
+            end = total * (cta + 1) / n_cta;
+        }
+    }
+
     // False: nothing for this CTA.  All threads call it.
     __device__ __forceinline__ bool start(LineSmem<W>& sm)
     {
         constexpr int kThreadsL = 32 * W;
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int B = p.c.B;
-        // Up to as many sequences as threads take one scan; more take one pass for the line's length and a scan
-        // of blocks of them.
-        seq = sequence(p, min(tid, B - 1), blockIdx.x == 0 && tid < B);
-        const bool one_scan = B <= kThreadsL;
-        const int n_first = tid < B ? count(seq) : 0;
-        total = n_first;
-        for (int i = tid + kThreadsL; i < B; i += kThreadsL) total += count(sequence(p, i, blockIdx.x == 0));
+        if (B <= 32) {
+            // every warp finds the CTA's place by itself: lane i holds sequence i
+            seq = sequence(p, min(lane, B - 1), blockIdx.x == 0 && tid < B);
+            const int mine = lane < B ? count(seq) : 0;
+            total = mine;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-        if (lane == 0) sm.scan[warp] = total;
-        if (one_scan) sm.cnt[tid] = n_first;
-        if (tid == 0) sm.b = -1;
-        __syncthreads();
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) total += sm.scan[w];
-        total *= per_seq;
-        cta = blockIdx.x;
-        const long long pieces = (long long)B * per_seq;
-        const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
-        n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
-        share = 0;
-        if (one_scan && pieces <= grid) {
-            // the smallest share of a few (a warp tries one) whose parts are no more than the CTAs
-            const long long ideal = max((long long)((float)total / (float)grid) + 1, (long long)(W * kMinTiles));
-            const int mine = warp == 0 ? 0x7fffffff : (int)min(ideal * (3 + W - warp) / 4, 0x7ffffffell);
-            long long parts = 0;
-            int most = 0;
-            for (int i = lane; i < B; i += 32) {
-                parts += (sm.cnt[i] - 1) / mine + 1;
-                most = max(most, sm.cnt[i]);
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) {
-                parts += __shfl_xor_sync(kFull, parts, d);
-                most = max(most, __shfl_xor_sync(kFull, most, d));
-            }
-            if (lane == 0) sm.share[warp] = warp == 0 ? most : (parts * per_seq <= grid ? mine : 0x7fffffff);
-            __syncthreads();
-            share = sm.share[0];
-#pragma unroll
-            for (int w = 1; w < W; ++w) share = min(share, sm.share[w]);
-            if (share > ideal + kSecondPiece) share = 0;
-        }
-        at = cta;
-        end = cta + 1;
-        if (share == 0) {
-            if (cta >= n_cta) return false;
-            at = total * cta / n_cta;
-            end = total * (cta + 1) / n_cta;
-        }
-        const int per = share == 0 ? 1 : share;   // tiles of one unit of the scan
-        long long before = 0;                     // units (of one piece each) of the sequences before this block
-        for (int b0 = 0; b0 < B; b0 += kThreadsL) {
-            const int i = b0 + tid;
-            if (b0 > 0 && i < B) seq = sequence(p, i, false);
-            const int n = i < B ? ((b0 == 0 ? n_first : count(seq)) - 1) / per + 1 : 0;
+            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+            total *= per_seq;
+            choose(B, [&](int i) { return __shfl_sync(kFull, mine, i); });
+            if (inv == 0.f && cta >= n_cta) return false;
+            const int n = lane < B ? (inv == 0.f ? mine : parts(mine)) : 0;
             long long inc = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const long long o = __shfl_up_sync(kFull, inc, d);
                 if (lane >= d) inc += o;
             }
-            __syncthreads();   // sm.scan is free
-            if (lane == 31) sm.scan[warp] = inc;
-            __syncthreads();
-            long long sum = 0, mine = 0;
+            const long long first = (inc - n) * per_seq;
+            const unsigned who = __ballot_sync(kFull, n > 0 && at >= first && at < first + (long long)n * per_seq);
+            if (who == 0) return false;   // more CTAs than parts
+            b = __ffs(who) - 1;
+            seq_start = __shfl_sync(kFull, first, b);
+            seq.len = __shfl_sync(kFull, seq.len, b);
+            seq.lo = __shfl_sync(kFull, seq.lo, b);
+        } else {
+            // Up to as many sequences as threads take one scan; more take one pass for the line's length and a
+            // scan of blocks of them.
+            seq = sequence(p, min(tid, B - 1), blockIdx.x == 0 && tid < B);
+            const bool one_scan = B <= kThreadsL;
+            const int n_first = tid < B ? count(seq) : 0;
+            total = n_first;
+            for (int i = tid + kThreadsL; i < B; i += kThreadsL) total += count(sequence(p, i, blockIdx.x == 0));
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if (w == warp) mine = sum;
-                sum += sm.scan[w];
-            }
-            const long long first = (before + mine + inc - n) * per_seq;
-            if (n > 0 && at >= first && at < first + (long long)n * per_seq) {
-                sm.b = i;
-                sm.start = first;
-                sm.len = seq.len;
-                sm.lo = seq.lo;
-            }
+            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+            if (lane == 0) sm.scan[warp] = total;
+            sm.cnt[tid] = n_first;
+            if (tid == 0) sm.b = -1;
             __syncthreads();
-            before += sum;
-            if (sm.b >= 0) break;
+            total = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) total += sm.scan[w];
+            total *= per_seq;
+            if (one_scan) {
+                choose(B, [&](int i) { return sm.cnt[i]; });
+            } else {
+                choose(0x7fffffff, [](int) { return 0; });   // (more pieces than CTAs can take one each)
+            }
+            if (inv == 0.f && cta >= n_cta) return false;
+            long long before = 0;   // units (of one piece each) of the sequences before this block
+            for (int b0 = 0; b0 < B; b0 += kThreadsL) {
+                const int i = b0 + tid;
+                if (b0 > 0 && i < B) seq = sequence(p, i, false);
+                const int c = b0 == 0 ? n_first : (i < B ? count(seq) : 0);
+                const int n = i < B ? (inv == 0.f ? c : parts(c)) : 0;
+                long long inc = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const long long o = __shfl_up_sync(kFull, inc, d);
+                    if (lane >= d) inc += o;
+                }
+                __syncthreads();   // sm.scan is free
+                if (lane == 31) sm.scan[warp] = inc;
+                __syncthreads();
+                long long sum = 0, mine = 0;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    if (w == warp) mine = sum;
+                    sum += sm.scan[w];
+                }
+                const long long first = (before + mine + inc - n) * per_seq;
+                if (n > 0 && at >= first && at < first + (long long)n * per_seq) {
+                    sm.b = i;
+                    sm.start = first;
+                    sm.len = seq.len;
+                    sm.lo = seq.lo;
+                }
+                __syncthreads();
+                before += sum;
+                if (sm.b >= 0) break;
+            }
+            b = sm.b;
+            if (b < 0) return false;   // more CTAs than parts
+            seq_start = sm.start;
+            seq.len = sm.len;
+            seq.lo = sm.lo;
         }
-        b = sm.b;
-        if (b < 0) return false;   // more CTAs than parts
-        seq_start = sm.start;
-        seq.len = sm.len;
-        seq.lo = sm.lo;
         seq.table = p.c.table + (int64_t)b * p.c.table_stride;
         ntile = count(seq);
         slot = cta * 2;
@@ -949,7 +1005,7 @@ struct Line {
     __device__ __forceinline__ bool next()
     {
         if (at >= end) return false;
-        if (share == 0) {
+        if (inv == 0.f) {
             while (at >= seq_start + (long long)ntile * per_seq) {
                 seq_start += (long long)ntile * per_seq;
                 seq = sequence(p, ++b, false);
@@ -967,7 +1023,7 @@ struct Line {
             slot = cta * 2 + (at == total * cta / n_cta ? 0 : 1);
             at = from + s1;
         } else {
-            n_part = (ntile - 1) / share + 1;
+            n_part = parts(ntile);
             piece = (int)((at - seq_start) / n_part);
             const int part = (int)(at - seq_start) - piece * n_part;
             s0 = (int)((long long)ntile * part / n_part);
@@ -980,7 +1036,8 @@ struct Line {
     }
 
 private:
-    int cta, n_cta, share;     // share: tiles of a part where every CTA takes one part of one piece; 0: stretches
+    int cta, n_cta;
+    float inv;                 // 1 / tiles of a part where every CTA takes one part of one piece; 0: stretches
     long long total, at, end;  // length of the line (tiles), next place and end of this CTA's (tiles, or parts)
     long long seq_start;       // place where the sequence starts
 };
@@ -1001,13 +1058,13 @@ template <bool E2M1, int NT, bool DUP>
 struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
     static constexpr int kWarps = 4;                     // few, so that other CTAs of the SM work while one starts or joins
-    static constexpr int kCtas = E2M1 ? (NT == 1 ? 4 : 3) : 2;   // per SM
+    static constexpr int kCtas = E2M1 && NT == 1 ? 3 : 2;       // per SM
     static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
     static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
     using Unit = Slot<E2M1, true, kUnit>;
     static constexpr int kRing = kStages * Unit::kBytes;   // bytes of a warp; its partial O later takes them
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
-    static_assert(kRows * kHeadDim * 4 <= kRing, "a warp's partial O lies in its ring");
+    static_assert(kRows * kOPitch * 4 <= kRing, "a warp's partial O lies in its ring");
 };
 
 // Decode.  A CTA's warps take a stretch each of its tiles of a piece and meet in shared memory; a piece that several
@@ -1020,7 +1077,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     paged_decode_kernel(const PagedAttnParams p)
 {
     using S = Shape<E2M1, NT, DUP>;
-    constexpr int kRows = S::kRows, W = S::kWarps, kThreadsA = 32 * W, kStages = S::kStages, U = S::kUnit, kSlot = S::Unit::kBytes;
+    constexpr int kRows = S::kRows, W = S::kWarps, kStages = S::kStages, U = S::kUnit, kSlot = S::Unit::kBytes;
     constexpr int kPitch = S::kRing / 4;   // floats between the warps' partial O
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
@@ -1055,21 +1112,6 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         // start at multiples of 32); the ring's first units go on their way, then each turn feeds the unit
         // kStages - 1 turns ahead
         Feeder<E2M1, true, U> feeder(p, seq, h, warp_start<U, W>(seq, s0, s1, warp), warp_start<U, W>(seq, s0, s1, warp + 1));
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float f = make_query<E2M1>(a.q[n]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                a.rs[n][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
-                a.bias[n][e] = INFINITY;
-                a.l[n][e] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
-        }
-
         uint32_t flags[kStages];   // of the units in the ring, oldest first
 #pragma unroll
         for (int k = 0; k < kStages; ++k) flags[k] = 1u << U;
@@ -1078,7 +1120,23 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             if (turn >= 0) cp_async_wait_stages<kStages - 1>();   // this lane's copies; the barrier covers the others'
             __syncwarp();
             flags[kStages - 1] = feeder.feed(into);
-            if (turn == -1) slot = ring;
+            if (turn == -1) {   // the first units are on their way
+                slot = ring;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float f = make_query<E2M1>(a.q[n]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a.rs[n][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
+                        a.bias[n][e] = INFINITY;
+                        a.l[n][e] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
+                }
+            }
             if (turn >= 0) {
                 const uint32_t edge = flags[0] & ((1u << U) - 1);
                 if (edge == 0) {
@@ -1120,23 +1178,35 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 #pragma unroll
                     for (int e = 0; e < 4; ++e) a.o[n][i][e] += __shfl_xor_sync(kFull, a.o[n][i][e], 2);
                 }
-                if (!DUP || t < 2) {
+                if (!E2M1) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sm_o[warp * kPitch + (8 * n + 2 * t + (e & 1)) * kHeadDim + v_dim<E2M1>(i, g, e >> 1)] = a.o[n][i][e];
+                        if (!DUP || t < 2)
+                            sm_o[warp * kPitch + (8 * n + 2 * t + (e & 1)) * kOPitch + v_dim<E2M1>(i, g, e >> 1)] = a.o[n][i][e];
+                } else if ((i & 1) && (!DUP || t < 2)) {   // M tiles i - 1, i: four neighbouring dimensions
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float4*>(sm_o + warp * kPitch + (8 * n + 2 * t + e) * kOPitch + v_dim<E2M1>(i - 1, g, 0)) =
+                            make_float4(a.o[n][i - 1][e], a.o[n][i - 1][e + 2], a.o[n][i][e], a.o[n][i][e + 2]);
                 }
             }
         __syncthreads();
 
-        if (n_part > 1) {
-            // this CTA's part of the piece goes to its slot; the last CTA to arrive takes all of them over
+        if (n_part == 1) {
+            for (int row = warp; row < kRows && r0 + row < p.R; row += W) {
+                float z, m;
+                const float4 acc = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, m, z);
+                write_row(p, b, h, r0 + row, acc, m, z);
+            }
+        } else {
+            // this CTA's part of the piece goes to its slot; the last CTA to arrive joins all of them
             constexpr int kPart = kRows * (kHeadDim + 2);
             float* part = p.part + (size_t)line.slot * kPart;
-            const int d = tid & (kHeadDim - 1);
-            for (int row = tid / kHeadDim; row < kRows; row += kThreadsA / kHeadDim) {
+#pragma unroll
+            for (int row = warp; row < kRows; row += W) {
                 float z, m;
-                part[row * kHeadDim + d] = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, d, m, z);
-                if (d == 0) {
+                reinterpret_cast<float4*>(part + row * kHeadDim)[lane] = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, m, z);
+                if (lane == 0) {
                     part[kRows * kHeadDim + row] = m;
                     part[kRows * kHeadDim + kRows + row] = z;
                 }
@@ -1152,81 +1222,58 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             }
             __syncthreads();
             if (sm_last) {
-                // all references and sums come to shared memory in one go, then kSplit warps take each row
-                const int n = n_part;
-                float* sm_pm = smem;
-                float* sm_pl = smem + n * kRows;
-                for (int i = tid; i < n * kRows; i += kThreadsA) {
-                    const int c = i / kRows;
-                    const float* from = p.part + (size_t)(c == 0 ? line.slot0 : (line.c0 + c) * 2) * kPart + kRows * kHeadDim + i % kRows;
-                    sm_pm[i] = __ldcg(from);
-                    sm_pl[i] = __ldcg(from + kRows);
+                // a warp takes every W-th row; 32 parts at a time, whose references and sums the lanes hold
+                constexpr int kMine = kRows / W;   // rows of a warp
+                float m[kMine], z[kMine];
+                float4 acc[kMine];
+#pragma unroll
+                for (int k = 0; k < kMine; ++k) {
+                    m[k] = -INFINITY;
+                    z[k] = 0.f;
+                    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
-                __syncthreads();
-                constexpr int kSplit = W / kRows > 0 ? W / kRows : 1;
-                float4* sm_acc = reinterpret_cast<float4*>(smem + ((2 * n * kRows + 3) & ~3));   // [row][32]
-                for (int row0 = 0; row0 < kRows; row0 += W / kSplit) {
-                    const int row = row0 + warp / kSplit, part0 = warp % kSplit;
-                    const bool live = row < kRows && r0 + row < p.R;
-                    float m = -INFINITY, z = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (live) {
-                        for (int c = lane; c < n; c += 32) m = fmaxf(m, sm_pm[c * kRows + row]);
+                for (int c1 = 0; c1 < n_part; c1 += 32) {
+                    const int mine = c1 + lane;
+                    const float* ref = p.part + (size_t)(mine == 0 ? line.slot0 : (line.c0 + mine) * 2) * kPart + kRows * kHeadDim;
+                    float f[kMine];
 #pragma unroll
-                        for (int d2 = 16; d2; d2 >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d2));
-                        for (int c = lane; c < n; c += 32) {
-                            const float mc = sm_pm[c * kRows + row];
-                            if (mc != -INFINITY) z += fast_exp2(mc - m) * sm_pl[c * kRows + row];
-                        }
+                    for (int k = 0; k < kMine; ++k) {
+                        const int row = warp + k * W;
+                        const float mp = mine < n_part ? __ldcg(ref + row) : -INFINITY;
+                        const float zp = mine < n_part ? __ldcg(ref + kRows + row) : 0.f;
+                        float mx = mp;
 #pragma unroll
-                        for (int d2 = 16; d2; d2 >>= 1) z += __shfl_xor_sync(kFull, z, d2);
-#pragma unroll 8
-                        for (int c = part0; c < n; c += kSplit) {
-                            const float* from = p.part + (size_t)(c == 0 ? line.slot0 : (line.c0 + c) * 2) * kPart + row * kHeadDim;
-                            const float4 o = __ldcg(reinterpret_cast<const float4*>(from) + lane);
-                            const float mc = sm_pm[c * kRows + row];
-                            const float f = mc == -INFINITY ? 0.f : fast_exp2(mc - m);
-                            acc.x += f * o.x;
-                            acc.y += f * o.y;
-                            acc.z += f * o.z;
-                            acc.w += f * o.w;
-                        }
+                        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                        mx = fmaxf(mx, m[k]);
+                        const float old = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - mx);
+                        f[k] = mp == -INFINITY ? 0.f : fast_exp2(mp - mx);
+                        float zs = f[k] * zp;
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) zs += __shfl_xor_sync(kFull, zs, d);
+                        z[k] = z[k] * old + zs;
+                        acc[k] = make_float4(acc[k].x * old, acc[k].y * old, acc[k].z * old, acc[k].w * old);
+                        m[k] = mx;
                     }
-                    if (kSplit > 1) {   // (kSplit is 1 or 2)
-                        if (live && part0 == 1) sm_acc[row * 32 + lane] = acc;
-                        __syncthreads();
-                        if (live && part0 == 0) {
-                            const float4 o = sm_acc[row * 32 + lane];
-                            acc.x += o.x;
-                            acc.y += o.y;
-                            acc.z += o.z;
-                            acc.w += o.w;
+                    const int n = min(32, n_part - c1);
+#pragma unroll 4
+                    for (int c = 0; c < n; ++c) {
+                        const int at = c1 + c;
+                        const float* from = p.part + (size_t)(at == 0 ? line.slot0 : (line.c0 + at) * 2) * kPart;
+#pragma unroll
+                        for (int k = 0; k < kMine; ++k) {
+                            const float4 o = __ldcg(reinterpret_cast<const float4*>(from + (warp + k * W) * kHeadDim) + lane);
+                            const float w = __shfl_sync(kFull, f[k], c);
+                            acc[k].x += w * o.x;
+                            acc[k].y += w * o.y;
+                            acc[k].z += w * o.z;
+                            acc[k].w += w * o.w;
                         }
-                    }
-                    if (live && part0 == 0) {
-                        const int r = r0 + row;
-                        const int64_t to = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
-                        const bool none = m == -INFINITY;
-                        const float f = p.c.v_mul;
-                        reinterpret_cast<float4*>(p.out + to * kHeadDim)[lane] =
-                            none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                 : make_float4(acc.x / z * f, acc.y / z * f, acc.z / z * f, acc.w / z * f);
-                        if (p.lse && lane == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+                    if (r0 + warp + k * W < p.R) write_row(p, b, h, r0 + warp + k * W, acc[k], m[k], z[k]);
             }
-            __syncthreads();   // shared memory is free for the next piece
-            continue;
-        }
-        const int d = tid & (kHeadDim - 1);
-        for (int row = tid / kHeadDim; row < kRows && r0 + row < p.R; row += kThreadsA / kHeadDim) {
-            float z, m;
-            const float acc = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, d, m, z);
-            const int r = r0 + row;
-            const int64_t to = ((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq;
-            const bool none = m == -INFINITY;
-            p.out[to * kHeadDim + d] = none ? 0.f : acc / z * p.c.v_mul;
-            if (p.lse && d == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
         }
         __syncthreads();   // shared memory is free for the next piece
     }
@@ -1400,7 +1447,7 @@ cudaError_t launch_importance(const PagedAttnParams& p, int sm_count, bool pdl, 
 // The counters' region, then two partials (one of each end of a CTA's stretch) per CTA.
 size_t paged_decode_workspace_bytes(int R, int sm_count)
 {
-    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16), ctas = (size_t)(R <= 8 ? 4 : 3) * sm_count;
+    const size_t rows = R <= 4 ? 4 : (R <= 8 ? 8 : 16), ctas = (size_t)(R <= 8 ? 3 : 2) * sm_count;
     return kCounterBytes + ctas * 2 * rows * (kHeadDim + 2) * sizeof(float);
 }
 
