@@ -1092,6 +1092,7 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
     p->G = Hq / cache->Hkv;
     p->Mq = Mq;
     p->R = p->G * Mq;
+    p->mq_inv = 65536 / Mq + 1;
     p->qscale = log2e_scale(scale) * p->c.k_mul;
     return FX_OK;
 }

@@ -265,6 +265,7 @@ struct PagedAttnParams {
     const uint16_t* q;
     int64_t q_b, q_h, q_i;
     int Hq, G, Mq, R;
+    int mq_inv;               // 65536 / Mq + 1: r / Mq = (r * mq_inv) >> 16 for r < 64
     const int32_t* idx;
     int kk;
     const int32_t* tail_lo;

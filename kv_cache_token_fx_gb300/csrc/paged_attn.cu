@@ -384,43 +384,55 @@ struct Feeder {
     }
 };
 
-// Calls f(j, a0, a1, a2, a3) with the A fragments of the eight 16-dimension steps of S^T = K Q^T.
-template <typename S, bool E2M1, typename F>
-__device__ __forceinline__ void k_steps(uint32_t slot, int u, F&& f)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if constexpr (E2M1) {
+// A tile's K rows: pair(j) gives the A fragments of the 16-dimension steps 2j and 2j + 1 of S^T = K Q^T.
+template <bool E2M1>
+struct KTile;
+template <>
+struct KTile<true> {
+    uint32_t w[2][4];    // 32 dimensions from 32t on of rows g and g + 8
+    uint32_t sc[2][2];   // [row][block of 16 of them]: the scale, twice
+
+    template <typename S>
+    __device__ __forceinline__ void load(uint32_t slot, int u)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const uint32_t at = slot + u * S::kTile + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (2 * ((g >> 1) & 3))) << 4);
-        const uint4 x0 = lds128(at), x1 = lds128(at + 512);
         const uint32_t sa = slot + S::kScale + u * 128 + 8 * g + 2 * t;
-        const uint32_t s0 = e4m3x2_to_f16x2(lds16(sa)), s1 = e4m3x2_to_f16x2(lds16(sa + 64));
-        const uint32_t sc[2][2] = {{__byte_perm(s0, 0, 0x1010), __byte_perm(s0, 0, 0x3232)},
-                                   {__byte_perm(s1, 0, 0x1010), __byte_perm(s1, 0, 0x3232)}};
-        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
-        const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t a[4], b[4];
-            e2m1x8_to_f16(w0[j], a[0], a[1], a[2], a[3]);
-            e2m1x8_to_f16(w1[j], b[0], b[1], b[2], b[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = hmul2_u32(a[i], sc[0][j >> 1]);
-                b[i] = hmul2_u32(b[i], sc[1][j >> 1]);
-            }
-            f(2 * j, a[0], b[0], a[1], b[1]);
-            f(2 * j + 1, a[2], b[2], a[3], b[3]);
-        }
-    } else {
-        const int row = lane & 15;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4(slot + u * S::kTile + kv_off(row, 2 * j + (lane >> 4)), a0, a1, a2, a3);
-            f(j, a0, a1, a2, a3);
+        for (int r = 0; r < 2; ++r) {
+            const uint4 x = lds128(at + 512 * r);
+            w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
+            const uint32_t z = e4m3x2_to_f16x2(lds16(sa + 64 * r));
+            sc[r][0] = __byte_perm(z, 0, 0x1010);
+            sc[r][1] = __byte_perm(z, 0, 0x3232);
         }
     }
-}
+    __device__ __forceinline__ void pair(int j, uint32_t (&x)[2][4]) const
+    {
+        uint32_t a[4], b[4];
+        e2m1x8_to_f16(w[0][j], a[0], a[1], a[2], a[3]);
+        e2m1x8_to_f16(w[1][j], b[0], b[1], b[2], b[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i >> 1][2 * (i & 1)] = hmul2_u32(a[i], sc[0][j >> 1]);
+            x[i >> 1][2 * (i & 1) + 1] = hmul2_u32(b[i], sc[1][j >> 1]);
+        }
+    }
+};
+template <>
+struct KTile<false> {
+    uint32_t at;
+
+    template <typename S>
+    __device__ __forceinline__ void load(uint32_t slot, int u) { at = slot + u * S::kTile; }
+    __device__ __forceinline__ void pair(int j, uint32_t (&x)[2][4]) const
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            ldsm_x4(at + kv_off(lane & 15, 2 * (2 * j + i) + (lane >> 4)), x[i][0], x[i][1], x[i][2], x[i][3]);
+    }
+};
 
 // A tile's V rows: get(i) gives the A fragment of M tile i of O^T += V^T P^T.  MASKED: rows outside `vm` count as
 // zero, whatever they hold.
@@ -604,7 +616,9 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h
 // The query rows of one warp and what it has summed for them.
 template <bool E2M1, int NT, bool DUP>
 struct Acc {
-    uint32_t q[NT][16];   // B fragments: registers 2j, 2j + 1 of step j
+    static constexpr bool kSharedQ = NT > 1;   // the queries' fragments lie in shared memory (16 registers an N tile)
+    uint32_t q[kSharedQ ? 1 : NT][16];         // B fragments: registers 2j, 2j + 1 of step j
+    uint32_t sq;                               // or the lane's place in [N tile][pair of steps][32] of 16 bytes
     float rs[NT][2];      // factor of the logits of rows 2t, 2t+1 (of each N tile)
     float bias[NT][2];    // minus the reference of those rows; +inf: none yet
     float l[NT][2];
@@ -612,13 +626,12 @@ struct Acc {
 };
 
 // Weights of U tiles from their logits s[u * NT + n][e] (row g + 8 (e >> 1) of tile u, query row 2t + (e & 1) of
-// N tile n), in place; moves the references when one would not fit.  With HIDE (one tile), bit 4n + e of hide:
+// N tile n), in place; moves the references when one would not fit.  With HIDE, bit 4 (u * NT + n) + e of hide:
 // that logit does not count.
 template <bool HIDE, int U, bool E2M1, int NT, bool DUP>
 __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT][4], uint32_t hide)
 {
-    static_assert(!HIDE || U == 1, "");
-    auto hidden = [&](int n, int e) { return HIDE && ((hide >> (4 * n + e)) & 1u) != 0; };
+    auto hidden = [&](int m, int e) { return HIDE && ((hide >> (4 * m + e)) & 1u) != 0; };
     float x2[U * NT][4];
     bool over = false;
 #pragma unroll
@@ -639,7 +652,7 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int z = e; z < 4; z += 2)
-                        if (!hidden(n, z)) m = fmaxf(m, s[u * NT + n][z] * a.rs[n][e]);
+                        if (!hidden(u * NT + n, z)) m = fmaxf(m, s[u * NT + n][z] * a.rs[n][e]);
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
@@ -658,7 +671,7 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int z = e; z < 4; z += 2)
-                        x2[u * NT + n][z] = hidden(n, z) ? -INFINITY : fmaf(s[u * NT + n][z], a.rs[n][e], nb);
+                        x2[u * NT + n][z] = hidden(u * NT + n, z) ? -INFINITY : fmaf(s[u * NT + n][z], a.rs[n][e], nb);
             }
     }
 #pragma unroll
@@ -677,24 +690,44 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
         }
 }
 
-// Logits of a tile: s[n][e] of row g + 8 (e >> 1) and query row 2t + (e & 1) of N tile n.
-template <typename S, bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slot, int u, float (&s)[NT][4])
+// Logits of U tiles from tile u0 of a slot on: s[u * NT + n][e] of row g + 8 (e >> 1) and query row 2t + (e & 1) of
+// N tile n.
+template <int U, typename S, bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slot, int u0, float (&s)[U * NT][4])
 {
-    float s2[NT][2][4];   // two chains of products, for their latency
-    k_steps<S, E2M1>(slot, u, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    float s2[U * NT][2][4];   // two chains of products, for their latency
+    KTile<E2M1> k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) k[u].template load<S>(slot, u0 + u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t x[U][2][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) k[u].pair(j, x[u]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (j < 2)
-                mma16_zero<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][2 * j], a.q[n][2 * j + 1]);
+            uint4 q;
+            if (Acc<E2M1, NT, DUP>::kSharedQ)
+                q = lds128(a.sq + (n * 4 + j) * 512);
             else
-                mma16<E2M1>(s2[n][j & 1], a0, a1, a2, a3, a.q[n][2 * j], a.q[n][2 * j + 1]);
+                q = make_uint4(a.q[n][4 * j], a.q[n][4 * j + 1], a.q[n][4 * j + 2], a.q[n][4 * j + 3]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float(&c)[2][4] = s2[u * NT + n];
+                if (j == 0) {
+                    mma16_zero<E2M1>(c[0], x[u][0][0], x[u][0][1], x[u][0][2], x[u][0][3], q.x, q.y);
+                    mma16_zero<E2M1>(c[1], x[u][1][0], x[u][1][1], x[u][1][2], x[u][1][3], q.z, q.w);
+                } else {
+                    mma16<E2M1>(c[0], x[u][0][0], x[u][0][1], x[u][0][2], x[u][0][3], q.x, q.y);
+                    mma16<E2M1>(c[1], x[u][1][0], x[u][1][1], x[u][1][2], x[u][1][3], q.z, q.w);
+                }
+            }
         }
-    });
+    }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < U * NT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][0][e] + s2[n][1][e];
+        for (int e = 0; e < 4; ++e) s[m][e] = s2[m][0][e] + s2[m][1][e];
 }
 
 // A tile's weights as B fragments: two 16-bit parts (with DUP the low part sits in columns 4..7 of the first).
@@ -730,31 +763,55 @@ __device__ __forceinline__ void term(float (&c)[4], const Weights<NT>& w, int n,
     if (!DUP) mma16<E2M1>(c, v[0], v[1], v[2], v[3], w.lo[n][0], w.lo[n][1]);
 }
 
-// U tiles whose rows all count for every query.
+// r % Mq of a query row (r < 64).
+__device__ __forceinline__ int query_pos(const PagedAttnParams& p, int r) { return r - ((r * p.mq_inv) >> 16) * p.Mq; }
+
+// A unit of U tiles.  EDGE: the tiles whose bit is set in `edge` (tile u: bit U - 1 - u) have rows that do not count
+// for every query: not valid, or past what some query sees.  Rows that are not valid may hold anything, and 0 *
+// NaN is NaN: their V counts as zeros.
 //
 // O^T += V^T P^T: the tiles' product starts from zero and is added to O by an fp32 addition.  The tensor core
 // aligns all products to the accumulator and cuts them off (2^-23 of it): accumulated over a long row that costs
 // small weights beside a large one, and drifts.
-template <int U, typename S, bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void attend(Acc<E2M1, NT, DUP>& a, uint32_t slot)
+template <int U, bool EDGE, typename S, bool E2M1, int NT, bool DUP>
+__device__ __forceinline__ void attend(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, uint32_t edge, int r0,
+                                       int seen)
 {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float s[U * NT][4];
+    logits<U, S, E2M1, NT, DUP>(a, slot, 0, s);
+    uint32_t hide = 0, vm[U];
+    if (EDGE) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) logits<S, E2M1, NT, DUP>(a, slot, u, reinterpret_cast<float(&)[NT][4]>(s[u * NT]));
-    weights<false, U, E2M1, NT, DUP>(a, s, 0);
+        for (int u = 0; u < U; ++u) {
+            int pos = 0;   // of a whole tile: seen by all
+            if ((edge >> (U - 1 - u)) & 1u) pos = (int)lds32(slot + S::kPos + 64 * u + 4 * (lane & 15));
+            vm[u] = __ballot_sync(kFull, pos >= 0) & 0xffffu;   // the valid rows
+            const int p0 = __shfl_sync(kFull, pos, g), p1 = __shfl_sync(kFull, pos, g + 8);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = e >> 1 ? p1 : p0;
+                    const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
+                    if (at < 0 || at > seen + query_pos(p, r)) hide |= 1u << (4 * (u * NT + n) + e);
+                }
+        }
+    }
+    weights<EDGE, U, E2M1, NT, DUP>(a, s, hide);
     Weights<NT> w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) fragments<E2M1, NT, DUP>(reinterpret_cast<float(&)[NT][4]>(s[u * NT]), w[u]);
     VTile<E2M1> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u].template load<false, S>(slot, u, 0);
+    for (int u = 0; u < U; ++u) v[u].template load<EDGE, S>(slot, u, EDGE ? vm[u] : 0u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float c[NT][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             uint32_t x[4];
-            v[u].template get<false>(i, x);
+            v[u].template get<EDGE>(i, x);
 #pragma unroll
             for (int n = 0; n < NT; ++n) term<E2M1, NT, DUP>(c[n], w[u], n, x, u == 0);
         }
@@ -765,11 +822,33 @@ __device__ __forceinline__ void attend(Acc<E2M1, NT, DUP>& a, uint32_t slot)
     }
 }
 
-// A tile with rows that do not count for every query (not valid, or past what some query sees), or a whole one
-// beside such a tile.
+// Whether a row of tile u past what query 0 sees holds an infinity or a NaN in V.
+template <typename S, bool E2M1>
+__device__ __forceinline__ bool late_not_finite(uint32_t slot, int u, int seen)
+{
+    const int lane = threadIdx.x & 31;
+    const int pos = (int)lds32(slot + S::kPos + 64 * u + 4 * (lane & 15));
+    if (!__any_sync(kFull, pos > seen)) return false;
+    bool bad = false;
+    if (E2M1) {   // a NaN scale (the lane looks at half the scales of row lane / 2)
+        const uint32_t z = lds32(slot + S::kScaleV + 128 * u + 4 * lane) & 0x7f7f7f7fu;
+        const int of = __shfl_sync(kFull, pos, lane >> 1);
+        bad = of > seen && __vcmpeq4(z, 0x7f7f7f7fu) != 0;
+    } else {      // an all-ones exponent
+        for (int j = 0; j < 16; ++j) {
+            const uint2 z = lds64(slot + S::kV + u * S::kTile + 256 * j + 8 * lane);
+            const uint32_t x = __vcmpeq2(z.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(z.y & 0x7f807f80u, 0x7f807f80u);
+            bad |= __shfl_sync(kFull, pos, j) > seen && x != 0;
+        }
+    }
+    return __any_sync(kFull, bad);
+}
+
+// A tile where rows that only later queries see hold an infinity or a NaN: one product per query position, over
+// the rows that it sees, taken by its query rows alone.  whole: a tile without an edge beside such a one.
 template <typename S, bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int u, int r0,
-                                            int seen, bool whole)
+__device__ __forceinline__ void attend_apart(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int u, int r0,
+                                             int seen, bool whole)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int pos = 0;   // of a whole tile: seen by all
@@ -777,7 +856,7 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
     const uint32_t vm = __ballot_sync(kFull, pos >= 0) & 0xffffu;   // the valid rows
     if (vm == 0) return;
     float s[NT][4];
-    logits<S, E2M1, NT, DUP>(a, slot, u, s);
+    logits<1, S, E2M1, NT, DUP>(a, slot, u, s);
     uint32_t hide = 0;
     const int p0 = __shfl_sync(kFull, pos, g), p1 = __shfl_sync(kFull, pos, g + 8);
 #pragma unroll
@@ -786,42 +865,21 @@ __device__ __forceinline__ void attend_edge(const PagedAttnParams& p, Acc<E2M1, 
         for (int e = 0; e < 4; ++e) {
             const int r = r0 + 8 * n + (DUP ? (2 * t + (e & 1)) & 3 : 2 * t + (e & 1));
             const int at = e >> 1 ? p1 : p0;
-            if (at < 0 || at > seen + r % p.Mq) hide |= 1u << (4 * n + e);
+            if (at < 0 || at > seen + query_pos(p, r)) hide |= 1u << (4 * n + e);
         }
     weights<true, 1, E2M1, NT, DUP>(a, s, hide);
     Weights<NT> w;
     fragments<E2M1, NT, DUP>(s, w);
-    // Rows that are not valid may hold anything, and 0 * NaN is NaN: they count as zeros.  Rows that only later
-    // queries see do so too where they hold an infinity or a NaN: then there is one product per query position,
-    // over the rows that it sees, taken by its query rows alone.
-    int passes = 1;
-    if (__any_sync(kFull, pos > seen)) {
-        bool bad = false;
-        if (E2M1) {   // a NaN scale (the lane looks at half the scales of row lane / 2)
-            const uint32_t z = lds32(slot + S::kScaleV + 128 * u + 4 * lane) & 0x7f7f7f7fu;
-            const int of = __shfl_sync(kFull, pos, lane >> 1);
-            bad = of > seen && __vcmpeq4(z, 0x7f7f7f7fu) != 0;
-        } else {      // an all-ones exponent
-            for (int j = 0; j < 16; ++j) {
-                const uint2 z = lds64(slot + S::kV + u * S::kTile + 256 * j + 8 * lane);
-                const uint32_t x = __vcmpeq2(z.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(z.y & 0x7f807f80u, 0x7f807f80u);
-                bad |= __shfl_sync(kFull, pos, j) > seen && x != 0;
-            }
-        }
-        if (__any_sync(kFull, bad)) passes = p.Mq;
-    }
-    for (int i = 0; i < passes; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < p.Mq; ++i) {
         uint32_t add = 0;   // bit 2n + e: query row 2t + e of N tile n
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
-                if (passes == 1 || r % p.Mq == i) add |= 1u << (2 * n + e);
-            }
-        const uint32_t vi = passes == 1 ? vm : __ballot_sync(kFull, pos <= seen + i) & vm;
+            for (int e = 0; e < 2; ++e)
+                if (query_pos(p, r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e)) == i) add |= 1u << (2 * n + e);
         VTile<E2M1> v;
-        v.template load<true, S>(slot, u, vi);
+        v.template load<true, S>(slot, u, __ballot_sync(kFull, pos <= seen + i) & vm);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             uint32_t x[4];
@@ -1082,6 +1140,8 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
     __shared__ float sm_m[W * kRows], sm_l[W * kRows];
+    __shared__ uint4 sm_q[NT > 1 ? NT * 128 : 1];   // the queries' fragments, the factors of their logits
+    __shared__ float sm_f[8 * NT];
     __shared__ LineSmem<W> sm_line;
     __shared__ unsigned sm_last;
 
@@ -1103,10 +1163,10 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 
         // the queries, the pages and the first rows are under way together
         Acc<E2M1, NT, DUP> a;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = r0 + 8 * n + (DUP ? g & 3 : g);
-            fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[n]);
+        constexpr bool kSharedQ = Acc<E2M1, NT, DUP>::kSharedQ;
+        if (!kSharedQ || warp < NT) {   // shared: a warp prepares one N tile
+            const int r = r0 + (kSharedQ ? 8 * warp + g : (DUP ? g & 3 : g));
+            fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[0]);
         }
         // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on; pairs
         // start at multiples of 32); the ring's first units go on their way, then each turn feeds the unit
@@ -1122,12 +1182,24 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
             flags[kStages - 1] = feeder.feed(into);
             if (turn == -1) {   // the first units are on their way
                 slot = ring;
+                if (!kSharedQ || warp < NT) {
+                    const float f = make_query<E2M1>(a.q[0]);
+                    if (kSharedQ) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            sm_q[(warp * 4 + j) * 32 + lane] = make_uint4(a.q[0][4 * j], a.q[0][4 * j + 1], a.q[0][4 * j + 2], a.q[0][4 * j + 3]);
+                        if (t == 0) sm_f[8 * warp + g] = f;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) a.rs[0][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
+                    }
+                }
+                if (kSharedQ) __syncthreads();   // (every warp comes here: the first turns feed, tiles or not)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float f = make_query<E2M1>(a.q[n]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        a.rs[n][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
+                        if (kSharedQ) a.rs[n][e] = p.qscale * sm_f[8 * n + 2 * t + e];
                         a.bias[n][e] = INFINITY;
                         a.l[n][e] = 0.f;
                     }
@@ -1136,15 +1208,24 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 #pragma unroll
                         for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
                 }
+                a.sq = smem_addr(sm_q) + 16 * lane;
             }
             if (turn >= 0) {
                 const uint32_t edge = flags[0] & ((1u << U) - 1);
                 if (edge == 0) {
-                    attend<U, typename S::Unit>(a, slot);
+                    attend<U, false, typename S::Unit>(p, a, slot, 0, r0, seen);
                 } else {
+                    bool apart = false;
 #pragma unroll 1
                     for (int u = 0; u < U; ++u)
-                        attend_edge<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
+                        if ((edge >> (U - 1 - u)) & 1u) apart |= late_not_finite<typename S::Unit, E2M1>(slot, u, seen);
+                    if (!apart) {
+                        attend<U, true, typename S::Unit>(p, a, slot, edge, r0, seen);
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < U; ++u)
+                            attend_apart<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
+                    }
                 }
                 slot = slot + kSlot == ring + S::kRing ? ring : slot + kSlot;
             }
@@ -1338,15 +1419,14 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
             row0 = base + feeder.it * kTileRows;
             const uint32_t next = slot == ring ? ring + S::kBytes : ring;
             flags = feeder.feed(next);
-            uint32_t a[U][8][4];
+            uint32_t a[U][4][2][4];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                k_steps<S, E2M1>(slot, u, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                    a[u][j][0] = a0;
-                    a[u][j][1] = a1;
-                    a[u][j][2] = a2;
-                    a[u][j][3] = a3;
-                });
+            for (int u = 0; u < U; ++u) {
+                KTile<E2M1> k;
+                k.template load<S>(slot, u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k.pair(j, a[u][j]);
+            }
             int pos[U][2];   // of the tile's rows g, g + 8
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -1365,7 +1445,7 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                     const uint4 q = sq[(n * 4 + j) * 32 + lane];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const uint32_t(&x)[4] = a[u][2 * j], (&y)[4] = a[u][2 * j + 1];
+                        const uint32_t(&x)[4] = a[u][j][0], (&y)[4] = a[u][j][1];
                         if (j == 0) {
                             mma16_zero<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
                             mma16_zero<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
@@ -1383,7 +1463,7 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                         float x = fmaf(s[u][0][e] + s[u][1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
                         if (edges != 0) {
                             const int row = pos[u][e >> 1];
-                            if (row < 0 || row > seen + (8 * n + 2 * t + (e & 1)) % p.Mq) x = -INFINITY;
+                            if (row < 0 || row > seen + query_pos(p, 8 * n + 2 * t + (e & 1))) x = -INFINITY;
                         }
                         sum[u][e >> 1] += fast_exp2(x);
                     }
