@@ -473,7 +473,7 @@ typedef struct {
  *            value outside [0, B) sets FX_DEVERR_INDEX, pos[i] outside [0, max_pages*page_rows)
  *            FX_DEVERR_LEN, a rotation position outside [0, n_pos) FX_DEVERR_INDEX: that token is skipped,
  *            its q_out rows included.  A bad page (FX_DEVERR_PAGE) skips the K and V rows only.
- *   cos_sin  fp32 [n_pos, rot], 16-byte aligned; rot is 0 or a multiple of 16 up to 128
+ *   cos_sin  fp32 [n_pos, rot], 16-byte aligned; rot is 0, 32, 64, 96 or 128
  * Tokens of one call write distinct rows of the pool (two that name the same row leave a mixture of both).
  * cache->len is not read (lengths stay the caller's) and may be NULL.  No workspace.
  */

@@ -1128,8 +1128,8 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
         if (rows->q == rows->q_out && (rows->q_stride_n != rows->qo_stride_n || rows->q_stride_h != rows->qo_stride_h))
             return fail(FX_ERR_INVALID_ARG, "rows: q_out in the place of q needs the strides of q");
     }
-    if (rows->rot < 0 || rows->rot > kHeadDim || rows->rot % 16 != 0)
-        return fail(FX_ERR_UNSUPPORTED, "rows: rot %d (0 or a multiple of 16 up to 128)", rows->rot);
+    if (rows->rot < 0 || rows->rot > kHeadDim || rows->rot % 32 != 0)
+        return fail(FX_ERR_UNSUPPORTED, "rows: rot %d (0, 32, 64, 96 or 128)", rows->rot);
     if (rows->rot > 0 && (!rows->cos_sin || !aligned16(rows->cos_sin) || rows->n_pos < 1))
         return fail(FX_ERR_INVALID_ARG, "rows: rot > 0 needs cos_sin (16-byte aligned) of n_pos >= 1 positions");
     const int Hq = rows->q ? rows->Hq : 0;

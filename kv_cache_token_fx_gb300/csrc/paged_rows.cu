@@ -2,8 +2,7 @@
 // format, the quantisation) on the way, and the gather back to contiguous bf16 rows.
 //
 // Both move rows of 128 values and compute a few operations a value: bytes bound them (a long append or
-// gather), or start-up (a decode step's few rows).  16 lanes take one row, 8 values (16 bytes of bf16, 4 bytes
-// of codes) a lane.
+// gather), or start-up (a decode step's few rows).
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -24,68 +23,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One member of a rotated pair: own * c -+ other * s, every product and the sum rounded to fp32 (no
-// contraction: the plain statement of the rotation then gives the same bits, and a 4-bit code never depends on
-// how a compiler fused it).
-__device__ __forceinline__ float turn(float own, float other, float c, float s, bool second)
-{
-    const float a = __fmul_rn(own, c), b = __fmul_rn(other, s);
-    return second ? __fadd_rn(a, b) : __fsub_rn(a, b);
-}
-
-// Cosines and sines of the lane's 8 dimensions at one position (only c[0..3], s[0..3] when pairs are neighbours).
-struct Turn {
-    float c[8], s[8];
-};
-__device__ __forceinline__ void load_turn(Turn& w, const float* cs, int c, int rot, bool interleaved)
-{
-    const int half = rot >> 1, hc = rot >> 4;
-    const float* at = cs + (interleaved ? 4 * c : 8 * (c >= hc ? c - hc : c));
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(at)), s0 = __ldg(reinterpret_cast<const float4*>(at + half));
-    w.c[0] = c0.x, w.c[1] = c0.y, w.c[2] = c0.z, w.c[3] = c0.w;
-    w.s[0] = s0.x, w.s[1] = s0.y, w.s[2] = s0.z, w.s[3] = s0.w;
-    if (!interleaved) {
-        const float4 c1 = __ldg(reinterpret_cast<const float4*>(at + 4)), s1 = __ldg(reinterpret_cast<const float4*>(at + half + 4));
-        w.c[4] = c1.x, w.c[5] = c1.y, w.c[6] = c1.z, w.c[7] = c1.w;
-        w.s[4] = s1.x, w.s[5] = s1.y, w.s[6] = s1.z, w.s[7] = s1.w;
-    }
-}
-
-// The lane's 8 values of a row, rotated (`on`: this row is).  Lane c of the 16 holds dimensions 8c .. 8c+7.  All
-// 32 lanes call it (the half-split form exchanges values between lanes).
-__device__ __forceinline__ uint4 rotate_chunk(uint4 x, int c, const Turn& w, int rot, bool interleaved, bool on)
-{
-    const int nc = rot >> 3, hc = rot >> 4;   // rotated chunks, chunks of one half
-    uint4 o = x;
-    if (!interleaved) {
-        const int partner = c < hc ? c + hc : (c < nc ? c - hc : c);
-        const int src = (threadIdx.x & 16) | partner;
-        o.x = __shfl_sync(kAll, x.x, src);
-        o.y = __shfl_sync(kAll, x.y, src);
-        o.z = __shfl_sync(kAll, x.z, src);
-        o.w = __shfl_sync(kAll, x.w, src);
-    }
-    if (c >= nc || !on) return x;
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-    const uint32_t os[4] = {o.x, o.y, o.z, o.w};
-    uint32_t r[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float a = bf16_lo(xs[j]), b = bf16_hi(xs[j]);
-        if (interleaved)
-            r[j] = pack_bf16x2(turn(a, b, w.c[j], w.s[j], false), turn(b, a, w.c[j], w.s[j], true));
-        else
-            r[j] = pack_bf16x2(turn(a, bf16_lo(os[j]), w.c[2 * j], w.s[2 * j], c >= hc),
-                               turn(b, bf16_hi(os[j]), w.c[2 * j + 1], w.s[2 * j + 1], c >= hc));
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
+// x' = x c - y s and y' = y c + x s of the pairs in two words of bf16 values, every product and sum rounded to fp32
+// (no contraction: the plain statement of the rotation then gives the same bits, and a 4-bit code never depends
+// on how a compiler fused it).
+__device__ __forceinline__ float turn_first(float x, float y, float c, float s) { return __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s)); }
+__device__ __forceinline__ float turn_second(float x, float y, float c, float s) { return __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s)); }
 
 // fp32 values to the nearest f16 and back.
 __device__ __forceinline__ float2 snap(float x, float y) { return __half22float2(__floats2half2_rn(x, y)); }
 
 // The codes (8 of them, 4 bytes) and the scale byte of the lane's half of a block of 16 values; the two lanes
-// of a block agree on the scale.  All 32 lanes call it.
+// of a block (neighbours) agree on the scale.  All 32 lanes call it.
 //
 // Both quotients, max|y| / 6 and y / scale, are products with a rounded reciprocal: off by less than 2^-22 of
 // themselves.  Their borders fall as in exact arithmetic all the same.  y is m 2^a with m < 256, an e4m3 border
@@ -95,13 +43,11 @@ __device__ __forceinline__ float2 snap(float x, float y) { return __half22float2
 __device__ __forceinline__ uint32_t quantize_chunk(uint4 x, float inv, uint32_t& scale_byte)
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t top = 0;   // largest magnitude as bits (ordered like the magnitudes; NaN above infinity)
+    uint32_t top2 = 0;   // largest magnitudes as bits (ordered like the magnitudes; NaN above infinity)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        top = max(top, (w[j] & 0x7fffu) << 16);
-        top = max(top, w[j] & 0x7fff0000u);
-    }
-    top = max(top, __shfl_xor_sync(kAll, top, 1));
+    for (int j = 0; j < 4; ++j) top2 = __vmaxu2(top2, w[j] & 0x7fff7fffu);
+    top2 = __vmaxu2(top2, __shfl_xor_sync(kAll, top2, 1));
+    const uint32_t top = max(top2 << 16, top2 & 0xffff0000u);
     const bool finite = top < 0x7f800000u;
     const float a = __uint_as_float(top) * inv * (1.f / 6.f);
     scale_byte = e4m3_from_f32(snap(fminf(fmaxf(a, 0.001953125f), 480.f), 0.f).x);   // 2^-9 to 448
@@ -120,82 +66,140 @@ __device__ __forceinline__ uint32_t quantize_chunk(uint4 x, float inv, uint32_t&
     return codes;
 }
 
-// 16 lanes take R rows (K heads, V heads, then query heads) of one token: their loads need neither the token's
-// place nor its position and go out first, and the rows share its cosines and sines.
-template <bool E2M1, int R>
+// 8 lanes take R rows of one token -- K heads, V heads or query heads -- and of each row two chunks of 8 values:
+// chunks c0 and c1, which are the two sides of 8 rotated pairs in the half-split form.  The rows' loads need
+// neither the token's place nor its position and go out first, and the rows share its cosines and sines.
+template <bool E2M1, int R, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreadsRows) paged_append_kernel(const PagedAppendParams p)
 {
     griddep_wait();
     griddep_launch();
-    const int per = 2 * p.c.Hkv + p.Hq;                            // rows of one token
-    const unsigned groups = (per + R - 1) / R;
-    const unsigned u = blockIdx.x * (unsigned)kCopyRows + (threadIdx.x >> 4);
-    const int c = threadIdx.x & 15;
+    const unsigned gk = (p.c.Hkv + R - 1) / R, groups = 2 * gk + (p.Hq + R - 1) / R;   // groups of one token
+    const unsigned u = blockIdx.x * (unsigned)(kThreadsRows / 8) + (threadIdx.x >> 3);
+    const int l = threadIdx.x & 7, half = p.rot >> 1, hc = p.rot >> 4;
     const int i = (int)(u / groups);
-    const int j0 = (int)(u - i * groups) * R;
+    const unsigned in = u - i * groups;
+    const int kind = in < gk ? 0 : (in < 2 * gk ? 1 : 2);          // K, V, queries
+    const int h0 = (int)(in - (kind == 0 ? 0 : (kind == 1 ? gk : 2 * gk))) * R;
+    // (hc is even, so chunk ^ 1 is the same chunk of lane ^ 1: the other half of its block of 16)
+    const int c0 = INTERLEAVED || l < hc ? l : l + hc, c1 = INTERLEAVED || l >= hc ? l + 8 : l + hc;
     bool live = i < p.n;
-    uint4 x[R];
+    const int rows = live ? min(R, (kind == 2 ? p.Hq : p.c.Hkv) - h0) : 0;
+    uint4 x[R][2];
+    {
+        const uint16_t* src = kind == 2 ? p.q + i * p.q_n + h0 * p.q_h : (kind ? p.v : p.k) + i * p.n_stride + h0 * p.h_stride;
+        const int64_t step = kind == 2 ? p.q_h : p.h_stride;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int j = j0 + r;
-        x[r] = make_uint4(0, 0, 0, 0);
-        if (live && j < per) {
-            const uint16_t* src = j >= 2 * p.c.Hkv ? p.q + i * p.q_n + (j - 2 * p.c.Hkv) * p.q_h
-                                                   : (j >= p.c.Hkv ? p.v + i * p.n_stride + (j - p.c.Hkv) * p.h_stride
-                                                                   : p.k + i * p.n_stride + j * p.h_stride);
-            x[r] = *reinterpret_cast<const uint4*>(src + 8 * c);   // q_out may be q: not a read-only load
+        for (int r = 0; r < R; ++r) {
+            x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                x[r][0] = *reinterpret_cast<const uint4*>(src + 8 * c0);   // q_out may be q: not read-only loads
+                x[r][1] = *reinterpret_cast<const uint4*>(src + 8 * c1);
+            }
+            src += step;
         }
     }
-    int seq = -1, pos = 0;
+    int seq = -1, pos = 0, at = 0, page = -1;
     if (live) {
         seq = __ldg(p.seq + i);
         pos = __ldg(p.pos + i);
-        const int t = p.rope_pos ? __ldg(p.rope_pos + i) : pos;
+        at = p.rope_pos ? __ldg(p.rope_pos + i) : pos;
         unsigned bad = 0;
         if (seq < 0 || seq >= p.c.B)
             bad = seq == -1 ? 0u : FX_DEVERR_INDEX;
         else if (pos < 0 || pos >= p.c.cap)
             bad = FX_DEVERR_LEN;
-        else if (p.rot > 0 && (t < 0 || t >= p.n_pos))
+        else if (p.rot > 0 && (at < 0 || at >= p.n_pos))
             bad = FX_DEVERR_INDEX;
         live = seq >= 0 && bad == 0;
-        if (bad && j0 == 0 && c == 0) atomicOr(p.err, bad);
+        if (bad && in == 0 && l == 0) atomicOr(p.err, bad);
+        if (live && kind != 2) page = paged_page(p.c, seq, pos, p.err);
     }
-    int page = -1;
-    if (live && j0 < 2 * p.c.Hkv) page = paged_page(p.c, seq, pos, p.err);
-    if (p.rot > 0) {
-        Turn w = {};
-        const bool turned = live && c < (p.rot >> 3);
-        if (turned) load_turn(w, p.cos_sin + (int64_t)(p.rope_pos ? __ldg(p.rope_pos + i) : pos) * p.rot, c, p.rot, p.interleaved != 0);
+    if (live && kind != 1 && p.rot > 0) {
+        const float* cs = p.cos_sin + (int64_t)at * p.rot;
+        float c[8], s[8];
+        if (!INTERLEAVED) {
+            if (l < hc) {   // pairs (8 l + j, 8 l + j + half)
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int j = j0 + r;
-            const bool is_v = j >= p.c.Hkv && j < 2 * p.c.Hkv;
-            x[r] = rotate_chunk(x[r], c, w, p.rot, p.interleaved != 0, turned && !is_v);
+                for (int j = 0; j < 2; ++j) {
+                    const float4 a = __ldg(reinterpret_cast<const float4*>(cs + 8 * l) + j);
+                    const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + 8 * l) + j);
+                    c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
+                    s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t a[4] = {x[r][0].x, x[r][0].y, x[r][0].z, x[r][0].w};
+                    const uint32_t b[4] = {x[r][1].x, x[r][1].y, x[r][1].z, x[r][1].w};
+                    uint32_t y[4], z[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a0 = bf16_lo(a[j]), a1 = bf16_hi(a[j]), b0 = bf16_lo(b[j]), b1 = bf16_hi(b[j]);
+                        y[j] = pack_bf16x2(turn_first(a0, b0, c[2 * j], s[2 * j]), turn_first(a1, b1, c[2 * j + 1], s[2 * j + 1]));
+                        z[j] = pack_bf16x2(turn_second(a0, b0, c[2 * j], s[2 * j]), turn_second(a1, b1, c[2 * j + 1], s[2 * j + 1]));
+                    }
+                    x[r][0] = make_uint4(y[0], y[1], y[2], y[3]);
+                    x[r][1] = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int chunk = k ? c1 : c0;
+                if (chunk >= 2 * hc) continue;
+                const float4 a = __ldg(reinterpret_cast<const float4*>(cs + 4 * chunk));
+                const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * chunk));
+                c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+                s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t w[4] = {x[r][k].x, x[r][k].y, x[r][k].z, x[r][k].w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        y[j] = pack_bf16x2(turn_first(bf16_lo(w[j]), bf16_hi(w[j]), c[j], s[j]),
+                                           turn_second(bf16_lo(w[j]), bf16_hi(w[j]), c[j], s[j]));
+                    x[r][k] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
         }
     }
     const int64_t row = pos & p.c.page_mask;
+    if (kind == 2 && live) {
+        uint16_t* to = p.q_out + i * p.qo_n + h0 * p.qo_h;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r < rows) {
+                *reinterpret_cast<uint4*>(to + 8 * c0) = x[r][0];
+                *reinterpret_cast<uint4*>(to + 8 * c1) = x[r][1];
+            }
+            to += p.qo_h;
+        }
+    }
+    const bool keep = page >= 0;   // K or V rows with a place in the pool
+    if (!__any_sync(kAll, keep)) return;
+    char* dst = (kind ? p.c.v : p.c.k) + (int64_t)max(page, 0) * p.c.sp + h0 * p.c.sh + row * p.c.st;
+    char* sd = (kind ? p.c.vs : p.c.ks) + (int64_t)max(page, 0) * p.c.ssp + h0 * p.c.ssh + row * p.c.sst;
+    const float inv = kind ? p.c.v_inv : p.c.k_inv;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int j = j0 + r;
-        const bool is_v = j >= p.c.Hkv;
-        const bool keep = page >= 0 && j < 2 * p.c.Hkv;   // a K or V row with a place in the pool
-        if (live && j >= 2 * p.c.Hkv && j < per)
-            *reinterpret_cast<uint4*>(p.q_out + i * p.qo_n + (j - 2 * p.c.Hkv) * p.qo_h + 8 * c) = x[r];
-        const int h = is_v ? j - p.c.Hkv : j;
-        char* dst = (is_v ? p.c.v : p.c.k) + (int64_t)page * p.c.sp + h * p.c.sh + row * p.c.st;
         if (E2M1) {
-            if (!__any_sync(kAll, keep)) continue;
-            uint32_t sb;
-            const uint32_t codes = quantize_chunk(x[r], is_v ? p.c.v_inv : p.c.k_inv, sb);
-            if (keep) {
-                *reinterpret_cast<uint32_t*>(dst + 4 * c) = codes;
-                char* sd = (is_v ? p.c.vs : p.c.ks) + (int64_t)page * p.c.ssp + h * p.c.ssh + row * p.c.sst;
-                if ((c & 1) == 0) sd[c >> 1] = (char)sb;
+            uint32_t b0, b1;
+            const uint32_t z0 = quantize_chunk(x[r][0], inv, b0), z1 = quantize_chunk(x[r][1], inv, b1);
+            if (keep && r < rows) {
+                *reinterpret_cast<uint32_t*>(dst + 4 * c0) = z0;
+                *reinterpret_cast<uint32_t*>(dst + 4 * c1) = z1;
+                if ((l & 1) == 0) {
+                    sd[c0 >> 1] = (char)b0;
+                    sd[c1 >> 1] = (char)b1;
+                }
             }
-        } else if (keep) {
-            *reinterpret_cast<uint4*>(dst + 16 * c) = x[r];
+        } else if (keep && r < rows) {
+            *reinterpret_cast<uint4*>(dst + 16 * c0) = x[r][0];
+            *reinterpret_cast<uint4*>(dst + 16 * c1) = x[r][1];
         }
+        dst += p.c.sh;
+        sd += p.c.ssh;
     }
 }
 
@@ -276,17 +280,17 @@ __global__ void __launch_bounds__(kThreadsRows) paged_gather_kernel(const PagedG
     }
 }
 
-template <bool E2M1>
+template <bool E2M1, bool INTERLEAVED>
 cudaError_t append(const PagedAppendParams& p, bool pdl, cudaStream_t s)
 {
-    // A decode step's few rows: one row each, for the shortest way through.  More than two rounds of the
-    // machine's 16-lane groups: four rows each, for their shared cosines and more loads in flight.
-    const int per = 2 * p.c.Hkv + p.Hq;
-    const bool many = (int64_t)p.n * per > 2 * 152 * 2048 / 16;
-    const int64_t groups = (int64_t)p.n * (many ? (per + 3) / 4 : per);
-    const dim3 grid((unsigned)((groups + kCopyRows - 1) / kCopyRows));
-    return many ? launch_kernel(paged_append_kernel<E2M1, 4>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
-                : launch_kernel(paged_append_kernel<E2M1, 1>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
+    // A decode step's few rows: one row each, for the shortest way through.  More rows than the machine has
+    // groups of 8 lanes: four rows each, for their shared cosines and more loads in flight.
+    const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > 152 * 2048 / 8;
+    const int R = many ? 4 : 1;
+    const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
+    const dim3 grid((unsigned)((groups + kThreadsRows / 8 - 1) / (kThreadsRows / 8)));
+    return many ? launch_kernel(paged_append_kernel<E2M1, 4, INTERLEAVED>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
+                : launch_kernel(paged_append_kernel<E2M1, 1, INTERLEAVED>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
 }
 
 template <bool E2M1>
@@ -303,7 +307,8 @@ cudaError_t gather(const PagedGatherParams& p, bool pdl, cudaStream_t s)
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, bool pdl, cudaStream_t s)
 {
-    return e2m1 ? append<true>(p, pdl, s) : append<false>(p, pdl, s);
+    if (p.interleaved) return e2m1 ? append<true, true>(p, pdl, s) : append<false, true>(p, pdl, s);
+    return e2m1 ? append<true, false>(p, pdl, s) : append<false, false>(p, pdl, s);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, bool pdl, cudaStream_t s)

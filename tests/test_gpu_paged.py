@@ -88,7 +88,9 @@ APPEND = [  # rows added per sequence, Hkv, G, page, rot, interleaved, layout, e
     ([1, 0, 1, 1, 1], 2, 3, 32, 128, True, "gap", (0, 0), True),
     ([37, 5, 16, 0, 1], 3, 2, 16, 96, False, "head", (-3, 2), False),
     ([130, 63], 2, 8, 128, 64, True, "row", (5, -9), True),
-    ([19, 300], 1, 5, 256, 16, False, "gap", (0, 0), False),
+    ([19, 300], 1, 5, 256, 32, False, "gap", (0, 0), False),
+    ([3, 700], 2, 5, 256, 96, True, "head", (0, 0), False),
+    ([900, 1], 5, 1, 64, 128, False, "row", (2, -2), False),
     ([40], 2, 1, 1024, 32, True, "head", (0, 64), False),
 ]
 
@@ -217,7 +219,7 @@ def test_append_and_gather_report_bad_values(fx):
     dev = c.device(fx)
     before = storage(fx, c, dev)
     x = torch.ones(4, 1, D, dtype=torch.bfloat16, device="cuda")
-    cs = cu(table_of(16, 8))
+    cs = cu(table_of(32, 8))
     q_out = torch.zeros_like(x)
 
     def app(seq, pos, at):

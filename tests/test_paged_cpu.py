@@ -70,7 +70,7 @@ def test_append_refusals(lib):
                              (dict(v=520), 1, b"aligned"), (dict(stride_n=4), 1, b"strides"),
                              (dict(q_out=None), 1, b"together"), (dict(q=None), 1, b"together"),
                              (dict(q=1032), 1, b"aligned"), (dict(Hq=0), 1, b"Hq"), (dict(qo_stride_h=12), 1, b"q strides"),
-                             (dict(q_out=1024, qo_stride_n=1024), 1, b"in the place"), (dict(rot=8), 2, b"rot"),
+                             (dict(q_out=1024, qo_stride_n=1024), 1, b"in the place"), (dict(rot=16), 2, b"rot"),
                              (dict(rot=144), 2, b"rot"), (dict(rot=-16), 2, b"rot"), (dict(cos_sin=None), 1, b"cos_sin"),
                              (dict(cos_sin=260), 1, b"cos_sin"), (dict(n_pos=0), 1, b"n_pos"),
                              (dict(Hq=65536), 2, b"rows"), (dict(flags=4), 1, b"flags")):
