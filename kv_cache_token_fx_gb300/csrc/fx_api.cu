@@ -1073,7 +1073,7 @@ fx_status paged_view(const fx_paged_desc* d, bool need_len, PagedCache* c)
 
 // The checks that fx_paged_decode and fx_paged_importance share; fills the queries' part of p.
 fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
-                        int64_t q_stride_i, int Hq, int Mq, float scale, unsigned flags, PagedAttnParams* p)
+                        int64_t q_stride_i, int Hq, int Mq, int k, float scale, unsigned flags, PagedAttnParams* p)
 {
     memset(p, 0, sizeof *p);
     fx_status st = paged_view(cache, true, &p->c);
@@ -1084,6 +1084,10 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
     if (!row_stride_ok(q_stride_b) || !row_stride_ok(q_stride_h) || !row_stride_ok(q_stride_i))
         return fail(FX_ERR_INVALID_ARG, "q strides must be non-negative multiples of 8 elements");
     if (!isfinite(scale)) return fail(FX_ERR_INVALID_ARG, "scale must be finite");
+    // the kernels count the tiles of 16 rows of all (sequence, KV head, 4 or more query rows) in 32 bits
+    const int64_t tiles = p->c.cap / 16 + k / 16 + 2, groups = (int64_t)(Hq / cache->Hkv) * Mq / 4 + 1;
+    if (tiles * cache->B * cache->Hkv >= ((int64_t)1 << 31) / groups)
+        return fail(FX_ERR_UNSUPPORTED, "more than 2^31 tiles of 16 rows over all sequences and heads");
     p->q = q;
     p->q_b = q_stride_b;
     p->q_h = q_stride_h;
@@ -1205,11 +1209,11 @@ fx_status fx_paged_decode(const fx_paged_desc* cache, const fx_bf16* q, int64_t 
 {
     fx::NvtxRange nvtx_range("fx_paged_decode");
     PagedAttnParams p;
-    fx_status st = paged_queries(cache, q, q_stride_b, q_stride_h, q_stride_i, Hq, Mq, scale, flags, &p);
-    if (st != FX_OK) return st;
-    if (!out || !aligned16(out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
     if (k < 0 || (k > 0 && !idx)) return fail(FX_ERR_INVALID_ARG, "need k >= 0 and idx when k > 0");
     if (k > (1 << 30)) return fail(FX_ERR_UNSUPPORTED, "k is at most 2^30");
+    fx_status st = paged_queries(cache, q, q_stride_b, q_stride_h, q_stride_i, Hq, Mq, k, scale, flags, &p);
+    if (st != FX_OK) return st;
+    if (!out || !aligned16(out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
     const size_t need = paged_decode_workspace_bytes(p.R, sm_count_or_default());
     if ((st = check_ws(ws, ws_bytes, need)) != FX_OK) return st;
     DeviceState* ds = nullptr;
@@ -1234,7 +1238,7 @@ fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int6
 {
     fx::NvtxRange nvtx_range("fx_paged_importance");
     PagedAttnParams p;
-    fx_status st = paged_queries(cache, q, q_stride_b, q_stride_h, q_stride_i, Hq, Mq, scale, flags, &p);
+    fx_status st = paged_queries(cache, q, q_stride_b, q_stride_h, q_stride_i, Hq, Mq, 0, scale, flags, &p);
     if (st != FX_OK) return st;
     if (!lse || !scores) return fail(FX_ERR_INVALID_ARG, "lse and scores must be non-NULL");
     if (cand_lo < 0 || cand_hi < cand_lo || cand_hi > p.c.cap)

@@ -903,8 +903,7 @@ __device__ __forceinline__ void attend_apart(const PagedAttnParams& p, Acc<E2M1,
 // leave no CTA with more to do than another.
 template <int W>
 struct LineSmem {
-    long long scan[W], start;
-    int b, len, lo, cnt[32 * W];
+    int scan[W], start, b, len, lo, cnt[32 * W];
 };
 template <int W, typename Count>
 struct Line {
@@ -931,11 +930,13 @@ struct Line {
     __device__ __forceinline__ void choose(int B, const Get& get)
     {
         cta = blockIdx.x;
-        const long long pieces = (long long)B * per_seq;
-        const int grid = (int)min((long long)gridDim.x, kMaxParts * pieces);
-        n_cta = (int)min((long long)grid, max(1ll, total / (W * kMinTiles)));
+        const int most = (int)gridDim.x;
+        const int grid = B >= most || B * per_seq >= most ? most : min(most, kMaxParts * B * per_seq);
+        n_cta = min(grid, max(1, total / (W * kMinTiles)));
+        quota = total / n_cta;
+        extra = total - quota * n_cta;
         inv = 0.f;
-        if (pieces <= grid) {
+        if (B < grid && B * per_seq <= grid) {
             const float ideal = fmaxf((float)total / (float)grid, (float)(W * kMinTiles));
             inv = 1.f / (ideal * (1.f + (float)(threadIdx.x & 31) / 32.f));
             int sum = 0;
@@ -945,7 +946,7 @@ struct Line {
                 sum += k;
                 longest = fmaxf(longest, __fdividef((float)n, (float)k));
             }
-            if ((long long)sum * per_seq > grid) longest = INFINITY;
+            if (sum > grid || sum * per_seq > grid) longest = INFINITY;
             float best = longest;
 #pragma unroll
             for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, d));
@@ -956,9 +957,16 @@ struct Line {
         at = cta;
         end = cta + 1;
         if (inv == 0.f) {
-            at = total * cta / n_cta;
-            end = total * (cta + 1) / n_cta;
+            at = place(cta);
+            end = place(cta + 1);
         }
+    }
+    // Stretches of the line: quota tiles to a CTA, one more to each of the first `extra`.
+    __device__ __forceinline__ int place(int c) const { return quota * c + min(c, extra); }
+    __device__ __forceinline__ int owner(int tile) const
+    {
+        const int big = extra * (quota + 1);
+        return tile < big ? tile / (quota + 1) : extra + (tile - big) / quota;
     }
 
     // False: nothing for this CTA.  All threads call it.
@@ -978,14 +986,14 @@ struct Line {
             choose(B, [&](int i) { return __shfl_sync(kFull, mine, i); });
             if (inv == 0.f && cta >= n_cta) return false;
             const int n = lane < B ? (inv == 0.f ? mine : parts(mine)) : 0;
-            long long inc = n;
+            int inc = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long o = __shfl_up_sync(kFull, inc, d);
+                const int o = __shfl_up_sync(kFull, inc, d);
                 if (lane >= d) inc += o;
             }
-            const long long first = (inc - n) * per_seq;
-            const unsigned who = __ballot_sync(kFull, n > 0 && at >= first && at < first + (long long)n * per_seq);
+            const int first = (inc - n) * per_seq;
+            const unsigned who = __ballot_sync(kFull, n > 0 && at >= first && at < first + n * per_seq);
             if (who == 0) return false;   // more CTAs than parts
             b = __ffs(who) - 1;
             seq_start = __shfl_sync(kFull, first, b);
@@ -1015,29 +1023,29 @@ struct Line {
                 choose(0x7fffffff, [](int) { return 0; });   // (more pieces than CTAs can take one each)
             }
             if (inv == 0.f && cta >= n_cta) return false;
-            long long before = 0;   // units (of one piece each) of the sequences before this block
+            int before = 0;   // units (of one piece each) of the sequences before this block
             for (int b0 = 0; b0 < B; b0 += kThreadsL) {
                 const int i = b0 + tid;
                 if (b0 > 0 && i < B) seq = sequence(p, i, false);
                 const int c = b0 == 0 ? n_first : (i < B ? count(seq) : 0);
                 const int n = i < B ? (inv == 0.f ? c : parts(c)) : 0;
-                long long inc = n;
+                int inc = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
-                    const long long o = __shfl_up_sync(kFull, inc, d);
+                    const int o = __shfl_up_sync(kFull, inc, d);
                     if (lane >= d) inc += o;
                 }
                 __syncthreads();   // sm.scan is free
                 if (lane == 31) sm.scan[warp] = inc;
                 __syncthreads();
-                long long sum = 0, mine = 0;
+                int sum = 0, mine = 0;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     if (w == warp) mine = sum;
                     sum += sm.scan[w];
                 }
-                const long long first = (before + mine + inc - n) * per_seq;
-                if (n > 0 && at >= first && at < first + (long long)n * per_seq) {
+                const int first = (before + mine + inc - n) * per_seq;
+                if (n > 0 && at >= first && at < first + n * per_seq) {
                     sm.b = i;
                     sm.start = first;
                     sm.len = seq.len;
@@ -1064,28 +1072,28 @@ struct Line {
     {
         if (at >= end) return false;
         if (inv == 0.f) {
-            while (at >= seq_start + (long long)ntile * per_seq) {
-                seq_start += (long long)ntile * per_seq;
+            while (at >= seq_start + ntile * per_seq) {
+                seq_start += ntile * per_seq;
                 seq = sequence(p, ++b, false);
                 ntile = count(seq);
             }
-            piece = (int)((at - seq_start) / ntile);
-            const long long from = seq_start + (long long)piece * ntile;
-            s0 = (int)(at - from);
-            s1 = (int)min((long long)ntile, end - from);
-            // CTA of line tile w: floor(((w + 1) n_cta - 1) / total)
-            c0 = (int)(((from + 1) * n_cta - 1) / total);
-            n_part = (int)(((from + ntile) * n_cta - 1) / total) - c0 + 1;
+            piece = (at - seq_start) / ntile;
+            const int from = seq_start + piece * ntile;
+            s0 = at - from;
+            s1 = min(ntile, end - from);
+            c0 = owner(from);
+            n_part = owner(from + ntile - 1) - c0 + 1;
             // a CTA's first piece uses its slot 0; this one is c0's first only if it starts c0's stretch
-            slot0 = c0 * 2 + (total * c0 / n_cta == from ? 0 : 1);
-            slot = cta * 2 + (at == total * cta / n_cta ? 0 : 1);
+            slot0 = c0 * 2 + (place(c0) == from ? 0 : 1);
+            slot = cta * 2 + (at == place(cta) ? 0 : 1);
             at = from + s1;
         } else {
             n_part = parts(ntile);
-            piece = (int)((at - seq_start) / n_part);
-            const int part = (int)(at - seq_start) - piece * n_part;
-            s0 = (int)((long long)ntile * part / n_part);
-            s1 = (int)((long long)ntile * (part + 1) / n_part);
+            piece = (at - seq_start) / n_part;
+            const int part = at - seq_start - piece * n_part;
+            const int least = ntile / n_part, more = ntile - least * n_part;
+            s0 = least * part + min(part, more);
+            s1 = s0 + least + (part < more ? 1 : 0);
             c0 = cta - part;
             slot0 = c0 * 2;
             at = end;
@@ -1094,10 +1102,10 @@ struct Line {
     }
 
 private:
-    int cta, n_cta;
+    int cta, n_cta, quota, extra;
     float inv;                 // 1 / tiles of a part where every CTA takes one part of one piece; 0: stretches
-    long long total, at, end;  // length of the line (tiles), next place and end of this CTA's (tiles, or parts)
-    long long seq_start;       // place where the sequence starts
+    int total, at, end;        // length of the line (tiles), next place and end of this CTA's (tiles, or parts)
+    int seq_start;             // place where the sequence starts
 };
 
 // Start of warp w's stretch of the tiles [s0, s1) of a sequence: nearly equal ones; where tiles are taken in pairs,
@@ -1105,7 +1113,8 @@ private:
 template <int U, int W>
 __device__ __forceinline__ int warp_start(const Seq& q, int s0, int s1, int w)
 {
-    const int x = s0 + (int)((long long)(s1 - s0) * w / W);
+    static_assert((W & (W - 1)) == 0, "");
+    const int x = s0 + (int)((unsigned)((s1 - s0) * w) / W);   // (fewer than 2^28 tiles)
     return w == W ? s1 : (w == 0 || U == 1 || x < q.nl ? x : min(x + (((q.lo >> 4) + x - q.nl) & 1), s1));
 }
 
