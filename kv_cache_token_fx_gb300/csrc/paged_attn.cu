@@ -616,7 +616,8 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h
 // The query rows of one warp and what it has summed for them.
 template <bool E2M1, int NT, bool DUP>
 struct Acc {
-    static constexpr bool kSharedQ = NT > 1;   // the queries' fragments lie in shared memory (16 registers an N tile)
+    static constexpr bool kSharedQ = E2M1 || NT > 1;   // the queries' fragments lie in shared memory (not in 16
+                                                       // registers an N tile)
     uint32_t q[kSharedQ ? 1 : NT][16];         // B fragments: registers 2j, 2j + 1 of step j
     uint32_t sq;                               // or the lane's place in [N tile][pair of steps][32] of 16 bytes
     float rs[NT][2];      // factor of the logits of rows 2t, 2t+1 (of each N tile)
@@ -1148,8 +1149,9 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     constexpr int kPitch = S::kRing / 4;   // floats between the warps' partial O
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
+    constexpr bool kSharedQ = Acc<E2M1, NT, DUP>::kSharedQ;
     __shared__ float sm_m[W * kRows], sm_l[W * kRows];
-    __shared__ uint4 sm_q[NT > 1 ? NT * 128 : 1];   // the queries' fragments, the factors of their logits
+    __shared__ uint4 sm_q[kSharedQ ? NT * 128 : 1];   // the queries' fragments, the factors of their logits
     __shared__ float sm_f[8 * NT];
     __shared__ LineSmem<W> sm_line;
     __shared__ unsigned sm_last;
@@ -1172,7 +1174,6 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 
         // the queries, the pages and the first rows are under way together
         Acc<E2M1, NT, DUP> a;
-        constexpr bool kSharedQ = Acc<E2M1, NT, DUP>::kSharedQ;
         if (!kSharedQ || warp < NT) {   // shared: a warp prepares one N tile
             const int r = r0 + (kSharedQ ? 8 * warp + g : (DUP ? g & 3 : g));
             fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[0]);
