@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         // the queries, the pages and the first rows are under way together
         Acc<E2M1, NT, DUP> a;
         if (!kSharedQ || warp < NT) {   // shared: a warp prepares one N tile
-            const int r = r0 + (kSharedQ ? 8 * warp + g : (DUP ? g & 3 : g));
+            const int r = r0 + (DUP ? g & 3 : (kSharedQ ? 8 * warp + g : g));
             fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, a.q[0]);
         }
         // a warp's share of the tiles is a stretch of them (in one page the next tile is 16 rows further on; pairs
