@@ -2,16 +2,16 @@
 //
 // Work unit of a warp: a tile of 16 cache rows of one (sequence, KV head); two tiles at a time in 4 bits.  Every
 // warp owns a ring of slots in shared memory and fills it with cp.async ahead of its work; no warp waits for
-// another until their results meet.  S^T = K Q^T has the cache rows on M and the query rows on N (mma.sync m16n8k16), O^T += V^T P^T the
-// dimensions on M and the cache rows on K.
+// another until their results meet.  S^T = K Q^T has the cache rows on M and the query rows on N (mma.sync
+// m16n8k16), O^T += V^T P^T the dimensions on M and the cache rows on K.
 //
 // 4-bit rows: a lane's K fragments are 16 bytes of codes of two rows (the dimensions are permuted inside the
 // product, the queries are laid out the same way), its V fragments 8 bytes of four rows (the dimensions of O^T
 // are permuted inside M).  The codes become f16 by cvt.f16x2.e2m1x2, and one multiplication by the block's scale
 // gives the value held, exactly (at most 6 significant bits, between 2^-10 and 2688).  The queries are f16
 // scaled by a power of two per row (largest magnitude in [2^14, 2^15)), so no bit of a bf16 query within 2^-24
-// of its row's largest is lost.  P is split into f16 hi + lo (22 bits); bf16 rows take bf16 queries as they are
-// and P as bf16 hi + lo (17 bits): outputs are fp32, and one 16-bit P would leave them 2^-12 (f16) or 2^-9 off.
+// of its row's largest is lost.  bf16 rows take bf16 queries as they are.  P enters as a sum of 16-bit parts, two
+// f16 or three bf16: outputs are fp32, and one part would leave them 2^-12 (f16) or 2^-9 (bf16) off.
 //
 // Softmax: base-2 logits, one pass.  p = 2^(x - m) with a reference m per row that all lanes of the row share;
 // it is set so that the largest logit so far gives 2^kBase and moves only when a p would exceed 2^kTop, so most
@@ -559,16 +559,24 @@ __device__ __forceinline__ const uint16_t* query_row(const PagedAttnParams& p, i
     return p.q + (int64_t)b * p.q_b + (int64_t)(h * p.G + r / p.Mq) * p.q_h + (int64_t)(r % p.Mq) * p.q_i;
 }
 
+// A pair of weights as a sum of 16-bit parts: two f16 beside 4-bit rows (23 bits: what is dropped is below 2^-23 of a
+// weight, or 2^-25 where a weight is below 2^-3: the largest of a row lies between 2^11 and 2^15), three bf16 beside
+// bf16 rows (all 24 bits; two would leave 17, and outputs 1.8 times as far off as fp32 arithmetic has them).
 template <bool E2M1>
-__device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32_t& lo)
+constexpr int kWeightParts = E2M1 ? 2 : 3;
+template <bool E2M1>
+__device__ __forceinline__ void split_p(float x0, float x1, uint32_t (&part)[kWeightParts<E2M1>])
 {
-    if (E2M1) {
+    if constexpr (E2M1) {
         const __half2 a = __floats2half2_rn(x0, x1);
         const __half2 b = __floats2half2_rn(x0 - __low2float(a), x1 - __high2float(a));
-        hi = *reinterpret_cast<const uint32_t*>(&a);
-        lo = *reinterpret_cast<const uint32_t*>(&b);
+        part[0] = *reinterpret_cast<const uint32_t*>(&a);
+        part[1] = *reinterpret_cast<const uint32_t*>(&b);
     } else {
-        split_bf16(x0, x1, hi, lo);
+        split_bf16(x0, x1, part[0], part[1]);
+        const float r0 = (x0 - __uint_as_float(part[0] << 16)) - __uint_as_float(part[1] << 16);   // exact
+        const float r1 = (x1 - __uint_as_float(part[0] & 0xffff0000u)) - __uint_as_float(part[1] & 0xffff0000u);
+        part[2] = pack_bf16(r0, r1);
     }
 }
 
@@ -679,15 +687,8 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
     for (int m = 0; m < U * NT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float w = fast_exp2(x2[m][e]);
-            if (!E2M1) {
-                // to 17 bits, which the two bf16 parts hold exactly: the sum then counts the weights as
-                // they are multiplied (one weight far above the others comes out as 1)
-                const float c = __fmul_rn(w, 129.f);
-                w = __fsub_rn(c, __fsub_rn(c, w));
-            }
-            s[m][e] = w;
-            a.l[m % NT][e & 1] += w;
+            s[m][e] = fast_exp2(x2[m][e]);
+            a.l[m % NT][e & 1] += s[m][e];
         }
 }
 
@@ -731,37 +732,44 @@ __device__ __forceinline__ void logits(const Acc<E2M1, NT, DUP>& a, uint32_t slo
         for (int e = 0; e < 4; ++e) s[m][e] = s2[m][0][e] + s2[m][1][e];
 }
 
-// A tile's weights as B fragments: two 16-bit parts (with DUP the low part sits in columns 4..7 of the first).
-template <int NT>
+// A tile's weights as B fragments, one for each product that its V takes part in: one for each part of the weights.
+// With DUP a fragment has two parts: one in columns 0..3, the next in columns 4..7.
+template <bool E2M1, int NT, bool DUP>
 struct Weights {
-    uint32_t hi[NT][2], lo[NT][2];
+    static constexpr int kTerms = DUP ? (kWeightParts<E2M1> + 1) / 2 : kWeightParts<E2M1>;
+    uint32_t x[kTerms][NT][2];
 };
 template <bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void fragments(const float (&s)[NT][4], Weights<NT>& w)
+__device__ __forceinline__ void fragments(const float (&s)[NT][4], Weights<E2M1, NT, DUP>& w)
 {
     const int t = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            uint32_t hi, lo;
-            split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], hi, lo);
-            if (DUP) {
-                w.hi[n][u] = movmatrix_t(t < 2 ? hi : lo);
-            } else {
-                w.hi[n][u] = movmatrix_t(hi);
-                w.lo[n][u] = movmatrix_t(lo);
+            uint32_t part[kWeightParts<E2M1>];
+            split_p<E2M1>(s[n][2 * u], s[n][2 * u + 1], part);
+#pragma unroll
+            for (int k = 0; k < w.kTerms; ++k) {
+                if (DUP) {
+                    const uint32_t next = 2 * k + 1 < kWeightParts<E2M1> ? part[(2 * k + 1) % kWeightParts<E2M1>] : 0u;
+                    w.x[k][n][u] = movmatrix_t(t < 2 ? part[2 * k % kWeightParts<E2M1>] : next);
+                } else {
+                    w.x[k][n][u] = movmatrix_t(part[k % kWeightParts<E2M1>]);
+                }
             }
         }
 }
 template <bool E2M1, int NT, bool DUP>
-__device__ __forceinline__ void term(float (&c)[4], const Weights<NT>& w, int n, const uint32_t (&v)[4], bool first)
+__device__ __forceinline__ void term(float (&c)[4], const Weights<E2M1, NT, DUP>& w, int n, const uint32_t (&v)[4], bool first)
 {
-    if (first)
-        mma16_zero<E2M1>(c, v[0], v[1], v[2], v[3], w.hi[n][0], w.hi[n][1]);
-    else
-        mma16<E2M1>(c, v[0], v[1], v[2], v[3], w.hi[n][0], w.hi[n][1]);
-    if (!DUP) mma16<E2M1>(c, v[0], v[1], v[2], v[3], w.lo[n][0], w.lo[n][1]);
+#pragma unroll
+    for (int k = 0; k < w.kTerms; ++k) {
+        if (first && k == 0)
+            mma16_zero<E2M1>(c, v[0], v[1], v[2], v[3], w.x[k][n][0], w.x[k][n][1]);
+        else
+            mma16<E2M1>(c, v[0], v[1], v[2], v[3], w.x[k][n][0], w.x[k][n][1]);
+    }
 }
 
 // r % Mq of a query row (r < 64).
@@ -800,7 +808,7 @@ __device__ __forceinline__ void attend(const PagedAttnParams& p, Acc<E2M1, NT, D
         }
     }
     weights<EDGE, U, E2M1, NT, DUP>(a, s, hide);
-    Weights<NT> w[U];
+    Weights<E2M1, NT, DUP> w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) fragments<E2M1, NT, DUP>(reinterpret_cast<float(&)[NT][4]>(s[u * NT]), w[u]);
     VTile<E2M1> v[U];
@@ -869,7 +877,7 @@ __device__ __forceinline__ void attend_apart(const PagedAttnParams& p, Acc<E2M1,
             if (at < 0 || at > seen + query_pos(p, r)) hide |= 1u << (4 * n + e);
         }
     weights<true, 1, E2M1, NT, DUP>(a, s, hide);
-    Weights<NT> w;
+    Weights<E2M1, NT, DUP> w;
     fragments<E2M1, NT, DUP>(s, w);
 #pragma unroll 1
     for (int i = 0; i < p.Mq; ++i) {
