@@ -36,6 +36,9 @@ constexpr int kSecondPiece = 32;   // a CTA that starts on a second piece loses 
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
+// Minus the reference of a row without one: any finite logit then asks for a reference, and a logit of -inf gives a
+// weight of 0 (beside +inf it would give NaN).
+constexpr float kNoRef = 3.402823466e38f;
 
 template <bool E2M1>
 __device__ __forceinline__ void mma16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -629,7 +632,7 @@ struct Acc {
     uint32_t q[kSharedQ ? 1 : NT][16];         // B fragments: registers 2j, 2j + 1 of step j
     uint32_t sq;                               // or the lane's place in [N tile][pair of steps][32] of 16 bytes
     float rs[NT][2];      // factor of the logits of rows 2t, 2t+1 (of each N tile)
-    float bias[NT][2];    // minus the reference of those rows; +inf: none yet
+    float bias[NT][2];    // minus the reference of those rows; kNoRef: none yet
     float l[NT][2];
     float o[NT][8][4];
 };
@@ -666,7 +669,7 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
                 const float nb = fminf(a.bias[n][e], kBase - m);
-                if (nb < a.bias[n][e]) {   // never for a row without a visible logit
+                if (nb < a.bias[n][e]) {   // never for a row without a visible logit above -inf
                     const float f = fast_exp2(nb - a.bias[n][e]);   // 0 for the first reference
                     a.l[n][e] *= f;
 #pragma unroll
@@ -1218,7 +1221,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         if (kSharedQ) a.rs[n][e] = p.qscale * sm_f[8 * n + 2 * t + e];
-                        a.bias[n][e] = INFINITY;
+                        a.bias[n][e] = kNoRef;
                         a.l[n][e] = 0.f;
                     }
 #pragma unroll
@@ -1265,7 +1268,8 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
                 z += __shfl_xor_sync(kFull, z, 16);
                 const int row = 8 * n + 2 * t + e;
                 if (g == 0 && row < kRows) {
-                    sm_m[warp * kRows + row] = z != z ? 0.f : -a.bias[n][e];   // a NaN logit leaves no reference but shows
+                    // a NaN logit leaves no reference but shows
+                    sm_m[warp * kRows + row] = z != z ? 0.f : (a.bias[n][e] == kNoRef ? -INFINITY : -a.bias[n][e]);
                     sm_l[warp * kRows + row] = z;
                 }
             }

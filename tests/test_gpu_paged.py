@@ -398,6 +398,27 @@ def test_values_in_unseen_rows_reach_nothing(fx, fmt):
     assert torch.isnan(fx.fx_paged_decode(dev, qt[:1, :, :1])).all()
 
 
+def test_logits_of_minus_infinity_weigh_nothing(fx):
+    """Rows whose logit is -inf (a bf16 key of -inf) come first, alone in their tiles and next to finite ones."""
+    lens = [40, 17, 3, 200, 33]
+    c = pr.Cache("bf16", lens, 2, 16, seed=4)
+    dead = [np.arange(32), np.arange(16), np.arange(3), np.arange(0, 200, 2), np.arange(31, 33)]
+    for G, Mq in ((1, 1), (5, 1), (3, 3)):
+        q, _ = queries(c, G, Mq, 3)
+        q[..., 5] = 1.5
+        dev = c.device(fx)
+        for b, at in enumerate(dead):
+            pg, row = c.spot(b, at)
+            dev.k[torch.from_numpy(pg).cuda(), :, torch.from_numpy(row).cuda(), 5] = -float("inf")
+        out, lse = fx.fx_paged_decode(dev, torch.from_numpy(q).to(torch.bfloat16).cuda(), want_lse=True)
+        alive = [np.setdiff1d(np.arange(n), at) for n, at in zip(lens, dead)]
+        c2 = pr.Cache("bf16", lens, 2, 16, seed=4)
+        c2.keys = lambda b, h, idx=None, tail_lo=None: alive[b]
+        check_out(out, lse, pr.attend(c2, q, 128 ** -0.5))
+        if Mq == 1:                                             # every logit of sequence 2
+            assert not out[2].any() and (lse[2] == -float("inf")).all()
+
+
 def test_decode_reports_bad_values(fx):
     c = pr.Cache("bf16", [50, 64], 1, 16, seed=3)
     q, qt = queries(c, 2, 1, 4)
