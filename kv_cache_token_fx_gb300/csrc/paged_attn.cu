@@ -1386,8 +1386,9 @@ constexpr int kImpWarps = 4;
 __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
 // Importance.  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
-// want them, and each of them serves a unit of tiles at a time.  Rows of the fragments beyond the last query row
-// repeat it and add 2^-inf.
+// want them, and each of them serves a unit of tiles at a time.  Rows of the fragments that
+// add nothing -- beyond the last query row, or with an lse of -inf, whatever the query holds -- are zeros and add
+// 2^-inf.
 template <bool E2M1>
 __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importance_kernel(const PagedAttnParams p)
 {
@@ -1420,15 +1421,18 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                                       warp_start<U, W>(seq, line.s0, line.s1, warp + 1));
         int row0 = base + feeder.it * kTileRows;     // first row of the unit in work
         for (int n = warp; n < nq; n += W) {
-            const int r = 8 * n + g, of = min(r, p.R - 1);
+            const int r = 8 * n + g;
             uint32_t q[16];
-            fetch_query<E2M1>(query_row(p, b, h, of), q);
-            // a row that saw nothing (lse = -inf) adds nothing
-            const float z = p.lse[((int64_t)b * p.Hq + h * p.G + of / p.Mq) * p.Mq + of % p.Mq];
+            fetch_query<E2M1>(r < p.R ? query_row(p, b, h, r) : nullptr, q);
+            const float z = r < p.R ? p.lse[((int64_t)b * p.Hq + h * p.G + r / p.Mq) * p.Mq + r % p.Mq] : -INFINITY;
+            if (z == -INFINITY) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) q[j] = 0;
+            }
             const float f = make_query<E2M1>(q);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sq[(n * 4 + j) * 32 + lane] = make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
-            if (t == 0) sf[r] = make_float2(p.qscale * f, r >= p.R || z == -INFINITY ? -INFINITY : z * -1.4426950408889634f);
+            if (t == 0) sf[r] = make_float2(p.qscale * f, z * -1.4426950408889634f);
         }
         __syncthreads();
         float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * n_cand - p.cand_lo;

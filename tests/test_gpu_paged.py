@@ -492,6 +492,23 @@ def test_importance(fx, fmt, G, Mq, Hkv, page, cand):
         assert np.allclose(got.sum(-1), np.array(want)[:, None], rtol=1e-3)
 
 
+@pytest.mark.parametrize("fmt", FMT)
+def test_importance_leaves_out_rows_without_lse(fx, fmt):
+    """Query rows with an lse of -inf add nothing, whatever they hold (a padded batch); their neighbours stay exact."""
+    c = pr.Cache(fmt, [70, 45, 16], 2, 16, seed=9)
+    q, qt = queries(c, 3, 2, 5)
+    dev = c.device(fx)
+    _, lse = fx.fx_paged_decode(dev, qt, want_lse=True)
+    lse[0, 1] = lse[1, 0, 1] = lse[1, 5, 0] = lse[2] = -float("inf")
+    qt[0, 1] = float("nan")
+    qt[1, 0, 1] = float("inf")
+    qt[2, :, :, ::2] = float("nan")
+    s = fx.fx_paged_importance(dev, qt, lse)
+    ref, dl = pr.importance(c, q, lse.double().cpu().numpy(), 128 ** -0.5, 0, c.max_pages * 16)
+    assert np.all(np.abs(s.double().cpu().numpy() - ref) <= 2.0 ** -19 * (dl + 1) * ref + 1e-37)
+    assert not s[2].any()
+
+
 # ---------------------------------------------------------------------------------------- together
 def test_matches_the_contiguous_calls(fx):
     """The same rows in a contiguous bf16 cache: focal attention, importance and sparse decode agree."""
