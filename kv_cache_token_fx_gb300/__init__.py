@@ -599,9 +599,9 @@ def _paged_view(cache, t, name, shape):
         if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == cache._index:
             st = t.stride()
             if st[-1] == 1:
-                for i in st:
-                    if i & 7 and i != 1:
-                        return t.data_ptr(), _strides(t)   # the library refuses what then still is no multiple of 8
+                for i in st[:-1]:
+                    if i & 7:
+                        return t.data_ptr(), _strides(t)   # (the library refuses what then still is no multiple of 8)
                 return t.data_ptr(), st
             raise FxError(FX_ERR_INVALID_ARG, f"{name} must have unit last stride")
     except AttributeError:

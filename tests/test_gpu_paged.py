@@ -651,6 +651,21 @@ def test_two_graphs_and_two_streams_at_once(fx):
             assert all(torch.equal(a, o) for o in os_)
 
 
+def test_views_whose_single_entries_have_any_stride(fx):
+    """The stride of a dimension of one entry addresses nothing, whatever it is."""
+    c = pr.Cache("e2m1", [20, 5], 1, 16, seed=1)
+    q, qt = queries(c, 1, 1, 2)
+    odd = torch.as_strided(qt, qt.shape, (128, 1, 1, 1))
+    assert torch.equal(fx.fx_paged_decode(c.device(fx), odd), fx.fx_paged_decode(c.device(fx), qt))
+    tok = qt[:1, 0]                                             # [1, 1, 128]
+    one = torch.as_strided(tok, tok.shape, (3, 1, 1))
+    dev = c.device(fx)
+    fx.fx_paged_append(dev, one, one, cu([1], torch.int32), cu([4], torch.int32))
+    k, v = fx.fx_paged_gather(dev, 1, lo=cu([0, 4], torch.int32))
+    want = pr.dequantize(*pr.quantize(q[0, 0, 0][None]))
+    assert np.array_equal(k[1, 0].double().cpu().numpy(), want) and torch.equal(k[1], v[1])
+
+
 def test_binding_refusals(fx):
     c = pr.Cache("e2m1", [20], 2, 16, seed=1)
     dev = c.device(fx)
