@@ -1432,7 +1432,7 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
             const float f = make_query<E2M1>(q);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sq[(n * 4 + j) * 32 + lane] = make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
-            if (t == 0) sf[r] = make_float2(p.qscale * f, z * -1.4426950408889634f);
+            if (t == 0) sf[r] = make_float2(p.qscale * f, z == -INFINITY ? z : z * -1.4426950408889634f);
         }
         __syncthreads();
         float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * n_cand - p.cand_lo;
