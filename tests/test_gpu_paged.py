@@ -471,6 +471,38 @@ def test_decode_many_sequences(fx):
     check_out(out, lse, pr.attend(c, q, 128 ** -0.5))
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("B,Hkv,G,Mq", [(31, 2, 1, 1), (33, 1, 4, 1), (40, 2, 2, 4), (64, 1, 2, 7), (127, 1, 8, 1),
+                                        (128, 2, 4, 1), (129, 1, 1, 3), (257, 2, 5, 2)])
+def test_batches_around_the_sizes_of_the_scan(fx, fmt, B, Hkv, G, Mq):
+    """Ragged batches, a few long sequences among short and empty ones: decode and importance."""
+    g = np.random.default_rng(B)
+    lens = [int(x) for x in g.integers(0, 70, B)]
+    lens[B // 3], lens[-1], lens[0] = 900, 333, 0
+    c = pr.Cache(fmt, lens, Hkv, 32, seed=B)
+    q, qt = queries(c, G, Mq, 2)
+    dev = c.device(fx)
+    out, lse = fx.fx_paged_decode(dev, qt, want_lse=True)
+    check_out(out, lse, pr.attend(c, q, 128 ** -0.5))
+    s = fx.fx_paged_importance(dev, qt, lse, cand=(3, 777))
+    ref, dl = pr.importance(c, q, lse.double().cpu().numpy(), 128 ** -0.5, 3, 777)
+    assert np.all(np.abs(s.double().cpu().numpy() - ref) <= 2.0 ** -19 * (dl + 1) * ref + 1e-37)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("page", [16, 1024])
+def test_long_lists_and_tails_over_many_ctas(fx, fmt, page):
+    lens = [6000, 40, 2999]
+    c = pr.Cache(fmt, lens, 2, page, seed=3)
+    g = np.random.default_rng(1)
+    q, qt = queries(c, 4, 1, 2)
+    k = 2501
+    idx = np.stack([np.stack([g.integers(0, n, k) for _ in range(2)]) for n in lens])   # rows may come twice
+    tail = [5211, 0, 2990]
+    out, lse = fx.fx_paged_decode(c.device(fx), qt, cu(idx, torch.int32), cu(tail, torch.int32), want_lse=True)
+    check_out(out, lse, pr.attend(c, q, 128 ** -0.5, idx, tail))
+
+
 # ---------------------------------------------------------------------------------------- importance
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("G,Mq,Hkv,page,cand", [(2, 1, 2, 16, None), (4, 1, 1, 64, (5, 301)), (1, 8, 1, 32, (0, 1)),
@@ -664,6 +696,49 @@ def test_views_whose_single_entries_have_any_stride(fx):
     k, v = fx.fx_paged_gather(dev, 1, lo=cu([0, 4], torch.int32))
     want = pr.dequantize(*pr.quantize(q[0, 0, 0][None]))
     assert np.array_equal(k[1, 0].double().cpu().numpy(), want) and torch.equal(k[1], v[1])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_chained_launches_and_other_streams_give_the_same_bits(fx, fmt):
+    """A chain of programmatic launches, and the same on a stream that is given instead of the current one."""
+    m = Model(fx, fmt)
+    Hq, H = m.G * m.H, m.H
+    zero = torch.zeros(m.B, dtype=torch.int32, device="cuda")
+
+    def chain(flags, stream):
+        kw = dict(flags=flags, stream=stream)
+        fx.fx_paged_append(m.c, m.prompt[:, Hq:Hq + H], m.prompt[:, Hq + H:], m.seq, m.pos, cos_sin=m.cs, **kw)
+        x, res = m.step_in[0], []
+        for i in range(3):
+            q = fx.fx_paged_append(m.c, x[:, Hq:Hq + H], x[:, Hq + H:], m.step_seq, m.len + (i - 3), cos_sin=m.cs,
+                                   q=x[:, :Hq], **kw)
+            q = q.view(m.B, 1, Hq, D).transpose(1, 2)
+            out, lse = fx.fx_paged_decode(m.c, q, want_lse=True, **kw)
+            s = fx.fx_paged_importance(m.c, q, lse, cand=(0, 60), **kw)
+            k, v = fx.fx_paged_gather(m.c, 60, k_out=torch.zeros(m.B, H, 60, D, dtype=torch.bfloat16, device="cuda"),
+                                      v_out=torch.zeros(m.B, H, 60, D, dtype=torch.bfloat16, device="cuda"), lo=zero, **kw)
+            res += [q, out, lse, s, k, v]
+        return res
+
+    want = chain(0, None)
+    torch.cuda.synchronize()
+    got = chain(fx.FX_LAUNCH_PDL, None)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    side = torch.cuda.Stream()
+    for flags in (0, fx.FX_LAUNCH_PDL):
+        torch.cuda.synchronize()      # (the chain's inputs are made on the current stream)
+        with torch.cuda.stream(side):
+            got = chain(flags, None)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    torch.cuda.synchronize()
+    q = want[0].contiguous()
+    torch.cuda.synchronize()
+    a = fx.fx_paged_decode(m.c, q)
+    b = fx.fx_paged_decode(m.c, q, stream=side)
+    c = fx.fx_paged_decode(m.c, q, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(a, c)
 
 
 def test_binding_refusals(fx):

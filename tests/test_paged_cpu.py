@@ -115,6 +115,11 @@ def test_decode_and_importance_refusals(lib):
         assert imp(**kw) == 1, kw
     assert imp(Mq=17) == 2
     assert imp(lo=10) == 0                                  # no candidates
+    d = ctypes.byref(desc(B=65535, Hkv=65535))              # 4e9 heads: their tiles are not counted in 32 bits
+    assert dec(Hq=65535, Mq=1) == 2 and b"tiles" in lib.fx_last_error()
+    assert lib.fx_paged_importance(d, 256, 0, 0, 0, 65535, 1, 256, 1.0, 0, 1, 256, 0, None) == 2
+    d = ctypes.byref(desc(B=64, Hkv=64))
+    assert dec(Hq=64, Mq=1, idx=256, k=1 << 29) == 2 and b"tiles" in lib.fx_last_error()
 
 
 def test_binding_refuses_other_tensors():
