@@ -31,7 +31,7 @@ constexpr int kTileRows = 16;
 constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call
 constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
-constexpr int kSecondPiece = 32;   // a CTA that starts on a second piece loses about the time of this many tiles
+constexpr int kSecondPiece = 48;   // a CTA that starts on a second piece loses about the time of this many tiles
                                    // (start-up and join, 7 us of a CTA that takes 0.22 us a tile)
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
@@ -1383,6 +1383,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 }
 
 constexpr int kImpWarps = 4;
+constexpr int kImpStages = 3;   // units in a warp's ring
 __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
 // Importance.  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
@@ -1401,12 +1402,18 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int nq = (p.R + 7) / 8, n_cand = p.cand_hi - p.cand_lo;
-    const uint32_t ring = smem_addr(sq + nq * 128) + warp * 2 * S::kBytes;   // two slots
+    const uint32_t ring = smem_addr(sq + nq * 128) + warp * kImpStages * S::kBytes, ring_end = ring + kImpStages * S::kBytes;
     const int base = p.cand_lo & ~(2 * kTileRows - 1);                       // first row of the first tile
-    // candidates past a sequence's end
-    for (int64_t i = blockIdx.x; i < (int64_t)p.c.B * p.c.Hkv; i += gridDim.x) {
-        const int len = sequence(p, (int)(i / p.c.Hkv), false).len;
-        for (int r = max(len, p.cand_lo) + threadIdx.x; r < p.cand_hi; r += 32 * W) p.scores[i * n_cand + r - p.cand_lo] = 0.f;
+    // candidates past a sequence's end: the grid's CTAs share the rows of scores
+    {
+        const int64_t rows = (int64_t)p.c.B * p.c.Hkv;
+        const int share = max((int)(gridDim.x / rows), 1);   // CTAs of a row
+        for (int64_t i = blockIdx.x; i < rows * share; i += gridDim.x) {
+            const int64_t at = i / share;
+            const int len = sequence(p, (int)(at / p.c.Hkv), false).len, part = (int)(i - at * share);
+            for (int64_t r = (int64_t)max(len, p.cand_lo) + part * (32 * W) + threadIdx.x; r < p.cand_hi; r += share * (32 * W))
+                p.scores[at * n_cand + r - p.cand_lo] = 0.f;
+        }
     }
     auto tiles = [&](const Seq& q) { return max((min(q.len, p.cand_hi) - base + kTileRows - 1) / kTileRows, 1); };
     Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv);
@@ -1419,7 +1426,15 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
         const int seen = seq.len - p.Mq, stop = min(seq.len, p.cand_hi);
         Feeder<E2M1, false, U> feeder(p, seq, h, warp_start<U, W>(seq, line.s0, line.s1, warp),
                                       warp_start<U, W>(seq, line.s0, line.s1, warp + 1));
-        int row0 = base + feeder.it * kTileRows;     // first row of the unit in work
+        // the ring's first units go on their way, then each turn feeds the unit kImpStages - 1 turns ahead
+        uint32_t flags[kImpStages];      // of the units in the ring, oldest first, and their first rows
+        int first[kImpStages + 1];
+#pragma unroll
+        for (int k = 0; k < kImpStages - 1; ++k) {
+            first[k] = base + feeder.it * kTileRows;
+            flags[k] = feeder.feed(ring + k * S::kBytes);
+        }
+        first[kImpStages - 1] = base + feeder.it * kTileRows;
         for (int n = warp; n < nq; n += W) {
             const int r = 8 * n + g;
             uint32_t q[16];
@@ -1436,15 +1451,13 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
         }
         __syncthreads();
         float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * n_cand - p.cand_lo;
-        uint32_t flags = feeder.feed(ring), slot = ring;
-        while (flags >> U) {
-            cp_async_wait_all_groups();   // this lane's copies of the unit; the barrier covers the others'
+        uint32_t slot = ring, into = ring + (kImpStages - 1) * S::kBytes;
+        while (flags[0] >> U) {
+            cp_async_wait_stages<kImpStages - 1>();   // this lane's copies of the unit; the barrier covers the others'
             __syncwarp();
-            const uint32_t edges = flags & ((1u << U) - 1);
-            const int here = row0;
-            row0 = base + feeder.it * kTileRows;
-            const uint32_t next = slot == ring ? ring + S::kBytes : ring;
-            flags = feeder.feed(next);
+            flags[kImpStages - 1] = feeder.feed(into);
+            first[kImpStages] = base + feeder.it * kTileRows;
+            const uint32_t edges = flags[0] & ((1u << U) - 1);
             uint32_t a[U][4][2][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -1502,13 +1515,19 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                     sum[u][e] += __shfl_xor_sync(kFull, sum[u][e], 2);
                 }
                 // (a tile of the unit that does not exist starts at or past `stop`, or the next unit writes it)
-                const int row = here + u * kTileRows + g + 8 * t;
-                const bool mine = u == 0 || !((edges >> (U - 1 - u)) & 1u) || here + u * kTileRows < row0;
+                const int row = first[0] + u * kTileRows + g + 8 * t;
+                const bool mine = u == 0 || !((edges >> (U - 1 - u)) & 1u) || first[0] + u * kTileRows < first[1];
                 if (t < 2 && mine && row >= p.cand_lo && row < stop) out[row] = t ? sum[u][1] : sum[u][0];
             }
-            slot = next;
+            into = slot;
+            slot = slot + S::kBytes == ring_end ? ring : slot + S::kBytes;
+#pragma unroll
+            for (int k = 0; k < kImpStages; ++k) first[k] = first[k + 1];
+#pragma unroll
+            for (int k = 0; k < kImpStages - 1; ++k) flags[k] = flags[k + 1];
         }
-        __syncthreads();   // the query fragments are free for the next piece
+        cp_async_wait_all_groups();
+        __syncthreads();   // the query fragments and the rings are free for the next piece
     }
 }
 
@@ -1540,7 +1559,7 @@ cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cuda
 template <bool E2M1>
 cudaError_t launch_importance(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    constexpr size_t ring = (size_t)kImpWarps * 2 * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
+    constexpr size_t ring = (size_t)kImpWarps * kImpStages * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(paged_importance_kernel<E2M1>, ring + kMaxRows / 8 * 2048, done);
     if (e != cudaSuccess) return e;
