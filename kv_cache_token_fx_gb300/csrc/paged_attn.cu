@@ -33,6 +33,8 @@ constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row g
                                 // of them joins all their parts
 constexpr int kSecondPiece = 48;   // a CTA that starts on a second piece loses about the time of this many tiles
                                    // (start-up and join, 7 us of a CTA that takes 0.22 us a tile)
+constexpr int kStart = 32;  // what the start of a piece counts in a line, in tiles
+constexpr int kNear = 16;   // tiles between a cut and an end of a piece
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -922,14 +924,16 @@ struct Line {
     const PagedAttnParams& p;
     const Count count;         // tiles of a sequence's piece, at least 1
     const int per_seq;         // pieces of one sequence
+    const int second;          // equal parts may be this many tiles longer than the ideal share
     Seq seq;
     int b, ntile;              // the sequence, tiles of its pieces
     int piece, s0, s1;         // the piece of the sequence, this CTA's tiles of it
     int c0, n_part, slot0;     // the CTAs that share it: c0 .. c0 + n_part - 1; the partial slot of the first
+    int part;                  // which of them this is
     int slot;                  // this CTA's partial slot
 
-    __device__ __forceinline__ Line(const PagedAttnParams& p_, Count count_, int per_seq_)
-        : p(p_), count(count_), per_seq(per_seq_)
+    __device__ __forceinline__ Line(const PagedAttnParams& p_, Count count_, int per_seq_, int second_)
+        : p(p_), count(count_), per_seq(per_seq_), second(second_)
     {
     }
 
@@ -943,10 +947,9 @@ struct Line {
     {
         cta = blockIdx.x;
         const int most = (int)gridDim.x;
-        const int grid = B >= most || B * per_seq >= most ? most : min(most, kMaxParts * B * per_seq);
-        n_cta = min(grid, max(1, total / (W * kMinTiles)));
-        quota = total / n_cta;
-        extra = total - quota * n_cta;
+        const bool many = B >= most || B * per_seq >= most;   // (of one tile at least)
+        const int grid = many ? most : min(most, kMaxParts * B * per_seq);
+        n_cta = many ? grid : min(grid, max(1, total / (W * kMinTiles)));
         inv = 0.f;
         if (B < grid && B * per_seq <= grid) {
             const float ideal = fmaxf((float)total / (float)grid, (float)(W * kMinTiles));
@@ -964,11 +967,14 @@ struct Line {
             for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, d));
             const unsigned who = __ballot_sync(kFull, longest == best);
             inv = __shfl_sync(kFull, inv, __ffs(who) - 1);
-            if (!(best <= ideal + kSecondPiece)) inv = 0.f;
+            if (!(best <= ideal + second)) inv = 0.f;
         }
         at = cta;
         end = cta + 1;
         if (inv == 0.f) {
+            total += p.c.B * per_seq * kStart;
+            quota = total / n_cta;
+            extra = total - quota * n_cta;
             at = place(cta);
             end = place(cta + 1);
         }
@@ -997,7 +1003,7 @@ struct Line {
             total *= per_seq;
             choose(B, [&](int i) { return __shfl_sync(kFull, mine, i); });
             if (inv == 0.f && cta >= n_cta) return false;
-            const int n = lane < B ? (inv == 0.f ? mine : parts(mine)) : 0;
+            const int n = lane < B ? (inv == 0.f ? mine + kStart : parts(mine)) : 0;
             int inc = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -1040,7 +1046,7 @@ struct Line {
                 const int i = b0 + tid;
                 if (b0 > 0 && i < B) seq = sequence(p, i, false);
                 const int c = b0 == 0 ? n_first : (i < B ? count(seq) : 0);
-                const int n = i < B ? (inv == 0.f ? c : parts(c)) : 0;
+                const int n = i < B ? (inv == 0.f ? c + kStart : parts(c)) : 0;
                 int inc = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -1075,48 +1081,55 @@ struct Line {
         }
         seq.table = p.c.table + (int64_t)b * p.c.table_stride;
         ntile = count(seq);
-        slot = cta * 2;
+        if (inv == 0.f) at -= (at - seq_start) % (ntile + kStart);   // the start of its first piece
         return true;
     }
 
     // The next piece of this CTA; false: there is none.
     __device__ __forceinline__ bool next()
     {
-        if (at >= end) return false;
         if (inv == 0.f) {
-            while (at >= seq_start + ntile * per_seq) {
-                seq_start += ntile * per_seq;
-                seq = sequence(p, ++b, false);
-                ntile = count(seq);
+            for (;;) {
+                if (at >= end) return false;
+                while (at >= seq_start + (ntile + kStart) * per_seq) {
+                    seq_start += (ntile + kStart) * per_seq;
+                    seq = sequence(p, ++b, false);
+                    ntile = count(seq);
+                }
+                // a cut near an end of the piece moves there, all cuts of a short piece do: no CTA comes for a few
+                // tiles, and a piece of one CTA has no parts to join
+                const int near = min(kNear, ntile / 2), from = at + kStart;
+                c0 = owner(from + near);
+                n_part = owner(max(from + ntile - near - 1, from + near)) - c0 + 1;
+                piece = (at - seq_start) / (ntile + kStart);
+                at += ntile + kStart;
+                part = cta - c0;
+                if (part < 0 || part >= n_part) continue;
+                s0 = part == 0 ? 0 : place(cta) - from;
+                s1 = part == n_part - 1 ? ntile : place(cta + 1) - from;
+                break;
             }
-            piece = (at - seq_start) / ntile;
-            const int from = seq_start + piece * ntile;
-            s0 = at - from;
-            s1 = min(ntile, end - from);
-            c0 = owner(from);
-            n_part = owner(from + ntile - 1) - c0 + 1;
-            // a CTA's first piece uses its slot 0; this one is c0's first only if it starts c0's stretch
-            slot0 = c0 * 2 + (place(c0) == from ? 0 : 1);
-            slot = cta * 2 + (at == place(cta) ? 0 : 1);
-            at = from + s1;
         } else {
+            if (at >= end) return false;
             n_part = parts(ntile);
             piece = (at - seq_start) / n_part;
-            const int part = at - seq_start - piece * n_part;
+            part = at - seq_start - piece * n_part;
             const int least = ntile / n_part, more = ntile - least * n_part;
             s0 = least * part + min(part, more);
             s1 = s0 + least + (part < more ? 1 : 0);
             c0 = cta - part;
-            slot0 = c0 * 2;
             at = end;
         }
+        // a CTA is the first of one shared piece at most, and comes later in one other at most
+        slot = cta * 2 + (part == 0 ? 1 : 0);
+        slot0 = c0 * 2 + 1;
         return true;
     }
 
 private:
     int cta, n_cta, quota, extra;
     float inv;                 // 1 / tiles of a part where every CTA takes one part of one piece; 0: stretches
-    int total, at, end;        // length of the line (tiles), next place and end of this CTA's (tiles, or parts)
+    int total, at, end;        // length of the line (tiles); the next piece's start and the CTA's end (tiles, or parts)
     int seq_start;             // place where the sequence starts
 };
 
@@ -1173,7 +1186,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const int nrg = (p.R + kRows - 1) / kRows;
     auto tiles = [](const Seq& q) { return tile_count(q); };
-    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv * nrg);
+    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv * nrg, kSecondPiece);
     if (!line.start(sm_line)) return;
 
     while (line.next()) {
@@ -1383,7 +1396,8 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
 }
 
 constexpr int kImpWarps = 4;
-constexpr int kImpStages = 3;   // units in a warp's ring
+constexpr int kImpSecond = 32;
+__host__ __device__ constexpr int imp_stages(bool e2m1) { return e2m1 ? 2 : 3; }   // units in a warp's ring
 __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
 // Importance.  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
@@ -1393,7 +1407,7 @@ __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }  
 template <bool E2M1>
 __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importance_kernel(const PagedAttnParams p)
 {
-    constexpr int U = E2M1 ? 2 : 1, W = kImpWarps;
+    constexpr int U = E2M1 ? 2 : 1, W = kImpWarps, kImpStages = imp_stages(E2M1);
     using S = Slot<E2M1, false, U>;
     extern __shared__ __align__(128) uint4 sq[];     // [8-row tile][4][32], then the warps' rings
     __shared__ float2 sf[kMaxRows];                  // factor of a row's logits, minus its lse (base 2)
@@ -1404,19 +1418,8 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
     const int nq = (p.R + 7) / 8, n_cand = p.cand_hi - p.cand_lo;
     const uint32_t ring = smem_addr(sq + nq * 128) + warp * kImpStages * S::kBytes, ring_end = ring + kImpStages * S::kBytes;
     const int base = p.cand_lo & ~(2 * kTileRows - 1);                       // first row of the first tile
-    // candidates past a sequence's end: the grid's CTAs share the rows of scores
-    {
-        const int64_t rows = (int64_t)p.c.B * p.c.Hkv;
-        const int share = max((int)(gridDim.x / rows), 1);   // CTAs of a row
-        for (int64_t i = blockIdx.x; i < rows * share; i += gridDim.x) {
-            const int64_t at = i / share;
-            const int len = sequence(p, (int)(at / p.c.Hkv), false).len, part = (int)(i - at * share);
-            for (int64_t r = (int64_t)max(len, p.cand_lo) + part * (32 * W) + threadIdx.x; r < p.cand_hi; r += share * (32 * W))
-                p.scores[at * n_cand + r - p.cand_lo] = 0.f;
-        }
-    }
     auto tiles = [&](const Seq& q) { return max((min(q.len, p.cand_hi) - base + kTileRows - 1) / kTileRows, 1); };
-    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv);
+    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv, kImpSecond);
     if (!line.start(sm_line)) return;
 
     while (line.next()) {
@@ -1527,6 +1530,9 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
             for (int k = 0; k < kImpStages - 1; ++k) flags[k] = flags[k + 1];
         }
         cp_async_wait_all_groups();
+        // the candidates past the end: the piece's CTAs share them
+        for (int64_t r = (int64_t)max(seq.len, p.cand_lo) + line.part * (32 * W) + threadIdx.x; r < p.cand_hi; r += line.n_part * (32 * W))
+            out[r] = 0.f;
         __syncthreads();   // the query fragments and the rings are free for the next piece
     }
 }
@@ -1559,7 +1565,7 @@ cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cuda
 template <bool E2M1>
 cudaError_t launch_importance(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    constexpr size_t ring = (size_t)kImpWarps * kImpStages * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
+    constexpr size_t ring = (size_t)kImpWarps * imp_stages(E2M1) * Slot<E2M1, false, E2M1 ? 2 : 1>::kBytes;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(paged_importance_kernel<E2M1>, ring + kMaxRows / 8 * 2048, done);
     if (e != cudaSuccess) return e;
