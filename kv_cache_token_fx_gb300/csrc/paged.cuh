@@ -61,17 +61,6 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// len[b], clamped into [0, cap] (flagging a value outside it).
-__device__ __forceinline__ int paged_len(const PagedCache& c, int b, unsigned* err)
-{
-    const int n = c.len[b];
-    if (n < 0 || n > c.cap) {
-        atomicOr(err, FX_DEVERR_LEN);
-        return n < 0 ? 0 : c.cap;
-    }
-    return n;
-}
-
 // Page number of row t of sequence b (0 <= t < cap), or -1 (flagged) for a bad table entry.
 __device__ __forceinline__ int paged_page(const PagedCache& c, int b, int t, unsigned* err)
 {

@@ -13,6 +13,11 @@
 // of its row's largest is lost.  bf16 rows take bf16 queries as they are.  P enters as a sum of 16-bit parts, two
 // f16 or three bf16: outputs are fp32, and one part would leave them 2^-12 (f16) or 2^-9 (bf16) off.
 //
+// Why mma.sync and not tcgen05: the codes must be unpacked by the threads in either case.  A version with 128-row tiles
+// unpacked into swizzled shared memory, S^T and O^T by tcgen05.mma and one cache row to a thread gave the same outputs,
+// but took 52 M warp instructions instead of 36 M for 64 x 3335 rows and 14 query rows (139 us against 94 then): the
+// stores of the operands and of P cost more than the products it saves.  At most 64 query rows share a cache row here.
+//
 // Softmax: base-2 logits, one pass.  p = 2^(x - m) with a reference m per row that all lanes of the row share;
 // it is set so that the largest logit so far gives 2^kBase and moves only when a p would exceed 2^kTop, so most
 // tiles take one vote instead of a reduction; f16 holds such a p to 2^-36 of the row's largest.  Sums are fp32.
@@ -28,13 +33,19 @@ namespace fx {
 namespace {
 
 constexpr int kTileRows = 16;
-constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call
+constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call (decode of 8 x 4864 4-bit rows:
+                                // 16.7 us with 1 or 2, 17.1 with 8)
 constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
-constexpr int kSecondPiece = 48;   // a CTA that starts on a second piece loses about the time of this many tiles
-                                   // (start-up and join, 7 us of a CTA that takes 0.22 us a tile)
-constexpr int kStart = 32;  // what the start of a piece counts in a line, in tiles
-constexpr int kNear = 16;   // tiles between a cut and an end of a piece
+// Where every CTA can take one part of one piece, parts this many tiles longer than an even share are better than a
+// second piece for some CTAs (8 x 4864 4-bit rows: 16.7 us against 20.1 with even shares; 16 x 32768: 89.6 against 91.4).
+constexpr int kSecondPiece = 48;
+// In a line the start of a piece counts as this many tiles: its first rows, queries and join take 7 us, a tile of a CTA
+// 0.22 us.  64 sequences of up to 40 rows: 17 us against 54 without; of up to 3335, 14 query rows: 80 us against 85 with
+// 16, 82 with 48 and 94 without.
+constexpr int kStart = 32;
+constexpr int kNear = 16;       // tiles between a cut and an end of a piece, at least (those 3335 rows: 91 us with 8, 90 with
+                                // 16, 92 with 32, 95 without, before the start of a piece counted)
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -1143,13 +1154,21 @@ __device__ __forceinline__ int warp_start(const Seq& q, int s0, int s1, int w)
     return w == W ? s1 : (w == 0 || U == 1 || x < q.nl ? x : min(x + (((q.lo >> 4) + x - q.nl) & 1), s1));
 }
 
-// Shape of the decode kernel for a format and up to 4 (DUP), 8 or 16 query rows a pass.  4-bit tiles are small
-// (2.3 KB) and cost many operations a byte: 16 warps an SM.  bf16 tiles (8 KB) fill the shared memory with 8
-// warps' rings.
+// Shape of the decode kernel for a format and up to 4 (DUP), 8 or 16 query rows a pass.
+//
+// bf16: bound by bytes.  A tile is 8 KB, and the rings of 8 warps fill the shared memory of an SM (8 x 32768 rows,
+// 755 MB: 118 us, 0.94 of the copy bandwidth; rings of 4 units instead of 3: 128 us).
+// 4 bits: a tile is 2.3 KB and takes 310 instructions of a warp, of which 64 are conversions of codes and 64 their
+// scaling (the conversion issues every second cycle): bound by the issue of instructions and their latency.  As many
+// warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 89.6 us, 0.68 of the copy
+// bandwidth; with 2 CTAs 96 us), 2 CTAs for 16 rows (3 spill, and gain nothing).  Two tiles at a time share the loads
+// of the queries and the additions to O (89.6 us against 102 with one; short rows like one better: 8 x 4864 rows
+// 16.6 us against 15.1).  DUP: 89.6 us against 105 for up to 4 rows.  One pass of 16 rows instead of two of 8: 94 us
+// against 112 (64 x 3335 rows, 14 query rows).
 template <bool E2M1, int NT, bool DUP>
 struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
-    static constexpr int kWarps = 4;                     // few, so that other CTAs of the SM work while one starts or joins
+    static constexpr int kWarps = 4;                  // few, so that other CTAs of the SM work while one starts or joins
     static constexpr int kCtas = E2M1 && NT == 1 ? 3 : 2;       // per SM
     static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
     static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
@@ -1400,7 +1419,10 @@ constexpr int kImpSecond = 32;
 __host__ __device__ constexpr int imp_stages(bool e2m1) { return e2m1 ? 2 : 3; }   // units in a warp's ring
 __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
-// Importance.  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
+// Importance.  4 bits: bound by the issue of instructions (4 x 32768 rows, 32 query rows: 32.7 us, 177 instructions a
+// tile and 55 more for each 8 query rows; 4 query rows: 18 us, 49 MB; 2 CTAs an SM instead of 3: 35 us).  bf16: by bytes
+// and the start (8 x 4864 rows, 2 query rows: 11.7 us for 46 MB; rings of 2 units instead of 3: 12.5 us, of 4, with
+// fewer CTAs: 16 us).  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
 // want them, and each of them serves a unit of tiles at a time.  Rows of the fragments that
 // add nothing -- beyond the last query row, or with an lse of -inf, whatever the query holds -- are zeros and add
 // 2^-inf.
