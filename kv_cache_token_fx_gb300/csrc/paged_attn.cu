@@ -37,6 +37,11 @@ constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs 
                                 // 16.7 us with 1 or 2, 17.1 with 8)
 constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
+// 4 bits, up to 8 query rows: tiles a warp may get at most for units of one tile instead of two (512 heads' 40 rows, a
+// tile: 9.4 us against 11.8; 833 rows, 15 tiles: 23.2 both; 1667 rows, 29 tiles: 33.4 against 31.3; 128 heads' 32768
+// rows, 144 tiles: 99 against 85).  Pages of 16 rows hold no pair of neighbours: always one (64 heads' 4864 rows 14.8 us
+// against 16.3, 38912 rows 73 against 76).
+constexpr int kShort = 16;
 // Where every CTA can take one part of one piece, parts this many tiles longer than an even share are better than a
 // second piece for some CTAs (8 x 4864 4-bit rows: 16.7 us against 20.1 with even shares; 16 x 32768: 89.6 against 91.4).
 constexpr int kSecondPiece = 48;
@@ -1160,19 +1165,18 @@ __device__ __forceinline__ int warp_start(const Seq& q, int s0, int s1, int w)
 // 755 MB: 118 us, 0.94 of the copy bandwidth; rings of 4 units instead of 3: 128 us).
 // 4 bits: a tile is 2.3 KB and takes 310 instructions of a warp, of which 64 are conversions of codes and 64 their
 // scaling (the conversion issues every second cycle): bound by the issue of instructions and their latency.  As many
-// warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 89.6 us, 0.68 of the copy
-// bandwidth; with 2 CTAs 96 us), 2 CTAs for 16 rows (3 spill, and gain nothing).  Two tiles at a time share the loads
-// of the queries and the additions to O (89.6 us against 102 with one; short rows like one better: 8 x 4864 rows
-// 16.6 us against 15.1).  DUP: 89.6 us against 105 for up to 4 rows.  One pass of 16 rows instead of two of 8: 94 us
+// warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 85 us, 0.71 of the copy
+// bandwidth; with 2 CTAs 7% longer), 2 CTAs for 16 rows (3 spill, and gain nothing).  Two tiles at a time share the loads
+// of the queries and the additions to O; where a warp gets few tiles, one at a time is sooner done (kShort).  DUP: 90 us
+// against 105 for up to 4 rows.  One pass of 16 rows instead of two of 8: 94 us
 // against 112 (64 x 3335 rows, 14 query rows).
-template <bool E2M1, int NT, bool DUP>
+template <bool E2M1, int NT, bool DUP, int U>
 struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
     static constexpr int kWarps = 4;                  // few, so that other CTAs of the SM work while one starts or joins
     static constexpr int kCtas = E2M1 && NT == 1 ? 3 : 2;       // per SM
-    static constexpr int kUnit = E2M1 ? 2 : 1;           // tiles that a warp attends at a time
-    static constexpr int kStages = E2M1 ? 2 : 3;         // units in a warp's ring
-    using Unit = Slot<E2M1, true, kUnit>;
+    static constexpr int kStages = U == 2 ? 2 : 3;       // units (of U tiles that a warp attends at a time) in its ring
+    using Unit = Slot<E2M1, true, U>;
     static constexpr int kRing = kStages * Unit::kBytes;   // bytes of a warp; its partial O later takes them
     static constexpr size_t kSmem = (size_t)kWarps * kRing;
     static_assert(kRows * kOPitch * 4 <= kRing, "a warp's partial O lies in its ring");
@@ -1183,12 +1187,12 @@ struct Shape {
 //
 // DUP: at most 4 query rows; columns 4..7 of the products repeat them, so that one product takes P's high part
 // (columns 0..3) and its low part (4..7).
-template <bool E2M1, int NT, bool DUP>
-__global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1, NT, DUP>::kCtas)
+template <bool E2M1, int NT, bool DUP, int U>
+__global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2M1, NT, DUP, U>::kCtas)
     paged_decode_kernel(const PagedAttnParams p)
 {
-    using S = Shape<E2M1, NT, DUP>;
-    constexpr int kRows = S::kRows, W = S::kWarps, kStages = S::kStages, U = S::kUnit, kSlot = S::Unit::kBytes;
+    using S = Shape<E2M1, NT, DUP, U>;
+    constexpr int kRows = S::kRows, W = S::kWarps, kStages = S::kStages, kSlot = S::Unit::kBytes;
     constexpr int kPitch = S::kRing / 4;   // floats between the warps' partial O
     extern __shared__ __align__(128) float smem[];
     float* const sm_o = smem;
@@ -1227,62 +1231,58 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP>::kWarps, Shape<E2M1,
         Feeder<E2M1, true, U> feeder(p, seq, h, warp_start<U, W>(seq, s0, s1, warp), warp_start<U, W>(seq, s0, s1, warp + 1));
         uint32_t flags[kStages];   // of the units in the ring, oldest first
 #pragma unroll
-        for (int k = 0; k < kStages; ++k) flags[k] = 1u << U;
-        uint32_t slot = ring + kSlot, into = ring;   // (the first turns only feed)
-        for (int turn = 1 - kStages; flags[0] >> U; ++turn) {
-            if (turn >= 0) cp_async_wait_stages<kStages - 1>();   // this lane's copies; the barrier covers the others'
+        for (int k = 0; k < kStages - 1; ++k) flags[k] = feeder.feed(ring + k * kSlot);
+        if (!kSharedQ || warp < NT) {
+            const float f = make_query<E2M1>(a.q[0]);
+            if (kSharedQ) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sm_q[(warp * 4 + j) * 32 + lane] = make_uint4(a.q[0][4 * j], a.q[0][4 * j + 1], a.q[0][4 * j + 2], a.q[0][4 * j + 3]);
+                if (t == 0) sm_f[8 * warp + g] = f;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a.rs[0][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
+            }
+        }
+        if (kSharedQ) __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (kSharedQ) a.rs[n][e] = p.qscale * sm_f[8 * n + 2 * t + e];
+                a.bias[n][e] = kNoRef;
+                a.l[n][e] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
+        }
+        a.sq = smem_addr(sm_q) + 16 * lane;
+
+        uint32_t slot = ring, into = ring + (kStages - 1) * kSlot;
+        while (flags[0] >> U) {
+            cp_async_wait_stages<kStages - 1>();   // this lane's copies; the barrier covers the others'
             __syncwarp();
             flags[kStages - 1] = feeder.feed(into);
-            if (turn == -1) {   // the first units are on their way
-                slot = ring;
-                if (!kSharedQ || warp < NT) {
-                    const float f = make_query<E2M1>(a.q[0]);
-                    if (kSharedQ) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            sm_q[(warp * 4 + j) * 32 + lane] = make_uint4(a.q[0][4 * j], a.q[0][4 * j + 1], a.q[0][4 * j + 2], a.q[0][4 * j + 3]);
-                        if (t == 0) sm_f[8 * warp + g] = f;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) a.rs[0][e] = p.qscale * __shfl_sync(kFull, f, (2 * t + e) * 4);
-                    }
-                }
-                if (kSharedQ) __syncthreads();   // (every warp comes here: the first turns feed, tiles or not)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (kSharedQ) a.rs[n][e] = p.qscale * sm_f[8 * n + 2 * t + e];
-                        a.bias[n][e] = kNoRef;
-                        a.l[n][e] = 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a.o[n][i][e] = 0.f;
-                }
-                a.sq = smem_addr(sm_q) + 16 * lane;
-            }
-            if (turn >= 0) {
-                const uint32_t edge = flags[0] & ((1u << U) - 1);
-                if (edge == 0) {
-                    attend<U, false, typename S::Unit>(p, a, slot, 0, r0, seen);
+            const uint32_t edge = flags[0] & ((1u << U) - 1);
+            if (edge == 0) {
+                attend<U, false, typename S::Unit>(p, a, slot, 0, r0, seen);
+            } else {
+                bool apart = false;
+#pragma unroll 1
+                for (int u = 0; u < U && p.Mq > 1; ++u)
+                    if ((edge >> (U - 1 - u)) & 1u) apart |= late_not_finite<typename S::Unit, E2M1>(slot, u, seen);
+                if (!apart) {
+                    attend<U, true, typename S::Unit>(p, a, slot, edge, r0, seen);
                 } else {
-                    bool apart = false;
 #pragma unroll 1
                     for (int u = 0; u < U; ++u)
-                        if ((edge >> (U - 1 - u)) & 1u) apart |= late_not_finite<typename S::Unit, E2M1>(slot, u, seen);
-                    if (!apart) {
-                        attend<U, true, typename S::Unit>(p, a, slot, edge, r0, seen);
-                    } else {
-#pragma unroll 1
-                        for (int u = 0; u < U; ++u)
-                            attend_apart<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
-                    }
+                        attend_apart<typename S::Unit>(p, a, slot, u, r0, seen, ((edge >> (U - 1 - u)) & 1u) == 0);
                 }
-                slot = slot + kSlot == ring + S::kRing ? ring : slot + kSlot;
             }
-            into = into + kSlot == ring + S::kRing ? ring : into + kSlot;
+            into = slot;
+            slot = slot + kSlot == ring + S::kRing ? ring : slot + kSlot;
 #pragma unroll
             for (int k = 0; k < kStages - 1; ++k) flags[k] = flags[k + 1];
         }
@@ -1573,14 +1573,14 @@ cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done)
     return e;
 }
 
-template <bool E2M1, int NT, bool DUP>
+template <bool E2M1, int NT, bool DUP, int U>
 cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    using S = Shape<E2M1, NT, DUP>;
+    using S = Shape<E2M1, NT, DUP, U>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(paged_decode_kernel<E2M1, NT, DUP>, S::kSmem, done);
+    const cudaError_t e = allow_smem(paged_decode_kernel<E2M1, NT, DUP, U>, S::kSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_kernel(paged_decode_kernel<E2M1, NT, DUP>, dim3(S::kCtas * sm_count), dim3(32 * S::kWarps), S::kSmem, s,
+    return launch_kernel(paged_decode_kernel<E2M1, NT, DUP, U>, dim3(S::kCtas * sm_count), dim3(32 * S::kWarps), S::kSmem, s,
                          pdl, 0u, p);
 }
 
@@ -1606,14 +1606,17 @@ size_t paged_decode_workspace_bytes(int R, int sm_count)
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    if (e2m1) {
-        if (p.R <= 4) return launch_decode<true, 1, true>(p, sm_count, pdl, s);
-        if (p.R <= 8) return launch_decode<true, 1, false>(p, sm_count, pdl, s);
-        return launch_decode<true, 2, false>(p, sm_count, pdl, s);
+    if (!e2m1) {
+        if (p.R <= 4) return launch_decode<false, 1, true, 1>(p, sm_count, pdl, s);
+        if (p.R <= 8) return launch_decode<false, 1, false, 1>(p, sm_count, pdl, s);
+        return launch_decode<false, 2, false, 1>(p, sm_count, pdl, s);
     }
-    if (p.R <= 4) return launch_decode<false, 1, true>(p, sm_count, pdl, s);
-    if (p.R <= 8) return launch_decode<false, 1, false>(p, sm_count, pdl, s);
-    return launch_decode<false, 2, false>(p, sm_count, pdl, s);
+    if (p.R > 8) return launch_decode<true, 2, false, 2>(p, sm_count, pdl, s);
+    // tiles a warp may get, if every sequence fills its pages
+    const int64_t most = (int64_t)p.c.B * p.c.Hkv * ((p.c.cap + p.kk) / kTileRows) / (12 * sm_count);
+    if (most <= kShort || p.c.page_mask < 2 * kTileRows - 1)
+        return p.R <= 4 ? launch_decode<true, 1, true, 1>(p, sm_count, pdl, s) : launch_decode<true, 1, false, 1>(p, sm_count, pdl, s);
+    return p.R <= 4 ? launch_decode<true, 1, true, 2>(p, sm_count, pdl, s) : launch_decode<true, 1, false, 2>(p, sm_count, pdl, s);
 }
 
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)

@@ -503,6 +503,53 @@ def test_long_lists_and_tails_over_many_ctas(fx, fmt, page):
     check_out(out, lse, pr.attend(c, q, 128 ** -0.5, idx, tail))
 
 
+ROOM = 1 << 19   # rows a sequence may grow to: 4-bit attention then takes tiles in pairs
+
+
+@pytest.mark.parametrize("G,Mq,Hkv,page,layout,ql", [
+    (2, 1, 3, 32, "row", "token"), (3, 1, 1, 64, "gap", "head"), (4, 1, 2, 128, "head", "token"), (8, 1, 1, 256, "gap", "head"),
+    (1, 4, 2, 32, "head", "head"), (2, 4, 1, 64, "row", "token"), (7, 1, 1, 1024, "head", "head"), (5, 1, 1, 16, "head", "token"),
+])
+def test_decode_with_room_to_grow(fx, G, Mq, Hkv, page, layout, ql):
+    lens = LENS + [1000, 32, 31, 47]
+    c = pr.Cache("e2m1", lens, Hkv, page, seed=G + Mq, layout=layout, exps=(1, -2), max_pages=ROOM // page)
+    q, qt = queries(c, G, Mq, G + Mq, layout=ql)
+    dev = c.device(fx)
+    out, lse = fx.fx_paged_decode(dev, qt, want_lse=True)
+    check_out(out, lse, pr.attend(c, q, 128 ** -0.5))
+    g = np.random.default_rng(page)
+    for k, tail in ((5, 7), (33, 40), (0, 100), (16, 0)):
+        idx = np.stack([g.integers(0, max(n, 1), (Hkv, k)) for n in lens])
+        idx[0] = -1                                                    # (an empty sequence has no row to list)
+        lo = np.array([max(0, n - tail) for n in lens])
+        out, lse = fx.fx_paged_decode(dev, qt, cu(idx, torch.int32) if k else None, cu(lo, torch.int32), want_lse=True)
+        assert fx.fx_device_errors() == (fx.FX_DEVERR_INDEX if k else 0)
+        check_out(out, lse, pr.attend(c, q, 128 ** -0.5, idx if k else None, lo))
+
+
+def test_decode_with_room_unseen_and_long_rows(fx):
+    c = pr.Cache("e2m1", [40, 33, 700, 64], 1, 32, seed=2, max_pages=ROOM // 32)
+    q, qt = queries(c, 2, 4, 3)
+    ref = pr.attend(c, q, 128 ** -0.5)
+    dev = c.device(fx)
+    for b in range(4):                                                 # the row of query 2: NaN
+        pg, row = c.spot(b, c.lens[b] - 2)
+        dev.v_scale[pg, :, row] = 0x7f
+    out, lse = fx.fx_paged_decode(dev, qt, want_lse=True)
+    check_out(out[:, :, :2], lse[:, :, :2], tuple(x[:, :, :2] for x in ref))
+    assert torch.isnan(out[:, :, 2:]).all()
+    g = np.random.default_rng(3)
+    lens = [int(x) for x in g.integers(0, 90, 150)] + [5000, 2047]
+    for Hkv, G, Mq in ((2, 4, 1), (1, 2, 3)):
+        c = pr.Cache("e2m1", lens, Hkv, 64, seed=G, max_pages=ROOM // 64, garbage=False)
+        q, qt = queries(c, G, Mq, 1)
+        dev = c.device(fx)
+        out, lse = fx.fx_paged_decode(dev, qt, want_lse=True)
+        check_out(out, lse, pr.attend(c, q, 128 ** -0.5))
+        o2, l2 = fx.fx_paged_decode(dev, qt, want_lse=True)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 # ---------------------------------------------------------------------------------------- importance
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("G,Mq,Hkv,page,cand", [(2, 1, 2, 16, None), (4, 1, 1, 64, (5, 301)), (1, 8, 1, 32, (0, 1)),
