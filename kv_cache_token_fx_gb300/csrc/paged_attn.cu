@@ -33,8 +33,8 @@ namespace fx {
 namespace {
 
 constexpr int kTileRows = 16;
-constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call (decode of 8 x 4864 4-bit rows:
-                                // 16.7 us with 1 or 2, 17.1 with 8)
+constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call (decode of 1024 4-bit rows of one
+                                // sequence: 8.0 us with 1, 7.7 with 2, 8.7 with 4)
 constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
 // 4 bits, up to 8 query rows: tiles a warp may get at most for units of one tile instead of two (512 heads' 40 rows, a
@@ -1390,19 +1390,29 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
                         m[k] = mx;
                     }
                     const int n = min(32, n_part - c1);
-#pragma unroll 4
-                    for (int c = 0; c < n; ++c) {
-                        const int at = c1 + c;
-                        const float* from = p.part + (size_t)(at == 0 ? line.slot0 : (line.c0 + at) * 2) * kPart;
+                    constexpr int kBatch = 16 / kMine;   // parts under way together (a divisor of 32)
+#pragma unroll 1
+                    for (int c = 0; c < n; c += kBatch) {
+                        float4 o[kBatch][kMine];
 #pragma unroll
-                        for (int k = 0; k < kMine; ++k) {
-                            const float4 o = __ldcg(reinterpret_cast<const float4*>(from + (warp + k * W) * kHeadDim) + lane);
-                            const float w = __shfl_sync(kFull, f[k], c);
-                            acc[k].x += w * o.x;
-                            acc[k].y += w * o.y;
-                            acc[k].z += w * o.z;
-                            acc[k].w += w * o.w;
+                        for (int u = 0; u < kBatch; ++u) {
+                            const int at = c1 + c + u;
+                            const float* from = p.part + (size_t)(at == 0 ? line.slot0 : (line.c0 + at) * 2) * kPart;
+#pragma unroll
+                            for (int k = 0; k < kMine; ++k)
+                                o[u][k] = c + u < n ? __ldcg(reinterpret_cast<const float4*>(from + (warp + k * W) * kHeadDim) + lane)
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                            for (int k = 0; k < kMine; ++k) {
+                                const float w = __shfl_sync(kFull, f[k], c + u);   // (0 past the last part)
+                                acc[k].x += w * o[u][k].x;
+                                acc[k].y += w * o[u][k].y;
+                                acc[k].z += w * o[u][k].z;
+                                acc[k].w += w * o[u][k].w;
+                            }
                     }
                 }
 #pragma unroll
@@ -1414,6 +1424,10 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
     }
 }
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
 constexpr int kImpWarps = 4;
 constexpr int kImpSecond = 32;
 __host__ __device__ constexpr int imp_stages(bool e2m1) { return e2m1 ? 2 : 3; }   // units in a warp's ring
@@ -1501,37 +1515,44 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                 }
             }
             float sum[U][2] = {};
+            auto add = [&](auto masked) {
+                constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll 1
-            for (int n = 0; n < nq; ++n) {
-                float s[U][2][4];
+                for (int n = 0; n < nq; ++n) {
+                    float s[U][2][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 q = sq[(n * 4 + j) * 32 + lane];
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 q = sq[(n * 4 + j) * 32 + lane];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const uint32_t(&x)[4] = a[u][j][0], (&y)[4] = a[u][j][1];
-                        if (j == 0) {
-                            mma16_zero<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
-                            mma16_zero<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
-                        } else {
-                            mma16<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
-                            mma16<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
+                        for (int u = 0; u < U; ++u) {
+                            const uint32_t(&x)[4] = a[u][j][0], (&y)[4] = a[u][j][1];
+                            if (j == 0) {
+                                mma16_zero<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
+                                mma16_zero<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
+                            } else {
+                                mma16<E2M1>(s[u][0], x[0], x[1], x[2], x[3], q.x, q.y);
+                                mma16<E2M1>(s[u][1], y[0], y[1], y[2], y[3], q.z, q.w);
+                            }
                         }
                     }
+                    const float4 f = *reinterpret_cast<const float4*>(&sf[8 * n + 2 * t]);   // rows 2t, 2t + 1
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float x = fmaf(s[u][0][e] + s[u][1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
+                            if (MASKED) {
+                                const int row = pos[u][e >> 1];
+                                if (row < 0 || row > seen + query_pos(p, 8 * n + 2 * t + (e & 1))) x = -INFINITY;
+                            }
+                            sum[u][e >> 1] += fast_exp2(x);
+                        }
                 }
-                const float4 f = *reinterpret_cast<const float4*>(&sf[8 * n + 2 * t]);   // rows 2t, 2t + 1
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[u][0][e] + s[u][1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
-                        if (edges != 0) {
-                            const int row = pos[u][e >> 1];
-                            if (row < 0 || row > seen + query_pos(p, 8 * n + 2 * t + (e & 1))) x = -INFINITY;
-                        }
-                        sum[u][e >> 1] += fast_exp2(x);
-                    }
-            }
+            };
+            if (edges == 0)
+                add(Flag<false>());
+            else
+                add(Flag<true>());
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
