@@ -520,7 +520,7 @@ FX_API fx_status fx_paged_gather(const fx_paged_desc* cache, const int32_t* idx,
  *   q         bf16 rows (b, g, i) at q + b*q_stride_b + g*q_stride_h + i*q_stride_i
  *   tail_lo   int32 [B] (device) or NULL, which means 0; a negative value sets FX_DEVERR_LEN and counts as 0
  *   out [B, Hq, Mq, 128] fp32, lse [B, Hq, Mq] fp32 or NULL;  G*Mq <= 64, scale finite
- * B*Hkv*(G*Mq/4 + 1)*(max_pages*page_rows + k)/16, the tiles of 16 rows a call may take, is below 2^31.
+ * B*Hkv*(G*Mq/4 + 1)*((max_pages*page_rows + k)/16 + 34), what a call may have to count, is below 2^31.
  * Workspace: fx_paged_decode_workspace_bytes(B, Hkv, Hq, Mq) bytes.
  */
 FX_API size_t fx_paged_decode_workspace_bytes(int B, int Hkv, int Hq, int Mq);

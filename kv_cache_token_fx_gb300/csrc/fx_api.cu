@@ -1084,9 +1084,9 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
     if (!row_stride_ok(q_stride_b) || !row_stride_ok(q_stride_h) || !row_stride_ok(q_stride_i))
         return fail(FX_ERR_INVALID_ARG, "q strides must be non-negative multiples of 8 elements");
     if (!isfinite(scale)) return fail(FX_ERR_INVALID_ARG, "scale must be finite");
-    // the kernels count the tiles of 16 rows of all (sequence, KV head, 4 or more query rows) in 32 bits, and 16 for the
-    // start of each
-    const int64_t tiles = p->c.cap / 16 + k / 16 + 18, groups = (int64_t)(Hq / cache->Hkv) * Mq / 4 + 1;
+    // the kernels count the tiles of 16 rows of all (sequence, KV head, 4 or more query rows), and the starts of these, in
+    // 32 bits
+    const int64_t tiles = p->c.cap / 16 + k / 16 + 2 + kPieceStart, groups = (int64_t)(Hq / cache->Hkv) * Mq / 4 + 1;
     if (tiles * cache->B * cache->Hkv >= ((int64_t)1 << 31) / groups)
         return fail(FX_ERR_UNSUPPORTED, "more than 2^31 tiles of 16 rows over all sequences and heads");
     p->q = q;

@@ -42,15 +42,25 @@ constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row g
 // rows, 144 tiles: 99 against 85).  Pages of 16 rows hold no pair of neighbours: always one (64 heads' 4864 rows 14.8 us
 // against 16.3, 38912 rows 73 against 76).
 constexpr int kShort = 16;
-// Where every CTA can take one part of one piece, parts this many tiles longer than an even share are better than a
-// second piece for some CTAs (8 x 4864 4-bit rows: 16.7 us against 20.1 with even shares; 16 x 32768: 89.6 against 91.4).
-constexpr int kSecondPiece = 48;
-// In a line the start of a piece counts as this many tiles: its first rows, queries and join take 7 us, a tile of a CTA
-// 0.22 us.  64 sequences of up to 40 rows: 17 us against 54 without; of up to 3335, 14 query rows: 80 us against 85 with
-// 16, 82 with 48 and 94 without.
-constexpr int kStart = 32;
-constexpr int kNear = 16;       // tiles between a cut and an end of a piece, at least (those 3335 rows: 91 us with 8, 90 with
-                                // 16, 92 with 32, 95 without, before the start of a piece counted)
+// What a piece costs a CTA besides its tiles -- its first rows and queries, its join: 5 to 10 us -- counted in tiles.
+struct LineCost {
+    int second;   // parts this much longer than an even share are better than a second piece for some CTAs
+    int start;    // the start of a piece in a line
+    int near;     // between a cut and an end of a piece, at least
+};
+// Decode, 4 bits (a tile of a CTA takes 0.2 us).  second: 16 x 32768 rows 89.6 us against 91.4 with 32, 8 x 4864 rows 16.7
+// against 20.1 with 0.  start: 64 sequences of up to 3335 rows, 14 query rows: 80 us against 85 with 16, 82 with 48, 90
+// without; of up to 40 rows: 17 us against 29 without.  near (before start counted): those 3335 rows 90 us, 91 with 8, 92
+// with 32, 95 without.
+// bf16 (a tile is 3.5 times the bytes): 64 sequences of up to 1000 rows, 14 query rows: 46.6 us against 51.8 with a start
+// of 32 and near of 16; 1667 rows, 2 query rows: 51.6 us against 52.2, and 53.2 with 8 and 4.
+__host__ __device__ constexpr LineCost decode_cost(bool e2m1) { return e2m1 ? LineCost{48, 32, 16} : LineCost{48, 16, 8}; }
+// Importance has no join, so cuts may fall anywhere (64 x 2000 4-bit rows: 20.6 us against 21.9 with near = 16; bf16:
+// 34.1 us against 38.1 with 32 and 16).
+__host__ __device__ constexpr LineCost importance_cost(bool e2m1) { return LineCost{32, e2m1 ? 32 : 8, 1}; }
+static_assert(decode_cost(true).start <= kPieceStart && decode_cost(false).start <= kPieceStart &&
+                  importance_cost(true).start <= kPieceStart && importance_cost(false).start <= kPieceStart,
+              "lines are counted in 32 bits");
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
@@ -940,7 +950,7 @@ struct Line {
     const PagedAttnParams& p;
     const Count count;         // tiles of a sequence's piece, at least 1
     const int per_seq;         // pieces of one sequence
-    const int second;          // equal parts may be this many tiles longer than the ideal share
+    const LineCost cost;
     Seq seq;
     int b, ntile;              // the sequence, tiles of its pieces
     int piece, s0, s1;         // the piece of the sequence, this CTA's tiles of it
@@ -948,8 +958,8 @@ struct Line {
     int part;                  // which of them this is
     int slot;                  // this CTA's partial slot
 
-    __device__ __forceinline__ Line(const PagedAttnParams& p_, Count count_, int per_seq_, int second_)
-        : p(p_), count(count_), per_seq(per_seq_), second(second_)
+    __device__ __forceinline__ Line(const PagedAttnParams& p_, Count count_, int per_seq_, LineCost cost_)
+        : p(p_), count(count_), per_seq(per_seq_), cost(cost_)
     {
     }
 
@@ -983,12 +993,12 @@ struct Line {
             for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, d));
             const unsigned who = __ballot_sync(kFull, longest == best);
             inv = __shfl_sync(kFull, inv, __ffs(who) - 1);
-            if (!(best <= ideal + second)) inv = 0.f;
+            if (!(best <= ideal + cost.second)) inv = 0.f;
         }
         at = cta;
         end = cta + 1;
         if (inv == 0.f) {
-            total += p.c.B * per_seq * kStart;
+            total += p.c.B * per_seq * cost.start;
             quota = total / n_cta;
             extra = total - quota * n_cta;
             at = place(cta);
@@ -1019,7 +1029,7 @@ struct Line {
             total *= per_seq;
             choose(B, [&](int i) { return __shfl_sync(kFull, mine, i); });
             if (inv == 0.f && cta >= n_cta) return false;
-            const int n = lane < B ? (inv == 0.f ? mine + kStart : parts(mine)) : 0;
+            const int n = lane < B ? (inv == 0.f ? mine + cost.start : parts(mine)) : 0;
             int inc = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -1062,7 +1072,7 @@ struct Line {
                 const int i = b0 + tid;
                 if (b0 > 0 && i < B) seq = sequence(p, i, false);
                 const int c = b0 == 0 ? n_first : (i < B ? count(seq) : 0);
-                const int n = i < B ? (inv == 0.f ? c + kStart : parts(c)) : 0;
+                const int n = i < B ? (inv == 0.f ? c + cost.start : parts(c)) : 0;
                 int inc = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -1097,7 +1107,7 @@ struct Line {
         }
         seq.table = p.c.table + (int64_t)b * p.c.table_stride;
         ntile = count(seq);
-        if (inv == 0.f) at -= (at - seq_start) % (ntile + kStart);   // the start of its first piece
+        if (inv == 0.f) at -= (at - seq_start) % (ntile + cost.start);   // the start of its first piece
         return true;
     }
 
@@ -1107,18 +1117,18 @@ struct Line {
         if (inv == 0.f) {
             for (;;) {
                 if (at >= end) return false;
-                while (at >= seq_start + (ntile + kStart) * per_seq) {
-                    seq_start += (ntile + kStart) * per_seq;
+                while (at >= seq_start + (ntile + cost.start) * per_seq) {
+                    seq_start += (ntile + cost.start) * per_seq;
                     seq = sequence(p, ++b, false);
                     ntile = count(seq);
                 }
                 // a cut near an end of the piece moves there, all cuts of a short piece do: no CTA comes for a few
                 // tiles, and a piece of one CTA has no parts to join
-                const int near = min(kNear, ntile / 2), from = at + kStart;
+                const int near = min(cost.near, ntile / 2), from = at + cost.start;
                 c0 = owner(from + near);
                 n_part = owner(max(from + ntile - near - 1, from + near)) - c0 + 1;
-                piece = (at - seq_start) / (ntile + kStart);
-                at += ntile + kStart;
+                piece = (at - seq_start) / (ntile + cost.start);
+                at += ntile + cost.start;
                 part = cta - c0;
                 if (part < 0 || part >= n_part) continue;
                 s0 = part == 0 ? 0 : place(cta) - from;
@@ -1162,10 +1172,10 @@ __device__ __forceinline__ int warp_start(const Seq& q, int s0, int s1, int w)
 // Shape of the decode kernel for a format and up to 4 (DUP), 8 or 16 query rows a pass.
 //
 // bf16: bound by bytes.  A tile is 8 KB, and the rings of 8 warps fill the shared memory of an SM (8 x 32768 rows,
-// 755 MB: 118 us, 0.94 of the copy bandwidth; rings of 4 units instead of 3: 128 us).
+// 755 MB: 117 us, 0.95 of the copy bandwidth; rings of 4 units instead of 3: 128 us).
 // 4 bits: a tile is 2.3 KB and takes 310 instructions of a warp, of which 64 are conversions of codes and 64 their
 // scaling (the conversion issues every second cycle): bound by the issue of instructions and their latency.  As many
-// warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 85 us, 0.71 of the copy
+// warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 84 us, 0.72 of the copy
 // bandwidth; with 2 CTAs 7% longer), 2 CTAs for 16 rows (3 spill, and gain nothing).  Two tiles at a time share the loads
 // of the queries and the additions to O; where a warp gets few tiles, one at a time is sooner done (kShort).  DUP: 90 us
 // against 105 for up to 4 rows.  One pass of 16 rows instead of two of 8: 94 us
@@ -1209,7 +1219,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const int nrg = (p.R + kRows - 1) / kRows;
     auto tiles = [](const Seq& q) { return tile_count(q); };
-    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv * nrg, kSecondPiece);
+    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv * nrg, decode_cost(E2M1));
     if (!line.start(sm_line)) return;
 
     while (line.next()) {
@@ -1429,17 +1439,15 @@ struct Flag {
     static constexpr bool value = B;
 };
 constexpr int kImpWarps = 4;
-constexpr int kImpSecond = 32;
 __host__ __device__ constexpr int imp_stages(bool e2m1) { return e2m1 ? 2 : 3; }   // units in a warp's ring
 __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
-// Importance.  4 bits: bound by the issue of instructions (4 x 32768 rows, 32 query rows: 32.7 us, 177 instructions a
-// tile and 55 more for each 8 query rows; 4 query rows: 18 us, 49 MB; 2 CTAs an SM instead of 3: 35 us).  bf16: by bytes
-// and the start (8 x 4864 rows, 2 query rows: 11.7 us for 46 MB; rings of 2 units instead of 3: 12.5 us, of 4, with
-// fewer CTAs: 16 us).  Pieces are (sequence, KV head)s; the query fragments of a piece lie in shared memory as the products
-// want them, and each of them serves a unit of tiles at a time.  Rows of the fragments that
-// add nothing -- beyond the last query row, or with an lse of -inf, whatever the query holds -- are zeros and add
-// 2^-inf.
+// Importance.  4 bits: bound by the issue of instructions (4 x 32768 rows, 49 MB, 32 query rows: 28.8 us, 4 query rows:
+// 17.8; 2 CTAs an SM instead of 3: 10% longer).  bf16: by bytes and the start (8 x 4864 rows, 2 query rows: 11.7 us for
+// 46 MB; rings of 2 units instead of 3: 12.5 us, of 4, with fewer CTAs: 16 us).  Pieces are (sequence, KV head)s; the
+// query fragments of a piece lie in shared memory as the products want them, and each of them serves a unit of tiles
+// at a time.  Rows of the fragments that add nothing -- beyond the last query row, or with an lse of -inf, whatever the
+// query holds -- are zeros and add 2^-inf.
 template <bool E2M1>
 __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importance_kernel(const PagedAttnParams p)
 {
@@ -1455,7 +1463,7 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
     const uint32_t ring = smem_addr(sq + nq * 128) + warp * kImpStages * S::kBytes, ring_end = ring + kImpStages * S::kBytes;
     const int base = p.cand_lo & ~(2 * kTileRows - 1);                       // first row of the first tile
     auto tiles = [&](const Seq& q) { return max((min(q.len, p.cand_hi) - base + kTileRows - 1) / kTileRows, 1); };
-    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv, kImpSecond);
+    Line<W, decltype(tiles)> line(p, tiles, p.c.Hkv, importance_cost(E2M1));
     if (!line.start(sm_line)) return;
 
     while (line.next()) {

@@ -118,6 +118,8 @@ def test_decode_and_importance_refusals(lib):
     d = ctypes.byref(desc(B=65535, Hkv=65535))              # 4e9 heads: their tiles are not counted in 32 bits
     assert dec(Hq=65535, Mq=1) == 2 and b"tiles" in lib.fx_last_error()
     assert lib.fx_paged_importance(d, 256, 0, 0, 0, 65535, 1, 256, 1.0, 0, 1, 256, 0, None) == 2
+    d = ctypes.byref(desc(B=65535, Hkv=1000, max_pages=1, page_rows=16))   # few rows, but too many starts
+    assert dec(Hq=1000, Mq=1) == 2 and b"tiles" in lib.fx_last_error()
     d = ctypes.byref(desc(B=64, Hkv=64))
     assert dec(Hq=64, Mq=1, idx=256, k=1 << 29) == 2 and b"tiles" in lib.fx_last_error()
 
