@@ -570,6 +570,7 @@ class PagedKV:
 # The current stream's handle without a Stream object around it (3 us against 0.1).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # (CUDA is up: a cache exists)
 _ROWS = struct.Struct("@PPqqPPqqqqPPPPiiiiixxxx")   # PagedRows
 assert _ROWS.size == ctypes.sizeof(PagedRows)
 
@@ -599,9 +600,8 @@ def _paged_view(cache, t, name, shape):
         if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == cache._index:
             st = t.stride()
             if st[-1] == 1:
-                for i in st[:-1]:
-                    if i & 7:
-                        return t.data_ptr(), _strides(t)   # (the library refuses what then still is no multiple of 8)
+                if (st[0] | st[1] | st[-2]) & 7:   # (views of 3 or 4 dimensions)
+                    return t.data_ptr(), _strides(t)   # (the library refuses what then still is no multiple of 8)
                 return t.data_ptr(), st
             raise FxError(FX_ERR_INVALID_ARG, f"{name} must have unit last stride")
     except AttributeError:
@@ -614,7 +614,7 @@ def _paged_launch(cache, stream):
     """(library, stream handle) of a call on the cache, which must live on the current device."""
     if type(cache) is not PagedKV and not isinstance(cache, PagedKV):
         raise FxError(FX_ERR_INVALID_ARG, "cache must be a PagedKV")
-    if torch.cuda.current_device() != cache._index:
+    if _current_device() != cache._index:
         raise FxError(FX_ERR_INVALID_ARG, f"the cache is on {cache.device}, the current device is another one")
     if stream is None:
         return _lib or load_library(), _raw_stream(cache._index)

@@ -1119,7 +1119,8 @@ struct Line {
                 if (at >= end) return false;
                 while (at >= seq_start + (ntile + cost.start) * per_seq) {
                     seq_start += (ntile + cost.start) * per_seq;
-                    seq = sequence(p, ++b, false);
+                    if (++b >= p.c.B) return false;   // (lengths that change during the call)
+                    seq = sequence(p, b, false);
                     ntile = count(seq);
                 }
                 // a cut near an end of the piece moves there, all cuts of a short piece do: no CTA comes for a few
