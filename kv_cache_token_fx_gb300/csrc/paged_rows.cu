@@ -3,7 +3,7 @@
 //
 // Both move rows of 128 values and compute a few operations a value.  Bytes bound the long gather (4 x 32768 4-bit rows
 // to bf16, 447 MB: 70 us, 0.94 of the copy bandwidth); the quantisation's instructions and bytes together the long
-// append (24 K tokens, 4 bits, with 32 query heads: 80% of the copy bandwidth, with the rows read back); start-up the
+// append (24 K tokens, 4 bits, with 32 query heads: 0.92 of the copy bandwidth, with the rows read back); start-up the
 // decode step's few rows (2.2 us for one token of a sequence).
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -13,7 +13,7 @@
 namespace fx {
 namespace {
 
-constexpr int kThreadsRows = 256;
+constexpr int kThreadsRows = 128;
 constexpr int kCopyRows = kThreadsRows / 16;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -71,8 +71,10 @@ __device__ __forceinline__ uint32_t quantize_chunk(uint4 x, float inv, uint32_t&
 // 8 lanes take R rows of one token -- K heads, V heads or query heads -- and of each row two chunks of 8 values:
 // chunks c0 and c1, which are the two sides of 8 rotated pairs in the half-split form.  The rows' loads need
 // neither the token's place nor its position and go out first, and the rows share its cosines and sines.
+// 8 CTAs of 128 threads an SM (64 registers), and queries and new rows that pass by L2's older contents when there are
+// many: a prompt of 24 K tokens, 4 bits, with its read-back 90 us, against 105 without either and 112 with 10 CTAs.
 template <bool E2M1, int R, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreadsRows) paged_append_kernel(const PagedAppendParams p)
+__global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const PagedAppendParams p)
 {
     griddep_wait();
     griddep_launch();
@@ -95,8 +97,9 @@ __global__ void __launch_bounds__(kThreadsRows) paged_append_kernel(const PagedA
         for (int r = 0; r < R; ++r) {
             x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
             if (r < rows) {
-                x[r][0] = *reinterpret_cast<const uint4*>(src + 8 * c0);   // q_out may be q: not read-only loads
-                x[r][1] = *reinterpret_cast<const uint4*>(src + 8 * c1);
+                // (q_out may be q: not read-only loads)
+                x[r][0] = R > 1 ? __ldcs(reinterpret_cast<const uint4*>(src + 8 * c0)) : *reinterpret_cast<const uint4*>(src + 8 * c0);
+                x[r][1] = R > 1 ? __ldcs(reinterpret_cast<const uint4*>(src + 8 * c1)) : *reinterpret_cast<const uint4*>(src + 8 * c1);
             }
             src += step;
         }
@@ -172,8 +175,13 @@ __global__ void __launch_bounds__(kThreadsRows) paged_append_kernel(const PagedA
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r < rows) {
-                *reinterpret_cast<uint4*>(to + 8 * c0) = x[r][0];
-                *reinterpret_cast<uint4*>(to + 8 * c1) = x[r][1];
+                if (R > 1) {
+                    __stcs(reinterpret_cast<uint4*>(to + 8 * c0), x[r][0]);
+                    __stcs(reinterpret_cast<uint4*>(to + 8 * c1), x[r][1]);
+                } else {
+                    *reinterpret_cast<uint4*>(to + 8 * c0) = x[r][0];
+                    *reinterpret_cast<uint4*>(to + 8 * c1) = x[r][1];
+                }
             }
             to += p.qo_h;
         }
@@ -287,7 +295,8 @@ cudaError_t append(const PagedAppendParams& p, bool pdl, cudaStream_t s)
 {
     // A decode step's few rows: one row each, for the shortest way through (a step of 64 sequences with its read-back
     // 4.5 us, against 5.8 with four).  More rows than the machine has groups of 8 lanes: four rows each, for their shared
-    // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 105 us, against 127 with one).
+    // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 105 us, against 127 with one, before the
+    // registers were bounded).
     const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > 152 * 2048 / 8;
     const int R = many ? 4 : 1;
     const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
