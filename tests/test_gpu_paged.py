@@ -788,6 +788,41 @@ def test_chained_launches_and_other_streams_give_the_same_bits(fx, fmt):
     assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_pools_past_32_bits(fx, fmt, heads_first):
+    """Pages, or heads, more than 4 GiB from the pool's start: the same bits as from a small pool."""
+    c = pr.Cache(fmt, [150, 70, 333], 2, 64, seed=8, garbage=False)
+    small = c.device(fx)
+    N = 140000 if fmt == "bf16" else 560000
+    n = c.n_pages
+
+    def far(t):
+        shape = (2, N) + t.shape[2:] if heads_first else (N, 2) + t.shape[2:]
+        big = torch.empty(shape, dtype=t.dtype, device="cuda")
+        big = big.transpose(0, 1) if heads_first else big
+        big[N - n:] = t.flip(0)
+        return big
+    k = far(small.k)
+    assert k[N - n, 1].data_ptr() - k.data_ptr() > 1 << 32             # the last head's rows
+    kw = {} if fmt == "bf16" else dict(k_scale=far(small.k_scale), v_scale=far(small.v_scale), k_exp=c.exps[0], v_exp=c.exps[1])
+    table = torch.where((small.table >= 0) & (small.table < n), N - 1 - small.table, small.table)
+    dev = fx.PagedKV(k, far(small.v), table, small.length, **kw)
+    g = np.random.default_rng(0)
+    x = cu(pr.bf16(g.standard_normal((3, 4, D))), torch.bfloat16)
+    q, qt = queries(c, 3, 2, 1)
+    idx = cu(np.stack([np.stack([g.integers(0, m, 40) for _ in range(2)]) for m in c.lens]), torch.int32)
+    got = []
+    for cache in (small, dev):
+        fx.fx_paged_append(cache, x[:, :2], x[:, 2:], cu([0, 1, 2], torch.int32), cu([140, 3, 332], torch.int32))
+        out, lse = fx.fx_paged_decode(cache, qt, want_lse=True)
+        some = fx.fx_paged_decode(cache, qt, idx, cu([120, 70, 300], torch.int32))
+        rows = [torch.zeros(3, 2, 333, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        fx.fx_paged_gather(cache, 333, k_out=rows[0], v_out=rows[1])
+        got.append([out, lse, some, fx.fx_paged_importance(cache, qt, lse), *fx.fx_paged_gather(cache, 40, idx=idx), *rows])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_binding_refusals(fx):
     c = pr.Cache("e2m1", [20], 2, 16, seed=1)
     dev = c.device(fx)
