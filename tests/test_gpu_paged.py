@@ -355,6 +355,33 @@ def test_decode_many_small_weights_count(fx, fmt):
         assert np.all(np.abs(o - r) <= tol), (drop, np.abs(o - r).max(), tol.max())
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("G,Mq", [(1, 1), (8, 1), (4, 4)])
+def test_weights_are_not_rounded_to_few_bits(fx, fmt, G, Mq):
+    """Logits that are exact up to the scale: what is left are the roundings of fp32 arithmetic.
+
+    In base 2 a logit is s * c + r with |s c| <= 10 * 0.09 * 1.45 < 1.4 and |r| <= 15: c is off by 2^-23 of itself (its
+    product and its rounding), the sum is rounded once below 16: 1.4 * 2^-23 + 2^-21 of the exponent, so ln 2 times
+    that, 2^-21.1, of a weight, and 2^-22 by the exponential: 2^-20.5.  Each part of a weight is exact to 2^-23 and
+    products and sums of few rows lose 2^-22 more, so a weight counts within 2^-19.8; numerator and denominator both
+    do, and the quotient's roundings are below 2^-22: outputs within 2^-18.8 of sum p |v|.  (Weights of 17 bits leave
+    some 2^-18.)"""
+    lens = [2, 3, 5, 16, 40]
+    c = pr.Cache(fmt, lens, 1, 16, seed=6)
+    g = np.random.default_rng(4)
+    keys = np.zeros(c.pool[0].shape)
+    keys[..., 0] = g.choice([-3.0, -2, -1.5, -1, -0.5, 0, 0.5, 1, 1.5, 2, 3], keys.shape[:-1])
+    c.pool[0] = keys
+    if fmt == "e2m1":
+        c.packed[0] = pr.quantize(keys)
+        c.pool[0] = pr.dequantize(*c.packed[0])          # (1 / 6 is no scale: these keys are a little off, and exact in 6 bits)
+    q = np.zeros((5, G, Mq, D))
+    q[..., 0] = pr.bf16(g.uniform(-3, 3, q.shape[:-1]))
+    out = fx.fx_paged_decode(c.device(fx), torch.from_numpy(q).to(torch.bfloat16).cuda(), scale=0.09)
+    r, _, mag, _, _ = pr.attend(c, q, np.float32(0.09).astype(np.float64))
+    assert np.all(np.abs(out.double().cpu().numpy() - r) <= 2.0 ** -18.8 * mag)
+
+
 def test_decode_tiny_and_huge_queries(fx):
     c = pr.Cache("e2m1", [70], 1, 16, seed=6)
     for mag in (2.0 ** -120, 2.0 ** -60, 2.0 ** 20, 2.0 ** 60):
