@@ -534,8 +534,8 @@ FX_API fx_status fx_paged_decode(const fx_paged_desc* cache, const fx_bf16* q, i
  *
  *   scores[b, h, t - cand_lo] = sum over the group's query heads g and positions i that see row t of
  *                               exp(scale * q_{g,i} . k_t - lse[b, g, i]),   cand_lo <= t < cand_hi
- * Rows t >= len[b] report 0, and query rows whose lse is -infinity add nothing.  Queries, strides, visibility
- * and limits as in fx_paged_decode.  scores [B, Hkv, cand_hi - cand_lo] fp32; 0 <= cand_lo <= cand_hi <=
+ * Rows t >= len[b] report 0, and query rows whose lse is -infinity add nothing, whatever they and the keys hold.
+ * Queries, strides, visibility and limits as in fx_paged_decode.  scores [B, Hkv, cand_hi - cand_lo] fp32; 0 <= cand_lo <= cand_hi <=
  * max_pages*page_rows.  No workspace.
  */
 FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b,

@@ -1448,7 +1448,8 @@ __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }  
 // 46 MB; rings of 2 units instead of 3: 12.5 us, of 4, with fewer CTAs: 16 us).  Pieces are (sequence, KV head)s; the
 // query fragments of a piece lie in shared memory as the products want them, and each of them serves a unit of tiles
 // at a time.  Rows of the fragments that add nothing -- beyond the last query row, or with an lse of -inf, whatever the
-// query holds -- are zeros and add 2^-inf.
+// query holds -- are zeros with a factor of 2^-inf.  Beside finite keys that is enough; tiles with an edge, and those whose
+// sums come out as NaN, leave such rows out one by one.
 template <bool E2M1>
 __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importance_kernel(const PagedAttnParams p)
 {
@@ -1552,16 +1553,27 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                             float x = fmaf(s[u][0][e] + s[u][1][e], e & 1 ? f.z : f.x, e & 1 ? f.w : f.y);
                             if (MASKED) {
                                 const int row = pos[u][e >> 1];
-                                if (row < 0 || row > seen + query_pos(p, 8 * n + 2 * t + (e & 1))) x = -INFINITY;
+                                if (row < 0 || row > seen + query_pos(p, 8 * n + 2 * t + (e & 1)) || (e & 1 ? f.w : f.y) == -INFINITY)
+                                    x = -INFINITY;
                             }
                             sum[u][e >> 1] += fast_exp2(x);
                         }
                 }
             };
-            if (edges == 0)
+            bool apart = edges != 0;
+            if (!apart) {
                 add(Flag<false>());
-            else
-                add(Flag<true>());
+                // 0 times a key's infinity or NaN is NaN: such a sum is formed again from the query rows that count
+                bool bad = false;
+#pragma unroll
+                for (int u = 0; u < U; ++u) bad |= sum[u][0] != sum[u][0] || sum[u][1] != sum[u][1];
+                apart = __any_sync(kFull, bad);
+                if (apart) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) sum[u][0] = sum[u][1] = 0.f;
+                }
+            }
+            if (apart) add(Flag<true>());
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
