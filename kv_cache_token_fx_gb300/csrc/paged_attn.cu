@@ -1456,7 +1456,8 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
     constexpr int U = E2M1 ? 2 : 1, W = kImpWarps, kImpStages = imp_stages(E2M1);
     using S = Slot<E2M1, false, U>;
     extern __shared__ __align__(128) uint4 sq[];     // [8-row tile][4][32], then the warps' rings
-    __shared__ float2 sf[kMaxRows];                  // factor of a row's logits, minus its lse (base 2)
+    __shared__ float4 sf[kMaxRows / 2];              // of two rows each: factor of the logits, minus the lse (base 2)
+    static_assert(alignof(decltype(sf)) == 16, "two rows are read at a time");
     __shared__ LineSmem<W> sm_line;
     griddep_wait();
     griddep_launch();
@@ -1496,7 +1497,7 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
             const float f = make_query<E2M1>(q);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sq[(n * 4 + j) * 32 + lane] = make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
-            if (t == 0) sf[r] = make_float2(p.qscale * f, z == -INFINITY ? z : z * -1.4426950408889634f);
+            if (t == 0) reinterpret_cast<float2*>(sf)[r] = make_float2(p.qscale * f, z == -INFINITY ? z : z * -1.4426950408889634f);
         }
         __syncthreads();
         float* out = p.scores + ((int64_t)b * p.c.Hkv + h) * n_cand - p.cand_lo;
@@ -1545,7 +1546,7 @@ __global__ void __launch_bounds__(32 * kImpWarps, imp_ctas(E2M1)) paged_importan
                             }
                         }
                     }
-                    const float4 f = *reinterpret_cast<const float4*>(&sf[8 * n + 2 * t]);   // rows 2t, 2t + 1
+                    const float4 f = sf[4 * n + t];   // rows 2t, 2t + 1
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
