@@ -64,6 +64,11 @@ static_assert(decode_cost(true).start <= kPieceStart && decode_cost(false).start
 // p is at most 2^kTop (f16 holds up to 2^15.99); a new reference puts the largest logit at 2^kBase.
 constexpr float kTop = 15.f;
 constexpr float kBase = 11.f;
+// bf16 rows: a weight is taken 2^-46 of that large (at most 2^-31, a change of its exponent alone), so that sums of up to
+// 2^31 products with values up to bf16's largest stay finite, as their weighted mean is.  The price is at the other end:
+// products below fp32's normal range lose bits, which values below some 2^-90 meet.  (4-bit values are at most 2688 here.)
+template <bool E2M1>
+constexpr float kWeightUnit = E2M1 ? 1.f : 1.f / (float)(1ull << 46);
 // Minus the reference of a row without one: any finite logit then asks for a reference, and a logit of -inf gives a
 // weight of 0 (beside +inf it would give NaN).
 constexpr float kNoRef = 3.402823466e38f;
@@ -592,7 +597,8 @@ __device__ __forceinline__ const uint16_t* query_row(const PagedAttnParams& p, i
 
 // A pair of weights as a sum of 16-bit parts: two f16 beside 4-bit rows (23 bits: what is dropped is below 2^-23 of a
 // weight, or 2^-25 where a weight is below 2^-3: the largest of a row lies between 2^11 and 2^15), three bf16 beside
-// bf16 rows (all 24 bits; two would leave 17, and outputs 1.8 times as far off as fp32 arithmetic has them).
+// bf16 rows (all 24 bits of a weight above 2^-103, which is 2^-68 of a row's largest at least; two would leave 17, and
+// outputs 1.8 times as far off as fp32 arithmetic has them).
 template <bool E2M1>
 constexpr int kWeightParts = E2M1 ? 2 : 3;
 template <bool E2M1>
@@ -641,6 +647,7 @@ __device__ __forceinline__ float4 join_row(const float* sm_o, int pitch, const f
 }
 
 // Writes one query row's output (the lane's dimensions 4 lane .. + 3) and its lse.
+template <bool E2M1>
 __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h, int r, float4 acc, float m, float z)
 {
     const int lane = threadIdx.x & 31;
@@ -649,7 +656,7 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h
     const float f = p.c.v_mul;
     reinterpret_cast<float4*>(p.out + to * kHeadDim)[lane] =
         none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / z * f, acc.y / z * f, acc.z / z * f, acc.w / z * f);
-    if (p.lse && lane == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
+    if (p.lse && lane == 0) p.lse[to] = none ? -INFINITY : (m + log2f(z / kWeightUnit<E2M1>)) * 0.6931471805599453f;
 }
 
 // The query rows of one warp and what it has summed for them.
@@ -718,7 +725,7 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
     for (int m = 0; m < U * NT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[m][e] = fast_exp2(x2[m][e]);
+            s[m][e] = fast_exp2(x2[m][e]) * kWeightUnit<E2M1>;
             a.l[m % NT][e & 1] += s[m][e];
         }
 }
@@ -1342,7 +1349,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
             for (int row = warp; row < kRows && r0 + row < p.R; row += W) {
                 float z, m;
                 const float4 acc = join_row<kRows, W>(sm_o, kPitch, sm_m, sm_l, row, m, z);
-                write_row(p, b, h, r0 + row, acc, m, z);
+                write_row<E2M1>(p, b, h, r0 + row, acc, m, z);
             }
         } else {
             // this CTA's part of the piece goes to its slot; the last CTA to arrive joins all of them
@@ -1428,7 +1435,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
                 }
 #pragma unroll
                 for (int k = 0; k < kMine; ++k)
-                    if (r0 + warp + k * W < p.R) write_row(p, b, h, r0 + warp + k * W, acc[k], m[k], z[k]);
+                    if (r0 + warp + k * W < p.R) write_row<E2M1>(p, b, h, r0 + warp + k * W, acc[k], m[k], z[k]);
             }
         }
         __syncthreads();   // shared memory is free for the next piece

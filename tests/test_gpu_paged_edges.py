@@ -1,4 +1,5 @@
-"""The paged-cache calls at the ends of their ranges, on a GPU: keys that are not finite."""
+"""The paged-cache calls at the ends of their ranges, on a GPU: keys that are not finite, values near bf16's largest
+and far below 1."""
 import numpy as np
 import pytest
 import torch
@@ -95,3 +96,42 @@ def test_importance_leaves_out_queries_without_lse_under_keys_that_are_nan(fx, f
     got[2][:, [5, 63]] = ref[2][:, [5, 63]]
     assert np.all(np.abs(got - ref) <= importance_tolerance(ref, dl))
     assert not got[0].any()
+
+
+# ---------------------------------------------------------------------------------------- values and logits
+def check_values(out, ref, floor):
+    """|out - ref| <= (2^-18 dl + 2^-15) sum p|v|: the logits' error (2^-19 dl) in numerator and sum, the weights, sums
+    and the quotient; and the floor."""
+    r, _, mag, dl, _ = ref
+    assert np.all(np.isfinite(out))
+    assert np.all(np.abs(out - r) <= (2.0 ** -18 * dl[..., None] + 2.0 ** -15) * mag + floor)
+
+
+@pytest.mark.parametrize("G,Mq", [(1, 1), (4, 1), (8, 1), (4, 4)])
+@pytest.mark.parametrize("lens", [[1, 2, 40, 33, 16], [9000, 70]])
+def test_values_near_the_largest_of_bf16(fx, lens, G, Mq):
+    """Weighted means of values near 3.3e38 are finite: many equal weights, alternating signs, ordinary weights."""
+    c = pr.Cache("bf16", lens, 1, 64, seed=2)
+    g = np.random.default_rng(5)
+    big = pr.bf16(3.3e38 * g.uniform(0.5, 1.0, c.pool[1].shape))
+    for signs in (np.ones(big.shape), g.choice([-1.0, 1.0], big.shape)):
+        c.pool[1] = big * signs
+        dev = c.device(fx)
+        for scale in (0.0, 2.0):
+            q, qt = queries(c, G, Mq, 3, scale=scale)
+            check_values(host(fx.fx_paged_decode(dev, qt)), pr.attend(c, q, 128 ** -0.5), 0.0)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("power", [-60, 60])
+def test_values_far_from_one(fx, fmt, power):
+    """No absolute error to speak of: values of 2^-60 come out as exactly as values of 2^60."""
+    exps = (0, 0) if fmt == "bf16" else (0, power)
+    for G, Mq, lens in ((1, 1, [1, 2, 40, 333]), (5, 1, [70, 9]), (3, 4, [500, 31])):
+        c = pr.Cache(fmt, lens, 2, 32, seed=G, exps=exps)
+        if fmt == "bf16":
+            c.pool[1] = c.pool[1] * 2.0 ** power
+        q, qt = queries(c, G, Mq, 4)
+        # (4-bit rows: a weight's parts are off by up to 2^-36 of the largest)
+        ref = pr.attend(c, q, 128 ** -0.5)
+        check_values(host(fx.fx_paged_decode(c.device(fx), qt)), ref, 2.0 ** -36 * ref[4])
