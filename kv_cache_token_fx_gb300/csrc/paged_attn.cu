@@ -69,6 +69,11 @@ constexpr float kBase = 11.f;
 // products below fp32's normal range lose bits, which values below some 2^-90 meet.  (4-bit values are at most 2688 here.)
 template <bool E2M1>
 constexpr float kWeightUnit = E2M1 ? 1.f : 1.f / (float)(1ull << 46);
+// A reference further than this from 0 comes of logits that fp32 holds to 1/2 at best.  It is taken from the rounded
+// product of a logit and its factor, an fma has the exact one, and what lies between them is then more than a weight has
+// room for (the largest might come out as 0 or as 2^1000).  So the tiles that ask for such a reference take the rounded
+// products as well, and weights of 2^kTop at most; later tiles come back here when theirs are larger.
+constexpr float kFarRef = 4194304.f;   // 2^22
 // Minus the reference of a row without one: any finite logit then asks for a reference, and a logit of -inf gives a
 // weight of 0 (beside +inf it would give NaN).
 constexpr float kNoRef = 3.402823466e38f;
@@ -699,7 +704,7 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int z = e; z < 4; z += 2)
-                        if (!hidden(u * NT + n, z)) m = fmaxf(m, s[u * NT + n][z] * a.rs[n][e]);
+                        if (!hidden(u * NT + n, z)) m = fmaxf(m, __fmul_rn(s[u * NT + n][z], a.rs[n][e]));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
@@ -714,11 +719,18 @@ __device__ __forceinline__ void weights(Acc<E2M1, NT, DUP>& a, float (&s)[U * NT
                     }
                     a.bias[n][e] = nb;
                 }
+                const bool far = fabsf(nb) > kFarRef;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int z = e; z < 4; z += 2)
-                        x2[u * NT + n][z] = hidden(u * NT + n, z) ? -INFINITY : fmaf(s[u * NT + n][z], a.rs[n][e], nb);
+                    for (int z = e; z < 4; z += 2) {
+                        float x = fmaf(s[u * NT + n][z], a.rs[n][e], nb);
+                        if (far) {
+                            x = __fadd_rn(__fmul_rn(s[u * NT + n][z], a.rs[n][e]), nb);
+                            x = x > kTop ? kTop : x;   // (a NaN stays)
+                        }
+                        x2[u * NT + n][z] = hidden(u * NT + n, z) ? -INFINITY : x;
+                    }
             }
     }
 #pragma unroll

@@ -1,5 +1,5 @@
 """The paged-cache calls at the ends of their ranges, on a GPU: keys that are not finite, values near bf16's largest
-and far below 1."""
+and far below 1, logits of any size."""
 import numpy as np
 import pytest
 import torch
@@ -135,3 +135,50 @@ def test_values_far_from_one(fx, fmt, power):
         # (4-bit rows: a weight's parts are off by up to 2^-36 of the largest)
         ref = pr.attend(c, q, 128 ** -0.5)
         check_values(host(fx.fx_paged_decode(c.device(fx), qt)), ref, 2.0 ** -36 * ref[4])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("G,Mq", [(2, 1), (5, 1), (6, 2)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_of_any_size(fx, fmt, G, Mq, sign):
+    """Logits up to 2^100 of either sign: the rows of the largest share the whole weight (the others' are at least a
+    quarter of it away).
+
+    Up to 2^20 they share it equally: exact weights, a sum of equal ones, one quotient; at most 2^-20 with the weights'
+    parts.  Beyond, what fp32 may lose of a logit (2^-24 of it by one rounding) is no longer small beside 1: how they share
+    is open, but the output lies between their values.  lse: 128 products, the scale times log2(e) and ln(2): within 2^-20
+    of itself."""
+    lens = [40, 3000, 17, 333]
+    c = pr.Cache(fmt, lens, 2, 32, seed=3)
+    g = np.random.default_rng(7)
+    keys = np.zeros(c.pool[0].shape)
+    keys[..., 0] = g.choice([0.0, 1.0, 2.0, 4.0] if sign > 0 else [2.0, 3.0, 4.0, 6.0], keys.shape[:-1])
+    top = [[33], [2, 1500, 1501, 2999 - Mq], [0, 15 - Mq], [100, 101, 300]]
+    for b, at in enumerate(top):
+        pg, row = c.spot(b, np.asarray(at))
+        keys[pg, :, row, 0] = 6.0 if sign > 0 else 1.0
+    c.pool[0] = keys
+    if fmt == "e2m1":
+        c.packed[0] = pr.quantize(keys)
+        c.pool[0] = pr.dequantize(*c.packed[0])
+    best = c.rows(0, 0, 0, 33)[0]
+    assert abs(np.sort(sign * np.unique(c.pool[0][..., 0]))[-2] - sign * best) > best / 4
+    dev = c.device(fx)
+    v = [np.stack([c.rows(1, b, h, at) for h in range(2)]).repeat(G, 0)[:, None] for b, at in enumerate(top)]
+    mean, least, most, mag = (np.stack([f(x) for x in v]) for f in (
+        lambda x: x.mean(2), lambda x: x.min(2), lambda x: x.max(2), lambda x: np.abs(x).max(2)))
+    for power in (0, 10, 18, 20, 22, 23, 24, 26, 28, 30, 33, 40, 70, 97):
+        q = np.zeros((len(lens), 2 * G, Mq, D))
+        q[..., 0] = pr.bf16(g.uniform(1.0, 2.0, q.shape[:-1])) * 2.0 ** power
+        s = sign * (3.0 if power < 10 else 0.7)
+        if power < 10:                                   # (ordinary sizes: the others count)
+            ref = pr.attend(c, q, s)
+            check_values(host(fx.fx_paged_decode(dev, bf16_cuda(q), scale=s)), ref, 2.0 ** -36 * ref[4])
+            continue
+        out, lse = fx.fx_paged_decode(dev, bf16_cuda(q), scale=s, want_lse=True)
+        out, lse = host(out), host(lse)
+        lo, hi = (mean, mean) if power < 20 else (least, most)
+        assert np.all(out >= lo - 2.0 ** -20 * mag) and np.all(out <= hi + 2.0 ** -20 * mag), power
+        n = np.array([len(at) for at in top])[:, None, None]
+        ref = np.float64(np.float32(s)) * best * q[..., 0] + np.log(n)
+        assert np.all(np.abs(lse - ref) <= 2.0 ** -20 * np.abs(ref)), power
