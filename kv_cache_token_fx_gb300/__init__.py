@@ -709,14 +709,15 @@ _stream_ws = {}
 
 def _paged_workspace(cache, nbytes, stream, handle):
     """The workspace of a call without one of its caller's: one for each device and stream (two streams never share
-    one).  A call that is being captured gets one of its own, from the graph's memory."""
-    if torch.cuda.is_current_stream_capturing():
-        ws = Workspace(cache.device)
-    else:
-        ws = _stream_ws.get((cache._index, handle))
-        if ws is None:
-            ws = _stream_ws[(cache._index, handle)] = Workspace(cache.device)
+    one), kept for the next call.  A call on a stream that is being captured gets one of its own, from the graph's
+    memory."""
     with _on(cache, stream):
+        if torch.cuda.is_current_stream_capturing():
+            ws = Workspace(cache.device)
+        else:
+            ws = _stream_ws.get((cache._index, handle))
+            if ws is None:
+                ws = _stream_ws[(cache._index, handle)] = Workspace(cache.device)
         return ws.ensure(nbytes, stream)
 
 
@@ -737,6 +738,9 @@ def fx_paged_decode(cache, q, idx=None, tail_lo=None, *, scale=None, out=None, l
 
     Dense, or over the rows idx [B, Hkv, k] (int32) and the tail from row tail_lo[b] (int32 [B]) on.  Returns out
     [B, Hq, Mq, 128] fp32, or (out, lse [B, Hq, Mq]) when lse is given or wanted.
+
+    Without ws the call takes the scratch memory that is kept for its stream, or, on a stream that is being captured, some
+    of the graph's.  A stream of one's own that is destroyed has finished its calls first: its handle may come back.
     """
     lib, st = _paged_launch(cache, stream)
     q_at, qs, Hq, Mq = _paged_queries(cache, q)

@@ -1,5 +1,5 @@
 """The paged-cache calls at the ends of their ranges, on a GPU: keys that are not finite, values near bf16's largest
-and far below 1, logits of any size."""
+and far below 1, logits of any size, scratch memory on streams that are not current."""
 import numpy as np
 import pytest
 import torch
@@ -182,3 +182,28 @@ def test_logits_of_any_size(fx, fmt, G, Mq, sign):
         n = np.array([len(at) for at in top])[:, None, None]
         ref = np.float64(np.float32(s)) * best * q[..., 0] + np.log(n)
         assert np.all(np.abs(lse - ref) <= 2.0 ** -20 * np.abs(ref)), power
+
+
+# ---------------------------------------------------------------------------------------- streams and scratch
+def test_capture_on_a_stream_that_is_not_current(fx):
+    """A call given a stream that is being captured takes its scratch from the graph, whatever the current stream does."""
+    c = pr.Cache("e2m1", [3000], 1, 64, seed=1, garbage=False)
+    dev = c.device(fx)
+    _, qt = queries(c, 4, 1, 3)
+    want = fx.fx_paged_decode(dev, qt)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    before = dict(fx._stream_ws)
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+    out = fx.fx_paged_decode(dev, qt, stream=side)
+    with torch.cuda.stream(side):
+        graph.capture_end()
+    assert fx._stream_ws == before
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
