@@ -621,10 +621,18 @@ def _paged_launch(cache, stream):
     return _lib or load_library(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# The handle of the per-thread default stream (cudaStreamPerThread): one number for another stream in every thread, so
+# that neither a workspace nor allocated memory can be told by it.
+_PER_THREAD = 2
+_PER_THREAD_TEXT = "the per-thread default stream needs the caller's own outputs and workspace"
+
+
 def _on(cache, stream):
     """Context in which memory is allocated for the stream that uses it."""
     if stream is None:
         return contextlib.nullcontext()
+    if (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) == _PER_THREAD:
+        raise FxError(FX_ERR_INVALID_ARG, _PER_THREAD_TEXT)
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(int(stream), cache.device))
 
@@ -711,6 +719,8 @@ def _paged_workspace(cache, nbytes, stream, handle):
     """The workspace of a call without one of its caller's: one for each device and stream (two streams never share
     one), kept for the next call.  A call on a stream that is being captured gets one of its own, from the graph's
     memory."""
+    if handle == _PER_THREAD:
+        raise FxError(FX_ERR_INVALID_ARG, _PER_THREAD_TEXT)
     with _on(cache, stream):
         if torch.cuda.is_current_stream_capturing():
             ws = Workspace(cache.device)
@@ -740,7 +750,8 @@ def fx_paged_decode(cache, q, idx=None, tail_lo=None, *, scale=None, out=None, l
     [B, Hq, Mq, 128] fp32, or (out, lse [B, Hq, Mq]) when lse is given or wanted.
 
     Without ws the call takes the scratch memory that is kept for its stream, or, on a stream that is being captured, some
-    of the graph's.  A stream of one's own that is destroyed has finished its calls first: its handle may come back.
+    of the graph's.  The per-thread default stream (handle 2) is refused without ws: its handle does not tell threads apart.
+    A stream of one's own that is destroyed has finished its calls first: its handle may come back.
     """
     lib, st = _paged_launch(cache, stream)
     q_at, qs, Hq, Mq = _paged_queries(cache, q)
