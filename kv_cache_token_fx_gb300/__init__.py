@@ -205,11 +205,33 @@ def _default_scale(d):
     return 1.0 / math.sqrt(d)
 
 
+# The handle of the per-thread default stream (cudaStreamPerThread): one number for another stream in every thread, so
+# that neither a workspace nor allocated memory can be told by it.
+_PER_THREAD = 2
+_PER_THREAD_TEXT = "the per-thread default stream needs the caller's own outputs and workspace"
+
+
+def _per_thread(stream):
+    return stream is not None and (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) == _PER_THREAD
+
+
+def _on_stream(device, stream):
+    """Context in which memory is allocated for the stream that uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if _per_thread(stream):
+        raise FxError(FX_ERR_INVALID_ARG, _PER_THREAD_TEXT)
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream), device))
+
+
 class Workspace:
     """A zero-initialised device scratch buffer reused across calls on one stream.
 
     ``ensure(nbytes)`` grows it (allocating a fresh zeroed buffer) when needed; a buffer that a CUDA
-    graph has captured must not be grown afterwards, so size it before capture.
+    graph has captured must not be grown afterwards, so size it before capture.  The buffer that it
+    gives up stays reserved until the stream's work of that moment is done, and the fresh one is
+    allocated for the stream.
     """
 
     def __init__(self, device=None, nbytes: int = 0):
@@ -220,8 +242,13 @@ class Workspace:
 
     def ensure(self, nbytes: int, stream=None):
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
-            _check(load_library().fx_workspace_init(_ptr(self.buf), self.buf.numel(), _stream(stream)))
+            # (a per-thread default stream: as the current stream's, which is all that is known of it)
+            with contextlib.nullcontext() if _per_thread(stream) else _on_stream(self.device, stream):
+                buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
+                if self.buf is not None:
+                    self.buf.record_stream(torch.cuda.current_stream(self.device))
+            _check(load_library().fx_workspace_init(_ptr(buf), buf.numel(), _stream(stream)))
+            self.buf = buf   # (zeroed in the stream's order before another thread finds it)
         return self.buf
 
 
@@ -621,24 +648,8 @@ def _paged_launch(cache, stream):
     return _lib or load_library(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-# The handle of the per-thread default stream (cudaStreamPerThread): one number for another stream in every thread, so
-# that neither a workspace nor allocated memory can be told by it.
-_PER_THREAD = 2
-_PER_THREAD_TEXT = "the per-thread default stream needs the caller's own outputs and workspace"
-
-
-def _on(cache, stream):
-    """Context in which memory is allocated for the stream that uses it."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) == _PER_THREAD:
-        raise FxError(FX_ERR_INVALID_ARG, _PER_THREAD_TEXT)
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(stream), cache.device))
-
-
 def _paged_alloc(cache, stream, shape, dtype):
-    with _on(cache, stream):
+    with _on_stream(cache.device, stream):
         return torch.empty(shape, dtype=dtype, device=cache.device)
 
 
@@ -721,7 +732,7 @@ def _paged_workspace(cache, nbytes, stream, handle):
     memory."""
     if handle == _PER_THREAD:
         raise FxError(FX_ERR_INVALID_ARG, _PER_THREAD_TEXT)
-    with _on(cache, stream):
+    with _on_stream(cache.device, stream):
         if torch.cuda.is_current_stream_capturing():
             ws = Workspace(cache.device)
         else:

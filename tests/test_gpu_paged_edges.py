@@ -207,3 +207,28 @@ def test_capture_on_a_stream_that_is_not_current(fx):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_a_workspace_grows_beside_work_in_flight(fx):
+    """The buffer that a workspace gives up stays reserved while calls on their stream still use it."""
+    c = pr.Cache("e2m1", [3000], 1, 64, seed=1, garbage=False)
+    dev = c.device(fx)
+    small, large = queries(c, 4, 1, 3)[1], queries(c, 16, 1, 3)[1]
+    want = [fx.fx_paged_decode(dev, q) for q in (small, large)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    ws = fx.Workspace(nbytes=fx.fx_paged_decode_workspace_bytes(1, 1, 4, 1))
+    torch.cuda.synchronize()
+    size, at = ws.buf.numel(), ws.buf.data_ptr()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1 << 30)
+    first = fx.fx_paged_decode(dev, small, stream=side, ws=ws)
+    assert ws.buf.data_ptr() == at
+    second = fx.fx_paged_decode(dev, large, stream=side, ws=ws)
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    asleep = not side.query()
+    torch.cuda.synchronize()
+    assert asleep and ws.buf.numel() > size
+    assert all(t.data_ptr() != at for t in others)
+    assert torch.equal(first, want[0]) and torch.equal(second, want[1])
