@@ -184,6 +184,31 @@ def test_logits_of_any_size(fx, fmt, G, Mq, sign):
         assert np.all(np.abs(lse - ref) <= 2.0 ** -20 * np.abs(ref)), power
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("G,Mq", [(2, 1), (8, 1), (2, 7)])
+def test_no_part_of_the_weights_is_lost_over_long_rows(fx, fmt, G, Mq):
+    """Thousands of weights of two sizes, the smaller one no short binary fraction, over values that are all 1.
+
+    The output is the sum of the weights' parts over the sum of the weights.  16 products of a tile are cut off at
+    2^-24 of their sum each, for every part but the first: 2 * 2^-20.  A warp's additions (24 tiles at most here) and
+    the sums over 4 warps and 16 CTAs at most round to 2^-24 each, in numerator and sum: 2 * 44 * 2^-24; quotient
+    2^-24: less than 2^-17 in all.  (Half the weights without their second part would be 2^-11 off.)"""
+    lens = [3000, 1501, 2222] * 8
+    c = pr.Cache(fmt, lens, 2, 64, seed=6, garbage=False)
+    keys = np.zeros(c.pool[0].shape)
+    keys[:, :, ::2, 0] = 6.0
+    c.pool = [keys, np.full(keys.shape, 6.0)]
+    if fmt == "e2m1":
+        c.packed = [pr.quantize(p) for p in c.pool]
+        assert all(np.array_equal(pr.dequantize(*x), p) for x, p in zip(c.packed, c.pool))
+    q = np.zeros((c.B, 2 * G, Mq, D))
+    q[..., 0] = 1.0
+    dev = c.device(fx)
+    for drop in (0.2, 0.35, 0.61):
+        out = host(fx.fx_paged_decode(dev, bf16_cuda(q), scale=drop / 6)) / 6
+        assert np.all(np.abs(out - 1.0) <= 2.0 ** -17), (drop, np.abs(out - 1.0).max())
+
+
 # ---------------------------------------------------------------------------------------- streams and scratch
 def test_capture_on_a_stream_that_is_not_current(fx):
     """A call given a stream that is being captured takes its scratch from the graph, whatever the current stream does."""
@@ -207,6 +232,31 @@ def test_capture_on_a_stream_that_is_not_current(fx):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("own_ws", [False, True])
+def test_programmatic_launches_are_captured(fx, own_ws):
+    c = pr.Cache("e2m1", [3000, 64], 1, 64, seed=1, garbage=False)
+    dev = c.device(fx)
+    _, qt = queries(c, 4, 2, 3)
+    ws = fx.Workspace(nbytes=fx.fx_paged_decode_workspace_bytes(2, 1, 4, 2)) if own_ws else None
+
+    def chain():
+        out, lse = fx.fx_paged_decode(dev, qt, want_lse=True, ws=ws, flags=fx.FX_LAUNCH_PDL)
+        s = fx.fx_paged_importance(dev, qt, lse, flags=fx.FX_LAUNCH_PDL)
+        again = fx.fx_paged_decode(dev, qt, ws=ws, flags=fx.FX_LAUNCH_PDL)
+        return out, lse, s, again
+    want = [t.clone() for t in chain()]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = chain()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_a_workspace_grows_beside_work_in_flight(fx):
