@@ -1163,7 +1163,7 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
     p.n_pos = rows->n_pos;
     p.interleaved = rows->interleaved != 0;
     p.err = ds->err;
-    cudaError_t e = launch_paged_append(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+    cudaError_t e = launch_paged_append(p, cache->format == FX_PAGED_E2M1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
                                         static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
     return FX_OK;
@@ -1192,7 +1192,7 @@ fx_status fx_paged_gather(const fx_paged_desc* cache, const int32_t* idx, const 
     p.k_out = k_out;
     p.v_out = v_out;
     p.err = ds->err;
-    cudaError_t e = launch_paged_gather(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+    cudaError_t e = launch_paged_gather(p, cache->format == FX_PAGED_E2M1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
                                         static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged gather launch");
     return FX_OK;

@@ -321,8 +321,8 @@ cudaError_t launch_compact(const CompactParams& p, bool pdl, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, bool pdl, cudaStream_t s);
 constexpr int kPieceStart = 32;   // tiles that the start of a (sequence, KV head, query rows) counts at most
 // Paged cache (paged_rows.cu, paged_attn.cu); `e2m1`: the 4-bit format.
-cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, bool pdl, cudaStream_t s);
-cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);

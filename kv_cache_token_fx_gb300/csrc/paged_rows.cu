@@ -291,13 +291,13 @@ __global__ void __launch_bounds__(kThreadsRows) paged_gather_kernel(const PagedG
 }
 
 template <bool E2M1, bool INTERLEAVED>
-cudaError_t append(const PagedAppendParams& p, bool pdl, cudaStream_t s)
+cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     // A decode step's few rows: one row each, for the shortest way through (a step of 64 sequences with its read-back
     // 4.5 us, against 5.8 with four).  More rows than the machine has groups of 8 lanes: four rows each, for their shared
     // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 105 us, against 127 with one, before the
     // registers were bounded).
-    const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > 152 * 2048 / 8;
+    const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > sm_count * 2048 / 8;
     const int R = many ? 4 : 1;
     const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
     const dim3 grid((unsigned)((groups + kThreadsRows / 8 - 1) / (kThreadsRows / 8)));
@@ -306,10 +306,10 @@ cudaError_t append(const PagedAppendParams& p, bool pdl, cudaStream_t s)
 }
 
 template <bool E2M1>
-cudaError_t gather(const PagedGatherParams& p, bool pdl, cudaStream_t s)
+cudaError_t gather(const PagedGatherParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     // few rows: one each (listed rows 3.7 us, against 4.7 with four); many: four in flight (70 us, against 86 with one)
-    const bool many = (int64_t)p.n * p.c.Hkv * p.c.B > 2 * 152 * 2048 / 16;
+    const bool many = (int64_t)p.n * p.c.Hkv * p.c.B > 2 * sm_count * 2048 / 16;
     const int rows = kCopyRows * (many ? 4 : 1);
     const dim3 grid((p.n + rows - 1) / rows, p.c.Hkv, p.c.B);
     return many ? launch_kernel(paged_gather_kernel<E2M1, 4>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
@@ -318,15 +318,15 @@ cudaError_t gather(const PagedGatherParams& p, bool pdl, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, bool pdl, cudaStream_t s)
+cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    if (p.interleaved) return e2m1 ? append<true, true>(p, pdl, s) : append<false, true>(p, pdl, s);
-    return e2m1 ? append<true, false>(p, pdl, s) : append<false, false>(p, pdl, s);
+    if (p.interleaved) return e2m1 ? append<true, true>(p, sm_count, pdl, s) : append<false, true>(p, sm_count, pdl, s);
+    return e2m1 ? append<true, false>(p, sm_count, pdl, s) : append<false, false>(p, sm_count, pdl, s);
 }
 
-cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, bool pdl, cudaStream_t s)
+cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    return e2m1 ? gather<true>(p, pdl, s) : gather<false>(p, pdl, s);
+    return e2m1 ? gather<true>(p, sm_count, pdl, s) : gather<false>(p, sm_count, pdl, s);
 }
 
 }  // namespace fx
