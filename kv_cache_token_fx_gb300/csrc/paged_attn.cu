@@ -1083,7 +1083,8 @@ struct Line {
             if (one_scan) {
                 choose(B, [&](int i) { return sm.cnt[i]; });
             } else {
-                choose(0x7fffffff, [](int) { return 0; });   // (more pieces than CTAs can take one each)
+                choose(0x7fffffff, [](int) { return 0; });   // (always stretches: equal parts are looked for among the
+                                                             // lengths of one scan)
             }
             if (inv == 0.f && cta >= n_cta) return false;
             int before = 0;   // units (of one piece each) of the sequences before this block
