@@ -429,7 +429,9 @@ FX_API int fx_branch_pool_batch(fx_branch_pool* pool, int32_t* ids, int32_t* suf
  *   table    device [B, table_stride] int32; entries of pages that hold no row in use are never read as
  *            pages.  A bad entry for a row in use sets FX_DEVERR_PAGE and its rows are skipped.
  *   len      device [B] int32: rows t < len[b] are valid (outside [0, max_pages*page_rows]: clamped,
- *            FX_DEVERR_LEN).  Rows at or past it are never used, whatever they hold.
+ *            FX_DEVERR_LEN).  Rows at or past it are never used, whatever they hold.  len and table stay as they
+ *            are while a call runs (a decode whose lengths change under it leaves its workspace to be initialised
+ *            again).
  *   page_rows  16, 32, 64, 128, 256, 512 or 1024;  n_pages: pages in the pool;  max_pages: table entries
  *            of one sequence.  n_pages*page_rows is below 2^31, max_pages*page_rows below 2^30,
  *            page and row strides below 2^31 bytes.
@@ -468,7 +470,8 @@ typedef struct {
  *   or a NaN gets a NaN scale (0x7f) and zero codes: all of it reads back as NaN.
  *   k, v     bf16 rows (i, h) at k + i*stride_n + h*stride_h (v with the same strides)
  *   q, q_out bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h, q_out + i*qo_stride_n + g*qo_stride_h;
- *            both NULL or both given; q_out may be q (same strides)
+ *            both NULL or both given; q_out may be q (same strides), and else its rows are distinct and overlap
+ *            nothing that the call reads
  *   seq      int32 [n]; seq[i] = -1 marks a padding token: its rows are not used, its q_out not written.  Another
  *            value outside [0, B) sets FX_DEVERR_INDEX, pos[i] outside [0, max_pages*page_rows)
  *            FX_DEVERR_LEN, a rotation position outside [0, n_pos) FX_DEVERR_INDEX: that token is skipped,
@@ -514,9 +517,11 @@ FX_API fx_status fx_paged_gather(const fx_paged_desc* cache, const int32_t* idx,
  *   S = { idx[b, h, 0..k) } followed by { tail_lo[b] .. len[b]-1 },  each only where query i sees it
  *   out[b, g, i, :] = sum_{t in S} softmax_S(scale * q . k_t) v_t
  *   lse[b, g, i]    = log sum_{t in S} exp(scale * q . k_t)                       (written when lse != NULL)
- * k = 0 with tail_lo = NULL is dense attention.  An empty S gives out = 0 and lse = -infinity.  An idx
- * entry outside [0, len[b]) sets FX_DEVERR_INDEX and is skipped; a row listed twice, or listed and in the
- * tail, counts twice.  A row that query i does not see does not reach it, whatever it holds.
+ * k = 0 with tail_lo = NULL is dense attention.  An empty S, or one whose logits are all -infinity, gives out = 0
+ * and lse = -infinity.  out is finite where its definition is and the logits fit fp32; an infinity among the values
+ * that a query sees may come out as NaN.  An idx entry outside [0, len[b]) sets FX_DEVERR_INDEX and is skipped; a
+ * row listed twice, or listed and in the tail, counts twice.  A row that query i does not see does not reach it,
+ * whatever it holds.  More than 16 query rows a KV head (G*Mq) read the cache once for every 16.
  *   q         bf16 rows (b, g, i) at q + b*q_stride_b + g*q_stride_h + i*q_stride_i
  *   tail_lo   int32 [B] (device) or NULL, which means 0; a negative value sets FX_DEVERR_LEN and counts as 0
  *   out [B, Hq, Mq, 128] fp32, lse [B, Hq, Mq] fp32 or NULL;  G*Mq <= 64, scale finite

@@ -16,7 +16,9 @@
 // Why mma.sync and not tcgen05: the codes must be unpacked by the threads in either case.  A version with 128-row tiles
 // unpacked into swizzled shared memory, S^T and O^T by tcgen05.mma and one cache row to a thread gave the same outputs,
 // but took 52 M warp instructions instead of 36 M for 64 x 3335 rows and 14 query rows (139 us against 94 then): the
-// stores of the operands and of P cost more than the products it saves.  At most 64 query rows share a cache row here.
+// stores of the operands and of P cost more than the products it saves.  That was timed for 14 query rows of a decode and
+// 32 of an importance.  At most 64 query rows share a cache row here; a decode of more than 16 takes a pass over the cache
+// for every 16 (64 x 3335 4-bit rows: 16 query rows 79 us, 32 146, 64 280), where one unpacking might yet pay.
 //
 // Softmax: base-2 logits, one pass.  p = 2^(x - m) with a reference m per row that all lanes of the row share;
 // it is set so that the largest logit so far gives 2^kBase and moves only when a p would exceed 2^kTop, so most
@@ -33,14 +35,17 @@ namespace fx {
 namespace {
 
 constexpr int kTileRows = 16;
-constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call (decode of 1024 4-bit rows of one
-                                // sequence: 8.0 us with 1, 7.7 with 2, 8.7 with 4)
+constexpr int kMinTiles = 2;    // tiles a warp gets at least, before more CTAs share a call (decode of one head's 1024 4-bit
+                                // rows: 7.3 us with 1, 7.7 with 2, 8.6 with 4; of 8 x 4864 rows: 14.7, 14.4 and 14.7)
 constexpr int kMaxParts = 128;  // CTAs that share one (sequence, KV head, row group) on average, at most: the last
                                 // of them joins all their parts
 // 4 bits, up to 8 query rows: tiles a warp may get at most for units of one tile instead of two (512 heads' 40 rows, a
-// tile: 9.4 us against 11.8; 833 rows, 15 tiles: 23.2 both; 1667 rows, 29 tiles: 33.4 against 31.3; 128 heads' 32768
-// rows, 144 tiles: 99 against 85).  Pages of 16 rows hold no pair of neighbours: always one (64 heads' 4864 rows 14.8 us
-// against 16.3, 38912 rows 73 against 76).
+// tile: 9.4 us against 11.6; 833 rows, 15 tiles: 23.3 against 22.3; 1667 rows, 29 tiles: 34.1 against 30.4; 128 heads'
+// 32768 rows, 144 tiles: 105 against 84).  Pages of 16 rows hold no pair of neighbours: always one (64 heads' 4864 rows
+// 14.4 us against 15.4, 38912 rows 76 against 74).
+// The host knows no lengths: it counts the rows that the table has room for, and the list.  Where a table has far more room
+// than its sequences use, short work runs in units of two: 64 heads' 1024 rows 9.9 us against 9.5, 4864 rows 13.9 both, 2048
+// listed rows and a tail of 512 14.7 against 14.2.
 constexpr int kShort = 16;
 // What a piece costs a CTA besides its tiles -- its first rows and queries, its join: 5 to 10 us -- counted in tiles.
 struct LineCost {
@@ -48,15 +53,14 @@ struct LineCost {
     int start;    // the start of a piece in a line
     int near;     // between a cut and an end of a piece, at least
 };
-// Decode, 4 bits (a tile of a CTA takes 0.2 us).  second: 16 x 32768 rows 89.6 us against 91.4 with 32, 8 x 4864 rows 16.7
-// against 20.1 with 0.  start: 64 sequences of up to 3335 rows, 14 query rows: 80 us against 85 with 16, 82 with 48, 90
-// without; of up to 40 rows: 17 us against 29 without.  near (before start counted): those 3335 rows 90 us, 91 with 8, 92
-// with 32, 95 without.
-// bf16 (a tile is 3.5 times the bytes): 64 sequences of up to 1000 rows, 14 query rows: 46.6 us against 51.8 with a start
-// of 32 and near of 16; 1667 rows, 2 query rows: 51.6 us against 52.2, and 53.2 with 8 and 4.
+// Decode, 4 bits (a tile of a CTA takes 0.2 us).  second: 8 x 4864 rows 14.4 us against 17.9 with 0; 16 x 32768 rows 84 us
+// with 0, 32 or 48.  start: 64 sequences of up to 3335 rows, 14 query rows: 79 us against 84 with 16, 89 without; of up to 40
+// rows: 17 us against 29 without.  near: those 3335 rows 78.7 us, 79.1 with 8, 81.8 with 32, 79.3 with 1.
+// bf16 (a tile is 3.5 times the bytes): 64 sequences of up to 1000 rows, 14 query rows: 48 us against 53 with a start of 32
+// and near of 16, 49 with 8 and 4; 1667 rows, 2 query rows: 51.8 us against 52.3 and 53.0.
 __host__ __device__ constexpr LineCost decode_cost(bool e2m1) { return e2m1 ? LineCost{48, 32, 16} : LineCost{48, 16, 8}; }
-// Importance has no join, so cuts may fall anywhere (64 x 2000 4-bit rows: 20.6 us against 21.9 with near = 16; bf16:
-// 34.1 us against 38.1 with 32 and 16).
+// Importance has no join, so cuts may fall anywhere (64 x 2000 4-bit rows: 21.3 us against 22.3 with near = 16; bf16:
+// 34.5 us against 35.4 with near = 16, 36.1 with a start of 32 as well).
 __host__ __device__ constexpr LineCost importance_cost(bool e2m1) { return LineCost{32, e2m1 ? 32 : 8, 1}; }
 static_assert(decode_cost(true).start <= kPieceStart && decode_cost(false).start <= kPieceStart &&
                   importance_cost(true).start <= kPieceStart && importance_cost(false).start <= kPieceStart,
@@ -1192,15 +1196,17 @@ __device__ __forceinline__ int warp_start(const Seq& q, int s0, int s1, int w)
 
 // Shape of the decode kernel for a format and up to 4 (DUP), 8 or 16 query rows a pass.
 //
-// bf16: bound by bytes.  A tile is 8 KB, and the rings of 8 warps fill the shared memory of an SM (8 x 32768 rows,
-// 755 MB: 117 us, 0.95 of the copy bandwidth; rings of 4 units instead of 3: 128 us).
+// bf16: bound by bytes.  A tile is 8 KB, and the rings of two CTAs fill the shared memory of an SM (8 x 32768 rows,
+// 755 MB: 117 us, 0.95 of the copy bandwidth; rings of 4 units instead of 3, with one CTA an SM: 117 us).
 // 4 bits: a tile is 2.3 KB and takes 310 instructions of a warp, of which 64 are conversions of codes and 64 their
-// scaling (the conversion issues every second cycle): bound by the issue of instructions and their latency.  As many
-// warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 84 us, 0.72 of the copy
-// bandwidth; with 2 CTAs 7% longer), 2 CTAs for 16 rows (3 spill, and gain nothing).  Two tiles at a time share the loads
-// of the queries and the additions to O; where a warp gets few tiles, one at a time is sooner done (kShort).  DUP: 90 us
-// against 105 for up to 4 rows.  One pass of 16 rows instead of two of 8: 94 us
-// against 112 (64 x 3335 rows, 14 query rows).
+// scaling (the conversion issues every second cycle).  Bytes are the floor (8 x 32768 rows: 32 us; to issue their 30 M
+// instructions 29), latency is the bound: the 3 warps of a scheduler issue in 54% of the cycles, and wait for the results
+// of chains of conversions, products and exponentials (1.0 cycle an instruction) and for instructions themselves (0.6).  As
+// many warps as the registers allow: 3 CTAs an SM for up to 8 rows (16 x 32768 rows, 411 MB: 84 us, 0.72 of the copy
+// bandwidth; 2 CTAs: 91 us), 2 CTAs for 16 rows (3 spilled 400 to 600 bytes, and gained nothing).  As it is, 16 rows spill
+// 32 to 40 bytes, and 8 rows in units of two tiles 60.  Two tiles at a time share the loads of the queries and the additions
+// to O; where a warp gets few tiles, one at a time is sooner done (kShort).  DUP: 84 us against 94 for up to 4 rows.  One
+// pass of 16 rows instead of two of 8: 79 us against 96 (64 x 3335 rows, 14 query rows).
 template <bool E2M1, int NT, bool DUP, int U>
 struct Shape {
     static constexpr int kRows = DUP ? 4 : 8 * NT;       // query rows of a pass over a (sequence, KV head)
@@ -1463,9 +1469,10 @@ constexpr int kImpWarps = 4;
 __host__ __device__ constexpr int imp_stages(bool e2m1) { return e2m1 ? 2 : 3; }   // units in a warp's ring
 __host__ __device__ constexpr int imp_ctas(bool e2m1) { return e2m1 ? 3 : 4; }   // per SM (registers)
 
-// Importance.  4 bits: bound by the issue of instructions (4 x 32768 rows, 49 MB, 32 query rows: 28.8 us, 4 query rows:
-// 17.8; 2 CTAs an SM instead of 3: 10% longer).  bf16: by bytes and the start (8 x 4864 rows, 2 query rows: 11.7 us for
-// 46 MB; rings of 2 units instead of 3: 12.5 us, of 4, with fewer CTAs: 16 us).  Pieces are (sequence, KV head)s; the
+// Importance.  4 bits: bound by latency, 3 warps a scheduler issuing in 43% of the cycles (4 x 32768 rows, 49 MB, 32 query
+// rows: 28.8 us, whose 13 M instructions would issue in 13.5; 4 query rows: 18.0; 2 CTAs an SM instead of 3: 28.8 and 21.2).
+// bf16: by bytes and the start (8 x 4864 rows, 2 query rows: 11.7 us for 46 MB; rings of 2 units instead of 3: 11.9 us, of 4,
+// with fewer CTAs: 15.8 us).  Pieces are (sequence, KV head)s; the
 // query fragments of a piece lie in shared memory as the products want them, and each of them serves a unit of tiles
 // at a time.  Rows of the fragments that add nothing -- beyond the last query row, or with an lse of -inf, whatever the
 // query holds -- are zeros with a factor of 2^-inf.  Beside finite keys that is enough; tiles with an edge, and those whose

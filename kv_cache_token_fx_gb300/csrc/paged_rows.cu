@@ -3,8 +3,8 @@
 //
 // Both move rows of 128 values and compute a few operations a value.  Bytes bound the long gather (4 x 32768 4-bit rows
 // to bf16, 447 MB: 70 us, 0.94 of the copy bandwidth); the quantisation's instructions and bytes together the long
-// append (24 K tokens, 4 bits, with 32 query heads: 0.92 of the copy bandwidth, with the rows read back); start-up the
-// decode step's few rows (2.2 us for one token of a sequence).
+// append (24 K tokens, 4 bits, with 32 query heads: 77 us, 0.88 of the copy bandwidth; bf16 79 us, 0.97); start-up the
+// decode step's few rows (2.0 us for one token of each of 8 sequences, 2.5 us of 64 in 4 bits).
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -72,7 +72,8 @@ __device__ __forceinline__ uint32_t quantize_chunk(uint4 x, float inv, uint32_t&
 // chunks c0 and c1, which are the two sides of 8 rotated pairs in the half-split form.  The rows' loads need
 // neither the token's place nor its position and go out first, and the rows share its cosines and sines.
 // 8 CTAs of 128 threads an SM (64 registers), and queries and new rows that pass by L2's older contents when there are
-// many: a prompt of 24 K tokens, 4 bits, with its read-back 90 us, against 105 without either and 112 with 10 CTAs.
+// many: a prompt of 24 K tokens, 4 bits, with its read-back 91 us, against 95 without the latter, 100 without either and
+// 105 with 10 CTAs.
 template <bool E2M1, int R, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const PagedAppendParams p)
 {
@@ -294,9 +295,8 @@ template <bool E2M1, bool INTERLEAVED>
 cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     // A decode step's few rows: one row each, for the shortest way through (a step of 64 sequences with its read-back
-    // 4.5 us, against 5.8 with four).  More rows than the machine has groups of 8 lanes: four rows each, for their shared
-    // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 105 us, against 127 with one, before the
-    // registers were bounded).
+    // 4.6 us, against 5.6 with four).  More rows than the machine has groups of 8 lanes: four rows each, for their shared
+    // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 92 us, against 124 with one).
     const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > sm_count * 2048 / 8;
     const int R = many ? 4 : 1;
     const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
@@ -308,7 +308,8 @@ cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStrea
 template <bool E2M1>
 cudaError_t gather(const PagedGatherParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
-    // few rows: one each (listed rows 3.7 us, against 4.7 with four); many: four in flight (70 us, against 86 with one)
+    // few rows: one each (205 listed rows of 64 heads: bf16 4.2 us, against 5.1 with four, 4 bits 3.5 against 4.4); many:
+    // four in flight (4 x 32768 4-bit rows 70 us, against 133 with one)
     const bool many = (int64_t)p.n * p.c.Hkv * p.c.B > 2 * sm_count * 2048 / 16;
     const int rows = kCopyRows * (many ? 4 : 1);
     const dim3 grid((p.n + rows - 1) / rows, p.c.Hkv, p.c.B);
