@@ -780,6 +780,8 @@ def fx_paged_decode(cache, q, idx=None, tail_lo=None, *, scale=None, out=None, l
     lse_at = None if lse is None else _paged_tensor(cache, lse, "lse", torch.float32, (B, Hq, Mq))
     nbytes = lib.fx_paged_decode_workspace_bytes(B, cache.Hkv, Hq, Mq)
     buf = _paged_workspace(cache, nbytes, stream, st) if ws is None else ws.ensure(nbytes, stream)
+    if buf.get_device() != cache._index:
+        raise FxError(FX_ERR_INVALID_ARG, f"ws must be a workspace on {cache.device}")
     rc = lib.fx_paged_decode(cache._ref, q_at, qs[0], qs[1], qs[2], Hq, Mq, idx_at, kk, lo_at,
                              _SCALE if scale is None else scale, out_at, lse_at, buf.data_ptr(), buf.numel(), flags, st)
     if rc:

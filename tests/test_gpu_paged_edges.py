@@ -282,3 +282,13 @@ def test_a_workspace_grows_beside_work_in_flight(fx):
     assert asleep and ws.buf.numel() > size
     assert all(t.data_ptr() != at for t in others)
     assert torch.equal(first, want[0]) and torch.equal(second, want[1])
+
+
+def test_a_workspace_of_another_device_is_refused(fx):
+    c = pr.Cache("e2m1", [20], 1, 16, seed=1)
+    _, qt = queries(c, 1, 1, 2)
+    for device in ("cpu", "meta"):
+        ws = fx.Workspace()
+        ws.buf = torch.zeros(1 << 23, dtype=torch.uint8, device=device)     # as one made for that device holds it
+        with pytest.raises(fx.FxError, match="ws must be"):
+            fx.fx_paged_decode(c.device(fx), qt, ws=ws)
