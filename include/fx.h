@@ -470,8 +470,8 @@ typedef struct {
  *   or a NaN gets a NaN scale (0x7f) and zero codes: all of it reads back as NaN.
  *   k, v     bf16 rows (i, h) at k + i*stride_n + h*stride_h (v with the same strides)
  *   q, q_out bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h, q_out + i*qo_stride_n + g*qo_stride_h;
- *            both NULL or both given; q_out may be q (same strides), and else its rows are distinct and overlap
- *            nothing that the call reads
+ *            both NULL or both given; q_out may be q (same strides), and else overlaps nothing that the call reads.
+ *            Rows that are written (q_out's, the pool's) lie apart: strides below a row's length are refused
  *   seq      int32 [n]; seq[i] = -1 marks a padding token: its rows are not used, its q_out not written.  Another
  *            value outside [0, B) sets FX_DEVERR_INDEX, pos[i] outside [0, max_pages*page_rows)
  *            FX_DEVERR_LEN, a rotation position outside [0, n_pos) FX_DEVERR_INDEX: that token is skipped,

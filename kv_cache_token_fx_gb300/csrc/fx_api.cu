@@ -1008,6 +1008,8 @@ fx_status fx_shared_prefix_decode(const fx_prefix_desc* prefix, const fx_branch_
 namespace {
 
 bool multiple_of(int64_t s, int64_t m) { return s >= 0 && s % m == 0; }
+// Whether rows of `row` elements that are written keep clear of their neighbours along a dimension of n entries.
+bool rows_apart(int64_t stride, int64_t row, int n) { return n <= 1 || stride >= row; }
 
 // Checks a paged cache and turns it into the kernels' view.  `need_len`: the call reads len.
 fx_status paged_view(const fx_paged_desc* d, bool need_len, PagedCache* c)
@@ -1137,6 +1139,16 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
         return fail(FX_ERR_UNSUPPORTED, "rows: rot %d (0, 32, 64, 96 or 128)", rows->rot);
     if (rows->rot > 0 && (!rows->cos_sin || !aligned16(rows->cos_sin) || rows->n_pos < 1))
         return fail(FX_ERR_INVALID_ARG, "rows: rot > 0 needs cos_sin (16-byte aligned) of n_pos >= 1 positions");
+    if (rows->q && (!rows_apart(rows->qo_stride_n, kHeadDim, rows->n) || !rows_apart(rows->qo_stride_h, kHeadDim, rows->Hq)))
+        return fail(FX_ERR_INVALID_ARG, "rows: q_out's rows share memory");
+    const bool e2m1 = cache->format == FX_PAGED_E2M1;
+    const int row = e2m1 ? kHeadDim / 2 : kHeadDim, scales = kHeadDim / 16;
+    if (!rows_apart(cache->stride_page, row, cache->n_pages) || !rows_apart(cache->stride_h, row, cache->Hkv) ||
+        !rows_apart(cache->stride_t, row, cache->page_rows) ||
+        (e2m1 && (!rows_apart(cache->scale_stride_page, scales, cache->n_pages) ||
+                  !rows_apart(cache->scale_stride_h, scales, cache->Hkv) ||
+                  !rows_apart(cache->scale_stride_t, scales, cache->page_rows))))
+        return fail(FX_ERR_INVALID_ARG, "cache: the pool's rows share memory, so none can be written");
     const int Hq = rows->q ? rows->Hq : 0;
     if (Hq > 65535 || (int64_t)rows->n * (2 * (int64_t)cache->Hkv + Hq) > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "too many rows");
@@ -1163,7 +1175,7 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
     p.n_pos = rows->n_pos;
     p.interleaved = rows->interleaved != 0;
     p.err = ds->err;
-    cudaError_t e = launch_paged_append(p, cache->format == FX_PAGED_E2M1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
+    cudaError_t e = launch_paged_append(p, e2m1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
                                         static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
     return FX_OK;
