@@ -704,6 +704,8 @@ def fx_paged_gather(cache, n: int, *, idx=None, lo=None, k_out=None, v_out=None,
     """
     lib, st = _paged_launch(cache, stream)
     n = int(n)
+    if n < 0:
+        raise FxError(FX_ERR_INVALID_ARG, "n must be >= 0")
     shape = (cache.B, cache.Hkv, n, 128)
     idx_at = None if idx is None else _paged_tensor(cache, idx, "idx", torch.int32, shape[:3])
     lo_at = None if lo is None else _paged_tensor(cache, lo, "lo", torch.int32, (cache.B,))
@@ -801,8 +803,10 @@ def fx_paged_importance(cache, q, lse, *, scale=None, cand=None, scores=None, st
         lo, hi = 0, cache._rows
         if isinstance(scores, torch.Tensor) and scores.dim() == 3:
             hi = scores.shape[2]
+    if not 0 <= lo <= hi <= cache._rows:
+        raise FxError(FX_ERR_INVALID_ARG, f"need 0 <= cand[0] <= cand[1] <= {cache._rows}")
     if scores is None:
-        scores = _paged_alloc(cache, stream, (cache.B, cache.Hkv, max(hi - lo, 0)), torch.float32)
+        scores = _paged_alloc(cache, stream, (cache.B, cache.Hkv, hi - lo), torch.float32)
     s_at = _paged_tensor(cache, scores, "scores", torch.float32, (cache.B, cache.Hkv, hi - lo))
     rc = 0 if hi == lo else lib.fx_paged_importance(cache._ref, q_at, qs[0], qs[1], qs[2], Hq, Mq, lse_at,
                                                     _SCALE if scale is None else scale, lo, hi, s_at, flags, st)

@@ -292,3 +292,18 @@ def test_a_workspace_of_another_device_is_refused(fx):
         ws.buf = torch.zeros(1 << 23, dtype=torch.uint8, device=device)     # as one made for that device holds it
         with pytest.raises(fx.FxError, match="ws must be"):
             fx.fx_paged_decode(c.device(fx), qt, ws=ws)
+
+
+def test_ranges_of_rows_that_do_not_exist_are_refused(fx):
+    c = pr.Cache("e2m1", [20], 2, 16, seed=1)
+    dev = c.device(fx)
+    _, qt = queries(c, 1, 1, 2)
+    _, lse = fx.fx_paged_decode(dev, qt, want_lse=True)
+    rows = c.max_pages * 16
+    with pytest.raises(fx.FxError):
+        fx.fx_paged_gather(dev, -1)
+    for cand in ((5, 4), (-1, -1), (rows + 1, rows + 1), (0, rows + 1)):
+        with pytest.raises(fx.FxError):
+            fx.fx_paged_importance(dev, qt, lse, cand=cand)
+    assert fx.fx_paged_importance(dev, qt, lse, cand=(rows, rows)).shape == (1, 2, 0)
+    assert fx.fx_paged_gather(dev, 0)[0].shape == (1, 2, 0, D)
