@@ -221,8 +221,11 @@ def _on_stream(device, stream):
         return contextlib.nullcontext()
     if _per_thread(stream):
         raise FxError(FX_ERR_INVALID_ARG, _PER_THREAD_TEXT)
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(stream), device))
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # (0 and 1 are the default stream; a stream object made of 0 would be some other one)
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class Workspace:

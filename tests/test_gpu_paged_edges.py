@@ -307,3 +307,19 @@ def test_ranges_of_rows_that_do_not_exist_are_refused(fx):
             fx.fx_paged_importance(dev, qt, lse, cand=cand)
     assert fx.fx_paged_importance(dev, qt, lse, cand=(rows, rows)).shape == (1, 2, 0)
     assert fx.fx_paged_gather(dev, 0)[0].shape == (1, 2, 0, D)
+
+
+def test_memory_is_allocated_for_the_stream_of_a_handle(fx):
+    """By number: the default stream's two handles, and another's.  What a call allocates belongs to its stream."""
+    c = pr.Cache("e2m1", [300], 1, 16, seed=1)
+    dev = c.device(fx)
+    _, qt = queries(c, 2, 1, 2)
+    want = fx.fx_paged_decode(dev, qt)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle, at in ((0, 0), (1, 0), (side.cuda_stream, side.cuda_stream)):
+        with torch.cuda.stream(side), fx._on_stream(dev.device, handle):
+            assert torch.cuda.current_stream().cuda_stream == at
+        out = fx.fx_paged_decode(dev, qt, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
