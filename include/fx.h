@@ -86,7 +86,8 @@ typedef enum {
 /* Bits of the device error word (fx_device_errors). */
 #define FX_DEVERR_LEN 1u      /* a length outside [0, capacity]; it was clamped */
 #define FX_DEVERR_INDEX 2u    /* a token index outside [0, len); that entry was skipped */
-#define FX_DEVERR_OFFSETS 4u  /* branch suffix offsets decreasing or past the suffix rows; branch suffix skipped */
+#define FX_DEVERR_OFFSETS 4u  /* branch suffix offsets decreasing or past the suffix rows; branch suffix skipped (and \
+                                 the new tokens' offsets of fx_paged_attend) */
 #define FX_DEVERR_CAPACITY 8u /* a compacted cache would exceed its capacity; extra rows not written */
 #define FX_DEVERR_TIMEOUT 16u /* a bounded wait for an asynchronous copy gave up; that call's output is invalid */
 #define FX_DEVERR_PAGE 32u    /* a page number outside [0, n_pages) for a row in use; that row was skipped */
@@ -547,6 +548,48 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
                                      int64_t q_stride_h, int64_t q_stride_i, int Hq, int Mq, const float* lse,
                                      float scale, int cand_lo, int cand_hi, float* scores, unsigned flags,
                                      void* stream);
+
+/* fx_paged_attend -- attention of new tokens over a paged cache: whole prompts, chunks of them, or one token of every
+ * sequence, ragged, with what layers put on their scores: a cap, a bias by distance, a window, an interval of rows that
+ * each token sees.  [FastKV] two-stage prefill and [HPD] decoding need it beside fx_paged_decode, which has none of these;
+ * the pages describe no kernel for it.
+ *
+ * The new tokens lie behind one another: sequence b owns tokens start[b] .. start[b+1]-1 of q, n_b of them, whose rows have
+ * been appended: its token j sits at position pos = len[b] - n_b + j.  Query head g of token i (KV head g / G) sees the rows
+ *   t in [first[i], last[i]) and [0, len[b]), and with window > 0 only t > pos - window
+ * (first NULL: 0; last NULL: pos + 1, what came before it and itself).  A document mask gives first, a prefix or a picture
+ * whose tokens see one another both ways gives last.
+ *   x_t = scale * q . k_t;   with cap > 0: x_t = cap * tanh(x_t / cap);   then x_t -= slope[g] * |pos - t|
+ *   out[i, g, :] = sum_t softmax(x)_t v_t   (bf16)        lse[i, g] = log sum_t exp(x_t)   (written when lse != NULL)
+ * A query that sees no row, or whose logits are all -infinity, gives out = 0 and lse = -infinity.
+ * Logits, sums and lse are fp32.  Weights are rounded once for the product with V: to bf16 beside bf16 pages (2^-8 of a
+ * weight), to f16 beside 4-bit pages.  A row that a query does not see does not reach it, whatever it holds.  A query that
+ * sees a V with an infinity or a NaN may give NaN in all of its dimensions.
+ *   start     int32 [B+1] on the device, or NULL: max_new tokens of every sequence (n = B * max_new).  Offsets that decrease
+ *             or leave [0, n] set FX_DEVERR_OFFSETS and the sequence is skipped; of a sequence with more than max_new tokens
+ *             the first max_new are done (FX_DEVERR_OFFSETS).  Tokens of no sequence keep their out and lse.
+ *   first, last   int32 [n] on the device or NULL; any values: the interval is cut to [0, len[b])
+ *   slope     fp32 [Hq] on the device or NULL (0)
+ *   q         bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h;   out bf16 [n, Hq, 128], lse fp32 [n, Hq], contiguous
+ *   max_new   host: tokens of one sequence, at most (G*max_new <= 2^30, n*Hq < 2^31)
+ * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes.
+ */
+typedef struct {
+    const fx_bf16* q;
+    int64_t q_stride_n, q_stride_h;
+    const int32_t* start;
+    const int32_t* first;
+    const int32_t* last;
+    const float* slope;
+    fx_bf16* out;
+    float* lse;
+    int32_t n, Hq, max_new, window;
+    float scale, cap;
+} fx_paged_queries;
+
+FX_API size_t fx_paged_attend_workspace_bytes(int B, int Hkv, int Hq, int max_new);
+FX_API fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes,
+                                 unsigned flags, void* stream);
 
 /* ------------------------------------------------------------------------------------------- */
 /* fx_test_stall_wait -- testing hook for the device-side failure path; the pages have no counterpart.

@@ -28,6 +28,7 @@ __all__ = [
     "FX_DEVERR_LEN", "FX_DEVERR_INDEX", "FX_DEVERR_OFFSETS", "FX_DEVERR_CAPACITY", "FX_DEVERR_TIMEOUT",
     "FX_LAUNCH_PDL", "FX_LAUNCH_INPUTS_READY", "BranchPool",
     "PagedKV", "fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance",
+    "fx_paged_attend", "fx_paged_attend_workspace_bytes",
     "fx_paged_decode_workspace_bytes", "FX_DEVERR_PAGE", "FX_PAGED_BF16", "FX_PAGED_E2M1",
 ]
 
@@ -84,6 +85,12 @@ class PagedRows(ctypes.Structure):
                 ("q_stride_n", c_i64), ("q_stride_h", c_i64), ("qo_stride_n", c_i64), ("qo_stride_h", c_i64),
                 ("seq", c_vp), ("pos", c_vp), ("rope_pos", c_vp), ("cos_sin", c_vp), ("n", c_i32), ("Hq", c_i32),
                 ("rot", c_i32), ("n_pos", c_i32), ("interleaved", c_i32)]
+
+
+class PagedQueries(ctypes.Structure):
+    _fields_ = [("q", c_vp), ("stride_n", c_i64), ("stride_h", c_i64), ("start", c_vp), ("first", c_vp), ("last", c_vp),
+                ("slope", c_vp), ("out", c_vp), ("lse", c_vp), ("n", c_i32), ("Hq", c_i32), ("max_new", c_i32),
+                ("window", c_i32), ("scale", c_float), ("cap", c_float)]
 
 
 _lib = None
@@ -156,7 +163,10 @@ def load_library():
                                         c_vp, c_vp, c_vp, c_size, c_uint, c_vp]
         lib.fx_paged_importance.argtypes = [paged, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_float, c_int,
                                             c_int, c_vp, c_uint, c_vp]
-        for name in ("fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance"):
+        lib.fx_paged_attend_workspace_bytes.argtypes = [c_int] * 4
+        lib.fx_paged_attend_workspace_bytes.restype = c_size
+        lib.fx_paged_attend.argtypes = [paged, ctypes.c_char_p, c_vp, c_size, c_uint, c_vp]   # the bytes of a PagedQueries
+        for name in ("fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance", "fx_paged_attend"):
             getattr(lib, name).restype = c_int
         for name in ("fx_device_errors", "fx_workspace_init", "fx_focal_attn_scores", "fx_topk_select",
                      "fx_focal_mass", "fx_choose_focal_layers", "fx_csfr_schedule",
@@ -602,7 +612,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # (CUDA is up: a cache exists)
 _ROWS = struct.Struct("@PPqqPPqqqqPPPPiiiiixxxx")   # PagedRows
-assert _ROWS.size == ctypes.sizeof(PagedRows)
+_QUERIES = struct.Struct("@PqqPPPPPPiiiiff")         # PagedQueries
+assert _ROWS.size == ctypes.sizeof(PagedRows) and _QUERIES.size == ctypes.sizeof(PagedQueries)
 
 
 def _paged_bad(cache, t, name, dtype, shape, contiguous):
@@ -816,6 +827,59 @@ def fx_paged_importance(cache, q, lse, *, scale=None, cand=None, scores=None, st
     if rc:
         _check(rc)
     return scores
+
+
+def fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) -> int:
+    return int(load_library().fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new))
+
+
+def fx_paged_attend(cache, q, start=None, *, max_new=None, first=None, last=None, window: int = 0, cap: float = 0.0,
+                    slope=None, scale=None, out=None, lse=None, want_lse=False, ws=None, stream=None, flags: int = 0):
+    """Attention of new tokens over a paged cache, ragged: q [n, Hq, 128] (bf16, any strides), of which sequence b owns
+    tokens start[b] .. start[b+1]-1 (start int32 [B+1]; without it every sequence has n / B).  Their rows have been
+    appended: token j of n_b sits at position len[b] - n_b + j.  Returns out [n, Hq, 128] bf16, or (out, lse [n, Hq]
+    fp32) when lse is given or wanted; tokens of no sequence keep theirs.
+
+    max_new: tokens of one sequence, at most (n when None; a tight bound saves work).  A token sees the rows first[i] <=
+    t < last[i] (int32 [n]; 0 and its position + 1 when None), with a window only t > position - window.  cap > 0: scores
+    become cap tanh(score / cap).  slope (fp32 [Hq]): each loses slope |position - t|.
+
+    Without ws the call takes scratch memory as fx_paged_decode does.
+    """
+    lib, st = _paged_launch(cache, stream)
+    n, Hq = q.shape[:2] if isinstance(q, torch.Tensor) and q.dim() == 3 else (-1, -1)
+    q_at, qs = _paged_view(cache, q, "q", (n, Hq, 128))
+    if start is None:
+        each = n // cache.B
+        if each * cache.B != n or (max_new is not None and max_new != each):
+            raise FxError(FX_ERR_INVALID_ARG, "without start every sequence has n / B tokens")
+        start_at, max_new = 0, each
+    else:
+        start_at = _paged_tensor(cache, start, "start", torch.int32, (cache.B + 1,))
+        max_new = n if max_new is None else int(max_new)
+    first_at = 0 if first is None else _paged_tensor(cache, first, "first", torch.int32, (n,))
+    last_at = 0 if last is None else _paged_tensor(cache, last, "last", torch.int32, (n,))
+    slope_at = 0 if slope is None else _paged_tensor(cache, slope, "slope", torch.float32, (Hq,))
+    if out is None:
+        out = _paged_alloc(cache, stream, (n, Hq, 128), torch.bfloat16)
+    out_at = _paged_tensor(cache, out, "out", torch.bfloat16, (n, Hq, 128))
+    if lse is None and want_lse:
+        lse = _paged_alloc(cache, stream, (n, Hq), torch.float32)
+    lse_at = 0 if lse is None else _paged_tensor(cache, lse, "lse", torch.float32, (n, Hq))
+    if n and max_new:
+        nbytes = lib.fx_paged_attend_workspace_bytes(cache.B, cache.Hkv, Hq, max_new)
+        buf = _paged_workspace(cache, nbytes, stream, st) if ws is None else ws.ensure(nbytes, stream)
+        if buf.get_device() != cache._index:
+            raise FxError(FX_ERR_INVALID_ARG, f"ws must be a workspace on {cache.device}")
+        ws_at, ws_bytes = buf.data_ptr(), buf.numel()
+    else:
+        ws_at, ws_bytes = None, 0
+    queries = _QUERIES.pack(q_at, qs[0], qs[1], start_at, first_at, last_at, slope_at, out_at, lse_at, n, Hq, max_new,
+                            window, _SCALE if scale is None else scale, cap)
+    rc = lib.fx_paged_attend(cache._ref, queries, ws_at, ws_bytes, flags, st)
+    if rc:
+        _check(rc)
+    return out if lse is None else (out, lse)
 
 
 class BranchPool:

@@ -1270,6 +1270,73 @@ fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int6
     return FX_OK;
 }
 
+size_t fx_paged_attend_workspace_bytes(int B, int Hkv, int Hq, int max_new)
+{
+    if (B < 1 || Hkv < 1 || Hq < Hkv || max_new < 1 || (int64_t)(Hq / Hkv) * max_new > (1ll << 30)) return 0;
+    return paged_attend_workspace_bytes(paged_attend_cut(B, Hkv, Hq / Hkv, max_new, sm_count_or_default()));
+}
+
+fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags,
+                          void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_attend");
+    PagedAttendParams p;
+    memset(&p, 0, sizeof p);
+    fx_status st = paged_view(cache, true, &p.c);
+    if (st != FX_OK) return st;
+    if ((st = check_flags(flags)) != FX_OK) return st;
+    if (!q) return fail(FX_ERR_INVALID_ARG, "queries is NULL");
+    if (q->n < 0 || q->max_new < 0) return fail(FX_ERR_INVALID_ARG, "queries: n and max_new must be >= 0");
+    if ((st = check_heads(q->Hq, cache->Hkv, 1)) != FX_OK) return st;
+    const int G = q->Hq / cache->Hkv;
+    if (!q->start && (int64_t)cache->B * q->max_new != q->n)
+        return fail(FX_ERR_INVALID_ARG, "queries: without start every sequence has max_new of them (n = B * max_new)");
+    if (!isfinite(q->scale)) return fail(FX_ERR_INVALID_ARG, "scale must be finite");
+    if (!isfinite(q->cap) || q->cap < 0.f) return fail(FX_ERR_INVALID_ARG, "cap must be finite and >= 0");
+    if (q->window < 0) return fail(FX_ERR_INVALID_ARG, "window must be >= 0");
+    if (!row_stride_ok(q->q_stride_n) || !row_stride_ok(q->q_stride_h))
+        return fail(FX_ERR_INVALID_ARG, "queries: strides must be non-negative multiples of 8 elements");
+    if (q->n == 0 || q->max_new == 0) return FX_OK;
+    if (!q->q || !aligned16(q->q)) return fail(FX_ERR_INVALID_ARG, "q must be non-NULL and 16-byte aligned");
+    if (!q->out || !aligned16(q->out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+    if ((int64_t)G * q->max_new > (1ll << 30) || (int64_t)q->n * q->Hq > 0x7fffffff)
+        return fail(FX_ERR_UNSUPPORTED, "queries: too many rows");
+    const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, sm_count_or_default());
+    if (!cut.split && cut.blocks > 65535) return fail(FX_ERR_UNSUPPORTED, "queries: too many of one sequence");
+    if ((st = check_ws(ws, ws_bytes, paged_attend_workspace_bytes(cut))) != FX_OK) return st;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.q = q->q;
+    p.q_n = q->q_stride_n;
+    p.q_h = q->q_stride_h;
+    p.start = q->start;
+    p.first = q->first;
+    p.last = q->last;
+    p.slope = q->slope;
+    p.n = q->n;
+    p.Hq = q->Hq;
+    p.G = G;
+    p.max_new = q->max_new;
+    p.window = q->window;
+    p.scale = fabsf(q->scale) * p.c.k_mul;
+    p.flip = q->scale < 0.f ? 0x80008000u : 0u;
+    p.cap = q->cap;
+    p.out = q->out;
+    p.lse = q->lse;
+    p.blocks = cut.blocks;
+    p.split = cut.split;
+    p.part_rows = cut.part_rows;
+    p.sm_count = ds->sm_count;
+    p.counters = static_cast<unsigned*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
+    p.part_ml = p.part + (size_t)cut.split * cut.part_rows * kHeadDim;
+    p.err = ds->err;
+    cudaError_t e = launch_paged_attend(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+                                        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged attend launch");
+    return FX_OK;
+}
+
 }  // extern "C"
 
 // Tensor maps of one layer's K and V for the streaming decode kernel: [B][Hkv][Tcap][128] bf16 with the

@@ -260,6 +260,32 @@ struct PagedGatherParams {
     unsigned* err;
 };
 
+// fx_paged_attend (paged_attend.cu).
+struct PagedAttendCut {
+    int blocks;      // blocks of query rows of one (sequence, KV head), at most
+    int split;       // CTAs among which the blocks' tiles are shared, or 0: one CTA to a block
+    int part_rows;   // query rows of a part
+};
+struct PagedAttendParams {
+    PagedCache c;
+    const uint16_t* q;
+    int64_t q_n, q_h;
+    const int32_t* start;
+    const int32_t* first;
+    const int32_t* last;
+    const float* slope;
+    int n, Hq, G, max_new, window;
+    float scale, cap;         // scale: of the logits, with 2^k_exp, not negative
+    uint32_t flip;            // 0x80008000: the queries' signs turn (a negative scale); else 0
+    uint16_t* out;            // [n, Hq, 128]
+    float* lse;               // [n, Hq] or nullptr
+    int blocks, split, part_rows, sm_count;
+    unsigned* counters;       // arrival counters (zero between calls), then the parts
+    float* part;              // [split][part_rows][128]
+    float* part_ml;           // [split][part_rows][2]: reference (base 2) and sum
+    unsigned* err;
+};
+
 struct PagedAttnParams {
     PagedCache c;
     const uint16_t* q;
@@ -326,6 +352,9 @@ cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, int sm_co
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);
+cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s);
+PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count);
+size_t paged_attend_workspace_bytes(const PagedAttendCut& c);
 
 // Launch `kern` with optional programmatic stream serialization and a (1, cluster_y, 1) cluster.
 template <typename... KArgs, typename... Args>

@@ -1,0 +1,1009 @@
+// Attention of ragged new tokens -- a prompt's, a chunk's, or one of every sequence -- over a paged cache for sm_103a
+// (tcgen05, accumulators in tensor memory): fx_paged_attend.
+//
+// The query rows of a (sequence, KV head) are its new tokens' G heads, token by token: row r is head r % G of token
+// r / G.  A CTA takes 256 of them as two subtiles of 128 and walks the tiles of 128 cache rows that any of them sees:
+//   S = Q K^T   (M = 128 query rows, N = 128 cache rows, K = 128 dimensions)   shared x shared -> tensor memory
+//   O += P V    (M = 128 query rows, N = 128 dimensions, K = 128 cache rows)   tensor memory x shared -> tensor memory
+// with an online softmax between them, P in the place of S.  Warps 0-3 and 4-7 are the softmax of the two subtiles, one
+// thread a query row, so that no row is shared; one subtile's products run while the other's weights are formed.  Warps
+// 8-11 fill a ring of operand slots (K and V tiles in turn) through the page table, warp 12 issues the products.
+//
+// bf16 pages: rows go to the swizzled slots by cp.async, as they are.  4-bit pages: codes and scales go to a small ring of
+// their own and become f16 values there (exact: at most 6 significant bits between 2^-10 and 2688); queries are f16 scaled
+// by a power of two per row (largest magnitude in [2^14, 2^15)), so no bit of a bf16 query within 2^-24 of its row's
+// largest is lost.
+//
+// P is rounded once, to the operands' type (bf16: at most 2^-8 of a weight; f16: 2^-11): the output is bf16, whose rounding is as
+// large.  Logits, maxima, sums and O are fp32.
+//
+// Few query rows (a decode step) are cut along the cache: every block's tiles become parts of nearly equal length by the
+// lengths found on the device, and the last CTA of a block to arrive joins its parts in their order.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace fx {
+namespace {
+
+constexpr int kThreadsA = 512;
+constexpr int kSub = 128;                        // query rows of a subtile: one tensor-memory lane each
+constexpr int kBlock = 2 * kSub;                 // query rows of a CTA
+constexpr int kKeys = 128;                       // cache rows of a tile
+constexpr int kOperand = 128 * 128 * 2;          // bytes of an operand tile
+constexpr int kRawTile = kKeys * 64 + kKeys * 8; // codes and scales of a 4-bit tile (K or V)
+constexpr int kRaw = 3;                          // such tiles in their ring
+// slots of the operand ring: what fits beside Q (and the raw ring)
+__host__ __device__ constexpr int slots(bool e2m1) { return e2m1 ? 4 : 5; }
+__host__ __device__ constexpr int attend_smem(bool e2m1)
+{
+    return 2 * kOperand + slots(e2m1) * kOperand + (e2m1 ? kRaw * kRawTile : 0) + 1024;
+}
+constexpr int kLag = 3;                          // bf16: tiles whose copies are under way
+// Registers a thread of the softmax, the fillers and the issuing warp; the launch's 128 a thread cover their sum.
+constexpr int kRegsSoftmax = 192, kRegsFill = 88, kRegsIssue = 40;
+static_assert(2 * kRegsSoftmax + kRegsFill + kRegsIssue <= 4 * 128, "a split above the launch's registers never starts");
+// tensor-memory columns: S (P in its first half) of the subtiles, O of the subtiles
+__device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * 128); }
+__device__ __forceinline__ uint32_t col_o(int x) { return (uint32_t)(256 + x * 128); }
+constexpr int kRing = 16;                        // tiles whose flags are kept (the fillers are at most 4 ahead, and what
+                                                 // they clear lies 8 behind)
+// The largest weight so far is 2^kWeightBase when its row's reference moves, and grows by 2^kMaxSlack at most before it
+// moves again.  f16: small weights stay normal numbers.  bf16: sums of products with values up to the type's largest
+// stay finite, as their mean is.
+template <bool E2M1>
+constexpr float kWeightBase = E2M1 ? 6.f : -32.f;
+constexpr float kFarRef = 4194304.f;   // 2^22: beyond it products and their rounded values lie too far apart for one fma
+
+constexpr int kMaxPlan = 512;                    // (sequence, block) pairs of a call that is cut along the cache
+
+struct AttendSmem {
+    uint64_t full[5], empty[5], s_full[2], p_full[2], o_done[2];
+    uint32_t tmem;
+    int vis_lo, vis_hi, com_lo, com_hi;          // rows that some query of the CTA sees; that all of them see
+    unsigned skip[kRing];                        // 16-row groups of a tile that lie in bad pages
+    unsigned bad_v[kRing][4];                    // rows of a tile whose V is not finite (only where not all see them)
+    int any_bad;
+    int scan[16];
+    int plan_i, plan_at, plan_parts, total;
+    unsigned last;
+};
+static_assert(attend_smem(true) + sizeof(AttendSmem) <= 227 * 1024 && attend_smem(false) + sizeof(AttendSmem) <= 227 * 1024,
+              "shared memory of a CTA");
+
+// One wait, given up after kSpinLimit polls; after a first such no later one is waited for.
+__device__ __forceinline__ void wait(uint64_t* bar, unsigned parity, unsigned* err, bool& dead)
+{
+    if (dead) return;
+    unsigned spins = 0, done = 0;
+    while (!done) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (!done && ++spins == kSpinLimit) {
+            atomicOr(err, FX_DEVERR_TIMEOUT);
+            dead = true;
+            break;
+        }
+    }
+}
+__device__ __forceinline__ void arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void init_barrier(uint64_t* bar, unsigned count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count));
+}
+__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <bool E2M1>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    if (E2M1) {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Instruction descriptor: 16-bit x 16-bit -> fp32, 128 x 128, A K-major, B K-major or MN-major.
+template <bool E2M1>
+__host__ __device__ constexpr uint32_t idesc(bool b_mn_major)
+{
+    const uint32_t d = idesc_bf16(128, 128, b_mn_major);
+    return E2M1 ? d & ~((1u << 7) | (1u << 10)) : d;   // (both operands f16 instead of bf16)
+}
+
+template <bool E2M1>
+__device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q_tile, uint32_t k_tile)
+{
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t off = (uint32_t)((ks >> 2) * (kOperand / 2) + (ks & 3) * 32);
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(sdesc(q_tile + off)), "l"(sdesc(k_tile + off)), "r"(idesc<E2M1>(false)), "r"(ks > 0 ? 1u : 0u));
+    }
+}
+template <bool E2M1>
+__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_tile, bool accumulate)
+{
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(p_tmem + 8 * ks), "l"(sdesc(v_tile + ks * 2048, kOperand / 2)), "r"(idesc<E2M1>(true)),
+            "r"((accumulate || ks > 0) ? 1u : 0u));
+    }
+}
+
+// 128 columns of this thread's tensor-memory lane, four loads under way together.
+__device__ __forceinline__ void tmem_issue32(uint32_t addr, uint32_t* u)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+          "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+          "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_row(uint32_t addr, float (&s)[128])
+{
+    uint32_t u[128];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_issue32(addr + 32 * c, u + 32 * c);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 128; ++i) {
+        asm volatile("" : "+r"(u[i]));   // (used after the wait only)
+        s[i] = __uint_as_float(u[i]);
+    }
+}
+
+// ---- the fillers -------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 8u : 0u) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The page of 16-row group lane % 8 of a tile: -1 for a group without a row in [lo, hi), -2 for a bad entry.
+__device__ __forceinline__ int group_page(const PagedCache& c, const int32_t* table, int tile, int lo, int hi, unsigned* err)
+{
+    const int row = tile * kKeys + 16 * (threadIdx.x & 7);
+    if (row >= hi || row + 16 <= lo) return -1;
+    const int pg = table[row >> c.page_shift];
+    if ((unsigned)pg < (unsigned)c.n_pages) return pg;
+    if ((threadIdx.x & 31) < 8) atomicOr(err, FX_DEVERR_PAGE);
+    return -2;
+}
+__device__ __forceinline__ unsigned bad_groups(int page) { return __ballot_sync(0xffffffffu, page == -2) & 0xffu; }
+
+// Whether 16 bytes of bf16 values hold an infinity or a NaN.
+__device__ __forceinline__ bool not_finite(uint4 x)
+{
+    const uint32_t e = 0x7f807f80u;
+    return (__vcmpeq2(x.x & e, e) | __vcmpeq2(x.y & e, e) | __vcmpeq2(x.z & e, e) | __vcmpeq2(x.w & e, e)) != 0;
+}
+
+struct FillRange {
+    int ta, tb;           // tiles
+    int lo, hi;           // rows that some query sees
+    int com_lo, com_hi;   // rows that all see
+    // whether a tile has rows that only some of the queries see
+    __device__ __forceinline__ bool partial(int t) const
+    {
+        const int a = t * kKeys, b = a + kKeys;
+        return max(a, lo) < min(b, com_lo) || max(a, com_hi) < min(b, hi);
+    }
+};
+
+// bf16: a thread copies 16-byte chunk tid % 16 of rows tid / 16 + 8 i of every tile.
+__device__ __forceinline__ void fill_bf16(const PagedAttendParams& p, AttendSmem& sm, uint32_t ring, const int32_t* table, int h,
+                                          const FillRange& r)
+{
+    constexpr int kSlots = slots(false);
+    const PagedCache& c = p.c;
+    const int tid = threadIdx.x & 127, chunk = tid & 15, row0 = tid >> 4;
+    const int n = 2 * (r.tb - r.ta);
+    const uint32_t to = sw128(row0, 8 * chunk, kKeys);
+    const char* const kb = c.k + (int64_t)h * c.sh + 16 * chunk;
+    const int64_t dv = c.v - c.k;
+    bool dead = false;
+    int page = group_page(c, table, r.ta, r.lo, r.hi, p.err), next = page;
+    auto done = [&](int m) {   // tile m's copies have landed
+        if ((m & 1) && r.partial(r.ta + (m >> 1))) {
+            const int t = r.ta + (m >> 1);
+            const uint32_t at = ring + (m % kSlots) * kOperand + to;
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                if (!not_finite(lds128(at + 1024 * i))) continue;
+                sts128(at + 1024 * i, make_uint4(0u, 0u, 0u, 0u));
+                const int row = row0 + 8 * i;
+                atomicOr(&sm.bad_v[t & (kRing - 1)][row >> 5], 1u << (row & 31));
+                sm.any_bad = 1;
+            }
+        }
+        fence_operands();
+        arrive(&sm.full[m % kSlots]);
+    };
+    for (int m = 0; m < n; ++m) {
+        const int t = r.ta + (m >> 1), slot = m % kSlots;
+        if ((m & 1) == 0) {
+            page = next;
+            if (t + 1 < r.tb) next = group_page(c, table, t + 1, r.lo, r.hi, p.err);
+            const unsigned bad = bad_groups(page);
+            if (tid == 0) {
+                sm.skip[t & (kRing - 1)] = bad;
+                // (the tile that last had these flags is long done)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) sm.bad_v[(t + 8) & (kRing - 1)][w] = 0u;
+            }
+        }
+        if (m >= kSlots) wait(&sm.empty[slot], (unsigned)(m / kSlots - 1) & 1u, p.err, dead);
+        const uint32_t dst = ring + slot * kOperand + to;
+        const char* const base = m & 1 ? kb + dv : kb;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, page, i >> 1);
+            const int row = t * kKeys + row0 + 8 * i;
+            const bool on = pg >= 0 && row >= r.lo && row < r.hi;
+            const char* src = base;
+            if (on) src += (uint64_t)(uint32_t)pg * c.sp + (uint64_t)(uint32_t)(row & c.page_mask) * c.st;
+            copy16(dst + 1024 * i, src, on);
+        }
+        commit_copies();
+        if (m >= kLag) {
+            wait_copies<kLag>();
+            done(m - kLag);
+        }
+    }
+    wait_copies<0>();
+    for (int m = max(n - kLag, 0); m < n; ++m) done(m);
+}
+
+// 4 bits: lane l of a warp takes chunk l / 8 (32 values) of rows 8 warp + l % 8 + 32 i, so that neither the codes' nor the
+// values' chunks of eight lanes meet in a bank.
+__device__ __forceinline__ void fill_e2m1(const PagedAttendParams& p, AttendSmem& sm, uint32_t ring, uint32_t raw,
+                                          const int32_t* table, int h, const FillRange& r)
+{
+    constexpr int kSlots = slots(true);
+    const PagedCache& c = p.c;
+    const int tid = threadIdx.x & 127, lane = tid & 31, chunk = lane >> 3, row0 = (tid >> 5) * 8 + (lane & 7);
+    const int n = 2 * (r.tb - r.ta);
+    const uint32_t from = (uint32_t)(row0 * 64 + ((chunk ^ ((row0 >> 1) & 3)) << 4));
+    const char* const kb = c.k + (int64_t)h * c.sh + 16 * chunk;
+    const char* const sb = c.ks + (int64_t)h * c.ssh;
+    const int64_t dv = c.v - c.k, ds = c.vs - c.ks;
+    bool dead = false;
+    int page = -1, next = group_page(c, table, r.ta, r.lo, r.hi, p.err);
+    auto feed = [&](int m) {
+        if (m < n) {
+            const int t = r.ta + (m >> 1);
+            if ((m & 1) == 0) {
+                page = next;
+                if (t + 1 < r.tb) next = group_page(c, table, t + 1, r.lo, r.hi, p.err);
+                const unsigned bad = bad_groups(page);
+                if (tid == 0) {
+                    sm.skip[t & (kRing - 1)] = bad;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) sm.bad_v[(t + 8) & (kRing - 1)][w] = 0u;
+                }
+            }
+            const uint32_t dst = raw + (m % kRaw) * kRawTile;
+            const char* const base = m & 1 ? kb + dv : kb;
+            const char* const sbase = m & 1 ? sb + ds : sb;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pg = __shfl_sync(0xffffffffu, page, (row0 >> 4) + 2 * i);
+                const int row = t * kKeys + row0 + 32 * i;
+                const bool on = pg >= 0 && row >= r.lo && row < r.hi;
+                const uint32_t in = (uint32_t)(row & c.page_mask);
+                const char* src = base;
+                if (on) src += (uint64_t)(uint32_t)pg * c.sp + (uint64_t)in * c.st;
+                copy16(dst + from + 2048 * i, src, on);
+                if (chunk == 0) {
+                    const char* ssrc = sbase;
+                    if (on) ssrc += (uint64_t)(uint32_t)pg * c.ssp + (uint64_t)in * c.sst;
+                    copy8(dst + kKeys * 64 + (row0 + 32 * i) * 8, ssrc, on);
+                }
+            }
+        }
+        commit_copies();
+    };
+    for (int m = 0; m < kRaw - 1; ++m) feed(m);
+    for (int m = 0; m < n; ++m) {
+        const int t = r.ta + (m >> 1), slot = m % kSlots;
+        wait_copies<kRaw - 2>();
+        __syncwarp();   // (a row's scales were copied by another lane)
+        if (m >= kSlots) wait(&sm.empty[slot], (unsigned)(m / kSlots - 1) & 1u, p.err, dead);
+        const uint32_t src = raw + (m % kRaw) * kRawTile, dst = ring + slot * kOperand;
+        const bool look = (m & 1) && r.partial(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 32 * i;
+            const uint4 x = lds128(src + from + 2048 * i);
+            uint32_t sc = lds16(src + kKeys * 64 + row * 8 + 2 * chunk);
+            if (look) {
+                const uint32_t nan = __vcmpeq4(sc & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0xffffu;
+                if (nan) {
+                    sc &= ~nan;
+                    atomicOr(&sm.bad_v[t & (kRing - 1)][row >> 5], 1u << (row & 31));
+                    sm.any_bad = 1;
+                }
+            }
+            const uint32_t z = e4m3x2_to_f16x2(sc);
+            const uint32_t s0 = __byte_perm(z, 0, 0x1010), s1 = __byte_perm(z, 0, 0x3232);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t at = dst + (chunk >> 1) * (kOperand / 2) + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t f0, f1, f2, f3;
+                e2m1x8_to_f16(w[k], f0, f1, f2, f3);
+                const uint32_t s = k < 2 ? s0 : s1;
+                sts128(at + ((((chunk & 1) * 4 + k) ^ (row & 7)) << 4),
+                       make_uint4(hmul2_u32(f0, s), hmul2_u32(f1, s), hmul2_u32(f2, s), hmul2_u32(f3, s)));
+            }
+        }
+        fence_operands();
+        arrive(&sm.full[slot]);
+        __syncwarp();   // every lane is done with the raw tile that the next copies overwrite
+        feed(m + kRaw - 1);
+    }
+    wait_copies<0>();
+}
+
+// ---- the softmax ---------------------------------------------------------------------------------------
+// tanh(y) = 1 - 2 / (exp(2y) + 1).
+__device__ __forceinline__ float tanh_exp(float y)
+{
+    float x = y * 2.885390081777927f;
+    x = x > 126.f ? 126.f : x;   // (a NaN stays)
+    const float e = ex2(x);
+    return fmaf(-2.f, __fdividef(1.f, e + 1.f), 1.f);
+}
+
+// The queries of sequence b: the first row of q and their number (0 for offsets that are not good).
+__device__ __forceinline__ void sequence_queries(const PagedAttendParams& p, int b, bool report, int& q0, int& nb, int& all)
+{
+    if (!p.start) {
+        q0 = b * p.max_new;
+        nb = all = p.max_new;
+        return;
+    }
+    q0 = p.start[b];
+    const int q1 = p.start[b + 1];
+    all = q1 - q0;
+    if (q0 < 0 || q1 < q0 || q1 > p.n) {
+        q0 = 0;
+        all = 0;
+        if (report) atomicOr(p.err, FX_DEVERR_OFFSETS);
+    } else if (all > p.max_new && report) {
+        atomicOr(p.err, FX_DEVERR_OFFSETS);
+    }
+    nb = min(all, p.max_new);
+}
+__device__ __forceinline__ int sequence_length(const PagedAttendParams& p, int b, bool report)
+{
+    const int len = p.c.len[b];
+    if (report && (len < 0 || len > p.c.cap)) atomicOr(p.err, FX_DEVERR_LEN);
+    return min(max(len, 0), p.c.cap);
+}
+
+// Tiles [t0, t1) that hold whatever a block's queries may see, as far as lengths, positions and the window tell.
+__device__ __forceinline__ void block_tiles(const PagedAttendParams& p, int len, int nb, int all, int blk, int& t0, int& t1)
+{
+    const int j0 = blk * kBlock / p.G, j1 = min((blk * kBlock + kBlock - 1) / p.G, nb - 1);
+    const int lo = p.window > 0 ? max(len - all + j0 - p.window + 1, 0) : 0;
+    const int hi = p.last ? len : min(len, len - all + j1 + 1);
+    t0 = lo / kKeys;
+    t1 = hi > lo ? (hi + kKeys - 1) / kKeys : t0;
+}
+
+constexpr int kSearch = 192;   // blocks up to which the shares are tried one by one
+constexpr int kPartCost = 6;   // what a part costs a CTA besides its tiles, counted in tiles
+
+// Shares the tiles of all blocks among the CTAs: parts of a block of n tiles are ceil(n / share).  Returns false when there
+// is nothing for this CTA; else its block (sm.plan_i) and its place among the parts of the block's heads.
+__device__ __forceinline__ bool plan(const PagedAttendParams& p, AttendSmem& sm, int* count, int& n_parts, int& at, int& i)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nq = p.c.B * p.blocks;
+    int mine = 0;
+    if (tid < nq) {
+        const int b = tid / p.blocks, blk = tid - b * p.blocks;
+        int q0, nb, all;
+        sequence_queries(p, b, blockIdx.x == 0 && blk == 0, q0, nb, all);
+        const int len = sequence_length(p, b, blockIdx.x == 0 && blk == 0);
+        if (blk * kBlock < nb * p.G) {
+            int t0, t1;
+            block_tiles(p, len, nb, all, blk, t0, t1);
+            mine = max(t1 - t0, 1);
+        }
+        count[tid] = mine;
+    }
+    int total = mine;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane == 0) sm.scan[warp] = total;
+    if (tid == 0) sm.plan_i = -1;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) total += sm.scan[w];
+    // lanes try shares: 1 to 3 times an even one, and a half to a quarter of it (several parts to a CTA in turn)
+    const float even = fmaxf((float)total * p.c.Hkv / (float)p.sm_count, 1.f);
+    float share = lane < 24 ? even * (1.f + lane / 12.f) : even / (1.f + 0.5f * (lane - 23));
+    if (lane == 23 || nq > kSearch) share = nq > kSearch ? even * 0.5f : 1e9f;   // (no cuts: always possible)
+    share = fmaxf(share, 4.f);
+    float inv = 1.f / share;
+    if (nq <= kSearch) {
+        int sum = 0;
+        float longest = 0.f;
+        for (int k = 0; k < nq; ++k) {
+            const int n = count[k];
+            const int parts = min((int)((float)n * inv) + 1, n);   // (0 for a block without rows)
+            sum += parts;
+            longest = fmaxf(longest, __fdividef((float)n, (float)max(parts, 1)));
+        }
+        const float all = (float)sum * p.c.Hkv;
+        float cost = longest + kPartCost;
+        if (all > (float)p.sm_count) cost = ((float)total * p.c.Hkv + kPartCost * all) / (float)p.sm_count + 0.5f * cost;
+        if (all > (float)gridDim.x) cost = 3e38f;
+        float best = cost;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, d));
+        inv = __shfl_sync(0xffffffffu, inv, __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1);
+    }
+    const int parts = mine > 0 ? min((int)((float)mine * inv) + 1, mine) : 0;
+    int inc = parts;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    __syncthreads();   // sm.scan is free
+    if (lane == 31) sm.scan[warp] = inc;
+    __syncthreads();
+    int before = inc - parts;
+#pragma unroll
+    for (int w = 0; w < 16; ++w)
+        if (w < warp) before += sm.scan[w];
+    const int64_t first = (int64_t)before * p.c.Hkv, here = blockIdx.x;
+    if (parts > 0 && here >= first && here < first + (int64_t)parts * p.c.Hkv) {
+        sm.plan_i = tid;
+        sm.plan_at = (int)(here - first);
+        sm.plan_parts = parts;
+    }
+    __syncthreads();
+    i = sm.plan_i;
+    at = sm.plan_at;
+    n_parts = sm.plan_parts;
+    return i >= 0;
+}
+
+template <bool E2M1, bool SHAPED>
+__global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid_constant__ PagedAttendParams p)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ __align__(16) AttendSmem sm;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t ring = base + 2 * kOperand, raw = ring + slots(E2M1) * kOperand;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    griddep_wait();
+    griddep_launch();
+    // ---- which rows, which tiles
+    int b, h, blk, part = 0, n_parts = 1, unit = 0;
+    if (p.split) {
+        int at, i;
+        if (!plan(p, sm, reinterpret_cast<int*>(smem_raw), n_parts, at, i)) return;
+        b = i / p.blocks;
+        blk = i - b * p.blocks;
+        h = at / n_parts;
+        part = at - h * n_parts;
+        unit = i * p.c.Hkv + h;
+    } else {
+        h = blockIdx.x;
+        blk = gridDim.y - 1 - blockIdx.y;   // the longest first, where a query sees what came before it
+        b = blockIdx.z;
+    }
+    int q0, nb, all;
+    const bool report = !p.split && h == 0 && blk == 0 && tid == 0;
+    sequence_queries(p, b, report, q0, nb, all);
+    if (blk * kBlock >= nb * p.G) return;
+    const int len = sequence_length(p, b, report);
+    const int rows = min(nb * p.G - blk * kBlock, kBlock);
+    const bool two = rows > kSub;
+
+    // ---- this thread's row (of the first 256 threads)
+    const int row = tid;
+    const bool live = row < rows;
+    int lo = 0, hi = 0, pos = 0;
+    int64_t qi = 0;   // token
+    int g = 0;
+    if (live) {
+        const int r = blk * kBlock + row, j = r / p.G;
+        g = h * p.G + r - j * p.G;
+        qi = (int64_t)q0 + j;
+        pos = len - all + j;
+        hi = p.last ? min(p.last[qi], len) : min(pos + 1, len);
+        lo = p.first ? max(p.first[qi], 0) : 0;
+        if (p.window > 0) lo = max(lo, pos - p.window + 1);
+    }
+    if (tid == 0) {
+        sm.vis_lo = sm.com_hi = 0x7fffffff;
+        sm.vis_hi = sm.com_lo = 0;
+        sm.any_bad = 0;
+        for (int i = 0; i < kRing; ++i)
+            for (int w = 0; w < 4; ++w) sm.bad_v[i][w] = 0u;
+        for (int i = 0; i < slots(E2M1); ++i) {
+            init_barrier(&sm.full[i], 128);
+            init_barrier(&sm.empty[i], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            init_barrier(&sm.s_full[x], 1);
+            init_barrier(&sm.p_full[x], kSub);
+            init_barrier(&sm.o_done[x], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // ---- the queries
+    float qs = p.scale;   // factor of the row's logits
+    if (tid < kBlock) {
+        const uint32_t tile = base + (row >> 7) * kOperand;
+        const uint16_t* src = p.q + qi * p.q_n + (int64_t)g * p.q_h;
+        uint4 x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            x[k] = live ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+            x[k] = make_uint4(x[k].x ^ p.flip, x[k].y ^ p.flip, x[k].z ^ p.flip, x[k].w ^ p.flip);
+        }
+        if (E2M1) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+            }
+            // 2^(14 - exponent of the largest); tiny rows (below 2^-100) are scaled as if they were that large
+            const int ex = min(max((int)(top >> 23) - 127, -100), 127);
+            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            const bool finite = top < 0x7f800000u;
+            auto half = [&](uint32_t w) {
+                const uint32_t v = pack2<true>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                return finite ? v : 0x7fff7fffu;   // else the row is NaN
+            };
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = make_uint4(half(x[k].x), half(x[k].y), half(x[k].z), half(x[k].w));
+            qs *= __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sts128(tile + sw128(row & 127, 8 * k, kSub), x[k]);
+        fence_operands();
+    }
+    __syncthreads();
+    if (tid < kBlock) {
+        const bool sees = live && lo < hi;
+        const int a = __reduce_min_sync(0xffffffffu, sees ? lo : 0x7fffffff), c = __reduce_min_sync(0xffffffffu, sees ? hi : 0x7fffffff);
+        const int d = __reduce_max_sync(0xffffffffu, sees ? lo : 0), e = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
+        if (lane == 0) {
+            atomicMin(&sm.vis_lo, a);
+            atomicMax(&sm.vis_hi, e);
+            atomicMax(&sm.com_lo, d);
+            atomicMin(&sm.com_hi, c);
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sm.tmem;
+    FillRange r;
+    r.lo = sm.vis_lo;
+    r.hi = sm.vis_hi;
+    r.com_lo = sm.com_lo;
+    r.com_hi = sm.com_hi;
+    r.ta = r.tb = 0;
+    if (r.lo < r.hi) {
+        r.ta = r.lo / kKeys;
+        r.tb = (r.hi + kKeys - 1) / kKeys;
+        if (n_parts > 1) {
+            int t0, t1;
+            block_tiles(p, len, nb, all, blk, t0, t1);
+            const int64_t n = t1 - t0;
+            r.ta = max(r.ta, t0 + (int)(n * part / n_parts));
+            r.tb = min(r.tb, t0 + (int)(n * (part + 1) / n_parts));
+            r.tb = max(r.tb, r.ta);
+        }
+    }
+    const int nt = r.tb - r.ta;
+
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 12 && nt > 0) {
+            constexpr int kSlots = slots(E2M1);
+            bool dead = false;
+            auto slot_of = [&](int m) { return ring + (uint32_t)(m % kSlots) * kOperand; };
+            auto wait_full = [&](int m) {
+                wait(&sm.full[m % kSlots], (unsigned)(m / kSlots) & 1u, p.err, dead);
+                tc_after();
+            };
+            wait_full(0);
+            if (lane == 0) {
+                mma_qk<E2M1>(tmem + col_s(0), base, slot_of(0));
+                mma_commit(&sm.s_full[0]);
+                if (two) {
+                    mma_qk<E2M1>(tmem + col_s(1), base + kOperand, slot_of(0));
+                    mma_commit(&sm.s_full[1]);
+                }
+                mma_commit(&sm.empty[0]);
+            }
+            __syncwarp();
+            for (int t = 0; t < nt; ++t) {
+                wait_full(2 * t + 1);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x == 1 && !two) break;
+                    const bool last_x = x == 1 || !two;
+                    wait(&sm.p_full[x], (unsigned)t & 1u, p.err, dead);
+                    tc_after();
+                    if (lane == 0) {
+                        mma_pv<E2M1>(tmem + col_o(x), tmem + col_s(x), slot_of(2 * t + 1), t > 0);
+                        if (last_x) mma_commit(&sm.empty[(2 * t + 1) % kSlots]);
+                    }
+                    __syncwarp();
+                    if (t + 1 < nt) {
+                        if (x == 0) wait_full(2 * t + 2);
+                        if (lane == 0) {
+                            mma_qk<E2M1>(tmem + col_s(x), base + x * kOperand, slot_of(2 * t + 2));
+                            mma_commit(&sm.s_full[x]);
+                            if (last_x) mma_commit(&sm.empty[(2 * t + 2) % kSlots]);
+                        }
+                    } else if (lane == 0) {
+                        mma_commit(&sm.o_done[x]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
+        if (nt > 0) {
+            const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
+            if constexpr (E2M1)
+                fill_e2m1(p, sm, ring, raw, table, h, r);
+            else
+                fill_bf16(p, sm, ring, table, h, r);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int x = warp >> 2;
+        const bool on = x == 0 || two;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        bool dead = false, poison = false;
+        float m = -INFINITY, l = 0.f;   // reference and sum (in units of 2^kWeightBase)
+        // rows that do not exist see every row of their zeros, so that they ask for no masks
+        const int my_lo = live ? lo : -0x40000000, my_hi = live ? hi : 0x7fffffff;
+        const float cap = p.cap, icap = cap > 0.f ? 1.f / cap : 0.f;
+        const float slope2 = SHAPED && p.slope && live ? p.slope[g] * 1.4426950408889634f : 0.f;
+        if (!SHAPED) qs *= 1.4426950408889634f;
+        auto check = [&](int t) {   // whether the row sees a value of tile t that is not finite (those were left out)
+            if (*(volatile int*)&sm.any_bad == 0) return;
+            for (int w = 0; w < 4; ++w) {
+                unsigned bits = *(volatile unsigned*)&sm.bad_v[t & (kRing - 1)][w];
+                while (bits) {
+                    const int at = t * kKeys + 32 * w + __ffs(bits) - 1;
+                    bits &= bits - 1;
+                    poison |= at >= my_lo && at < my_hi;
+                }
+            }
+        };
+        if (on) {
+            for (int t = 0; t < nt; ++t) {
+                wait(&sm.s_full[x], (unsigned)t & 1u, p.err, dead);
+                tc_after();
+                float s[128];
+                tmem_row(lanes + col_s(x), s);
+                const int tile = r.ta + t, j0 = tile * kKeys;
+                if (t > 0) check(tile - 1);
+                const unsigned skip = *(volatile unsigned*)&sm.skip[tile & (kRing - 1)];
+                const int a = my_lo - j0, e = my_hi - j0;   // the row sees keys a <= k < e of the tile
+                const bool whole = a <= 0 && e >= kKeys;
+                float f = qs;
+                if (SHAPED) {
+                    // base-2 logits in place
+                    const float d0 = (float)(pos - j0);
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) {
+                        float v = s[k] * qs;
+                        if (cap > 0.f) v = cap * tanh_exp(v * icap);
+                        s[k] = fmaf(fabsf(d0 - (float)k), -slope2, v * 1.4426950408889634f);
+                    }
+                    f = 1.f;
+                }
+                // the largest logit that the row sees
+                const bool masked = __any_sync(0xffffffffu, !whole) || skip != 0;
+                float mt = -INFINITY;
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) {
+                        const bool see = k >= a && k < e && ((skip >> (k >> 4)) & 1u) == 0;
+                        s[k] = see ? s[k] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 128; k += 2) mt = max3(mt, s[k], s[k + 1]);
+                // (a negative factor was moved into the queries; a hidden logit stays -inf also with a factor of 0)
+                mt = mt == -INFINITY ? mt : __fmul_rn(mt, f);
+                const bool grow = mt > m + kMaxSlack;   // also when there is none yet and the row sees something
+                const float mnew = grow ? mt : m;
+                if (t > 0 && __any_sync(0xffffffffu, grow)) {   // O of the tiles before is complete: S was issued after it
+                    const float z = !grow ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mnew));
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        uint32_t w[32];
+                        tmem_ld32(lanes + col_o(x) + 32 * c, v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(v[k] * z);
+                        tmem_st32(lanes + col_o(x) + 32 * c, w);
+                    }
+                    l *= z;
+                }
+                m = mnew;
+                const float bias = (m == -INFINITY ? 0.f : -m) + kWeightBase<E2M1>;
+                uint32_t w[64];
+                float2 l2 = make_float2(0.f, 0.f);
+                const bool far = __any_sync(0xffffffffu, fabsf(bias) > kFarRef);
+                if (!far && !(masked && f == 0.f)) {
+                    const float2 ff = make_float2(f, f), bb = make_float2(bias, bias);
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        const float2 y = fma2(make_float2(s[2 * k], s[2 * k + 1]), ff, bb);
+                        const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+                        l2 = add2(l2, pp);
+                        w[k] = pack2<E2M1>(pp.x, pp.y);
+                    }
+                } else {
+                    // (rounded products, as the reference is one; a hidden logit is -inf whatever the factor)
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        float y[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float v = s[2 * k + u];
+                            y[u] = v == -INFINITY ? 0.f
+                                                  : ex2(__fadd_rn(__fadd_rn(__fmul_rn(v, f), m == -INFINITY ? 0.f : -m), kWeightBase<E2M1>));
+                        }
+                        l2 = add2(l2, make_float2(y[0], y[1]));
+                        w[k] = pack2<E2M1>(y[0], y[1]);
+                    }
+                }
+                l += l2.x + l2.y;
+                tmem_st32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
+                tmem_st32(lanes + col_s(x) + 32, reinterpret_cast<uint32_t(&)[32]>(w[32]));
+                tc_before();
+                arrive(&sm.p_full[x]);
+            }
+            if (nt > 0) {
+                wait(&sm.o_done[x], 0u, p.err, dead);
+                tc_after();
+                check(r.tb - 1);
+            }
+            const bool none = l == 0.f;
+            if (n_parts == 1) {
+                const float z = none ? 0.f : p.c.v_mul / l;
+                uint16_t* out = p.out + (qi * p.Hq + g) * kHeadDim;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    if (nt > 0) tmem_ld32(lanes + col_o(x) + 32 * c, v);
+                    if (live) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const float v0 = v[8 * k + 2 * u] * z, v1 = v[8 * k + 2 * u + 1] * z;
+                                y[u] = poison ? 0x7fff7fffu : (none ? 0u : pack2<false>(v0, v1));
+                            }
+                            *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                }
+                if (live && p.lse)
+                    p.lse[qi * p.Hq + g] = none ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kWeightBase<E2M1>) * 0.6931471805599453f;
+            } else {
+                const int64_t at = (int64_t)blockIdx.x * p.part_rows;
+                float* o = p.part + (at + row) * kHeadDim;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    if (nt > 0) tmem_ld32(lanes + col_o(x) + 32 * c, v);
+                    if (!live) continue;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 y = poison ? make_float4(NAN, NAN, NAN, NAN)
+                                                : (none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+                        *reinterpret_cast<float4*>(o + 32 * c + k) = y;
+                    }
+                }
+                if (live) {
+                    p.part_ml[2 * (at + row)] = m == -INFINITY && !none ? 0.f : m;   // (NaN logits leave no reference, but show)
+                    p.part_ml[2 * (at + row) + 1] = l;
+                }
+            }
+        }
+    }
+    // ---- the parts of a block meet
+    tc_before();
+    __syncthreads();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (n_parts == 1) return;
+    if (tid == 0) {
+        __threadfence();   // the CTA's part, which the barrier orders before this fence
+        sm.last = atomicAdd(p.counters + unit, 1u) == (unsigned)(n_parts - 1) ? 1u : 0u;
+        if (sm.last) {
+            p.counters[unit] = 0;   // ready for the next call
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    if (!sm.last) return;
+    const int64_t at0 = (int64_t)(blockIdx.x - part) * p.part_rows;
+    for (int w = warp; w < rows; w += kThreadsA / 32) {
+        float mx = -INFINITY;
+        for (int k = lane; k < n_parts; k += 32) mx = fmaxf(mx, __ldcg(p.part_ml + 2 * (at0 + (int64_t)k * p.part_rows + w)));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        float z = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n_parts; ++k) {
+            const int64_t at = at0 + (int64_t)k * p.part_rows + w;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part + at * kHeadDim) + lane);
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+            if (ml.y == 0.f) continue;   // that part saw nothing
+            z = fmaf(f, ml.y, z);
+            acc.x = fmaf(f, o.x, acc.x);
+            acc.y = fmaf(f, o.y, acc.y);
+            acc.z = fmaf(f, o.z, acc.z);
+            acc.w = fmaf(f, o.w, acc.w);
+        }
+        const bool none = z == 0.f;
+        const float y = none ? 0.f : p.c.v_mul / z;
+        const int rr = blk * kBlock + w, j = rr / p.G, head = h * p.G + rr - j * p.G;
+        const int64_t to = ((int64_t)q0 + j) * p.Hq + head;
+        *reinterpret_cast<uint2*>(p.out + to * kHeadDim + 4 * lane) =
+            none ? make_uint2(0u, 0u) : make_uint2(pack2<false>(acc.x * y, acc.y * y), pack2<false>(acc.z * y, acc.w * y));
+        if (p.lse && lane == 0) p.lse[to] = none ? -INFINITY : (mx + log2f(z) - kWeightBase<E2M1>) * 0.6931471805599453f;
+    }
+}
+
+template <bool E2M1, bool SHAPED>
+cudaError_t launch(const PagedAttendParams& p, bool pdl, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(paged_attend_kernel<E2M1, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(E2M1));
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const dim3 grid = p.split ? dim3(p.split) : dim3(p.c.Hkv, p.blocks, p.c.B);
+    return launch_kernel(paged_attend_kernel<E2M1, SHAPED>, grid, dim3(kThreadsA), attend_smem(E2M1), s, pdl, 0u, p);
+}
+
+}  // namespace
+
+// How a call is cut.  Calls of few query rows a (sequence, KV head) -- up to 64: they are bound by the cache's bytes -- are
+// cut along the cache wherever the plan holds them: several parts to an SM in turn even out ragged lengths.  Calls of more
+// rows only where their blocks leave SMs without work.
+PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count)
+{
+    PagedAttendCut c;
+    const int64_t rows = max_new * G;
+    c.blocks = (int)((rows + kBlock - 1) / kBlock);
+    c.part_rows = (int)(rows < kBlock ? rows : kBlock);
+    const int64_t plan = (int64_t)B * c.blocks, units = plan * Hkv;
+    c.split = 0;
+    if (plan <= kMaxPlan && units <= 4096) {
+        if (rows <= 64)
+            c.split = (int)(units + 5 * sm_count);
+        else if (units < sm_count)
+            c.split = sm_count;
+    }
+    return c;
+}
+size_t paged_attend_workspace_bytes(const PagedAttendCut& c)
+{
+    return c.split ? kCounterBytes + (size_t)c.split * c.part_rows * (kHeadDim + 2) * sizeof(float) : kCounterBytes;
+}
+
+cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s)
+{
+    const bool shaped = p.cap > 0.f || p.slope != nullptr;
+    if (e2m1) return shaped ? launch<true, true>(p, pdl, s) : launch<true, false>(p, pdl, s);
+    return shaped ? launch<false, true>(p, pdl, s) : launch<false, false>(p, pdl, s);
+}
+
+}  // namespace fx
