@@ -569,7 +569,7 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
  *             or leave [0, n] set FX_DEVERR_OFFSETS and the sequence is skipped; of a sequence with more than max_new tokens
  *             the first max_new are done (FX_DEVERR_OFFSETS).  Tokens of no sequence keep their out and lse.
  *   first, last   int32 [n] on the device or NULL; any values: the interval is cut to [0, len[b])
- *   slope     fp32 [Hq] on the device or NULL (0)
+ *   slope     fp32 [Hq] on the device or NULL (0);   cap 0 (none) or from 2^-64 to 2^64;   G <= 64
  *   q         bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h;   out bf16 [n, Hq, 128], lse fp32 [n, Hq], contiguous
  *   max_new   host: tokens of one sequence, at most (G*max_new <= 2^30, n*Hq < 2^31)
  * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes.

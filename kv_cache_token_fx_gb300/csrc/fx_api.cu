@@ -1104,6 +1104,38 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
     return FX_OK;
 }
 
+// fx_paged_attend with up to kMaxRows query rows a (sequence, KV head); its own checks are done.
+fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags, void* stream)
+{
+    PagedAttnParams p;
+    fx_status st = paged_queries(cache, q->q, 0, q->q_stride_h, q->q_stride_n, q->Hq, q->max_new, 0, q->scale, flags, &p);
+    if (st != FX_OK) return st;
+    const int sms = sm_count_or_default();
+    if ((st = check_ws(ws, ws_bytes, paged_decode_workspace_bytes(p.R, sms))) != FX_OK) return st;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.qscale = q->scale * p.c.k_mul;
+    p.start = q->start;
+    p.first = q->first;
+    p.last = q->last;
+    p.slope = q->slope;
+    p.n = q->n;
+    p.window = q->window;
+    p.cap = q->cap;
+    p.icap = q->cap > 0.f ? 1.f / q->cap : 0.f;
+    p.out16 = q->out;
+    p.lse = q->lse;
+    p.counters = static_cast<unsigned*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
+    p.err = ds->err;
+    const bool pdl = (flags & FX_LAUNCH_PDL) != 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache->format == FX_PAGED_E2M1 ? launch_paged_attend_few_e2m1(p, sms, pdl, s)
+                                                         : launch_paged_attend_few_bf16(p, sms, pdl, s);
+    if (e != cudaSuccess) return cuda_fail(e, "paged attend launch");
+    return FX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1273,7 +1305,9 @@ fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int6
 size_t fx_paged_attend_workspace_bytes(int B, int Hkv, int Hq, int max_new)
 {
     if (B < 1 || Hkv < 1 || Hq < Hkv || max_new < 1 || (int64_t)(Hq / Hkv) * max_new > (1ll << 30)) return 0;
-    return paged_attend_workspace_bytes(paged_attend_cut(B, Hkv, Hq / Hkv, max_new, sm_count_or_default()));
+    const int sms = sm_count_or_default(), G = Hq / Hkv;
+    if ((int64_t)G * max_new <= kMaxRows) return paged_decode_workspace_bytes(G * max_new, sms);
+    return paged_attend_workspace_bytes(paged_attend_cut(B, Hkv, G, max_new, sms));
 }
 
 fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags,
@@ -1292,7 +1326,8 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     if (!q->start && (int64_t)cache->B * q->max_new != q->n)
         return fail(FX_ERR_INVALID_ARG, "queries: without start every sequence has max_new of them (n = B * max_new)");
     if (!isfinite(q->scale)) return fail(FX_ERR_INVALID_ARG, "scale must be finite");
-    if (!isfinite(q->cap) || q->cap < 0.f) return fail(FX_ERR_INVALID_ARG, "cap must be finite and >= 0");
+    if (q->cap != 0.f && !(q->cap >= 0x1p-64f && q->cap <= 0x1p64f))
+        return fail(FX_ERR_INVALID_ARG, "cap must be 0 or from 2^-64 to 2^64");
     if (q->window < 0) return fail(FX_ERR_INVALID_ARG, "window must be >= 0");
     if (!row_stride_ok(q->q_stride_n) || !row_stride_ok(q->q_stride_h))
         return fail(FX_ERR_INVALID_ARG, "queries: strides must be non-negative multiples of 8 elements");
@@ -1301,6 +1336,7 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     if (!q->out || !aligned16(q->out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
     if ((int64_t)G * q->max_new > (1ll << 30) || (int64_t)q->n * q->Hq > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "queries: too many rows");
+    if (G * q->max_new <= kMaxRows) return attend_few(cache, q, ws, ws_bytes, flags, stream);
     const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, sm_count_or_default());
     if (!cut.split && cut.blocks > 65535) return fail(FX_ERR_UNSUPPORTED, "queries: too many of one sequence");
     if ((st = check_ws(ws, ws_bytes, paged_attend_workspace_bytes(cut))) != FX_OK) return st;

@@ -303,6 +303,15 @@ struct PagedAttnParams {
     unsigned* counters;       // decode: arrival counters (zero between calls), then the split partials
     float* part;
     unsigned* err;
+    // fx_paged_attend, few query rows (Mq: tokens of a sequence, at most; q_i: the tokens' stride; qscale: the scale with
+    // 2^k_exp, natural)
+    const int32_t* start;
+    const int32_t* first;
+    const int32_t* last;
+    const float* slope;
+    int n, window;
+    float cap, icap;          // icap = 1 / cap
+    uint16_t* out16;          // [n, Hq, 128]
 };
 
 // An NVTX range over one library call, so that profiler timelines show each fx_* call by name (header-only
@@ -352,6 +361,9 @@ cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, int sm_co
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);
+// fx_paged_attend with up to kMaxRows query rows a (sequence, KV head): kernels of fx_paged_decode's kind.
+cudaError_t launch_paged_attend_few_bf16(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_few_e2m1(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s);
 PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count);
 size_t paged_attend_workspace_bytes(const PagedAttendCut& c);

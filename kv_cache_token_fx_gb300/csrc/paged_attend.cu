@@ -17,8 +17,9 @@
 // P is rounded once, to the operands' type (bf16: at most 2^-8 of a weight; f16: 2^-11): the output is bf16, whose rounding is as
 // large.  Logits, maxima, sums and O are fp32.
 //
-// Few query rows (a decode step) are cut along the cache: every block's tiles become parts of nearly equal length by the
-// lengths found on the device, and the last CTA of a block to arrive joins its parts in their order.
+// Calls of fewer blocks than SMs are cut along the cache: every block's tiles become parts of nearly equal length by the
+// lengths found on the device, and the last CTA of a block to arrive joins its parts in their order.  (Calls of up to 64
+// query rows a (sequence, KV head) go to the kernels of paged_attn.cuh, which are bound by the cache's bytes.)
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -59,7 +60,7 @@ template <bool E2M1>
 constexpr float kWeightBase = E2M1 ? 6.f : -32.f;
 constexpr float kFarRef = 4194304.f;   // 2^22: beyond it products and their rounded values lie too far apart for one fma
 
-constexpr int kMaxPlan = 512;                    // (sequence, block) pairs of a call that is cut along the cache
+constexpr int kMaxPlan = 256;                    // (sequence, block) pairs of a call that is cut along the cache
 
 struct AttendSmem {
     uint64_t full[5], empty[5], s_full[2], p_full[2], o_done[2];
@@ -424,15 +425,6 @@ __device__ __forceinline__ void fill_e2m1(const PagedAttendParams& p, AttendSmem
 }
 
 // ---- the softmax ---------------------------------------------------------------------------------------
-// tanh(y) = 1 - 2 / (exp(2y) + 1).
-__device__ __forceinline__ float tanh_exp(float y)
-{
-    float x = y * 2.885390081777927f;
-    x = x > 126.f ? 126.f : x;   // (a NaN stays)
-    const float e = ex2(x);
-    return fmaf(-2.f, __fdividef(1.f, e + 1.f), 1.f);
-}
-
 // The queries of sequence b: the first row of q and their number (0 for offsets that are not good).
 __device__ __forceinline__ void sequence_queries(const PagedAttendParams& p, int b, bool report, int& q0, int& nb, int& all)
 {
@@ -470,8 +462,7 @@ __device__ __forceinline__ void block_tiles(const PagedAttendParams& p, int len,
     t1 = hi > lo ? (hi + kKeys - 1) / kKeys : t0;
 }
 
-constexpr int kSearch = 192;   // blocks up to which the shares are tried one by one
-constexpr int kPartCost = 6;   // what a part costs a CTA besides its tiles, counted in tiles
+constexpr int kMinPart = 4;   // tiles of a part, at least
 
 // Shares the tiles of all blocks among the CTAs: parts of a block of n tiles are ceil(n / share).  Returns false when there
 // is nothing for this CTA; else its block (sm.plan_i) and its place among the parts of the block's heads.
@@ -501,30 +492,21 @@ __device__ __forceinline__ bool plan(const PagedAttendParams& p, AttendSmem& sm,
     total = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) total += sm.scan[w];
-    // lanes try shares: 1 to 3 times an even one, and a half to a quarter of it (several parts to a CTA in turn)
-    const float even = fmaxf((float)total * p.c.Hkv / (float)p.sm_count, 1.f);
-    float share = lane < 24 ? even * (1.f + lane / 12.f) : even / (1.f + 0.5f * (lane - 23));
-    if (lane == 23 || nq > kSearch) share = nq > kSearch ? even * 0.5f : 1e9f;   // (no cuts: always possible)
-    share = fmaxf(share, 4.f);
-    float inv = 1.f / share;
-    if (nq <= kSearch) {
-        int sum = 0;
-        float longest = 0.f;
-        for (int k = 0; k < nq; ++k) {
-            const int n = count[k];
-            const int parts = min((int)((float)n * inv) + 1, n);   // (0 for a block without rows)
-            sum += parts;
-            longest = fmaxf(longest, __fdividef((float)n, (float)max(parts, 1)));
-        }
-        const float all = (float)sum * p.c.Hkv;
-        float cost = longest + kPartCost;
-        if (all > (float)p.sm_count) cost = ((float)total * p.c.Hkv + kPartCost * all) / (float)p.sm_count + 0.5f * cost;
-        if (all > (float)gridDim.x) cost = 3e38f;
-        float best = cost;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, d));
-        inv = __shfl_sync(0xffffffffu, inv, __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1);
+    // lanes try shares of 1 to 3.6 times an even one and no cuts at all (always possible); the shortest longest part wins
+    const float even = fmaxf((float)total * p.c.Hkv / (float)gridDim.x, 1.f);
+    float inv = lane == 31 ? 0.f : 1.f / fmaxf(even * (1.f + lane / 12.f), (float)kMinPart);
+    int sum = 0;
+    float longest = 0.f;
+    for (int k = 0; k < nq; ++k) {
+        const int n = count[k], parts = min((int)((float)n * inv) + 1, n);   // (0 for a block without rows)
+        sum += parts;
+        longest = fmaxf(longest, __fdividef((float)n, (float)max(parts, 1)));
     }
+    if ((int64_t)sum * p.c.Hkv > (int64_t)gridDim.x) longest = 3e38f;
+    float best = longest;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, d));
+    inv = __shfl_sync(0xffffffffu, inv, __ffs(__ballot_sync(0xffffffffu, longest == best)) - 1);
     const int parts = mine > 0 ? min((int)((float)mine * inv) + 1, mine) : 0;
     int inc = parts;
 #pragma unroll
@@ -791,7 +773,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
 #pragma unroll
                     for (int k = 0; k < 128; ++k) {
                         float v = s[k] * qs;
-                        if (cap > 0.f) v = cap * tanh_exp(v * icap);
+                        if (cap > 0.f) v = soft_cap(v, cap, icap);
                         s[k] = fmaf(fabsf(d0 - (float)k), -slope2, v * 1.4426950408889634f);
                     }
                     f = 1.f;
@@ -975,23 +957,15 @@ cudaError_t launch(const PagedAttendParams& p, bool pdl, cudaStream_t s)
 
 }  // namespace
 
-// How a call is cut.  Calls of few query rows a (sequence, KV head) -- up to 64: they are bound by the cache's bytes -- are
-// cut along the cache wherever the plan holds them: several parts to an SM in turn even out ragged lengths.  Calls of more
-// rows only where their blocks leave SMs without work.
+// A call whose blocks leave SMs without work is cut along the cache: one part to a CTA, one CTA to an SM.
 PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count)
 {
     PagedAttendCut c;
     const int64_t rows = max_new * G;
     c.blocks = (int)((rows + kBlock - 1) / kBlock);
     c.part_rows = (int)(rows < kBlock ? rows : kBlock);
-    const int64_t plan = (int64_t)B * c.blocks, units = plan * Hkv;
-    c.split = 0;
-    if (plan <= kMaxPlan && units <= 4096) {
-        if (rows <= 64)
-            c.split = (int)(units + 5 * sm_count);
-        else if (units < sm_count)
-            c.split = sm_count;
-    }
+    const int64_t plan = (int64_t)B * c.blocks;
+    c.split = plan <= kMaxPlan && plan * Hkv < sm_count ? sm_count : 0;
     return c;
 }
 size_t paged_attend_workspace_bytes(const PagedAttendCut& c)
