@@ -497,6 +497,71 @@ typedef struct {
 
 FX_API fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows, unsigned flags, void* stream);
 
+/* fx_paged_append_axes -- fx_paged_append for positions of several axes: a picture's or a film's tokens have a time, a row
+ * and a column, and each pair of a head turns by one of them.
+ *
+ * rows->rope_pos is int32 [n_axes, n] (axis a of token i at rope_pos[a*n + i]) and pair j < rot/2 takes its angle's cosine
+ * and sine at t = rope_pos[axis[j]*n + i]; everything else as in fx_paged_append.  Every axis' position must be in [0, n_pos)
+ * (FX_DEVERR_INDEX: the token is skipped).
+ *   axis      HOST array of rot/2 bytes, read by the call: the axis of every pair;  1 <= n_axes <= 4, rot > 0
+ */
+FX_API fx_status fx_paged_append_axes(const fx_paged_desc* cache, const fx_paged_rows* rows, const uint8_t* axis, int n_axes,
+                                      unsigned flags, void* stream);
+
+/* fx_paged_compact -- decoupled KV retention for a paged cache ([FastKV] 2.B, as fx_kv_compact): the retained rows of every
+ * sequence move into other pages, so that the old ones can be freed; with k = 0, whole sequences (or their ends) do.
+ *
+ * Row i of sequence b, KV head h of dst receives row t of src, bit for bit:
+ *   t = idx[b, h, i] for i < k,  then, with tail_lo given, t = tail_lo[b] + i - k while t < len[b]
+ * and dst->len[b] = k + max(0, len[b] - tail_lo[b]) is WRITTEN (k without tail_lo).  idx: int32 [B, Hkv, k], tail_lo: int32
+ * [B] or NULL (no tail), both on the device.  An idx entry outside [0, len[b]) sets FX_DEVERR_INDEX and its row is not
+ * written; a tail_lo below 0 sets FX_DEVERR_LEN and counts as 0; more rows than dst has room for set FX_DEVERR_CAPACITY and
+ * are cut (dst->len too).
+ * src and dst have the same format, exponents, B and Hkv, and tables and lengths of their own; pool and page_rows may be the
+ * same or not.  The pages that dst's rows go to hold no row that src reads, and no page twice.  No workspace.
+ */
+FX_API fx_status fx_paged_compact(const fx_paged_desc* src, const fx_paged_desc* dst, const int32_t* idx, int k,
+                                  const int32_t* tail_lo, unsigned flags, void* stream);
+
+/* fx_paged_copy -- pages dst[i] receive all rows (every KV head, K and V, scales) of pages src[i], i < n: the copies that a
+ * forked sequence needs before it writes to a page that it shares (fx_page_pool_append names them).  [HPD] part 2.
+ *
+ * src, dst: int32 [n] on the device.  A pair with a -1 is left out; another number outside [0, n_pages) sets FX_DEVERR_PAGE
+ * and its pair is skipped.  A page that is written is named once in dst and not in src.  cache->table and len are not read
+ * (len may be NULL).  No workspace.
+ */
+FX_API fx_status fx_paged_copy(const fx_paged_desc* cache, const int32_t* src, const int32_t* dst, int n, unsigned flags,
+                               void* stream);
+
+/* Page pool -- host-side bookkeeping of a paged cache's pages: sequences that grow, fork without a copy, are cut back and
+ * released, and pages shared by reference count.  [HPD] part 2, as the branch pool, for caches that live in pages.
+ *
+ * The pool does no GPU work and owns no device memory.  Calls returning int give -1 on error, with nothing changed (message
+ * in fx_last_error); the pool is thread-safe.
+ *   create       n_pages pages of page_rows rows, at most max_seqs live sequences of at most max_pages pages; NULL on bad
+ *                sizes
+ *   open         a new empty sequence: its id (the lowest free one)
+ *   append       room for n more rows of a sequence.  Returns 1 when rows will go to a page that others share: it got a page
+ *                of its own, and the caller copies page *copy_src to page *copy_dst (fx_paged_copy) before it writes (both
+ *                -1 when 0 is returned).  -1 when pages run out
+ *   fork         a new sequence with the same rows, all pages shared: its id
+ *   truncate     a sequence keeps its first n rows: the number of pages that became free
+ *   release      a sequence is done: the number of pages that became free
+ *   length, free_pages
+ *   batch        the page tables ([n, max_pages], -1 past a sequence's pages) and lengths ([n]) of n sequences, host arrays
+ */
+typedef struct fx_page_pool fx_page_pool;
+FX_API fx_page_pool* fx_page_pool_create(int n_pages, int page_rows, int max_seqs, int max_pages);
+FX_API void fx_page_pool_destroy(fx_page_pool* pool);
+FX_API int fx_page_pool_open(fx_page_pool* pool);
+FX_API int fx_page_pool_append(fx_page_pool* pool, int seq, int n, int32_t* copy_src, int32_t* copy_dst);
+FX_API int fx_page_pool_fork(fx_page_pool* pool, int seq);
+FX_API int fx_page_pool_truncate(fx_page_pool* pool, int seq, int n);
+FX_API int fx_page_pool_release(fx_page_pool* pool, int seq);
+FX_API int fx_page_pool_length(fx_page_pool* pool, int seq);
+FX_API int fx_page_pool_free_pages(fx_page_pool* pool);
+FX_API int fx_page_pool_batch(fx_page_pool* pool, const int32_t* seqs, int n, int32_t* table, int32_t* len);
+
 /* fx_paged_gather -- rows of a paged cache as contiguous bf16 rows (exact for both formats), for the calls
  * that take a contiguous cache.
  *

@@ -28,7 +28,7 @@ __all__ = [
     "FX_DEVERR_LEN", "FX_DEVERR_INDEX", "FX_DEVERR_OFFSETS", "FX_DEVERR_CAPACITY", "FX_DEVERR_TIMEOUT",
     "FX_LAUNCH_PDL", "FX_LAUNCH_INPUTS_READY", "BranchPool",
     "PagedKV", "fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance",
-    "fx_paged_attend", "fx_paged_attend_workspace_bytes",
+    "fx_paged_attend", "fx_paged_attend_workspace_bytes", "fx_paged_compact", "fx_paged_copy", "fx_rope_axes", "PagePool",
     "fx_paged_decode_workspace_bytes", "FX_DEVERR_PAGE", "FX_PAGED_BF16", "FX_PAGED_E2M1",
 ]
 
@@ -166,7 +166,22 @@ def load_library():
         lib.fx_paged_attend_workspace_bytes.argtypes = [c_int] * 4
         lib.fx_paged_attend_workspace_bytes.restype = c_size
         lib.fx_paged_attend.argtypes = [paged, ctypes.c_char_p, c_vp, c_size, c_uint, c_vp]   # the bytes of a PagedQueries
-        for name in ("fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance", "fx_paged_attend"):
+        lib.fx_paged_append_axes.argtypes = [paged, ctypes.c_char_p, ctypes.c_char_p, c_int, c_uint, c_vp]
+        lib.fx_paged_compact.argtypes = [paged, paged, c_vp, c_int, c_vp, c_uint, c_vp]
+        lib.fx_paged_copy.argtypes = [paged, c_vp, c_vp, c_int, c_uint, c_vp]
+        lib.fx_page_pool_create.argtypes = [c_int] * 4
+        lib.fx_page_pool_create.restype = c_vp
+        lib.fx_page_pool_destroy.argtypes = [c_vp]
+        lib.fx_page_pool_destroy.restype = None
+        i32p = ctypes.POINTER(ctypes.c_int32)
+        for name, args in (("open", [c_vp]), ("append", [c_vp, c_int, c_int, i32p, i32p]), ("fork", [c_vp, c_int]),
+                           ("truncate", [c_vp, c_int, c_int]), ("release", [c_vp, c_int]), ("length", [c_vp, c_int]),
+                           ("free_pages", [c_vp]), ("batch", [c_vp, i32p, c_int, i32p, i32p])):
+            f = getattr(lib, "fx_page_pool_" + name)
+            f.argtypes = args
+            f.restype = c_int
+        for name in ("fx_paged_append", "fx_paged_gather", "fx_paged_decode", "fx_paged_importance", "fx_paged_attend",
+                     "fx_paged_append_axes", "fx_paged_compact", "fx_paged_copy"):
             getattr(lib, name).restype = c_int
         for name in ("fx_device_errors", "fx_workspace_init", "fx_focal_attn_scores", "fx_topk_select",
                      "fx_focal_mass", "fx_choose_focal_layers", "fx_csfr_schedule",
@@ -667,14 +682,34 @@ def _paged_alloc(cache, stream, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=cache.device)
 
 
-def fx_paged_append(cache, k_new, v_new, seq, pos, *, cos_sin=None, rope_pos=None, interleaved: bool = False, q=None,
-                    q_out=None, stream=None, flags: int = 0):
+def fx_rope_axes(sections, cyclic: bool = False) -> bytes:
+    """The axis of every pair, as fx_paged_append takes it: sections[a] pairs turn by axis a, one section after the other,
+    or (cyclic) in turns -- axis 0, 1, .., 0, 1, .. -- until an axis has had its share."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or sum(left) > 64:
+        raise FxError(FX_ERR_INVALID_ARG, "sections must be 1 to 4 numbers of pairs, 64 at most in all")
+    if not cyclic:
+        return b"".join(bytes([a]) * n for a, n in enumerate(left))
+    out = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                out.append(a)
+    return bytes(out)
+
+
+def fx_paged_append(cache, k_new, v_new, seq, pos, *, cos_sin=None, rope_pos=None, interleaved: bool = False, axes=None,
+                    q=None, q_out=None, stream=None, flags: int = 0):
     """Append the rows of n tokens to a paged cache, rotated by position on the way; returns the rotated queries.
 
     k_new, v_new [n, Hkv, 128] bf16 views with equal strides; seq, pos int32 [n]: the sequence (-1: padding, left
     out) and the row each token writes.  cos_sin fp32 [n_pos, rot] (rot/2 cosines, rot/2 sines a row) rotates the
     first rot dimensions of K and of q [n, Hq, 128] by rope_pos (int32 [n]; pos when None), in halves or, with
     interleaved, in neighbouring pairs.  q_out [n, Hq, 128] (allocated when None; may be q).
+
+    axes (bytes of rot/2 entries, from fx_rope_axes): pair j turns by the position of axis axes[j], and rope_pos is int32
+    [A, n], A = 1 to 4 axes.
     """
     lib, st = _paged_launch(cache, stream)
     n = seq.shape[0] if isinstance(seq, torch.Tensor) and seq.dim() == 1 else -1
@@ -698,17 +733,56 @@ def fx_paged_append(cache, k_new, v_new, seq, pos, *, cos_sin=None, rope_pos=Non
         raise FxError(FX_ERR_INVALID_ARG, "q_out needs q")
     if n == 0:
         return q_out
-    rope_at = 0 if rope_pos is None else _paged_tensor(cache, rope_pos, "rope_pos", torch.int32, (n,))
+    if axes is None:
+        rope_at = 0 if rope_pos is None else _paged_tensor(cache, rope_pos, "rope_pos", torch.int32, (n,))
+    else:
+        n_axes = rope_pos.shape[0] if isinstance(rope_pos, torch.Tensor) and rope_pos.dim() == 2 else -1
+        rope_at = _paged_tensor(cache, rope_pos, "rope_pos", torch.int32, (n_axes, n))
     cs_at = rot = n_pos = 0
     if cos_sin is not None:
         n_pos, rot = cos_sin.shape if isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2 else (-1, -1)
         cs_at = _paged_tensor(cache, cos_sin, "cos_sin", torch.float32, (n_pos, rot))
     rows = _ROWS.pack(k_at, v_at, ks[0], ks[1], q_at, o_at, qs[0], qs[1], os_[0], os_[1], seq_at, pos_at, rope_at, cs_at,
                       n, Hq, rot, n_pos, 1 if interleaved else 0)
-    rc = lib.fx_paged_append(cache._ref, rows, flags, st)
+    if axes is None:
+        rc = lib.fx_paged_append(cache._ref, rows, flags, st)
+    else:
+        if type(axes) is not bytes or len(axes) * 2 != rot:
+            raise FxError(FX_ERR_INVALID_ARG, "axes must be bytes (fx_rope_axes), one for each of cos_sin's rot/2 pairs")
+        rc = lib.fx_paged_append_axes(cache._ref, rows, axes, n_axes, flags, st)
     if rc:
         _check(rc)
     return q_out
+
+
+def fx_paged_compact(cache, dst, *, idx=None, tail_lo=None, stream=None, flags: int = 0):
+    """Move rows of a paged cache into the pages of another one, dst (a PagedKV of the same format, exponents, B and Hkv,
+    with a table and lengths of its own; its pages hold no row that is read): rows idx [B, Hkv, k] (int32) of each
+    (sequence, KV head), then the tail from row tail_lo[b] (int32 [B]) on.  Writes dst.length; returns dst."""
+    lib, st = _paged_launch(cache, stream)
+    if not isinstance(dst, PagedKV) or dst._index != cache._index:
+        raise FxError(FX_ERR_INVALID_ARG, f"dst must be a PagedKV on {cache.device}")
+    kk, idx_at = 0, None
+    if idx is not None:
+        kk = idx.shape[-1] if isinstance(idx, torch.Tensor) and idx.dim() == 3 else -1
+        idx_at = _paged_tensor(cache, idx, "idx", torch.int32, (cache.B, cache.Hkv, kk)) or None
+    lo_at = None if tail_lo is None else _paged_tensor(cache, tail_lo, "tail_lo", torch.int32, (cache.B,))
+    rc = lib.fx_paged_compact(cache._ref, dst._ref, idx_at, kk, lo_at, flags, st)
+    if rc:
+        _check(rc)
+    return dst
+
+
+def fx_paged_copy(cache, src, dst, *, stream=None, flags: int = 0):
+    """Copy pages src[i] (int32 [n], on the device) of a paged cache's pool to pages dst[i], every KV head's rows; a pair
+    with a -1 is left out.  A page that is written is named once in dst and not in src."""
+    lib, st = _paged_launch(cache, stream)
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
+    src_at = _paged_tensor(cache, src, "src", torch.int32, (n,))
+    dst_at = _paged_tensor(cache, dst, "dst", torch.int32, (n,))
+    rc = lib.fx_paged_copy(cache._ref, src_at, dst_at, n, flags, st)
+    if rc:
+        _check(rc)
 
 
 def fx_paged_gather(cache, n: int, *, idx=None, lo=None, k_out=None, v_out=None, stream=None, flags: int = 0):
@@ -932,6 +1006,65 @@ class BranchPool:
         h, self._h = getattr(self, "_h", None), None
         if h:
             self._lib.fx_branch_pool_destroy(h)
+
+
+class PagePool:
+    """Host bookkeeping of a paged cache's pages (include/fx.h: page pool): sequences that grow, fork without a copy, are
+    cut back and released.  Thin wrapper: every method is one C call; errors raise FxError and change nothing."""
+
+    def __init__(self, n_pages: int, page_rows: int, max_seqs: int, max_pages: int):
+        self._h = None
+        lib = load_library()
+        self._lib = lib
+        self._h = lib.fx_page_pool_create(int(n_pages), int(page_rows), int(max_seqs), int(max_pages))
+        if not self._h:
+            _check(FX_ERR_INVALID_ARG)
+        self.max_pages = int(max_pages)
+
+    def _int(self, r):
+        if r < 0:
+            raise FxError(FX_ERR_INVALID_ARG, self._lib.fx_last_error().decode(errors="replace"))
+        return int(r)
+
+    def open(self) -> int:
+        return self._int(self._lib.fx_page_pool_open(self._h))
+
+    def append(self, seq: int, n: int):
+        """Room for n more rows; returns None, or the pages (src, dst) that fx_paged_copy has to copy before the rows
+        are written."""
+        src, dst = ctypes.c_int32(), ctypes.c_int32()
+        r = self._int(self._lib.fx_page_pool_append(self._h, int(seq), int(n), ctypes.byref(src), ctypes.byref(dst)))
+        return (src.value, dst.value) if r else None
+
+    def fork(self, seq: int) -> int:
+        return self._int(self._lib.fx_page_pool_fork(self._h, int(seq)))
+
+    def truncate(self, seq: int, n: int) -> int:
+        return self._int(self._lib.fx_page_pool_truncate(self._h, int(seq), int(n)))
+
+    def release(self, seq: int) -> int:
+        return self._int(self._lib.fx_page_pool_release(self._h, int(seq)))
+
+    def length(self, seq: int) -> int:
+        return self._int(self._lib.fx_page_pool_length(self._h, int(seq)))
+
+    def free_pages(self) -> int:
+        return self._int(self._lib.fx_page_pool_free_pages(self._h))
+
+    def batch(self, seqs):
+        """(table [n, max_pages], length [n]) of those sequences, as int32 CPU tensors for a PagedKV."""
+        ids = [int(x) for x in seqs]
+        n = len(ids)
+        table, length = torch.empty(n, self.max_pages, dtype=torch.int32), torch.empty(n, dtype=torch.int32)
+        i32p = ctypes.POINTER(ctypes.c_int32)
+        self._int(self._lib.fx_page_pool_batch(self._h, (ctypes.c_int32 * n)(*ids), n, ctypes.cast(table.data_ptr(), i32p),
+                                               ctypes.cast(length.data_ptr(), i32p)))
+        return table, length
+
+    def __del__(self):
+        h, self._h = getattr(self, "_h", None), None
+        if h:
+            self._lib.fx_page_pool_destroy(h)
 
 
 def fx_device_errors(stream=None) -> int:

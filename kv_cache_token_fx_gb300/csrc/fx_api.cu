@@ -1138,11 +1138,24 @@ fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows, unsigned flags, void* stream)
+// Whether no two rows of a pool share memory (only such a pool is written).
+bool pool_apart(const fx_paged_desc* cache)
 {
-    fx::NvtxRange nvtx_range("fx_paged_append");
+    const bool e2m1 = cache->format == FX_PAGED_E2M1;
+    const int row = e2m1 ? kHeadDim / 2 : kHeadDim, scales = kHeadDim / 16;
+    return rows_apart(cache->stride_page, row, cache->n_pages) && rows_apart(cache->stride_h, row, cache->Hkv) &&
+           rows_apart(cache->stride_t, row, cache->page_rows) &&
+           (!e2m1 || (rows_apart(cache->scale_stride_page, scales, cache->n_pages) &&
+                      rows_apart(cache->scale_stride_h, scales, cache->Hkv) &&
+                      rows_apart(cache->scale_stride_t, scales, cache->page_rows)));
+}
+
+// fx_paged_append, and with axes (n_axes > 0) fx_paged_append_axes.
+fx_status append_rows(const fx_paged_desc* cache, const fx_paged_rows* rows, const uint8_t* axis, int n_axes, unsigned flags,
+                      void* stream)
+{
     PagedAppendParams p;
     memset(&p, 0, sizeof p);
     fx_status st = paged_view(cache, false, &p.c);
@@ -1174,13 +1187,16 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
     if (rows->q && (!rows_apart(rows->qo_stride_n, kHeadDim, rows->n) || !rows_apart(rows->qo_stride_h, kHeadDim, rows->Hq)))
         return fail(FX_ERR_INVALID_ARG, "rows: q_out's rows share memory");
     const bool e2m1 = cache->format == FX_PAGED_E2M1;
-    const int row = e2m1 ? kHeadDim / 2 : kHeadDim, scales = kHeadDim / 16;
-    if (!rows_apart(cache->stride_page, row, cache->n_pages) || !rows_apart(cache->stride_h, row, cache->Hkv) ||
-        !rows_apart(cache->stride_t, row, cache->page_rows) ||
-        (e2m1 && (!rows_apart(cache->scale_stride_page, scales, cache->n_pages) ||
-                  !rows_apart(cache->scale_stride_h, scales, cache->Hkv) ||
-                  !rows_apart(cache->scale_stride_t, scales, cache->page_rows))))
-        return fail(FX_ERR_INVALID_ARG, "cache: the pool's rows share memory, so none can be written");
+    if (!pool_apart(cache)) return fail(FX_ERR_INVALID_ARG, "cache: the pool's rows share memory, so none can be written");
+    if (n_axes > 0) {
+        if (rows->rot == 0 || !rows->rope_pos || !axis)
+            return fail(FX_ERR_INVALID_ARG, "axes need rot > 0, rope_pos [n_axes, n] and the axis of every pair");
+        for (int j = 0; j < rows->rot / 2; ++j) {
+            if (axis[j] >= n_axes) return fail(FX_ERR_INVALID_ARG, "axes: pair %d has axis %d of %d", j, axis[j], n_axes);
+            p.axis[j] = axis[j];
+        }
+        p.n_axes = n_axes;
+    }
     const int Hq = rows->q ? rows->Hq : 0;
     if (Hq > 65535 || (int64_t)rows->n * (2 * (int64_t)cache->Hkv + Hq) > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "too many rows");
@@ -1210,6 +1226,79 @@ fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows,
     cudaError_t e = launch_paged_append(p, e2m1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
                                         static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+    return FX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fx_status fx_paged_append(const fx_paged_desc* cache, const fx_paged_rows* rows, unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_append");
+    return append_rows(cache, rows, nullptr, 0, flags, stream);
+}
+
+fx_status fx_paged_append_axes(const fx_paged_desc* cache, const fx_paged_rows* rows, const uint8_t* axis, int n_axes,
+                               unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_append_axes");
+    if (n_axes < 1 || n_axes > kMaxAxes) return fail(FX_ERR_UNSUPPORTED, "%d axes (1 to %d)", n_axes, kMaxAxes);
+    return append_rows(cache, rows, axis, n_axes, flags, stream);
+}
+
+fx_status fx_paged_compact(const fx_paged_desc* src, const fx_paged_desc* dst, const int32_t* idx, int k, const int32_t* tail_lo,
+                           unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_compact");
+    PagedCompactParams p;
+    memset(&p, 0, sizeof p);
+    fx_status st = paged_view(src, true, &p.src);
+    if (st != FX_OK) return st;
+    if ((st = paged_view(dst, true, &p.dst)) != FX_OK) return st;
+    if ((st = check_flags(flags)) != FX_OK) return st;
+    if (src->format != dst->format || src->B != dst->B || src->Hkv != dst->Hkv || src->k_exp != dst->k_exp || src->v_exp != dst->v_exp)
+        return fail(FX_ERR_INVALID_ARG, "src and dst must have one format (and exponents), B and Hkv");
+    if (src->len == dst->len || src->table == dst->table)
+        return fail(FX_ERR_INVALID_ARG, "dst needs a page table and lengths of its own");
+    if (!pool_apart(dst)) return fail(FX_ERR_INVALID_ARG, "dst: the pool's rows share memory, so none can be written");
+    if (k < 0 || (k > 0 && !idx)) return fail(FX_ERR_INVALID_ARG, "need k >= 0 and idx when k > 0");
+    if (k > (1 << 30)) return fail(FX_ERR_UNSUPPORTED, "k is at most 2^30");
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.idx = k > 0 ? idx : nullptr;
+    p.tail_lo = tail_lo;
+    p.k = k;
+    const int64_t most = k + (tail_lo ? (int64_t)p.src.cap : 0);
+    p.rows = (int)(most < p.dst.cap ? (most > 1 ? most : 1) : p.dst.cap);   // (one at least: the lengths are written)
+    p.err = ds->err;
+    cudaError_t e = launch_paged_compact(p, src->format == FX_PAGED_E2M1, ds->sm_count, (flags & FX_LAUNCH_PDL) != 0,
+                                         static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged compact launch");
+    return FX_OK;
+}
+
+fx_status fx_paged_copy(const fx_paged_desc* cache, const int32_t* src, const int32_t* dst, int n, unsigned flags, void* stream)
+{
+    fx::NvtxRange nvtx_range("fx_paged_copy");
+    PagedCopyParams p;
+    memset(&p, 0, sizeof p);
+    fx_status st = paged_view(cache, false, &p.c);
+    if (st != FX_OK) return st;
+    if ((st = check_flags(flags)) != FX_OK) return st;
+    if (n < 0) return fail(FX_ERR_INVALID_ARG, "n must be >= 0");
+    if (n > 0 && (!src || !dst)) return fail(FX_ERR_INVALID_ARG, "src and dst must be non-NULL");
+    if (!pool_apart(cache)) return fail(FX_ERR_INVALID_ARG, "cache: the pool's rows share memory, so none can be written");
+    if (n == 0) return FX_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != FX_OK) return st;
+    p.from = src;
+    p.to = dst;
+    p.n = n;
+    p.err = ds->err;
+    cudaError_t e = launch_paged_copy(p, cache->format == FX_PAGED_E2M1, (flags & FX_LAUNCH_PDL) != 0,
+                                      static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged copy launch");
     return FX_OK;
 }
 

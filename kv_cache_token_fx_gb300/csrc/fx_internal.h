@@ -247,6 +247,25 @@ struct PagedAppendParams {
     const int32_t* rope_pos;
     const float* cos_sin;
     int n, Hq, rot, n_pos, interleaved;   // Hq = 0: no queries
+    int n_axes;                           // 0: one position for all pairs; else rope_pos is [n_axes, n]
+    uint8_t axis[kHeadDim / 2];           // of every pair
+    unsigned* err;
+};
+constexpr int kMaxAxes = 4;
+
+struct PagedCompactParams {
+    PagedCache src, dst;      // dst.len is written
+    const int32_t* idx;
+    const int32_t* tail_lo;   // nullptr: no tail
+    int k, rows;              // rows: of the destination, at most
+    unsigned* err;
+};
+
+struct PagedCopyParams {
+    PagedCache c;
+    const int32_t* from;
+    const int32_t* to;
+    int n;
     unsigned* err;
 };
 
@@ -358,6 +377,8 @@ constexpr int kPieceStart = 32;   // tiles that the start of a (sequence, KV hea
 // Paged cache (paged_rows.cu, paged_attn.cu); `e2m1`: the 4-bit format.
 cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_compact(const PagedCompactParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_copy(const PagedCopyParams& p, bool e2m1, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);

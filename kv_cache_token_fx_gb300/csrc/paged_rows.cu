@@ -1,5 +1,6 @@
-// Rows into and out of a paged cache for sm_103a: the append with the position rotation (and, for the 4-bit
-// format, the quantisation) on the way, and the gather back to contiguous bf16 rows.
+// Rows into, out of and about a paged cache for sm_103a: the append with the position rotation (and, for the 4-bit
+// format, the quantisation) on the way, the gather back to contiguous bf16 rows, compaction into other pages and copies of
+// pages.
 //
 // Both move rows of 128 values and compute a few operations a value.  Bytes bound the long gather (4 x 32768 4-bit rows
 // to bf16, 447 MB: 70 us, 0.94 of the copy bandwidth); the quantisation's instructions and bytes together the long
@@ -68,13 +69,34 @@ __device__ __forceinline__ uint32_t quantize_chunk(uint4 x, float inv, uint32_t&
     return codes;
 }
 
+// Cosines and sines of pairs j .. j + 3 (j a multiple of 4), each at the position of its axis.
+__device__ __forceinline__ void pairs_of_axes(const PagedAppendParams& p, const int (&ax)[kMaxAxes], int j, float4& c, float4& s)
+{
+    const int half = p.rot >> 1;
+    auto at = [&](int a) { return a == 0 ? ax[0] : (a == 1 ? ax[1] : (a == 2 ? ax[2] : ax[3])); };
+    const uchar4 w = *reinterpret_cast<const uchar4*>(p.axis + j);
+    if (w.x == w.y && w.x == w.z && w.x == w.w) {
+        const float* cs = p.cos_sin + (int64_t)at(w.x) * p.rot + j;
+        c = __ldg(reinterpret_cast<const float4*>(cs));
+        s = __ldg(reinterpret_cast<const float4*>(cs + half));
+    } else {
+        const float* cs = p.cos_sin + j;
+        const int64_t a0 = (int64_t)at(w.x) * p.rot, a1 = (int64_t)at(w.y) * p.rot + 1, a2 = (int64_t)at(w.z) * p.rot + 2,
+                      a3 = (int64_t)at(w.w) * p.rot + 3;
+        c = make_float4(__ldg(cs + a0), __ldg(cs + a1), __ldg(cs + a2), __ldg(cs + a3));
+        s = make_float4(__ldg(cs + half + a0), __ldg(cs + half + a1), __ldg(cs + half + a2), __ldg(cs + half + a3));
+    }
+}
+
 // 8 lanes take R rows of one token -- K heads, V heads or query heads -- and of each row two chunks of 8 values:
 // chunks c0 and c1, which are the two sides of 8 rotated pairs in the half-split form.  The rows' loads need
 // neither the token's place nor its position and go out first, and the rows share its cosines and sines.
 // 8 CTAs of 128 threads an SM (64 registers), and queries and new rows that pass by L2's older contents when there are
 // many: a prompt of 24 K tokens, 4 bits, with its read-back 91 us, against 95 without the latter, 100 without either and
 // 105 with 10 CTAs.
-template <bool E2M1, int R, bool INTERLEAVED>
+//
+// AXES: a pair's cosine and sine are of its own axis' position.  Four neighbouring pairs of one axis are loaded as one.
+template <bool E2M1, int R, bool INTERLEAVED, bool AXES>
 __global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const PagedAppendParams p)
 {
     griddep_wait();
@@ -106,16 +128,25 @@ __global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const Pag
         }
     }
     int seq = -1, pos = 0, at = 0, page = -1;
+    int ax[kMaxAxes] = {};
     if (live) {
         seq = __ldg(p.seq + i);
         pos = __ldg(p.pos + i);
         at = p.rope_pos ? __ldg(p.rope_pos + i) : pos;
+        bool at_bad = p.rot > 0 && (at < 0 || at >= p.n_pos);
+        if (AXES) {
+#pragma unroll
+            for (int a = 0; a < kMaxAxes; ++a) {
+                ax[a] = a < p.n_axes ? __ldg(p.rope_pos + (int64_t)a * p.n + i) : 0;
+                at_bad |= ax[a] < 0 || ax[a] >= p.n_pos;
+            }
+        }
         unsigned bad = 0;
         if (seq < 0 || seq >= p.c.B)
             bad = seq == -1 ? 0u : FX_DEVERR_INDEX;
         else if (pos < 0 || pos >= p.c.cap)
             bad = FX_DEVERR_LEN;
-        else if (p.rot > 0 && (at < 0 || at >= p.n_pos))
+        else if (at_bad)
             bad = FX_DEVERR_INDEX;
         live = seq >= 0 && bad == 0;
         if (bad && in == 0 && l == 0) atomicOr(p.err, bad);
@@ -128,8 +159,13 @@ __global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const Pag
             if (l < hc) {   // pairs (8 l + j, 8 l + j + half)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 a = __ldg(reinterpret_cast<const float4*>(cs + 8 * l) + j);
-                    const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + 8 * l) + j);
+                    float4 a, b;
+                    if (AXES) {
+                        pairs_of_axes(p, ax, 8 * l + 4 * j, a, b);
+                    } else {
+                        a = __ldg(reinterpret_cast<const float4*>(cs + 8 * l) + j);
+                        b = __ldg(reinterpret_cast<const float4*>(cs + half + 8 * l) + j);
+                    }
                     c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
                     s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
                 }
@@ -153,8 +189,13 @@ __global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const Pag
             for (int k = 0; k < 2; ++k) {
                 const int chunk = k ? c1 : c0;
                 if (chunk >= 2 * hc) continue;
-                const float4 a = __ldg(reinterpret_cast<const float4*>(cs + 4 * chunk));
-                const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * chunk));
+                float4 a, b;
+                if (AXES) {
+                    pairs_of_axes(p, ax, 4 * chunk, a, b);
+                } else {
+                    a = __ldg(reinterpret_cast<const float4*>(cs + 4 * chunk));
+                    b = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * chunk));
+                }
                 c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
                 s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
 #pragma unroll
@@ -291,7 +332,128 @@ __global__ void __launch_bounds__(kThreadsRows) paged_gather_kernel(const PagedG
     }
 }
 
-template <bool E2M1, bool INTERLEAVED>
+// Rows of K and V as they are stored, 16 bytes (and a 4-bit row's 8 bytes of scales) at a time.
+//
+// Compaction: kLanes lanes take R rows, a CTA's rows apart, of one (sequence, KV head): the loads of all go out before the
+// first store.
+template <bool E2M1, int R>
+__global__ void __launch_bounds__(kThreadsRows) paged_compact_kernel(const PagedCompactParams p)
+{
+    griddep_wait();
+    griddep_launch();
+    constexpr int kLanes = E2M1 ? 4 : 16, kRows = kThreadsRows / kLanes;
+    const int c = threadIdx.x % kLanes, h = blockIdx.y, b = blockIdx.z;
+    const int64_t first = (int64_t)blockIdx.x * (kRows * R);
+    int len = p.src.len[b], lo = p.tail_lo ? p.tail_lo[b] : 0;
+    const bool report = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
+    if (report && (len < 0 || len > p.src.cap || lo < 0)) atomicOr(p.err, FX_DEVERR_LEN);
+    len = min(max(len, 0), p.src.cap);
+    lo = max(lo, 0);
+    const int64_t total = (int64_t)p.k + (p.tail_lo ? max(len - lo, 0) : 0);
+    const int rows = (int)(total < p.dst.cap ? total : p.dst.cap);
+    if (report) {
+        if (total > rows) atomicOr(p.err, FX_DEVERR_CAPACITY);
+        const_cast<int32_t*>(p.dst.len)[b] = rows;
+    }
+    if (first >= rows) return;
+    const int32_t* idx = p.idx + ((int64_t)b * p.src.Hkv + h) * p.k;
+    int t[R], from[R], to[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t i = first + r * kRows + threadIdx.x / kLanes;
+        t[r] = -1;
+        if (i < rows) {
+            t[r] = i < p.k ? idx[i] : lo + (int)(i - p.k);
+            if (t[r] < 0 || t[r] >= len) {
+                if (c == 0) atomicOr(p.err, FX_DEVERR_INDEX);
+                t[r] = -1;
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = (int)(first + r * kRows) + threadIdx.x / kLanes;
+        from[r] = t[r] >= 0 ? paged_page(p.src, b, t[r], p.err) : -1;
+        to[r] = t[r] >= 0 ? paged_page(p.dst, b, i, p.err) : -1;
+    }
+    uint4 x[R][2];
+    uint2 z[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (from[r] < 0 || to[r] < 0) continue;
+        const int64_t row = t[r] & p.src.page_mask;
+        const int64_t at = (int64_t)from[r] * p.src.sp + h * p.src.sh + row * p.src.st + 16 * c;
+        x[r][0] = __ldcs(reinterpret_cast<const uint4*>(p.src.k + at));
+        x[r][1] = __ldcs(reinterpret_cast<const uint4*>(p.src.v + at));
+        if (E2M1 && c < 2)
+            z[r] = __ldcs(reinterpret_cast<const uint2*>((c ? p.src.vs : p.src.ks) + (int64_t)from[r] * p.src.ssp + h * p.src.ssh +
+                                                            row * p.src.sst));
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (from[r] < 0 || to[r] < 0) continue;
+        const int64_t row = ((int)(first + r * kRows) + threadIdx.x / kLanes) & p.dst.page_mask;
+        const int64_t at = (int64_t)to[r] * p.dst.sp + h * p.dst.sh + row * p.dst.st + 16 * c;
+        __stcs(reinterpret_cast<uint4*>(p.dst.k + at), x[r][0]);
+        __stcs(reinterpret_cast<uint4*>(p.dst.v + at), x[r][1]);
+        if (E2M1 && c < 2)
+            __stcs(reinterpret_cast<uint2*>((c ? p.dst.vs : p.dst.ks) + (int64_t)to[r] * p.dst.ssp + h * p.dst.ssh + row * p.dst.sst),
+                   z[r]);
+    }
+}
+
+// Copies of pages: a CTA takes the rows of one (page, KV head), R pieces of 16 bytes of K and of V a thread at a time.
+template <bool E2M1, int R>
+__global__ void __launch_bounds__(kThreadsRows) paged_copy_kernel(const PagedCopyParams p)
+{
+    griddep_wait();
+    griddep_launch();
+    constexpr int kLanes = E2M1 ? 4 : 16, kRows = kThreadsRows / kLanes;
+    const int h = blockIdx.y;
+    const int from = p.from[blockIdx.x], to = p.to[blockIdx.x];
+    if (from == -1 || to == -1) return;
+    if ((unsigned)from >= (unsigned)p.c.n_pages || (unsigned)to >= (unsigned)p.c.n_pages) {
+        if (h == 0 && threadIdx.x == 0) atomicOr(p.err, FX_DEVERR_PAGE);
+        return;
+    }
+    const int64_t in = h * p.c.sh + 16 * (threadIdx.x % kLanes);
+    const char* const src = p.c.k + (int64_t)from * p.c.sp + in;
+    char* const dst = p.c.k + (int64_t)to * p.c.sp + in;
+    const int64_t dv = p.c.v - p.c.k;
+    const int page_rows = p.c.page_mask + 1;
+    for (int row0 = threadIdx.x / kLanes; row0 < page_rows; row0 += R * kRows) {
+        uint4 x[R][2];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = (int64_t)(row0 + r * kRows) * p.c.st;
+            if (row0 + r * kRows < page_rows) {
+                x[r][0] = __ldcs(reinterpret_cast<const uint4*>(src + at));
+                x[r][1] = __ldcs(reinterpret_cast<const uint4*>(src + dv + at));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = (int64_t)(row0 + r * kRows) * p.c.st;
+            if (row0 + r * kRows < page_rows) {
+                __stcs(reinterpret_cast<uint4*>(dst + at), x[r][0]);
+                __stcs(reinterpret_cast<uint4*>(dst + dv + at), x[r][1]);
+            }
+        }
+    }
+    if (E2M1) {
+        const int64_t ds = p.c.vs - p.c.ks;
+        for (int row = threadIdx.x; row < page_rows; row += kThreadsRows) {
+            const int64_t at = h * p.c.ssh + (int64_t)row * p.c.sst;
+            const char* s = p.c.ks + (int64_t)from * p.c.ssp + at;
+            char* d = p.c.ks + (int64_t)to * p.c.ssp + at;
+            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(s)), b = __ldcs(reinterpret_cast<const uint2*>(s + ds));
+            __stcs(reinterpret_cast<uint2*>(d), a);
+            __stcs(reinterpret_cast<uint2*>(d + ds), b);
+        }
+    }
+}
+
+template <bool E2M1, bool INTERLEAVED, bool AXES>
 cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     // A decode step's few rows: one row each, for the shortest way through (a step of 64 sequences with its read-back
@@ -301,8 +463,8 @@ cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStrea
     const int R = many ? 4 : 1;
     const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
     const dim3 grid((unsigned)((groups + kThreadsRows / 8 - 1) / (kThreadsRows / 8)));
-    return many ? launch_kernel(paged_append_kernel<E2M1, 4, INTERLEAVED>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
-                : launch_kernel(paged_append_kernel<E2M1, 1, INTERLEAVED>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
+    return many ? launch_kernel(paged_append_kernel<E2M1, 4, INTERLEAVED, AXES>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
+                : launch_kernel(paged_append_kernel<E2M1, 1, INTERLEAVED, AXES>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
 }
 
 template <bool E2M1>
@@ -321,8 +483,27 @@ cudaError_t gather(const PagedGatherParams& p, int sm_count, bool pdl, cudaStrea
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    if (p.interleaved) return e2m1 ? append<true, true>(p, sm_count, pdl, s) : append<false, true>(p, sm_count, pdl, s);
-    return e2m1 ? append<true, false>(p, sm_count, pdl, s) : append<false, false>(p, sm_count, pdl, s);
+    if (p.n_axes) {
+        if (p.interleaved) return e2m1 ? append<true, true, true>(p, sm_count, pdl, s) : append<false, true, true>(p, sm_count, pdl, s);
+        return e2m1 ? append<true, false, true>(p, sm_count, pdl, s) : append<false, false, true>(p, sm_count, pdl, s);
+    }
+    if (p.interleaved) return e2m1 ? append<true, true, false>(p, sm_count, pdl, s) : append<false, true, false>(p, sm_count, pdl, s);
+    return e2m1 ? append<true, false, false>(p, sm_count, pdl, s) : append<false, false, false>(p, sm_count, pdl, s);
+}
+
+cudaError_t launch_paged_compact(const PagedCompactParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
+{
+    const int rows = kThreadsRows / (e2m1 ? 4 : 16) * 4;
+    const dim3 grid((unsigned)((p.rows + (int64_t)rows - 1) / rows), p.src.Hkv, p.src.B);
+    return e2m1 ? launch_kernel(paged_compact_kernel<true, 4>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
+                : launch_kernel(paged_compact_kernel<false, 4>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
+}
+
+cudaError_t launch_paged_copy(const PagedCopyParams& p, bool e2m1, bool pdl, cudaStream_t s)
+{
+    const dim3 grid(p.n, p.c.Hkv);
+    return e2m1 ? launch_kernel(paged_copy_kernel<true, 2>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
+                : launch_kernel(paged_copy_kernel<false, 4>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)

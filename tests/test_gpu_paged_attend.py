@@ -192,3 +192,199 @@ def test_attend_scales(fx, fmt):
         for cap in (0.0, 4.0):
             got = fx.fx_paged_attend(dev, t, st, max_new=5, scale=scale, cap=cap, want_lse=True)
             check(c, got, attend_ref(c, q, start, scale, cap=cap), slice(0, 5))
+
+
+# ---------------------------------------------------------------------------------------- edges
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("lens,news", [([300, 90], [1, 1]), ([300, 90], [6, 3]), ([300, 200], [300, 130])])
+def test_attend_bad_pages(fx, fmt, lens, news):
+    """Rows of a bad page are left out; the bit is set."""
+    c, q, start = case(fmt, lens, news, 2, 2, 16, seed=5)
+    dev = c.device(fx)
+    dev.table[0, 3], dev.table[1, 0], dev.table[0, 18] = 1 << 29, -2, c.n_pages
+    gone = {0: (3, 18), 1: (0,)}
+    got = fx.fx_paged_attend(dev, cu(q, torch.bfloat16), cu(start, torch.int32), max_new=max(news), want_lse=True)
+    assert fx.fx_device_errors() == fx.FX_DEVERR_PAGE
+    ref = attend_ref(c, q, start, D ** -0.5, skip=lambda b, t: np.isin(t // 16, gone[b]))
+    check(c, got, ref, slice(0, start[-1]))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("G,news", [(2, [40]), (8, [40]), (1, [3]), (4, [140])])
+def test_attend_values_that_are_not_finite(fx, fmt, G, news):
+    """A row whose V (or K) holds an infinity or NaN reaches the queries that see it and no others."""
+    n = news[0]
+    c, q, start = case(fmt, [200], news, 1, G, 16, seed=9, pad=0)
+    dev = c.device(fx)
+    at = np.array([200 - n // 2, 37])        # seen by the late queries, and by those whose first row lies before it
+    first = np.zeros(n, np.int64)
+    first[n // 3:] = 40
+    for what in (0, 1):
+        d = c.device(fx)
+        for t in at:
+            pg, row = c.spot(0, t)
+            if fmt == "bf16":
+                (d.k, d.v)[what][pg, 0, row, 5] = float("nan") if what == 0 or t % 2 else float("inf")
+            else:
+                (d.k_scale, d.v_scale)[what][pg, 0, row, 3] = 0x7f
+        got = fx.fx_paged_attend(d, cu(q, torch.bfloat16), cu(start, torch.int32), max_new=n, first=cu(first, torch.int32),
+                                 want_lse=True)
+        ref = attend_ref(c, q, start, D ** -0.5, first=first)
+        pos = 200 - n + np.arange(n)
+        sees = ((at[None] <= pos[:, None]) & (at[None] >= first[:, None])).any(1)
+        assert sees.any() and not sees.all()
+        check(c, got, ref, np.flatnonzero(~sees))
+        o = got[0].float().cpu().numpy()[sees]
+        assert not np.isfinite(o).all(-1).any()            # it shows in every head that sees it
+        assert np.isfinite(got[1].cpu().numpy()[sees]).all() or what == 0
+    check(c, fx.fx_paged_attend(dev, cu(q, torch.bfloat16), cu(start, torch.int32), max_new=n, want_lse=True),
+          attend_ref(c, q, start, D ** -0.5))
+
+
+def test_attend_queries_that_are_not_finite(fx):
+    """Such a query's own output is NaN, its neighbours' are not."""
+    for fmt in FMT:
+        for n in (5, 100):
+            c, q, start = case(fmt, [150], [n], 1, 2, 16, seed=2, pad=0)
+            t = cu(q, torch.bfloat16)
+            t[n // 2, 1, 7] = float("nan")
+            t[n - 1, 0, 3] = float("inf")
+            out, lse = fx.fx_paged_attend(c.device(fx), t, cu(start, torch.int32), max_new=n, want_lse=True)
+            bad = np.zeros((n, 2), bool)
+            bad[n // 2, 1] = bad[n - 1, 0] = True
+            assert np.array_equal(np.isnan(out.float().cpu().numpy()).all(-1), bad)
+            r, _, tol, _ = attend_ref(c, q, start, D ** -0.5)
+            ok = ~bad
+            assert np.all(np.abs(out.double().cpu().numpy() - r)[ok] <= tol[ok])
+
+
+@pytest.mark.parametrize("n", [3, 90])
+def test_attend_bad_offsets_and_lengths(fx, n):
+    """A sequence whose offsets are not good is skipped, one with too many tokens is cut; lengths are clamped."""
+    c, q, _ = case("bf16", [100, 95, 120], [n] * 3, 1, 2, 16, seed=4, pad=0)
+    dev, t = c.device(fx), cu(q, torch.bfloat16)
+    whole = np.array([0, n, 2 * n, 3 * n])
+    ref = attend_ref(c, q, whole, D ** -0.5)
+    for start, rows in (([0, n, 2 * n, 3 * n + 1], np.r_[0:2 * n]), ([-1, n, 2 * n, 3 * n], np.r_[n:3 * n]),
+                        ([0, n, n - 1, n - 1], np.r_[0:n])):
+        out = torch.full((3 * n, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((3 * n, 2), 7.0, device="cuda")
+        fx.fx_paged_attend(dev, t, cu(start, torch.int32), max_new=n, out=out, lse=lse)
+        assert fx.fx_device_errors() == fx.FX_DEVERR_OFFSETS
+        check(c, (out, lse), ref, rows)
+        rest = np.setdiff1d(np.arange(3 * n), rows)
+        assert torch.all(out[rest] == 7.0) and torch.all(lse[rest] == 7.0)
+    out = torch.full((3 * n, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3 * n, 2), 7.0, device="cuda")
+    fx.fx_paged_attend(dev, t, cu(whole, torch.int32), max_new=n - 1, out=out, lse=lse)
+    assert fx.fx_device_errors() == fx.FX_DEVERR_OFFSETS
+    last = whole[1:] - 1
+    check(c, (out, lse), ref, np.setdiff1d(np.arange(3 * n), last))
+    assert torch.all(out[last] == 7.0)
+    # lengths outside the cache: clamped (the largest to the whole capacity, whose pages exist for none of the rows past)
+    dev.length[0] = -4
+    got = fx.fx_paged_attend(dev, t, cu(whole, torch.int32), max_new=n, want_lse=True)
+    assert fx.fx_device_errors() == fx.FX_DEVERR_LEN
+    assert torch.all(got[0][:n] == 0) and torch.all(got[1][:n] == -float("inf"))
+    check(c, got, ref, np.r_[n:3 * n])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_attend_without_start_and_strided(fx, fmt):
+    """Equal numbers of tokens need no offsets; queries are views of a fused projection; no tokens at all are fine."""
+    c, q, start = case(fmt, [70, 70, 33], [2, 2, 2], 2, 2, 16, seed=6, pad=0)
+    dev = c.device(fx)
+    qkv = torch.randn(6, 9, D, device="cuda").to(torch.bfloat16)
+    qkv[:, 3:7] = cu(q, torch.bfloat16)
+    check(c, fx.fx_paged_attend(dev, qkv[:, 3:7], want_lse=True), attend_ref(c, q, start, D ** -0.5))
+    heads = cu(q, torch.bfloat16).transpose(0, 1).contiguous().transpose(0, 1)
+    check(c, fx.fx_paged_attend(dev, heads, cu(start, torch.int32), want_lse=True), attend_ref(c, q, start, D ** -0.5))
+    assert fx.fx_paged_attend(dev, qkv[:0, :4]).shape == (0, 4, D)
+    for bad in (dict(max_new=3), dict(first=torch.zeros(5, dtype=torch.int32, device="cuda")),
+                dict(slope=torch.ones(3, device="cuda")), dict(out=torch.zeros(6, 4, D, device="cuda")),
+                dict(lse=torch.zeros(4, 6, device="cuda")), dict(start=torch.zeros(3, dtype=torch.int32, device="cuda")),
+                dict(window=-1), dict(cap=-2.0), dict(scale=float("nan"))):
+        with pytest.raises(fx.FxError):
+            fx.fx_paged_attend(dev, heads, **bad)
+    with pytest.raises(fx.FxError):
+        fx.fx_paged_attend(dev, heads[:5])
+
+
+def test_attend_large_values_stay_finite(fx):
+    """Means of values near the type's largest are finite; the row's largest weight may come late."""
+    for n in (2, 80):
+        c, q, start = case("bf16", [400], [n], 1, 2, 16, seed=3, pad=0)
+        c.pool[1] = np.sign(c.pool[1]) * pr.bf16(3.3e38)
+        c.pool[0][c.table[0, 20]] *= 32.0       # (still bf16 values)
+        got = fx.fx_paged_attend(c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32), max_new=n, want_lse=True)
+        assert torch.isfinite(got[0]).all()
+        check(c, got, attend_ref(c, q, start, D ** -0.5))
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_attend_streams_graphs_and_workspaces(fx, new):
+    """Two streams at once, two captured graphs replayed in turn with new contents, and chained programmatic launches, all
+    with workspaces of the library's choice: the same bits as one call."""
+    made = []
+    for seed in (1, 2):
+        c, q, start = case("e2m1" if seed == 1 else "bf16", [900, 500], [new, new], 1, 4, 16, seed=seed, pad=0)
+        made.append((c, q, start, c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32)))
+    alone = []
+    for c, q, start, dev, t, st in made:
+        alone.append(fx.fx_paged_attend(dev, t, st, max_new=new, want_lse=True))
+        check(c, alone[-1], attend_ref(c, q, start, D ** -0.5))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    outs = [[] for _ in made]
+    for _ in range(20):
+        for s, o, (c, q, start, dev, t, st) in zip(streams, outs, made):
+            o.append(fx.fx_paged_attend(dev, t, st, max_new=new, want_lse=True, stream=s))
+    torch.cuda.synchronize()
+    for o, a in zip(outs, alone):
+        for x in o:
+            assert torch.equal(x[0], a[0]) and torch.equal(x[1], a[1])
+    graphs = []
+    for c, q, start, dev, t, st in made:
+        side = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            first = fx.fx_paged_attend(dev, t, st, max_new=new, want_lse=True)
+            second = fx.fx_paged_attend(dev, t, st, max_new=new, want_lse=True, flags=fx.FX_LAUNCH_PDL)
+        graphs.append((g, first, second))
+    for turn in range(3):
+        for (c, q, start, dev, t, st), (g, first, second) in zip(made, graphs):
+            t.neg_()
+            g.replay()
+        torch.cuda.synchronize()
+        for (c, q, start, dev, t, st), (g, first, second) in zip(made, graphs):
+            eager = fx.fx_paged_attend(dev, t, st, max_new=new, want_lse=True)
+            for got in (first, second):
+                assert torch.equal(got[0], eager[0]) and torch.equal(got[1], eager[1])
+
+
+def test_attend_many_sequences_and_spare_pages(fx):
+    """Batches around the scans' sizes, lengths of zero, tables with far more room than rows."""
+    for B, new, G in ((33, 1, 2), (140, 2, 1), (300, 1, 1), (40, 9, 8), (200, 66, 1)):
+        g = np.random.default_rng(B)
+        lens = [int(x) for x in g.integers(0, 60, B)]
+        news = [int(min(n, g.integers(0, new + 1))) for n in lens]
+        start = np.concatenate(([0], np.cumsum(news)))
+        c = pr.Cache("bf16", lens, 1, 16, seed=B, max_pages=500)
+        q = pr.bf16(2.0 * g.standard_normal((max(int(start[-1]), 1), G, D)))
+        got = fx.fx_paged_attend(c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32), max_new=new, want_lse=True)
+        check(c, got, attend_ref(c, q, start, D ** -0.5), slice(0, start[-1]))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_attend_long_rows_in_parts(fx, fmt):
+    """A chunk of few blocks over a long cache is cut into many parts; a window and documents leave some of them empty."""
+    c, q, start = case(fmt, [5000, 2500], [70, 33], 1, 2, 64, seed=12, pad=0)
+    dev, t, st = c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32)
+    n = q.shape[0]
+    first = np.zeros(n, np.int64)
+    first[:40], first[70:90] = 4300, 2490
+    sl = np.array([0.01, 0.0001])
+    for kw in (dict(), dict(window=700), dict(first=first, cap=8.0), dict(slope=sl)):
+        dk = {k: cu(v, torch.int32 if k == "first" else torch.float32) if k in ("first", "slope") else v for k, v in kw.items()}
+        got = fx.fx_paged_attend(dev, t, st, max_new=70, want_lse=True, **dk)
+        check(c, got, attend_ref(c, q, start, D ** -0.5, **kw))
