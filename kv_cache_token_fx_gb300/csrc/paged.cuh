@@ -64,16 +64,14 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
 // cap tanh(x / cap), with icap = 1 / cap.  Up to x = cap, where capped scores mostly lie, tanh(y) = y + y^3 Q(y^2) with Q
 // interpolated at Chebyshev nodes (off by 2^-23.4 of itself in fp32, and no function unit is asked); beyond,
 // tanh(y) = 1 - 2 / (exp(2y) + 1), whose subtrahend is below 1/4.
+__device__ constexpr float kTanh[7] = {-0.3333333134651184f,  0.1333312839269638f,    -0.053934790194034576f, 0.02166011556982994f,
+                                       -0.008218921720981598f, 0.0025104593951255083f, -0.00042069549090228975f};
 __device__ __forceinline__ float tanh_near(float y)
 {
     const float u = y * y;
-    float q = -0.00042069549090228975f;
-    q = fmaf(q, u, 0.0025104593951255083f);
-    q = fmaf(q, u, -0.008218921720981598f);
-    q = fmaf(q, u, 0.02166011556982994f);
-    q = fmaf(q, u, -0.053934790194034576f);
-    q = fmaf(q, u, 0.1333312839269638f);
-    q = fmaf(q, u, -0.3333333134651184f);
+    float q = kTanh[6];
+#pragma unroll
+    for (int i = 5; i >= 0; --i) q = fmaf(q, u, kTanh[i]);
     return fmaf(y * u, q, y);
 }
 __device__ __forceinline__ float tanh_far(float y)

@@ -56,6 +56,7 @@ constexpr int kRing = 16;                        // tiles whose flags are kept (
 // The largest weight so far is 2^kWeightBase when its row's reference moves, and grows by 2^kMaxSlack at most before it
 // moves again.  f16: small weights stay normal numbers.  bf16: sums of products with values up to the type's largest
 // stay finite, as their mean is.
+enum Mode { kPlain, kCap, kBias };   // what is put on the logits: nothing, a cap, a bias by distance (and perhaps a cap)
 template <bool E2M1>
 constexpr float kWeightBase = E2M1 ? 6.f : -32.f;
 constexpr float kFarRef = 4194304.f;   // 2^22: beyond it products and their rounded values lie too far apart for one fma
@@ -131,6 +132,24 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// tanh_near of two values.
+__device__ __forceinline__ float2 tanh_near2(float2 y)
+{
+    const float2 u = mul2(y, y);
+    float2 q = make_float2(kTanh[6], kTanh[6]);
+#pragma unroll
+    for (int i = 5; i >= 0; --i) q = fma2(q, u, make_float2(kTanh[i], kTanh[i]));
+    return fma2(mul2(y, u), q, y);
+}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -205,6 +224,20 @@ __device__ __forceinline__ void tmem_row(uint32_t addr, float (&s)[128])
         s[i] = __uint_as_float(u[i]);
     }
 }
+
+// 32 columns of this thread's tensor-memory lane, without waiting for the store.
+__device__ __forceinline__ void tmem_put32(uint32_t addr, const uint32_t (&u)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
+        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]),
+        "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]),
+        "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- the fillers -------------------------------------------------------------------------------------
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on)
@@ -452,14 +485,13 @@ __device__ __forceinline__ int sequence_length(const PagedAttendParams& p, int b
     return min(max(len, 0), p.c.cap);
 }
 
-// Tiles [t0, t1) that hold whatever a block's queries may see, as far as lengths, positions and the window tell.
-__device__ __forceinline__ void block_tiles(const PagedAttendParams& p, int len, int nb, int all, int blk, int& t0, int& t1)
+// What token j of a sequence sees: rows x <= t < y.
+__device__ __forceinline__ int2 token_interval(const PagedAttendParams& p, int q0, int len, int all, int j)
 {
-    const int j0 = blk * kBlock / p.G, j1 = min((blk * kBlock + kBlock - 1) / p.G, nb - 1);
-    const int lo = p.window > 0 ? max(len - all + j0 - p.window + 1, 0) : 0;
-    const int hi = p.last ? len : min(len, len - all + j1 + 1);
-    t0 = lo / kKeys;
-    t1 = hi > lo ? (hi + kKeys - 1) / kKeys : t0;
+    const int pos = len - all + j;
+    int2 see = make_int2(p.first ? max(p.first[q0 + j], 0) : 0, min(p.last ? p.last[q0 + j] : pos + 1, len));
+    if (p.window > 0) see.x = max(see.x, pos - p.window + 1);
+    return see;
 }
 
 constexpr int kMinPart = 4;   // tiles of a part, at least
@@ -470,19 +502,30 @@ __device__ __forceinline__ bool plan(const PagedAttendParams& p, AttendSmem& sm,
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nq = p.c.B * p.blocks;
-    int mine = 0;
-    if (tid < nq) {
-        const int b = tid / p.blocks, blk = tid - b * p.blocks;
+    for (int k = warp; k < nq; k += kThreadsA / 32) {   // a warp counts a block's tiles: from what its tokens see
+        const int b = k / p.blocks, blk = k - b * p.blocks;
+        const bool report = blockIdx.x == 0 && blk == 0 && lane == 0;
         int q0, nb, all;
-        sequence_queries(p, b, blockIdx.x == 0 && blk == 0, q0, nb, all);
-        const int len = sequence_length(p, b, blockIdx.x == 0 && blk == 0);
+        sequence_queries(p, b, report, q0, nb, all);
+        const int len = sequence_length(p, b, report);
+        int n = 0;
         if (blk * kBlock < nb * p.G) {
-            int t0, t1;
-            block_tiles(p, len, nb, all, blk, t0, t1);
-            mine = max(t1 - t0, 1);
+            const int j0 = blk * kBlock / p.G, j1 = min((blk * kBlock + kBlock - 1) / p.G, nb - 1);
+            int lo = 0x7fffffff, hi = 0;
+            for (int j = j0 + lane; j <= j1; j += 32) {
+                const int2 see = token_interval(p, q0, len, all, j);
+                if (see.x >= see.y) continue;
+                lo = min(lo, see.x);
+                hi = max(hi, see.y);
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            n = lo < hi ? (hi + kKeys - 1) / kKeys - lo / kKeys : 1;
         }
-        count[tid] = mine;
+        if (lane == 0) count[k] = n;
     }
+    __syncthreads();
+    const int mine = tid < nq ? count[tid] : 0;
     int total = mine;
 #pragma unroll
     for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
@@ -534,7 +577,7 @@ __device__ __forceinline__ bool plan(const PagedAttendParams& p, AttendSmem& sm,
     return i >= 0;
 }
 
-template <bool E2M1, bool SHAPED>
+template <bool E2M1, int MODE>
 __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid_constant__ PagedAttendParams p)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -579,9 +622,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         g = h * p.G + r - j * p.G;
         qi = (int64_t)q0 + j;
         pos = len - all + j;
-        hi = p.last ? min(p.last[qi], len) : min(pos + 1, len);
-        lo = p.first ? max(p.first[qi], 0) : 0;
-        if (p.window > 0) lo = max(lo, pos - p.window + 1);
+        const int2 see = token_interval(p, q0, len, all, j);
+        lo = see.x;
+        hi = see.y;
     }
     if (tid == 0) {
         sm.vis_lo = sm.com_hi = 0x7fffffff;
@@ -665,12 +708,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         r.ta = r.lo / kKeys;
         r.tb = (r.hi + kKeys - 1) / kKeys;
         if (n_parts > 1) {
-            int t0, t1;
-            block_tiles(p, len, nb, all, blk, t0, t1);
-            const int64_t n = t1 - t0;
-            r.ta = max(r.ta, t0 + (int)(n * part / n_parts));
-            r.tb = min(r.tb, t0 + (int)(n * (part + 1) / n_parts));
-            r.tb = max(r.tb, r.ta);
+            const int64_t n = r.tb - r.ta;
+            r.tb = r.ta + (int)(n * (part + 1) / n_parts);
+            r.ta += (int)(n * part / n_parts);
         }
     }
     const int nt = r.tb - r.ta;
@@ -737,13 +777,13 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         const int x = warp >> 2;
         const bool on = x == 0 || two;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        bool dead = false, poison = false;
+        bool dead = false, poison = false, odd = false;
         float m = -INFINITY, l = 0.f;   // reference and sum (in units of 2^kWeightBase)
         // rows that do not exist see every row of their zeros, so that they ask for no masks
         const int my_lo = live ? lo : -0x40000000, my_hi = live ? hi : 0x7fffffff;
         const float cap = p.cap, icap = cap > 0.f ? 1.f / cap : 0.f;
-        const float slope2 = SHAPED && p.slope && live ? p.slope[g] * 1.4426950408889634f : 0.f;
-        if (!SHAPED) qs *= 1.4426950408889634f;
+        const float slope2 = MODE == kBias && live ? p.slope[g] * 1.4426950408889634f : 0.f;
+        if (MODE == kPlain) qs *= 1.4426950408889634f;
         auto check = [&](int t) {   // whether the row sees a value of tile t that is not finite (those were left out)
             if (*(volatile int*)&sm.any_bad == 0) return;
             for (int w = 0; w < 4; ++w) {
@@ -766,63 +806,117 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 const unsigned skip = *(volatile unsigned*)&sm.skip[tile & (kRing - 1)];
                 const int a = my_lo - j0, e = my_hi - j0;   // the row sees keys a <= k < e of the tile
                 const bool whole = a <= 0 && e >= kKeys;
-                float f = qs;
-                if (SHAPED) {
-                    // base-2 logits in place
-                    const float d0 = (float)(pos - j0);
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) {
-                        float v = s[k] * qs;
-                        if (cap > 0.f) v = soft_cap(v, cap, icap);
-                        s[k] = fmaf(fabsf(d0 - (float)k), -slope2, v * 1.4426950408889634f);
-                    }
-                    f = 1.f;
-                }
-                // the largest logit that the row sees
+                // which keys each row sees, as bits; rows that see all of them take no masks
+                uint32_t see[4];
                 const bool masked = __any_sync(0xffffffffu, !whole) || skip != 0;
-                float mt = -INFINITY;
+                if (masked) {
+                    bool any = false;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int from = min(max(a - 32 * w, 0), 32), to = min(max(e - 32 * w, 0), 32);
+                        uint32_t bits = to > from ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+                        if ((skip >> (2 * w)) & 1u) bits &= 0xffff0000u;
+                        if ((skip >> (2 * w)) & 2u) bits &= 0x0000ffffu;
+                        see[w] = bits;
+                        any |= bits != 0;
+                    }
+                    if (!__any_sync(0xffffffffu, any)) {   // nothing of this tile for any row of the warp
+                        uint32_t zero[32] = {};
+                        tmem_put32(lanes + col_s(x), zero);
+                        tmem_put32(lanes + col_s(x) + 32, zero);
+                        tmem_wait_st();
+                        tc_before();
+                        arrive(&sm.p_full[x]);
+                        continue;
+                    }
+                }
+                float f = MODE == kPlain ? qs : 1.f;   // factor from s to base-2 logits
+                if (MODE != kPlain) {
+                    if (cap > 0.f) {
+                        // tanh by its polynomial for two at a time, where no logit is past the cap
+                        const float k = qs * icap;
+                        float top = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 128; i += 4) {
+                            const float u = max3(fabsf(s[i]), fabsf(s[i + 1]), fabsf(s[i + 2]));
+                            top = max3(top, u, fabsf(s[i + 3]));
+                        }
+                        if (!__any_sync(0xffffffffu, !(top * k <= 1.f))) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) {
+                                const float2 y = tanh_near2(mul2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(k, k)));
+                                s[2 * i] = y.x;
+                                s[2 * i + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) {
+                                const float y = s[i] * k;
+                                s[i] = fabsf(y) <= 1.f ? tanh_near(y) : tanh_far(y);
+                            }
+                        }
+                    }
+                    f = (cap > 0.f ? cap : qs) * 1.4426950408889634f;
+                    if (MODE == kBias) {
+                        const float d0 = (float)(pos - j0);
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) s[i] = fmaf(fabsf(d0 - (float)i), -slope2, s[i] * f);
+                        f = 1.f;
+                    }
+                }
                 if (masked) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) {
-                        const bool see = k >= a && k < e && ((skip >> (k >> 4)) & 1u) == 0;
-                        s[k] = see ? s[k] : -INFINITY;
-                    }
+                    for (int k = 0; k < 128; ++k) s[k] = (see[k >> 5] >> (k & 31)) & 1u ? s[k] : -INFINITY;
                 }
+                // the largest logit that the row sees
+                float mt;
+                {
+                    float c[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 128; k += 2) mt = max3(mt, s[k], s[k + 1]);
-                // (a negative factor was moved into the queries; a hidden logit stays -inf also with a factor of 0)
+                    for (int k = 0; k < 128; k += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) c[u] = max3(c[u], s[k + 2 * u], s[k + 2 * u + 1]);
+                    mt = fmaxf(max3(c[0], c[1], c[2]), c[3]);
+                }
+                // (factors are not negative; a hidden logit stays -inf also with a factor of 0)
                 mt = mt == -INFINITY ? mt : __fmul_rn(mt, f);
                 const bool grow = mt > m + kMaxSlack;   // also when there is none yet and the row sees something
-                const float mnew = grow ? mt : m;
-                if (t > 0 && __any_sync(0xffffffffu, grow)) {   // O of the tiles before is complete: S was issued after it
-                    const float z = !grow ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mnew));
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float mnew = grow ? mt : m;
+                    if (t > 0) {   // O of the tiles before is complete: S was issued after it
+                        const float z = !grow ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mnew));
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        uint32_t w[32];
-                        tmem_ld32(lanes + col_o(x) + 32 * c, v);
+                        for (int c = 0; c < 4; ++c) {
+                            float v[32];
+                            uint32_t w[32];
+                            tmem_ld32(lanes + col_o(x) + 32 * c, v);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(v[k] * z);
-                        tmem_st32(lanes + col_o(x) + 32 * c, w);
+                            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(v[k] * z);
+                            tmem_st32(lanes + col_o(x) + 32 * c, w);
+                        }
+                        l *= z;
                     }
-                    l *= z;
+                    m = mnew;
+                    // a far reference, or hidden logits beside a factor of 0, take rounded products one by one
+                    odd = __any_sync(0xffffffffu, fabsf(m) > kFarRef && m != -INFINITY);
                 }
-                m = mnew;
                 const float bias = (m == -INFINITY ? 0.f : -m) + kWeightBase<E2M1>;
                 uint32_t w[64];
-                float2 l2 = make_float2(0.f, 0.f);
-                const bool far = __any_sync(0xffffffffu, fabsf(bias) > kFarRef);
-                if (!far && !(masked && f == 0.f)) {
+                float2 l2 = make_float2(0.f, 0.f), l3 = make_float2(0.f, 0.f);
+                if (!odd && !(masked && f == 0.f)) {
                     const float2 ff = make_float2(f, f), bb = make_float2(bias, bias);
 #pragma unroll
                     for (int k = 0; k < 64; ++k) {
                         const float2 y = fma2(make_float2(s[2 * k], s[2 * k + 1]), ff, bb);
                         const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-                        l2 = add2(l2, pp);
+                        if (k & 1)
+                            l3 = add2(l3, pp);
+                        else
+                            l2 = add2(l2, pp);
                         w[k] = pack2<E2M1>(pp.x, pp.y);
+                        if (k == 31) tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
                     }
                 } else {
-                    // (rounded products, as the reference is one; a hidden logit is -inf whatever the factor)
 #pragma unroll
                     for (int k = 0; k < 64; ++k) {
                         float y[2];
@@ -835,10 +929,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         l2 = add2(l2, make_float2(y[0], y[1]));
                         w[k] = pack2<E2M1>(y[0], y[1]);
                     }
+                    tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
                 }
+                l2 = add2(l2, l3);
                 l += l2.x + l2.y;
-                tmem_st32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
-                tmem_st32(lanes + col_s(x) + 32, reinterpret_cast<uint32_t(&)[32]>(w[32]));
+                tmem_put32(lanes + col_s(x) + 32, reinterpret_cast<uint32_t(&)[32]>(w[32]));
+                tmem_wait_st();
                 tc_before();
                 arrive(&sm.p_full[x]);
             }
@@ -938,7 +1034,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
     }
 }
 
-template <bool E2M1, bool SHAPED>
+template <bool E2M1, int MODE>
 cudaError_t launch(const PagedAttendParams& p, bool pdl, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
@@ -947,12 +1043,12 @@ cudaError_t launch(const PagedAttendParams& p, bool pdl, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(paged_attend_kernel<E2M1, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(E2M1));
+        e = cudaFuncSetAttribute(paged_attend_kernel<E2M1, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(E2M1));
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
     const dim3 grid = p.split ? dim3(p.split) : dim3(p.c.Hkv, p.blocks, p.c.B);
-    return launch_kernel(paged_attend_kernel<E2M1, SHAPED>, grid, dim3(kThreadsA), attend_smem(E2M1), s, pdl, 0u, p);
+    return launch_kernel(paged_attend_kernel<E2M1, MODE>, grid, dim3(kThreadsA), attend_smem(E2M1), s, pdl, 0u, p);
 }
 
 }  // namespace
@@ -975,9 +1071,9 @@ size_t paged_attend_workspace_bytes(const PagedAttendCut& c)
 
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s)
 {
-    const bool shaped = p.cap > 0.f || p.slope != nullptr;
-    if (e2m1) return shaped ? launch<true, true>(p, pdl, s) : launch<true, false>(p, pdl, s);
-    return shaped ? launch<false, true>(p, pdl, s) : launch<false, false>(p, pdl, s);
+    if (p.slope) return e2m1 ? launch<true, kBias>(p, pdl, s) : launch<false, kBias>(p, pdl, s);
+    if (p.cap > 0.f) return e2m1 ? launch<true, kCap>(p, pdl, s) : launch<false, kCap>(p, pdl, s);
+    return e2m1 ? launch<true, kPlain>(p, pdl, s) : launch<false, kPlain>(p, pdl, s);
 }
 
 }  // namespace fx
