@@ -46,7 +46,7 @@ __host__ __device__ constexpr int attend_smem(bool e2m1)
 }
 constexpr int kLag = 3;                          // bf16: tiles whose copies are under way
 // Registers a thread of the softmax, the fillers and the issuing warp; the launch's 128 a thread cover their sum.
-constexpr int kRegsSoftmax = 192, kRegsFill = 88, kRegsIssue = 40;
+constexpr int kRegsSoftmax = 184, kRegsFill = 88, kRegsIssue = 56;
 static_assert(2 * kRegsSoftmax + kRegsFill + kRegsIssue <= 4 * 128, "a split above the launch's registers never starts");
 // tensor-memory columns: S (P in its first half) of the subtiles, O of the subtiles
 __device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * 128); }
@@ -175,28 +175,43 @@ __host__ __device__ constexpr uint32_t idesc(bool b_mn_major)
     return E2M1 ? d & ~((1u << 7) | (1u << 10)) : d;   // (both operands f16 instead of bf16)
 }
 
-template <bool E2M1>
-__device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q_tile, uint32_t k_tile)
+// One lane of the warp, as a predicate that the compiler knows for one: what the products take then stays in uniform
+// registers (with lane == 0 in its place each product took 115 cycles to issue, twice its time on the tensor core).
+__device__ __forceinline__ bool elect_lane()
 {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+// The low words of an operand's descriptors (their high words are one constant).
+__device__ __forceinline__ uint32_t sdesc_low(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// S = Q K^T: eight steps of 16 dimensions.  q, k: the low words of the tiles' first descriptors.
+template <bool E2M1>
+__device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q, uint32_t k)
+{
+    constexpr uint32_t kIdesc = idesc<E2M1>(false);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t off = (uint32_t)((ks >> 2) * (kOperand / 2) + (ks & 3) * 32);
+        const uint32_t off = (uint32_t)((ks >> 2) * (kOperand / 2) + (ks & 3) * 32) >> 4;
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(sdesc(q_tile + off)), "l"(sdesc(k_tile + off)), "r"(idesc<E2M1>(false)), "r"(ks > 0 ? 1u : 0u));
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+            "r"(q + off), "r"(k + off), "n"(kDescHigh), "n"(kIdesc), "r"(ks > 0 ? 1u : 0u));
     }
 }
+// O (+)= P V: eight steps of 16 cache rows.  v: the low word of the tile's first descriptor.
 template <bool E2M1>
-__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_tile, bool accumulate)
+__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, uint32_t accumulate)
 {
+    constexpr uint32_t kIdesc = idesc<E2M1>(true);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "r"(p_tmem + 8 * ks), "l"(sdesc(v_tile + ks * 2048, kOperand / 2)), "r"(idesc<E2M1>(true)),
-            "r"((accumulate || ks > 0) ? 1u : 0u));
+            "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+            "r"(p_tmem + 8 * ks), "r"(v + (uint32_t)(ks * 2048 >> 4)), "n"(kDescHigh), "n"(kIdesc), "r"(ks > 0 ? 1u : accumulate));
     }
 }
 
@@ -247,6 +262,10 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on)
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 8u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -302,7 +321,41 @@ struct FillRange {
     }
 };
 
-// bf16: a thread copies 16-byte chunk tid % 16 of rows tid / 16 + 8 i of every tile.
+// Where the rows of a tile lie: lane g (of every eight) holds 16-row group g.
+struct Groups {
+    int64_t at;      // the group's first row from row 0 of page 0 (of this head), scales too
+    int64_t scale;
+    unsigned good;   // groups with a page
+    bool whole;      // all rows of the tile are copied
+};
+template <bool E2M1>
+__device__ __forceinline__ Groups find_groups(const PagedCache& c, int page, int tile, const FillRange& r)
+{
+    Groups g;
+    const uint32_t in = (uint32_t)((tile * kKeys + 16 * (threadIdx.x & 7)) & c.page_mask), pg = (uint32_t)max(page, 0);
+    g.at = (int64_t)((uint64_t)pg * c.sp + (uint64_t)in * c.st);
+    g.scale = E2M1 ? (int64_t)((uint64_t)pg * c.ssp + (uint64_t)in * c.sst) : 0;
+    g.good = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
+    g.whole = g.good == 0xffu && tile * kKeys >= r.lo && (tile + 1) * kKeys <= r.hi;
+    return g;
+}
+__device__ __forceinline__ int64_t group_at(int64_t mine, int g)
+{
+    return (int64_t)__shfl_sync(0xffffffffu, (long long)mine, g);
+}
+// The flags of tile t, for the softmax; clears those of a later one.
+__device__ __forceinline__ void put_flags(AttendSmem& sm, int page, int t)
+{
+    const unsigned bad = bad_groups(page);
+    if ((threadIdx.x & 127) == 0) {
+        sm.skip[t & (kRing - 1)] = bad;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sm.bad_v[(t + 8) & (kRing - 1)][w] = 0u;   // (the tile that had these is long done)
+    }
+}
+
+// bf16: a thread copies 16-byte chunk tid % 16 of rows tid / 16 + 8 i of every tile.  A tile whose rows are all copied --
+// most are -- takes a copy and an addition for each 16 bytes.
 __device__ __forceinline__ void fill_bf16(const PagedAttendParams& p, AttendSmem& sm, uint32_t ring, const int32_t* table, int h,
                                           const FillRange& r)
 {
@@ -312,10 +365,9 @@ __device__ __forceinline__ void fill_bf16(const PagedAttendParams& p, AttendSmem
     const int n = 2 * (r.tb - r.ta);
     const uint32_t to = sw128(row0, 8 * chunk, kKeys);
     const char* const kb = c.k + (int64_t)h * c.sh + 16 * chunk;
-    const int64_t dv = c.v - c.k;
+    const int64_t mine = (int64_t)row0 * c.st, eight = 8 * (int64_t)c.st, dv = c.v - c.k;
     bool dead = false;
-    int page = group_page(c, table, r.ta, r.lo, r.hi, p.err), next = page;
-    auto done = [&](int m) {   // tile m's copies have landed
+    auto landed = [&](int m) {   // tile m's copies have landed
         if ((m & 1) && r.partial(r.ta + (m >> 1))) {
             const int t = r.ta + (m >> 1);
             const uint32_t at = ring + (m % kSlots) * kOperand + to;
@@ -331,39 +383,52 @@ __device__ __forceinline__ void fill_bf16(const PagedAttendParams& p, AttendSmem
         fence_operands();
         arrive(&sm.full[m % kSlots]);
     };
-    for (int m = 0; m < n; ++m) {
-        const int t = r.ta + (m >> 1), slot = m % kSlots;
-        if ((m & 1) == 0) {
-            page = next;
-            if (t + 1 < r.tb) next = group_page(c, table, t + 1, r.lo, r.hi, p.err);
-            const unsigned bad = bad_groups(page);
-            if (tid == 0) {
-                sm.skip[t & (kRing - 1)] = bad;
-                // (the tile that last had these flags is long done)
+    int next = group_page(c, table, r.ta, r.lo, r.hi, p.err);
+    int slot = 0, turn = 0;
+    for (int t = r.ta; t < r.tb; ++t) {
+        const int page = next;
+        if (t + 1 < r.tb) next = group_page(c, table, t + 1, r.lo, r.hi, p.err);
+        put_flags(sm, page, t);
+        const Groups g = find_groups<false>(c, page, t, r);
+        const char* src[8];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) sm.bad_v[(t + 8) & (kRing - 1)][w] = 0u;
+        for (int u = 0; u < 8; ++u) src[u] = kb + mine + group_at(g.at, u);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (turn > 0) wait(&sm.empty[slot], (unsigned)(turn - 1) & 1u, p.err, dead);
+            const uint32_t dst = ring + slot * kOperand + to;
+            if (g.whole) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    cp16(dst + 2048 * u, src[u]);
+                    cp16(dst + 2048 * u + 1024, src[u] + eight);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const int row = t * kKeys + row0 + 8 * u;
+                    const bool on = ((g.good >> (u >> 1)) & 1u) && row >= r.lo && row < r.hi;
+                    copy16(dst + 1024 * u, on ? src[u >> 1] + (u & 1) * eight : kb, on);
+                }
             }
-        }
-        if (m >= kSlots) wait(&sm.empty[slot], (unsigned)(m / kSlots - 1) & 1u, p.err, dead);
-        const uint32_t dst = ring + slot * kOperand + to;
-        const char* const base = m & 1 ? kb + dv : kb;
+            commit_copies();
+            const int m = 2 * (t - r.ta) + which;
+            if (m >= kLag) {
+                wait_copies<kLag>();
+                landed(m - kLag);
+            }
+            if (++slot == kSlots) {
+                slot = 0;
+                ++turn;
+            }
+            if (which == 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int pg = __shfl_sync(0xffffffffu, page, i >> 1);
-            const int row = t * kKeys + row0 + 8 * i;
-            const bool on = pg >= 0 && row >= r.lo && row < r.hi;
-            const char* src = base;
-            if (on) src += (uint64_t)(uint32_t)pg * c.sp + (uint64_t)(uint32_t)(row & c.page_mask) * c.st;
-            copy16(dst + 1024 * i, src, on);
-        }
-        commit_copies();
-        if (m >= kLag) {
-            wait_copies<kLag>();
-            done(m - kLag);
+                for (int u = 0; u < 8; ++u) src[u] += dv;
+            }
         }
     }
     wait_copies<0>();
-    for (int m = max(n - kLag, 0); m < n; ++m) done(m);
+    for (int m = max(n - kLag, 0); m < n; ++m) landed(m);
 }
 
 // 4 bits: lane l of a warp takes chunk l / 8 (32 values) of rows 8 warp + l % 8 + 32 i, so that neither the codes' nor the
@@ -374,71 +439,77 @@ __device__ __forceinline__ void fill_e2m1(const PagedAttendParams& p, AttendSmem
     constexpr int kSlots = slots(true);
     const PagedCache& c = p.c;
     const int tid = threadIdx.x & 127, lane = tid & 31, chunk = lane >> 3, row0 = (tid >> 5) * 8 + (lane & 7);
-    const int n = 2 * (r.tb - r.ta);
+    const int n = 2 * (r.tb - r.ta), g0 = row0 >> 4;   // the warp's rows lie in groups g0 + 2 i
     const uint32_t from = (uint32_t)(row0 * 64 + ((chunk ^ ((row0 >> 1) & 3)) << 4));
-    const char* const kb = c.k + (int64_t)h * c.sh + 16 * chunk;
-    const char* const sb = c.ks + (int64_t)h * c.ssh;
+    const char* const kb = c.k + (int64_t)h * c.sh + 16 * chunk + (int64_t)(row0 & 15) * c.st;
+    const char* const sb = c.ks + (int64_t)h * c.ssh + (int64_t)(row0 & 15) * c.sst;
     const int64_t dv = c.v - c.k, ds = c.vs - c.ks;
     bool dead = false;
-    int page = -1, next = group_page(c, table, r.ta, r.lo, r.hi, p.err);
+    int next = group_page(c, table, r.ta, r.lo, r.hi, p.err);
+    Groups g = {};
     auto feed = [&](int m) {
         if (m < n) {
             const int t = r.ta + (m >> 1);
             if ((m & 1) == 0) {
-                page = next;
+                const int page = next;
                 if (t + 1 < r.tb) next = group_page(c, table, t + 1, r.lo, r.hi, p.err);
-                const unsigned bad = bad_groups(page);
-                if (tid == 0) {
-                    sm.skip[t & (kRing - 1)] = bad;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) sm.bad_v[(t + 8) & (kRing - 1)][w] = 0u;
-                }
+                put_flags(sm, page, t);
+                g = find_groups<true>(c, page, t, r);
             }
-            const uint32_t dst = raw + (m % kRaw) * kRawTile;
+            const uint32_t dst = raw + (m % kRaw) * kRawTile, sdst = dst + kKeys * 64 + row0 * 8;
             const char* const base = m & 1 ? kb + dv : kb;
             const char* const sbase = m & 1 ? sb + ds : sb;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int pg = __shfl_sync(0xffffffffu, page, (row0 >> 4) + 2 * i);
-                const int row = t * kKeys + row0 + 32 * i;
-                const bool on = pg >= 0 && row >= r.lo && row < r.hi;
-                const uint32_t in = (uint32_t)(row & c.page_mask);
-                const char* src = base;
-                if (on) src += (uint64_t)(uint32_t)pg * c.sp + (uint64_t)in * c.st;
-                copy16(dst + from + 2048 * i, src, on);
-                if (chunk == 0) {
-                    const char* ssrc = sbase;
-                    if (on) ssrc += (uint64_t)(uint32_t)pg * c.ssp + (uint64_t)in * c.sst;
-                    copy8(dst + kKeys * 64 + (row0 + 32 * i) * 8, ssrc, on);
+                const char* src = base + group_at(g.at, g0 + 2 * i);
+                const char* ssrc = sbase + group_at(g.scale, g0 + 2 * i);
+                bool on = true;
+                if (!g.whole) {
+                    const int row = t * kKeys + row0 + 32 * i;
+                    on = ((g.good >> (g0 + 2 * i)) & 1u) && row >= r.lo && row < r.hi;
+                    if (!on) src = base, ssrc = sbase;
                 }
+                copy16(dst + from + 2048 * i, src, on);
+                if (chunk == 0) copy8(sdst + 256 * i, ssrc, on);
             }
         }
         commit_copies();
     };
     for (int m = 0; m < kRaw - 1; ++m) feed(m);
+    int slot = 0, turn = 0;
     for (int m = 0; m < n; ++m) {
-        const int t = r.ta + (m >> 1), slot = m % kSlots;
+        const int t = r.ta + (m >> 1);
         wait_copies<kRaw - 2>();
         __syncwarp();   // (a row's scales were copied by another lane)
-        if (m >= kSlots) wait(&sm.empty[slot], (unsigned)(m / kSlots - 1) & 1u, p.err, dead);
         const uint32_t src = raw + (m % kRaw) * kRawTile, dst = ring + slot * kOperand;
-        const bool look = (m & 1) && r.partial(t);
+        uint4 x[4];
+        uint32_t sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = row0 + 32 * i;
-            const uint4 x = lds128(src + from + 2048 * i);
-            uint32_t sc = lds16(src + kKeys * 64 + row * 8 + 2 * chunk);
-            if (look) {
-                const uint32_t nan = __vcmpeq4(sc & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0xffffu;
+            x[i] = lds128(src + from + 2048 * i);
+            sc[i] = lds16(src + kKeys * 64 + (row0 + 32 * i) * 8 + 2 * chunk);
+        }
+        __syncwarp();   // every lane has read the raw tile's neighbour in the ring
+        feed(m + kRaw - 1);
+        if ((m & 1) && r.partial(t)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 32 * i;
+                const uint32_t nan = __vcmpeq4(sc[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0xffffu;
                 if (nan) {
-                    sc &= ~nan;
+                    sc[i] &= ~nan;
                     atomicOr(&sm.bad_v[t & (kRing - 1)][row >> 5], 1u << (row & 31));
                     sm.any_bad = 1;
                 }
             }
-            const uint32_t z = e4m3x2_to_f16x2(sc);
+        }
+        if (turn > 0) wait(&sm.empty[slot], (unsigned)(turn - 1) & 1u, p.err, dead);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 32 * i;
+            const uint32_t z = e4m3x2_to_f16x2(sc[i]);
             const uint32_t s0 = __byte_perm(z, 0, 0x1010), s1 = __byte_perm(z, 0, 0x3232);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             const uint32_t at = dst + (chunk >> 1) * (kOperand / 2) + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -451,8 +522,10 @@ __device__ __forceinline__ void fill_e2m1(const PagedAttendParams& p, AttendSmem
         }
         fence_operands();
         arrive(&sm.full[slot]);
-        __syncwarp();   // every lane is done with the raw tile that the next copies overwrite
-        feed(m + kRaw - 1);
+        if (++slot == kSlots) {
+            slot = 0;
+            ++turn;
+        }
     }
     wait_copies<0>();
 }
@@ -720,47 +793,70 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         if (warp == 12 && nt > 0) {
             constexpr int kSlots = slots(E2M1);
             bool dead = false;
-            auto slot_of = [&](int m) { return ring + (uint32_t)(m % kSlots) * kOperand; };
-            auto wait_full = [&](int m) {
-                wait(&sm.full[m % kSlots], (unsigned)(m / kSlots) & 1u, p.err, dead);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const int tiles = __shfl_sync(0xffffffffu, nt, 0);
+            const uint32_t q0d = sdesc_low(base, 16), ringd = ring >> 4;
+            // the ring's place: slots of K (the current tile's V is the one before it)
+            auto k_of = [&](int slot) { return sdesc_low((ringd + (uint32_t)slot * (kOperand >> 4)) << 4, 16); };
+            auto v_of = [&](int slot) { return sdesc_low((ringd + (uint32_t)slot * (kOperand >> 4)) << 4, kOperand / 2); };
+            int slot = 0, turn = 0;   // of the next operand tile
+            auto wait_full = [&]() {
+                wait(&sm.full[slot], (unsigned)turn & 1u, p.err, dead);
                 tc_after();
             };
-            wait_full(0);
-            if (lane == 0) {
-                mma_qk<E2M1>(tmem + col_s(0), base, slot_of(0));
+            auto next = [&]() {
+                if (++slot == kSlots) {
+                    slot = 0;
+                    ++turn;
+                }
+            };
+            wait_full();
+            if (elect_lane()) {
+                mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
                 mma_commit(&sm.s_full[0]);
                 if (two) {
-                    mma_qk<E2M1>(tmem + col_s(1), base + kOperand, slot_of(0));
+                    mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
                     mma_commit(&sm.s_full[1]);
                 }
-                mma_commit(&sm.empty[0]);
+                mma_commit(&sm.empty[slot]);
             }
-            __syncwarp();
-            for (int t = 0; t < nt; ++t) {
-                wait_full(2 * t + 1);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x == 1 && !two) break;
-                    const bool last_x = x == 1 || !two;
-                    wait(&sm.p_full[x], (unsigned)t & 1u, p.err, dead);
-                    tc_after();
-                    if (lane == 0) {
-                        mma_pv<E2M1>(tmem + col_o(x), tmem + col_s(x), slot_of(2 * t + 1), t > 0);
-                        if (last_x) mma_commit(&sm.empty[(2 * t + 1) % kSlots]);
-                    }
-                    __syncwarp();
-                    if (t + 1 < nt) {
-                        if (x == 0) wait_full(2 * t + 2);
-                        if (lane == 0) {
-                            mma_qk<E2M1>(tmem + col_s(x), base + x * kOperand, slot_of(2 * t + 2));
-                            mma_commit(&sm.s_full[x]);
-                            if (last_x) mma_commit(&sm.empty[(2 * t + 2) % kSlots]);
-                        }
-                    } else if (lane == 0) {
-                        mma_commit(&sm.o_done[x]);
-                    }
-                    __syncwarp();
+            next();
+            for (int t = 0; t < tiles; ++t) {
+                wait_full();   // V
+                const int vs = slot;
+                next();
+                const bool more = t + 1 < tiles;
+                wait(&sm.p_full[0], (unsigned)t & 1u, p.err, dead);
+                tc_after();
+                if (elect_lane()) {
+                    mma_pv<E2M1>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
+                    if (!two) mma_commit(&sm.empty[vs]);
+                    if (!more) mma_commit(&sm.o_done[0]);
                 }
+                if (more) {
+                    wait_full();   // K of the next tile
+                    if (elect_lane()) {
+                        mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
+                        mma_commit(&sm.s_full[0]);
+                        if (!two) mma_commit(&sm.empty[slot]);
+                    }
+                }
+                if (two) {
+                    wait(&sm.p_full[1], (unsigned)t & 1u, p.err, dead);
+                    tc_after();
+                    if (elect_lane()) {
+                        mma_pv<E2M1>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
+                        mma_commit(&sm.empty[vs]);
+                        if (more) {
+                            mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
+                            mma_commit(&sm.s_full[1]);
+                            mma_commit(&sm.empty[slot]);
+                        } else {
+                            mma_commit(&sm.o_done[1]);
+                        }
+                    }
+                }
+                if (more) next();
             }
         }
     } else if (warp >= 8) {
