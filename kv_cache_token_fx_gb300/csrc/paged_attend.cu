@@ -141,6 +141,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+// tanh(y) = 1 - 2 / (exp(2y) + 1), of x = 2 y log2(e): off by 2^-21 at most (not of itself: of 1).
+__device__ __forceinline__ float tanh_exp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(x) + 1.f));
+    return fmaf(-2.f, r, 1.f);
+}
 // tanh_near of two values.
 __device__ __forceinline__ float2 tanh_near2(float2 y)
 {
@@ -790,20 +797,18 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 12 && nt > 0) {
+        // One lane does it all: a wait that the whole warp takes part in costs some 250 cycles more, which the tensor core
+        // stands still (the products' queue is short).
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int tiles = warp == 12 ? __shfl_sync(0xffffffffu, nt, 0) : 0;
+        if (tiles > 0 && elect_lane()) {
             constexpr int kSlots = slots(E2M1);
             bool dead = false;
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const int tiles = __shfl_sync(0xffffffffu, nt, 0);
-            const uint32_t q0d = sdesc_low(base, 16), ringd = ring >> 4;
-            // the ring's place: slots of K (the current tile's V is the one before it)
-            auto k_of = [&](int slot) { return sdesc_low((ringd + (uint32_t)slot * (kOperand >> 4)) << 4, 16); };
-            auto v_of = [&](int slot) { return sdesc_low((ringd + (uint32_t)slot * (kOperand >> 4)) << 4, kOperand / 2); };
+            const uint32_t q0d = sdesc_low(base, 16);
+            auto k_of = [&](int slot) { return sdesc_low(ring + (uint32_t)slot * kOperand, 16); };
+            auto v_of = [&](int slot) { return sdesc_low(ring + (uint32_t)slot * kOperand, kOperand / 2); };
             int slot = 0, turn = 0;   // of the next operand tile
-            auto wait_full = [&]() {
-                wait(&sm.full[slot], (unsigned)turn & 1u, p.err, dead);
-                tc_after();
-            };
+            auto wait_full = [&]() { wait(&sm.full[slot], (unsigned)turn & 1u, p.err, dead); };
             auto next = [&]() {
                 if (++slot == kSlots) {
                     slot = 0;
@@ -811,54 +816,49 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 }
             };
             wait_full();
-            if (elect_lane()) {
-                mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
-                mma_commit(&sm.s_full[0]);
-                if (two) {
-                    mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
-                    mma_commit(&sm.s_full[1]);
-                }
-                mma_commit(&sm.empty[slot]);
+            tc_after();
+            mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
+            mma_commit(&sm.s_full[0]);
+            if (two) {
+                mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
+                mma_commit(&sm.s_full[1]);
             }
+            mma_commit(&sm.empty[slot]);
             next();
             for (int t = 0; t < tiles; ++t) {
                 wait_full();   // V
                 const int vs = slot;
                 next();
                 const bool more = t + 1 < tiles;
+                if (more) wait_full();   // K of the next tile
                 wait(&sm.p_full[0], (unsigned)t & 1u, p.err, dead);
                 tc_after();
-                if (elect_lane()) {
-                    mma_pv<E2M1>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
-                    if (!two) mma_commit(&sm.empty[vs]);
-                    if (!more) mma_commit(&sm.o_done[0]);
-                }
+                mma_pv<E2M1>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
+                if (!two) mma_commit(&sm.empty[vs]);
                 if (more) {
-                    wait_full();   // K of the next tile
-                    if (elect_lane()) {
-                        mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
-                        mma_commit(&sm.s_full[0]);
-                        if (!two) mma_commit(&sm.empty[slot]);
-                    }
+                    mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
+                    mma_commit(&sm.s_full[0]);
+                    if (!two) mma_commit(&sm.empty[slot]);
+                } else {
+                    mma_commit(&sm.o_done[0]);
                 }
                 if (two) {
                     wait(&sm.p_full[1], (unsigned)t & 1u, p.err, dead);
                     tc_after();
-                    if (elect_lane()) {
-                        mma_pv<E2M1>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
-                        mma_commit(&sm.empty[vs]);
-                        if (more) {
-                            mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
-                            mma_commit(&sm.s_full[1]);
-                            mma_commit(&sm.empty[slot]);
-                        } else {
-                            mma_commit(&sm.o_done[1]);
-                        }
+                    mma_pv<E2M1>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
+                    mma_commit(&sm.empty[vs]);
+                    if (more) {
+                        mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
+                        mma_commit(&sm.s_full[1]);
+                        mma_commit(&sm.empty[slot]);
+                    } else {
+                        mma_commit(&sm.o_done[1]);
                     }
                 }
                 if (more) next();
             }
         }
+        __syncwarp();
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
         if (nt > 0) {
@@ -929,8 +929,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 float f = MODE == kPlain ? qs : 1.f;   // factor from s to base-2 logits
                 if (MODE != kPlain) {
                     if (cap > 0.f) {
-                        // tanh by its polynomial for two at a time, where no logit is past the cap
-                        const float k = qs * icap;
+                        // Where no logit is past the cap, the polynomial (10 steps of the fp32 units for two at a time)
+                        // takes five of eight pairs, the exponential (3 steps, and 12 of the function unit for one) the
+                        // others, so that both are busy alike; else the exponential takes all.
+                        const float k = qs * icap, k2 = k * 2.885390081777927f;
                         float top = 0.f;
 #pragma unroll
                         for (int i = 0; i < 128; i += 4) {
@@ -940,16 +942,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         if (!__any_sync(0xffffffffu, !(top * k <= 1.f))) {
 #pragma unroll
                             for (int i = 0; i < 64; ++i) {
-                                const float2 y = tanh_near2(mul2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(k, k)));
+                                float2 y;
+                                if (i % 8 == 1 || i % 8 == 4 || i % 8 == 6)
+                                    y = make_float2(tanh_exp(s[2 * i] * k2), tanh_exp(s[2 * i + 1] * k2));
+                                else
+                                    y = tanh_near2(mul2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(k, k)));
                                 s[2 * i] = y.x;
                                 s[2 * i + 1] = y.y;
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 128; ++i) {
-                                const float y = s[i] * k;
-                                s[i] = fabsf(y) <= 1.f ? tanh_near(y) : tanh_far(y);
-                            }
+                            for (int i = 0; i < 128; ++i) s[i] = tanh_exp(s[i] * k2);
                         }
                     }
                     f = (cap > 0.f ? cap : qs) * 1.4426950408889634f;
