@@ -64,16 +64,18 @@ constexpr float kFarRef = 4194304.f;   // 2^22: beyond it products and their rou
 constexpr int kMaxPlan = 256;                    // (sequence, block) pairs of a call that is cut along the cache
 
 struct AttendSmem {
-    uint64_t full[5], empty[5], s_full[2], p_full[2], o_done[2];
+    uint64_t full[5], empty[5], q_full, s_full[2], p_half[2], p_full[2], o_done[2];
     uint32_t tmem;
-    int vis_lo, vis_hi, com_lo, com_hi;          // rows that some query of the CTA sees; that all of them see
+    int4 seen[8];                                // of a warp's query rows: rows that some see, rows that all see
     unsigned skip[kRing];                        // 16-row groups of a tile that lie in bad pages
+    float q_factor[kBlock];                      // 4-bit pages: what the f16 queries' logits are multiplied by
     unsigned bad_v[kRing][4];                    // rows of a tile whose V is not finite (only where not all see them)
-    int any_bad;
+    int flags;                                   // kBadV, kSkip: some tile of this CTA has such rows
     int scan[16];
     int plan_i, plan_at, plan_parts, total;
     unsigned last;
 };
+constexpr int kBadV = 1, kSkip = 2;
 static_assert(attend_smem(true) + sizeof(AttendSmem) <= 227 * 1024 && attend_smem(false) + sizeof(AttendSmem) <= 227 * 1024,
               "shared memory of a CTA");
 
@@ -208,13 +210,13 @@ __device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q, uint32_t k)
             "r"(q + off), "r"(k + off), "n"(kDescHigh), "n"(kIdesc), "r"(ks > 0 ? 1u : 0u));
     }
 }
-// O (+)= P V: eight steps of 16 cache rows.  v: the low word of the tile's first descriptor.
-template <bool E2M1>
+// O (+)= P V over half of a tile's cache rows (HALF): four steps of 16.  v: the low word of the tile's first descriptor.
+template <bool E2M1, int HALF>
 __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, uint32_t accumulate)
 {
     constexpr uint32_t kIdesc = idesc<E2M1>(true);
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
+    for (int ks = 4 * HALF; ks < 4 * HALF + 4; ++ks) {
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
@@ -356,6 +358,7 @@ __device__ __forceinline__ void put_flags(AttendSmem& sm, int page, int t)
     const unsigned bad = bad_groups(page);
     if ((threadIdx.x & 127) == 0) {
         sm.skip[t & (kRing - 1)] = bad;
+        if (bad) atomicOr(&sm.flags, kSkip);
 #pragma unroll
         for (int w = 0; w < 4; ++w) sm.bad_v[(t + 8) & (kRing - 1)][w] = 0u;   // (the tile that had these is long done)
     }
@@ -384,7 +387,7 @@ __device__ __forceinline__ void fill_bf16(const PagedAttendParams& p, AttendSmem
                 sts128(at + 1024 * i, make_uint4(0u, 0u, 0u, 0u));
                 const int row = row0 + 8 * i;
                 atomicOr(&sm.bad_v[t & (kRing - 1)][row >> 5], 1u << (row & 31));
-                sm.any_bad = 1;
+                atomicOr(&sm.flags, kBadV);
             }
         }
         fence_operands();
@@ -506,7 +509,7 @@ __device__ __forceinline__ void fill_e2m1(const PagedAttendParams& p, AttendSmem
                 if (nan) {
                     sc[i] &= ~nan;
                     atomicOr(&sm.bad_v[t & (kRing - 1)][row >> 5], 1u << (row & 31));
-                    sm.any_bad = 1;
+                    atomicOr(&sm.flags, kBadV);
                 }
             }
         }
@@ -692,97 +695,69 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
     const bool two = rows > kSub;
 
     // ---- this thread's row (of the first 256 threads)
+    // token (of the sequence) and head of a row; G divides short numbers by a product
+    const int j_first = blk * kBlock / p.G, r_first = blk * kBlock - j_first * p.G, g_inv = 65536 / p.G + 1;
+    auto row_of = [&](int r, int& head) {
+        const int at = r_first + r, j = (at * g_inv) >> 16;   // (at < 256 + 64)
+        head = h * p.G + at - j * p.G;
+        return j_first + j;
+    };
     const int row = tid;
     const bool live = row < rows;
     int lo = 0, hi = 0, pos = 0;
     int64_t qi = 0;   // token
     int g = 0;
     if (live) {
-        const int r = blk * kBlock + row, j = r / p.G;
-        g = h * p.G + r - j * p.G;
+        const int j = row_of(row, g);
         qi = (int64_t)q0 + j;
         pos = len - all + j;
         const int2 see = token_interval(p, q0, len, all, j);
         lo = see.x;
         hi = see.y;
     }
-    if (tid == 0) {
-        sm.vis_lo = sm.com_hi = 0x7fffffff;
-        sm.vis_hi = sm.com_lo = 0;
-        sm.any_bad = 0;
-        for (int i = 0; i < kRing; ++i)
-            for (int w = 0; w < 4; ++w) sm.bad_v[i][w] = 0u;
-        for (int i = 0; i < slots(E2M1); ++i) {
-            init_barrier(&sm.full[i], 128);
-            init_barrier(&sm.empty[i], 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            init_barrier(&sm.s_full[x], 1);
-            init_barrier(&sm.p_full[x], kSub);
-            init_barrier(&sm.o_done[x], 1);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "r"(512));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    // ---- the queries
-    float qs = p.scale;   // factor of the row's logits
-    if (tid < kBlock) {
-        const uint32_t tile = base + (row >> 7) * kOperand;
-        const uint16_t* src = p.q + qi * p.q_n + (int64_t)g * p.q_h;
-        uint4 x[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            x[k] = live ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
-            x[k] = make_uint4(x[k].x ^ p.flip, x[k].y ^ p.flip, x[k].z ^ p.flip, x[k].w ^ p.flip);
-        }
-        if (E2M1) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
-            }
-            // 2^(14 - exponent of the largest); tiny rows (below 2^-100) are scaled as if they were that large
-            const int ex = min(max((int)(top >> 23) - 127, -100), 127);
-            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            const bool finite = top < 0x7f800000u;
-            auto half = [&](uint32_t w) {
-                const uint32_t v = pack2<true>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-                return finite ? v : 0x7fff7fffu;   // else the row is NaN
-            };
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = make_uint4(half(x[k].x), half(x[k].y), half(x[k].z), half(x[k].w));
-            qs *= __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) sts128(tile + sw128(row & 127, 8 * k, kSub), x[k]);
-        fence_operands();
-    }
-    __syncthreads();
     if (tid < kBlock) {
         const bool sees = live && lo < hi;
-        const int a = __reduce_min_sync(0xffffffffu, sees ? lo : 0x7fffffff), c = __reduce_min_sync(0xffffffffu, sees ? hi : 0x7fffffff);
-        const int d = __reduce_max_sync(0xffffffffu, sees ? lo : 0), e = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
-        if (lane == 0) {
-            atomicMin(&sm.vis_lo, a);
-            atomicMax(&sm.vis_hi, e);
-            atomicMax(&sm.com_lo, d);
-            atomicMin(&sm.com_hi, c);
+        int4 w;
+        w.x = __reduce_min_sync(0xffffffffu, sees ? lo : 0x7fffffff);
+        w.y = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
+        w.z = __reduce_max_sync(0xffffffffu, sees ? lo : 0);
+        w.w = __reduce_min_sync(0xffffffffu, sees ? hi : 0x7fffffff);
+        if (lane == 0) sm.seen[warp] = w;
+    } else if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else if (warp == 13) {
+        if (lane < 2) {
+            init_barrier(&sm.s_full[lane], 1);
+            init_barrier(&sm.p_half[lane], kSub);
+            init_barrier(&sm.p_full[lane], kSub);
+            init_barrier(&sm.o_done[lane], 1);
         }
+        if (lane < slots(E2M1)) {
+            init_barrier(&sm.full[lane], 128);
+            init_barrier(&sm.empty[lane], 1);
+        }
+        if (lane == 31) init_barrier(&sm.q_full, kBlock);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 14) {
+        if (lane == 0) sm.flags = 0;
+        for (int i = lane; i < kRing * 4; i += 32) sm.bad_v[i >> 2][i & 3] = 0u;
     }
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = sm.tmem;
     FillRange r;
-    r.lo = sm.vis_lo;
-    r.hi = sm.vis_hi;
-    r.com_lo = sm.com_lo;
-    r.com_hi = sm.com_hi;
+    r.lo = r.com_hi = 0x7fffffff;
+    r.hi = r.com_lo = 0;
+#pragma unroll
+    for (int w = 0; w < kBlock / 32; ++w) {
+        const int4 v = sm.seen[w];
+        r.lo = min(r.lo, v.x);
+        r.hi = max(r.hi, v.y);
+        r.com_lo = max(r.com_lo, v.z);
+        r.com_hi = min(r.com_hi, v.w);
+    }
     r.ta = r.tb = 0;
     if (r.lo < r.hi) {
         r.ta = r.lo / kKeys;
@@ -815,6 +790,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     ++turn;
                 }
             };
+            wait(&sm.q_full, 0u, p.err, dead);
             wait_full();
             tc_after();
             mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
@@ -831,9 +807,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 next();
                 const bool more = t + 1 < tiles;
                 if (more) wait_full();   // K of the next tile
+                wait(&sm.p_half[0], (unsigned)t & 1u, p.err, dead);
+                tc_after();
+                mma_pv<E2M1, 0>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
                 wait(&sm.p_full[0], (unsigned)t & 1u, p.err, dead);
                 tc_after();
-                mma_pv<E2M1>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
+                mma_pv<E2M1, 1>(tm + col_o(0), tm + col_s(0), v_of(vs), 1u);
                 if (!two) mma_commit(&sm.empty[vs]);
                 if (more) {
                     mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
@@ -843,9 +822,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     mma_commit(&sm.o_done[0]);
                 }
                 if (two) {
+                    wait(&sm.p_half[1], (unsigned)t & 1u, p.err, dead);
+                    tc_after();
+                    mma_pv<E2M1, 0>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
                     wait(&sm.p_full[1], (unsigned)t & 1u, p.err, dead);
                     tc_after();
-                    mma_pv<E2M1>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
+                    mma_pv<E2M1, 1>(tm + col_o(1), tm + col_s(1), v_of(vs), 1u);
                     mma_commit(&sm.empty[vs]);
                     if (more) {
                         mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
@@ -872,6 +854,48 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int x = warp >> 2;
         const bool on = x == 0 || two;
+        float qs = p.scale;   // factor of the row's logits
+        {
+            // The queries, 16 lanes to a row, so that a load takes whole lines: lanes take 16-byte chunk tid % 16 of rows
+            // tid / 16 + 8 i of their subtile.  4-bit pages: as f16 values, whose factor goes to the row's thread.
+            const int chunk = lane & 15, first = (warp & 3) * 2 + (lane >> 4);
+            const uint32_t tile = base + x * kOperand;
+            uint4 q[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                int head;
+                const int r = x * kSub + first + 8 * i, j = row_of(r, head);
+                q[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) q[i] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)q0 + j) * p.q_n + (int64_t)head * p.q_h + 8 * chunk);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                uint4 v = make_uint4(q[i].x ^ p.flip, q[i].y ^ p.flip, q[i].z ^ p.flip, q[i].w ^ p.flip);
+                if (E2M1) {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+#pragma unroll
+                    for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    // 2^(14 - exponent of the largest); tiny rows (below 2^-100) are scaled as if they were that large
+                    const int ex = min(max((int)(top >> 23) - 127, -100), 127);
+                    const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+                    auto half = [&](uint32_t u) {
+                        const uint32_t z = pack2<true>(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xffff0000u) * up);
+                        return top < 0x7f800000u ? z : 0x7fff7fffu;   // else the row is NaN
+                    };
+                    v = make_uint4(half(v.x), half(v.y), half(v.z), half(v.w));
+                    if (chunk == 0) sm.q_factor[x * kSub + first + 8 * i] = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+                }
+                sts128(tile + sw128(first + 8 * i, 8 * chunk, kSub), v);
+            }
+            fence_operands();
+            arrive(&sm.q_full);
+            // (the subtile's threads; without tiles nothing else orders these stores and those of the outputs)
+            if (E2M1 || nt == 0) asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+            if (E2M1) qs *= sm.q_factor[row];
+        }
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         bool dead = false, poison = false, odd = false;
         float m = -INFINITY, l = 0.f;   // reference and sum (in units of 2^kWeightBase)
@@ -881,7 +905,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         const float slope2 = MODE == kBias && live ? p.slope[g] * 1.4426950408889634f : 0.f;
         if (MODE == kPlain) qs *= 1.4426950408889634f;
         auto check = [&](int t) {   // whether the row sees a value of tile t that is not finite (those were left out)
-            if (*(volatile int*)&sm.any_bad == 0) return;
             for (int w = 0; w < 4; ++w) {
                 unsigned bits = *(volatile unsigned*)&sm.bad_v[t & (kRing - 1)][w];
                 while (bits) {
@@ -895,11 +918,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
             for (int t = 0; t < nt; ++t) {
                 wait(&sm.s_full[x], (unsigned)t & 1u, p.err, dead);
                 tc_after();
+                const int flags = *(volatile int*)&sm.flags;
                 float s[128];
                 tmem_row(lanes + col_s(x), s);
                 const int tile = r.ta + t, j0 = tile * kKeys;
-                if (t > 0) check(tile - 1);
-                const unsigned skip = *(volatile unsigned*)&sm.skip[tile & (kRing - 1)];
+                unsigned skip = 0;
+                if (flags) {
+                    if (t > 0 && (flags & kBadV)) check(tile - 1);
+                    skip = *(volatile unsigned*)&sm.skip[tile & (kRing - 1)];
+                }
                 const int a = my_lo - j0, e = my_hi - j0;   // the row sees keys a <= k < e of the tile
                 const bool whole = a <= 0 && e >= kKeys;
                 // which keys each row sees, as bits; rows that see all of them take no masks
@@ -922,11 +949,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         tmem_put32(lanes + col_s(x) + 32, zero);
                         tmem_wait_st();
                         tc_before();
+                        arrive(&sm.p_half[x]);
                         arrive(&sm.p_full[x]);
                         continue;
                     }
                 }
-                float f = MODE == kPlain ? qs : 1.f;   // factor from s to base-2 logits
+                float f = MODE == kPlain ? qs : 1.f, off = 0.f;   // from s to base-2 logits: s * f + off
                 if (MODE != kPlain) {
                     if (cap > 0.f) {
                         // Where no logit is past the cap, the polynomial (10 steps of the fp32 units for two at a time)
@@ -958,8 +986,20 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     f = (cap > 0.f ? cap : qs) * 1.4426950408889634f;
                     if (MODE == kBias) {
                         const float d0 = (float)(pos - j0);
+                        if (!__any_sync(0xffffffffu, live && pos < j0 + kKeys - 1)) {
+                            // all keys lie before the queries: their bias grows by slope from one to the next
+                            off = -slope2 * d0;
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) s[i] = fmaf(fabsf(d0 - (float)i), -slope2, s[i] * f);
+                            for (int i = 0; i < 64; ++i) {
+                                const float2 y = fma2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(f, f),
+                                                      mul2(make_float2(2 * i, 2 * i + 1), make_float2(slope2, slope2)));
+                                s[2 * i] = y.x;
+                                s[2 * i + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) s[i] = fmaf(fabsf(d0 - (float)i), -slope2, s[i] * f);
+                        }
                         f = 1.f;
                     }
                 }
@@ -979,6 +1019,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 }
                 // (factors are not negative; a hidden logit stays -inf also with a factor of 0)
                 mt = mt == -INFINITY ? mt : __fmul_rn(mt, f);
+                if (MODE == kBias) mt = __fadd_rn(mt, off);
                 const bool grow = mt > m + kMaxSlack;   // also when there is none yet and the row sees something
                 if (__any_sync(0xffffffffu, grow)) {
                     const float mnew = grow ? mt : m;
@@ -999,7 +1040,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     // a far reference, or hidden logits beside a factor of 0, take rounded products one by one
                     odd = __any_sync(0xffffffffu, fabsf(m) > kFarRef && m != -INFINITY);
                 }
-                const float bias = (m == -INFINITY ? 0.f : -m) + kWeightBase<E2M1>;
+                const float ref = (m == -INFINITY ? 0.f : -m) + (MODE == kBias ? off : 0.f), bias = ref + kWeightBase<E2M1>;
                 uint32_t w[64];
                 float2 l2 = make_float2(0.f, 0.f), l3 = make_float2(0.f, 0.f);
                 if (!odd && !(masked && f == 0.f)) {
@@ -1014,6 +1055,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                             l2 = add2(l2, pp);
                         w[k] = pack2<E2M1>(pp.x, pp.y);
                         if (k == 31) tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
+                        if (k == 39) {   // half of P is there by now: its products may begin
+                            tmem_wait_st();
+                            tc_before();
+                            arrive(&sm.p_half[x]);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -1023,12 +1069,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         for (int u = 0; u < 2; ++u) {
                             const float v = s[2 * k + u];
                             y[u] = v == -INFINITY ? 0.f
-                                                  : ex2(__fadd_rn(__fadd_rn(__fmul_rn(v, f), m == -INFINITY ? 0.f : -m), kWeightBase<E2M1>));
+                                                  : ex2(__fadd_rn(__fadd_rn(__fmul_rn(v, f), ref), kWeightBase<E2M1>));
                         }
                         l2 = add2(l2, make_float2(y[0], y[1]));
                         w[k] = pack2<E2M1>(y[0], y[1]);
                     }
                     tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
+                    tmem_wait_st();
+                    tc_before();
+                    arrive(&sm.p_half[x]);
                 }
                 l2 = add2(l2, l3);
                 l += l2.x + l2.y;
@@ -1040,45 +1089,67 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
             if (nt > 0) {
                 wait(&sm.o_done[x], 0u, p.err, dead);
                 tc_after();
-                check(r.tb - 1);
+                if (*(volatile int*)&sm.flags & kBadV) check(r.tb - 1);
             }
             const bool none = l == 0.f;
+            // Rows leave through the query tile, which nothing reads any more, so that a store takes whole lines.
+            const uint32_t stage = base + x * kOperand;
+            const int chunk = lane & 15, first = (warp & 3) * 32 + (lane >> 4);
             if (n_parts == 1) {
                 const float z = none ? 0.f : p.c.v_mul / l;
-                uint16_t* out = p.out + (qi * p.Hq + g) * kHeadDim;
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float v[32];
                     if (nt > 0) tmem_ld32(lanes + col_o(x) + 32 * c, v);
-                    if (live) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t y[4];
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t y[4];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float v0 = v[8 * k + 2 * u] * z, v1 = v[8 * k + 2 * u + 1] * z;
-                                y[u] = poison ? 0x7fff7fffu : (none ? 0u : pack2<false>(v0, v1));
-                            }
-                            *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int u = 0; u < 4; ++u) {
+                            const float v0 = v[8 * k + 2 * u] * z, v1 = v[8 * k + 2 * u + 1] * z;
+                            y[u] = poison ? 0x7fff7fffu : (none ? 0u : pack2<false>(v0, v1));
                         }
+                        sts128(stage + sw128(row & 127, 32 * c + 8 * k, kSub), make_uint4(y[0], y[1], y[2], y[3]));
                     }
                 }
                 if (live && p.lse)
                     p.lse[qi * p.Hq + g] = none ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kWeightBase<E2M1>) * 0.6931471805599453f;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    int head;
+                    const int r = first + 2 * i, j = row_of(x * kSub + r, head);
+                    const uint4 y = lds128(stage + sw128(r, 8 * chunk, kSub));
+                    if (x * kSub + r < rows)
+                        *reinterpret_cast<uint4*>(p.out + (((int64_t)q0 + j) * p.Hq + head) * kHeadDim + 8 * chunk) = y;
+                }
             } else {
                 const int64_t at = (int64_t)blockIdx.x * p.part_rows;
-                float* o = p.part + (at + row) * kHeadDim;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    if (nt > 0) tmem_ld32(lanes + col_o(x) + 32 * c, v);
-                    if (!live) continue;
+                for (int c = 0; c < 2; ++c) {   // 64 dimensions (256 bytes of a row) at a time
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 y = poison ? make_float4(NAN, NAN, NAN, NAN)
-                                                : (none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
-                        *reinterpret_cast<float4*>(o + 32 * c + k) = y;
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        float v[32];
+                        if (nt > 0) tmem_ld32(lanes + col_o(x) + 64 * c + 32 * k2, v);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint4 y;
+                            y.x = __float_as_uint(v[4 * k]), y.y = __float_as_uint(v[4 * k + 1]);
+                            y.z = __float_as_uint(v[4 * k + 2]), y.w = __float_as_uint(v[4 * k + 3]);
+                            if (none) y = make_uint4(0u, 0u, 0u, 0u);
+                            if (poison) y = make_uint4(0x7fffffffu, 0x7fffffffu, 0x7fffffffu, 0x7fffffffu);
+                            sts128(stage + sw128(row & 127, 64 * k2 + 8 * k, kSub), y);
+                        }
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = first + 2 * i;
+                        const uint4 y = lds128(stage + sw128(r, 8 * chunk, kSub));
+                        if (x * kSub + r < rows)
+                            *reinterpret_cast<uint4*>(p.part + (at + x * kSub + r) * kHeadDim + 64 * c + 4 * chunk) = y;
+                    }
+                    __syncwarp();
                 }
                 if (live) {
                     p.part_ml[2 * (at + row)] = m == -INFINITY && !none ? 0.f : m;   // (NaN logits leave no reference, but show)
@@ -1125,7 +1196,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         }
         const bool none = z == 0.f;
         const float y = none ? 0.f : p.c.v_mul / z;
-        const int rr = blk * kBlock + w, j = rr / p.G, head = h * p.G + rr - j * p.G;
+        int head;
+        const int j = row_of(w, head);
         const int64_t to = ((int64_t)q0 + j) * p.Hq + head;
         *reinterpret_cast<uint2*>(p.out + to * kHeadDim + 4 * lane) =
             none ? make_uint2(0u, 0u) : make_uint2(pack2<false>(acc.x * y, acc.y * y), pack2<false>(acc.z * y, acc.w * y));
