@@ -44,7 +44,7 @@ __host__ __device__ constexpr int attend_smem(bool e2m1)
 {
     return 2 * kOperand + slots(e2m1) * kOperand + (e2m1 ? kRaw * kRawTile : 0) + 1024;
 }
-constexpr int kLag = 3;                          // bf16: tiles whose copies are under way
+constexpr int kLag = 1;                          // bf16: tiles whose copies are under way
 // Registers a thread of the softmax, the fillers and the issuing warp; the launch's 128 a thread cover their sum.
 constexpr int kRegsSoftmax = 184, kRegsFill = 88, kRegsIssue = 56;
 static_assert(2 * kRegsSoftmax + kRegsFill + kRegsIssue <= 4 * 128, "a split above the launch's registers never starts");
@@ -64,7 +64,7 @@ constexpr float kFarRef = 4194304.f;   // 2^22: beyond it products and their rou
 constexpr int kMaxPlan = 256;                    // (sequence, block) pairs of a call that is cut along the cache
 
 struct AttendSmem {
-    uint64_t full[5], empty[5], q_full, s_full[2], p_half[2], p_full[2], o_done[2];
+    uint64_t full[5], empty[5], q_full, s_full[2], p_full[2], o_done[2];
     uint32_t tmem;
     int4 seen[8];                                // of a warp's query rows: rows that some see, rows that all see
     unsigned skip[kRing];                        // 16-row groups of a tile that lie in bad pages
@@ -143,21 +143,11 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// tanh(y) = 1 - 2 / (exp(2y) + 1), of x = 2 y log2(e): off by 2^-21 at most (not of itself: of 1).
-__device__ __forceinline__ float tanh_exp(float x)
+__device__ __forceinline__ float rcp(float x)
 {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(x) + 1.f));
-    return fmaf(-2.f, r, 1.f);
-}
-// tanh_near of two values.
-__device__ __forceinline__ float2 tanh_near2(float2 y)
-{
-    const float2 u = mul2(y, y);
-    float2 q = make_float2(kTanh[6], kTanh[6]);
-#pragma unroll
-    for (int i = 5; i >= 0; --i) q = fma2(q, u, make_float2(kTanh[i], kTanh[i]));
-    return fma2(mul2(y, u), q, y);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -210,13 +200,13 @@ __device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q, uint32_t k)
             "r"(q + off), "r"(k + off), "n"(kDescHigh), "n"(kIdesc), "r"(ks > 0 ? 1u : 0u));
     }
 }
-// O (+)= P V over half of a tile's cache rows (HALF): four steps of 16.  v: the low word of the tile's first descriptor.
-template <bool E2M1, int HALF>
+// O (+)= P V: eight steps of 16 cache rows.  v: the low word of the tile's first descriptor.
+template <bool E2M1>
 __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, uint32_t accumulate)
 {
     constexpr uint32_t kIdesc = idesc<E2M1>(true);
 #pragma unroll
-    for (int ks = 4 * HALF; ks < 4 * HALF + 4; ++ks) {
+    for (int ks = 0; ks < 8; ++ks) {
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
@@ -729,7 +719,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
     } else if (warp == 13) {
         if (lane < 2) {
             init_barrier(&sm.s_full[lane], 1);
-            init_barrier(&sm.p_half[lane], kSub);
             init_barrier(&sm.p_full[lane], kSub);
             init_barrier(&sm.o_done[lane], 1);
         }
@@ -807,12 +796,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 next();
                 const bool more = t + 1 < tiles;
                 if (more) wait_full();   // K of the next tile
-                wait(&sm.p_half[0], (unsigned)t & 1u, p.err, dead);
-                tc_after();
-                mma_pv<E2M1, 0>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
                 wait(&sm.p_full[0], (unsigned)t & 1u, p.err, dead);
                 tc_after();
-                mma_pv<E2M1, 1>(tm + col_o(0), tm + col_s(0), v_of(vs), 1u);
+                mma_pv<E2M1>(tm + col_o(0), tm + col_s(0), v_of(vs), t > 0 ? 1u : 0u);
                 if (!two) mma_commit(&sm.empty[vs]);
                 if (more) {
                     mma_qk<E2M1>(tm + col_s(0), q0d, k_of(slot));
@@ -822,12 +808,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     mma_commit(&sm.o_done[0]);
                 }
                 if (two) {
-                    wait(&sm.p_half[1], (unsigned)t & 1u, p.err, dead);
-                    tc_after();
-                    mma_pv<E2M1, 0>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
                     wait(&sm.p_full[1], (unsigned)t & 1u, p.err, dead);
                     tc_after();
-                    mma_pv<E2M1, 1>(tm + col_o(1), tm + col_s(1), v_of(vs), 1u);
+                    mma_pv<E2M1>(tm + col_o(1), tm + col_s(1), v_of(vs), t > 0 ? 1u : 0u);
                     mma_commit(&sm.empty[vs]);
                     if (more) {
                         mma_qk<E2M1>(tm + col_s(1), q0d + (kOperand >> 4), k_of(slot));
@@ -949,7 +932,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         tmem_put32(lanes + col_s(x) + 32, zero);
                         tmem_wait_st();
                         tc_before();
-                        arrive(&sm.p_half[x]);
                         arrive(&sm.p_full[x]);
                         continue;
                     }
@@ -957,9 +939,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 float f = MODE == kPlain ? qs : 1.f, off = 0.f;   // from s to base-2 logits: s * f + off
                 if (MODE != kPlain) {
                     if (cap > 0.f) {
-                        // Where no logit is past the cap, the polynomial (10 steps of the fp32 units for two at a time)
-                        // takes five of eight pairs, the exponential (3 steps, and 12 of the function unit for one) the
-                        // others, so that both are busy alike; else the exponential takes all.
+                        // tanh(y) = y + y^3 Q(y^2) (10 steps of the fp32 units for two values) where no logit is past the
+                        // cap, and beside it tanh(y) = 1 - 2 / (exp(2y) + 1), off by 2^-21 at most (of 1, not of itself; 3
+                        // steps, and 12 of the function unit for one value), so that both units are busy; else the latter
+                        // alone.
                         const float k = qs * icap, k2 = k * 2.885390081777927f;
                         float top = 0.f;
 #pragma unroll
@@ -969,18 +952,39 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         }
                         if (!__any_sync(0xffffffffu, !(top * k <= 1.f))) {
 #pragma unroll
-                            for (int i = 0; i < 64; ++i) {
-                                float2 y;
-                                if (i % 8 == 1 || i % 8 == 4 || i % 8 == 6)
-                                    y = make_float2(tanh_exp(s[2 * i] * k2), tanh_exp(s[2 * i + 1] * k2));
-                                else
-                                    y = tanh_near2(mul2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(k, k)));
-                                s[2 * i] = y.x;
-                                s[2 * i + 1] = y.y;
+                            for (int i = 0; i < 128; i += 16) {   // side by side: ten values by one, six by the other
+                                float2 y[5], u[5], q[5];
+                                float z[6];
+#pragma unroll
+                                for (int e = 0; e < 5; ++e) {
+                                    y[e] = mul2(make_float2(s[i + 2 * e], s[i + 2 * e + 1]), make_float2(k, k));
+                                    u[e] = mul2(y[e], y[e]);
+                                    q[e] = make_float2(kTanh[6], kTanh[6]);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 6; ++e) z[e] = ex2(s[i + 10 + e] * k2) + 1.f;
+#pragma unroll
+                                for (int c = 5; c >= 0; --c) {
+#pragma unroll
+                                    for (int e = 0; e < 5; ++e) q[e] = fma2(q[e], u[e], make_float2(kTanh[c], kTanh[c]));
+                                    s[i + 10 + c] = fmaf(-2.f, rcp(z[c]), 1.f);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 5; ++e) {
+                                    const float2 r = fma2(mul2(y[e], u[e]), q[e], y[e]);
+                                    s[i + 2 * e] = r.x;
+                                    s[i + 2 * e + 1] = r.y;
+                                }
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 128; ++i) s[i] = tanh_exp(s[i] * k2);
+                            for (int i = 0; i < 128; i += 8) {
+                                float z[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) z[e] = ex2(s[i + e] * k2) + 1.f;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) s[i + e] = fmaf(-2.f, rcp(z[e]), 1.f);
+                            }
                         }
                     }
                     f = (cap > 0.f ? cap : qs) * 1.4426950408889634f;
@@ -1046,20 +1050,21 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 if (!odd && !(masked && f == 0.f)) {
                     const float2 ff = make_float2(f, f), bb = make_float2(bias, bias);
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        const float2 y = fma2(make_float2(s[2 * k], s[2 * k + 1]), ff, bb);
-                        const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-                        if (k & 1)
-                            l3 = add2(l3, pp);
-                        else
-                            l2 = add2(l2, pp);
-                        w[k] = pack2<E2M1>(pp.x, pp.y);
-                        if (k == 31) tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
-                        if (k == 39) {   // half of P is there by now: its products may begin
-                            tmem_wait_st();
-                            tc_before();
-                            arrive(&sm.p_half[x]);
+                    for (int k0 = 0; k0 < 64; k0 += 4) {   // eight values side by side
+                        float2 y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = fma2(make_float2(s[2 * (k0 + e)], s[2 * (k0 + e) + 1]), ff, bb);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (e & 1)
+                                l3 = add2(l3, y[e]);
+                            else
+                                l2 = add2(l2, y[e]);
+                            w[k0 + e] = pack2<E2M1>(y[e].x, y[e].y);
                         }
+                        if (k0 == 28) tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
                     }
                 } else {
 #pragma unroll
@@ -1075,9 +1080,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         w[k] = pack2<E2M1>(y[0], y[1]);
                     }
                     tmem_put32(lanes + col_s(x), reinterpret_cast<uint32_t(&)[32]>(w[0]));
-                    tmem_wait_st();
-                    tc_before();
-                    arrive(&sm.p_half[x]);
                 }
                 l2 = add2(l2, l3);
                 l += l2.x + l2.y;
