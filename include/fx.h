@@ -516,7 +516,7 @@ FX_API fx_status fx_paged_append_axes(const fx_paged_desc* cache, const fx_paged
  * and dst->len[b] = k + max(0, len[b] - tail_lo[b]) is WRITTEN (k without tail_lo).  idx: int32 [B, Hkv, k], tail_lo: int32
  * [B] or NULL (no tail), both on the device.  An idx entry outside [0, len[b]) sets FX_DEVERR_INDEX and its row is not
  * written; a tail_lo below 0 sets FX_DEVERR_LEN and counts as 0; more rows than dst has room for set FX_DEVERR_CAPACITY and
- * are cut (dst->len too).
+ * are cut (dst->len too).  dst->len overlaps nothing that the call reads.
  * src and dst have the same format, exponents, B and Hkv, and tables and lengths of their own; pool and page_rows may be the
  * same or not.  The pages that dst's rows go to hold no row that src reads, and no page twice.  No workspace.
  */
@@ -635,8 +635,9 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
  *             the first max_new are done (FX_DEVERR_OFFSETS).  Tokens of no sequence keep their out and lse.
  *   first, last   int32 [n] on the device or NULL; any values: the interval is cut to [0, len[b])
  *   slope     fp32 [Hq] on the device or NULL (0);   cap 0 (none) or from 2^-64 to 2^64;   G <= 64
- *   q         bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h;   out bf16 [n, Hq, 128], lse fp32 [n, Hq], contiguous
- *   max_new   host: tokens of one sequence, at most (G*max_new <= 2^30, n*Hq < 2^31)
+ *   q         bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h;   out bf16 [n, Hq, 128], lse fp32 [n, Hq], contiguous;
+ *             they overlap nothing that the call reads
+ *   max_new   host: tokens of one sequence, at most (G*max_new <= 2^30, n <= 2^30, n*Hq < 2^31)
  * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes.
  */
 typedef struct {

@@ -1120,9 +1120,10 @@ fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void
     p.last = q->last;
     p.slope = q->slope;
     p.n = q->n;
-    p.window = q->window;
+    p.window = min(q->window, 1 << 30);
     p.cap = q->cap;
     p.icap = q->cap > 0.f ? 1.f / q->cap : 0.f;
+    p.cap2 = q->cap > 0.f ? q->cap * 1.4426950408889634f : 1.f;
     p.out16 = q->out;
     p.lse = q->lse;
     p.counters = static_cast<unsigned*>(ws);
@@ -1259,7 +1260,7 @@ fx_status fx_paged_compact(const fx_paged_desc* src, const fx_paged_desc* dst, c
     if ((st = check_flags(flags)) != FX_OK) return st;
     if (src->format != dst->format || src->B != dst->B || src->Hkv != dst->Hkv || src->k_exp != dst->k_exp || src->v_exp != dst->v_exp)
         return fail(FX_ERR_INVALID_ARG, "src and dst must have one format (and exponents), B and Hkv");
-    if (src->len == dst->len || src->table == dst->table)
+    if (src->len == dst->len || src->table == dst->table || (tail_lo && tail_lo == dst->len))
         return fail(FX_ERR_INVALID_ARG, "dst needs a page table and lengths of its own");
     if (!pool_apart(dst)) return fail(FX_ERR_INVALID_ARG, "dst: the pool's rows share memory, so none can be written");
     if (k < 0 || (k > 0 && !idx)) return fail(FX_ERR_INVALID_ARG, "need k >= 0 and idx when k > 0");
@@ -1423,7 +1424,7 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     if (q->n == 0 || q->max_new == 0) return FX_OK;
     if (!q->q || !aligned16(q->q)) return fail(FX_ERR_INVALID_ARG, "q must be non-NULL and 16-byte aligned");
     if (!q->out || !aligned16(q->out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
-    if ((int64_t)G * q->max_new > (1ll << 30) || (int64_t)q->n * q->Hq > 0x7fffffff)
+    if ((int64_t)G * q->max_new > (1ll << 30) || q->n > (1 << 30) || (int64_t)q->n * q->Hq > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "queries: too many rows");
     if (G * q->max_new <= kMaxRows) return attend_few(cache, q, ws, ws_bytes, flags, stream);
     const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, sm_count_or_default());
@@ -1442,7 +1443,7 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     p.Hq = q->Hq;
     p.G = G;
     p.max_new = q->max_new;
-    p.window = q->window;
+    p.window = min(q->window, 1 << 30);   // (positions lie between -2^30 and 2^30)
     p.scale = fabsf(q->scale) * p.c.k_mul;
     p.flip = q->scale < 0.f ? 0x80008000u : 0u;
     p.cap = q->cap;

@@ -329,7 +329,7 @@ struct PagedAttnParams {
     const int32_t* last;
     const float* slope;
     int n, window;
-    float cap, icap;          // icap = 1 / cap
+    float cap, icap, cap2;    // icap = 1 / cap; cap2: from a tanh to a base-2 logit (1 without a cap)
     uint16_t* out16;          // [n, Hq, 128]
 };
 

@@ -61,9 +61,9 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// cap tanh(x / cap), with icap = 1 / cap.  Up to x = cap, where capped scores mostly lie, tanh(y) = y + y^3 Q(y^2) with Q
-// interpolated at Chebyshev nodes (off by 2^-23.4 of itself in fp32, and no function unit is asked); beyond,
-// tanh(y) = 1 - 2 / (exp(2y) + 1), whose subtrahend is below 1/4.
+// The tanh of capped scores.  Up to 1, where they mostly lie, tanh(y) = y + y^3 Q(y^2) with Q interpolated at Chebyshev nodes
+// (off by 2^-23.4 of itself in fp32, and no function unit is asked); beyond, tanh(y) = 1 - 2 / (exp(2y) + 1), whose
+// subtrahend is below 1/4.
 __device__ constexpr float kTanh[7] = {-0.3333333134651184f,  0.1333312839269638f,    -0.053934790194034576f, 0.02166011556982994f,
                                        -0.008218921720981598f, 0.0025104593951255083f, -0.00042069549090228975f};
 __device__ __forceinline__ float tanh_near(float y)
@@ -81,12 +81,6 @@ __device__ __forceinline__ float tanh_far(float y)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
     return copysignf(1.f - __fdividef(2.f, e + 1.f), y);
 }
-__device__ __forceinline__ float soft_cap(float x, float cap, float icap)
-{
-    const float y = x * icap;
-    return cap * (fabsf(y) <= 1.f ? tanh_near(y) : tanh_far(y));
-}
-
 // Page number of row t of sequence b (0 <= t < cap), or -1 (flagged) for a bad table entry.
 __device__ __forceinline__ int paged_page(const PagedCache& c, int b, int t, unsigned* err)
 {

@@ -747,26 +747,48 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, const Seq& q
 // SHAPED: what fx_paged_attend puts on the logits.
 template <int NT>
 struct Shaping {
-    float f[NT][2];       // factor of the logits of rows 2t, 2t + 1 (of each N tile), before the cap
+    float f[NT][2];       // to the tanh's argument (without a cap: to base-2 logits) of rows 2t, 2t + 1 of each N tile
     float at[NT][2];      // the rows' positions
     float slope[NT][2];   // base 2
     const int2* see;      // shared memory: what the query positions see
 };
-// Logits of U tiles whose first row is `first`, as logits() gives them, to base-2 logits.
+// Logits of U tiles whose first row is `first`, as logits() gives them: under the cap, and with their bias by distance as
+// base-2 logits (without one, the factor of a capped logit, p.cap2, is left to weights()).
 template <int U, int NT>
 __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Shaping<NT>& sh, float (&s)[U * NT][4], int first)
 {
-    const int g = (threadIdx.x & 31) >> 2;
-    const float row = (float)(first + g);
 #pragma unroll
     for (int m = 0; m < U * NT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float x = s[m][e] * sh.f[m % NT][e & 1];
-            if (p.cap > 0.f) x = soft_cap(x, p.cap, p.icap);
-            s[m][e] = fmaf(fabsf(sh.at[m % NT][e & 1] - row - (float)(16 * (m / NT) + 8 * (e >> 1))), -sh.slope[m % NT][e & 1],
-                           x * 1.4426950408889634f);
+        for (int e = 0; e < 4; ++e) s[m][e] *= sh.f[m % NT][e & 1];
+    if (p.cap > 0.f) {
+        float top = 0.f;
+#pragma unroll
+        for (int m = 0; m < U * NT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(s[m][e]));
+        if (!__any_sync(kFull, top > 1.f)) {   // (a NaN stays one)
+#pragma unroll
+            for (int m = 0; m < U * NT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[m][e] = tanh_near(s[m][e]);
+        } else {
+#pragma unroll
+            for (int m = 0; m < U * NT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[m][e] = fabsf(s[m][e]) <= 1.f ? tanh_near(s[m][e]) : tanh_far(s[m][e]);
         }
+    }
+    if (p.slope) {
+        const float row = (float)(first + ((threadIdx.x & 31) >> 2));
+#pragma unroll
+        for (int m = 0; m < U * NT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float far = sh.at[m % NT][e & 1] - row;   // of the unit's first row
+                s[m][e] = fmaf(fabsf(far - (float)(16 * (m / NT) + 8 * (e >> 1))), -sh.slope[m % NT][e & 1], s[m][e] * p.cap2);
+            }
+    }
 }
 
 template <bool E2M1, int NT, bool DUP>
@@ -1425,8 +1447,8 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
                 if (kSharedQ) a.rs[n][e] = p.qscale * sm_f[8 * n + 2 * t + e];
                 if (SHAPED) {
                     const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
-                    sh.f[n][e] = a.rs[n][e];
-                    a.rs[n][e] = 1.f;
+                    sh.f[n][e] = a.rs[n][e] * (p.cap > 0.f ? p.icap : 1.4426950408889634f);
+                    a.rs[n][e] = p.slope ? 1.f : p.cap2;
                     sh.at[n][e] = (float)(seq.pos0 + query_pos(p, r));
                     sh.slope[n][e] = p.slope && r < p.R ? p.slope[h * p.G + r / p.Mq] * 1.4426950408889634f : 0.f;
                 }

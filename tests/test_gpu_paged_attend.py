@@ -388,3 +388,37 @@ def test_attend_long_rows_in_parts(fx, fmt):
         dk = {k: cu(v, torch.int32 if k == "first" else torch.float32) if k in ("first", "slope") else v for k, v in kw.items()}
         got = fx.fx_paged_attend(dev, t, st, max_new=70, want_lse=True, **dk)
         check(c, got, attend_ref(c, q, start, D ** -0.5, **kw))
+
+
+def test_attend_far_pages_and_wide_windows(fx):
+    """Pages past 2^32 bytes of the pool, for a step and for a prompt; a window as wide as an int holds."""
+    pages = (5 << 30) // (16 * 256)
+    k, v = (torch.empty(pages, 1, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c = pr.Cache("bf16", [150, 40], 1, 16, seed=2)
+    used = np.concatenate([c.table[b, :-(-n // 16)] for b, n in enumerate(c.lens)])
+    far = {int(p): pages - 1 - 7 * i for i, p in enumerate(used)}
+    table = torch.full((2, c.max_pages), -1, dtype=torch.int32)
+    for b, n in enumerate(c.lens):
+        for j in range(-(-n // 16)):
+            at = far[int(c.table[b, j])]
+            table[b, j] = at
+            for t, p in ((k, c.pool[0]), (v, c.pool[1])):
+                t[at] = cu(p[c.table[b, j]], torch.bfloat16)
+    dev = fx.PagedKV(k, v, table.cuda(), cu(c.lens, torch.int32))
+    for news in ([1, 1], [150, 40], [90, 3]):
+        g = np.random.default_rng(3)
+        start = np.concatenate(([0], np.cumsum(news)))
+        q = pr.bf16(2.0 * g.standard_normal((start[-1], 2, D)))
+        for window in (0, (1 << 31) - 1):
+            got = fx.fx_paged_attend(dev, cu(q, torch.bfloat16), cu(start, torch.int32), max_new=max(news), window=window,
+                                     want_lse=True)
+            check(c, got, attend_ref(c, q, start, D ** -0.5))
+    # rows of those pages copied, and moved, where 32 bits do not reach
+    ids = torch.tensor(sorted(far.values()), dtype=torch.int32, device="cuda")
+    fx.fx_paged_copy(dev, ids, ids - 1)
+    assert torch.equal(k[ids.long()], k[ids.long() - 1]) and torch.equal(v[ids.long()], v[ids.long() - 1])
+    to = fx.PagedKV(k, v, (table - 2).clamp(min=-1).cuda(), torch.zeros(2, dtype=torch.int32, device="cuda"))
+    fx.fx_paged_compact(dev, to, tail_lo=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert to.length.tolist() == c.lens
+    for a, b in zip(fx.fx_paged_gather(dev, 40), fx.fx_paged_gather(to, 40)):
+        assert torch.equal(a, b)

@@ -51,6 +51,7 @@ def test_attend_refusals(lib):  # noqa: F811
                              (dict(stride_h=-8), 1, b"strides"), (dict(q=None), 1, b"q must"), (dict(q=264), 1, b"q must"),
                              (dict(out=None), 1, b"out must"), (dict(out=520), 1, b"out must"),
                              (dict(max_new=(1 << 30) + 1), 2, b"too many"), (dict(n=1 << 29), 2, b"too many"),
+                             (dict(n=(1 << 30) + 1, Hq=4, cache=desc(Hkv=1)), 2, b"too many"),
                              (dict(max_new=1 << 25), 2, b"too many"),
                              (dict(ws=None), 3, b"workspace"), (dict(ws_bytes=64), 3, b"workspace"),
                              (dict(ws_bytes=64, max_new=300), 3, b"workspace"), (dict(flags=4), 1, b"flags")):
@@ -88,7 +89,7 @@ def test_compact_and_copy_refusals(lib):  # noqa: F811
 
     def call(idx=None, k=0, lo=256, flags=0, dst=None, **kw):
         return lib.fx_paged_compact(ctypes.byref(src), ctypes.byref(dst or desc(**(other | kw))), idx, k, lo, flags, None)
-    for kw, status, word in ((dict(len=src.len), 1, b"of its own"), (dict(table=src.table), 1, b"of its own"),
+    for kw, status, word in ((dict(len=src.len), 1, b"of its own"), (dict(lo=other["len"]), 1, b"of its own"), (dict(table=src.table), 1, b"of its own"),
                              (dict(B=1), 1, b"one format"), (dict(Hkv=1), 1, b"one format"), (dict(k_exp=1), 1, b"one format"),
                              (dict(v_exp=-1), 1, b"one format"), (dict(dst=desc(**(other | BF16))), 1, b"one format"),
                              (dict(stride_t=0), 1, b"share memory"), (dict(scale_stride_h=0), 1, b"share memory"),
