@@ -1131,8 +1131,11 @@ fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void
     p.err = ds->err;
     const bool pdl = (flags & FX_LAUNCH_PDL) != 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->format == FX_PAGED_E2M1 ? launch_paged_attend_few_e2m1(p, sms, pdl, s)
-                                                         : launch_paged_attend_few_bf16(p, sms, pdl, s);
+    cudaError_t e;
+    if (cache->format == FX_PAGED_E2M1)
+        e = p.cap > 0.f ? launch_paged_attend_few_e2m1_cap(p, sms, pdl, s) : launch_paged_attend_few_e2m1_open(p, sms, pdl, s);
+    else
+        e = p.cap > 0.f ? launch_paged_attend_few_bf16_cap(p, sms, pdl, s) : launch_paged_attend_few_bf16_open(p, sms, pdl, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged attend launch");
     return FX_OK;
 }

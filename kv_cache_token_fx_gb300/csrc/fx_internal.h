@@ -383,8 +383,10 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_coun
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);
 // fx_paged_attend with up to kMaxRows query rows a (sequence, KV head): kernels of fx_paged_decode's kind.
-cudaError_t launch_paged_attend_few_bf16(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
-cudaError_t launch_paged_attend_few_e2m1(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_few_bf16_open(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_few_bf16_cap(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_few_e2m1_open(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_few_e2m1_cap(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s);
 PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count);
 size_t paged_attend_workspace_bytes(const PagedAttendCut& c);

@@ -26,7 +26,7 @@ size_t paged_decode_workspace_bytes(int R, int sm_count)
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)
 {
-    return e2m1 ? launch_decode_e2m1<false>(p, sm_count, pdl, s) : launch_decode_bf16<false>(p, sm_count, pdl, s);
+    return e2m1 ? launch_decode_e2m1<0>(p, sm_count, pdl, s) : launch_decode_bf16<0>(p, sm_count, pdl, s);
 }
 
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s)

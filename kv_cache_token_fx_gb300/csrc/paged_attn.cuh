@@ -218,7 +218,7 @@ __device__ __forceinline__ void shaped_sequence(const PagedAttnParams& p, int b,
     q.idx = nullptr;
 }
 // Tiles of sequence b (at least one: an empty sequence's tile holds no valid row, and its output is written).
-template <bool SHAPED>
+template <int SHAPED>
 __device__ __forceinline__ Seq sequence(const PagedAttnParams& p, int b, bool report)
 {
     Seq q;
@@ -272,7 +272,7 @@ struct Slot {
 // Tail: the lanes hold the next 32 page numbers, and inside a page the lane's addresses only advance; a pair of
 // whole tiles of one page is ten copies and a few additions.  List: the lanes hold the rows of two tiles (lane
 // L: entry L of them), looked up a batch ahead, their positions another batch ahead.
-template <bool E2M1, bool WITH_V, int U, bool SHAPED = false>
+template <bool E2M1, bool WITH_V, int U, int SHAPED = 0>
 struct Feeder {
     using S = Slot<E2M1, WITH_V, U>;
     const PagedAttnParams& p;
@@ -720,7 +720,7 @@ __device__ __forceinline__ float4 join_row(const float* sm_o, int pitch, const f
 }
 
 // Writes one query row's output (the lane's dimensions 4 lane .. + 3) and its lse.
-template <bool E2M1, bool SHAPED>
+template <bool E2M1, int SHAPED>
 __device__ __forceinline__ void write_row(const PagedAttnParams& p, const Seq& q, int b, int h, int r, float4 acc, float m, float z)
 {
     const int lane = threadIdx.x & 31;
@@ -744,24 +744,38 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, const Seq& q
 }
 
 // The query rows of one warp and what it has summed for them.
-// SHAPED: what fx_paged_attend puts on the logits.
-template <int NT>
+// SHAPED: what fx_paged_attend puts on the logits.  It lies in shared memory and is read for every unit: registers are what
+// 4-bit rows have least of.
 struct Shaping {
-    float f[NT][2];       // to the tanh's argument (without a cap: to base-2 logits) of rows 2t, 2t + 1 of each N tile
-    float at[NT][2];      // the rows' positions
-    float slope[NT][2];   // base 2
-    const int2* see;      // shared memory: what the query positions see
+    const int2* see;      // what the query positions see
+    uint32_t rows;        // of rows 2t, 2t + 1 of each N tile (64 bytes a tile): their positions, their slopes (base 2)
+    uint32_t factors;     // of the rows' logits (32 bytes a tile), or 0: one factor for all
 };
+__device__ __forceinline__ float4 lds_float4(uint32_t a)
+{
+    const uint4 v = lds128(a);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
 // Logits of U tiles whose first row is `first`, as logits() gives them: under the cap, and with their bias by distance as
 // base-2 logits (without one, the factor of a capped logit, p.cap2, is left to weights()).
-template <int U, int NT>
-__device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Shaping<NT>& sh, float (&s)[U * NT][4], int first)
+template <bool CAP, int U, int NT>
+__device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Shaping& sh, float (&s)[U * NT][4], int first)
 {
+    const float unit = p.qscale * (CAP ? p.icap : 1.4426950408889634f);
 #pragma unroll
-    for (int m = 0; m < U * NT; ++m)
+    for (int n = 0; n < NT; ++n) {
+        float f0 = unit, f1 = unit;
+        if (sh.factors) {
+            const uint2 w = lds64(sh.factors + 32 * n);
+            f0 *= __uint_as_float(w.x);
+            f1 *= __uint_as_float(w.y);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][e] *= sh.f[m % NT][e & 1];
-    if (p.cap > 0.f) {
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u * NT + n][e] *= e & 1 ? f1 : f0;
+    }
+    if (CAP) {
         float top = 0.f;
 #pragma unroll
         for (int m = 0; m < U * NT; ++m)
@@ -782,12 +796,17 @@ __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Sha
     if (p.slope) {
         const float row = (float)(first + ((threadIdx.x & 31) >> 2));
 #pragma unroll
-        for (int m = 0; m < U * NT; ++m)
+        for (int n = 0; n < NT; ++n) {
+            const float4 w = lds_float4(sh.rows + 64 * n);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float far = sh.at[m % NT][e & 1] - row;   // of the unit's first row
-                s[m][e] = fmaf(fabsf(far - (float)(16 * (m / NT) + 8 * (e >> 1))), -sh.slope[m % NT][e & 1], s[m][e] * p.cap2);
-            }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float far = (e & 1 ? w.z : w.x) - row;   // of the unit's first row
+                    float& x = s[u * NT + n][e];
+                    x = fmaf(fabsf(far - (float)(16 * u + 8 * (e >> 1))), -(e & 1 ? w.w : w.y), CAP ? x * p.cap2 : x);
+                }
+        }
     }
 }
 
@@ -958,14 +977,14 @@ __device__ __forceinline__ int query_pos(const PagedAttnParams& p, int r) { retu
 // O^T += V^T P^T: the tiles' product starts from zero and is added to O by an fp32 addition.  The tensor core
 // aligns all products to the accumulator and cuts them off (2^-23 of it): accumulated over a long row that costs
 // small weights beside a large one, and drifts.
-template <int U, bool EDGE, typename S, bool SHAPED, bool E2M1, int NT, bool DUP>
+template <int U, bool EDGE, typename S, int SHAPED, bool E2M1, int NT, bool DUP>
 __device__ __forceinline__ void attend(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, uint32_t edge, int r0,
-                                       int seen, const Shaping<NT>& sh, int first)
+                                       int seen, const Shaping& sh, int first)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float s[U * NT][4];
     logits<U, S, E2M1, NT, DUP>(a, slot, 0, s);
-    if (SHAPED) shape_logits<U, NT>(p, sh, s, first);
+    if (SHAPED) shape_logits<SHAPED == 2, U, NT>(p, sh, s, first);
     uint32_t hide = 0, vm[U];
     if (EDGE) {
 #pragma unroll
@@ -1039,9 +1058,9 @@ __device__ __forceinline__ bool not_all_finite(uint32_t slot, int u, int from, i
 
 // A tile where rows that only later queries see hold an infinity or a NaN: one product per query position, over
 // the rows that it sees, taken by its query rows alone.  whole: a tile without an edge beside such a one.
-template <typename S, bool SHAPED, bool E2M1, int NT, bool DUP>
+template <typename S, int SHAPED, bool E2M1, int NT, bool DUP>
 __device__ __forceinline__ void attend_apart(const PagedAttnParams& p, Acc<E2M1, NT, DUP>& a, uint32_t slot, int u, int r0,
-                                             int seen, bool whole, const Shaping<NT>& sh, int first)
+                                             int seen, bool whole, const Shaping& sh, int first)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int pos = 0;   // of a whole tile: seen by all
@@ -1050,7 +1069,7 @@ __device__ __forceinline__ void attend_apart(const PagedAttnParams& p, Acc<E2M1,
     if (vm == 0) return;
     float s[NT][4];
     logits<1, S, E2M1, NT, DUP>(a, slot, u, s);
-    if (SHAPED) shape_logits<1, NT>(p, sh, s, first);
+    if (SHAPED) shape_logits<SHAPED == 2, 1, NT>(p, sh, s, first);
     uint32_t hide = 0;
     const int p0 = __shfl_sync(kFull, pos, g), p1 = __shfl_sync(kFull, pos, g + 8);
 #pragma unroll
@@ -1106,7 +1125,7 @@ template <int W>
 struct LineSmem {
     int scan[W], start, b, len, lo, cnt[32 * W];
 };
-template <int W, typename Count, bool SHAPED = false>
+template <int W, typename Count, int SHAPED = 0>
 struct Line {
     const PagedAttnParams& p;
     const Count count;         // tiles of a sequence's piece, at least 1
@@ -1366,7 +1385,7 @@ struct Shape {
 //
 // SHAPED: fx_paged_attend -- new tokens of ragged sequences, a cap and a bias on the logits, an interval of rows for each
 // query position; the positions of a unit's rows follow from its place.
-template <bool E2M1, int NT, bool DUP, int U, bool SHAPED>
+template <bool E2M1, int NT, bool DUP, int U, int SHAPED>
 __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2M1, NT, DUP, U>::kCtas)
     paged_decode_kernel(const PagedAttnParams p)
 {
@@ -1378,9 +1397,10 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
     constexpr bool kSharedQ = Acc<E2M1, NT, DUP>::kSharedQ;
     __shared__ float sm_m[W * kRows], sm_l[W * kRows];
     __shared__ uint4 sm_q[kSharedQ ? NT * 128 : 1];   // the queries' fragments, the factors of their logits
-    __shared__ float sm_f[8 * NT];
+    __shared__ __align__(8) float sm_f[8 * NT];
     __shared__ LineSmem<W> sm_line;
     __shared__ int2 sm_see[SHAPED ? kMaxRows : 1];
+    __shared__ __align__(16) float2 sm_row[SHAPED ? 8 * NT : 1];   // positions and slopes
     __shared__ unsigned sm_last;
 
     griddep_wait();
@@ -1401,6 +1421,11 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
         const int base = seq.lo & ~(kTileRows - 1);   // first row of the first tile
         if (SHAPED) {
             for (int i = tid; i < p.Mq; i += 32 * W) sm_see[i] = i < seq.nb ? shaped_interval(p, seq, i) : make_int2(0, 0);
+            if (tid < 8 * NT) {
+                const int r = r0 + (DUP ? tid & 3 : tid);
+                sm_row[tid] = make_float2((float)(seq.pos0 + query_pos(p, r)),
+                                          p.slope && r < p.R ? p.slope[h * p.G + r / p.Mq] * 1.4426950408889634f : 0.f);
+            }
         }
 
         // the queries, the pages and the first rows are under way together
@@ -1438,20 +1463,13 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
             }
         }
         if (kSharedQ || SHAPED) __syncthreads();
-        Shaping<NT> sh;
-        sh.see = sm_see;
+        const Shaping sh{sm_see, smem_addr(sm_row) + 16 * t, kSharedQ ? smem_addr(sm_f) + 8 * t : 0u};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (kSharedQ) a.rs[n][e] = p.qscale * sm_f[8 * n + 2 * t + e];
-                if (SHAPED) {
-                    const int r = r0 + 8 * n + (DUP ? (2 * t + e) & 3 : 2 * t + e);
-                    sh.f[n][e] = a.rs[n][e] * (p.cap > 0.f ? p.icap : 1.4426950408889634f);
-                    a.rs[n][e] = p.slope ? 1.f : p.cap2;
-                    sh.at[n][e] = (float)(seq.pos0 + query_pos(p, r));
-                    sh.slope[n][e] = p.slope && r < p.R ? p.slope[h * p.G + r / p.Mq] * 1.4426950408889634f : 0.f;
-                }
+                if (SHAPED) a.rs[n][e] = SHAPED == 2 && !p.slope ? p.cap2 : 1.f;
                 a.bias[n][e] = kNoRef;
                 a.l[n][e] = 0.f;
             }
@@ -1814,7 +1832,7 @@ cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done)
     return e;
 }
 
-template <bool E2M1, int NT, bool DUP, int U, bool SHAPED>
+template <bool E2M1, int NT, bool DUP, int U, int SHAPED>
 cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     using S = Shape<E2M1, NT, DUP, U>;
@@ -1826,14 +1844,14 @@ cudaError_t launch_decode(const PagedAttnParams& p, int sm_count, bool pdl, cuda
 }
 
 // The kernel for a call's query rows.
-template <bool SHAPED>
+template <int SHAPED>
 cudaError_t launch_decode_bf16(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     if (p.R <= 4) return launch_decode<false, 1, true, 1, SHAPED>(p, sm_count, pdl, s);
     if (p.R <= 8) return launch_decode<false, 1, false, 1, SHAPED>(p, sm_count, pdl, s);
     return launch_decode<false, 2, false, 1, SHAPED>(p, sm_count, pdl, s);
 }
-template <bool SHAPED>
+template <int SHAPED>
 cudaError_t launch_decode_e2m1(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s)
 {
     if (p.R > 8) return launch_decode<true, 2, false, 2, SHAPED>(p, sm_count, pdl, s);
