@@ -1104,16 +1104,34 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
     return FX_OK;
 }
 
-// fx_paged_attend with up to kMaxRows query rows a (sequence, KV head); its own checks are done.
+// Whether the decode's kernels take a call of fx_paged_attend: of up to 16 query rows a (sequence, KV head), which are one
+// pass over the cache, always; of more (a pass for every 16) where the prompts' kernel takes longer.  Steps of 8 x 32768
+// rows, 8 KV heads, us: bf16, 20 query rows 235 here, 178 there; with a cap 249 and 380; 64 rows with a cap 485 and 387; 4 bits,
+// 32 query rows 152 and 199, 64 rows 281 and 200.  Little work (by the room that the tables have) starts sooner here: 2 x 4
+// heads' 1024 bf16 rows, 24 query rows 15.9 and 19.6; 8 heads' 8192, 64 query rows 32 and 34.
+bool attend_takes_few(const PagedCache& c, bool e2m1, int rows, bool cap)
+{
+    if (rows <= 16) return true;
+    if (rows > kMaxRows) return false;
+    return (rows <= 32 && (e2m1 || cap)) || (int64_t)c.B * c.Hkv * c.cap <= 1 << 17;
+}
+// Scratch memory of a call, whichever kernel takes it.
+size_t attend_workspace_bytes(int B, int Hkv, int G, int max_new, int sms)
+{
+    const size_t many = paged_attend_workspace_bytes(paged_attend_cut(B, Hkv, G, max_new, sms));
+    const size_t few = (int64_t)G * max_new <= kMaxRows ? paged_decode_workspace_bytes(G * max_new, sms) : 0;
+    return many > few ? many : few;
+}
+
+// fx_paged_attend by the decode's kernels; the call's own checks are done.
 fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags, void* stream)
 {
     PagedAttnParams p;
     fx_status st = paged_queries(cache, q->q, 0, q->q_stride_h, q->q_stride_n, q->Hq, q->max_new, 0, q->scale, flags, &p);
     if (st != FX_OK) return st;
-    const int sms = sm_count_or_default();
-    if ((st = check_ws(ws, ws_bytes, paged_decode_workspace_bytes(p.R, sms))) != FX_OK) return st;
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != FX_OK) return st;
+    const int sms = ds->sm_count;
     p.qscale = q->scale * p.c.k_mul;
     p.start = q->start;
     p.first = q->first;
@@ -1399,8 +1417,7 @@ size_t fx_paged_attend_workspace_bytes(int B, int Hkv, int Hq, int max_new)
 {
     if (B < 1 || Hkv < 1 || Hq < Hkv || max_new < 1 || (int64_t)(Hq / Hkv) * max_new > (1ll << 30)) return 0;
     const int sms = sm_count_or_default(), G = Hq / Hkv;
-    if ((int64_t)G * max_new <= kMaxRows) return paged_decode_workspace_bytes(G * max_new, sms);
-    return paged_attend_workspace_bytes(paged_attend_cut(B, Hkv, G, max_new, sms));
+    return attend_workspace_bytes(B, Hkv, G, max_new, sms);
 }
 
 fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags,
@@ -1429,10 +1446,12 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     if (!q->out || !aligned16(q->out)) return fail(FX_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
     if ((int64_t)G * q->max_new > (1ll << 30) || q->n > (1 << 30) || (int64_t)q->n * q->Hq > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "queries: too many rows");
-    if (G * q->max_new <= kMaxRows) return attend_few(cache, q, ws, ws_bytes, flags, stream);
-    const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, sm_count_or_default());
+    const int sms = sm_count_or_default();
+    const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, sms);
     if (!cut.split && cut.blocks > 65535) return fail(FX_ERR_UNSUPPORTED, "queries: too many of one sequence");
-    if ((st = check_ws(ws, ws_bytes, paged_attend_workspace_bytes(cut))) != FX_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, attend_workspace_bytes(cache->B, cache->Hkv, G, q->max_new, sms))) != FX_OK) return st;
+    if (attend_takes_few(p.c, cache->format == FX_PAGED_E2M1, G * q->max_new, q->cap > 0.f))
+        return attend_few(cache, q, ws, ws_bytes, flags, stream);
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != FX_OK) return st;
     p.q = q->q;

@@ -279,7 +279,7 @@ struct PagedGatherParams {
     unsigned* err;
 };
 
-// fx_paged_attend (paged_attend.cu).
+// fx_paged_attend's prompts (paged_attend.cu).
 struct PagedAttendCut {
     int blocks;      // blocks of query rows of one (sequence, KV head), at most
     int split;       // CTAs among which the blocks' tiles are shared, or 0: one CTA to a block
@@ -382,7 +382,7 @@ cudaError_t launch_paged_copy(const PagedCopyParams& p, bool e2m1, bool pdl, cud
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_importance(const PagedAttnParams& p, bool e2m1, int sm_count, bool pdl, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int R, int sm_count);
-// fx_paged_attend with up to kMaxRows query rows a (sequence, KV head): kernels of fx_paged_decode's kind.
+// fx_paged_attend with few query rows a (sequence, KV head): kernels of fx_paged_decode's kind.
 cudaError_t launch_paged_attend_few_bf16_open(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend_few_bf16_cap(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend_few_e2m1_open(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);

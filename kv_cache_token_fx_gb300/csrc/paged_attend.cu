@@ -18,7 +18,7 @@
 // large.  Logits, maxima, sums and O are fp32.
 //
 // Calls of fewer blocks than SMs are cut along the cache: every block's tiles become parts of nearly equal length by the
-// lengths found on the device, and the last CTA of a block to arrive joins its parts in their order.  (Calls of up to 64
+// lengths found on the device, and the last CTA of a block to arrive joins its parts in their order.  (Calls of few
 // query rows a (sequence, KV head) go to the kernels of paged_attn.cuh, which are bound by the cache's bytes.)
 #include <cuda_bf16.h>
 #include <stdint.h>

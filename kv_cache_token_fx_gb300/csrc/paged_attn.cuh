@@ -1,5 +1,5 @@
 // Attention over a paged cache for sm_103a, bf16 or 4-bit: the kernels of fx_paged_decode and fx_paged_importance
-// (paged_attn.cu), and of fx_paged_attend where a (sequence, KV head) has up to 64 query rows (paged_attn_shaped_*.cu).
+// (paged_attn.cu), and of fx_paged_attend where a (sequence, KV head) has few query rows (paged_attn_shaped_*.cu).
 //
 // Work unit of a warp: a tile of 16 cache rows of one (sequence, KV head); two tiles at a time in 4 bits.  Every
 // warp owns a ring of slots in shared memory and fills it with cp.async ahead of its work; no warp waits for

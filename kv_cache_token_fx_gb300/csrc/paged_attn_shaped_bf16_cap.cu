@@ -1,4 +1,4 @@
-// fx_paged_attend over bf16 pages, with a cap on the scores, where a (sequence, KV head) has up to 64 query rows: decode steps
+// fx_paged_attend over bf16 pages, with a cap on the scores, where a (sequence, KV head) has few query rows: decode steps
 // and drafts, bound by the cache's bytes (kernels: paged_attn.cuh; a unit of its own, compiled beside the others).
 #include "paged_attn.cuh"
 

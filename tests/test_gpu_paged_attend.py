@@ -422,3 +422,18 @@ def test_attend_far_pages_and_wide_windows(fx):
     assert to.length.tolist() == c.lens
     for a, b in zip(fx.fx_paged_gather(dev, 40), fx.fx_paged_gather(to, 40)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_attend_between_steps_and_prompts(fx, fmt):
+    """17 to 64 query rows of a KV head, over tables with little room and with much: either kernel may take them."""
+    for lens, news, G, pages, cap in (([300, 90], [5, 5], 4, None, 0.0), ([300, 90], [5, 2], 4, 5000, 0.0), ([300, 90], [8, 8], 4, 5000, 6.0),
+                                      ([200, 260], [8, 7], 8, 5000, 6.0), ([200, 260], [16, 3], 4, None, 0.0)):
+        c = pr.Cache(fmt, lens, 1, 16, seed=G, max_pages=pages)
+        g = np.random.default_rng(G)
+        start = np.concatenate(([0], np.cumsum(news)))
+        q = pr.bf16(2.0 * g.standard_normal((int(start[-1]), G, D)))
+        sl = 2.0 ** -np.arange(1, G + 1)
+        got = fx.fx_paged_attend(c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32), max_new=max(news), cap=cap,
+                                 slope=cu(sl, torch.float32), want_lse=True)
+        check(c, got, attend_ref(c, q, start, D ** -0.5, cap=cap, slope=sl))

@@ -64,7 +64,8 @@ def test_attend_refusals(lib):  # noqa: F811
 def test_attend_workspace():
     import kv_cache_token_fx_gb300 as fx
     w = fx.fx_paged_attend_workspace_bytes
-    assert w(4, 2, 8, 1) == fx.fx_paged_decode_workspace_bytes(4, 2, 8, 1)
+    assert w(4, 2, 8, 1) >= fx.fx_paged_decode_workspace_bytes(4, 2, 8, 1) > 0
+    assert w(64, 8, 64, 8) >= fx.fx_paged_decode_workspace_bytes(64, 8, 64, 8)
     assert w(1, 1, 4, 100) > w(64, 8, 32, 4096) > 0       # only calls of few blocks are cut into parts
     for bad in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 2, 1, 1), (1, 1, 1, 0), (1, 1, 2, 1 << 30)):
         assert w(*bad) == 0
