@@ -97,7 +97,7 @@ __device__ __forceinline__ void pairs_of_axes(const PagedAppendParams& p, const 
 //
 // AXES: a pair's cosine and sine are of its own axis' position.  Four neighbouring pairs of one axis are loaded as one.
 template <bool E2M1, int R, bool INTERLEAVED, bool AXES>
-__global__ void __launch_bounds__(kThreadsRows, 8) paged_append_kernel(const PagedAppendParams p)
+__global__ void __launch_bounds__(kThreadsRows, AXES ? 10 : 8) paged_append_kernel(const PagedAppendParams p)
 {
     griddep_wait();
     griddep_launch();
@@ -460,10 +460,13 @@ cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStrea
     // 4.6 us, against 5.6 with four).  More rows than the machine has groups of 8 lanes: four rows each, for their shared
     // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 92 us, against 124 with one).
     const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > sm_count * 2048 / 8;
-    const int R = many ? 4 : 1;
+    // With axes two rows each and 10 CTAs an SM: the angles are more loads, which more warps wait for (four such prompts in
+    // bf16 94 us, against 103 with four rows and 8 CTAs, 100 with two and 8, 106 with two and 12).
+    constexpr int kMany = AXES ? 2 : 4;
+    const int R = many ? kMany : 1;
     const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
     const dim3 grid((unsigned)((groups + kThreadsRows / 8 - 1) / (kThreadsRows / 8)));
-    return many ? launch_kernel(paged_append_kernel<E2M1, 4, INTERLEAVED, AXES>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
+    return many ? launch_kernel(paged_append_kernel<E2M1, kMany, INTERLEAVED, AXES>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p)
                 : launch_kernel(paged_append_kernel<E2M1, 1, INTERLEAVED, AXES>, grid, dim3(kThreadsRows), 0, s, pdl, 0u, p);
 }
 
