@@ -948,8 +948,11 @@ def fx_paged_attend(cache, q, start=None, *, max_new=None, first=None, last=None
         ws_at, ws_bytes = buf.data_ptr(), buf.numel()
     else:
         ws_at, ws_bytes = None, 0
-    queries = _QUERIES.pack(q_at, qs[0], qs[1], start_at, first_at, last_at, slope_at, out_at, lse_at, n, Hq, max_new,
-                            window, _SCALE if scale is None else scale, cap)
+    try:
+        queries = _QUERIES.pack(q_at, qs[0], qs[1], start_at, first_at, last_at, slope_at, out_at, lse_at, n, Hq, max_new,
+                                window, _SCALE if scale is None else scale, cap)
+    except (struct.error, OverflowError, TypeError) as e:
+        raise FxError(FX_ERR_INVALID_ARG, f"window, max_new: 32-bit integers, scale, cap: fp32 numbers ({e})") from None
     rc = lib.fx_paged_attend(cache._ref, queries, ws_at, ws_bytes, flags, st)
     if rc:
         _check(rc)
@@ -1016,7 +1019,7 @@ class PagePool:
         self._h = None
         lib = load_library()
         self._lib = lib
-        self._h = lib.fx_page_pool_create(int(n_pages), int(page_rows), int(max_seqs), int(max_pages))
+        self._h = lib.fx_page_pool_create(*map(self._i32, (n_pages, page_rows, max_seqs, max_pages)))
         if not self._h:
             _check(FX_ERR_INVALID_ARG)
         self.max_pages = int(max_pages)
@@ -1026,6 +1029,14 @@ class PagePool:
             raise FxError(FX_ERR_INVALID_ARG, self._lib.fx_last_error().decode(errors="replace"))
         return int(r)
 
+    @staticmethod
+    def _i32(x):
+        """An int that ctypes does not cut."""
+        x = int(x)
+        if not -(1 << 31) <= x < 1 << 31:
+            raise FxError(FX_ERR_INVALID_ARG, f"{x} is no 32-bit integer")
+        return x
+
     def open(self) -> int:
         return self._int(self._lib.fx_page_pool_open(self._h))
 
@@ -1033,27 +1044,27 @@ class PagePool:
         """Room for n more rows; returns None, or the pages (src, dst) that fx_paged_copy has to copy before the rows
         are written."""
         src, dst = ctypes.c_int32(), ctypes.c_int32()
-        r = self._int(self._lib.fx_page_pool_append(self._h, int(seq), int(n), ctypes.byref(src), ctypes.byref(dst)))
+        r = self._int(self._lib.fx_page_pool_append(self._h, self._i32(seq), self._i32(n), ctypes.byref(src), ctypes.byref(dst)))
         return (src.value, dst.value) if r else None
 
     def fork(self, seq: int) -> int:
-        return self._int(self._lib.fx_page_pool_fork(self._h, int(seq)))
+        return self._int(self._lib.fx_page_pool_fork(self._h, self._i32(seq)))
 
     def truncate(self, seq: int, n: int) -> int:
-        return self._int(self._lib.fx_page_pool_truncate(self._h, int(seq), int(n)))
+        return self._int(self._lib.fx_page_pool_truncate(self._h, self._i32(seq), self._i32(n)))
 
     def release(self, seq: int) -> int:
-        return self._int(self._lib.fx_page_pool_release(self._h, int(seq)))
+        return self._int(self._lib.fx_page_pool_release(self._h, self._i32(seq)))
 
     def length(self, seq: int) -> int:
-        return self._int(self._lib.fx_page_pool_length(self._h, int(seq)))
+        return self._int(self._lib.fx_page_pool_length(self._h, self._i32(seq)))
 
     def free_pages(self) -> int:
         return self._int(self._lib.fx_page_pool_free_pages(self._h))
 
     def batch(self, seqs):
         """(table [n, max_pages], length [n]) of those sequences, as int32 CPU tensors for a PagedKV."""
-        ids = [int(x) for x in seqs]
+        ids = [self._i32(x) for x in seqs]
         n = len(ids)
         table, length = torch.empty(n, self.max_pages, dtype=torch.int32), torch.empty(n, dtype=torch.int32)
         i32p = ctypes.POINTER(ctypes.c_int32)

@@ -303,7 +303,8 @@ def test_attend_without_start_and_strided(fx, fmt):
     for bad in (dict(max_new=3), dict(first=torch.zeros(5, dtype=torch.int32, device="cuda")),
                 dict(slope=torch.ones(3, device="cuda")), dict(out=torch.zeros(6, 4, D, device="cuda")),
                 dict(lse=torch.zeros(4, 6, device="cuda")), dict(start=torch.zeros(3, dtype=torch.int32, device="cuda")),
-                dict(window=-1), dict(cap=-2.0), dict(scale=float("nan"))):
+                dict(window=-1), dict(cap=-2.0), dict(scale=float("nan")), dict(window=1 << 31), dict(window=0.5),
+                dict(scale=1e300), dict(cap="30")):
         with pytest.raises(fx.FxError):
             fx.fx_paged_attend(dev, heads, **bad)
     with pytest.raises(fx.FxError):

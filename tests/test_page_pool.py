@@ -53,6 +53,7 @@ def test_errors_change_nothing():
     b = p.fork(a)
     for call in (lambda: p.append(a, 40), lambda: p.append(b, 32), lambda: p.append(a, -1), lambda: p.append(5, 1),
                  lambda: p.fork(a), lambda: p.open(), lambda: p.truncate(a, 18), lambda: p.truncate(a, -1),
+                 lambda: p.append(a, (1 << 32) + 1), lambda: p.fork(1 << 32), lambda: p.release((1 << 32) + a),
                  lambda: p.release(2), lambda: p.release(-1), lambda: p.length(9), lambda: p.batch([a, 7])):
         with pytest.raises(fx.FxError):
             call()
