@@ -558,11 +558,12 @@ __device__ __forceinline__ int sequence_length(const PagedAttendParams& p, int b
     return min(max(len, 0), p.c.cap);
 }
 
-// What token j of a sequence sees: rows x <= t < y.
+// What token j of a sequence sees: rows x <= t < y, both within [0, len] (any int may be given: arithmetic on these ends
+// must not overflow).
 __device__ __forceinline__ int2 token_interval(const PagedAttendParams& p, int q0, int len, int all, int j)
 {
     const int pos = len - all + j;
-    int2 see = make_int2(p.first ? max(p.first[q0 + j], 0) : 0, min(p.last ? p.last[q0 + j] : pos + 1, len));
+    int2 see = make_int2(p.first ? min(max(p.first[q0 + j], 0), len) : 0, max(min(p.last ? p.last[q0 + j] : pos + 1, len), 0));
     if (p.window > 0) see.x = max(see.x, pos - p.window + 1);
     return see;
 }

@@ -165,11 +165,13 @@ struct Seq {
     int com_lo, com_hi;     // rows that every query sees
     int rows;               // rows of the cache
 };
-// What query i of a sequence sees: rows x <= t < y.
+// What query i of a sequence sees: rows x <= t < y, both within [0, rows] (any int may be given: arithmetic on these ends
+// must not overflow).
 __device__ __forceinline__ int2 shaped_interval(const PagedAttnParams& p, const Seq& q, int i)
 {
     const int pos = q.pos0 + i;
-    int2 see = make_int2(p.first ? max(p.first[q.q0 + i], 0) : 0, min(p.last ? p.last[q.q0 + i] : pos + 1, q.rows));
+    int2 see = make_int2(p.first ? min(max(p.first[q.q0 + i], 0), q.rows) : 0,
+                         max(min(p.last ? p.last[q.q0 + i] : pos + 1, q.rows), 0));
     if (p.window > 0) see.x = max(see.x, pos - p.window + 1);
     return see;
 }
