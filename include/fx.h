@@ -627,7 +627,8 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
  *   x_t = scale * q . k_t;   with cap > 0: x_t = cap * tanh(x_t / cap);   then x_t -= slope[g] * |pos - t|
  *   out[i, g, :] = sum_t softmax(x)_t v_t   (bf16)        lse[i, g] = log sum_t exp(x_t)   (written when lse != NULL)
  * A query that sees no row, or whose logits are all -infinity, gives out = 0 and lse = -infinity.
- * Logits, sums and lse are fp32.  Weights are rounded once for the product with V: to bf16 beside bf16 pages (2^-8 of a
+ * Logits, sums and lse are fp32 (with more than 16 query rows a KV head, G*max_new, logits under a cap of up to 64 may be off
+ * by 2^-21 of the cap besides).  Weights are rounded once for the product with V: to bf16 beside bf16 pages (2^-8 of a
  * weight), to f16 beside 4-bit pages.  A row that a query does not see does not reach it, whatever it holds.  A query that
  * sees a V with an infinity or a NaN may give NaN in all of its dimensions.
  *   start     int32 [B+1] on the device, or NULL: max_new tokens of every sequence (n = B * max_new).  Offsets that decrease

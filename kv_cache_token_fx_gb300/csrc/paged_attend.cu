@@ -59,6 +59,9 @@ constexpr int kRing = 16;                        // tiles whose flags are kept (
 enum Mode { kPlain, kCap, kBias };   // what is put on the logits: nothing, a cap, a bias by distance (and perhaps a cap)
 template <bool E2M1>
 constexpr float kWeightBase = E2M1 ? 6.f : -32.f;
+// Caps up to which two forms of tanh are mixed: the one that is off by 2^-21 of 1 leaves 2^-15 of a logit at most then, an
+// eighth of what f16 weights are rounded by (bf16: a 64th).
+constexpr float kMixedCap = 64.f;
 constexpr float kFarRef = 4194304.f;   // 2^22: beyond it products and their rounded values lie too far apart for one fma
 
 constexpr int kMaxPlan = 256;                    // (sequence, block) pairs of a call that is cut along the cache
@@ -651,7 +654,9 @@ __device__ __forceinline__ bool plan(const PagedAttendParams& p, AttendSmem& sm,
     return i >= 0;
 }
 
-template <bool E2M1, int MODE>
+// WIDE: caps whose logits have to be exact relative to themselves (kMixedCap).  A kernel of its own: with both in one, the
+// smaller caps' windowed 4-bit prompt took 413 us instead of 405.
+template <bool E2M1, int MODE, bool WIDE>
 __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid_constant__ PagedAttendParams p)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -888,6 +893,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         const float cap = p.cap, icap = cap > 0.f ? 1.f / cap : 0.f;
         const float slope2 = MODE == kBias && live ? p.slope[g] * 1.4426950408889634f : 0.f;
         if (MODE == kPlain) qs *= 1.4426950408889634f;
+        // from s to y of tanh(y); finite with its factors, so that a logit of 0 stays 0
+        const float k = fminf(qs * icap, 0x1p126f), k2 = k * 2.885390081777927f;
         auto check = [&](int t) {   // whether the row sees a value of tile t that is not finite (those were left out)
             for (int w = 0; w < 4; ++w) {
                 unsigned bits = *(volatile unsigned*)&sm.bad_v[t & (kRing - 1)][w];
@@ -940,18 +947,49 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                 float f = MODE == kPlain ? qs : 1.f, off = 0.f;   // from s to base-2 logits: s * f + off
                 if (MODE != kPlain) {
                     if (cap > 0.f) {
-                        // tanh(y) = y + y^3 Q(y^2) (10 steps of the fp32 units for two values) where no logit is past the
-                        // cap, and beside it tanh(y) = 1 - 2 / (exp(2y) + 1), off by 2^-21 at most (of 1, not of itself; 3
-                        // steps, and 12 of the function unit for one value), so that both units are busy; else the latter
-                        // alone.
-                        const float k = qs * icap, k2 = k * 2.885390081777927f;
                         float top = 0.f;
 #pragma unroll
                         for (int i = 0; i < 128; i += 4) {
                             const float u = max3(fabsf(s[i]), fabsf(s[i + 1]), fabsf(s[i + 2]));
                             top = max3(top, u, fabsf(s[i + 3]));
                         }
-                        if (!__any_sync(0xffffffffu, !(top * k <= 1.f))) {
+                        // tanh(y) = y + y^3 Q(y^2), exact to 2^-22 of itself for y up to 1 (10 steps of the fp32 units for two
+                        // values).  Caps up to kMixedCap: beside it tanh(y) = 1 - 2 / (exp(2y) + 1), off by 2^-21 at most (of
+                        // 1, not of itself; 3 steps, and 12 of the function unit for one value), so that both units are
+                        // busy, and the latter alone where a logit is past the cap.  WIDE: the polynomial alone, and past the
+                        // cap each value's own of the two, whose errors are relative to it (the same prompt with a cap of 65:
+                        // 426 us; of 64: 391).
+                        if (WIDE) {
+                            if (!__any_sync(0xffffffffu, !(top * qs * icap <= 1.f))) {
+#pragma unroll
+                                for (int i = 0; i < 128; i += 8) {
+                                    float2 y[4], u[4], q[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        y[e] = mul2(mul2(make_float2(s[i + 2 * e], s[i + 2 * e + 1]), make_float2(qs, qs)),
+                                                    make_float2(icap, icap));
+                                        u[e] = mul2(y[e], y[e]);
+                                        q[e] = make_float2(kTanh[6], kTanh[6]);
+                                    }
+#pragma unroll
+                                    for (int c = 5; c >= 0; --c)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) q[e] = fma2(q[e], u[e], make_float2(kTanh[c], kTanh[c]));
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float2 r = fma2(mul2(y[e], u[e]), q[e], y[e]);
+                                        s[i + 2 * e] = r.x;
+                                        s[i + 2 * e + 1] = r.y;
+                                    }
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 128; ++i) {
+                                    const float y = s[i] * qs * icap;
+                                    s[i] = fabsf(y) <= 1.f ? tanh_near(y) : tanh_far(y);
+                                }
+                            }
+                        } else if (!__any_sync(0xffffffffu, !(top * k <= 1.f))) {
 #pragma unroll
                             for (int i = 0; i < 128; i += 16) {   // side by side: ten values by one, six by the other
                                 float2 y[5], u[5], q[5];
@@ -1208,7 +1246,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
     }
 }
 
-template <bool E2M1, int MODE>
+template <bool E2M1, int MODE, bool WIDE>
 cudaError_t launch(const PagedAttendParams& p, bool pdl, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
@@ -1217,12 +1255,12 @@ cudaError_t launch(const PagedAttendParams& p, bool pdl, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(paged_attend_kernel<E2M1, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(E2M1));
+        e = cudaFuncSetAttribute(paged_attend_kernel<E2M1, MODE, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, attend_smem(E2M1));
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
     const dim3 grid = p.split ? dim3(p.split) : dim3(p.c.Hkv, p.blocks, p.c.B);
-    return launch_kernel(paged_attend_kernel<E2M1, MODE>, grid, dim3(kThreadsA), attend_smem(E2M1), s, pdl, 0u, p);
+    return launch_kernel(paged_attend_kernel<E2M1, MODE, WIDE>, grid, dim3(kThreadsA), attend_smem(E2M1), s, pdl, 0u, p);
 }
 
 }  // namespace
@@ -1245,9 +1283,14 @@ size_t paged_attend_workspace_bytes(const PagedAttendCut& c)
 
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s)
 {
-    if (p.slope) return e2m1 ? launch<true, kBias>(p, pdl, s) : launch<false, kBias>(p, pdl, s);
-    if (p.cap > 0.f) return e2m1 ? launch<true, kCap>(p, pdl, s) : launch<false, kCap>(p, pdl, s);
-    return e2m1 ? launch<true, kPlain>(p, pdl, s) : launch<false, kPlain>(p, pdl, s);
+    // (a scale so small beside the cap that their quotient is no normal number has to be applied by itself, too)
+    if (p.cap > kMixedCap || (double)p.scale < (double)p.cap * 0x1p-126) {
+        if (p.slope) return e2m1 ? launch<true, kBias, true>(p, pdl, s) : launch<false, kBias, true>(p, pdl, s);
+        return e2m1 ? launch<true, kCap, true>(p, pdl, s) : launch<false, kCap, true>(p, pdl, s);
+    }
+    if (p.slope) return e2m1 ? launch<true, kBias, false>(p, pdl, s) : launch<false, kBias, false>(p, pdl, s);
+    if (p.cap > 0.f) return e2m1 ? launch<true, kCap, false>(p, pdl, s) : launch<false, kCap, false>(p, pdl, s);
+    return e2m1 ? launch<true, kPlain, false>(p, pdl, s) : launch<false, kPlain, false>(p, pdl, s);
 }
 
 }  // namespace fx

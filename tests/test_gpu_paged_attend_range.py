@@ -45,3 +45,77 @@ def test_attend_interval_ends(fx, fmt, lens, news, G, pages):  # noqa: F811
         got = fx.fx_paged_attend(dev, t, st, max_new=max(news), first=cu(first, torch.int32), last=cu(last, torch.int32),
                                  want_lse=True)
         check(c, got, attend_ref(c, q, start, D ** -0.5, first, last), slice(0, n))
+
+
+def tight_ref(c, q, start, scale, cap=0.0, slope=None, mixed=False):
+    """attend_ref over the rows up to each token, with tolerances that follow each logit's own error.
+
+    The products of a logit x leave 2^-19 of |scale| sum |q_d k_d| (test_gpu_paged_attend.py).  Under the cap, cap tanh(x / cap)
+    has a slope of at most 1 for that, and four products (scale, 1 / cap, cap, log2 e) and a tanh off by 2^-21.5 of itself at
+    most (a polynomial off by 2^-22; past 1, exp off by 2^-22 of itself and 2^-24 of its argument, whose quotient is below 1/4 of
+    1 - 2 / (exp + 1)) leave 2^-20 of the capped logit.  mixed: kernels that may take the second form below 1 too, for caps up
+    to 64: 2^-21 of the cap.  A bias leaves 2^-22 of itself.  A weight p is then off by p (dx + sum p dx) and its rounding.
+    """
+    n, Hq, _ = q.shape
+    G = Hq // c.Hkv
+    out, lse = np.zeros(q.shape), np.zeros((n, Hq))
+    tol, ltol = np.zeros(q.shape), np.zeros((n, Hq))
+    for b in range(c.B):
+        nb = start[b + 1] - start[b]
+        for j in range(nb):
+            i, pos = start[b] + j, c.lens[b] - nb + j
+            t = np.arange(pos + 1)
+            for g in range(Hq):
+                k, v = c.rows(0, b, g // G, t), c.rows(1, b, g // G, t)
+                x = scale * (k @ q[i, g])
+                dx = 2.0 ** -19 * abs(scale) * (np.abs(k) @ np.abs(q[i, g]))
+                if cap:
+                    x = cap * np.tanh(x / cap)
+                    dx = dx + 2.0 ** -20 * np.abs(x) + (2.0 ** -21 * cap if mixed and cap <= 64 else 0.0)
+                if slope is not None:
+                    far = slope[g] * np.abs(pos - t)
+                    x, dx = x - far, dx + 2.0 ** -22 * (np.abs(far) + np.abs(x))
+                m = x.max()
+                p = np.exp(x - m)
+                z = p.sum()
+                p /= z
+                out[i, g], lse[i, g] = p @ v, m + np.log(z)
+                mean = p @ dx
+                dp = (2.0 ** -8 if c.fmt == "bf16" else 2.0 ** -11) + 2.0 ** -20 + len(t) * 2.0 ** -26
+                tol[i, g] = 2.0 ** -8 * np.abs(out[i, g]) + 1.004 * ((p * (dp + dx + mean)) @ np.abs(v))
+                if c.fmt == "e2m1":
+                    tol[i, g] += 2.0 ** -31 * np.abs(v).sum(0)
+                ltol[i, g] = mean + 2.0 ** -20 * (1 + abs(lse[i, g])) + len(t) * 2.0 ** -26
+    return out, lse, tol + 1e-38, ltol
+
+
+CAPS = [50.0, 1000.0, 1e5, 1e6, 2.0 ** 30, 2.0 ** 64]
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("lens,news,G", [([300, 90], [4, 1], 3), ([300, 90], [100, 35], 2)])
+def test_attend_caps_of_any_size(fx, fmt, cap, lens, news, G):  # noqa: F811
+    """Ordinary logits under caps of any size keep their fp32 bits, in steps and in prompts, also beside a query whose logits
+    lie past the cap."""
+    c = pr.Cache(fmt, lens, 1, 32, seed=G)
+    g = np.random.default_rng(7)
+    start = np.concatenate(([0], np.cumsum(news)))
+    n = int(start[-1])
+    q = pr.bf16(4.0 * g.standard_normal((n, G, D)))
+    q[1, 0] = pr.bf16(np.clip(cap, 1e3, 2.0 ** 64) * q[1, 0])
+    rest = np.ones((n, G), bool)
+    rest[1, 0] = False
+    sl = np.full(G, 2.0 ** -7)
+    dev, t, st = c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32)
+    mixed = max(news) * G > 64
+    for slope in (None, sl):
+        got = fx.fx_paged_attend(dev, t, st, max_new=max(news), cap=cap, want_lse=True,
+                                 slope=None if slope is None else cu(slope, torch.float32))
+        out, lse = (x.double().cpu().numpy() for x in got)
+        assert np.isfinite(out).all() and np.isfinite(lse).all()
+        q1 = q.copy()
+        q1[1, 0] = 0.0                               # (not compared)
+        r, rl, tol, ltol = tight_ref(c, q1, start, D ** -0.5, cap, slope, mixed)
+        assert np.all((np.abs(lse - rl) <= ltol)[rest]), (np.abs(lse - rl) / ltol)[rest].max()
+        assert np.all((np.abs(out - r) <= tol)[rest]), (np.abs(out - r) / tol)[rest].max()
