@@ -1142,6 +1142,11 @@ fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void
     p.cap = q->cap;
     p.icap = q->cap > 0.f ? 1.f / q->cap : 0.f;
     p.cap2 = q->cap > 0.f ? q->cap * 1.4426950408889634f : 1.f;
+    // The logits' factor over the cap is one number where that is a normal one, and stays so with the factor of a 4-bit
+    // cache's queries (up to 2^113); else two, of which the second finds logits that fit fp32.
+    const float unit = fabsf(p.qscale * p.icap);
+    p.cap_apart = !(unit >= 0x1p-126f && unit <= 0x1p14f);
+    p.cap_unit = p.cap_apart ? p.qscale : p.qscale * p.icap;
     p.out16 = q->out;
     p.lse = q->lse;
     p.counters = static_cast<unsigned*>(ws);

@@ -330,6 +330,8 @@ struct PagedAttnParams {
     const float* slope;
     int n, window;
     float cap, icap, cap2;    // icap = 1 / cap; cap2: from a tanh to a base-2 logit (1 without a cap)
+    float cap_unit;           // from a query's product to tanh's argument, or (cap_apart) qscale, and icap follows by itself
+    int cap_apart;
     uint16_t* out16;          // [n, Hq, 128]
 };
 

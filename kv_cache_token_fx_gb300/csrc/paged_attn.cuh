@@ -763,7 +763,7 @@ __device__ __forceinline__ float4 lds_float4(uint32_t a)
 template <bool CAP, int U, int NT>
 __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Shaping& sh, float (&s)[U * NT][4], int first)
 {
-    const float unit = p.qscale * (CAP ? p.icap : 1.4426950408889634f);
+    const float unit = CAP ? p.cap_unit : p.qscale * 1.4426950408889634f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float f0 = unit, f1 = unit;
@@ -778,6 +778,12 @@ __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Sha
             for (int e = 0; e < 4; ++e) s[u * NT + n][e] *= e & 1 ? f1 : f0;
     }
     if (CAP) {
+        if (p.cap_apart) {
+#pragma unroll
+            for (int m = 0; m < U * NT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[m][e] *= p.icap;
+        }
         float top = 0.f;
 #pragma unroll
         for (int m = 0; m < U * NT; ++m)

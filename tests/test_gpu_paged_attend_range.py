@@ -119,3 +119,23 @@ def test_attend_caps_of_any_size(fx, fmt, cap, lens, news, G):  # noqa: F811
         r, rl, tol, ltol = tight_ref(c, q1, start, D ** -0.5, cap, slope, mixed)
         assert np.all((np.abs(lse - rl) <= ltol)[rest]), (np.abs(lse - rl) / ltol)[rest].max()
         assert np.all((np.abs(out - r) <= tol)[rest]), (np.abs(out - r) / tol)[rest].max()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("G,n", [(2, 2), (4, 4), (2, 90)])
+def test_attend_scales_far_from_caps(fx, fmt, G, n):  # noqa: F811
+    """Scales whose quotient by the cap leaves the range of fp32: ordinary logits, and queries of zeros under them.  (Queries
+    stay below 2^122 and the magnitudes of a logit's products below 2^127 in all, so that fp32 holds the sums.)"""
+    c = pr.Cache(fmt, [200], 1, 32, seed=G)
+    g = np.random.default_rng(9)
+    start = np.array([0, n])
+    dev, st = c.device(fx), cu(start, torch.int32)
+    q = pr.bf16(4.0 * g.standard_normal((n, G, D)))
+    q[n // 2] = 0.0
+    for e, cap in ((-80, 2.0 ** 64), (-100, 2.0 ** 30), (-118, 60.0), (100, 2.0 ** -60), (70, 2.0 ** -64)):
+        scale, q1 = 2.0 ** (e - 3), q * 2.0 ** -e
+        got = fx.fx_paged_attend(dev, cu(q1, torch.bfloat16), st, max_new=n, scale=scale, cap=cap, want_lse=True)
+        out, lse = (x.double().cpu().numpy() for x in got)
+        r, rl, tol, ltol = tight_ref(c, q1, start, scale, cap, None, n * G > 64)
+        assert np.all(np.abs(lse - rl) <= ltol), (e, cap, np.abs(lse - rl).max())
+        assert np.all(np.abs(out - r) <= tol), (e, cap)
