@@ -750,7 +750,8 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, const Seq& q
 // 4-bit rows have least of.
 struct Shaping {
     const int2* see;      // what the query positions see
-    uint32_t rows;        // of rows 2t, 2t + 1 of each N tile (64 bytes a tile): their positions, their slopes (base 2)
+    uint32_t rows;        // of rows 2t, 2t + 1 of each N tile (64 bytes a tile): their positions from the first query's on,
+                          // their slopes (base 2)
     uint32_t factors;     // of the rows' logits (32 bytes a tile), or 0: one factor for all
 };
 __device__ __forceinline__ float4 lds_float4(uint32_t a)
@@ -758,7 +759,8 @@ __device__ __forceinline__ float4 lds_float4(uint32_t a)
     const uint4 v = lds128(a);
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
-// Logits of U tiles whose first row is `first`, as logits() gives them: under the cap, and with their bias by distance as
+// Logits of U tiles whose first row is `first` (from the first query's position on, as the queries': near rows then have their
+// exact distances at any length of the cache, which positions past 2^24 by themselves do not have in fp32), as logits() gives them: under the cap, and with their bias by distance as
 // base-2 logits (without one, the factor of a capped logit, p.cap2, is left to weights()).
 template <bool CAP, int U, int NT>
 __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Shaping& sh, float (&s)[U * NT][4], int first)
@@ -802,7 +804,7 @@ __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Sha
         }
     }
     if (p.slope) {
-        const float row = (float)(first + ((threadIdx.x & 31) >> 2));
+        const float row = (float)(first + (int)((threadIdx.x & 31) >> 2));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float4 w = lds_float4(sh.rows + 64 * n);
@@ -1426,12 +1428,12 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
         Seq seq = line.seq;
         const int seen = seq.len - p.Mq;   // query i sees rows <= seen + i
         seq.idx = p.idx ? p.idx + ((int64_t)b * p.c.Hkv + h) * p.kk : nullptr;
-        const int base = seq.lo & ~(kTileRows - 1);   // first row of the first tile
+        const int base = SHAPED ? (seq.lo & ~(kTileRows - 1)) - seq.pos0 : 0;   // first row of the first tile, from the first query on
         if (SHAPED) {
             for (int i = tid; i < p.Mq; i += 32 * W) sm_see[i] = i < seq.nb ? shaped_interval(p, seq, i) : make_int2(0, 0);
             if (tid < 8 * NT) {
                 const int r = r0 + (DUP ? tid & 3 : tid);
-                sm_row[tid] = make_float2((float)(seq.pos0 + query_pos(p, r)),
+                sm_row[tid] = make_float2((float)query_pos(p, r),
                                           p.slope && r < p.R ? p.slope[h * p.G + r / p.Mq] * 1.4426950408889634f : 0.f);
             }
         }
@@ -1452,7 +1454,7 @@ __global__ void __launch_bounds__(32 * Shape<E2M1, NT, DUP, U>::kWarps, Shape<E2
         // kStages - 1 turns ahead
         Feeder<E2M1, true, U, SHAPED> feeder(p, seq, h, warp_start<U, W>(seq, s0, s1, warp), warp_start<U, W>(seq, s0, s1, warp + 1));
         uint32_t flags[kStages];   // of the units in the ring, oldest first
-        int first[kStages];        // SHAPED: their first rows
+        int first[kStages];        // SHAPED: their first rows, from the first query on
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) {
             if (SHAPED) first[k] = base + feeder.it * kTileRows;

@@ -139,3 +139,25 @@ def test_attend_scales_far_from_caps(fx, fmt, G, n):  # noqa: F811
         r, rl, tol, ltol = tight_ref(c, q1, start, scale, cap, None, n * G > 64)
         assert np.all(np.abs(lse - rl) <= ltol), (e, cap, np.abs(lse - rl).max())
         assert np.all(np.abs(out - r) <= tol), (e, cap)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("n,G", [(1, 4), (5, 3), (90, 2)])
+def test_attend_bias_far_into_a_cache(fx, fmt, n, G):  # noqa: F811
+    """Distances of near rows are exact where positions are past 2^24, as at the start of a cache."""
+    ahead = 1024 * 20001                                     # rows before the ones that are seen; fp32 holds every second
+    c = pr.Cache(fmt, [300], 2, 1024, seed=n)
+    g = np.random.default_rng(n)
+    q = cu(pr.bf16(2.0 * g.standard_normal((n, 2 * G, D))), torch.bfloat16)
+    sl = cu(2.0 ** (1 - np.arange(2 * G)), torch.float32)
+    near = c.device(fx)
+    table = torch.full((1, ahead // 1024 + 1), -7, dtype=torch.int32, device="cuda")
+    table[:, ahead // 1024:] = near.table[:, :1]
+    far = fx.PagedKV(near.k, near.v, table, near.length + ahead, k_scale=near.k_scale, v_scale=near.v_scale)
+    start = np.array([0, n])
+    for cap in (0.0, 20.0):
+        kw = dict(max_new=n, slope=sl, cap=cap, want_lse=True)
+        got = fx.fx_paged_attend(far, q, cu(start, torch.int32), first=torch.full((n,), ahead, dtype=torch.int32, device="cuda"), **kw)
+        ref = attend_ref(c, q.double().cpu().numpy(), start, D ** -0.5, cap=cap, slope=sl.double().cpu().numpy())
+        check(c, got, ref)
+        check(c, fx.fx_paged_attend(near, q, cu(start, torch.int32), **kw), ref)
