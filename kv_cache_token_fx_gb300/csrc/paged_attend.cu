@@ -892,6 +892,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
         const int my_lo = live ? lo : -0x40000000, my_hi = live ? hi : 0x7fffffff;
         const float cap = p.cap, icap = cap > 0.f ? 1.f / cap : 0.f;
         const float slope2 = MODE == kBias && live ? p.slope[g] * 1.4426950408889634f : 0.f;
+        // A bias that grows along a tile is added from the tile's first key on, 127 slopes long, and taken off again with the
+        // reference: 2^-24 of that is lost, so that slopes past 2 (base 2: 2^-16 of a logit there) are taken key by key.
+        const int linear_from = !live ? 0x7fffffff : (fabsf(slope2) <= 2.f ? pos : -0x7fffffff);
         if (MODE == kPlain) qs *= 1.4426950408889634f;
         // from s to y of tanh(y); finite with its factors, so that a logit of 0 stays 0
         const float k = fminf(qs * icap, 0x1p126f), k2 = k * 2.885390081777927f;
@@ -1029,7 +1032,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     f = (cap > 0.f ? cap : qs) * 1.4426950408889634f;
                     if (MODE == kBias) {
                         const float d0 = (float)(pos - j0);
-                        if (!__any_sync(0xffffffffu, live && pos < j0 + kKeys - 1)) {
+                        if (!__any_sync(0xffffffffu, linear_from < j0 + kKeys - 1)) {
                             // all keys lie before the queries: their bias grows by slope from one to the next
                             off = -slope2 * d0;
 #pragma unroll

@@ -161,3 +161,23 @@ def test_attend_bias_far_into_a_cache(fx, fmt, n, G):  # noqa: F811
         ref = attend_ref(c, q.double().cpu().numpy(), start, D ** -0.5, cap=cap, slope=sl.double().cpu().numpy())
         check(c, got, ref)
         check(c, fx.fx_paged_attend(near, q, cu(start, torch.int32), **kw), ref)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("lens,news", [([300, 90], [4, 1]), ([400, 90], [200, 80]),
+                                       ([399, 90], [200, 80])])    # (a warp's first token sees itself as a tile's last key)
+def test_attend_steep_biases(fx, fmt, lens, news):  # noqa: F811
+    """A bias of any slope leaves the logits of near rows their fp32 bits."""
+    G = 4
+    c = pr.Cache(fmt, lens, 1, 32, seed=len(lens))
+    g = np.random.default_rng(11)
+    start = np.concatenate(([0], np.cumsum(news)))
+    q = pr.bf16(2.0 * g.standard_normal((int(start[-1]), G, D)))
+    for slopes in ([0.5, 0.0, 1.3, -0.02], [2.0, 30.0, 1000.0, 3e4], [-1.0, 1e6, 2.0 ** 20, 1.0]):
+        sl = np.float32(slopes).astype(np.float64)
+        got = fx.fx_paged_attend(c.device(fx), cu(q, torch.bfloat16), cu(start, torch.int32), max_new=max(news),
+                                 slope=cu(sl, torch.float32), want_lse=True)
+        out, lse = (x.double().cpu().numpy() for x in got)
+        r, rl, tol, ltol = tight_ref(c, q, start, D ** -0.5, 0.0, sl)
+        assert np.all(np.abs(lse - rl) <= ltol), (slopes, (np.abs(lse - rl) / ltol).max())
+        assert np.all(np.abs(out - r) <= tol), (slopes, (np.abs(out - r) / tol).max())
