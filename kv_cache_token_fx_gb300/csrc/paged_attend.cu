@@ -1032,9 +1032,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                     f = (cap > 0.f ? cap : qs) * 1.4426950408889634f;
                     if (MODE == kBias) {
                         const float d0 = (float)(pos - j0);
-                        if (!__any_sync(0xffffffffu, linear_from < j0 + kKeys - 1)) {
-                            // all keys lie before the queries: their bias grows by slope from one to the next
-                            off = -slope2 * d0;
+                        off = -slope2 * d0;
+                        if (!__any_sync(0xffffffffu, linear_from < j0 + kKeys - 1 || fabsf(off) > kFarRef)) {
+                            // all keys lie before the queries: their bias grows by slope from one to the next (not where it is
+                            // so large that it and the reference, rounded each for itself, lie apart)
 #pragma unroll
                             for (int i = 0; i < 64; ++i) {
                                 const float2 y = fma2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(f, f),
@@ -1045,6 +1046,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid
                         } else {
 #pragma unroll
                             for (int i = 0; i < 128; ++i) s[i] = fmaf(fabsf(d0 - (float)i), -slope2, s[i] * f);
+                            off = 0.f;
                         }
                         f = 1.f;
                     }

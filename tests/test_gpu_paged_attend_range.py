@@ -181,3 +181,29 @@ def test_attend_steep_biases(fx, fmt, lens, news):  # noqa: F811
         r, rl, tol, ltol = tight_ref(c, q, start, D ** -0.5, 0.0, sl)
         assert np.all(np.abs(lse - rl) <= ltol), (slopes, (np.abs(lse - rl) / ltol).max())
         assert np.all(np.abs(out - r) <= tol), (slopes, (np.abs(out - r) / tol).max())
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("n", [1, 70])
+def test_attend_only_rows_far_away(fx, fmt, n):  # noqa: F811
+    """Tokens that see nothing but rows millions of positions before them, with a bias: fp32 holds those logits to 2^-24 of
+    themselves only, but the weights stay weights.  (n = 70: 140 query rows, of a prompt's kernel.)"""
+    c = pr.Cache(fmt, [300], 1, 1024, seed=n)
+    g = np.random.default_rng(n)
+    near = c.device(fx)
+    q = cu(pr.bf16(2.0 * g.standard_normal((n, 2, D))), torch.bfloat16)
+    last = torch.full((n,), 300, dtype=torch.int32, device="cuda")
+    start = cu(np.array([0, n]), torch.int32)
+    v = c.rows(1, 0, 0, np.arange(300))
+    for ahead in (1 << 22, 1 << 25, 1 << 27, 1 << 29):
+        table = torch.full((1, ahead // 1024 + 1), -7, dtype=torch.int32, device="cuda")
+        table[0, 0] = near.table[0, 0]
+        far = fx.PagedKV(near.k, near.v, table, torch.tensor([ahead + 300], dtype=torch.int32, device="cuda"),
+                         k_scale=near.k_scale, v_scale=near.v_scale)
+        for slope in (0.7, 1.3):
+            sl = torch.full((2,), slope, device="cuda")
+            out, lse = fx.fx_paged_attend(far, q, start, max_new=n, last=last, slope=sl, want_lse=True)
+            out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+            assert np.isfinite(out).all() and np.isfinite(lse).all()
+            assert np.all(out <= v.max(0) + 0.01 * abs(v.max(0))) and np.all(out >= v.min(0) - 0.01 * abs(v.min(0)))
+            assert np.all(np.abs(lse / -(slope * ahead) - 1) < 0.001)
