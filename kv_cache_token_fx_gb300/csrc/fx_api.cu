@@ -1073,6 +1073,14 @@ fx_status paged_view(const fx_paged_desc* d, bool need_len, PagedCache* c)
     return FX_OK;
 }
 
+// The decode's kernels count the tiles of 16 rows of all (sequence, KV head, 4 or more query rows), and the starts of these,
+// in 32 bits: whether a call of `rows` query rows a KV head and k listed rows has that many, by the room of its tables.
+bool decode_counts(const PagedCache& c, int rows, int k)
+{
+    const int64_t tiles = c.cap / 16 + k / 16 + 2 + kPieceStart, groups = rows / 4 + 1;
+    return tiles * c.B * c.Hkv < ((int64_t)1 << 31) / groups;
+}
+
 // The checks that fx_paged_decode and fx_paged_importance share; fills the queries' part of p.
 fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_stride_b, int64_t q_stride_h,
                         int64_t q_stride_i, int Hq, int Mq, int k, float scale, unsigned flags, PagedAttnParams* p)
@@ -1086,10 +1094,7 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
     if (!row_stride_ok(q_stride_b) || !row_stride_ok(q_stride_h) || !row_stride_ok(q_stride_i))
         return fail(FX_ERR_INVALID_ARG, "q strides must be non-negative multiples of 8 elements");
     if (!isfinite(scale)) return fail(FX_ERR_INVALID_ARG, "scale must be finite");
-    // the kernels count the tiles of 16 rows of all (sequence, KV head, 4 or more query rows), and the starts of these, in
-    // 32 bits
-    const int64_t tiles = p->c.cap / 16 + k / 16 + 2 + kPieceStart, groups = (int64_t)(Hq / cache->Hkv) * Mq / 4 + 1;
-    if (tiles * cache->B * cache->Hkv >= ((int64_t)1 << 31) / groups)
+    if (!decode_counts(p->c, Hq / cache->Hkv * Mq, k))
         return fail(FX_ERR_UNSUPPORTED, "more than 2^31 tiles of 16 rows over all sequences and heads");
     p->q = q;
     p->q_b = q_stride_b;
@@ -1111,8 +1116,8 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
 // heads' 1024 bf16 rows, 24 query rows 15.9 and 19.6; 8 heads' 8192, 64 query rows 32 and 34.
 bool attend_takes_few(const PagedCache& c, bool e2m1, int rows, bool cap)
 {
+    if (rows > kMaxRows || !decode_counts(c, rows, 0)) return false;   // (more tiles than the decode counts: prompts' kernel)
     if (rows <= 16) return true;
-    if (rows > kMaxRows) return false;
     return (rows <= 32 && (e2m1 || cap)) || (int64_t)c.B * c.Hkv * c.cap <= 1 << 17;
 }
 // Scratch memory of a call, whichever kernel takes it.

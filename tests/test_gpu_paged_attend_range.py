@@ -207,3 +207,24 @@ def test_attend_only_rows_far_away(fx, fmt, n):  # noqa: F811
             assert np.isfinite(out).all() and np.isfinite(lse).all()
             assert np.all(out <= v.max(0) + 0.01 * abs(v.max(0))) and np.all(out >= v.min(0) - 0.01 * abs(v.min(0)))
             assert np.all(np.abs(lse / -(slope * ahead) - 1) < 0.001)
+
+
+@pytest.mark.parametrize("fmt,G,new", [("bf16", 4, 4), ("e2m1", 8, 1), ("bf16", 1, 1)])
+def test_attend_steps_over_tables_with_room_for_billions(fx, fmt, G, new):  # noqa: F811
+    """Steps whose tables have more room than the decode's kernels count tiles of: the prompts' kernel takes them."""
+    B, Hkv, few = 2048, 8, 8
+    pages = 1024 * (2 if G == 1 else 1)                  # of 1024 rows: 2^20 rows of room a sequence
+    g = np.random.default_rng(G)
+    lens = [int(x) for x in g.integers(new, 80, few)]
+    c = pr.Cache(fmt, lens, Hkv, 1024, seed=G)
+    dev = c.device(fx)
+    table = torch.full((B, pages), -7, dtype=torch.int32, device="cuda")
+    table[:, 0] = dev.table[:, 0].repeat(B // few)
+    big = fx.PagedKV(dev.k, dev.v, table, dev.length.repeat(B // few), k_scale=dev.k_scale, v_scale=dev.v_scale)
+    assert B * Hkv * (G * new // 4 + 1) * (pages * 64 + 34) >= 1 << 31
+    q = pr.bf16(2.0 * g.standard_normal((few * new, Hkv * G, D)))
+    t = cu(q, torch.bfloat16)
+    out, lse = fx.fx_paged_attend(big, t.repeat(B // few, 1, 1), want_lse=True)
+    out, lse = out.view(B // few, few * new, -1, D), lse.view(B // few, few * new, -1)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    check(c, (out[0], lse[0]), attend_ref(c, q, np.arange(few + 1) * new, D ** -0.5))
