@@ -639,7 +639,8 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
  *   q         bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h;   out bf16 [n, Hq, 128], lse fp32 [n, Hq], contiguous;
  *             they overlap nothing that the call reads
  *   max_new   host: tokens of one sequence, at most (G*max_new <= 2^30, n <= 2^30, n*Hq < 2^31)
- * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes.
+ * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes, which suffice for every smaller max_new of that B too
+ * (calls of few tokens may need more than long ones: they are cut along the cache).
  */
 typedef struct {
     const fx_bf16* q;

@@ -1127,6 +1127,13 @@ size_t attend_workspace_bytes(int B, int Hkv, int G, int max_new, int sms)
     const size_t few = (int64_t)G * max_new <= kMaxRows ? paged_decode_workspace_bytes(G * max_new, sms) : 0;
     return many > few ? many : few;
 }
+// Scratch memory of any call with up to max_new tokens a sequence: fewer of them may need more, as only calls of few blocks are
+// cut into parts.
+size_t attend_workspace_bound(int B, int Hkv, int G, int max_new, int sms)
+{
+    const int64_t rows = (int64_t)G * max_new;
+    return std::max(paged_attend_workspace_bound(B, Hkv, rows, sms), paged_decode_workspace_bytes((int)std::min<int64_t>(rows, kMaxRows), sms));
+}
 
 // fx_paged_attend by the decode's kernels; the call's own checks are done.
 fx_status attend_few(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags, void* stream)
@@ -1426,8 +1433,7 @@ fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* q, int6
 size_t fx_paged_attend_workspace_bytes(int B, int Hkv, int Hq, int max_new)
 {
     if (B < 1 || Hkv < 1 || Hq < Hkv || max_new < 1 || (int64_t)(Hq / Hkv) * max_new > (1ll << 30)) return 0;
-    const int sms = sm_count_or_default(), G = Hq / Hkv;
-    return attend_workspace_bytes(B, Hkv, G, max_new, sms);
+    return attend_workspace_bound(B, Hkv, Hq / Hkv, max_new, sm_count_or_default());
 }
 
 fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q, void* ws, size_t ws_bytes, unsigned flags,

@@ -392,6 +392,7 @@ cudaError_t launch_paged_attend_few_e2m1_cap(const PagedAttnParams& p, int sm_co
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s);
 PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count);
 size_t paged_attend_workspace_bytes(const PagedAttendCut& c);
+size_t paged_attend_workspace_bound(int B, int Hkv, int64_t rows, int sm_count);
 
 // Launch `kern` with optional programmatic stream serialization and a (1, cluster_y, 1) cluster.
 template <typename... KArgs, typename... Args>

@@ -1285,6 +1285,15 @@ size_t paged_attend_workspace_bytes(const PagedAttendCut& c)
 {
     return c.split ? kCounterBytes + (size_t)c.split * c.part_rows * (kHeadDim + 2) * sizeof(float) : kCounterBytes;
 }
+// Of every call of up to `rows` query rows a (sequence, KV head): one of a single block each is cut if any is, and a part has
+// no more rows than a block.
+size_t paged_attend_workspace_bound(int B, int Hkv, int64_t rows, int sm_count)
+{
+    PagedAttendCut c;
+    c.split = paged_attend_cut(B, Hkv, 1, 1, sm_count).split;
+    c.part_rows = (int)(rows < kBlock ? rows : kBlock);
+    return paged_attend_workspace_bytes(c);
+}
 
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s)
 {

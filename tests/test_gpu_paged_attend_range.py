@@ -228,3 +228,22 @@ def test_attend_steps_over_tables_with_room_for_billions(fx, fmt, G, new):  # no
     out, lse = out.view(B // few, few * new, -1, D), lse.view(B // few, few * new, -1)
     assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
     check(c, (out[0], lse[0]), attend_ref(c, q, np.arange(few + 1) * new, D ** -0.5))
+
+
+def test_attend_one_workspace_for_prompt_chunks_and_steps(fx):  # noqa: F811
+    """Scratch memory sized once, for the longest prompt, serves every shorter call of the same sequences (through the C entry
+    point, which grows nothing)."""
+    c = pr.Cache("bf16", [700], 2, 32, seed=1)
+    dev, G = c.device(fx), 4
+    g = np.random.default_rng(1)
+    lib = fx.load_library()
+    nbytes = fx.fx_paged_attend_workspace_bytes(1, 2, 2 * G, 8191)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    for n in (700, 1, 100, 4, 16, 65, 300):
+        q = pr.bf16(2.0 * g.standard_normal((n, 2 * G, D)))
+        t = cu(q, torch.bfloat16)
+        out, lse = torch.zeros(n, 2 * G, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 2 * G, device="cuda")
+        qs = fx.PagedQueries(t.data_ptr(), 2 * G * D, D, None, None, None, None, out.data_ptr(), lse.data_ptr(), n, 2 * G, n, 0,
+                             D ** -0.5, 0.0)
+        assert lib.fx_paged_attend(dev._ref, bytes(qs), ws.data_ptr(), nbytes, 0, None) == 0, lib.fx_last_error()
+        check(c, (out, lse), attend_ref(c, q, np.array([0, n]), D ** -0.5))
