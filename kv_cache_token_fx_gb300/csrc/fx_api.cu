@@ -1298,11 +1298,26 @@ fx_status fx_paged_compact(const fx_paged_desc* src, const fx_paged_desc* dst, c
     if ((st = check_flags(flags)) != FX_OK) return st;
     if (src->format != dst->format || src->B != dst->B || src->Hkv != dst->Hkv || src->k_exp != dst->k_exp || src->v_exp != dst->v_exp)
         return fail(FX_ERR_INVALID_ARG, "src and dst must have one format (and exponents), B and Hkv");
-    if (src->len == dst->len || src->table == dst->table || (tail_lo && tail_lo == dst->len))
-        return fail(FX_ERR_INVALID_ARG, "dst needs a page table and lengths of its own");
+    if (src->table == dst->table) return fail(FX_ERR_INVALID_ARG, "dst needs a page table of its own");
     if (!pool_apart(dst)) return fail(FX_ERR_INVALID_ARG, "dst: the pool's rows share memory, so none can be written");
     if (k < 0 || (k > 0 && !idx)) return fail(FX_ERR_INVALID_ARG, "need k >= 0 and idx when k > 0");
     if (k > (1 << 30)) return fail(FX_ERR_UNSUPPORTED, "k is at most 2^30");
+    // (dst's lengths are written while other blocks read the rest)
+    auto meets_lengths = [&](const int32_t* at, int64_t n) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), len = reinterpret_cast<uintptr_t>(dst->len);
+        return at && n > 0 && a < len + 4 * (uintptr_t)dst->B && len < a + 4 * (uintptr_t)n;
+    };
+    auto meets_table = [&](const fx_paged_desc* d) {
+        bool any = meets_lengths(d->table, (d->B - 1) * d->table_stride + d->max_pages);
+        if (any && d->table_stride > d->max_pages) {   // (or they lie between its rows)
+            any = false;
+            for (int b = 0; b < d->B && !any; ++b) any = meets_lengths(d->table + b * d->table_stride, d->max_pages);
+        }
+        return any;
+    };
+    if (meets_lengths(src->len, src->B) || meets_lengths(tail_lo, src->B) || meets_table(src) || meets_table(dst) ||
+        (k > 0 && meets_lengths(idx, (int64_t)src->B * src->Hkv * k)))
+        return fail(FX_ERR_INVALID_ARG, "dst needs lengths of its own: they overlap what the call reads");
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != FX_OK) return st;
     p.idx = k > 0 ? idx : nullptr;

@@ -247,3 +247,17 @@ def test_attend_one_workspace_for_prompt_chunks_and_steps(fx):  # noqa: F811
                              D ** -0.5, 0.0)
         assert lib.fx_paged_attend(dev._ref, bytes(qs), ws.data_ptr(), nbytes, 0, None) == 0, lib.fx_last_error()
         check(c, (out, lse), attend_ref(c, q, np.array([0, n]), D ** -0.5))
+
+
+def test_compact_lengths_between_the_rows_of_a_table(fx):  # noqa: F811
+    """Lengths may lie in the room between a table's rows: nothing that is read is written."""
+    c = pr.Cache("bf16", [50, 33], 1, 16, seed=3)
+    src = c.device(fx)
+    room = torch.full((2, 16), -1, dtype=torch.int32, device="cuda")
+    room[:, :4] = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    k, v = (torch.zeros(8, 1, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dst = fx.PagedKV(k, v, room[:, :4], room.view(-1)[6:8])
+    fx.fx_paged_compact(src, dst, tail_lo=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert dst.length.tolist() == c.lens
+    for a, b in zip(fx.fx_paged_gather(src, 33), fx.fx_paged_gather(dst, 33)):
+        assert torch.equal(a, b)
