@@ -1049,13 +1049,13 @@ __device__ __forceinline__ bool not_all_finite(uint32_t slot, int u, int from, i
 {
     const int lane = threadIdx.x & 31;
     const int pos = (int)lds32(slot + S::kPos + 64 * u + 4 * (lane & 15));
-    const bool some = pos >= to || (pos >= 0 && pos < from);
+    auto outside = [&](int t) { return t >= to || (t >= 0 && t < from); };
+    const bool some = outside(pos);
     if (!__any_sync(kFull, some)) return false;
     bool bad = false;
     if (E2M1) {   // a NaN scale (the lane looks at half the scales of row lane / 2)
         const uint32_t z = lds32(slot + S::kScaleV + 128 * u + 4 * lane) & 0x7f7f7f7fu;
-        const bool of = __shfl_sync(kFull, some, lane >> 1);
-        bad = of && __vcmpeq4(z, 0x7f7f7f7fu) != 0;
+        bad = outside(__shfl_sync(kFull, pos, lane >> 1)) && __vcmpeq4(z, 0x7f7f7f7fu) != 0;
     } else {      // an all-ones exponent
         for (int j = 0; j < 16; ++j) {
             const uint2 z = lds64(slot + S::kV + u * S::kTile + 256 * j + 8 * lane);
