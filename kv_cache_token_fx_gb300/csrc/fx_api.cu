@@ -1110,15 +1110,25 @@ fx_status paged_queries(const fx_paged_desc* cache, const fx_bf16* q, int64_t q_
 }
 
 // Whether the decode's kernels take a call of fx_paged_attend: of up to 16 query rows a (sequence, KV head), which are one
-// pass over the cache, always; of more (a pass for every 16) where the prompts' kernel takes longer.  Steps of 8 x 32768
-// rows, 8 KV heads, us: bf16, 20 query rows 235 here, 178 there; with a cap 249 and 380; 64 rows with a cap 485 and 387; 4 bits,
-// 32 query rows 152 and 199, 64 rows 281 and 200.  Little work (by the room that the tables have) starts sooner here: 2 x 4
-// heads' 1024 bf16 rows, 24 query rows 15.9 and 19.6; 8 heads' 8192, 64 query rows 32 and 34.
+// pass over the cache, always; of more (a pass for every 16) where the prompts' kernel takes longer.  us here and there, 4
+// heads, 20 to 32 query rows | 40 and 48 | 64:
+//   8 x 32768 rows, 8 KV heads   bf16 241, 178 | 283, 179 | 428, 180     4 bits 152, 196 | 217, 196 | 279, 197
+//     with a cap                      252, 375 | 363, 375 | 481, 376            215, 388 | 305, 388 | 403, 389
+//   64 x 3328, 8                      197, 131 | 281, 131 | 370, 133            149, 143 | 212, 143 | 285, 144
+//     with a cap                      228, 240 | 333, 242 | 441, 244            210, 253 | 300, 253 | 405, 254
+//   8 x 8192, 8                        72,  55 |  94,  55 | 121,  56             55,  57 |  74,  57 |  93,  58
+//   8 x 1024, 8                        20,  20 |  23,  20 |  27,  22             21,  21 |  23,  22 |  23,  23
+//     with a cap                       23,  26 |  27,  27 |  33,  28             28,  29 |  32,  29 |  35,  31
+//   2 x 8192, 1                        24,  23 |  24,  26 |  24,  26             25,  24 |  26,  27 |  26,  27
+//     with a cap                       26,  31 |  25,  34 |  25,  34             27,  33 |  29,  36 |  29,  36
+//   2 x 1024, 4                        15,  19 |  15,  21 |  16,  21             18,  21 |  18,  22 |  18,  23
+// So: up to 32 rows in 4 bits or with a cap, and the little work (by the room that the tables have: lengths are on the device)
+// of the last two lines.  The prompts' kernel rounds weights that the decode's holds in two or three parts.
 bool attend_takes_few(const PagedCache& c, bool e2m1, int rows, bool cap)
 {
     if (rows > kMaxRows || !decode_counts(c, rows, 0)) return false;   // (more tiles than the decode counts: prompts' kernel)
     if (rows <= 16) return true;
-    return (rows <= 32 && (e2m1 || cap)) || (int64_t)c.B * c.Hkv * c.cap <= 1 << 17;
+    return (rows <= 32 && (e2m1 || cap)) || (int64_t)c.B * c.Hkv * c.cap <= 1 << 14;
 }
 // Scratch memory of a call, whichever kernel takes it.
 size_t attend_workspace_bytes(int B, int Hkv, int G, int max_new, int sms)
