@@ -460,8 +460,14 @@ cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStrea
     // 4.6 us, against 5.6 with four).  More rows than the machine has groups of 8 lanes: four rows each, for their shared
     // cosines and more loads in flight (a prompt of 24 K tokens with its read-back 92 us, against 124 with one).
     const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > sm_count * 2048 / 8;
-    // With axes two rows each and 10 CTAs an SM: the angles are more loads, which more warps wait for (four such prompts in
-    // bf16 94 us, against 103 with four rows and 8 CTAs, 100 with two and 8, 106 with two and 12).
+    // With axes two rows each and 10 CTAs an SM: the angles are more loads, which more warps wait for.  Four prompts of up to
+    // 8191 tokens, us with axes in sections and in turns:
+    //   rows, CTAs    bf16 halves    bf16 neighbours    4 bits halves    4 bits neighbours
+    //   2, 10           87,  92         84,  92            79,  91           76,  88
+    //   4, 8            97, 102         98, 105            85,  87           84,  88
+    //   2, 8            91,  98         95, 105            80,  94           81,  96
+    //   4, 10          102, 111        103, 109            99, 106           87,  92
+    //   1, 10          116, 131        124, 153           115, 138          123, 154
     constexpr int kMany = AXES ? 2 : 4;
     const int R = many ? kMany : 1;
     const int64_t groups = (int64_t)p.n * (2 * ((p.c.Hkv + R - 1) / R) + (p.Hq + R - 1) / R);
