@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(kThreadsRows, AXES ? 10 : 8) paged_append_kern
         seq = __ldg(p.seq + i);
         pos = __ldg(p.pos + i);
         at = p.rope_pos ? __ldg(p.rope_pos + i) : pos;
-        bool at_bad = p.rot > 0 && (at < 0 || at >= p.n_pos);
+        // Neighbours: tested before the chain below (prompts of up to 8191 tokens in 4 bits 71.2 us for 73.5).  Halves: within it
+        // (bf16 79.3 for 81.0); with axes, axis by axis (bf16 81.7 for 87.0).
+        bool at_bad = INTERLEAVED && p.rot > 0 && (at < 0 || at >= p.n_pos);
         if (AXES) {
 #pragma unroll
             for (int a = 0; a < kMaxAxes; ++a) {
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreadsRows, AXES ? 10 : 8) paged_append_kern
             bad = seq == -1 ? 0u : FX_DEVERR_INDEX;
         else if (pos < 0 || pos >= p.c.cap)
             bad = FX_DEVERR_LEN;
-        else if (at_bad)
+        else if (INTERLEAVED || AXES ? at_bad : p.rot > 0 && (at < 0 || at >= p.n_pos))
             bad = FX_DEVERR_INDEX;
         live = seq >= 0 && bad == 0;
         if (bad && in == 0 && l == 0) atomicOr(p.err, bad);
@@ -462,8 +464,9 @@ cudaError_t append(const PagedAppendParams& p, int sm_count, bool pdl, cudaStrea
     const bool many = (int64_t)p.n * (2 * p.c.Hkv + p.Hq) > sm_count * 2048 / 8;
     // With axes two rows each and 10 CTAs an SM: the angles are more loads, which more warps wait for.  Four prompts of up to
     // 8191 tokens, us with axes in sections and in turns:
-    //   rows, CTAs    bf16 halves    bf16 neighbours    4 bits halves    4 bits neighbours
-    //   2, 10           87,  92         84,  92            79,  91           76,  88
+    //   rows, CTAs    bf16 halves    bf16 neighbours    4 bits halves    4 bits neighbours   (halves: 5 us less in the first
+    //                                                                                        line since, as noted in the kernel)
+    //   2, 10           82,  86         84,  92            76,  88           76,  88
     //   4, 8            97, 102         98, 105            85,  87           84,  88
     //   2, 8            91,  98         95, 105            80,  94           81,  96
     //   4, 10          102, 111        103, 109            99, 106           87,  92
