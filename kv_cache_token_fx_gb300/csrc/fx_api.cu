@@ -1130,15 +1130,8 @@ bool attend_takes_few(const PagedCache& c, bool e2m1, int rows, bool cap)
     if (rows <= 16) return true;
     return (rows <= 32 && (e2m1 || cap)) || (int64_t)c.B * c.Hkv * c.cap <= 1 << 14;
 }
-// Scratch memory of a call, whichever kernel takes it.
-size_t attend_workspace_bytes(int B, int Hkv, int G, int max_new, int sms)
-{
-    const size_t many = paged_attend_workspace_bytes(paged_attend_cut(B, Hkv, G, max_new, sms));
-    const size_t few = (int64_t)G * max_new <= kMaxRows ? paged_decode_workspace_bytes(G * max_new, sms) : 0;
-    return many > few ? many : few;
-}
-// Scratch memory of any call with up to max_new tokens a sequence: fewer of them may need more, as only calls of few blocks are
-// cut into parts.
+// Scratch memory of any call with up to max_new tokens a sequence, over any table: fewer tokens may need more, as only calls of
+// few blocks are cut into parts.
 size_t attend_workspace_bound(int B, int Hkv, int G, int max_new, int sms)
 {
     const int64_t rows = (int64_t)G * max_new;
@@ -1488,11 +1481,13 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     if ((int64_t)G * q->max_new > (1ll << 30) || q->n > (1 << 30) || (int64_t)q->n * q->Hq > 0x7fffffff)
         return fail(FX_ERR_UNSUPPORTED, "queries: too many rows");
     const int sms = sm_count_or_default();
-    const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, sms);
+    const PagedAttendCut cut = paged_attend_cut(cache->B, cache->Hkv, G, q->max_new, p.c.cap, sms);
+    const bool few = attend_takes_few(p.c, cache->format == FX_PAGED_E2M1, G * q->max_new, q->cap > 0.f);
     if (!cut.split && cut.blocks > 65535) return fail(FX_ERR_UNSUPPORTED, "queries: too many of one sequence");
-    if ((st = check_ws(ws, ws_bytes, attend_workspace_bytes(cache->B, cache->Hkv, G, q->max_new, sms))) != FX_OK) return st;
-    if (attend_takes_few(p.c, cache->format == FX_PAGED_E2M1, G * q->max_new, q->cap > 0.f))
-        return attend_few(cache, q, ws, ws_bytes, flags, stream);
+    if (cut.slots > 32 * kSlotWords) return fail(FX_ERR_UNSUPPORTED, "a device of %d SMs", sms);
+    const size_t need = few ? paged_decode_workspace_bytes(G * q->max_new, sms) : paged_attend_workspace_bytes(cut);
+    if ((st = check_ws(ws, ws_bytes, need)) != FX_OK) return st;
+    if (few) return attend_few(cache, q, ws, ws_bytes, flags, stream);
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != FX_OK) return st;
     p.q = q->q;
@@ -1515,6 +1510,7 @@ fx_status fx_paged_attend(const fx_paged_desc* cache, const fx_paged_queries* q,
     p.blocks = cut.blocks;
     p.split = cut.split;
     p.part_rows = cut.part_rows;
+    p.slots = cut.slots;
     p.sm_count = ds->sm_count;
     p.counters = static_cast<unsigned*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);

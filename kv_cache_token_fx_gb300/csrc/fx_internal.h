@@ -284,6 +284,7 @@ struct PagedAttendCut {
     int blocks;      // blocks of query rows of one (sequence, KV head), at most
     int split;       // CTAs among which the blocks' tiles are shared, or 0: one CTA to a block
     int part_rows;   // query rows of a part
+    int slots;       // places for a CTA's sums over long rows, where there are no parts
 };
 struct PagedAttendParams {
     PagedCache c;
@@ -298,9 +299,9 @@ struct PagedAttendParams {
     uint32_t flip;            // 0x80008000: the queries' signs turn (a negative scale); else 0
     uint16_t* out;            // [n, Hq, 128]
     float* lse;               // [n, Hq] or nullptr
-    int blocks, split, part_rows, sm_count;
+    int blocks, split, part_rows, slots, sm_count;
     unsigned* counters;       // arrival counters (zero between calls), then the parts
-    float* part;              // [split][part_rows][128]
+    float* part;              // [split][part_rows][128], or sums [slots][256][128]
     float* part_ml;           // [split][part_rows][2]: reference (base 2) and sum
     unsigned* err;
 };
@@ -389,8 +390,13 @@ cudaError_t launch_paged_attend_few_bf16_open(const PagedAttnParams& p, int sm_c
 cudaError_t launch_paged_attend_few_bf16_cap(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend_few_e2m1_open(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend_few_e2m1_cap(const PagedAttnParams& p, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_bf16(const PagedAttendParams& p, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_e2m1(const PagedAttendParams& p, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_long_bf16(const PagedAttendParams& p, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_attend_long_e2m1(const PagedAttendParams& p, bool pdl, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedAttendParams& p, bool e2m1, bool pdl, cudaStream_t s);
-PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int sm_count);
+PagedAttendCut paged_attend_cut(int B, int Hkv, int G, int64_t max_new, int cap, int sm_count);
+constexpr int kSlotWords = 32;   // masks of the places taken: the last words of the counters
 size_t paged_attend_workspace_bytes(const PagedAttendCut& c);
 size_t paged_attend_workspace_bound(int B, int Hkv, int64_t rows, int sm_count);
 

@@ -261,3 +261,88 @@ def test_compact_lengths_between_the_rows_of_a_table(fx):  # noqa: F811
     assert dst.length.tolist() == c.lens
     for a, b in zip(fx.fx_paged_gather(src, 33), fx.fx_paged_gather(dst, 33)):
         assert torch.equal(a, b)
+
+
+def shared_pages(fx, fmt, T, Hkv, B=1, positive=False, pages=32):  # noqa: F811
+    """A cache of B sequences of T rows whose tables name a few pages of 1024 rows over and over: (cache, K and V of those pages in
+    64 bits [pages, Hkv, 1024, 128])."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    shape = (pages, Hkv, 1024)
+    if fmt == "bf16":
+        k, v = (torch.randn(*shape, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        v = v.abs() + 1 if positive else v
+        kw, vals = {}, [k.double(), v.double()]
+    else:
+        k, v = (torch.randint(0, 256, (*shape, D // 2), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2))
+        v = v & 0x77 if positive else v
+        kw = {n: torch.randint(0x30, 0x38, (*shape, 8), generator=g, device="cuda", dtype=torch.uint8) for n in ("k_scale", "v_scale")}
+        grid = torch.tensor(np.concatenate((pr.GRID, -pr.GRID)), device="cuda")
+        vals = [(grid[torch.stack((x & 15, x >> 4), -1).flatten(-2).long()].unflatten(-1, (8, 16)) *
+                 kw[n].view(torch.float8_e4m3fn).double()[..., None]).flatten(-2) for x, n in ((k, "k_scale"), (v, "v_scale"))]
+    table = (torch.arange(T // 1024, device="cuda") * 7 % pages).to(torch.int32).expand(B, -1).contiguous()
+    return fx.PagedKV(k, v, table, torch.full((B,), T, dtype=torch.int32, device="cuda"), **kw), vals
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T,n", [(1 << 20, 160), (1 << 22, 160), (1 << 22, 16)])
+def test_attend_sums_over_long_rows(fx, fmt, T, n):  # noqa: F811
+    """Equal weights over millions of rows of values of one sign: no part of the sum is lost.
+
+    64 query rows a token: 160 blocks, one to a CTA, or 16, cut along the cache.  Equal weights are powers of two, and so are the
+    sums of their pages: nothing is rounded there.  O's sum in the tensor core loses up to 2^-23 of itself with each of 2^17 / 16
+    products before it leaves for memory, 2^-10 in all; the sums there 2^-24 with each of T / 2^17 (2^-19 at most); the output is
+    rounded by 2^-8."""
+    G = 64
+    cache, (k, v) = shared_pages(fx, fmt, T, 4, positive=True)
+    q = torch.zeros(n, 4 * G, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = fx.fx_paged_attend(cache, q, last=torch.full((n,), T, dtype=torch.int32, device="cuda"), want_lse=True)
+    want = v[cache.table[0].long()[:32]].mean((0, 2))          # (every page comes up as often)
+    off = out.double().view(n, 4, G, D) / want[None, :, None] - 1
+    assert float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -19, float(off.abs().max())
+    assert float((lse.double() - np.log(T)).abs().max()) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("B,kw", [(160, {}), (160, dict(slope=True)), (160, dict(cap=5.0)), (160, dict(window=100000)),
+                                  (160, dict(window=200000)), (3, dict(slope=True)), (1, {}), (1, dict(window=140000, cap=5.0))])
+def test_attend_rows_past_a_flush(fx, fmt, B, kw):  # noqa: F811
+    """More rows than O's sums stay in the tensor core for, with references that move between: against 64 bits."""
+    T, G, n = 300 * 1024, 4, 17
+    cache, (k, v) = shared_pages(fx, fmt, T, 1, B=B)
+    g = torch.Generator(device="cuda").manual_seed(B)
+    q = torch.randn(B * n, G, D, generator=g, device="cuda").mul_(2).to(torch.bfloat16)
+    slope = torch.tensor([3e-5, -1e-4, 2e-3, 0.0], device="cuda") if kw.get("slope") else None
+    first = torch.zeros(B * n, dtype=torch.int32, device="cuda")
+    first[3::n], first[5::n] = 250000, T                        # one that sees the end only, one nothing
+    args = dict(max_new=n, first=first, slope=slope, window=kw.get("window", 0), cap=kw.get("cap", 0.0), want_lse=True)
+    start = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+    out, lse = fx.fx_paged_attend(cache, q, start, **args)
+    again = fx.fx_paged_attend(cache, q, start, **args)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    at = cache.table[0].long()
+    kk, vv = k[at, 0].flatten(0, 1), v[at, 0].flatten(0, 1)
+    t = torch.arange(T, device="cuda")
+    for b in sorted({0, B // 2, B - 1}):
+        for i in range(n):
+            pos, row = T - n + i, b * n + i
+            x = D ** -0.5 * q[row].double() @ kk.T
+            dx = 2.0 ** -19 * D ** -0.5 * q[row].double().abs() @ kk.T.abs()
+            if args["cap"]:
+                x = args["cap"] * torch.tanh(x / args["cap"])
+                dx = dx + 2.0 ** -20 * args["cap"]
+            if slope is not None:
+                far = slope.double()[:, None] * (pos - t).abs()
+                x, dx = x - far, dx + 2.0 ** -22 * (far.abs() + x.abs())
+            hidden = (t < first[row]) | (t > pos) | ((t <= pos - args["window"]) if args["window"] else False)
+            x = x.masked_fill(hidden, -np.inf)
+            z = torch.logsumexp(x, -1)
+            if first[row] == T:
+                assert torch.all(out[row] == 0) and torch.all(lse[row] == -np.inf)
+                continue
+            p = torch.exp(x - z[:, None])
+            mean = (p * dx).sum(-1, keepdim=True)
+            dp = (2.0 ** -8 if fmt == "bf16" else 2.0 ** -11) + 2.0 ** -20 + 2.0 ** -10     # (2^-10: the sums' part, as above)
+            ref = p @ vv
+            tol = 2.0 ** -8 * ref.abs() + 1.004 * (p * (dp + dx + mean)) @ vv.abs() + 2.0 ** -31 * vv.abs().sum(0)
+            assert torch.all((out[row].double() - ref).abs() <= tol), (b, i, float(((out[row].double() - ref).abs() / tol).max()))
+            assert torch.all((lse[row].double() - z).abs() <= mean[:, 0] + 2.0 ** -20 * (1 + z.abs()) + T / 128 * 2.0 ** -24)
