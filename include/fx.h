@@ -627,9 +627,13 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
  *   x_t = scale * q . k_t;   with cap > 0: x_t = cap * tanh(x_t / cap);   then x_t -= slope[g] * |pos - t|
  *   out[i, g, :] = sum_t softmax(x)_t v_t   (bf16)        lse[i, g] = log sum_t exp(x_t)   (written when lse != NULL)
  * A query that sees no row, or whose logits are all -infinity, gives out = 0 and lse = -infinity.
- * Logits, sums and lse are fp32 (with more than 16 query rows a KV head, G*max_new, logits under a cap of up to 64 may be off
- * by 2^-21 of the cap besides).  Weights are rounded once for the product with V: to bf16 beside bf16 pages (2^-8 of a
- * weight), to f16 beside 4-bit pages.  A row that a query does not see does not reach it, whatever it holds.  A query that
+ * Two kinds of kernels take these calls.  Up to 16 query rows a KV head (G*max_new) go to those of fx_paged_decode, and so do
+ * up to 32 with 4-bit pages or a cap and up to 64 over tables with room for little (2^14 rows over all heads); more rows, and
+ * tables with room for more than fx_paged_decode's limit, go to the prompts' kernels.  Logits, sums and lse are fp32 in both.
+ * The former hold weights to 2^-22 of themselves for the product with V; the latter round them once, to bf16 beside bf16 pages
+ * (2^-8 of a weight), to f16 beside 4-bit pages (2^-11), and their logits under a cap of up to 64 may be off by 2^-21 of the
+ * cap.  The same tokens may so differ by these roundings between tables with more room and with less.
+ * A row that a query does not see does not reach it, whatever it holds.  A query that
  * sees a V with an infinity or a NaN may give NaN in all of its dimensions.
  *   start     int32 [B+1] on the device, or NULL: max_new tokens of every sequence (n = B * max_new).  Offsets that decrease
  *             or leave [0, n] set FX_DEVERR_OFFSETS and the sequence is skipped; of a sequence with more than max_new tokens
@@ -639,8 +643,9 @@ FX_API fx_status fx_paged_importance(const fx_paged_desc* cache, const fx_bf16* 
  *   q         bf16 rows (i, g) at q + i*q_stride_n + g*q_stride_h;   out bf16 [n, Hq, 128], lse fp32 [n, Hq], contiguous;
  *             they overlap nothing that the call reads
  *   max_new   host: tokens of one sequence, at most (G*max_new <= 2^30, n <= 2^30, n*Hq < 2^31)
- * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes, which suffice for every smaller max_new of that B too
- * (calls of few tokens may need more than long ones: they are cut along the cache).
+ * Workspace: fx_paged_attend_workspace_bytes(B, Hkv, Hq, max_new) bytes, which suffice for every smaller max_new of that B too,
+ * over any table (calls of few tokens may need more than long ones: they are cut along the cache; some 20 MB, for parts, or for
+ * the sums of rows past 2^17).
  */
 typedef struct {
     const fx_bf16* q;

@@ -918,6 +918,9 @@ def fx_paged_attend(cache, q, start=None, *, max_new=None, first=None, last=None
     t < last[i] (int32 [n]; 0 and its position + 1 when None), with a window only t > position - window.  cap > 0: scores
     become cap tanh(score / cap).  slope (fp32 [Hq]): each loses slope |position - t|.
 
+    How many query rows a KV head has (heads of it times max_new), and for 17 to 64 of them the room of the table, choose between
+    two kinds of kernels, whose weights have other roundings (include/fx.h).
+
     Without ws the call takes scratch memory as fx_paged_decode does.
     """
     lib, st = _paged_launch(cache, stream)

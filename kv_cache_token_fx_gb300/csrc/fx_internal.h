@@ -279,7 +279,7 @@ struct PagedGatherParams {
     unsigned* err;
 };
 
-// fx_paged_attend's prompts (paged_attend.cu).
+// fx_paged_attend's prompts (paged_attend.cuh).
 struct PagedAttendCut {
     int blocks;      // blocks of query rows of one (sequence, KV head), at most
     int split;       // CTAs among which the blocks' tiles are shared, or 0: one CTA to a block

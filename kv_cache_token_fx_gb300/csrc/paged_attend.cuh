@@ -15,7 +15,9 @@
 // largest is lost.
 //
 // P is rounded once, to the operands' type (bf16: at most 2^-8 of a weight; f16: 2^-11): the output is bf16, whose rounding is as
-// large.  Logits, maxima, sums and O are fp32.
+// large, and a second part would be another product with V for every tile, half as many again as there are.  (The decode, whose
+// output is fp32 and whose time is the cache's bytes, holds weights in two or three parts.)  Logits, maxima, sums and O are fp32;
+// over long rows O leaves the tensor core for memory (kFlush).
 //
 // Calls of fewer blocks than SMs are cut along the cache: every block's tiles become parts of nearly equal length by the
 // lengths found on the device, and the last CTA of a block to arrive joins its parts in their order.  (Calls of few
@@ -692,7 +694,7 @@ __device__ __forceinline__ bool plan(const PagedAttendParams& p, AttendSmem& sm,
 // WIDE: caps whose logits have to be exact relative to themselves (kMixedCap).  A kernel of its own: with both in one, the
 // smaller caps' windowed 4-bit prompt took 413 us instead of 405.
 // LONG: rows past kFlush tiles, by the room of the tables (the lengths are on the device).  Kernels of their own, too: sequences
-// short all the same take 3% (prompts with pictures) to 5% (windowed 4-bit prompts) longer in them.
+// short all the same take 2% (prompts with pictures 934 us, 955) to 4% longer in them (windowed 4-bit prompts 395, 412).
 template <bool E2M1, int MODE, bool WIDE, bool LONG>
 __global__ void __launch_bounds__(kThreadsA, 1) paged_attend_kernel(const __grid_constant__ PagedAttendParams p)
 {
