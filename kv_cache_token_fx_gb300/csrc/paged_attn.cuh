@@ -759,9 +759,10 @@ __device__ __forceinline__ float4 lds_float4(uint32_t a)
     const uint4 v = lds128(a);
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
-// Logits of U tiles whose first row is `first` (from the first query's position on, as the queries': near rows then have their
-// exact distances at any length of the cache, which positions past 2^24 by themselves do not have in fp32), as logits() gives them: under the cap, and with their bias by distance as
-// base-2 logits (without one, the factor of a capped logit, p.cap2, is left to weights()).
+// Logits of U tiles whose first row is `first`, as logits() gives them: under the cap, and with their bias by distance as
+// base-2 logits (without one, the factor of a capped logit, p.cap2, is left to weights()).  Rows and queries are counted from
+// the first query's position on: near rows then have their exact distances at any length of the cache, which positions past
+// 2^24 by themselves do not have in fp32.
 template <bool CAP, int U, int NT>
 __device__ __forceinline__ void shape_logits(const PagedAttnParams& p, const Shaping& sh, float (&s)[U * NT][4], int first)
 {

@@ -346,3 +346,36 @@ def test_attend_rows_past_a_flush(fx, fmt, B, kw):  # noqa: F811
             tol = 2.0 ** -8 * ref.abs() + 1.004 * (p * (dp + dx + mean)) @ vv.abs() + 2.0 ** -31 * vv.abs().sum(0)
             assert torch.all((out[row].double() - ref).abs() <= tol), (b, i, float(((out[row].double() - ref).abs() / tol).max()))
             assert torch.all((lse[row].double() - z).abs() <= mean[:, 0] + 2.0 ** -20 * (1 + z.abs()) + T / 128 * 2.0 ** -24)
+
+
+def test_attend_long_rows_at_once(fx):  # noqa: F811
+    """Calls over long rows on two streams at the same time, one after the other as programmatic launches, and in two graphs:
+    the bits of a call alone (sums in memory lie in each call's own scratch)."""
+    made = []
+    for seed, fmt in enumerate(FMT):
+        cache, _ = shared_pages(fx, fmt, 150 * 1024, 2, B=90)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        made.append((cache, torch.randn(90 * 20, 8, D, generator=g, device="cuda").mul_(2).to(torch.bfloat16)))
+    alone = [fx.fx_paged_attend(c, q, want_lse=True) for c, q in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    outs = [[], []]
+    for _ in range(3):
+        for s, o, (c, q) in zip(streams, outs, made):
+            o.append(fx.fx_paged_attend(c, q, want_lse=True, stream=s))
+            o.append(fx.fx_paged_attend(c, q, want_lse=True, stream=s, flags=fx.FX_LAUNCH_PDL))
+    torch.cuda.synchronize()
+    graphs = []
+    for c, q in made:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            got = fx.fx_paged_attend(c, q, want_lse=True)
+        graphs.append((g, got))
+    for _ in range(2):
+        for s, (g, got) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, (g, got), a in zip(outs, graphs, alone):
+        for x in o + [got]:
+            assert torch.equal(x[0], a[0]) and torch.equal(x[1], a[1])
